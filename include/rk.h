@@ -78,6 +78,16 @@ typedef enum {
 #define RK_DEVERR_LSE 0x4           /* a backward row had more than 64 columns with
                                        p >= 1/64: the lse passed in does not belong
                                        to these inputs (results unspecified) */
+#define RK_DEVERR_RULES 0x8         /* a row's sampling rules are not usable: a request or
+                                       mask index out of range, offsets that do not
+                                       ascend or leave their list, a temperature or
+                                       repetition penalty outside its range */
+
+/* Element type of a matrix that is passed as void*. */
+typedef enum {
+    RK_BF16 = 0, /* IEEE bfloat16 bit patterns, 2 bytes */
+    RK_FP32 = 1  /* 4 bytes */
+} rk_dtype;
 
 /*
  * Bytes of workspace rk_linear_logp needs for T rows (>= 0).  The layout is
@@ -388,6 +398,168 @@ rk_status rk_linear_logp_bwd_full_saved(const uint16_t *h, const uint16_t *W,
                                         const int64_t *row_order, int64_t n_order,
                                         float *dh, float *dW,
                                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Sampling rules: what a decoding loop does to the logits before it draws a
+ * token.  A token drawn under rules has the logprob of the distribution the
+ * rules leave, not that of the raw logits, so scoring it again for training
+ * has to apply the same rules ("dense vs indexed selected-logprob paths" and
+ * generate-then-re-score equivalence, issue #101 Scope and issue #244
+ * Workstream 2 #152).  Three calls share one description of them:
+ * rk_logits_rules_apply, rk_logp_from_logits_rules and
+ * rk_logp_from_logits_rules_bwd.
+ *
+ * Row t belongs to request r = row_request[t] (or t) and has seen the first
+ * L = row_length[t] tokens of that request (or all of them), of which the
+ * first prompt_lengths[r] are its prompt and the others were produced.  With
+ * n[v] the number of times v is among the produced ones, seen[v] whether it
+ * is among the L at all, and z = logits[t, :]:
+ *     y[v] = z[v],  or where seen[v]:  z[v] / repetition[r]  if z[v] > 0,
+ *                                      z[v] * repetition[r]  otherwise
+ *     y[v] = y[v] - frequency[r] * n[v] - presence[r] * (n[v] > 0) + bias[r, v]
+ *     x[v] = y[v] / temperature[r],  or -inf where the row's mask has a 0 bit.
+ * All in fp32.  What the logits hold in masked places (NaN, infinities) never
+ * reaches a result.
+ *
+ * The struct itself is host memory, read during the call; its pointers are
+ * device memory.  A NULL pointer leaves the rule out.
+ *   num_requests      R >= 0; with R == 0 every per-request pointer is NULL
+ *   temperature       fp32 [R], each in [1e-6, 1e6]
+ *   repetition        fp32 [R], each in [1e-6, 1e6]
+ *   frequency, presence  fp32 [R]
+ *   tokens            int64 [num_tokens]: request r's tokens, prompt first, are
+ *                     tokens[token_offsets[r]] .. tokens[token_offsets[r+1] - 1];
+ *                     ids outside [0, V) are passed over
+ *   token_offsets     int64 [R + 1]
+ *   prompt_lengths    int32 [R]; NULL: no prompt, every token was produced
+ *   bias_ids, bias_values  int64 / fp32 [num_bias]: request r's biases are entries
+ *                     bias_offsets[r] .. bias_offsets[r+1] - 1; ids outside [0, V)
+ *                     are passed over; an id listed twice takes its last value
+ *   bias_offsets      int64 [R + 1]
+ *   mask              int32 [mask_rows, ceil(V / 32)]: bit v % 32 of word v / 32 set
+ *                     = token v is allowed; bits past V are not read
+ *   row_request       int32 [T]; -1: the row is padding (no output of
+ *                     rk_logits_rules_apply is written, the others treat it as
+ *                     inactive); NULL: row t belongs to request t (T == R)
+ *   row_length        int32 [T], clamped to the request's length; NULL: all tokens
+ *   row_mask          int32 [T], the row's mask, negative: none; NULL: row t has
+ *                     mask t (T == mask_rows)
+ * A row whose rules are not usable (RK_DEVERR_RULES) gets NaN outputs and sets
+ * the device error word.
+ *
+ * For a given row the results are bitwise the same whatever the batch around
+ * it, and whichever way its history is described (its own request, or a
+ * prefix of a longer one through row_length).
+ */
+typedef struct {
+    int64_t num_requests;
+    const float *temperature;
+    const float *repetition;
+    const float *frequency;
+    const float *presence;
+    const int64_t *tokens;
+    int64_t num_tokens;
+    const int64_t *token_offsets;
+    const int32_t *prompt_lengths;
+    const int64_t *bias_ids;
+    const float *bias_values;
+    int64_t num_bias;
+    const int64_t *bias_offsets;
+    const int32_t *mask;
+    int64_t mask_rows;
+    const int32_t *row_request;
+    const int32_t *row_length;
+    const int32_t *row_mask;
+} rk_logits_rules;
+
+/*
+ * out[t, v] = x[v] of row t, the logits under the rules.
+ *   logits  bf16 or fp32 [T, V], row stride ld_logits >= V elements, aligned to
+ *           its element
+ *   out     bf16 or fp32 [T, V], row stride ld_out >= V (columns >= V untouched);
+ *           one rounding when it is bf16.  Must not overlap logits.
+ * Supported: 1 <= V < 2^31, 0 <= T < 2^31.  Needs no workspace.
+ */
+rk_status rk_logits_rules_apply(const void *logits, rk_dtype logits_type, int64_t ld_logits,
+                                const rk_logits_rules *rules, int64_t T, int64_t V,
+                                void *out, rk_dtype out_type, int64_t ld_out, void *stream);
+
+/*
+ * rk_logp_from_logits under the rules, x never written to memory:
+ *     lse[t] = log sum_v exp(x[v]),   logp[t] = x[targets[t]] - lse[t].
+ * A row of which the mask (or biases of -inf) leaves nothing has lse = logp =
+ * -inf, and a target that is masked has logp = -inf.
+ *   logits as for rk_logits_rules_apply; targets, cu_seqlens, num_seqs, logp and
+ *   lse (may be NULL) as for rk_logp_from_logits
+ *   workspace  >= rk_logp_from_logits_rules_workspace_size(T, V) bytes, 16-byte
+ *              aligned: per row a (max, sum-exp) partial for every 1024 columns
+ *              and the target's y
+ */
+size_t rk_logp_from_logits_rules_workspace_size(int64_t T, int64_t V);
+rk_status rk_logp_from_logits_rules(const void *logits, rk_dtype logits_type, int64_t ld_logits,
+                                    const int64_t *targets, const int32_t *cu_seqlens,
+                                    int32_t num_seqs, const rk_logits_rules *rules, int64_t T,
+                                    int64_t V, float *logp, float *lse, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
+ * The gradient of that logp with respect to the logits: for every active row
+ *     dlogits[t, v] = g[t] * ([v == targets[t]] - exp(x[v] - lse[t])) * s[v]
+ * with s = dx/dz: 1 / temperature[r], where seen[v] also 1 / repetition[r] (z[v] >
+ * 0) or repetition[r] (otherwise), and 0 in masked places.  0 on inactive rows and
+ * on rows of which the rules leave nothing (lse = -inf).
+ *   lse      fp32 [T] from rk_logp_from_logits_rules on the same inputs
+ *   dlogits  bf16 or fp32 [T, V], row stride ld_dlogits >= V (columns >= V
+ *            untouched), one rounding when it is bf16
+ */
+rk_status rk_logp_from_logits_rules_bwd(const void *logits, rk_dtype logits_type,
+                                        int64_t ld_logits, const int64_t *targets,
+                                        const int32_t *cu_seqlens, int32_t num_seqs,
+                                        const rk_logits_rules *rules, int64_t T, int64_t V,
+                                        const float *lse, const float *grad_logp, void *dlogits,
+                                        rk_dtype dlogits_type, int64_t ld_dlogits, void *stream);
+
+/*
+ * Token embedding, the other end of the vocabulary ("embedding", issue #101 P0
+ * list; chain index 0 of PR #264):
+ *     out[t, :] = scale * E[ids[t], :]
+ * for every active row (ids[t] >= 0 and inside the cu_seqlens range), 0 on the
+ * others; NaN and RK_DEVERR_TARGET_RANGE where ids[t] >= V.
+ *   ids  int64 [T];  E  bf16 or fp32 [V, H];  out  bf16 or fp32 [T, H] (the product in
+ *   fp32, rounded once when out is bf16); both contiguous, aligned to their element
+ * Supported: 1 <= H < 2^31, 1 <= V < 2^31, 0 <= T < 2^31.
+ */
+rk_status rk_embedding(const int64_t *ids, const int32_t *cu_seqlens, int32_t num_seqs,
+                       const void *E, rk_dtype e_type, int64_t T, int64_t H, int64_t V,
+                       float scale, void *out, rk_dtype out_type, void *stream);
+
+/*
+ * The gradient of rk_embedding with respect to E, over canonical tokens as for
+ * rk_linear_logp_dw (embedding gradients are named with dW as parameter gradients
+ * that need a fixed order and no atomicAdd, issue #244 Workstream 3 #153):
+ *     dE[v, :] (+)= scale * sum over canonical tokens i with ids[i] = v of dout[i, :]
+ * The canonical tokens are the active rows among row_order[0..n_order), out-of-range
+ * entries skipped, or rows 0..T-1 when row_order is NULL.  They are sorted by id with
+ * their order kept, and each id's rows are summed in that order, in fp32, in pieces of
+ * 64 occurrences whose sums are then added in order: dE[v] is bitwise the same for the
+ * same tokens of id v in the same canonical order, whatever their physical layout and
+ * whatever the other tokens are.  A row listed twice counts twice.
+ *   dout  bf16 or fp32 [T, H]; dE fp32 [V, H]; both contiguous, aligned to their element
+ *   accumulate  0: dE is overwritten (0 in rows without a token); 1: the sum is added to
+ *               what dE holds, as for a weight tied to the lm_head's (rows without a
+ *               token are not touched)
+ *   ids >= V on active rows contribute nothing and set RK_DEVERR_TARGET_RANGE
+ *   workspace  >= rk_embedding_bwd_workspace_size(n, H, V) bytes, 16-byte aligned, n =
+ *              n_order (or T): the sort's keys and counts, the list of pieces, and
+ *              fp32 [n / 32 + 1, H] for the sums of ids with more than 64 rows
+ * Supported: as rk_embedding, V < 2^31 - 1, n < 2^31.
+ */
+size_t rk_embedding_bwd_workspace_size(int64_t n, int64_t H, int64_t V);
+rk_status rk_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *ids,
+                           const int32_t *cu_seqlens, int32_t num_seqs, int64_t T, int64_t H,
+                           int64_t V, float scale, const int64_t *row_order, int64_t n_order,
+                           float *dE, int32_t accumulate, void *workspace,
+                           size_t workspace_bytes, void *stream);
 
 /*
  * rk_linear_logp without a workspace argument, for callers that cannot

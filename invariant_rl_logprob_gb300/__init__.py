@@ -11,6 +11,12 @@ Operators (RL-Kernel issue #101, maintainer comment, P0 operator list):
 * :func:`linear_logp`      -- ``logp[t] = z[t, target_t] - logsumexp_v z[t, v]``, ``z = h W^T``
 * :func:`logp_from_logits` -- the same from materialised bf16 logits
 * :func:`linear_logp_bwd`  -- ``dh[t] = g[t] (W[target_t] - softmax(z[t]) W)``
+* :func:`logits_rules_apply`, :func:`logp_from_logits_rules`,
+  :func:`logp_from_logits_rules_bwd` -- logits under sampling rules
+  (:class:`LogitsRules`: penalties, biases, grammar masks, temperature), the
+  selected logprob under them and its gradient
+* :func:`embedding`, :func:`embedding_bwd` -- the scaled token embedding and
+  its gradient, summed per token in canonical order
 
 Each is bitwise invariant for a given logical row under changes of batch
 size, row position, neighbour content, padding and varlen packing.
@@ -32,7 +38,11 @@ __all__ = [
     "linear_logp_bwd_saved_workspace_size", "linear_logp_bwd_full_saved",
     "linear_greedy_workspace_size", "linear_logp_dw", "linear_logp_dw_workspace_size",
     "linear_logp_bwd_full", "linear_logp_bwd_full_workspace_size", "lm_head_workspace_size",
+    "LogitsRules", "logits_rules_apply", "logp_from_logits_rules",
+    "logp_from_logits_rules_workspace_size", "logp_from_logits_rules_bwd",
+    "embedding", "embedding_bwd", "embedding_bwd_workspace_size",
     "get_device_error", "selftest_wait_timeout", "set_row_blocks", "last_row_blocks", "DEVERR_TARGET_RANGE", "DEVERR_TIMEOUT", "DEVERR_LSE",
+    "DEVERR_RULES",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -43,6 +53,7 @@ RK_OK, RK_ERR_INVALID_ARG, RK_ERR_UNSUPPORTED, RK_ERR_WORKSPACE, RK_ERR_CUDA = r
 DEVERR_TARGET_RANGE = 0x1
 DEVERR_TIMEOUT = 0x2
 DEVERR_LSE = 0x4
+DEVERR_RULES = 0x8
 
 
 class RkError(RuntimeError):
@@ -139,6 +150,24 @@ def load_library() -> ctypes.CDLL:
     lib.rk_last_row_blocks.restype = i32
     lib.rk_last_tile_order.argtypes = [i32]
     lib.rk_last_tile_order.restype = i32
+    rp = ctypes.c_void_p  # a _RulesStruct, passed by address
+    lib.rk_logits_rules_apply.argtypes = [vp, i32, i64, rp, i64, i64, vp, i32, i64, vp]
+    lib.rk_logits_rules_apply.restype = ctypes.c_int
+    lib.rk_logp_from_logits_rules_workspace_size.argtypes = [i64, i64]
+    lib.rk_logp_from_logits_rules_workspace_size.restype = sz
+    lib.rk_logp_from_logits_rules.argtypes = [vp, i32, i64, vp, vp, i32, rp, i64, i64, vp, vp, vp, sz,
+                                              vp]
+    lib.rk_logp_from_logits_rules.restype = ctypes.c_int
+    lib.rk_logp_from_logits_rules_bwd.argtypes = [vp, i32, i64, vp, vp, i32, rp, i64, i64, vp, vp, vp,
+                                                  i32, i64, vp]
+    lib.rk_logp_from_logits_rules_bwd.restype = ctypes.c_int
+    lib.rk_embedding.argtypes = [vp, vp, i32, vp, i32, i64, i64, i64, f32, vp, i32, vp]
+    lib.rk_embedding.restype = ctypes.c_int
+    lib.rk_embedding_bwd_workspace_size.argtypes = [i64, i64, i64]
+    lib.rk_embedding_bwd_workspace_size.restype = sz
+    lib.rk_embedding_bwd.argtypes = [vp, i32, vp, vp, i32, i64, i64, i64, f32, vp, i64, vp, i32, vp,
+                                     sz, vp]
+    lib.rk_embedding_bwd.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -591,6 +620,340 @@ def linear_logp_bwd_full(h: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
                                      _stream_handle(stream, h.device))
     _check(st, "rk_linear_logp_bwd_full")
     return dh, dW
+
+
+class _RulesStruct(ctypes.Structure):
+    """rk_logits_rules of include/rk.h."""
+    _fields_ = [("num_requests", ctypes.c_int64)] + \
+        [(n, ctypes.c_void_p) for n in ("temperature", "repetition", "frequency", "presence",
+                                        "tokens")] + \
+        [("num_tokens", ctypes.c_int64), ("token_offsets", ctypes.c_void_p),
+         ("prompt_lengths", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p),
+         ("bias_values", ctypes.c_void_p), ("num_bias", ctypes.c_int64),
+         ("bias_offsets", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+         ("mask_rows", ctypes.c_int64)] + \
+        [(n, ctypes.c_void_p) for n in ("row_request", "row_length", "row_mask")]
+
+
+_RULE_PARAMS = ("temperature", "repetition", "frequency", "presence")
+
+
+class LogitsRules:
+    """What a decoding loop does to the logits before it draws a token.
+
+    Row ``t`` belongs to request ``r = row_request[t]`` (default ``t``) and has
+    seen the first ``row_length[t]`` (default: all) of that request's tokens,
+    ``tokens[token_offsets[r] : token_offsets[r + 1]]``, of which the first
+    ``prompt_lengths[r]`` (default 0) are the prompt and the others were
+    produced.  With ``n[v]`` how often ``v`` was produced::
+
+        y = z;  where v was seen at all:  z / repetition  (z > 0),  z * repetition  (z <= 0)
+        y = y - frequency * n - presence * (n > 0) + bias
+        x = y / temperature,  -inf where the row's mask has a 0 bit
+
+    Per request: ``temperature``, ``repetition``, ``frequency``, ``presence``
+    (fp32 ``[R]``), ``prompt_lengths`` (int32 ``[R]``), ``token_offsets`` and
+    ``bias_offsets`` (int64 ``[R + 1]``) into ``tokens`` (int64) and into
+    ``bias_ids`` (int64) / ``bias_values`` (fp32).  ``mask`` is int32
+    ``[M, ceil(V / 32)]``, bit ``v % 32`` of word ``v // 32`` set where token ``v``
+    is allowed.  Per row, int32 ``[T]``: ``row_request`` (-1: padding),
+    ``row_length``, ``row_mask`` (default ``t``; negative: no mask).  All are
+    contiguous CUDA tensors, kept by the object; whatever is left out does not
+    apply.  The tensors are read when an operator runs, so their contents may
+    change between calls (a replayed CUDA graph reads the new ones).
+    """
+
+    __slots__ = ("device", "struct", "address", "rows", "mask_words", "_kept")
+
+    def __init__(self, *, temperature: torch.Tensor | None = None,
+                 repetition: torch.Tensor | None = None, frequency: torch.Tensor | None = None,
+                 presence: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                 token_offsets: torch.Tensor | None = None,
+                 prompt_lengths: torch.Tensor | None = None, bias_ids: torch.Tensor | None = None,
+                 bias_values: torch.Tensor | None = None, bias_offsets: torch.Tensor | None = None,
+                 mask: torch.Tensor | None = None, row_request: torch.Tensor | None = None,
+                 row_length: torch.Tensor | None = None, row_mask: torch.Tensor | None = None):
+        kept = {"temperature": temperature, "repetition": repetition, "frequency": frequency,
+                "presence": presence, "tokens": tokens, "token_offsets": token_offsets,
+                "prompt_lengths": prompt_lengths, "bias_ids": bias_ids, "bias_values": bias_values,
+                "bias_offsets": bias_offsets, "mask": mask, "row_request": row_request,
+                "row_length": row_length, "row_mask": row_mask}
+        if (tokens is None) != (token_offsets is None):
+            raise ValueError("tokens and token_offsets go together")
+        if prompt_lengths is not None and tokens is None:
+            raise ValueError("prompt_lengths needs tokens")
+        if not ((bias_ids is None) == (bias_values is None) == (bias_offsets is None)):
+            raise ValueError("bias_ids, bias_values and bias_offsets go together")
+        if row_length is not None and tokens is None:
+            raise ValueError("row_length needs tokens")
+        if row_mask is not None and mask is None:
+            raise ValueError("row_mask needs mask")
+        s = _RulesStruct()
+        device = requests = rows = None
+        for name, t in kept.items():
+            if t is None:
+                continue
+            dtype, ndim = _RULE_TYPES[name]
+            _need(t, name, dtype, ndim)
+            if device is None:
+                device = t.device
+            elif t.device != device:
+                raise ValueError(f"{name} is on {t.device}, not on {device}")
+            n = t.shape[0]
+            if name in _RULE_PER_REQUEST:
+                n -= _RULE_PER_REQUEST[name]
+                if n < 1 or (requests is not None and n != requests):
+                    raise ValueError(f"{name} does not fit {requests if requests else 'one or more'} "
+                                     "requests")
+                requests = n
+            elif name in _RULE_PER_ROW:
+                if rows is not None and n != rows:
+                    raise ValueError(f"{name} does not fit {rows} rows")
+                rows = n
+            setattr(s, name, t.data_ptr())
+        if bias_ids is not None and bias_ids.shape[0] != bias_values.shape[0]:
+            raise ValueError("bias_ids and bias_values differ in length")
+        s.num_requests = requests or 0
+        s.num_tokens = 0 if tokens is None else tokens.shape[0]
+        s.num_bias = 0 if bias_ids is None else bias_ids.shape[0]
+        s.mask_rows = 0 if mask is None else mask.shape[0]
+        if requests and row_request is None:
+            if rows is not None and rows != requests:
+                raise ValueError(f"{requests} requests for {rows} rows: row_request is missing")
+            rows = requests
+        if mask is not None and row_mask is None:
+            if rows is not None and rows != mask.shape[0]:
+                raise ValueError(f"{mask.shape[0]} masks for {rows} rows: row_mask is missing")
+            rows = mask.shape[0]
+        # an empty list still has to be told from a missing one
+        for name in ("tokens", "bias_ids", "bias_values", "mask"):
+            if kept[name] is not None and kept[name].numel() == 0:
+                setattr(s, name, _EMPTY)
+        self.device, self.rows = device, rows
+        self.mask_words = None if mask is None else mask.shape[1]
+        self.struct, self.address, self._kept = s, ctypes.addressof(s), kept
+
+
+_EMPTY = 256  # an address that an empty list never reads
+_RULE_TYPES = {"temperature": (torch.float32, 1), "repetition": (torch.float32, 1),
+               "frequency": (torch.float32, 1), "presence": (torch.float32, 1),
+               "tokens": (torch.int64, 1), "token_offsets": (torch.int64, 1),
+               "prompt_lengths": (torch.int32, 1), "bias_ids": (torch.int64, 1),
+               "bias_values": (torch.float32, 1), "bias_offsets": (torch.int64, 1),
+               "mask": (torch.int32, 2), "row_request": (torch.int32, 1),
+               "row_length": (torch.int32, 1), "row_mask": (torch.int32, 1)}
+_RULE_PER_REQUEST = {"temperature": 0, "repetition": 0, "frequency": 0, "presence": 0,
+                     "prompt_lengths": 0, "token_offsets": 1, "bias_offsets": 1}
+_RULE_PER_ROW = ("row_request", "row_length", "row_mask")
+_TYPE_CODES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _matrix(t: torch.Tensor, name: str, shape=None, device=None):
+    """(type code, row stride) of a bf16 or fp32 [T, V] matrix with unit column stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path), got {t.device}")
+    if t.dtype not in _TYPE_CODES:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be {list(shape) if shape else '[T, V]'}, "
+                         f"got shape {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    T, V = t.shape
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    ld = t.stride(0) if T > 1 else max(V, 1)
+    if ld < V:
+        raise ValueError(f"{name}'s rows overlap")
+    return _TYPE_CODES[t.dtype], ld
+
+
+def _rules_for(rules: LogitsRules, T: int, V: int, device) -> None:
+    if not isinstance(rules, LogitsRules):
+        raise TypeError("rules must be a LogitsRules")
+    if rules.device is not None and rules.device != device:
+        raise ValueError(f"the rules are on {rules.device}, the logits on {device}")
+    if rules.rows is not None and rules.rows != T:
+        raise ValueError(f"the rules are for {rules.rows} rows, the logits have {T}")
+    if rules.mask_words is not None and rules.mask_words != (V + 31) // 32:
+        raise ValueError(f"mask must have ceil(V / 32) = {(V + 31) // 32} words a row, "
+                         f"got {rules.mask_words}")
+
+
+def _vector(t: torch.Tensor, name: str, T: int, device) -> None:
+    _need(t, name, torch.float32, 1)
+    if t.shape[0] != T or t.device != device:
+        raise ValueError(f"{name} must be [T] on {device}")
+
+
+def _scratch(workspace, need: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", torch.uint8, 1)
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    return workspace
+
+
+def logits_rules_apply(logits: torch.Tensor, rules: LogitsRules, *,
+                       out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+                       stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """The logits under ``rules``, ``[T, V]`` in ``out_dtype`` (bf16 or fp32).
+
+    ``logits`` is bf16 or fp32 ``[T, V]`` with any row stride (the output of
+    :func:`lm_head` as it is).  Rows with ``row_request`` -1 are left as they
+    are in ``out``."""
+    lib = _lib or load_library()
+    code, ld = _matrix(logits, "logits")
+    T, V = logits.shape
+    device = logits.device
+    _rules_for(rules, T, V, device)
+    if out is None:
+        out = torch.empty((T, V), dtype=out_dtype, device=device)
+    out_code, out_ld = _matrix(out, "out", (T, V), device)
+    with torch.cuda.device(device):
+        st = lib.rk_logits_rules_apply(logits.data_ptr(), code, ld, rules.address, T, V,
+                                       out.data_ptr(), out_code, out_ld,
+                                       _stream_handle(stream, device))
+    _check(st, "rk_logits_rules_apply")
+    return out
+
+
+def logp_from_logits_rules_workspace_size(T: int, V: int) -> int:
+    return int(load_library().rk_logp_from_logits_rules_workspace_size(T, V))
+
+
+def logp_from_logits_rules(logits: torch.Tensor, targets: torch.Tensor, rules: LogitsRules,
+                           cu_seqlens: torch.Tensor | None = None, *,
+                           out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None,
+                           stream: torch.cuda.Stream | None = None):
+    """Selected-token logprob of the distribution that ``rules`` leave: returns
+    ``(logp, lse)``, fp32 ``[T]``.  Both are -inf on a row of which the rules
+    leave nothing, logp where the target is masked."""
+    lib = _lib or load_library()
+    code, ld = _matrix(logits, "logits")
+    T, V = logits.shape
+    device = logits.device
+    cu, ns = _rows(targets, cu_seqlens, T, device)
+    _rules_for(rules, T, V, device)
+    if out is None:
+        out = torch.empty(T, dtype=torch.float32, device=device)
+    if lse is None:
+        lse = torch.empty(T, dtype=torch.float32, device=device)
+    _vector(out, "out", T, device)
+    _vector(lse, "lse", T, device)
+    workspace = _scratch(workspace, lib.rk_logp_from_logits_rules_workspace_size(T, V), device)
+    with torch.cuda.device(device):
+        st = lib.rk_logp_from_logits_rules(logits.data_ptr(), code, ld, targets.data_ptr(), _ptr(cu),
+                                           ns, rules.address, T, V, out.data_ptr(), lse.data_ptr(),
+                                           workspace.data_ptr(), workspace.numel(),
+                                           _stream_handle(stream, device))
+    _check(st, "rk_logp_from_logits_rules")
+    return out, lse
+
+
+def logp_from_logits_rules_bwd(logits: torch.Tensor, targets: torch.Tensor, rules: LogitsRules,
+                               lse: torch.Tensor, grad_logp: torch.Tensor,
+                               cu_seqlens: torch.Tensor | None = None, *,
+                               out: torch.Tensor | None = None,
+                               out_dtype: torch.dtype = torch.float32,
+                               stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """The gradient of :func:`logp_from_logits_rules` with respect to the logits,
+    ``[T, V]`` in ``out_dtype`` (bf16 or fp32)."""
+    lib = _lib or load_library()
+    code, ld = _matrix(logits, "logits")
+    T, V = logits.shape
+    device = logits.device
+    cu, ns = _rows(targets, cu_seqlens, T, device)
+    _rules_for(rules, T, V, device)
+    _vector(lse, "lse", T, device)
+    _vector(grad_logp, "grad_logp", T, device)
+    if out is None:
+        out = torch.empty((T, V), dtype=out_dtype, device=device)
+    out_code, out_ld = _matrix(out, "out", (T, V), device)
+    with torch.cuda.device(device):
+        st = lib.rk_logp_from_logits_rules_bwd(logits.data_ptr(), code, ld, targets.data_ptr(),
+                                               _ptr(cu), ns, rules.address, T, V, lse.data_ptr(),
+                                               grad_logp.data_ptr(), out.data_ptr(), out_code, out_ld,
+                                               _stream_handle(stream, device))
+    _check(st, "rk_logp_from_logits_rules_bwd")
+    return out
+
+
+def _dense(t: torch.Tensor, name: str, shape, device) -> int:
+    """Type code of a contiguous bf16 or fp32 matrix."""
+    code, _ = _matrix(t, name, shape, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return code
+
+
+def embedding(ids: torch.Tensor, E: torch.Tensor, cu_seqlens: torch.Tensor | None = None, *,
+              scale: float = 1.0, out: torch.Tensor | None = None,
+              out_dtype: torch.dtype | None = None,
+              stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """``scale * E[ids]``, ``[T, H]`` in ``out_dtype`` (default: E's), 0 in rows with a
+    negative id or outside ``cu_seqlens``; E is bf16 or fp32 ``[V, H]``."""
+    lib = _lib or load_library()
+    code = _dense(E, "E", None, None)
+    V, H = E.shape
+    device = E.device
+    _need(ids, "ids", torch.int64, 1)
+    T = ids.shape[0]
+    cu, ns = _rows(ids, cu_seqlens, T, device)
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype or E.dtype, device=device)
+    out_code = _dense(out, "out", (T, H), device)
+    with torch.cuda.device(device):
+        st = lib.rk_embedding(ids.data_ptr(), _ptr(cu), ns, E.data_ptr(), code, T, H, V, scale,
+                              out.data_ptr(), out_code, _stream_handle(stream, device))
+    _check(st, "rk_embedding")
+    return out
+
+
+def embedding_bwd_workspace_size(n: int, H: int, V: int) -> int:
+    return int(load_library().rk_embedding_bwd_workspace_size(n, H, V))
+
+
+def embedding_bwd(grad_out: torch.Tensor, ids: torch.Tensor, V: int,
+                  cu_seqlens: torch.Tensor | None = None, *, scale: float = 1.0,
+                  row_order: torch.Tensor | None = None, dE: torch.Tensor | None = None,
+                  accumulate: bool = False, workspace: torch.Tensor | None = None,
+                  stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """dE fp32 ``[V, H]``: ``scale *`` the sum of ``grad_out``'s rows (bf16 or fp32
+    ``[T, H]``) of each id over the active rows in canonical order (``row_order``, int64
+    physical row indices; ascending rows by default).  With ``accumulate`` it is added
+    to what ``dE`` holds (a weight tied to the lm_head's: ``dE`` from
+    :func:`linear_logp_dw`)."""
+    lib = _lib or load_library()
+    code = _dense(grad_out, "grad_out", None, None)
+    T, H = grad_out.shape
+    device = grad_out.device
+    cu, ns = _rows(ids, cu_seqlens, T, device)
+    n, order = T, None
+    if row_order is not None:
+        _need(row_order, "row_order", torch.int64, 1)
+        if row_order.device != device:
+            raise ValueError(f"row_order must be on {device}")
+        n = row_order.shape[0]
+        order = row_order.data_ptr() or _EMPTY
+    if dE is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dE to add to")
+        dE = torch.empty((V, H), dtype=torch.float32, device=device)
+    if _dense(dE, "dE", (V, H), device) != 1:
+        raise TypeError("dE must be float32")
+    workspace = _scratch(workspace, lib.rk_embedding_bwd_workspace_size(n, H, V), device)
+    with torch.cuda.device(device):
+        st = lib.rk_embedding_bwd(grad_out.data_ptr(), code, ids.data_ptr(), _ptr(cu), ns, T, H, V,
+                                  scale, order, n, dE.data_ptr(), int(accumulate),
+                                  workspace.data_ptr(), workspace.numel(),
+                                  _stream_handle(stream, device))
+    _check(st, "rk_embedding_bwd")
+    return dE
 
 
 def selftest_wait_timeout(limit_ns: int, stream: torch.cuda.Stream | None = None) -> None:

@@ -546,6 +546,159 @@ rk_status rk_linear_logp_bwd_full_saved(const uint16_t *h, const uint16_t *W,
     return RK_OK;
 }
 
+static bool good_type(rk_dtype t) { return t == RK_BF16 || t == RK_FP32; }
+static bool elem_aligned(const void *p, rk_dtype t) { return aligned(p, t == RK_BF16 ? 2 : 4); }
+
+// Argument checks of a rules struct against T rows.
+static rk_status check_rules(const rk_logits_rules *r, int64_t T) {
+    if (!r) return RK_ERR_INVALID_ARG;
+    if (r->num_requests < 0 || r->num_tokens < 0 || r->num_bias < 0 || r->mask_rows < 0)
+        return RK_ERR_INVALID_ARG;
+    if (r->num_requests >= (int64_t(1) << 31)) return RK_ERR_UNSUPPORTED;
+    if (r->num_requests == 0 &&
+        (r->temperature || r->repetition || r->frequency || r->presence || r->tokens || r->bias_ids))
+        return RK_ERR_INVALID_ARG;
+    if (r->tokens && !r->token_offsets) return RK_ERR_INVALID_ARG;
+    if (r->prompt_lengths && !r->tokens) return RK_ERR_INVALID_ARG;
+    if (r->bias_ids && (!r->bias_values || !r->bias_offsets)) return RK_ERR_INVALID_ARG;
+    if (r->num_requests > 0 && !r->row_request && r->num_requests != T) return RK_ERR_INVALID_ARG;
+    if (r->mask && !r->row_mask && r->mask_rows != T) return RK_ERR_INVALID_ARG;
+    return RK_OK;
+}
+
+rk_status rk_logits_rules_apply(const void *logits, rk_dtype logits_type, int64_t ld_logits,
+                                const rk_logits_rules *rules, int64_t T, int64_t V, void *out,
+                                rk_dtype out_type, int64_t ld_out, void *stream) {
+    if (T < 0 || V <= 0 || !good_type(logits_type) || !good_type(out_type)) return RK_ERR_INVALID_ARG;
+    if (T == 0) return RK_OK;
+    if (!logits || !out || ld_logits < V || ld_out < V) return RK_ERR_INVALID_ARG;
+    if (V >= (int64_t(1) << 31) || T >= (int64_t(1) << 31)) return RK_ERR_UNSUPPORTED;
+    rk_status st = check_rules(rules, T);
+    if (st != RK_OK) return st;
+    if (!elem_aligned(logits, logits_type) || !elem_aligned(out, out_type)) return RK_ERR_INVALID_ARG;
+    DeviceInfo di;
+    cudaError_t e = rk::current_device_info(&di);
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    e = rk::launch_rules_apply({logits, logits_type, ld_logits}, *rules, T, V,
+                               {out, out_type, ld_out}, di, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    return RK_OK;
+}
+
+size_t rk_logp_from_logits_rules_workspace_size(int64_t T, int64_t V) {
+    if (T <= 0 || V <= 0) return 0;
+    return rk::logp_rules_workspace_bytes(T, V);
+}
+
+rk_status rk_logp_from_logits_rules(const void *logits, rk_dtype logits_type, int64_t ld_logits,
+                                    const int64_t *targets, const int32_t *cu_seqlens,
+                                    int32_t num_seqs, const rk_logits_rules *rules, int64_t T,
+                                    int64_t V, float *logp, float *lse, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
+    if (T < 0 || V <= 0 || !good_type(logits_type)) return RK_ERR_INVALID_ARG;
+    if (T == 0) return RK_OK;
+    if (!logits || !logp || ld_logits < V) return RK_ERR_INVALID_ARG;
+    rk_status st = check_rows(targets, cu_seqlens, num_seqs);
+    if (st != RK_OK) return st;
+    if (V >= (int64_t(1) << 31) || T >= (int64_t(1) << 31)) return RK_ERR_UNSUPPORTED;
+    st = check_rules(rules, T);
+    if (st != RK_OK) return st;
+    if (!elem_aligned(logits, logits_type)) return RK_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < rk::logp_rules_workspace_bytes(T, V)) return RK_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return RK_ERR_INVALID_ARG;
+    DeviceInfo di;
+    cudaError_t e = rk::current_device_info(&di);
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    e = rk::launch_rules_logp({logits, logits_type, ld_logits}, targets, cu_seqlens, num_seqs, *rules,
+                              T, V, logp, lse, workspace, di, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    return RK_OK;
+}
+
+rk_status rk_logp_from_logits_rules_bwd(const void *logits, rk_dtype logits_type,
+                                        int64_t ld_logits, const int64_t *targets,
+                                        const int32_t *cu_seqlens, int32_t num_seqs,
+                                        const rk_logits_rules *rules, int64_t T, int64_t V,
+                                        const float *lse, const float *grad_logp, void *dlogits,
+                                        rk_dtype dlogits_type, int64_t ld_dlogits, void *stream) {
+    if (T < 0 || V <= 0 || !good_type(logits_type) || !good_type(dlogits_type))
+        return RK_ERR_INVALID_ARG;
+    if (T == 0) return RK_OK;
+    if (!logits || !lse || !grad_logp || !dlogits || ld_logits < V || ld_dlogits < V)
+        return RK_ERR_INVALID_ARG;
+    rk_status st = check_rows(targets, cu_seqlens, num_seqs);
+    if (st != RK_OK) return st;
+    if (V >= (int64_t(1) << 31) || T >= (int64_t(1) << 31)) return RK_ERR_UNSUPPORTED;
+    st = check_rules(rules, T);
+    if (st != RK_OK) return st;
+    if (!elem_aligned(logits, logits_type) || !elem_aligned(dlogits, dlogits_type))
+        return RK_ERR_INVALID_ARG;
+    DeviceInfo di;
+    cudaError_t e = rk::current_device_info(&di);
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    e = rk::launch_rules_bwd({logits, logits_type, ld_logits}, targets, cu_seqlens, num_seqs, *rules,
+                             T, V, lse, grad_logp, {dlogits, dlogits_type, ld_dlogits}, di,
+                             static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    return RK_OK;
+}
+
+rk_status rk_embedding(const int64_t *ids, const int32_t *cu_seqlens, int32_t num_seqs,
+                       const void *E, rk_dtype e_type, int64_t T, int64_t H, int64_t V, float scale,
+                       void *out, rk_dtype out_type, void *stream) {
+    if (T < 0 || H <= 0 || V <= 0 || !good_type(e_type) || !good_type(out_type))
+        return RK_ERR_INVALID_ARG;
+    if (T == 0) return RK_OK;
+    if (!E || !out) return RK_ERR_INVALID_ARG;
+    rk_status st = check_rows(ids, cu_seqlens, num_seqs);
+    if (st != RK_OK) return st;
+    const int64_t lim = int64_t(1) << 31;
+    if (V >= lim || T >= lim || H >= lim) return RK_ERR_UNSUPPORTED;
+    if (!elem_aligned(E, e_type) || !elem_aligned(out, out_type)) return RK_ERR_INVALID_ARG;
+    DeviceInfo di;
+    cudaError_t e = rk::current_device_info(&di);
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    e = rk::launch_embedding(ids, cu_seqlens, num_seqs, E, e_type, T, H, V, scale, out, out_type, di,
+                             static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    return RK_OK;
+}
+
+size_t rk_embedding_bwd_workspace_size(int64_t n, int64_t H, int64_t V) {
+    if (n <= 0 || H <= 0 || V <= 0) return 0;
+    return rk::embedding_bwd_workspace_bytes(n, H, V);
+}
+
+rk_status rk_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *ids,
+                           const int32_t *cu_seqlens, int32_t num_seqs, int64_t T, int64_t H,
+                           int64_t V, float scale, const int64_t *row_order, int64_t n_order,
+                           float *dE, int32_t accumulate, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+    if (T < 0 || H <= 0 || V <= 0 || !good_type(dout_type)) return RK_ERR_INVALID_ARG;
+    if (!dE || (accumulate != 0 && accumulate != 1)) return RK_ERR_INVALID_ARG;
+    const int64_t n = row_order ? n_order : T;
+    if (n < 0) return RK_ERR_INVALID_ARG;
+    if (T > 0 && n > 0) {
+        if (!dout) return RK_ERR_INVALID_ARG;
+        rk_status st = check_rows(ids, cu_seqlens, num_seqs);
+        if (st != RK_OK) return st;
+    }
+    const int64_t lim = int64_t(1) << 31;
+    if (V >= lim - 1 || T >= lim || H >= lim || n >= lim) return RK_ERR_UNSUPPORTED;
+    if ((dout && !elem_aligned(dout, dout_type)) || !aligned(dE, 4)) return RK_ERR_INVALID_ARG;
+    if (n > 0 && (!workspace || workspace_bytes < rk::embedding_bwd_workspace_bytes(n, H, V)))
+        return RK_ERR_WORKSPACE;
+    if (n > 0 && !aligned(workspace, 16)) return RK_ERR_INVALID_ARG;
+    DeviceInfo di;
+    cudaError_t e = rk::current_device_info(&di);
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    e = rk::launch_embedding_bwd(dout, dout_type, ids, cu_seqlens, num_seqs, T, H, V, scale,
+                                 row_order, T > 0 ? n : 0, dE, accumulate != 0, workspace, di,
+                                 static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    return RK_OK;
+}
+
 rk_status rk_selftest_wait_timeout(int64_t limit_ns, void *stream) {
     if (limit_ns <= 0 || limit_ns > 10000000000ll) return RK_ERR_INVALID_ARG;
     DeviceInfo di;

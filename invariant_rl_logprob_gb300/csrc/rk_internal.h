@@ -74,6 +74,36 @@ cudaError_t launch_logits_bwd(const uint16_t *logits, const int64_t *targets, co
                               const float *grad, float *dlogits, const DeviceInfo &di,
                               cudaStream_t st);
 
+// ---- logits under sampling rules (logits_rules.cu) ----
+struct RulesMatrix {  // logits, or what is made of them
+    const void *p;  // written through where it is an output
+    rk_dtype type;
+    int64_t ld;
+};
+size_t logp_rules_workspace_bytes(int64_t T, int64_t V);
+cudaError_t launch_rules_apply(const RulesMatrix &logits, const rk_logits_rules &rules, int64_t T,
+                               int64_t V, const RulesMatrix &out, const DeviceInfo &di,
+                               cudaStream_t st);
+cudaError_t launch_rules_logp(const RulesMatrix &logits, const int64_t *targets, const int32_t *cu,
+                              int num_seqs, const rk_logits_rules &rules, int64_t T, int64_t V,
+                              float *logp, float *lse, void *workspace, const DeviceInfo &di,
+                              cudaStream_t st);
+cudaError_t launch_rules_bwd(const RulesMatrix &logits, const int64_t *targets, const int32_t *cu,
+                             int num_seqs, const rk_logits_rules &rules, int64_t T, int64_t V,
+                             const float *lse, const float *grad, const RulesMatrix &dlogits,
+                             const DeviceInfo &di, cudaStream_t st);
+
+// ---- embedding and its gradient (embedding.cu) ----
+cudaError_t launch_embedding(const int64_t *ids, const int32_t *cu, int num_seqs, const void *E,
+                             rk_dtype e_type, int64_t T, int64_t H, int64_t V, float scale,
+                             void *out, rk_dtype out_type, const DeviceInfo &di, cudaStream_t st);
+size_t embedding_bwd_workspace_bytes(int64_t n, int64_t H, int64_t V);
+cudaError_t launch_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *ids,
+                                 const int32_t *cu, int num_seqs, int64_t T, int64_t H, int64_t V,
+                                 float scale, const int64_t *order, int64_t n, float *dE,
+                                 bool accumulate, void *workspace, const DeviceInfo &di,
+                                 cudaStream_t st);
+
 // ---- per-token GRPO loss (token_loss.cu) ----
 cudaError_t launch_grpo_token(const float *logp, const float *logp_old, const float *logp_ref,
                               const float *adv, const int64_t *targets, const int32_t *cu,
