@@ -80,8 +80,9 @@ typedef enum {
                                        to these inputs (results unspecified) */
 #define RK_DEVERR_RULES 0x8         /* a row's sampling rules are not usable: a request or
                                        mask index out of range, offsets that do not
-                                       ascend or leave their list, a temperature or
-                                       repetition penalty outside its range */
+                                       ascend or leave their list, too many biases, a
+                                       temperature or repetition penalty outside its
+                                       range */
 
 /* Element type of a matrix that is passed as void*. */
 typedef enum {
@@ -434,7 +435,8 @@ rk_status rk_linear_logp_bwd_full_saved(const uint16_t *h, const uint16_t *W,
  *   prompt_lengths    int32 [R]; NULL: no prompt, every token was produced
  *   bias_ids, bias_values  int64 / fp32 [num_bias]: request r's biases are entries
  *                     bias_offsets[r] .. bias_offsets[r+1] - 1; ids outside [0, V)
- *                     are passed over; an id listed twice takes its last value
+ *                     are passed over; an id listed twice takes its last value; at
+ *                     most 65534 per request
  *   bias_offsets      int64 [R + 1]
  *   mask              int32 [mask_rows, ceil(V / 32)]: bit v % 32 of word v / 32 set
  *                     = token v is allowed; bits past V are not read

@@ -5,23 +5,36 @@
 //
 // Decomposition.  A block works on a slice of kSliceCols columns and a run of
 // consecutive rows; each of its warps owns a segment of kSegCols columns of
-// that slice, and each lane kGroups groups of 8 columns of the segment (group
-// g of the segment = columns [8g, 8g + 8); lane l owns groups l, l + 32, ...).
-// For a lane's 32 columns a bit set tells which of them the rules touch
-// (seen before, or biased); the others need the temperature and the mask only.
+// that slice, and each lane 32 neighbouring columns of the segment: one word
+// of a grammar mask, and one word that tells which of them the rules touch
+// (seen before, or biased).  The others need the temperature and mask only.
+//
+// Data.  A warp copies its segment of the next rows into a ring of its own in
+// shared memory (cp.async, 16 bytes a lane, or 4 where rows are not 16-byte
+// aligned; the mask words with them) while it works on the present one, so no
+// barrier stands between the rows and a touched column's logit is a
+// shared-memory read.  What the rows say about themselves is read once per
+// block.  Results of
+// kApply and kBwd go out through shared memory too, so that a warp writes
+// whole lines although a lane owns 32 columns.  The lanes take their 16-byte
+// pieces in rotated order, which spreads a quarter warp over all banks.
 //
 // History.  The block counts a request's tokens of its slice in shared
 // memory (one word per column: bit 31 in the prompt, bits 0-30 times
-// produced).  Integer atomics only, so the order does not matter.  Rows of
-// one request with growing prefixes (a packed training sequence) add the new
-// token or two to the counts they have: each lane then updates its own
-// columns, without a barrier.  Any other change counts anew.
+// produced).  Integer atomics only, so the order does not matter.  A row that
+// has one token more than the row before (a packed training sequence) adds it
+// to the counts without a barrier: its column belongs to one lane.  Longer
+// steps add their tokens block-wide; any other change counts anew.  Each warp
+// lists its touched columns in ascending order, 32 of which its lanes take at
+// a time: text is made of few tokens, which sit at the low ids, so lanes that
+// looped over their own columns would wait for the first lane's 32.
 //
 // Batch invariance: a row's partial (max, sum) of a segment is formed by a
 // tree fixed by the column index alone, and the segments' partials are merged
 // in a fixed order: nothing depends on T, on where the row sits or on how the
 // rows were cut into runs.
 #include <algorithm>
+#include <cfloat>
 
 #include "rk_device.cuh"
 #include "rk_internal.h"
@@ -29,14 +42,16 @@
 namespace rk {
 namespace {
 
-constexpr int kGroups = 4;                    // groups of 8 columns per lane
-constexpr int kSegCols = 32 * 8 * kGroups;    // 1024 columns per warp
+constexpr int kLaneCols = 32;
+constexpr int kSegCols = 32 * kLaneCols;       // 1024 columns per warp
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSliceCols = kSegCols * kWarps;  // 8192 columns per block
 constexpr int kMaxRun = 64;                    // rows per block at most
-constexpr int kInlineTokens = 4;  // new tokens that lanes add on their own
+constexpr int kMaxBiases = 65534;  // per request: indices are kept in 16 bits
 constexpr uint32_t kPromptBit = 0x80000000u;
+constexpr uint32_t kNegInf2 = 0xFF80FF80u;  // two bf16 -inf
+constexpr uint32_t kLowest2 = 0xFF7FFF7Fu;  // two bf16 lowest finite values
 
 enum RulesOp { kApply, kLogp, kBwd };
 
@@ -48,7 +63,7 @@ struct RulesIo {
     int num_seqs;
     int64_t T, V;
     int run;         // rows per block
-    int vec_in;      // 16-byte loads of a group are aligned
+    int vec_in;      // every row starts on a 16-byte boundary
     const float *lse, *grad;  // kBwd
     void *out;       // kApply, kBwd
     int64_t ld_out;
@@ -58,25 +73,38 @@ struct RulesIo {
     unsigned *err;
 };
 
-// What a row says about itself.  `ok` is false when an index is out of range.
+// What a row says about itself.
+constexpr int32_t kInactive = -1, kBadTarget = -2, kBadRules = -3;
 struct RowInfo {
-    int64_t tgt;
+    int32_t tgt;  // the target, or one of the codes above
     int32_t req, len, mrow;
-    bool active, ok;
+    // how its history differs from the row before: by one token, by none, or
+    // else (kAnew); a token outside the vocabulary counts as none
+    int32_t step;
+    int32_t step_prompt;
+    float lse, g;
 };
+constexpr int32_t kNoToken = -1, kAnew = -2;
 
 template <RulesOp OP>
 __device__ __forceinline__ RowInfo row_info(const RulesIo &io, const rk_logits_rules &r, int64_t t) {
+    const int64_t tgt = (OP == kApply) ? 0 : io.targets[t];
     RowInfo i;
-    i.tgt = (OP == kApply) ? 0 : io.targets[t];
-    i.active = OP == kApply || row_active(t, i.tgt, io.cu, io.num_seqs);
     i.req = r.row_request ? r.row_request[t] : (r.num_requests > 0 ? (int32_t)t : 0);
-    if (r.row_request && i.req == -1) i.active = false;
     i.len = r.row_length ? max(r.row_length[t], 0) : 0x7fffffff;
     i.mrow = r.mask ? (r.row_mask ? r.row_mask[t] : (int32_t)t) : -1;
-    i.ok = (r.num_requests == 0 && !r.row_request) || (i.req >= 0 && i.req < r.num_requests) ||
-           (r.num_requests == 0 && i.req >= 0);
-    i.ok = i.ok && (i.mrow < 0 || i.mrow < r.mask_rows);
+    i.tgt = (int32_t)tgt;
+    i.step = kAnew;
+    i.step_prompt = 0;
+    i.lse = OP == kBwd ? io.lse[t] : 0.f;
+    i.g = OP == kBwd ? io.grad[t] : 0.f;
+    if ((OP != kApply && !row_active(t, tgt, io.cu, io.num_seqs)) || (r.row_request && i.req == -1))
+        i.tgt = kInactive;
+    else if (i.req < 0 || (r.num_requests > 0 && i.req >= r.num_requests) ||
+             (i.mrow >= 0 && i.mrow >= r.mask_rows))
+        i.tgt = kBadRules;
+    else if (tgt >= io.V)
+        i.tgt = kBadTarget;
     return i;
 }
 
@@ -120,7 +148,7 @@ __device__ __forceinline__ Request load_request(const rk_logits_rules &r, int32_
     s.nbias = 0;
     if (any && r.bias_ids) {
         const int64_t a = r.bias_offsets[q], b = r.bias_offsets[q + 1];
-        if (a >= 0 && b >= a && b <= r.num_bias && b - a < 0x7fffffff) {
+        if (a >= 0 && b >= a && b <= r.num_bias && b - a <= kMaxBiases) {
             s.bias0 = a;
             s.nbias = (int32_t)(b - a);
         } else {
@@ -128,6 +156,25 @@ __device__ __forceinline__ Request load_request(const rk_logits_rules &r, int32_
         }
     }
     return s;
+}
+
+// row.step and row.step_prompt, given the row before.
+__device__ __forceinline__ void find_step(const RulesIo &io, const rk_logits_rules &r,
+                                          const RowInfo &before, RowInfo &row) {
+    if (row.tgt < 0 || before.tgt < 0 || row.req != before.req) return;
+    row.step = kNoToken;
+    if (r.num_requests == 0 || !r.tokens) return;
+    const int64_t a = r.token_offsets[row.req], b = r.token_offsets[row.req + 1];
+    if (!(a >= 0 && b >= a && b <= r.num_tokens && b - a < 0x7fffffff)) return;  // refused by load_request
+    const int32_t ntok = (int32_t)(b - a), len = min(row.len, ntok), was = min(before.len, ntok);
+    if (len == was) return;
+    if (len != was + 1) {
+        row.step = kAnew;
+        return;
+    }
+    const int64_t v = r.tokens[a + was];
+    if (v >= 0 && v < io.V) row.step = (int32_t)v;
+    row.step_prompt = r.prompt_lengths && was < r.prompt_lengths[row.req];
 }
 
 // y of a touched column from z, its count word and its bias.
@@ -139,70 +186,54 @@ __device__ __forceinline__ float rule_y(float z, uint32_t w, float bias, const R
     return __fadd_rn(y, bias);
 }
 
-__device__ __forceinline__ float load_elem(const uint16_t *p) { return bf16_bits_to_f32(*p); }
-__device__ __forceinline__ float load_elem(const float *p) { return *p; }
+// ---- elements and 16-byte pieces in shared memory ----
 
-// One group of 8 columns; columns without a bit in `live` are not read.
-__device__ __forceinline__ void load_group(const uint16_t *p, bool vec, uint32_t live, float (&z)[8]) {
-    if (vec && live == 0xffu) {
-        const uint4 w = reinterpret_cast<const uint4 *>(p)[0];
-        const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            z[2 * j] = bf16_lo(q[j]);
-            z[2 * j + 1] = bf16_hi(q[j]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = (live >> j & 1u) ? load_elem(p + j) : -INFINITY;
-    }
-}
-__device__ __forceinline__ void load_group(const float *p, bool vec, uint32_t live, float (&z)[8]) {
-    if (vec && live == 0xffu) {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0];
-        const float4 b = reinterpret_cast<const float4 *>(p)[1];
-        z[0] = a.x; z[1] = a.y; z[2] = a.z; z[3] = a.w;
-        z[4] = b.x; z[5] = b.y; z[6] = b.z; z[7] = b.w;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = (live >> j & 1u) ? load_elem(p + j) : -INFINITY;
-    }
-}
-
-__device__ __forceinline__ void store_elem(uint16_t *p, float v) {
+__device__ __forceinline__ float elem(const uint16_t *p) { return bf16_bits_to_f32(*p); }
+__device__ __forceinline__ float elem(const float *p) { return *p; }
+__device__ __forceinline__ void put(uint16_t *p, float v) {
     *p = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
 }
-__device__ __forceinline__ void store_elem(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
 
-// One group of 8 columns; columns without a bit in `inside` are not written.
-__device__ __forceinline__ void store_group(uint16_t *p, bool vec, uint32_t inside, const float (&x)[8]) {
-    if (vec && inside == 0xffu) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                   pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (inside >> j & 1u) store_elem(p + j, x[j]);
-    }
+// Pairs of fp32 (one instruction for both).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
 }
-__device__ __forceinline__ void store_group(float *p, bool vec, uint32_t inside, const float (&x)[8]) {
-    if (vec && inside == 0xffu) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (inside >> j & 1u) store_elem(p + j, x[j]);
-    }
+__device__ __forceinline__ void unpair(uint64_t p, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
 }
-
-// exp(y / temperature - lse), 1 / temperature = itau + i1.  -inf stays out of
-// the product with i1, whose sign it would take.
-__device__ __forceinline__ float prob(float y, float itau, float i1, float lse) {
-    const float v = y < -3.3e38f ? -3.3e38f : y;
-    return ex2(__fmul_rn(__fmaf_rn(v, i1, __fmaf_rn(v, itau, -lse)), kLog2e));
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
-
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
@@ -214,288 +245,559 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Shared memory: the slice's count words, its bias values when there are
-// biases, and per lane the touched bits.
-struct Shared {
-    uint32_t *count;    // [kSliceCols]
-    int32_t *bias;    // [kSliceCols], or null: first 1 + entry index, then the value's bits
-    uint32_t *touched;  // [kThreads]
+// A lane's 32 columns as 16-byte pieces.  Piece register i holds piece
+// order(i) of the lane: rotated by lane so that the eight lanes of a quarter
+// warp read eight different bank groups.
+template <typename T>
+struct Lane;
+template <>
+struct Lane<uint16_t> {
+    static constexpr int kPieces = 4, kCols = 8;  // pieces, columns of a piece
+    static __device__ __forceinline__ int order(int lane, int i) { return (i + (lane >> 1)) & 3; }
+    static __device__ __forceinline__ int bits(int lane) { return 8 * ((lane >> 1) & 3); }
+};
+template <>
+struct Lane<float> {
+    static constexpr int kPieces = 8, kCols = 4;
+    static __device__ __forceinline__ int order(int lane, int i) { return (i + lane) & 7; }
+    static __device__ __forceinline__ int bits(int lane) { return 4 * (lane & 7); }
 };
 
-// Sets a slice column's touched bit (any thread).
-__device__ __forceinline__ void mark(const Shared &sh, int c) {
-    const int g = (c & (kSegCols - 1)) >> 3;
-    atomicOr(&sh.touched[(c / kSegCols) * 32 + (g & 31)], 1u << ((g >> 5) * 8 + (c & 7)));
+// One ring stage: the segment, 16 bytes more for rows that start on an odd
+// element (they sit one element further in), and the segment's mask words.
+template <typename T>
+constexpr int mask_at() { return kSegCols * (int)sizeof(T) + 16; }
+template <typename T>
+constexpr int stage_bytes() { return mask_at<T>() + kSegCols / 8; }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The column of a segment that bit k of a lane stands for.
-__device__ __forceinline__ int lane_column(int lane, int k) {
-    return 8 * (lane + 32 * (k >> 3)) + (k & 7);
+// Whether a row starts on an odd 2-byte element.
+__device__ __forceinline__ bool odd_start(const uint16_t *src) {
+    return (reinterpret_cast<uintptr_t>(src) & 2) != 0;
+}
+__device__ __forceinline__ bool odd_start(const float *) { return false; }
+
+// Starts the copy of `cols` columns from src into a stage (2 bytes into it
+// after an odd start).  Nothing outside [src, src + cols) is read.
+template <typename T>
+__device__ __forceinline__ void start_copy(unsigned char *stage, const T *src, int cols, bool vec,
+                                           int lane) {
+    const uint32_t dst = smem_u32(stage);
+    if (vec) {
+        constexpr int kPer = 16 / (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < kSegCols / kPer / 32; ++i) {
+            const int c = (lane + 32 * i) * kPer;
+            const int n = min(kPer, cols - c);
+            if (n > 0) cp_async16(dst + c * (int)sizeof(T), src + c, n * (int)sizeof(T));
+        }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll 8
+        for (int c = lane; c < cols; c += 32) cp_async4(dst + 4 * c, src + c);
+    } else {
+        // words on 4-byte boundaries; a word that the row does not fill is
+        // copied by element
+        const int odd = odd_start(src) ? 1 : 0;
+        uint16_t *d = reinterpret_cast<uint16_t *>(stage);
+#pragma unroll 8
+        for (int w = lane; 2 * w < cols + odd; w += 32) {
+            const int c = 2 * w - odd;  // its first column
+            if (c >= 0 && c + 1 < cols) {
+                cp_async4(dst + 4 * w, src + c);
+            } else {
+                if (c >= 0) d[2 * w] = src[c];
+                if (c + 1 < cols) d[2 * w + 1] = src[c + 1];
+            }
+        }
+    }
+}
+
+// Piece i of a lane, from a stage; `odd`: it sits one element further in.
+__device__ __forceinline__ uint4 load_piece(const unsigned char *p, bool odd) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    if (!odd) return a;
+    const uint32_t b = *reinterpret_cast<const uint32_t *>(p + 16);
+    return make_uint4(__funnelshift_r(a.x, a.y, 16), __funnelshift_r(a.y, a.z, 16),
+                      __funnelshift_r(a.z, a.w, 16), __funnelshift_r(a.w, b, 16));
+}
+
+// ---- history ----
+
+// Shared memory of a block.
+struct Shared {
+    uint32_t *count;    // [kSliceCols]
+    uint32_t *touched;  // [kThreads]: bit c % 32 of word c / 32 for slice column c
+    uint16_t *list;     // [kSliceCols]: each warp's touched columns, ascending
+    uint16_t *bias;     // [kSliceCols], or null: 1 + the index of the column's bias, 0: none
+};
+
+__device__ __forceinline__ void mark(const Shared &sh, int c) {
+    atomicOr(&sh.touched[c >> 5], 1u << (c & 31));
 }
 
 // Block-wide: tokens [from, to) of the request into the counts of columns
 // [slice0, slice0 + width).
 __device__ __forceinline__ void count_tokens(const Shared &sh, const Request &q, int32_t from,
                                              int32_t to, int64_t slice0, int width) {
-    for (int32_t i = from + (int32_t)threadIdx.x; i < to; i += kThreads) {
-        const int64_t c = q.tokens[i] - slice0;
-        if (c >= 0 && c < width) {
-            if (i < q.prompt)
-                atomicOr(&sh.count[c], kPromptBit);
-            else
-                atomicAdd(&sh.count[c], 1u);
-            mark(sh, (int)c);
+    constexpr int kBatch = 8;  // loads in flight per thread
+    for (int32_t i0 = from + (int32_t)threadIdx.x; i0 < to; i0 += kBatch * kThreads) {
+        int64_t v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) v[k] = i0 + k * kThreads < to ? q.tokens[i0 + k * kThreads] : -1;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t c = v[k] - slice0;
+            if (v[k] >= 0 && c >= 0 && c < width) {
+                if (i0 + k * kThreads < q.prompt)
+                    atomicOr(&sh.count[c], kPromptBit);
+                else
+                    atomicAdd(&sh.count[c], 1u);
+                mark(sh, (int)c);
+            }
         }
+    }
+}
+
+// Block-wide: the request's first `len` tokens and its biases from scratch.
+// Of biases for one column the last counts: the count words find it first.
+__device__ __forceinline__ void count_request(const Shared &sh, const rk_logits_rules &rules,
+                                              const Request &q, int32_t len, int64_t slice0, int width) {
+    __syncthreads();
+    for (int k = threadIdx.x; k < kSliceCols / 4; k += kThreads)
+        reinterpret_cast<uint4 *>(sh.count)[k] = make_uint4(0, 0, 0, 0);
+    sh.touched[threadIdx.x] = 0;
+    if (sh.bias)
+        for (int k = threadIdx.x; k < kSliceCols / 8; k += kThreads)
+            reinterpret_cast<uint4 *>(sh.bias)[k] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    if (q.nbias > 0) {
+        for (int k = threadIdx.x; k < q.nbias; k += kThreads) {
+            const int64_t v = rules.bias_ids[q.bias0 + k], c = v - slice0;
+            if (v >= 0 && c >= 0 && c < width) {
+                atomicMax(&sh.count[c], (uint32_t)(k + 1));
+                mark(sh, (int)c);
+            }
+        }
+        __syncthreads();
+        for (uint32_t b = sh.touched[threadIdx.x]; b; b &= b - 1) {
+            const int c = threadIdx.x * kLaneCols + __ffs(b) - 1;
+            sh.bias[c] = (uint16_t)sh.count[c];
+            sh.count[c] = 0;
+        }
+        __syncthreads();
+    }
+    count_tokens(sh, q, 0, len, slice0, width);
+    __syncthreads();
+}
+
+// A warp's list of its touched columns (segment columns, ascending) from its
+// lanes' bits; returns their number.
+__device__ __forceinline__ int make_list(uint16_t *list, uint32_t touched, int lane) {
+    const int mine = __popc(touched);
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+    }
+    int at = incl - mine;
+    for (uint32_t b = touched; b; b &= b - 1)
+        list[at++] = (uint16_t)(lane * kLaneCols + __ffs(b) - 1);
+    return __shfl_sync(0xffffffffu, incl, 31);
+}
+
+// exp(y / temperature - lse), 1 / temperature = itau + i1.  -inf stays out of
+// the product with i1, whose sign it would take.
+__device__ __forceinline__ float prob(float y, float itau, float i1, float lse) {
+    const float v = max_nan(y, -FLT_MAX);
+    return ex2(__fmul_rn(__fmaf_rn(v, i1, __fmaf_rn(v, itau, -lse)), kLog2e));
+}
+
+// bf16 pieces: where a pair's two bits in `keep` are 0, -inf.  Byte i of `keep`
+// belongs to piece i, bit j of it to column j.
+__device__ __forceinline__ void keep_columns(uint4 (&w)[4], uint32_t keep) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        // the sign bit of byte i of a (of b) is bit 2j (2j + 1) of piece i
+        const uint32_t a = keep << (7 - 2 * j), b = keep << (6 - 2 * j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t m;  // each byte: the sign of byte i of a, twice, and of b, twice
+            asm("prmt.b32 %0, %1, %2, %3;" : "=r"(m) : "r"(a), "r"(b), "r"(0xCC88 + 0x1111 * i));
+            uint32_t &q = j == 0 ? w[i].x : j == 1 ? w[i].y : j == 2 ? w[i].z : w[i].w;
+            q = (q & m) | (kNegInf2 & ~m);
+        }
+    }
+}
+
+__device__ __forceinline__ void unpack(const uint4 &w, uint64_t (&z)[4]) {
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] = pair(bf16_lo(q[j]), bf16_hi(q[j]));
+}
+
+template <RulesOp OP, typename TIn, typename TOut>
+struct Config {
+    static constexpr int kStages = 2;
+    static constexpr int kOutBytes = OP == kLogp ? 0 : kSegCols * (int)sizeof(TOut);
+    // fp32 results of bf16 pieces: neighbouring lanes would write the same bank
+    // group, so odd lanes swap neighbouring pieces
+    static constexpr int kSwap = (sizeof(TIn) == 2 && sizeof(TOut) == 4) ? 1 : 0;
+    static constexpr int kWarpBytes = kStages * stage_bytes<TIn>() + kOutBytes;
+    static size_t smem(bool bias) {
+        return (size_t)(kSliceCols + kThreads) * 4 + kMaxRun * sizeof(RowInfo) +
+               (size_t)kSliceCols * (bias ? 4 : 2) + (size_t)kWarps * kWarpBytes;
+    }
+};
+
+// Writes `cols` results of a segment from the warp's staging area to dst.
+template <int SWAP>
+__device__ __forceinline__ void write_out(const unsigned char *stage, float *dst, int cols, bool vec,
+                                          int lane) {
+    const float4 *s4 = reinterpret_cast<const float4 *>(stage);
+    if (vec && cols == kSegCols) {
+#pragma unroll
+        for (int i = 0; i < kSegCols / 128; ++i) {
+            const int x = lane + 32 * i;
+            reinterpret_cast<float4 *>(dst)[x] = s4[x ^ (SWAP ? (x >> 3) & 1 : 0)];
+        }
+    } else {
+        const float *s = reinterpret_cast<const float *>(stage);
+#pragma unroll 8
+        for (int c = lane; c < cols; c += 32) dst[c] = s[c ^ (SWAP ? ((c >> 5) & 1) << 2 : 0)];
+    }
+}
+template <int SWAP>
+__device__ __forceinline__ void write_out(const unsigned char *stage, uint16_t *dst, int cols,
+                                          bool vec, int lane) {
+    if (vec && cols == kSegCols) {
+#pragma unroll
+        for (int i = 0; i < kSegCols / 256; ++i)
+            reinterpret_cast<uint4 *>(dst)[lane + 32 * i] =
+                reinterpret_cast<const uint4 *>(stage)[lane + 32 * i];
+    } else {
+        const uint16_t *s = reinterpret_cast<const uint16_t *>(stage);
+#pragma unroll 8
+        for (int c = lane; c < cols; c += 32) dst[c] = s[c];
     }
 }
 
 template <RulesOp OP, typename TIn, typename TOut>
 __global__ void __launch_bounds__(kThreads)
     rules_kernel(const __grid_constant__ RulesIo io, const __grid_constant__ rk_logits_rules rules) {
+    using C = Config<OP, TIn, TOut>;
+    using L = Lane<TIn>;
     extern __shared__ uint4 smem[];
     Shared sh;
     sh.count = reinterpret_cast<uint32_t *>(smem);
     sh.touched = sh.count + kSliceCols;
-    sh.bias = rules.bias_ids ? reinterpret_cast<int32_t *>(sh.touched + kThreads) : nullptr;
+    RowInfo *rows = reinterpret_cast<RowInfo *>(sh.touched + kThreads);
+    sh.list = reinterpret_cast<uint16_t *>(rows + kMaxRun);
+    sh.bias = rules.bias_ids ? sh.list + kSliceCols : nullptr;
+    unsigned char *p = reinterpret_cast<unsigned char *>(sh.list + (rules.bias_ids ? 2 : 1) * kSliceCols);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned char *ring = p + warp * C::kWarpBytes;
+    unsigned char *staged = ring + C::kStages * stage_bytes<TIn>();
     // Launched with programmatic stream serialisation: wait until the previous
     // kernel of the stream has completed before reading or writing anything.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t slices = (io.V + kSliceCols - 1) / kSliceCols;
     const int64_t slice0 = (int64_t)(blockIdx.x % slices) * kSliceCols;
     const int width = (int)min((int64_t)kSliceCols, io.V - slice0);
-    const int64_t seg0 = slice0 + (int64_t)warp * kSegCols;
-    const int64_t nseg = (io.V + kSegCols - 1) / kSegCols;
     const int64_t t0 = (int64_t)(blockIdx.x / slices) * io.run;
-    const int64_t t1 = min(io.T, t0 + io.run);
-    const bool first_thread = slice0 == 0 && threadIdx.x == 0;
-
-    // this lane's columns that exist
-    uint32_t inside = 0;
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-        const int64_t left = io.V - (seg0 + 8 * (lane + 32 * i));
-        inside |= (left >= 8 ? 0xffu : left > 0 ? (1u << left) - 1u : 0u) << (8 * i);
-    }
+    const int n = (int)min((int64_t)io.run, io.T - t0);
+    const int64_t seg0 = slice0 + (int64_t)warp * kSegCols;
+    const int cols = (int)max((int64_t)0, min((int64_t)kSegCols, io.V - seg0));  // of this warp
+    const int64_t nseg = (io.V + kSegCols - 1) / kSegCols;
     const int64_t words = (io.V + 31) / 32;
+    const int own = lane * kLaneCols;  // the lane's first column in the segment
+    const uint32_t inside =
+        cols >= own + 32 ? 0xffffffffu : cols > own ? (1u << (cols - own)) - 1u : 0u;
+    uint32_t *count = sh.count + warp * kSegCols;  // of the segment
+    const uint16_t *bias = sh.bias ? sh.bias + warp * kSegCols : nullptr;
+    uint16_t *list = sh.list + warp * kSegCols;
+
+    for (int k = threadIdx.x; k < n; k += kThreads) rows[k] = row_info<OP>(io, rules, t0 + k);
+    __syncthreads();
+
+    const TIn *zseg = reinterpret_cast<const TIn *>(io.logits) + t0 * io.ld + seg0;
+    auto prefetch = [&](int k) {
+        if (k < n && rows[k].tgt >= 0) {
+            unsigned char *stage = ring + (k % C::kStages) * stage_bytes<TIn>();
+            start_copy(stage, zseg + k * io.ld, cols, io.vec_in, lane);
+            if (rows[k].mrow >= 0 && inside)
+                cp_async4(smem_u32(stage + mask_at<TIn>()) + 4 * lane,
+                          rules.mask + (int64_t)rows[k].mrow * words + (seg0 >> 5) + lane);
+        }
+        cp_commit();
+    };
+    for (int k = 0; k < C::kStages - 1; ++k) prefetch(k);
+    for (int k = threadIdx.x + 1; k < n; k += kThreads) find_step(io, rules, rows[k - 1], rows[k]);
+    __syncthreads();
 
     int32_t cur = -1, counted = 0;
     uint32_t touched = 0;
+    int listed = 0;  // touched columns of the warp
     Request q{};
-    for (int64_t t = t0; t < t1; ++t) {
-        const RowInfo row = row_info<OP>(io, rules, t);
-        TOut *orow = reinterpret_cast<TOut *>(io.out) + t * io.ld_out;
-        bool ok = row.ok && (OP == kApply || row.tgt < io.V);
-        if (row.active && row.ok) {
+    for (int k = 0; k < n; ++k) {
+        const RowInfo row = rows[k];
+        const int64_t t = t0 + k;
+        bool ok = row.tgt >= 0;
+        if (ok && (row.req != cur || (q.ok && row.step == kAnew))) {
             const bool other = row.req != cur;
             if (other) {
                 q = load_request(rules, row.req);
                 cur = row.req;
             }
-            const int32_t len = min(row.len, q.ntok);
-            if (q.ok && (other || len < counted)) {  // count from the start
-                __syncthreads();
-                for (int k = threadIdx.x; k < kSliceCols / 4; k += kThreads)
-                    reinterpret_cast<uint4 *>(sh.count)[k] = make_uint4(0, 0, 0, 0);
-                if (sh.bias)
-                    for (int k = threadIdx.x; k < kSliceCols / 4; k += kThreads)
-                        reinterpret_cast<uint4 *>(sh.bias)[k] = make_uint4(0, 0, 0, 0);
-                sh.touched[threadIdx.x] = 0;
-                __syncthreads();
-                for (int k = threadIdx.x; k < q.nbias; k += kThreads) {
-                    const int64_t c = rules.bias_ids[q.bias0 + k] - slice0;
-                    if (c >= 0 && c < width) {
-                        atomicMax(&sh.bias[c], k + 1);
-                        mark(sh, (int)c);
-                    }
+            if (q.ok) {
+                const int32_t len = min(row.len, q.ntok);
+                if (other || len < counted) {
+                    count_request(sh, rules, q, len, slice0, width);
+                } else {
+                    __syncthreads();
+                    sh.touched[threadIdx.x] = touched;
+                    __syncthreads();
+                    count_tokens(sh, q, counted, len, slice0, width);
+                    __syncthreads();
                 }
-                count_tokens(sh, q, 0, len, slice0, width);
-                __syncthreads();
+                counted = len;
                 touched = sh.touched[threadIdx.x];
-                if (sh.bias)  // entry indices to values, by each column's lane
-                    for (uint32_t b = touched; b; b &= b - 1) {
-                        int32_t *p = &sh.bias[warp * kSegCols + lane_column(lane, __ffs(b) - 1)];
-                        if (*p > 0) *p = __float_as_int(rules.bias_values[q.bias0 + *p - 1]);
-                    }
-            } else if (q.ok && len - counted <= kInlineTokens) {  // each lane its own columns
-                for (int32_t i = counted; i < len; ++i) {
-                    const int64_t c = q.tokens[i] - seg0;
-                    if (c >= 0 && c < kSegCols && seg0 + c < io.V && ((c >> 3) & 31) == lane) {
-                        uint32_t *w = &sh.count[warp * kSegCols + c];
-                        *w = i < q.prompt ? (*w | kPromptBit) : *w + 1u;
-                        touched |= 1u << ((c >> 8) * 8 + (c & 7));
-                    }
-                }
-            } else if (q.ok) {  // add the new tokens
-                __syncthreads();
-                sh.touched[threadIdx.x] = touched;
-                __syncthreads();
-                count_tokens(sh, q, counted, len, slice0, width);
-                __syncthreads();
-                touched = sh.touched[threadIdx.x];
+                listed = make_list(list, touched, lane);
             }
-            if (q.ok) counted = len;
-            ok = ok && q.ok;
-        }
-        if (!row.active) {
-            if (OP == kBwd) {
-                const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < kGroups; ++i)
-                    store_group(orow + seg0 + 8 * (lane + 32 * i), io.vec_out, inside >> (8 * i) & 0xffu,
-                                zero);
+        } else if (ok && q.ok) {
+            counted = min(row.len, q.ntok);
+            const int64_t c = row.step - seg0;  // negative where there is no token
+            if (row.step >= 0 && c >= 0 && c < cols) {
+                const uint32_t bit = (c >> 5) == lane ? 1u << (c & 31) : 0u;
+                if (bit) count[c] = row.step_prompt ? (count[c] | kPromptBit) : count[c] + 1u;
+                const bool fresh = (bit & ~touched) != 0;
+                touched |= bit;
+                if (__any_sync(0xffffffffu, fresh)) listed = make_list(list, touched, lane);
             }
-            continue;
         }
+        ok = ok && q.ok;
+        // the row's stage is complete once all but the newest copies are
+        prefetch(k + C::kStages - 1);
+        cp_wait<C::kStages - 1>();
+        __syncwarp();
+        TOut *orow = reinterpret_cast<TOut *>(io.out) + t * io.ld_out + seg0;
         if (!ok) {
-            const float nan = __int_as_float(0x7fc00000);
-            if (first_thread)
-                atomicOr(io.err, OP != kApply && row.tgt >= io.V ? kErrTargetRange : kErrRules);
-            if (OP == kLogp) {
-                if (lane == 0 && seg0 < io.V) io.part[t * nseg + seg0 / kSegCols] = make_float2(0.f, nan);
-                if (first_thread) io.ytgt[t] = nan;
-            } else {
-                const float x[8] = {nan, nan, nan, nan, nan, nan, nan, nan};
-#pragma unroll
-                for (int i = 0; i < kGroups; ++i)
-                    store_group(orow + seg0 + 8 * (lane + 32 * i), io.vec_out, inside >> (8 * i) & 0xffu,
-                                x);
+            const float fill = row.tgt == kInactive ? 0.f : __int_as_float(0x7fc00000);
+            if (row.tgt != kInactive) {
+                if (slice0 == 0 && threadIdx.x == 0)
+                    atomicOr(io.err, row.tgt == kBadTarget ? kErrTargetRange : kErrRules);
+                if (OP == kLogp && lane == 0 && cols > 0) {
+                    io.part[t * nseg + seg0 / kSegCols] = make_float2(0.f, fill);
+                    if (seg0 == 0) io.ytgt[t] = fill;
+                }
             }
+            if (OP == kBwd || (OP == kApply && row.tgt != kInactive))
+                for (int c = lane; c < cols; c += 32) put(orow + c, fill);
             continue;
         }
-
-        // this lane's columns that the mask allows
-        uint32_t live = inside;
-        if (row.mrow >= 0) {
-            const uint8_t *m = reinterpret_cast<const uint8_t *>(rules.mask + (int64_t)row.mrow * words);
-            uint32_t allowed = 0;
+        const unsigned char *stage = ring + (k % C::kStages) * stage_bytes<TIn>();
+        const bool odd = !io.vec_in && odd_start(zseg + k * io.ld);
+        const TIn *zs = reinterpret_cast<const TIn *>(stage) + (odd ? 1 : 0);
+        const uint32_t *masks = reinterpret_cast<const uint32_t *>(stage + mask_at<TIn>());
+        const bool masked = row.mrow >= 0;
+        const uint32_t live = masked ? inside & masks[lane] : inside;  // columns the mask allows
+        // a listed column's y from its logit z (false: masked)
+        auto listed_y = [&](int j, float &z, uint32_t &cw, float &y) {
+            if (masked && !(masks[j >> 5] >> (j & 31) & 1u)) return false;
+            z = elem(zs + j);
+            cw = count[j];
+            const int bi = bias ? bias[j] : 0;
+            y = rule_y(z, cw, bi ? rules.bias_values[q.bias0 + bi - 1] : 0.f, q);
+            return true;
+        };
+        const int rot = L::bits(lane);
+        uint4 w[L::kPieces];
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i)
-                if (inside >> (8 * i) & 0xffu)
-                    allowed |= (uint32_t)m[(seg0 >> 3) + lane + 32 * i] << (8 * i);
-            live &= allowed;
-        }
-        const TIn *zrow = reinterpret_cast<const TIn *>(io.logits) + t * io.ld;
-        float z[kGroups][8];
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i)
-            load_group(zrow + seg0 + 8 * (lane + 32 * i), io.vec_in, inside >> (8 * i) & 0xffu, z[i]);
+        for (int i = 0; i < L::kPieces; ++i)
+            w[i] = load_piece(stage + 16 * (lane * L::kPieces + L::order(lane, i)), odd);
 
-        const uint32_t special = touched & live;
         if (OP == kLogp) {
             const float c = __fmul_rn(kLog2e, q.itau);
+            const int tcol = row.tgt >= seg0 && row.tgt < seg0 + cols ? row.tgt - (int)seg0 : -1;
+            // touched columns: running maximum and sum, each lane its share of the list
+            float mt = -INFINITY, st = 0.f;
+            for (int e = lane; e < listed; e += 32) {
+                const int j = list[e];
+                float z, y = -INFINITY;
+                uint32_t cw;
+                const bool allowed = listed_y(j, z, cw, y);
+                if (j == tcol) io.ytgt[t] = y;
+                if (!allowed || y == -INFINITY) continue;  // masked, or banned by its bias
+                const float mn = fmaxf(mt, y);
+                st = __fmaf_rn(st, ex2(__fmul_rn(__fsub_rn(mt, mn), c)),
+                               ex2(__fmul_rn(__fsub_rn(y, mn), c)));
+                mt = mn;
+            }
             // untouched columns: one maximum, then the terms relative to it
             const uint32_t plain = live & ~touched;
-            float m = -INFINITY;
+            if (tcol >= 0 && (tcol >> 5) == lane && !(touched >> (tcol & 31) & 1u))
+                io.ytgt[t] = plain >> (tcol & 31) & 1u ? elem(zs + tcol) : -INFINITY;
+            const uint32_t keep = __funnelshift_r(plain, plain, rot);
+            float m;
+            if constexpr (sizeof(TIn) == 2) {
+                if (!__all_sync(0xffffffffu, plain == 0xffffffffu)) keep_columns(w, keep);
+                uint32_t x[4];
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i)
+                for (int i = 0; i < 4; ++i)
+                    x[i] = max_bf16x2(max_bf16x2(w[i].x, w[i].y), max_bf16x2(w[i].z, w[i].w));
+                x[0] = max_bf16x2(max_bf16x2(x[0], x[1]), max_bf16x2(x[2], x[3]));
+                m = fmaxf(bf16_lo(x[0]), bf16_hi(x[0]));
+            } else {
+                float x[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (!(plain >> (8 * i + j) & 1u)) z[i][j] = -INFINITY;
-                    m = fmaxf(m, z[i][j]);
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t *f = &w[i].x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if ((int32_t)(keep << (31 - 4 * i - j)) >= 0) f[j] = 0xff800000u;
+                    x[i] = fmaxf(fmaxf(__uint_as_float(w[i].x), __uint_as_float(w[i].y)),
+                                 fmaxf(__uint_as_float(w[i].z), __uint_as_float(w[i].w)));
                 }
-            // touched columns: running maximum and sum, in column order
-            float mt = -INFINITY, st = 0.f;
-            const int64_t tc = row.tgt - seg0;
-            const bool mine = tc >= 0 && tc < kSegCols && ((tc >> 3) & 31) == lane;
-            const int tbit = mine ? (int)((tc >> 8) * 8 + (tc & 7)) : -1;
-            float yt = -INFINITY;
-            uint32_t b = special;
-            while (b) {
-                const int k = __ffs(b) - 1;
-                b &= b - 1;
-                const int sc = warp * kSegCols + lane_column(lane, k);
-                const float y = rule_y(load_elem(zrow + slice0 + sc), sh.count[sc],
-                                       sh.bias ? __int_as_float(sh.bias[sc]) : 0.f, q);
-                if (k == tbit) yt = y;
-                if (y == -INFINITY) continue;  // banned by its bias
-                if (y > mt) {
-                    st = __fadd_rn(__fmul_rn(st, ex2(__fmul_rn(__fsub_rn(mt, y), c))),
-                                   ex2(__fmul_rn(__fsub_rn(y, y), c)));  // 1, or NaN for inf
-                    mt = y;
-                } else {
-                    st = __fadd_rn(st, ex2(__fmul_rn(__fsub_rn(y, mt), c)));
-                }
+                m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                          fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
             }
-            if (mine && (plain >> tbit & 1u)) yt = load_elem(zrow + row.tgt);
-            if (mine) io.ytgt[t] = yt;
             // terms relative to the segment's maximum: (z - m) c rather than one
             // fused z c - m c, whose product overflows next to the type's lowest
             // value, and with the maximum's own term exactly 1
             m = warp_max(fmaxf(m, mt));
             const float ref = m == -INFINITY ? 0.f : m;
-            float s = 0.f;
+            const uint64_t nref = pair(-ref, -ref), cc = pair(c, c);
+            uint64_t acc[2] = {0, 0};  // pairs of +0
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i) {
-                float e[8];
+            for (int i = 0; i < L::kPieces; ++i) {
+                uint64_t z[4];
+                if constexpr (sizeof(TIn) == 2) {
+                    unpack(w[i], z);
+                } else {
+                    z[0] = pair(__uint_as_float(w[i].x), __uint_as_float(w[i].y));
+                    z[1] = pair(__uint_as_float(w[i].z), __uint_as_float(w[i].w));
+                }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) e[j] = ex2(__fmul_rn(__fsub_rn(z[i][j], ref), c));
-                s = __fadd_rn(s, __fadd_rn(__fadd_rn(__fadd_rn(e[0], e[1]), __fadd_rn(e[2], e[3])),
-                                           __fadd_rn(__fadd_rn(e[4], e[5]), __fadd_rn(e[6], e[7]))));
+                for (int j = 0; j < L::kCols / 2; ++j) {
+                    float a, b;
+                    unpair(mul2(add2(z[j], nref), cc), a, b);
+                    acc[j & 1] = add2(acc[j & 1], pair(ex2(a), ex2(b)));
+                }
             }
+            float s0, s1;
+            unpair(add2(acc[0], acc[1]), s0, s1);
+            float s = __fadd_rn(s0, s1);
             s = __fadd_rn(s, mt == -INFINITY ? st : __fmul_rn(st, ex2(__fmul_rn(__fsub_rn(mt, ref), c))));
             s = warp_sum(s);
-            if (lane == 0 && seg0 < io.V) io.part[t * nseg + seg0 / kSegCols] = make_float2(m, s);
-        } else if (OP == kApply) {
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i) {
-                float x[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = (live >> (8 * i + j) & 1u) ? __fmul_rn(z[i][j], q.itau) : -INFINITY;
-                store_group(orow + seg0 + 8 * (lane + 32 * i), io.vec_out, inside >> (8 * i) & 0xffu, x);
-            }
-            uint32_t b = special;
-            while (b) {
-                const int k = __ffs(b) - 1;
-                b &= b - 1;
-                const int sc = warp * kSegCols + lane_column(lane, k);
-                const float y = rule_y(load_elem(zrow + slice0 + sc), sh.count[sc],
-                                       sh.bias ? __int_as_float(sh.bias[sc]) : 0.f, q);
-                store_elem(orow + slice0 + sc, __fmul_rn(y, q.itau));
-            }
+            if (lane == 0 && cols > 0) io.part[t * nseg + seg0 / kSegCols] = make_float2(m, s);
         } else {
-            const float l = io.lse[t];
-            const bool none = l == -INFINITY;  // the rules leave nothing
-            const float g = none ? 0.f : __fmul_rn(io.grad[t], q.itau);
+            const float l = row.lse;
+            const bool none = OP == kBwd && l == -INFINITY;  // the rules leave nothing
+            const float g = OP == kBwd && !none ? __fmul_rn(row.g, q.itau) : 0.f;
             // x - lse with 1 / temperature to 48 bits (itau + i1): the rounding of
             // 1 / temperature alone would weigh |x| times half a step
             const float i1 = __fmul_rn(__fmaf_rn(-q.tau, q.itau, 1.f), q.itau);
-            const float a = -g;
+            const uint32_t shown = none ? 0u : live;
+            const uint32_t keep = __funnelshift_r(shown, shown, rot);
+            const uint64_t it2 = pair(q.itau, q.itau);
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i) {
-                float d[8];
+            for (int i = 0; i < L::kPieces; ++i) {
+                constexpr int N = L::kCols;
+                uint64_t z[4];
+                float x[8];
+                if constexpr (sizeof(TIn) == 2) {
+                    if (OP == kBwd) {  // -inf out of the products (see prob)
+                        w[i].x = max_nan_bf16x2(w[i].x, kLowest2);
+                        w[i].y = max_nan_bf16x2(w[i].y, kLowest2);
+                        w[i].z = max_nan_bf16x2(w[i].z, kLowest2);
+                        w[i].w = max_nan_bf16x2(w[i].w, kLowest2);
+                    }
+                    unpack(w[i], z);
+                } else {
+                    float f[4] = {__uint_as_float(w[i].x), __uint_as_float(w[i].y),
+                                  __uint_as_float(w[i].z), __uint_as_float(w[i].w)};
+                    if (OP == kBwd)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float p = prob(z[i][j], q.itau, i1, l);
-                    d[j] = (!none && (live >> (8 * i + j) & 1u)) ? __fmul_rn(a, p) : 0.f;
+                        for (int j = 0; j < 4; ++j) f[j] = max_nan(f[j], -FLT_MAX);
+                    z[0] = pair(f[0], f[1]);
+                    z[1] = pair(f[2], f[3]);
                 }
-                store_group(orow + seg0 + 8 * (lane + 32 * i), io.vec_out, inside >> (8 * i) & 0xffu, d);
+#pragma unroll
+                for (int j = 0; j < N / 2; ++j) {
+                    uint64_t v;
+                    if (OP == kApply) {
+                        v = mul2(z[j], it2);
+                    } else {
+                        v = fma2(z[j], pair(i1, i1), fma2(z[j], it2, pair(-l, -l)));
+                        v = mul2(v, pair(kLog2e, kLog2e));
+                        float a, b;
+                        unpair(v, a, b);
+                        v = mul2(pair(ex2(a), ex2(b)), pair(-g, -g));
+                    }
+                    unpair(v, x[2 * j], x[2 * j + 1]);
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if ((int32_t)(keep << (31 - N * i - j)) >= 0) x[j] = OP == kApply ? -INFINITY : 0.f;
+                const int piece = lane * L::kPieces + L::order(lane, i);  // of the segment
+                if constexpr (sizeof(TOut) == 4) {
+                    float4 *o = reinterpret_cast<float4 *>(staged);
+#pragma unroll
+                    for (int h = 0; h < N / 4; ++h)
+                        o[(piece * (N / 4) + h) ^ (C::kSwap ? lane & 1 : 0)] =
+                            make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
+                } else {
+                    uint32_t *o = reinterpret_cast<uint32_t *>(staged) + piece * (N / 2);
+                    if constexpr (N == 8)
+                        *reinterpret_cast<uint4 *>(o) =
+                            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                       pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+                    else
+                        *reinterpret_cast<uint2 *>(o) =
+                            make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+                }
             }
-            const int64_t tc = row.tgt - seg0;
-            uint32_t b = special;
-            int tbit = -1;
-            if (tc >= 0 && tc < kSegCols && ((tc >> 3) & 31) == lane) {
-                tbit = (int)((tc >> 8) * 8 + (tc & 7));
-                b |= (1u << tbit) & live;
+            // the touched columns, and the target's, over what stands there
+            __syncwarp();
+            auto put_column = [&](int j, float v) {
+                put(reinterpret_cast<TOut *>(staged) + (j ^ (C::kSwap ? (j >> 3) & 4 : 0)), v);
+            };
+            if (OP == kBwd && row.tgt >= seg0 && row.tgt < seg0 + cols) {
+                const int j = row.tgt - (int)seg0;
+                if ((j >> 5) == lane && ((shown & ~touched) >> (j & 31) & 1u))
+                    put_column(j, __fmul_rn(g, __fsub_rn(1.f, prob(elem(zs + j), q.itau, i1, l))));
             }
-            if (none) b = 0;
-            while (b) {
-                const int k = __ffs(b) - 1;
-                b &= b - 1;
-                const int sc = warp * kSegCols + lane_column(lane, k);
-                const bool tch = touched >> k & 1u;
-                const float zv = load_elem(zrow + slice0 + sc);
-                const uint32_t w = tch ? sh.count[sc] : 0u;
-                const float y = tch ? rule_y(zv, w, sh.bias ? __int_as_float(sh.bias[sc]) : 0.f, q) : zv;
-                const float p = prob(y, q.itau, i1, l);
-                const float slope = w ? (zv > 0.f ? q.irep : q.rep) : 1.f;
-                store_elem(orow + slice0 + sc,
-                           __fmul_rn(__fmul_rn(g, __fsub_rn(k == tbit ? 1.f : 0.f, p)), slope));
+            for (int e = lane; e < (none ? 0 : listed); e += 32) {
+                const int j = list[e];
+                float z, y;
+                uint32_t cw;
+                if (!listed_y(j, z, cw, y)) continue;
+                if (OP == kApply) {
+                    put_column(j, __fmul_rn(y, q.itau));
+                } else {
+                    const float slope = cw ? (z > 0.f ? q.irep : q.rep) : 1.f;
+                    const float hot = j == row.tgt - seg0 ? 1.f : 0.f;
+                    put_column(j, __fmul_rn(__fmul_rn(g, __fsub_rn(hot, prob(y, q.itau, i1, l))), slope));
+                }
             }
+            __syncwarp();
+            write_out<C::kSwap>(staged, orow, cols, io.vec_out, lane);
         }
+        __syncwarp();  // the stage and the staging area are free again
     }
 }
 
@@ -525,14 +827,14 @@ __global__ void __launch_bounds__(32 * kMergeRows)
     const int64_t t = (int64_t)blockIdx.x * kMergeRows + (threadIdx.x >> 5);
     if (t >= io.T) return;
     const RowInfo row = row_info<kLogp>(io, rules, t);
-    if (!row.active) {
+    if (row.tgt == kInactive) {
         if (lane == 0) {
             logp[t] = 0.f;
             if (lse) lse[t] = 0.f;
         }
         return;
     }
-    const bool has_tau = row.ok && rules.num_requests > 0 && rules.temperature;
+    const bool has_tau = row.tgt >= 0 && rules.num_requests > 0 && rules.temperature;
     const float tau = has_tau ? rules.temperature[row.req] : 1.f;
     const float c = __fmul_rn(kLog2e, __frcp_rn(tau));
     const int64_t nseg = (io.V + kSegCols - 1) / kSegCols;
@@ -550,7 +852,7 @@ __global__ void __launch_bounds__(32 * kMergeRows)
     if (lane == 0) {
         const float nan = __int_as_float(0x7fc00000);
         float l, p;
-        if (!row.ok || row.tgt >= io.V || s != s) {
+        if (row.tgt < 0 || s != s) {
             l = p = nan;
         } else if (s == 0.f) {
             l = p = -INFINITY;
@@ -564,10 +866,6 @@ __global__ void __launch_bounds__(32 * kMergeRows)
         logp[t] = p;
         if (lse) lse[t] = l;
     }
-}
-
-size_t smem_bytes(const rk_logits_rules &r) {
-    return (size_t)(kSliceCols + kThreads + (r.bias_ids ? kSliceCols : 0)) * 4;
 }
 
 void dependent(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, unsigned grid, unsigned block,
@@ -594,7 +892,7 @@ int rows_per_block(int64_t T, int64_t V, const DeviceInfo &di) {
 template <RulesOp OP, typename TIn, typename TOut>
 cudaError_t launch(RulesIo io, const rk_logits_rules &r, const DeviceInfo &di, cudaStream_t st) {
     auto *kernel = rules_kernel<OP, TIn, TOut>;
-    const size_t smem = smem_bytes(r);
+    const size_t smem = Config<OP, TIn, TOut>::smem(r.bias_ids != nullptr);
     if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -230,6 +230,23 @@ def test_values_at_the_edges_of_the_type(rk):
     assert bool((d[3, ::2] == 0).all()) and abs(float(d[3, 7]) - (1 - 1 / 650)) < 1e-6
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_a_row_at_the_lowest_value_of_its_type(rk, dtype):
+    # lse = lowest + ln V, which rounds to lowest: every p is exp(0) of that rounded lse
+    V = 2100
+    z = torch.full((2, V), torch.finfo(dtype).min, dtype=dtype, device=DEV)
+    tg = torch.tensor([7, 2099], device=DEV)
+    for kw in (dict(), dict(temperature=torch.ones(2, device=DEV), presence=torch.ones(2, device=DEV),
+                            tokens=torch.tensor([7, 8], device=DEV), token_offsets=torch.tensor([0, 1, 2], device=DEV))):
+        rules = rk.LogitsRules(**kw)
+        logp, lse = rk.logp_from_logits_rules(z, tg, rules)
+        assert bool((lse == torch.finfo(dtype).min).all())
+        assert bool((logp + np.log(V) < 1e-5).all()) and bool((logp + np.log(V) > -1e-5).all())
+        d = rk.logp_from_logits_rules_bwd(z, tg, rules, lse, torch.ones(2, device=DEV))
+        assert d[0, 7] == 0 and d[1, 2099] == 0 and d[0, 9] == -1 and bool(torch.isfinite(d).all())
+        assert bool((rk.logits_rules_apply(z, rules) == torch.finfo(dtype).min).all())
+
+
 def test_a_mask_that_leaves_nothing_and_a_bias_of_minus_infinity(rk):
     V = 9000
     mask = torch.full((3, (V + 31) // 32), 0, dtype=torch.int32)
@@ -324,6 +341,21 @@ def test_unusable_rules_give_nan_and_the_error_word(rk):
     def target(c):
         c.targets[3] = 1100
     call(target, [3], rk.DEVERR_TARGET_RANGE)
+
+
+def test_too_many_biases(rk):
+    z = torch.randn(2, 70000, device=DEV)
+    tg = torch.zeros(2, dtype=torch.int64, device=DEV)
+    for n, bit in ((65534, 0), (65535, rk.DEVERR_RULES)):
+        rules = rk.LogitsRules(bias_ids=torch.arange(n, device=DEV), bias_values=torch.arange(n, device=DEV) * 1e-3,
+                               bias_offsets=torch.tensor([0, n, n], device=DEV))
+        x = rk.logits_rules_apply(z, rules)
+        assert rk.get_device_error() == bit
+        assert same_bits(x[1], z[1])
+        if bit:
+            assert bool(torch.isnan(x[0]).all())
+        else:
+            assert same_bits(x[0, :n], z[0, :n] + torch.arange(n, device=DEV) * 1e-3) and same_bits(x[0, n:], z[0, n:])
 
 
 def test_ids_outside_the_vocabulary_are_passed_over(rk):
