@@ -543,7 +543,7 @@ rk_status rk_embedding(const int64_t *ids, const int32_t *cu_seqlens, int32_t nu
  * The canonical tokens are the active rows among row_order[0..n_order), out-of-range
  * entries skipped, or rows 0..T-1 when row_order is NULL.  They are sorted by id with
  * their order kept, and each id's rows are summed in that order, in fp32, in pieces of
- * 64 occurrences whose sums are then added in order: dE[v] is bitwise the same for the
+ * 32 occurrences whose sums are then added in order: dE[v] is bitwise the same for the
  * same tokens of id v in the same canonical order, whatever their physical layout and
  * whatever the other tokens are.  A row listed twice counts twice.
  *   dout  bf16 or fp32 [T, H]; dE fp32 [V, H]; both contiguous, aligned to their element
@@ -553,7 +553,7 @@ rk_status rk_embedding(const int64_t *ids, const int32_t *cu_seqlens, int32_t nu
  *   ids >= V on active rows contribute nothing and set RK_DEVERR_TARGET_RANGE
  *   workspace  >= rk_embedding_bwd_workspace_size(n, H, V) bytes, 16-byte aligned, n =
  *              n_order (or T): the sort's keys and counts, the list of pieces, and
- *              fp32 [n / 32 + 1, H] for the sums of ids with more than 64 rows
+ *              fp32 [n / 16 + 1, H] for the sums of ids with more than 32 rows
  * Supported: as rk_embedding, V < 2^31 - 1, n < 2^31.
  */
 size_t rk_embedding_bwd_workspace_size(int64_t n, int64_t H, int64_t V);

@@ -635,9 +635,6 @@ class _RulesStruct(ctypes.Structure):
         [(n, ctypes.c_void_p) for n in ("row_request", "row_length", "row_mask")]
 
 
-_RULE_PARAMS = ("temperature", "repetition", "frequency", "presence")
-
-
 class LogitsRules:
     """What a decoding loop does to the logits before it draws a token.
 
@@ -688,35 +685,35 @@ class LogitsRules:
             raise ValueError("row_length needs tokens")
         if row_mask is not None and mask is None:
             raise ValueError("row_mask needs mask")
-        s = _RulesStruct()
+        address = dict.fromkeys(kept)
         device = requests = rows = None
         for name, t in kept.items():
             if t is None:
                 continue
-            dtype, ndim = _RULE_TYPES[name]
-            _need(t, name, dtype, ndim)
+            dtype, ndim, off = _RULES[name]
+            if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
+                    and t.dim() == ndim and t.is_contiguous()):
+                _need(t, name, dtype, ndim)
             if device is None:
                 device = t.device
             elif t.device != device:
                 raise ValueError(f"{name} is on {t.device}, not on {device}")
-            n = t.shape[0]
-            if name in _RULE_PER_REQUEST:
-                n -= _RULE_PER_REQUEST[name]
-                if n < 1 or (requests is not None and n != requests):
-                    raise ValueError(f"{name} does not fit {requests if requests else 'one or more'} "
-                                     "requests")
-                requests = n
-            elif name in _RULE_PER_ROW:
-                if rows is not None and n != rows:
-                    raise ValueError(f"{name} does not fit {rows} rows")
-                rows = n
-            setattr(s, name, t.data_ptr())
+            if off is not None:
+                n = t.shape[0] - off
+                if off < 0:  # per row
+                    n = t.shape[0]
+                    if rows is not None and n != rows:
+                        raise ValueError(f"{name} does not fit {rows} rows")
+                    rows = n
+                else:  # per request
+                    if n < 1 or (requests is not None and n != requests):
+                        raise ValueError(f"{name} does not fit "
+                                         f"{requests if requests else 'one or more'} requests")
+                    requests = n
+            # an empty list still has to be told from a missing one
+            address[name] = t.data_ptr() or _EMPTY
         if bias_ids is not None and bias_ids.shape[0] != bias_values.shape[0]:
             raise ValueError("bias_ids and bias_values differ in length")
-        s.num_requests = requests or 0
-        s.num_tokens = 0 if tokens is None else tokens.shape[0]
-        s.num_bias = 0 if bias_ids is None else bias_ids.shape[0]
-        s.mask_rows = 0 if mask is None else mask.shape[0]
         if requests and row_request is None:
             if rows is not None and rows != requests:
                 raise ValueError(f"{requests} requests for {rows} rows: row_request is missing")
@@ -725,26 +722,27 @@ class LogitsRules:
             if rows is not None and rows != mask.shape[0]:
                 raise ValueError(f"{mask.shape[0]} masks for {rows} rows: row_mask is missing")
             rows = mask.shape[0]
-        # an empty list still has to be told from a missing one
-        for name in ("tokens", "bias_ids", "bias_values", "mask"):
-            if kept[name] is not None and kept[name].numel() == 0:
-                setattr(s, name, _EMPTY)
+        s = _RulesStruct(requests or 0, address["temperature"], address["repetition"],
+                         address["frequency"], address["presence"], address["tokens"],
+                         0 if tokens is None else tokens.shape[0], address["token_offsets"],
+                         address["prompt_lengths"], address["bias_ids"], address["bias_values"],
+                         0 if bias_ids is None else bias_ids.shape[0], address["bias_offsets"],
+                         address["mask"], 0 if mask is None else mask.shape[0],
+                         address["row_request"], address["row_length"], address["row_mask"])
         self.device, self.rows = device, rows
         self.mask_words = None if mask is None else mask.shape[1]
         self.struct, self.address, self._kept = s, ctypes.addressof(s), kept
 
 
 _EMPTY = 256  # an address that an empty list never reads
-_RULE_TYPES = {"temperature": (torch.float32, 1), "repetition": (torch.float32, 1),
-               "frequency": (torch.float32, 1), "presence": (torch.float32, 1),
-               "tokens": (torch.int64, 1), "token_offsets": (torch.int64, 1),
-               "prompt_lengths": (torch.int32, 1), "bias_ids": (torch.int64, 1),
-               "bias_values": (torch.float32, 1), "bias_offsets": (torch.int64, 1),
-               "mask": (torch.int32, 2), "row_request": (torch.int32, 1),
-               "row_length": (torch.int32, 1), "row_mask": (torch.int32, 1)}
-_RULE_PER_REQUEST = {"temperature": 0, "repetition": 0, "frequency": 0, "presence": 0,
-                     "prompt_lengths": 0, "token_offsets": 1, "bias_offsets": 1}
-_RULE_PER_ROW = ("row_request", "row_length", "row_mask")
+# type, dimensions, and entries beyond one per request (-1: one per row, None: neither)
+_RULES = {"temperature": (torch.float32, 1, 0), "repetition": (torch.float32, 1, 0),
+          "frequency": (torch.float32, 1, 0), "presence": (torch.float32, 1, 0),
+          "tokens": (torch.int64, 1, None), "token_offsets": (torch.int64, 1, 1),
+          "prompt_lengths": (torch.int32, 1, 0), "bias_ids": (torch.int64, 1, None),
+          "bias_values": (torch.float32, 1, None), "bias_offsets": (torch.int64, 1, 1),
+          "mask": (torch.int32, 2, None), "row_request": (torch.int32, 1, -1),
+          "row_length": (torch.int32, 1, -1), "row_mask": (torch.int32, 1, -1)}
 _TYPE_CODES = {torch.bfloat16: 0, torch.float32: 1}
 
 
@@ -752,22 +750,25 @@ def _matrix(t: torch.Tensor, name: str, shape=None, device=None):
     """(type code, row stride) of a bf16 or fp32 [T, V] matrix with unit column stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path), got {t.device}")
-    if t.dtype not in _TYPE_CODES:
+    code = _TYPE_CODES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be {list(shape) if shape else '[T, V]'}, "
                          f"got shape {tuple(t.shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     T, V = t.shape
-    if V > 1 and t.stride(1) != 1:
+    ld, unit = t.stride()
+    if V > 1 and unit != 1:
         raise ValueError(f"{name} must have unit column stride")
-    ld = t.stride(0) if T > 1 else max(V, 1)
+    if T <= 1:
+        ld = max(V, 1)
     if ld < V:
         raise ValueError(f"{name}'s rows overlap")
-    return _TYPE_CODES[t.dtype], ld
+    return code, ld
 
 
 def _rules_for(rules: LogitsRules, T: int, V: int, device) -> None:
@@ -786,6 +787,19 @@ def _vector(t: torch.Tensor, name: str, T: int, device) -> None:
     _need(t, name, torch.float32, 1)
     if t.shape[0] != T or t.device != device:
         raise ValueError(f"{name} must be [T] on {device}")
+
+
+def _run(what: str, fn, device, stream, *args) -> None:
+    """Calls the library on ``device``, with the stream's handle behind ``args``."""
+    handle = stream.cuda_stream if stream is not None else \
+        torch._C._cuda_getCurrentRawStream(device.index)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if st != RK_OK:
+        _check(st, what)
 
 
 def _scratch(workspace, need: int, device) -> torch.Tensor:
@@ -813,11 +827,8 @@ def logits_rules_apply(logits: torch.Tensor, rules: LogitsRules, *,
     if out is None:
         out = torch.empty((T, V), dtype=out_dtype, device=device)
     out_code, out_ld = _matrix(out, "out", (T, V), device)
-    with torch.cuda.device(device):
-        st = lib.rk_logits_rules_apply(logits.data_ptr(), code, ld, rules.address, T, V,
-                                       out.data_ptr(), out_code, out_ld,
-                                       _stream_handle(stream, device))
-    _check(st, "rk_logits_rules_apply")
+    _run("rk_logits_rules_apply", lib.rk_logits_rules_apply, device, stream, logits.data_ptr(), code,
+         ld, rules.address, T, V, out.data_ptr(), out_code, out_ld)
     return out
 
 
@@ -846,12 +857,9 @@ def logp_from_logits_rules(logits: torch.Tensor, targets: torch.Tensor, rules: L
     _vector(out, "out", T, device)
     _vector(lse, "lse", T, device)
     workspace = _scratch(workspace, lib.rk_logp_from_logits_rules_workspace_size(T, V), device)
-    with torch.cuda.device(device):
-        st = lib.rk_logp_from_logits_rules(logits.data_ptr(), code, ld, targets.data_ptr(), _ptr(cu),
-                                           ns, rules.address, T, V, out.data_ptr(), lse.data_ptr(),
-                                           workspace.data_ptr(), workspace.numel(),
-                                           _stream_handle(stream, device))
-    _check(st, "rk_logp_from_logits_rules")
+    _run("rk_logp_from_logits_rules", lib.rk_logp_from_logits_rules, device, stream,
+         logits.data_ptr(), code, ld, targets.data_ptr(), _ptr(cu), ns, rules.address, T, V,
+         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
@@ -874,12 +882,9 @@ def logp_from_logits_rules_bwd(logits: torch.Tensor, targets: torch.Tensor, rule
     if out is None:
         out = torch.empty((T, V), dtype=out_dtype, device=device)
     out_code, out_ld = _matrix(out, "out", (T, V), device)
-    with torch.cuda.device(device):
-        st = lib.rk_logp_from_logits_rules_bwd(logits.data_ptr(), code, ld, targets.data_ptr(),
-                                               _ptr(cu), ns, rules.address, T, V, lse.data_ptr(),
-                                               grad_logp.data_ptr(), out.data_ptr(), out_code, out_ld,
-                                               _stream_handle(stream, device))
-    _check(st, "rk_logp_from_logits_rules_bwd")
+    _run("rk_logp_from_logits_rules_bwd", lib.rk_logp_from_logits_rules_bwd, device, stream,
+         logits.data_ptr(), code, ld, targets.data_ptr(), _ptr(cu), ns, rules.address, T, V,
+         lse.data_ptr(), grad_logp.data_ptr(), out.data_ptr(), out_code, out_ld)
     return out
 
 
@@ -907,10 +912,8 @@ def embedding(ids: torch.Tensor, E: torch.Tensor, cu_seqlens: torch.Tensor | Non
     if out is None:
         out = torch.empty((T, H), dtype=out_dtype or E.dtype, device=device)
     out_code = _dense(out, "out", (T, H), device)
-    with torch.cuda.device(device):
-        st = lib.rk_embedding(ids.data_ptr(), _ptr(cu), ns, E.data_ptr(), code, T, H, V, scale,
-                              out.data_ptr(), out_code, _stream_handle(stream, device))
-    _check(st, "rk_embedding")
+    _run("rk_embedding", lib.rk_embedding, device, stream, ids.data_ptr(), _ptr(cu), ns, E.data_ptr(),
+         code, T, H, V, scale, out.data_ptr(), out_code)
     return out
 
 
@@ -947,12 +950,9 @@ def embedding_bwd(grad_out: torch.Tensor, ids: torch.Tensor, V: int,
     if _dense(dE, "dE", (V, H), device) != 1:
         raise TypeError("dE must be float32")
     workspace = _scratch(workspace, lib.rk_embedding_bwd_workspace_size(n, H, V), device)
-    with torch.cuda.device(device):
-        st = lib.rk_embedding_bwd(grad_out.data_ptr(), code, ids.data_ptr(), _ptr(cu), ns, T, H, V,
-                                  scale, order, n, dE.data_ptr(), int(accumulate),
-                                  workspace.data_ptr(), workspace.numel(),
-                                  _stream_handle(stream, device))
-    _check(st, "rk_embedding_bwd")
+    _run("rk_embedding_bwd", lib.rk_embedding_bwd, device, stream, grad_out.data_ptr(), code,
+         ids.data_ptr(), _ptr(cu), ns, T, H, V, scale, order, n, dE.data_ptr(), int(accumulate),
+         workspace.data_ptr(), workspace.numel())
     return dE
 
 

@@ -9,12 +9,15 @@
 // Both are memory bound.  The gradient runs in three stages:
 //   sort    (id, row) pairs of the canonical tokens by id with a stable
 //           least-significant-digit radix sort (digits of up to
-//           kMaxDigitBits; inactive tokens get the key V and end up last);
+//           kMaxDigitBits; inactive tokens get the key V and end up last):
+//           in the shared memory of one block for up to kSmallSort tokens,
+//           by tiles of kSortTile otherwise;
 //   pieces  each id's run in the sorted list is cut into pieces of kPiece
 //           occurrences, counted from the run's own start;
-//   sum     a block per (piece, slice of columns) adds the piece's rows in
-//           order in fp32.  An id with one piece writes its row of dE; the
-//           others write partial sums, which a last kernel adds in order.
+//   sum     a warp per (piece, 512 columns) adds the piece's rows in order in
+//           fp32, with the loads of several rows and columns in flight.  An id
+//           with one piece writes its row of dE; the others write partial
+//           sums, which a last kernel adds in order.
 // The pieces of an id depend on its own occurrences alone, so its row of dE
 // does too.  The order in which blocks find the pieces does not matter: no
 // two write the same place.
@@ -36,11 +39,12 @@ __device__ __forceinline__ void wait_prior_grid() {
 // become resident while the previous kernel of the stream ends; each waits
 // (wait_prior_grid) before it reads or writes anything.
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kernel)(P...), int64_t grid, int block, cudaStream_t st,
-                             A... args) {
+cudaError_t launch_dependent_smem(void (*kernel)(P...), int64_t grid, int block, size_t smem,
+                                  cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -48,6 +52,12 @@ cudaError_t launch_dependent(void (*kernel)(P...), int64_t grid, int block, cuda
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), int64_t grid, int block, cudaStream_t st,
+                             A... args) {
+    return launch_dependent_smem(kernel, grid, block, 0, st, args...);
 }
 
 // ---- elements, eight at a time or one by one ----
@@ -121,145 +131,253 @@ __global__ void __launch_bounds__(kLookupThreads)
 
 constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortPerWarp = 512;                       // items per warp, in order
-constexpr int kSortTile = kSortPerWarp * kSortWarps;    // 4096
+constexpr int kSortItems = 8;                                   // per lane
+constexpr int kSortTile = kSortThreads * kSortItems;            // 2048
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxBins = 1 << kMaxDigitBits;
-constexpr int kPiece = 64;       // occurrences of an id summed by one block
+constexpr int kInlineScanTiles = 64;  // up to here each block scans the counts itself
+constexpr int kTinyThreads = 128, kSmallThreads = 1024;         // blocks that sort alone
+constexpr int kSmallSort = kSmallThreads * kSortItems;          // 8192
+constexpr int kPiece = 32;       // occurrences of an id summed by one warp
 constexpr int kHalf = kPiece / 2;
 constexpr int kScanThreads = 1024;
+constexpr int kZeroAllShare = 8;
 
-// Keys and rows of the canonical tokens, in canonical order; row_end cleared.
-__global__ void __launch_bounds__(256)
-    emb_keys(const int64_t *ids, const int32_t *cu, int num_seqs,
-             int64_t T, int64_t V, const int64_t *order, int64_t n,
-             int32_t *key, int32_t *val, int32_t *row_end,
-             int32_t *counters, unsigned *err) {
-    wait_prior_grid();
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (first < 2) counters[first] = 0;
-    for (int64_t v = first; v < V; v += step) row_end[v] = 0;
-    for (int64_t i = first; i < n; i += step) {
-        const int64_t r = order ? order[i] : i;
-        int64_t k = V;
-        if (r >= 0 && r < T) {
-            const int64_t id = ids[r];
-            if (row_active(r, id, cu, num_seqs)) {
-                if (id < V)
-                    k = id;
-                else
-                    atomicOr(err, kErrTargetRange);
-            }
+struct Canonical {  // the canonical tokens
+    const int64_t *ids;
+    const int32_t *cu;
+    int num_seqs;
+    int64_t T, V;
+    const int64_t *order;
+    int64_t n;
+    unsigned *err;
+};
+
+// Key (the id, or V: inactive) and row of canonical token i.
+__device__ __forceinline__ void canonical_token(const Canonical &c, int64_t i, int32_t &key, int32_t &row) {
+    const int64_t r = c.order ? c.order[i] : i;
+    int64_t k = c.V;
+    if (r >= 0 && r < c.T) {
+        const int64_t id = c.ids[r];
+        if (row_active(r, id, c.cu, c.num_seqs)) {
+            if (id < c.V)
+                k = id;
+            else
+                atomicOr(c.err, kErrTargetRange);
         }
-        key[i] = (int32_t)k;
-        val[i] = (int32_t)(k < V ? r : 0);
+    }
+    key = (int32_t)k;
+    row = (int32_t)(k < c.V ? r : 0);
+}
+
+// Exclusive prefix sum of one int per thread over a block of 32 * WARPS
+// threads; `total` gets the sum.
+template <int WARPS>
+__device__ __forceinline__ int block_scan(int x, int *total) {
+    __shared__ int warp_sums[WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    int w = lane < WARPS ? warp_sums[lane] : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, off);
+        if (lane >= off) w += y;
+    }
+    *total = __shfl_sync(0xffffffffu, w, WARPS - 1);
+    const int before = warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
+    __syncthreads();
+    return before + incl - x;
+}
+
+// Counts the digits of a tile's keys; a thread's items are strided by the
+// block's size.
+__device__ __forceinline__ void count_digits(const int32_t (&k)[kSortItems], int64_t first, int64_t n,
+                                             int shift, int bins, int *cnt) {
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j)
+        if (first + j * kSortThreads < n) atomicAdd(&cnt[(k[j] >> shift) & (bins - 1)], 1);
+}
+
+// Where digit d's count of tile b stands: rows of `pitch` tiles, the columns
+// past the last tile 0.
+__device__ __forceinline__ void write_counts(const int *cnt, int bins, int32_t *hist, int64_t tiles,
+                                             int64_t pitch) {
+    for (int d = threadIdx.x; d < bins; d += kSortThreads) {
+        hist[d * pitch + blockIdx.x] = cnt[d];
+        if (blockIdx.x == 0)
+            for (int64_t b = tiles; b < pitch; ++b) hist[d * pitch + b] = 0;
     }
 }
 
-// Radix pass, first part: hist[d * tiles + b] = items of tile b with digit d.
+// Keys and rows of the canonical tokens, and the first pass's counts.
 __global__ void __launch_bounds__(kSortThreads)
-    emb_histogram(const int32_t *key, int64_t n, int shift, int bins,
-                  int32_t *hist, int64_t tiles) {
+    emb_keys(const __grid_constant__ Canonical c, int32_t *key, int32_t *val, int bins, int32_t *hist,
+             int64_t tiles, int64_t pitch, int32_t *counters) {
     __shared__ int cnt[kMaxBins];
     wait_prior_grid();
     for (int d = threadIdx.x; d < bins; d += kSortThreads) cnt[d] = 0;
+    if (blockIdx.x == 0 && threadIdx.x < 2) counters[threadIdx.x] = 0;
     __syncthreads();
-    const int64_t base = (int64_t)blockIdx.x * kSortTile;
-    for (int i = threadIdx.x; i < kSortTile; i += kSortThreads)
-        if (base + i < n) atomicAdd(&cnt[(key[base + i] >> shift) & (bins - 1)], 1);
+    const int64_t first = (int64_t)blockIdx.x * kSortTile + threadIdx.x;
+    int32_t k[kSortItems];
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+        const int64_t i = first + j * kSortThreads;
+        if (i < c.n) {
+            int32_t r;
+            canonical_token(c, i, k[j], r);
+            key[i] = k[j];
+            val[i] = r;
+        }
+    }
+    count_digits(k, first, c.n, 0, bins, cnt);
     __syncthreads();
-    for (int d = threadIdx.x; d < bins; d += kSortThreads) hist[d * tiles + blockIdx.x] = cnt[d];
+    write_counts(cnt, bins, hist, tiles, pitch);
 }
 
-// Exclusive prefix sums over cnt[0..len) in place, by one block.
-__global__ void __launch_bounds__(kScanThreads)
-    emb_scan(int32_t *cnt, int64_t len) {
-    __shared__ int warp_sums[32];
+// A later pass's counts.
+__global__ void __launch_bounds__(kSortThreads)
+    emb_histogram(const int32_t *key, int64_t n, int shift, int bins, int32_t *hist, int64_t tiles,
+                  int64_t pitch) {
+    __shared__ int cnt[kMaxBins];
     wait_prior_grid();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int d = threadIdx.x; d < bins; d += kSortThreads) cnt[d] = 0;
+    const int64_t first = (int64_t)blockIdx.x * kSortTile + threadIdx.x;
+    int32_t k[kSortItems];
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j)
+        k[j] = first + j * kSortThreads < n ? key[first + j * kSortThreads] : 0;
+    __syncthreads();
+    count_digits(k, first, n, shift, bins, cnt);
+    __syncthreads();
+    write_counts(cnt, bins, hist, tiles, pitch);
+}
+
+// Exclusive prefix sums over cnt[0..len) in place, by one block (len a
+// multiple of 4).
+__global__ void __launch_bounds__(kScanThreads) emb_scan(int32_t *cnt, int64_t len) {
+    wait_prior_grid();
     int carry = 0;
-    for (int64_t base = 0; base < len; base += 8 * kScanThreads) {
-        const int64_t i0 = base + 8 * (int64_t)threadIdx.x;
-        int v[8], sum = 0;
+    for (int64_t base = 0; base < len; base += 16 * kScanThreads) {
+        int4 v[4];
+        const int64_t i0 = base + 16 * (int64_t)threadIdx.x;
+        int sum = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] = i0 + j < len ? cnt[i0 + j] : 0;
-            sum += v[j];
+        for (int j = 0; j < 4; ++j) {
+            v[j] = i0 + 4 * j < len ? *reinterpret_cast<const int4 *>(cnt + i0 + 4 * j)
+                                    : make_int4(0, 0, 0, 0);
+            sum += v[j].x + v[j].y + v[j].z + v[j].w;
         }
-        int incl = sum;
+        int all;
+        int run = carry + block_scan<kScanThreads / 32>(sum, &all);
+        carry += all;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
+        for (int j = 0; j < 4; ++j) {
+            const int4 o = make_int4(run, run + v[j].x, run + v[j].x + v[j].y, run + v[j].x + v[j].y + v[j].z);
+            run = o.w + v[j].w;
+            if (i0 + 4 * j < len) *reinterpret_cast<int4 *>(cnt + i0 + 4 * j) = o;
         }
-        if (lane == 31) warp_sums[warp] = incl;
-        __syncthreads();
-        if (warp == 0) {
-            int w = warp_sums[lane];
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, w, off);
-                if (lane >= off) w += y;
-            }
-            warp_sums[lane] = w;
-        }
-        __syncthreads();
-        int run = carry + (warp > 0 ? warp_sums[warp - 1] : 0) + incl - sum;
-        carry += warp_sums[31];
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (i0 + j < len) {
-                cnt[i0 + j] = run;
-                run += v[j];
-            }
     }
 }
 
-// Radix pass, last part: a tile's items to their digit's place, order kept.
-// Each warp walks its own kSortPerWarp consecutive items 32 at a time; an
-// item's rank is the number of earlier lanes with its digit plus the warp's
-// running count of that digit.
+// A warp's kSortItems * 32 consecutive items, item j * 32 + lane in register
+// j, to their digit's place, order kept: an item's rank is the number of
+// earlier lanes with its digit plus the warp's running place of that digit.
+template <typename Store>
+__device__ __forceinline__ void place_items(const int32_t (&k)[kSortItems], int64_t left, int shift,
+                                            int bins, int *place, int lane, Store store) {
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+        const bool live = 32 * j + lane < left;
+        const int d = live ? (k[j] >> shift) & (bins - 1) : 0;
+        unsigned peers = __ballot_sync(0xffffffffu, live);  // live lanes with this digit
+#pragma unroll
+        for (int b = 0; b < kMaxDigitBits; ++b) {
+            const bool set = d >> b & 1;
+            const unsigned m = __ballot_sync(0xffffffffu, set);
+            peers &= set ? m : ~m;
+        }
+        const int rank = __popc(peers & ((1u << lane) - 1u));
+        const int at = live ? place[d] + rank : 0;
+        __syncwarp();
+        if (live) {
+            if (rank == 0) place[d] = at + __popc(peers);
+            store(j, at);
+        }
+        __syncwarp();
+    }
+}
+
+// Radix pass, last part: a tile's items to their digit's place.  SCANNED: hist
+// holds prefix sums; otherwise counts, which the block sums up itself.
+template <bool SCANNED>
 __global__ void __launch_bounds__(kSortThreads)
-    emb_scatter(const int32_t *ks, const int32_t *vs,
-                int32_t *kd, int32_t *vd, int64_t n, int shift, int bins,
-                const int32_t *hist, int64_t tiles) {
-    __shared__ int cnt[kSortWarps][kMaxBins];
+    emb_scatter(const int32_t *ks, const int32_t *vs, int32_t *kd, int32_t *vd, int64_t n, int shift,
+                int bins, const int32_t *hist, int64_t pitch) {
+    __shared__ int place[kSortWarps][kMaxBins];
     wait_prior_grid();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int d = threadIdx.x; d < kSortWarps * kMaxBins; d += kSortThreads) (&cnt[0][0])[d] = 0;
+    const int64_t base = (int64_t)blockIdx.x * kSortTile + (int64_t)warp * 32 * kSortItems;
+    int32_t k[kSortItems], v[kSortItems];
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+        const int64_t i = base + 32 * j + lane;
+        k[j] = i < n ? ks[i] : 0;
+        v[j] = i < n ? vs[i] : 0;
+    }
+    for (int d = threadIdx.x; d < kSortWarps * kMaxBins; d += kSortThreads) (&place[0][0])[d] = 0;
     __syncthreads();
-    const int64_t base = (int64_t)blockIdx.x * kSortTile + (int64_t)warp * kSortPerWarp;
-    for (int i = lane; i < kSortPerWarp; i += 32)
-        if (base + i < n) atomicAdd(&cnt[warp][(ks[base + i] >> shift) & (bins - 1)], 1);
-    __syncthreads();
-    for (int d = threadIdx.x; d < bins; d += kSortThreads) {
-        int run = hist[d * tiles + blockIdx.x];
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j)
+        if (base + 32 * j + lane < n) atomicAdd(&place[warp][(k[j] >> shift) & (bins - 1)], 1);
+    // the tile's first place of digits 2 threadIdx and 2 threadIdx + 1
+    constexpr int kPer = kMaxBins / kSortThreads;
+    int first[kPer], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int d = kPer * threadIdx.x + j;
+        first[j] = 0;
+        if (d >= bins) continue;
+        if (SCANNED) {
+            first[j] = hist[d * pitch + blockIdx.x];
+        } else {
+            int before = 0, all = 0;
+#pragma unroll 4
+            for (int b = 0; b < (int)pitch; b += 4) {
+                const int4 h = *reinterpret_cast<const int4 *>(hist + d * pitch + b);
+                all += h.x + h.y + h.z + h.w;
+                const int m = (int)blockIdx.x - b;  // tiles before this one
+                before += (m > 0 ? h.x : 0) + (m > 1 ? h.y : 0) + (m > 2 ? h.z : 0) + (m > 3 ? h.w : 0);
+            }
+            first[j] = sum + before;
+            sum += all;
+        }
+    }
+    int total;
+    const int prefix = block_scan<kSortWarps>(sum, &total);  // a barrier too
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int d = kPer * threadIdx.x + j;
+        int run = prefix + first[j];
 #pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
-            const int c = cnt[w][d];
-            cnt[w][d] = run;
+            const int c = place[w][d];
+            place[w][d] = run;
             run += c;
         }
     }
     __syncthreads();
-    for (int i0 = 0; i0 < kSortPerWarp; i0 += 32) {
-        const bool live = base + i0 + lane < n;
-        const int32_t k = live ? ks[base + i0 + lane] : 0;
-        const int32_t v = live ? vs[base + i0 + lane] : 0;
-        const int d = live ? (k >> shift) & (bins - 1) : -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, d);
-        const int rank = __popc(peers & ((1u << lane) - 1u));
-        const int at = live ? cnt[warp][d] + rank : 0;
-        __syncwarp();
-        if (live) {
-            if (rank == 0) cnt[warp][d] += __popc(peers);
-            kd[at] = k;
-            vd[at] = v;
-        }
-        __syncwarp();
-    }
+    place_items(k, n - base, shift, bins, place[warp], lane, [&](int j, int at) {
+        kd[at] = k[j];
+        vd[at] = v[j];
+    });
 }
 
 // ---- gradient: pieces ----
@@ -269,170 +387,334 @@ struct Piece {
     int32_t slot;          // partial sum, or -1: the id has this piece alone
 };
 
-// For each run of equal ids below V: row_end[id] = its end, and its pieces.
-// The partial sums of a run that starts at b take slots ceil(b / kHalf), ...:
-// a run of more than kPiece items has at least as many multiples of kHalf as
-// pieces, so no two runs share a slot.
-__global__ void __launch_bounds__(256)
-    emb_pieces(const int32_t *key, int64_t n, int32_t V, int32_t *row_end,
-               Piece *pieces, Piece *joins, int32_t *counters) {
-    __shared__ int block_base, warp_cnt[8];
-    wait_prior_grid();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int32_t k = i < n ? key[i] : V;
-    const bool start = k < V && (i == 0 || key[i - 1] != k);
-    int64_t end = 0;
-    if (start) {
-        int64_t lo = i + 1, hi = min(n, i + kPiece);  // first position past the run
-        if (hi < n && key[hi] == k) {
-            lo = hi + 1;
-            hi = n;
-        }
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2;
-            if (key[mid] == k)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        end = lo;
-        row_end[k] = (int32_t)end;
+// First position past the run of equal keys that starts at i.
+template <typename K>
+__device__ __forceinline__ int64_t run_end(const K *key, int64_t i, int64_t n, int32_t k) {
+    int64_t lo = i + 1, hi = min(n, i + kPiece);
+    if (hi < n && key[hi] == k) {
+        lo = hi + 1;
+        hi = n;
     }
-    const int np = start ? (int)((end - i + kPiece - 1) / kPiece) : 0;
-    int incl = np;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (key[mid] == k)
+            lo = mid + 1;
+        else
+            hi = mid;
     }
-    if (lane == 31) warp_cnt[warp] = incl;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int all = 0;
-        for (int w = 0; w < 8; ++w) {
-            const int c = warp_cnt[w];
-            warp_cnt[w] = all;
-            all += c;
-        }
-        block_base = all ? atomicAdd(&counters[0], all) : 0;
-    }
-    __syncthreads();
-    if (!start) return;
-    Piece *p = pieces + block_base + warp_cnt[warp] + incl - np;
+    return lo;
+}
+
+// The pieces of the run [i, end) of id k.  Their partial sums take slots
+// ceil(i / kHalf), ...: a run of more than kPiece items has at least as many
+// multiples of kHalf as pieces, so no two runs share a slot.
+__device__ __forceinline__ void write_pieces(Piece *p, int np, int32_t k, int64_t i, int64_t end) {
     const int32_t slot = (int32_t)((i + kHalf - 1) / kHalf);
     for (int j = 0; j < np; ++j) {
         const int64_t at = i + (int64_t)j * kPiece;
         p[j] = Piece{k, (int32_t)at, (int32_t)min((int64_t)kPiece, end - at), np > 1 ? slot + j : -1};
     }
-    if (np > 1) joins[atomicAdd(&counters[1], 1)] = Piece{k, (int32_t)i, np, slot};
+}
+__device__ __forceinline__ Piece join_of(int np, int32_t k, int64_t i) {
+    return Piece{k, (int32_t)i, np, (int32_t)((i + kHalf - 1) / kHalf)};
+}
+
+__global__ void __launch_bounds__(256)
+    emb_pieces(const int32_t *key, int64_t n, int32_t V, Piece *pieces, Piece *joins, int32_t *counters) {
+    __shared__ int block_base;
+    wait_prior_grid();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int32_t k = i < n ? key[i] : V;
+    const bool start = k < V && (i == 0 || key[i - 1] != k);
+    const int64_t end = start ? run_end(key, i, n, k) : 0;
+    const int np = start ? (int)((end - i + kPiece - 1) / kPiece) : 0;
+    int all;
+    const int at = block_scan<8>(np, &all);
+    if (threadIdx.x == 0) block_base = all ? atomicAdd(&counters[0], all) : 0;
+    __syncthreads();
+    if (!start) return;
+    write_pieces(pieces + block_base + at, np, k, i, end);
+    if (np > 1) joins[atomicAdd(&counters[1], 1)] = join_of(np, k, i);
+}
+
+// Keys, sort and pieces of up to kSortItems * THREADS tokens in one block.
+template <int THREADS>
+struct SmallSort {
+    int32_t key[2][kSortItems * THREADS];
+    uint16_t item[2][kSortItems * THREADS];  // canonical index
+    int place[THREADS / 32][kMaxBins];
+    int joins;
+};
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    emb_sort_small(const __grid_constant__ Canonical c, int passes, int digit, int32_t *key, int32_t *val,
+                   Piece *pieces, Piece *joins, int32_t *counters) {
+    constexpr int kWarps = THREADS / 32;
+    constexpr int kPer = kMaxBins > THREADS ? kMaxBins / THREADS : 1;  // digits of a thread
+    extern __shared__ uint4 raw[];
+    SmallSort<THREADS> &s = *reinterpret_cast<SmallSort<THREADS> *>(raw);
+    wait_prior_grid();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = (int)c.n, base = warp * 32 * kSortItems, bins = 1 << digit;
+    if (threadIdx.x == 0) s.joins = 0;
+    int32_t k[kSortItems], v[kSortItems];
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+        const int i = base + 32 * j + lane;
+        v[j] = i;
+        k[j] = 0;
+        int32_t row;
+        if (i < n) canonical_token(c, i, k[j], row);
+    }
+    for (int p = 0; p < passes; ++p) {
+        const int shift = p * digit, to = p & 1;
+        for (int d = threadIdx.x; d < kWarps * kMaxBins / 4; d += THREADS)
+            reinterpret_cast<int4 *>(s.place)[d] = make_int4(0, 0, 0, 0);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSortItems; ++j)
+            if (base + 32 * j + lane < n) atomicAdd(&s.place[warp][(k[j] >> shift) & (bins - 1)], 1);
+        __syncthreads();
+        int sum = 0;
+#pragma unroll
+        for (int d = kPer * threadIdx.x; d < kPer * (threadIdx.x + 1); ++d)
+            if (d < bins)
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) sum += s.place[w][d];
+        int total;
+        int run = block_scan<kWarps>(sum, &total);
+#pragma unroll
+        for (int d = kPer * threadIdx.x; d < kPer * (threadIdx.x + 1); ++d)
+            if (d < bins)
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const int x = s.place[w][d];
+                    s.place[w][d] = run;
+                    run += x;
+                }
+        __syncthreads();
+        place_items(k, n - base, shift, bins, s.place[warp], lane, [&](int j, int at) {
+            s.key[to][at] = k[j];
+            s.item[to][at] = (uint16_t)v[j];
+        });
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSortItems; ++j) {
+            const int i = base + 32 * j + lane;
+            if (i < n) {
+                k[j] = s.key[to][i];
+                v[j] = s.item[to][i];
+            }
+        }
+    }
+    const int32_t *sorted = s.key[(passes - 1) & 1];
+    int np[kSortItems], mine = 0;  // pieces that start at this thread's items
+    int end[kSortItems];
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+        const int i = base + 32 * j + lane;
+        np[j] = end[j] = 0;
+        if (i >= n) continue;
+        key[i] = k[j];
+        val[i] = (int32_t)(k[j] < c.V ? (c.order ? c.order[v[j]] : (int64_t)v[j]) : 0);
+        if (k[j] >= c.V || (i > 0 && sorted[i - 1] == k[j])) continue;
+        end[j] = (int)run_end(sorted, i, n, k[j]);
+        np[j] = (end[j] - i + kPiece - 1) / kPiece;
+        mine += np[j];
+    }
+    int total;
+    int at = block_scan<kWarps>(mine, &total);
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+        if (np[j] == 0) continue;
+        const int i = base + 32 * j + lane;
+        write_pieces(pieces + at, np[j], k[j], i, end[j]);
+        at += np[j];
+        if (np[j] > 1) joins[atomicAdd(&s.joins, 1)] = join_of(np[j], k[j], i);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        counters[0] = total;
+        counters[1] = s.joins;
+    }
+}
+
+// ---- gradient: rows of dE without a token ----
+//
+// Zeros leave in many short blocks, in order: 2.2 GB took 281 us so (7.8 TB/s)
+// and 332 to 342 us in resident blocks that loop, whose warps drift apart.
+
+constexpr int kZeroThreads = 256;
+constexpr int kZeroVectors = 4;  // per thread
+
+// All of dE, beside the one block that sorts.  That block lets this grid start
+// once the work before it is complete; the last block here waits for the sort,
+// so that whoever waits for this grid has waited for both.
+__global__ void __launch_bounds__(kZeroThreads) emb_zero_all(float *dE, int64_t n4, int64_t n1) {
+    const int64_t first = (int64_t)blockIdx.x * kZeroThreads * kZeroVectors + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kZeroVectors; ++k) {
+        const int64_t i = first + k * kZeroThreads;
+        if (i < n4)
+            reinterpret_cast<float4 *>(dE)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        else if (4 * n4 + (i - n4) < n1)  // unaligned, or what is left
+            dE[4 * n4 + (i - n4)] = 0.f;
+    }
+    if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The rows that no sorted key names, a warp per row.
+constexpr int kAbsentThreads = 128;
+template <bool VEC>
+__global__ void __launch_bounds__(kAbsentThreads)
+    emb_zero_absent(const int32_t *key, int64_t n, int64_t H, int64_t V, float *dE) {
+    wait_prior_grid();
+    const int lane = threadIdx.x & 31;
+    const int64_t v = (int64_t)blockIdx.x * (kAbsentThreads / 32) + (threadIdx.x >> 5);
+    if (v >= V) return;
+    int64_t lo = 0, hi = n;  // first key >= v
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (key[mid] < v)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    if (lo < n && key[lo] == v) return;
+    float *row = dE + v * H;
+    if (VEC) {
+        for (int64_t c = 4 * lane; c < H; c += 128)
+            *reinterpret_cast<float4 *>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+        for (int64_t c = lane; c < H; c += 32) row[c] = 0.f;
+    }
 }
 
 // ---- gradient: sums ----
 
 constexpr int kSumThreads = 128;
+constexpr int kSumWarps = kSumThreads / 32;
+constexpr int kSumBlocks = 6;  // per SM
+constexpr int kLaneCols = 16;
+constexpr int kSumCols = 32 * kLaneCols;  // columns of a warp: 512
 
-// dE row and column c0.. of one id from its sum.
+// A lane's 16 columns of a warp's kSumCols: two vectors of 8 (VEC; vector k at
+// column 8 (lane + 32 k)), or 16 single ones (k at lane + 32 k).
 template <bool VEC>
-__device__ __forceinline__ void put_row(float *p, bool accumulate, float scale, float (&s)[8]) {
-    constexpr int N = VEC ? 8 : 1;
+struct Cols {
+    static constexpr int kN = VEC ? 2 : kLaneCols, kW = VEC ? 8 : 1;
+    static __device__ __forceinline__ int at(int lane, int k) { return VEC ? 8 * (lane + 32 * k) : lane + 32 * k; }
+};
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void get_cols(const T *src, int64_t cols, int lane, float (&v)[kLaneCols]) {
+    using C = Cols<VEC>;
 #pragma unroll
-    for (int j = 0; j < N; ++j) s[j] = __fmul_rn(scale, s[j]);
-    if (accumulate) {
-        float old[8];
-        if (VEC) {
-            const float4 a = reinterpret_cast<const float4 *>(p)[0];
-            const float4 b = reinterpret_cast<const float4 *>(p)[1];
-            old[0] = a.x; old[1] = a.y; old[2] = a.z; old[3] = a.w;
-            old[4] = b.x; old[5] = b.y; old[6] = b.z; old[7] = b.w;
+    for (int k = 0; k < C::kN; ++k) {
+        const int c = C::at(lane, k);
+        if constexpr (VEC) {
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (c < cols) get8(src + c, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[8 * k + j] = x[j];
         } else {
-            old[0] = *p;
+            v[k] = c < cols ? get1(src + c) : 0.f;
         }
-#pragma unroll
-        for (int j = 0; j < N; ++j) s[j] = __fadd_rn(old[j], s[j]);
     }
-    if (VEC)
-        put8(p, s);
-    else
-        *p = s[0];
 }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kSumThreads)
-    emb_sum(const T *dout, int64_t H, int64_t V, float scale,
-            const int32_t *val, const int32_t *row_end,
-            const Piece *pieces, const int32_t *counters, int accumulate,
-            float *dE, float *partial) {
-    constexpr int N = VEC ? 8 : 1;
-    constexpr int kCols = N * kSumThreads;
-    wait_prior_grid();
-    const int64_t ncb = (H + kCols - 1) / kCols;
-    const int64_t units = (int64_t)counters[0] * ncb;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const Piece p = pieces[u / ncb];
-        const int64_t c = (u % ncb) * kCols + N * (int64_t)threadIdx.x;
-        if (c >= H) continue;
-        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int i = 0; i < p.len; ++i) {
-            const T *src = dout + (int64_t)val[p.pos + i] * H + c;
-            if (VEC) {
-                float v[8];
-                get8(src, v);
+template <bool VEC>
+__device__ __forceinline__ void put_cols(float *dst, int64_t cols, int lane, const float (&v)[kLaneCols]) {
+    using C = Cols<VEC>;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[j] = __fadd_rn(s[j], v[j]);
-            } else {
-                s[0] = __fadd_rn(s[0], get1(src));
-            }
-        }
-        if (p.slot < 0) {
-            put_row<VEC>(dE + (int64_t)p.id * H + c, accumulate, scale, s);
-        } else if (VEC) {
-            put8(partial + (int64_t)p.slot * H + c, s);
+    for (int k = 0; k < C::kN; ++k) {
+        const int c = C::at(lane, k);
+        if (c >= cols) continue;
+        if constexpr (VEC) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = v[8 * k + j];
+            put8(dst + c, x);
         } else {
-            partial[(int64_t)p.slot * H + c] = s[0];
+            dst[c] = v[k];
         }
     }
-    if (accumulate) return;
-    for (int64_t v = blockIdx.x; v < V; v += gridDim.x) {  // rows without a token
-        if (row_end[v] != 0) continue;
-        float *row = dE + v * H;
-        if (VEC) {
-            const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            for (int64_t c = 8 * (int64_t)threadIdx.x; c < H; c += kCols) put8(row + c, zero);
-        } else {
-            for (int64_t c = threadIdx.x; c < H; c += kCols) row[c] = 0.f;
+}
+
+// Warps take units in fixed strides (drawing them from a counter put a
+// latency into every unit's chain: 300 us instead of 219 at 65536 x 4096).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kSumThreads, VEC ? kSumBlocks : 3)
+    emb_sum(const T *dout, int64_t H, float scale, const int32_t *val, const Piece *pieces,
+            const int32_t *counters, int accumulate, float *dE, float *partial) {
+    wait_prior_grid();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t ncb = (H + kSumCols - 1) / kSumCols;
+    const int64_t units = (int64_t)counters[0] * ncb, step = (int64_t)gridDim.x * kSumWarps;
+    int64_t u = (int64_t)blockIdx.x * kSumWarps + warp;
+    Piece next = u < units ? pieces[u / ncb] : Piece{};
+    for (; u < units; u += step) {
+        const Piece p = next;
+        const int row = lane < p.len ? val[p.pos + lane] : 0;  // kPiece == 32
+        if (u + step < units) next = pieces[(u + step) / ncb];
+        const int64_t c0 = (u % ncb) * kSumCols, cols = H - c0;
+        const T *src = dout + c0;
+        const bool last = p.slot < 0;
+        float *dst = (last ? dE + (int64_t)p.id * H : partial + (int64_t)p.slot * H) + c0;
+        float s[kLaneCols], old[kLaneCols];
+        if (last && accumulate) get_cols<VEC>(dst, cols, lane, old);
+        get_cols<VEC>(src + (int64_t)__shfl_sync(0xffffffffu, row, 0) * H, cols, lane, s);
+        int i = 1;
+        for (; i + 2 <= p.len; i += 2) {
+            float a[kLaneCols], b[kLaneCols];
+            get_cols<VEC>(src + (int64_t)__shfl_sync(0xffffffffu, row, i) * H, cols, lane, a);
+            get_cols<VEC>(src + (int64_t)__shfl_sync(0xffffffffu, row, i + 1) * H, cols, lane, b);
+#pragma unroll
+            for (int j = 0; j < kLaneCols; ++j) s[j] = __fadd_rn(__fadd_rn(s[j], a[j]), b[j]);
         }
+        if (i < p.len) {
+            float a[kLaneCols];
+            get_cols<VEC>(src + (int64_t)__shfl_sync(0xffffffffu, row, i) * H, cols, lane, a);
+#pragma unroll
+            for (int j = 0; j < kLaneCols; ++j) s[j] = __fadd_rn(s[j], a[j]);
+        }
+        if (last) {
+#pragma unroll
+            for (int j = 0; j < kLaneCols; ++j) {
+                s[j] = __fmul_rn(scale, s[j]);
+                if (accumulate) s[j] = __fadd_rn(old[j], s[j]);
+            }
+        }
+        put_cols<VEC>(dst, cols, lane, s);
     }
 }
 
 // The ids with more than one piece: their partial sums, added in order.
-template <bool VEC>
+constexpr int kJoinAhead = 16;  // loads in flight
 __global__ void __launch_bounds__(kSumThreads)
-    emb_join(int64_t H, float scale, const Piece *joins,
-             const int32_t *counters, int accumulate, float *dE,
-             const float *partial) {
-    constexpr int N = VEC ? 8 : 1;
-    constexpr int kCols = N * kSumThreads;
+    emb_join(int64_t H, float scale, const Piece *joins, const int32_t *counters, int accumulate,
+             float *dE, const float *partial) {
     wait_prior_grid();
-    const int64_t ncb = (H + kCols - 1) / kCols;
+    const int64_t ncb = (H + kSumThreads - 1) / kSumThreads;  // a column per thread
     const int64_t units = (int64_t)counters[1] * ncb;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const Piece p = joins[u / ncb];
-        const int64_t c = (u % ncb) * kCols + N * (int64_t)threadIdx.x;
+        const int64_t c = (u % ncb) * kSumThreads + threadIdx.x;
         if (c >= H) continue;
-        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int i = 0; i < p.len; ++i) {
-            const float *src = partial + (int64_t)(p.slot + i) * H + c;
-            if (VEC) {
-                float v[8];
-                get8(src, v);
+        const float *src = partial + (int64_t)p.slot * H + c;
+        float s = 0.f;
+        for (int i0 = 0; i0 < p.len; i0 += kJoinAhead) {
+            float v[kJoinAhead];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[j] = __fadd_rn(s[j], v[j]);
-            } else {
-                s[0] = __fadd_rn(s[0], *src);
-            }
+            for (int j = 0; j < kJoinAhead; ++j) v[j] = i0 + j < p.len ? src[(int64_t)(i0 + j) * H] : 0.f;
+#pragma unroll
+            for (int j = 0; j < kJoinAhead; ++j)
+                if (i0 + j < p.len) s = __fadd_rn(s, v[j]);
         }
-        put_row<VEC>(dE + (int64_t)p.id * H + c, accumulate, scale, s);
+        float *dst = dE + (int64_t)p.id * H + c;
+        s = __fmul_rn(scale, s);
+        *dst = accumulate ? __fadd_rn(*dst, s) : s;
     }
 }
 
@@ -441,7 +723,7 @@ __global__ void __launch_bounds__(kSumThreads)
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 struct BwdBuffers {
-    int32_t *key[2], *val[2], *hist, *row_end, *counters;
+    int32_t *key[2], *val[2], *hist, *counters;
     Piece *pieces, *joins;
     float *partial;
     size_t bytes;
@@ -453,7 +735,9 @@ int key_bits(int64_t V) {  // keys are 0 .. V
     return bits;
 }
 
-BwdBuffers carve(void *base, int64_t n, int64_t H, int64_t V) {
+int64_t tile_pitch(int64_t n) { return ((n + kSortTile - 1) / kSortTile + 3) / 4 * 4; }
+
+BwdBuffers carve(void *base, int64_t n, int64_t H) {
     BwdBuffers b{};
     char *p = static_cast<char *>(base);
     size_t at = 0;
@@ -462,14 +746,12 @@ BwdBuffers carve(void *base, int64_t n, int64_t H, int64_t V) {
         at += round256(bytes);
         return static_cast<void *>(q);
     };
-    const size_t tiles = (size_t)((n + kSortTile - 1) / kSortTile);
     for (int i = 0; i < 2; ++i) {
         b.key[i] = static_cast<int32_t *>(take((size_t)n * 4));
         b.val[i] = static_cast<int32_t *>(take((size_t)n * 4));
     }
-    b.hist = static_cast<int32_t *>(take(tiles * kMaxBins * 4));
-    b.row_end = static_cast<int32_t *>(take((size_t)V * 4));
-    b.counters = static_cast<int32_t *>(take(2 * 4));
+    b.hist = static_cast<int32_t *>(take((size_t)tile_pitch(n) * kMaxBins * 4));
+    b.counters = static_cast<int32_t *>(take(2 * 4));  // pieces, joins
     b.pieces = static_cast<Piece *>(take((size_t)n * sizeof(Piece)));
     b.joins = static_cast<Piece *>(take((size_t)(n / kPiece + 1) * sizeof(Piece)));
     b.partial = static_cast<float *>(take((size_t)(n / kHalf + 1) * (size_t)H * 4));
@@ -477,16 +759,63 @@ BwdBuffers carve(void *base, int64_t n, int64_t H, int64_t V) {
     return b;
 }
 
-template <typename T, bool VEC>
-cudaError_t launch_sums(const void *dout, int64_t H, int64_t V, float scale, const int32_t *val,
-                        const BwdBuffers &b, bool accumulate, float *dE, const DeviceInfo &di,
-                        cudaStream_t st) {
-    cudaError_t e = launch_dependent(emb_sum<T, VEC>, (int64_t)di.sm_count * 16, kSumThreads, st,
-                                     static_cast<const T *>(dout), H, V, scale, val, b.row_end,
-                                     b.pieces, b.counters, (int)accumulate, dE, b.partial);
+template <int THREADS>
+cudaError_t launch_small(const Canonical &c, const BwdBuffers &b, int passes, int digit, cudaStream_t st) {
+    constexpr size_t smem = sizeof(SmallSort<THREADS>);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(emb_sort_small<THREADS>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent_smem(emb_sort_small<THREADS>, 1, THREADS, smem, st, c, passes, digit, b.key[0],
+                                 b.val[0], b.pieces, b.joins, b.counters);
+}
+
+// Sorts the canonical tokens and finds their pieces; *where: which of the two
+// buffers holds the sorted keys and rows.
+cudaError_t launch_sort(const Canonical &c, const BwdBuffers &b, int *where, cudaStream_t st) {
+    const int bits = key_bits(c.V);
+    const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
+    const int digit = (bits + passes - 1) / passes;
+    *where = 0;
+    if (c.n <= kSortItems * kTinyThreads) return launch_small<kTinyThreads>(c, b, passes, digit, st);
+    if (c.n <= kSmallSort) return launch_small<kSmallThreads>(c, b, passes, digit, st);
+    const int64_t tiles = (c.n + kSortTile - 1) / kSortTile, pitch = tile_pitch(c.n);
+    const int bins = 1 << digit;
+    cudaError_t e = launch_dependent(emb_keys, tiles, kSortThreads, st, c, b.key[0], b.val[0], bins, b.hist,
+                                     tiles, pitch, b.counters);
+    int src = 0;
+    for (int p = 0; p < passes && e == cudaSuccess; ++p) {
+        const int shift = p * digit;
+        if (p > 0)
+            e = launch_dependent(emb_histogram, tiles, kSortThreads, st, (const int32_t *)b.key[src], c.n, shift,
+                                 bins, b.hist, tiles, pitch);
+        if (e != cudaSuccess) return e;
+        const bool scanned = tiles > kInlineScanTiles;
+        if (scanned) e = launch_dependent(emb_scan, 1, kScanThreads, st, b.hist, pitch * bins);
+        if (e != cudaSuccess) return e;
+        e = launch_dependent(scanned ? emb_scatter<true> : emb_scatter<false>, tiles, kSortThreads, st,
+                             (const int32_t *)b.key[src], (const int32_t *)b.val[src], b.key[1 - src],
+                             b.val[1 - src], c.n, shift, bins, (const int32_t *)b.hist, pitch);
+        src = 1 - src;
+    }
     if (e != cudaSuccess) return e;
-    return launch_dependent(emb_join<VEC>, (int64_t)di.sm_count * 4, kSumThreads, st, H, scale,
-                            b.joins, b.counters, (int)accumulate, dE, b.partial);
+    *where = src;
+    return launch_dependent(emb_pieces, (c.n + 255) / 256, 256, st, (const int32_t *)b.key[src], c.n,
+                            (int32_t)c.V, b.pieces, b.joins, b.counters);
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_sums(const void *dout, int64_t H, float scale, int64_t n, int where, const BwdBuffers &b,
+                        bool accumulate, float *dE, const DeviceInfo &di, cudaStream_t st) {
+    cudaError_t e = launch_dependent(emb_sum<T, VEC>, (int64_t)di.sm_count * kSumBlocks, kSumThreads, st,
+                                     static_cast<const T *>(dout), H, scale, (const int32_t *)b.val[where],
+                                     (const Piece *)b.pieces, (const int32_t *)b.counters, (int)accumulate, dE,
+                                     b.partial);
+    if (e != cudaSuccess || n <= kPiece) return e;
+    return launch_dependent(emb_join, (int64_t)di.sm_count * 16, kSumThreads, st, H, scale,
+                            (const Piece *)b.joins, (const int32_t *)b.counters, (int)accumulate, dE,
+                            (const float *)b.partial);
 }
 
 template <typename TE, typename TO>
@@ -513,9 +842,7 @@ cudaError_t launch_embedding(const int64_t *ids, const int32_t *cu, int num_seqs
                : launch_lookup<float, float>(ids, cu, num_seqs, E, T, H, V, scale, out, di, st);
 }
 
-size_t embedding_bwd_workspace_bytes(int64_t n, int64_t H, int64_t V) {
-    return carve(nullptr, n, H, V).bytes;
-}
+size_t embedding_bwd_workspace_bytes(int64_t n, int64_t H) { return carve(nullptr, n, H).bytes; }
 
 cudaError_t launch_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *ids,
                                  const int32_t *cu, int num_seqs, int64_t T, int64_t H, int64_t V,
@@ -524,38 +851,34 @@ cudaError_t launch_embedding_bwd(const void *dout, rk_dtype dout_type, const int
                                  cudaStream_t st) {
     if (n == 0)
         return accumulate ? cudaSuccess : cudaMemsetAsync(dE, 0, (size_t)V * (size_t)H * 4, st);
-    const BwdBuffers b = carve(workspace, n, H, V);
-    const int64_t blocks = std::min<int64_t>((std::max(n, V) + 255) / 256, (int64_t)di.sm_count * 8);
-    cudaError_t e = launch_dependent(emb_keys, blocks, 256, st, ids, cu, num_seqs, T, V, order, n,
-                                     b.key[0], b.val[0], b.row_end, b.counters, di.err);
+    const BwdBuffers b = carve(workspace, n, H);
+    const Canonical c{ids, cu, num_seqs, T, V, order, n, di.err};
+    int where;
+    cudaError_t e = launch_sort(c, b, &where, st);
     if (e != cudaSuccess) return e;
-    const int bits = key_bits(V);
-    const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
-    const int digit = (bits + passes - 1) / passes;
-    const int64_t tiles = (n + kSortTile - 1) / kSortTile;
-    int src = 0;
-    for (int p = 0; p < passes; ++p) {
-        const int shift = p * digit, bins = 1 << digit;
-        e = launch_dependent(emb_histogram, tiles, kSortThreads, st, b.key[src], n, shift, bins, b.hist,
-                             tiles);
-        if (e != cudaSuccess) return e;
-        e = launch_dependent(emb_scan, 1, kScanThreads, st, b.hist, tiles * bins);
-        if (e != cudaSuccess) return e;
-        e = launch_dependent(emb_scatter, tiles, kSortThreads, st, b.key[src], b.val[src],
-                             b.key[1 - src], b.val[1 - src], n, shift, bins, b.hist, tiles);
-        if (e != cudaSuccess) return e;
-        src = 1 - src;
+    // Zeros in the rows without a token.  While one block sorts, the rest of
+    // the device writes zeros over all of dE, and the rows with a token are
+    // written again, at most 1 / kZeroAllShare of them (8192 tokens, 152064 x
+    // 3584: 34 us of sorting hidden for 8 us more to write).  Otherwise each
+    // row looks itself up in the sorted keys.
+    if (!accumulate && n <= kSmallSort && n * kZeroAllShare <= V) {
+        const int64_t n1 = V * H, n4 = aligned(dE, 16) ? n1 / 4 : 0;
+        const int64_t per = kZeroThreads * kZeroVectors, blocks = (n4 + (n1 - 4 * n4) + per - 1) / per;
+        if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        e = launch_dependent(emb_zero_all, blocks, kZeroThreads, st, dE, n4, n1);
+    } else if (!accumulate) {
+        const int64_t blocks = (V + kAbsentThreads / 32 - 1) / (kAbsentThreads / 32);
+        const bool v4 = H % 4 == 0 && aligned(dE, 16);
+        e = launch_dependent(v4 ? emb_zero_absent<true> : emb_zero_absent<false>, blocks, kAbsentThreads, st,
+                             (const int32_t *)b.key[where], n, H, V, dE);
     }
-    e = launch_dependent(emb_pieces, (n + 255) / 256, 256, st, b.key[src], n, (int32_t)V, b.row_end,
-                         b.pieces, b.joins, b.counters);
     if (e != cudaSuccess) return e;
     const bool vec = H % 8 == 0 && aligned(dout, 16) && aligned(dE, 16);
-    const int32_t *val = b.val[src];
     if (dout_type == RK_BF16)
-        return vec ? launch_sums<uint16_t, true>(dout, H, V, scale, val, b, accumulate, dE, di, st)
-                   : launch_sums<uint16_t, false>(dout, H, V, scale, val, b, accumulate, dE, di, st);
-    return vec ? launch_sums<float, true>(dout, H, V, scale, val, b, accumulate, dE, di, st)
-               : launch_sums<float, false>(dout, H, V, scale, val, b, accumulate, dE, di, st);
+        return vec ? launch_sums<uint16_t, true>(dout, H, scale, n, where, b, accumulate, dE, di, st)
+                   : launch_sums<uint16_t, false>(dout, H, scale, n, where, b, accumulate, dE, di, st);
+    return vec ? launch_sums<float, true>(dout, H, scale, n, where, b, accumulate, dE, di, st)
+               : launch_sums<float, false>(dout, H, scale, n, where, b, accumulate, dE, di, st);
 }
 
 }  // namespace rk

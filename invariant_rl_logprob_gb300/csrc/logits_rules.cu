@@ -12,12 +12,11 @@
 // Data.  A warp copies its segment of the next rows into a ring of its own in
 // shared memory (cp.async, 16 bytes a lane, or 4 where rows are not 16-byte
 // aligned; the mask words with them) while it works on the present one, so no
-// barrier stands between the rows and a touched column's logit is a
-// shared-memory read.  What the rows say about themselves is read once per
-// block.  Results of
-// kApply and kBwd go out through shared memory too, so that a warp writes
-// whole lines although a lane owns 32 columns.  The lanes take their 16-byte
-// pieces in rotated order, which spreads a quarter warp over all banks.
+// barrier stands between the rows.  What the rows say about themselves is read
+// once per block.  Results of kApply and kBwd leave through the same stage, so
+// that a warp writes whole lines although a lane owns 32 columns.  The lanes
+// take their 16-byte pieces in rotated order, which spreads a quarter warp
+// over all banks.
 //
 // History.  The block counts a request's tokens of its slice in shared
 // memory (one word per column: bit 31 in the prompt, bits 0-30 times
@@ -263,12 +262,6 @@ struct Lane<float> {
     static __device__ __forceinline__ int bits(int lane) { return 4 * (lane & 7); }
 };
 
-// One ring stage: the segment, 16 bytes more for rows that start on an odd
-// element (they sit one element further in), and the segment's mask words.
-template <typename T>
-constexpr int mask_at() { return kSegCols * (int)sizeof(T) + 16; }
-template <typename T>
-constexpr int stage_bytes() { return mask_at<T>() + kSegCols / 8; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -448,17 +441,23 @@ __device__ __forceinline__ void unpack(const uint4 &w, uint64_t (&z)[4]) {
     for (int j = 0; j < 4; ++j) z[j] = pair(bf16_lo(q[j]), bf16_hi(q[j]));
 }
 
+// Shared memory of a block: counts, touched words, rows, lists and bias
+// indices, and a ring of stages per warp.  A stage holds the segment's logits
+// (16 bytes more for rows that start on an odd element: they sit one element
+// further in) and afterwards its results, and the segment's mask words.
+// Blocks of up to 113 KB run two to an SM, which beats a second stage.
 template <RulesOp OP, typename TIn, typename TOut>
 struct Config {
-    static constexpr int kStages = 2;
-    static constexpr int kOutBytes = OP == kLogp ? 0 : kSegCols * (int)sizeof(TOut);
+    static constexpr int kElem = OP != kLogp && sizeof(TOut) > sizeof(TIn) ? sizeof(TOut) : sizeof(TIn);
+    static constexpr int kStages = kElem == 2 ? 2 : 1;
+    static constexpr int kMaskAt = kSegCols * kElem + 16;
+    static constexpr int kStageBytes = kMaskAt + kSegCols / 8;
     // fp32 results of bf16 pieces: neighbouring lanes would write the same bank
     // group, so odd lanes swap neighbouring pieces
     static constexpr int kSwap = (sizeof(TIn) == 2 && sizeof(TOut) == 4) ? 1 : 0;
-    static constexpr int kWarpBytes = kStages * stage_bytes<TIn>() + kOutBytes;
     static size_t smem(bool bias) {
         return (size_t)(kSliceCols + kThreads) * 4 + kMaxRun * sizeof(RowInfo) +
-               (size_t)kSliceCols * (bias ? 4 : 2) + (size_t)kWarps * kWarpBytes;
+               (size_t)kSliceCols * (bias ? 4 : 2) + (size_t)kWarps * kStages * kStageBytes;
     }
 };
 
@@ -508,8 +507,7 @@ __global__ void __launch_bounds__(kThreads)
     sh.bias = rules.bias_ids ? sh.list + kSliceCols : nullptr;
     unsigned char *p = reinterpret_cast<unsigned char *>(sh.list + (rules.bias_ids ? 2 : 1) * kSliceCols);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned char *ring = p + warp * C::kWarpBytes;
-    unsigned char *staged = ring + C::kStages * stage_bytes<TIn>();
+    unsigned char *ring = p + warp * C::kStages * C::kStageBytes;
     // Launched with programmatic stream serialisation: wait until the previous
     // kernel of the stream has completed before reading or writing anything.
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -537,15 +535,15 @@ __global__ void __launch_bounds__(kThreads)
     const TIn *zseg = reinterpret_cast<const TIn *>(io.logits) + t0 * io.ld + seg0;
     auto prefetch = [&](int k) {
         if (k < n && rows[k].tgt >= 0) {
-            unsigned char *stage = ring + (k % C::kStages) * stage_bytes<TIn>();
+            unsigned char *stage = ring + (k % C::kStages) * C::kStageBytes;
             start_copy(stage, zseg + k * io.ld, cols, io.vec_in, lane);
             if (rows[k].mrow >= 0 && inside)
-                cp_async4(smem_u32(stage + mask_at<TIn>()) + 4 * lane,
+                cp_async4(smem_u32(stage + C::kMaskAt) + 4 * lane,
                           rules.mask + (int64_t)rows[k].mrow * words + (seg0 >> 5) + lane);
         }
         cp_commit();
     };
-    for (int k = 0; k < C::kStages - 1; ++k) prefetch(k);
+    for (int k = 0; k < C::kStages; ++k) prefetch(k);
     for (int k = threadIdx.x + 1; k < n; k += kThreads) find_step(io, rules, rows[k - 1], rows[k]);
     __syncthreads();
 
@@ -590,9 +588,7 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
         ok = ok && q.ok;
-        // the row's stage is complete once all but the newest copies are
-        prefetch(k + C::kStages - 1);
-        cp_wait<C::kStages - 1>();
+        cp_wait<C::kStages - 1>();  // all copies but those of later rows
         __syncwarp();
         TOut *orow = reinterpret_cast<TOut *>(io.out) + t * io.ld_out + seg0;
         if (!ok) {
@@ -607,12 +603,14 @@ __global__ void __launch_bounds__(kThreads)
             }
             if (OP == kBwd || (OP == kApply && row.tgt != kInactive))
                 for (int c = lane; c < cols; c += 32) put(orow + c, fill);
+            prefetch(k + C::kStages);
             continue;
         }
-        const unsigned char *stage = ring + (k % C::kStages) * stage_bytes<TIn>();
+        unsigned char *stage = ring + (k % C::kStages) * C::kStageBytes;
         const bool odd = !io.vec_in && odd_start(zseg + k * io.ld);
-        const TIn *zs = reinterpret_cast<const TIn *>(stage) + (odd ? 1 : 0);
-        const uint32_t *masks = reinterpret_cast<const uint32_t *>(stage + mask_at<TIn>());
+        // single logits: from the stage, or, where results replace it, from the row
+        const TIn *zs = OP == kLogp ? reinterpret_cast<const TIn *>(stage) + (odd ? 1 : 0) : zseg + k * io.ld;
+        const uint32_t *masks = reinterpret_cast<const uint32_t *>(stage + C::kMaskAt);
         const bool masked = row.mrow >= 0;
         const uint32_t live = masked ? inside & masks[lane] : inside;  // columns the mask allows
         // a listed column's y from its logit z (false: masked)
@@ -629,6 +627,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int i = 0; i < L::kPieces; ++i)
             w[i] = load_piece(stage + 16 * (lane * L::kPieces + L::order(lane, i)), odd);
+        if (OP != kLogp) __syncwarp();  // the stage is read
 
         if (OP == kLogp) {
             const float c = __fmul_rn(kLog2e, q.itau);
@@ -755,13 +754,13 @@ __global__ void __launch_bounds__(kThreads)
                     if ((int32_t)(keep << (31 - N * i - j)) >= 0) x[j] = OP == kApply ? -INFINITY : 0.f;
                 const int piece = lane * L::kPieces + L::order(lane, i);  // of the segment
                 if constexpr (sizeof(TOut) == 4) {
-                    float4 *o = reinterpret_cast<float4 *>(staged);
+                    float4 *o = reinterpret_cast<float4 *>(stage);
 #pragma unroll
                     for (int h = 0; h < N / 4; ++h)
                         o[(piece * (N / 4) + h) ^ (C::kSwap ? lane & 1 : 0)] =
                             make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
                 } else {
-                    uint32_t *o = reinterpret_cast<uint32_t *>(staged) + piece * (N / 2);
+                    uint32_t *o = reinterpret_cast<uint32_t *>(stage) + piece * (N / 2);
                     if constexpr (N == 8)
                         *reinterpret_cast<uint4 *>(o) =
                             make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
@@ -774,7 +773,7 @@ __global__ void __launch_bounds__(kThreads)
             // the touched columns, and the target's, over what stands there
             __syncwarp();
             auto put_column = [&](int j, float v) {
-                put(reinterpret_cast<TOut *>(staged) + (j ^ (C::kSwap ? (j >> 3) & 4 : 0)), v);
+                put(reinterpret_cast<TOut *>(stage) + (j ^ (C::kSwap ? (j >> 3) & 4 : 0)), v);
             };
             if (OP == kBwd && row.tgt >= seg0 && row.tgt < seg0 + cols) {
                 const int j = row.tgt - (int)seg0;
@@ -795,9 +794,10 @@ __global__ void __launch_bounds__(kThreads)
                 }
             }
             __syncwarp();
-            write_out<C::kSwap>(staged, orow, cols, io.vec_out, lane);
+            write_out<C::kSwap>(stage, orow, cols, io.vec_out, lane);
         }
-        __syncwarp();  // the stage and the staging area are free again
+        __syncwarp();  // the stage is free again
+        prefetch(k + C::kStages);
     }
 }
 
@@ -881,11 +881,11 @@ void dependent(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, unsigned grid
     cfg->numAttrs = 1;
 }
 
-// Rows per block: about eight blocks per SM, so that a block counts a
-// history as seldom as that allows.
+// Rows per block: one wave of two blocks per SM where kMaxRun allows it, so
+// that a block counts a history as seldom as possible.
 int rows_per_block(int64_t T, int64_t V, const DeviceInfo &di) {
-    const int64_t slices = (V + kSliceCols - 1) / kSliceCols;
-    const int64_t want = T * slices / ((int64_t)di.sm_count * 8);
+    const int64_t slices = (V + kSliceCols - 1) / kSliceCols, blocks = (int64_t)di.sm_count * 2;
+    const int64_t want = (T * slices + blocks - 1) / blocks;
     return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxRun, want));
 }
 

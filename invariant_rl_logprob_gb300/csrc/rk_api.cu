@@ -666,7 +666,7 @@ rk_status rk_embedding(const int64_t *ids, const int32_t *cu_seqlens, int32_t nu
 
 size_t rk_embedding_bwd_workspace_size(int64_t n, int64_t H, int64_t V) {
     if (n <= 0 || H <= 0 || V <= 0) return 0;
-    return rk::embedding_bwd_workspace_bytes(n, H, V);
+    return rk::embedding_bwd_workspace_bytes(n, H);
 }
 
 rk_status rk_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *ids,
@@ -686,7 +686,7 @@ rk_status rk_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *
     const int64_t lim = int64_t(1) << 31;
     if (V >= lim - 1 || T >= lim || H >= lim || n >= lim) return RK_ERR_UNSUPPORTED;
     if ((dout && !elem_aligned(dout, dout_type)) || !aligned(dE, 4)) return RK_ERR_INVALID_ARG;
-    if (n > 0 && (!workspace || workspace_bytes < rk::embedding_bwd_workspace_bytes(n, H, V)))
+    if (n > 0 && (!workspace || workspace_bytes < rk::embedding_bwd_workspace_bytes(n, H)))
         return RK_ERR_WORKSPACE;
     if (n > 0 && !aligned(workspace, 16)) return RK_ERR_INVALID_ARG;
     DeviceInfo di;

@@ -97,7 +97,7 @@ cudaError_t launch_rules_bwd(const RulesMatrix &logits, const int64_t *targets, 
 cudaError_t launch_embedding(const int64_t *ids, const int32_t *cu, int num_seqs, const void *E,
                              rk_dtype e_type, int64_t T, int64_t H, int64_t V, float scale,
                              void *out, rk_dtype out_type, const DeviceInfo &di, cudaStream_t st);
-size_t embedding_bwd_workspace_bytes(int64_t n, int64_t H, int64_t V);
+size_t embedding_bwd_workspace_bytes(int64_t n, int64_t H);
 cudaError_t launch_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *ids,
                                  const int32_t *cu, int num_seqs, int64_t T, int64_t H, int64_t V,
                                  float scale, const int64_t *order, int64_t n, float *dE,
