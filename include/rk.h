@@ -494,7 +494,7 @@ rk_status rk_logits_rules_apply(const void *logits, rk_dtype logits_type, int64_
  *   logits as for rk_logits_rules_apply; targets, cu_seqlens, num_seqs, logp and
  *   lse (may be NULL) as for rk_logp_from_logits
  *   workspace  >= rk_logp_from_logits_rules_workspace_size(T, V) bytes, 16-byte
- *              aligned: per row a (max, sum-exp) partial for every 1024 columns
+ *              aligned: per row eight (max, sum-exp) partials for every 8192 columns
  *              and the target's y
  */
 size_t rk_logp_from_logits_rules_workspace_size(int64_t T, int64_t V);

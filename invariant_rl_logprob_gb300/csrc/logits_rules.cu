@@ -4,19 +4,22 @@
 // (kLogp: selected logprob and log-sum-exp) and differentiated (kBwd).
 //
 // Decomposition.  A block works on a slice of kSliceCols columns and a run of
-// consecutive rows; each of its warps owns a segment of kSegCols columns of
-// that slice, and each lane 32 neighbouring columns of the segment: one word
-// of a grammar mask, and one word that tells which of them the rules touch
-// (seen before, or biased).  The others need the temperature and mask only.
+// consecutive rows.  Its warps own the slice's blocks of 64 columns in turn,
+// because text is made of few tokens and those sit at the low ids: so the
+// warps of the first slice share them.  Each lane owns 32 neighbouring
+// columns: one word of a grammar mask, and one word that tells which of them
+// the rules touch (seen before, or biased).  The others need the temperature
+// and the mask only.
 //
-// Data.  A warp copies its segment of the next rows into a ring of its own in
-// shared memory (cp.async, 16 bytes a lane, or 4 where rows are not 16-byte
-// aligned; the mask words with them) while it works on the present one, so no
-// barrier stands between the rows.  What the rows say about themselves is read
-// once per block.  Results of kApply and kBwd leave through the same stage, so
-// that a warp writes whole lines although a lane owns 32 columns.  The lanes
-// take their 16-byte pieces in rotated order, which spreads a quarter warp
-// over all banks.
+// Data.  A warp copies its columns of the next row into shared memory of its
+// own (cp.async, 16 bytes a lane, or 4 where rows are not 16-byte aligned; the
+// mask words with them) while it works on the present one, so no barrier
+// stands between the rows.  What the rows say about themselves is read once
+// per block.  Results of kApply and kBwd leave through the same memory, so
+// that a warp writes whole lines although a lane owns 32 columns.  Each lane's
+// 32 columns are followed by 16 bytes: they spread a quarter warp's 16-byte
+// accesses over all banks, and hold the end of a row that starts on an odd
+// element.
 //
 // History.  The block counts a request's tokens of its slice in shared
 // memory (one word per column: bit 31 in the prompt, bits 0-30 times
@@ -25,15 +28,15 @@
 // to the counts without a barrier: its column belongs to one lane.  Longer
 // steps add their tokens block-wide; any other change counts anew.  Each warp
 // lists its touched columns in ascending order, 32 of which its lanes take at
-// a time: text is made of few tokens, which sit at the low ids, so lanes that
-// looped over their own columns would wait for the first lane's 32.
+// a time; lanes that looped over their own would wait for the one with the
+// most.
 //
-// Batch invariance: a row's partial (max, sum) of a segment is formed by a
-// tree fixed by the column index alone, and the segments' partials are merged
-// in a fixed order: nothing depends on T, on where the row sits or on how the
-// rows were cut into runs.
+// Batch invariance: a warp's partial (max, sum) of a row is formed by a tree
+// fixed by the columns' indices and by which of them are touched, and the
+// partials are merged in a fixed order: nothing depends on T, on where the row
+// sits or on how the rows were cut into runs.
 #include <algorithm>
-#include <cfloat>
+#include <type_traits>
 
 #include "rk_device.cuh"
 #include "rk_internal.h"
@@ -42,17 +45,24 @@ namespace rk {
 namespace {
 
 constexpr int kLaneCols = 32;
-constexpr int kSegCols = 32 * kLaneCols;       // 1024 columns per warp
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSliceCols = kSegCols * kWarps;  // 8192 columns per block
+constexpr int kSliceCols = kThreads * kLaneCols;  // 8192 columns per block
 constexpr int kMaxRun = 64;                    // rows per block at most
 constexpr int kMaxBiases = 65534;  // per request: indices are kept in 16 bits
 constexpr uint32_t kPromptBit = 0x80000000u;
 constexpr uint32_t kNegInf2 = 0xFF80FF80u;  // two bf16 -inf
-constexpr uint32_t kLowest2 = 0xFF7FFF7Fu;  // two bf16 lowest finite values
+constexpr float kLn2 = 0.69314718055994531f;
 
 enum RulesOp { kApply, kLogp, kBwd };
+
+// The first of a lane's columns in the slice.
+__device__ __forceinline__ int lane_col(int warp, int lane) {
+    return ((lane >> 1) * kWarps + warp) * 64 + (lane & 1) * kLaneCols;
+}
+// The warp and lane that own a slice's column.
+__device__ __forceinline__ int owner_warp(int c) { return (c >> 6) & (kWarps - 1); }
+__device__ __forceinline__ int owner_lane(int c) { return (c >> 9 << 1) | (c >> 5 & 1); }
 
 struct RulesIo {
     const void *logits;
@@ -62,28 +72,27 @@ struct RulesIo {
     int num_seqs;
     int64_t T, V;
     int run;         // rows per block
-    int vec_in;      // every row starts on a 16-byte boundary
     const float *lse, *grad;  // kBwd
     void *out;       // kApply, kBwd
     int64_t ld_out;
-    int vec_out;
-    float2 *part;    // kLogp: [T][segments] (max of y, sum relative to it)
+    float2 *part;    // kLogp: [T][kWarps per slice] (max of y, sum relative to it)
     float *ytgt;     // kLogp: [T] y of the target, -inf when it is masked
     unsigned *err;
 };
 
 // What a row says about itself.
 constexpr int32_t kInactive = -1, kBadTarget = -2, kBadRules = -3;
-struct RowInfo {
+struct __align__(16) RowInfo {
     int32_t tgt;  // the target, or one of the codes above
-    int32_t req, len, mrow;
-    // how its history differs from the row before: by one token, by none, or
-    // else (kAnew); a token outside the vocabulary counts as none
+    int32_t mrow;
+    // how its history differs from the row before: by one token (kPassed: which
+    // is not in the vocabulary), by none, or else (kAnew)
     int32_t step;
     int32_t step_prompt;
     float lse, g;
+    int32_t req, len;
 };
-constexpr int32_t kNoToken = -1, kAnew = -2;
+constexpr int32_t kNoToken = -1, kAnew = -2, kPassed = -3;
 
 template <RulesOp OP>
 __device__ __forceinline__ RowInfo row_info(const RulesIo &io, const rk_logits_rules &r, int64_t t) {
@@ -172,7 +181,7 @@ __device__ __forceinline__ void find_step(const RulesIo &io, const rk_logits_rul
         return;
     }
     const int64_t v = r.tokens[a + was];
-    if (v >= 0 && v < io.V) row.step = (int32_t)v;
+    row.step = v >= 0 && v < io.V ? (int32_t)v : kPassed;
     row.step_prompt = r.prompt_lengths && was < r.prompt_lengths[row.req];
 }
 
@@ -223,20 +232,10 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-    return v;
+    float d;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+    return d;
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -244,26 +243,21 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// A lane's 32 columns as 16-byte pieces.  Piece register i holds piece
-// order(i) of the lane: rotated by lane so that the eight lanes of a quarter
-// warp read eight different bank groups.
+// A lane's 32 columns as 16-byte pieces, and the bytes from lane to lane.
 template <typename T>
-struct Lane;
-template <>
-struct Lane<uint16_t> {
-    static constexpr int kPieces = 4, kCols = 8;  // pieces, columns of a piece
-    static __device__ __forceinline__ int order(int lane, int i) { return (i + (lane >> 1)) & 3; }
-    static __device__ __forceinline__ int bits(int lane) { return 8 * ((lane >> 1) & 3); }
-};
-template <>
-struct Lane<float> {
-    static constexpr int kPieces = 8, kCols = 4;
-    static __device__ __forceinline__ int order(int lane, int i) { return (i + lane) & 7; }
-    static __device__ __forceinline__ int bits(int lane) { return 4 * (lane & 7); }
+struct Lane {
+    static constexpr int kCols = 16 / (int)sizeof(T), kPieces = kLaneCols / kCols;
+    static constexpr int kPitch = kLaneCols * (int)sizeof(T) + 16;
+    // Spread over the warp piece by piece, lane l has pieces l, l + 32, ...: the
+    // step from one to the next in shared memory and in columns.
+    static constexpr int kLanes = 32 / kPieces;
+    static constexpr int kPieceRow = kLanes * kPitch, kPieceCols = kLanes / 2 * kWarps * 64;
 };
 
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
@@ -282,45 +276,59 @@ __device__ __forceinline__ bool odd_start(const uint16_t *src) {
 }
 __device__ __forceinline__ bool odd_start(const float *) { return false; }
 
-// Starts the copy of `cols` columns from src into a stage (2 bytes into it
-// after an odd start).  Nothing outside [src, src + cols) is read.
-template <typename T>
-__device__ __forceinline__ void start_copy(unsigned char *stage, const T *src, int cols, bool vec,
+// Starts the copy of a warp's columns of a row's slice (`src`: its first
+// element, `width`: its columns) into a stage.  After an odd start the columns
+// sit one element further in.  Nothing outside the slice is read.
+template <bool VEC, typename T>
+__device__ __forceinline__ void start_copy(unsigned char *stage, const T *src, int width, int warp,
                                            int lane) {
+    using L = Lane<T>;
     const uint32_t dst = smem_u32(stage);
-    if (vec) {
-        constexpr int kPer = 16 / (int)sizeof(T);
+    if constexpr (VEC) {
+        // piece x = lane + 32 i of the warp's: a fixed step from i to i + 1
+        const int o = lane / L::kPieces, part = lane % L::kPieces;
+        const int c = lane_col(warp, o) + part * L::kCols;
+        const uint32_t d = dst + o * L::kPitch + 16 * part;
+        if (width == kSliceCols) {
 #pragma unroll
-        for (int i = 0; i < kSegCols / kPer / 32; ++i) {
-            const int c = (lane + 32 * i) * kPer;
-            const int n = min(kPer, cols - c);
-            if (n > 0) cp_async16(dst + c * (int)sizeof(T), src + c, n * (int)sizeof(T));
+            for (int i = 0; i < L::kPieces; ++i)
+                cp_async16(d + i * L::kPieceRow, src + c + i * L::kPieceCols);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < L::kPieces; ++i) {
+                const int n = min(L::kCols, width - c - i * L::kPieceCols);
+                if (n > 0)
+                    cp_async16_part(d + i * L::kPieceRow, src + c + i * L::kPieceCols, n * (int)sizeof(T));
+            }
         }
     } else if constexpr (sizeof(T) == 4) {
-#pragma unroll 8
-        for (int c = lane; c < cols; c += 32) cp_async4(dst + 4 * c, src + c);
+#pragma unroll 4
+        for (int o = 0; o < 32; ++o) {
+            const int c = lane_col(warp, o) + lane;
+            if (c < width) cp_async4(dst + o * L::kPitch + 4 * lane, src + c);
+        }
     } else {
-        // words on 4-byte boundaries; a word that the row does not fill is
+        // words on 4-byte boundaries; one that reaches out of the slice is
         // copied by element
-        const int odd = odd_start(src) ? 1 : 0;
-        uint16_t *d = reinterpret_cast<uint16_t *>(stage);
-#pragma unroll 8
-        for (int w = lane; 2 * w < cols + odd; w += 32) {
-            const int c = 2 * w - odd;  // its first column
-            if (c >= 0 && c + 1 < cols) {
-                cp_async4(dst + 4 * w, src + c);
+        const int odd = odd_start(src) ? 1 : 0, per = kLaneCols / 2 + odd;  // words of a lane's columns
+#pragma unroll 2
+        for (int x = lane; x < 32 * per; x += 32) {
+            const int o = odd ? x / (kLaneCols / 2 + 1) : x / (kLaneCols / 2), w = x - o * per;
+            const int c = lane_col(warp, o) + 2 * w - odd;  // its first column
+            if (c >= 0 && c + 1 < width) {
+                cp_async4(dst + o * L::kPitch + 4 * w, src + c);
             } else {
-                if (c >= 0) d[2 * w] = src[c];
-                if (c + 1 < cols) d[2 * w + 1] = src[c + 1];
+                uint16_t *d = reinterpret_cast<uint16_t *>(stage + o * L::kPitch) + 2 * w;
+                if (c >= 0 && c < width) d[0] = src[c];
+                if (c + 1 < width) d[1] = src[c + 1];
             }
         }
     }
 }
 
-// Piece i of a lane, from a stage; `odd`: it sits one element further in.
-__device__ __forceinline__ uint4 load_piece(const unsigned char *p, bool odd) {
+// A 16-byte piece that sits one 2-byte element further in.
+__device__ __forceinline__ uint4 load_odd_piece(const unsigned char *p) {
     const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    if (!odd) return a;
     const uint32_t b = *reinterpret_cast<const uint32_t *>(p + 16);
     return make_uint4(__funnelshift_r(a.x, a.y, 16), __funnelshift_r(a.y, a.z, 16),
                       __funnelshift_r(a.z, a.w, 16), __funnelshift_r(a.w, b, 16));
@@ -332,28 +340,50 @@ __device__ __forceinline__ uint4 load_piece(const unsigned char *p, bool odd) {
 struct Shared {
     uint32_t *count;    // [kSliceCols]
     uint32_t *touched;  // [kThreads]: bit c % 32 of word c / 32 for slice column c
-    uint16_t *list;     // [kSliceCols]: each warp's touched columns, ascending
+    uint16_t *list;     // [kWarps][1024]: each warp's touched columns, ascending
     uint16_t *bias;     // [kSliceCols], or null: 1 + the index of the column's bias, 0: none
+    RowInfo *rows;      // [kMaxRun]
+    unsigned char *rings;
 };
+constexpr int kWarpCols = 32 * kLaneCols;
+
+extern __shared__ uint4 rules_smem[];
+
+// Its layout: counts, touched words, rows, lists, bias indices if there are
+// biases, and then the warps' rings.
+__device__ __forceinline__ Shared shared_view(bool has_bias) {
+    Shared sh;
+    sh.count = reinterpret_cast<uint32_t *>(rules_smem);
+    sh.touched = sh.count + kSliceCols;
+    sh.rows = reinterpret_cast<RowInfo *>(sh.touched + kThreads);
+    sh.list = reinterpret_cast<uint16_t *>(sh.rows + kMaxRun);
+    sh.bias = has_bias ? sh.list + kSliceCols : nullptr;
+    sh.rings = reinterpret_cast<unsigned char *>(sh.list + (has_bias ? 2 : 1) * kSliceCols);
+    return sh;
+}
 
 __device__ __forceinline__ void mark(const Shared &sh, int c) {
     atomicOr(&sh.touched[c >> 5], 1u << (c & 31));
 }
 
-// Block-wide: tokens [from, to) of the request into the counts of columns
+// The functions below run seldom: out of line, and with plain arguments, so
+// that the row loop keeps its values in registers.
+
+// Block-wide: tokens [from, to) of a request into the counts of the columns
 // [slice0, slice0 + width).
-__device__ __forceinline__ void count_tokens(const Shared &sh, const Request &q, int32_t from,
-                                             int32_t to, int64_t slice0, int width) {
+__device__ __noinline__ void count_tokens(const int64_t *tokens, int32_t prompt, int32_t from, int32_t to,
+                                          int64_t slice0, int width) {
+    const Shared sh = shared_view(false);
     constexpr int kBatch = 8;  // loads in flight per thread
     for (int32_t i0 = from + (int32_t)threadIdx.x; i0 < to; i0 += kBatch * kThreads) {
         int64_t v[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) v[k] = i0 + k * kThreads < to ? q.tokens[i0 + k * kThreads] : -1;
+        for (int k = 0; k < kBatch; ++k) v[k] = i0 + k * kThreads < to ? tokens[i0 + k * kThreads] : -1;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int64_t c = v[k] - slice0;
             if (v[k] >= 0 && c >= 0 && c < width) {
-                if (i0 + k * kThreads < q.prompt)
+                if (i0 + k * kThreads < prompt)
                     atomicOr(&sh.count[c], kPromptBit);
                 else
                     atomicAdd(&sh.count[c], 1u);
@@ -363,21 +393,22 @@ __device__ __forceinline__ void count_tokens(const Shared &sh, const Request &q,
     }
 }
 
-// Block-wide: the request's first `len` tokens and its biases from scratch.
-// Of biases for one column the last counts: the count words find it first.
-__device__ __forceinline__ void count_request(const Shared &sh, const rk_logits_rules &rules,
-                                              const Request &q, int32_t len, int64_t slice0, int width) {
+// Block-wide: nothing counted, the request's biases (`ids` null: none).  Of
+// biases for one column the last counts: the count words find it.
+__device__ __noinline__ void start_request(bool has_bias, const int64_t *ids, int32_t nbias, int64_t slice0,
+                                           int width) {
+    const Shared sh = shared_view(has_bias);
     __syncthreads();
     for (int k = threadIdx.x; k < kSliceCols / 4; k += kThreads)
         reinterpret_cast<uint4 *>(sh.count)[k] = make_uint4(0, 0, 0, 0);
     sh.touched[threadIdx.x] = 0;
-    if (sh.bias)
+    if (has_bias)
         for (int k = threadIdx.x; k < kSliceCols / 8; k += kThreads)
             reinterpret_cast<uint4 *>(sh.bias)[k] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    if (q.nbias > 0) {
-        for (int k = threadIdx.x; k < q.nbias; k += kThreads) {
-            const int64_t v = rules.bias_ids[q.bias0 + k], c = v - slice0;
+    if (nbias > 0) {
+        for (int k = threadIdx.x; k < nbias; k += kThreads) {
+            const int64_t v = ids[k], c = v - slice0;
             if (v >= 0 && c >= 0 && c < width) {
                 atomicMax(&sh.count[c], (uint32_t)(k + 1));
                 mark(sh, (int)c);
@@ -391,13 +422,11 @@ __device__ __forceinline__ void count_request(const Shared &sh, const rk_logits_
         }
         __syncthreads();
     }
-    count_tokens(sh, q, 0, len, slice0, width);
-    __syncthreads();
 }
 
-// A warp's list of its touched columns (segment columns, ascending) from its
-// lanes' bits; returns their number.
-__device__ __forceinline__ int make_list(uint16_t *list, uint32_t touched, int lane) {
+// A warp's list of its touched columns (of the slice, ascending) from its
+// lanes' bits, `own`: the lane's first column; returns their number.
+__device__ __forceinline__ int make_list(uint16_t *list, uint32_t touched, int own, int lane) {
     const int mine = __popc(touched);
     int incl = mine;
 #pragma unroll
@@ -407,15 +436,15 @@ __device__ __forceinline__ int make_list(uint16_t *list, uint32_t touched, int l
     }
     int at = incl - mine;
     for (uint32_t b = touched; b; b &= b - 1)
-        list[at++] = (uint16_t)(lane * kLaneCols + __ffs(b) - 1);
+        list[at++] = (uint16_t)(own + __ffs(b) - 1);
     return __shfl_sync(0xffffffffu, incl, 31);
 }
 
-// exp(y / temperature - lse), 1 / temperature = itau + i1.  -inf stays out of
-// the product with i1, whose sign it would take.
-__device__ __forceinline__ float prob(float y, float itau, float i1, float lse) {
-    const float v = max_nan(y, -FLT_MAX);
-    return ex2(__fmul_rn(__fmaf_rn(v, i1, __fmaf_rn(v, itau, -lse)), kLog2e));
+// exp(y / temperature - lse), 1 / temperature = id + i1, i1 >= 0 (-inf stays -inf).
+__device__ __forceinline__ float prob(float y, float id, float i1, float lse) {
+    float x = __fmaf_rn(y, id, -lse);
+    if (i1 > 0.f) x = __fmaf_rn(y, i1, x);
+    return ex2(__fmul_rn(x, kLog2e));
 }
 
 // bf16 pieces: where a pair's two bits in `keep` are 0, -inf.  Byte i of `keep`
@@ -435,111 +464,108 @@ __device__ __forceinline__ void keep_columns(uint4 (&w)[4], uint32_t keep) {
     }
 }
 
-__device__ __forceinline__ void unpack(const uint4 &w, uint64_t (&z)[4]) {
+// fp32 pieces: bit 4 i + j of `keep` belongs to column j of piece i.
+__device__ __forceinline__ void keep_columns(uint4 (&w)[8], uint32_t keep) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (!(keep >> (4 * i) & 1u)) w[i].x = 0xff800000u;
+        if (!(keep >> (4 * i + 1) & 1u)) w[i].y = 0xff800000u;
+        if (!(keep >> (4 * i + 2) & 1u)) w[i].z = 0xff800000u;
+        if (!(keep >> (4 * i + 3) & 1u)) w[i].w = 0xff800000u;
+    }
+}
+
+// A piece's columns as pairs of fp32.
+template <typename T>
+__device__ __forceinline__ void pairs_of(const uint4 &w, uint64_t (&z)[4]) {
     const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) z[j] = pair(bf16_lo(q[j]), bf16_hi(q[j]));
+    for (int j = 0; j < 16 / (int)sizeof(T) / 2; ++j)
+        z[j] = sizeof(T) == 2 ? pair(bf16_lo(q[j]), bf16_hi(q[j]))
+                              : pair(__uint_as_float(q[(2 * j) & 3]), __uint_as_float(q[(2 * j + 1) & 3]));
 }
 
 // Shared memory of a block: counts, touched words, rows, lists and bias
-// indices, and a ring of stages per warp.  A stage holds the segment's logits
-// (16 bytes more for rows that start on an odd element: they sit one element
-// further in) and afterwards its results, and the segment's mask words.
-// Blocks of up to 113 KB run two to an SM, which beats a second stage.
+// indices, and a ring of stages per warp.  A stage holds the warp's logits and
+// afterwards its results, and its mask words.  Blocks of up to 113 KB run two
+// to an SM, which beats a second stage.
 template <RulesOp OP, typename TIn, typename TOut>
 struct Config {
-    static constexpr int kElem = OP != kLogp && sizeof(TOut) > sizeof(TIn) ? sizeof(TOut) : sizeof(TIn);
-    static constexpr int kStages = kElem == 2 ? 2 : 1;
-    static constexpr int kMaskAt = kSegCols * kElem + 16;
-    static constexpr int kStageBytes = kMaskAt + kSegCols / 8;
-    // fp32 results of bf16 pieces: neighbouring lanes would write the same bank
-    // group, so odd lanes swap neighbouring pieces
-    static constexpr int kSwap = (sizeof(TIn) == 2 && sizeof(TOut) == 4) ? 1 : 0;
+    static constexpr bool kWider = OP != kLogp && sizeof(TOut) > sizeof(TIn);
+    static constexpr int kStages = sizeof(TIn) == 2 && !kWider ? 2 : 1;
+    static constexpr int kMaskAt = 32 * (kWider ? Lane<TOut>::kPitch : Lane<TIn>::kPitch);
+    static constexpr int kStageBytes = kMaskAt + 32 * 4;
     static size_t smem(bool bias) {
         return (size_t)(kSliceCols + kThreads) * 4 + kMaxRun * sizeof(RowInfo) +
                (size_t)kSliceCols * (bias ? 4 : 2) + (size_t)kWarps * kStages * kStageBytes;
     }
 };
 
-// Writes `cols` results of a segment from the warp's staging area to dst.
-template <int SWAP>
-__device__ __forceinline__ void write_out(const unsigned char *stage, float *dst, int cols, bool vec,
-                                          int lane) {
-    const float4 *s4 = reinterpret_cast<const float4 *>(stage);
-    if (vec && cols == kSegCols) {
+// Writes a warp's results from its stage to the row's slice.
+template <bool VEC, typename T>
+__device__ __forceinline__ void write_out(const unsigned char *stage, T *dst, int width, int warp, int lane) {
+    using L = Lane<T>;
+    if (VEC && width == kSliceCols) {
+        const int o = lane / L::kPieces, part = lane % L::kPieces;
+        const unsigned char *from = stage + o * L::kPitch + 16 * part;
+        T *to = dst + lane_col(warp, o) + part * L::kCols;
 #pragma unroll
-        for (int i = 0; i < kSegCols / 128; ++i) {
-            const int x = lane + 32 * i;
-            reinterpret_cast<float4 *>(dst)[x] = s4[x ^ (SWAP ? (x >> 3) & 1 : 0)];
+        for (int i = 0; i < L::kPieces; ++i)
+            *reinterpret_cast<uint4 *>(to + i * L::kPieceCols) =
+                *reinterpret_cast<const uint4 *>(from + i * L::kPieceRow);
+    } else {
+#pragma unroll 4
+        for (int o = 0; o < 32; ++o) {
+            const int c = lane_col(warp, o) + lane;
+            if (c < width) dst[c] = reinterpret_cast<const T *>(stage + o * L::kPitch)[lane];
         }
-    } else {
-        const float *s = reinterpret_cast<const float *>(stage);
-#pragma unroll 8
-        for (int c = lane; c < cols; c += 32) dst[c] = s[c ^ (SWAP ? ((c >> 5) & 1) << 2 : 0)];
-    }
-}
-template <int SWAP>
-__device__ __forceinline__ void write_out(const unsigned char *stage, uint16_t *dst, int cols,
-                                          bool vec, int lane) {
-    if (vec && cols == kSegCols) {
-#pragma unroll
-        for (int i = 0; i < kSegCols / 256; ++i)
-            reinterpret_cast<uint4 *>(dst)[lane + 32 * i] =
-                reinterpret_cast<const uint4 *>(stage)[lane + 32 * i];
-    } else {
-        const uint16_t *s = reinterpret_cast<const uint16_t *>(stage);
-#pragma unroll 8
-        for (int c = lane; c < cols; c += 32) dst[c] = s[c];
     }
 }
 
-template <RulesOp OP, typename TIn, typename TOut>
-__global__ void __launch_bounds__(kThreads)
+// VEC: every row of the logits, and of what is written, starts on a 16-byte
+// boundary.
+template <RulesOp OP, typename TIn, typename TOut, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2)
     rules_kernel(const __grid_constant__ RulesIo io, const __grid_constant__ rk_logits_rules rules) {
     using C = Config<OP, TIn, TOut>;
     using L = Lane<TIn>;
-    extern __shared__ uint4 smem[];
-    Shared sh;
-    sh.count = reinterpret_cast<uint32_t *>(smem);
-    sh.touched = sh.count + kSliceCols;
-    RowInfo *rows = reinterpret_cast<RowInfo *>(sh.touched + kThreads);
-    sh.list = reinterpret_cast<uint16_t *>(rows + kMaxRun);
-    sh.bias = rules.bias_ids ? sh.list + kSliceCols : nullptr;
-    unsigned char *p = reinterpret_cast<unsigned char *>(sh.list + (rules.bias_ids ? 2 : 1) * kSliceCols);
+    const Shared sh = shared_view(rules.bias_ids != nullptr);
+    RowInfo *rows = sh.rows;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned char *ring = p + warp * C::kStages * C::kStageBytes;
+    unsigned char *ring = sh.rings + warp * C::kStages * C::kStageBytes;
     // Launched with programmatic stream serialisation: wait until the previous
     // kernel of the stream has completed before reading or writing anything.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const int64_t slices = (io.V + kSliceCols - 1) / kSliceCols;
-    const int64_t slice0 = (int64_t)(blockIdx.x % slices) * kSliceCols;
+    const int64_t slices = (io.V + kSliceCols - 1) / kSliceCols, slice = blockIdx.x % slices;
+    const int64_t slice0 = slice * kSliceCols;
     const int width = (int)min((int64_t)kSliceCols, io.V - slice0);
     const int64_t t0 = (int64_t)(blockIdx.x / slices) * io.run;
     const int n = (int)min((int64_t)io.run, io.T - t0);
-    const int64_t seg0 = slice0 + (int64_t)warp * kSegCols;
-    const int cols = (int)max((int64_t)0, min((int64_t)kSegCols, io.V - seg0));  // of this warp
-    const int64_t nseg = (io.V + kSegCols - 1) / kSegCols;
     const int64_t words = (io.V + 31) / 32;
-    const int own = lane * kLaneCols;  // the lane's first column in the segment
+    const int own = lane_col(warp, lane);  // the lane's first column
     const uint32_t inside =
-        cols >= own + 32 ? 0xffffffffu : cols > own ? (1u << (cols - own)) - 1u : 0u;
-    uint32_t *count = sh.count + warp * kSegCols;  // of the segment
-    const uint16_t *bias = sh.bias ? sh.bias + warp * kSegCols : nullptr;
-    uint16_t *list = sh.list + warp * kSegCols;
+        width >= own + 32 ? 0xffffffffu : width > own ? (1u << (width - own)) - 1u : 0u;
+    uint32_t *my_word = sh.touched + (own >> 5);
+    uint16_t *list = sh.list + warp * kWarpCols;
 
     for (int k = threadIdx.x; k < n; k += kThreads) rows[k] = row_info<OP>(io, rules, t0 + k);
     __syncthreads();
 
-    const TIn *zseg = reinterpret_cast<const TIn *>(io.logits) + t0 * io.ld + seg0;
+    const TIn *zslice = reinterpret_cast<const TIn *>(io.logits) + t0 * io.ld + slice0;
+    TOut *oslice = OP == kLogp ? nullptr : reinterpret_cast<TOut *>(io.out) + t0 * io.ld_out + slice0;
+    float2 *parts = OP == kLogp ? io.part + (t0 * slices + slice) * kWarps + warp : nullptr;
     auto prefetch = [&](int k) {
-        if (k < n && rows[k].tgt >= 0) {
-            unsigned char *stage = ring + (k % C::kStages) * C::kStageBytes;
-            start_copy(stage, zseg + k * io.ld, cols, io.vec_in, lane);
-            if (rows[k].mrow >= 0 && inside)
-                cp_async4(smem_u32(stage + C::kMaskAt) + 4 * lane,
-                          rules.mask + (int64_t)rows[k].mrow * words + (seg0 >> 5) + lane);
+        if (k < n) {
+            const int2 r = *reinterpret_cast<const int2 *>(&rows[k]);  // tgt, mrow
+            if (r.x >= 0) {
+                unsigned char *stage = ring + (C::kStages == 1 ? 0 : (k % C::kStages) * C::kStageBytes);
+                start_copy<VEC>(stage, zslice + k * io.ld, width, warp, lane);
+                if (r.y >= 0 && inside)
+                    cp_async4(smem_u32(stage + C::kMaskAt) + 4 * lane,
+                              rules.mask + (int64_t)r.y * words + ((slice0 + own) >> 5));
+            }
         }
         cp_commit();
     };
@@ -551,253 +577,308 @@ __global__ void __launch_bounds__(kThreads)
     uint32_t touched = 0;
     int listed = 0;  // touched columns of the warp
     Request q{};
-    for (int k = 0; k < n; ++k) {
-        const RowInfo row = rows[k];
-        const int64_t t = t0 + k;
-        bool ok = row.tgt >= 0;
-        if (ok && (row.req != cur || (q.ok && row.step == kAnew))) {
-            const bool other = row.req != cur;
+    for (int k = 0; k < n;) {
+        // The whole block: a request, or a step of more than one token.
+        if (rows[k].tgt >= 0 && (rows[k].req != cur || rows[k].step == kAnew)) {
+            const bool other = rows[k].req != cur;
             if (other) {
-                q = load_request(rules, row.req);
-                cur = row.req;
+                cur = rows[k].req;
+                q = load_request(rules, cur);
             }
             if (q.ok) {
-                const int32_t len = min(row.len, q.ntok);
-                if (other || len < counted) {
-                    count_request(sh, rules, q, len, slice0, width);
+                const int32_t len = min(rows[k].len, q.ntok);
+                const bool anew = other || len < counted;
+                if (anew) {
+                    start_request(sh.bias != nullptr, rules.bias_ids + q.bias0, q.nbias, slice0, width);
                 } else {
                     __syncthreads();
-                    sh.touched[threadIdx.x] = touched;
-                    __syncthreads();
-                    count_tokens(sh, q, counted, len, slice0, width);
+                    *my_word = touched;
                     __syncthreads();
                 }
+                count_tokens(q.tokens, q.prompt, anew ? 0 : counted, len, slice0, width);
+                __syncthreads();
                 counted = len;
-                touched = sh.touched[threadIdx.x];
-                listed = make_list(list, touched, lane);
-            }
-        } else if (ok && q.ok) {
-            counted = min(row.len, q.ntok);
-            const int64_t c = row.step - seg0;  // negative where there is no token
-            if (row.step >= 0 && c >= 0 && c < cols) {
-                const uint32_t bit = (c >> 5) == lane ? 1u << (c & 31) : 0u;
-                if (bit) count[c] = row.step_prompt ? (count[c] | kPromptBit) : count[c] + 1u;
-                const bool fresh = (bit & ~touched) != 0;
-                touched |= bit;
-                if (__any_sync(0xffffffffu, fresh)) listed = make_list(list, touched, lane);
+                touched = *my_word;
+                listed = make_list(list, touched, own, lane);
             }
         }
-        ok = ok && q.ok;
-        cp_wait<C::kStages - 1>();  // all copies but those of later rows
-        __syncwarp();
-        TOut *orow = reinterpret_cast<TOut *>(io.out) + t * io.ld_out + seg0;
-        if (!ok) {
-            const float fill = row.tgt == kInactive ? 0.f : __int_as_float(0x7fc00000);
-            if (row.tgt != kInactive) {
-                if (slice0 == 0 && threadIdx.x == 0)
-                    atomicOr(io.err, row.tgt == kBadTarget ? kErrTargetRange : kErrRules);
-                if (OP == kLogp && lane == 0 && cols > 0) {
-                    io.part[t * nseg + seg0 / kSegCols] = make_float2(0.f, fill);
-                    if (seg0 == 0) io.ytgt[t] = fill;
+        // A row without a result, or without usable rules.
+        if (rows[k].tgt < 0 || !q.ok) {
+            const int32_t tgt = rows[k].tgt;
+            const float fill = tgt == kInactive ? 0.f : __int_as_float(0x7fc00000);
+            if (tgt != kInactive) {
+                if (slice == 0 && threadIdx.x == 0) {
+                    atomicOr(io.err, tgt == kBadTarget ? kErrTargetRange : kErrRules);
+                    if (OP == kLogp) io.ytgt[t0 + k] = fill;
                 }
+                if (OP == kLogp && lane == 0) parts[k * slices * kWarps] = make_float2(0.f, fill);
             }
-            if (OP == kBwd || (OP == kApply && row.tgt != kInactive))
-                for (int c = lane; c < cols; c += 32) put(orow + c, fill);
+            if (OP == kBwd || (OP == kApply && tgt != kInactive))
+#pragma unroll 1
+                for (int o = 0; o < 32; ++o) {
+                    const int c = lane_col(warp, o) + lane;
+                    if (c < width) put(oslice + k * io.ld_out + c, fill);
+                }
+            cp_wait<0>();
             prefetch(k + C::kStages);
+            ++k;
             continue;
         }
-        unsigned char *stage = ring + (k % C::kStages) * C::kStageBytes;
-        const bool odd = !io.vec_in && odd_start(zseg + k * io.ld);
-        // single logits: from the stage, or, where results replace it, from the row
-        const TIn *zs = OP == kLogp ? reinterpret_cast<const TIn *>(stage) + (odd ? 1 : 0) : zseg + k * io.ld;
-        const uint32_t *masks = reinterpret_cast<const uint32_t *>(stage + C::kMaskAt);
-        const bool masked = row.mrow >= 0;
-        const uint32_t live = masked ? inside & masks[lane] : inside;  // columns the mask allows
-        // a listed column's y from its logit z (false: masked)
-        auto listed_y = [&](int j, float &z, uint32_t &cw, float &y) {
-            if (masked && !(masks[j >> 5] >> (j & 31) & 1u)) return false;
-            z = elem(zs + j);
-            cw = count[j];
-            const int bi = bias ? bias[j] : 0;
-            y = rule_y(z, cw, bi ? rules.bias_values[q.bias0 + bi - 1] : 0.f, q);
-            return true;
-        };
-        const int rot = L::bits(lane);
-        uint4 w[L::kPieces];
-#pragma unroll
-        for (int i = 0; i < L::kPieces; ++i)
-            w[i] = load_piece(stage + 16 * (lane * L::kPieces + L::order(lane, i)), odd);
-        if (OP != kLogp) __syncwarp();  // the stage is read
-
-        if (OP == kLogp) {
-            const float c = __fmul_rn(kLog2e, q.itau);
-            const int tcol = row.tgt >= seg0 && row.tgt < seg0 + cols ? row.tgt - (int)seg0 : -1;
-            // touched columns: running maximum and sum, each lane its share of the list
-            float mt = -INFINITY, st = 0.f;
-            for (int e = lane; e < listed; e += 32) {
-                const int j = list[e];
-                float z, y = -INFINITY;
-                uint32_t cw;
-                const bool allowed = listed_y(j, z, cw, y);
-                if (j == tcol) io.ytgt[t] = y;
-                if (!allowed || y == -INFINITY) continue;  // masked, or banned by its bias
-                const float mn = fmaxf(mt, y);
-                st = __fmaf_rn(st, ex2(__fmul_rn(__fsub_rn(mt, mn), c)),
-                               ex2(__fmul_rn(__fsub_rn(y, mn), c)));
-                mt = mn;
-            }
-            // untouched columns: one maximum, then the terms relative to it
-            const uint32_t plain = live & ~touched;
-            if (tcol >= 0 && (tcol >> 5) == lane && !(touched >> (tcol & 31) & 1u))
-                io.ytgt[t] = plain >> (tcol & 31) & 1u ? elem(zs + tcol) : -INFINITY;
-            const uint32_t keep = __funnelshift_r(plain, plain, rot);
-            float m;
-            if constexpr (sizeof(TIn) == 2) {
-                if (!__all_sync(0xffffffffu, plain == 0xffffffffu)) keep_columns(w, keep);
-                uint32_t x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = max_bf16x2(max_bf16x2(w[i].x, w[i].y), max_bf16x2(w[i].z, w[i].w));
-                x[0] = max_bf16x2(max_bf16x2(x[0], x[1]), max_bf16x2(x[2], x[3]));
-                m = fmaxf(bf16_lo(x[0]), bf16_hi(x[0]));
-            } else {
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t *f = &w[i].x;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if ((int32_t)(keep << (31 - 4 * i - j)) >= 0) f[j] = 0xff800000u;
-                    x[i] = fmaxf(fmaxf(__uint_as_float(w[i].x), __uint_as_float(w[i].y)),
-                                 fmaxf(__uint_as_float(w[i].z), __uint_as_float(w[i].w)));
-                }
-                m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                          fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-            }
-            // terms relative to the segment's maximum: (z - m) c rather than one
-            // fused z c - m c, whose product overflows next to the type's lowest
-            // value, and with the maximum's own term exactly 1
-            m = warp_max(fmaxf(m, mt));
-            const float ref = m == -INFINITY ? 0.f : m;
-            const uint64_t nref = pair(-ref, -ref), cc = pair(c, c);
-            uint64_t acc[2] = {0, 0};  // pairs of +0
-#pragma unroll
-            for (int i = 0; i < L::kPieces; ++i) {
-                uint64_t z[4];
-                if constexpr (sizeof(TIn) == 2) {
-                    unpack(w[i], z);
-                } else {
-                    z[0] = pair(__uint_as_float(w[i].x), __uint_as_float(w[i].y));
-                    z[1] = pair(__uint_as_float(w[i].z), __uint_as_float(w[i].w));
-                }
-#pragma unroll
-                for (int j = 0; j < L::kCols / 2; ++j) {
-                    float a, b;
-                    unpair(mul2(add2(z[j], nref), cc), a, b);
-                    acc[j & 1] = add2(acc[j & 1], pair(ex2(a), ex2(b)));
-                }
-            }
-            float s0, s1;
-            unpair(add2(acc[0], acc[1]), s0, s1);
-            float s = __fadd_rn(s0, s1);
-            s = __fadd_rn(s, mt == -INFINITY ? st : __fmul_rn(st, ex2(__fmul_rn(__fsub_rn(mt, ref), c))));
-            s = warp_sum(s);
-            if (lane == 0 && cols > 0) io.part[t * nseg + seg0 / kSegCols] = make_float2(m, s);
-        } else {
-            const float l = row.lse;
-            const bool none = OP == kBwd && l == -INFINITY;  // the rules leave nothing
-            const float g = OP == kBwd && !none ? __fmul_rn(row.g, q.itau) : 0.f;
-            // x - lse with 1 / temperature to 48 bits (itau + i1): the rounding of
-            // 1 / temperature alone would weigh |x| times half a step
-            const float i1 = __fmul_rn(__fmaf_rn(-q.tau, q.itau, 1.f), q.itau);
-            const uint32_t shown = none ? 0u : live;
-            const uint32_t keep = __funnelshift_r(shown, shown, rot);
-            const uint64_t it2 = pair(q.itau, q.itau);
-#pragma unroll
-            for (int i = 0; i < L::kPieces; ++i) {
-                constexpr int N = L::kCols;
-                uint64_t z[4];
-                float x[8];
-                if constexpr (sizeof(TIn) == 2) {
-                    if (OP == kBwd) {  // -inf out of the products (see prob)
-                        w[i].x = max_nan_bf16x2(w[i].x, kLowest2);
-                        w[i].y = max_nan_bf16x2(w[i].y, kLowest2);
-                        w[i].z = max_nan_bf16x2(w[i].z, kLowest2);
-                        w[i].w = max_nan_bf16x2(w[i].w, kLowest2);
-                    }
-                    unpack(w[i], z);
-                } else {
-                    float f[4] = {__uint_as_float(w[i].x), __uint_as_float(w[i].y),
-                                  __uint_as_float(w[i].z), __uint_as_float(w[i].w)};
-                    if (OP == kBwd)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) f[j] = max_nan(f[j], -FLT_MAX);
-                    z[0] = pair(f[0], f[1]);
-                    z[1] = pair(f[2], f[3]);
-                }
-#pragma unroll
-                for (int j = 0; j < N / 2; ++j) {
-                    uint64_t v;
-                    if (OP == kApply) {
-                        v = mul2(z[j], it2);
-                    } else {
-                        v = fma2(z[j], pair(i1, i1), fma2(z[j], it2, pair(-l, -l)));
-                        v = mul2(v, pair(kLog2e, kLog2e));
-                        float a, b;
-                        unpair(v, a, b);
-                        v = mul2(pair(ex2(a), ex2(b)), pair(-g, -g));
-                    }
-                    unpair(v, x[2 * j], x[2 * j + 1]);
-                }
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if ((int32_t)(keep << (31 - N * i - j)) >= 0) x[j] = OP == kApply ? -INFINITY : 0.f;
-                const int piece = lane * L::kPieces + L::order(lane, i);  // of the segment
-                if constexpr (sizeof(TOut) == 4) {
-                    float4 *o = reinterpret_cast<float4 *>(stage);
-#pragma unroll
-                    for (int h = 0; h < N / 4; ++h)
-                        o[(piece * (N / 4) + h) ^ (C::kSwap ? lane & 1 : 0)] =
-                            make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
-                } else {
-                    uint32_t *o = reinterpret_cast<uint32_t *>(stage) + piece * (N / 2);
-                    if constexpr (N == 8)
-                        *reinterpret_cast<uint4 *>(o) =
-                            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                       pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-                    else
-                        *reinterpret_cast<uint2 *>(o) =
-                            make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-                }
-            }
-            // the touched columns, and the target's, over what stands there
+        // Rows of the request, each warp for itself.
+        const float c = __fmul_rn(kLog2e, q.itau);
+        int32_t tgt = rows[k].tgt, mrow = rows[k].mrow;
+        do {
+            cp_wait<C::kStages - 1>();  // all copies but those of later rows
             __syncwarp();
-            auto put_column = [&](int j, float v) {
-                put(reinterpret_cast<TOut *>(stage) + (j ^ (C::kSwap ? (j >> 3) & 4 : 0)), v);
+            unsigned char *stage = ring + (C::kStages == 1 ? 0 : (k % C::kStages) * C::kStageBytes);
+            const TIn *zrow = zslice + k * io.ld;
+            const int odd = VEC ? 0 : odd_start(zrow);
+            const uint32_t *masks = reinterpret_cast<const uint32_t *>(stage + C::kMaskAt);
+            const bool masked = mrow >= 0;
+            const uint32_t live = masked ? inside & masks[lane] : inside;  // columns the mask allows
+            uint4 w[L::kPieces];
+#pragma unroll
+            for (int i = 0; i < L::kPieces; ++i)
+                w[i] = VEC || !odd ? *reinterpret_cast<const uint4 *>(stage + lane * L::kPitch + 16 * i)
+                                   : load_odd_piece(stage + lane * L::kPitch + 16 * i);
+            // a column's logit in the stage; a touched one's y from its logit
+            auto staged = [&](int j) {
+                return elem(reinterpret_cast<const TIn *>(stage + owner_lane(j) * L::kPitch) + (j & 31) + odd);
             };
-            if (OP == kBwd && row.tgt >= seg0 && row.tgt < seg0 + cols) {
-                const int j = row.tgt - (int)seg0;
-                if ((j >> 5) == lane && ((shown & ~touched) >> (j & 31) & 1u))
-                    put_column(j, __fmul_rn(g, __fsub_rn(1.f, prob(elem(zs + j), q.itau, i1, l))));
-            }
-            for (int e = lane; e < (none ? 0 : listed); e += 32) {
-                const int j = list[e];
-                float z, y;
-                uint32_t cw;
-                if (!listed_y(j, z, cw, y)) continue;
-                if (OP == kApply) {
-                    put_column(j, __fmul_rn(y, q.itau));
+            auto touched_y = [&](int j, float z, uint32_t cw) {
+                const int bi = sh.bias ? sh.bias[j] : 0;
+                return rule_y(z, cw, bi ? rules.bias_values[q.bias0 + bi - 1] : 0.f, q);
+            };
+            auto allowed = [&](int j) { return !masked || (masks[owner_lane(j)] >> (j & 31) & 1u); };
+            // the target, if it is one of this warp's columns
+            const uint32_t tc = (uint32_t)tgt - (uint32_t)slice0;
+            const bool has_target = OP != kApply && tc < (uint32_t)width && owner_warp(tc) == warp;
+            // the list's first 32 columns, one to a lane
+            int c0 = -1;
+            float z0 = 0.f, y0 = -INFINITY;
+            uint32_t cw0 = 0;
+            if (listed > 0 && lane < listed) {
+                c0 = list[lane];
+                if (allowed(c0)) {
+                    z0 = staged(c0);
+                    cw0 = sh.count[c0];
+                    y0 = touched_y(c0, z0, cw0);
                 } else {
-                    const float slope = cw ? (z > 0.f ? q.irep : q.rep) : 1.f;
-                    const float hot = j == row.tgt - seg0 ? 1.f : 0.f;
-                    put_column(j, __fmul_rn(__fmul_rn(g, __fsub_rn(hot, prob(y, q.itau, i1, l))), slope));
+                    c0 = -1;
                 }
             }
-            __syncwarp();
-            write_out<C::kSwap>(stage, orow, cols, io.vec_out, lane);
-        }
-        __syncwarp();  // the stage is free again
-        prefetch(k + C::kStages);
+
+            if constexpr (OP == kLogp) {
+                // the rest of the list: running maximum and sum, four columns at a time
+                float mt = -INFINITY, st = 0.f;
+                for (int e0 = 32 + lane; e0 - lane < listed; e0 += 128) {
+                    float y[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int cu = e0 + 32 * u < listed ? list[e0 + 32 * u] : -1;
+                        y[u] = -INFINITY;
+                        if (cu >= 0 && allowed(cu)) y[u] = touched_y(cu, staged(cu), sh.count[cu]);
+                    }
+                    const float mn = fmaxf(fmaxf(mt, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
+                    const float r = mn == -INFINITY ? 0.f : mn;
+                    if (mt != -INFINITY) st = __fmul_rn(st, ex2(__fmul_rn(__fsub_rn(mt, r), c)));
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) st = __fadd_rn(st, ex2(__fmul_rn(__fsub_rn(y[u], r), c)));
+                    mt = mn;
+                }
+                if (has_target && owner_lane(tc) == lane) {
+                    float y = -INFINITY;
+                    if (live >> (tc & 31) & 1u) {
+                        y = staged(tc);
+                        if (touched >> (tc & 31) & 1u) y = touched_y(tc, y, sh.count[tc]);
+                    }
+                    io.ytgt[t0 + k] = y;
+                }
+                // untouched columns: one maximum, then the terms relative to it
+                const uint32_t plain = live & ~touched;
+                float m;
+                if constexpr (sizeof(TIn) == 2) {
+                    if (!__all_sync(0xffffffffu, plain == 0xffffffffu)) keep_columns(w, plain);
+                    uint32_t x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[i] = max_bf16x2(max_bf16x2(w[i].x, w[i].y), max_bf16x2(w[i].z, w[i].w));
+                    x[0] = max_bf16x2(max_bf16x2(x[0], x[1]), max_bf16x2(x[2], x[3]));
+                    m = fmaxf(bf16_lo(x[0]), bf16_hi(x[0]));
+                } else {
+                    if (!__all_sync(0xffffffffu, plain == 0xffffffffu)) keep_columns(w, plain);
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = fmaxf(fmaxf(__uint_as_float(w[i].x), __uint_as_float(w[i].y)),
+                                     fmaxf(__uint_as_float(w[i].z), __uint_as_float(w[i].w)));
+                    m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                              fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+                }
+                // Terms 2^(z c - r), r = the warp's maximum m times c, rounded: one
+                // rounding of the small difference each.  Where m c might leave the
+                // type's range (logits next to its lowest value), 2^((z - m) c).
+                m = warp_max(fmaxf(m, fmaxf(mt, y0)));
+                const float ref = m == -INFINITY ? 0.f : m;
+                const bool far = !(fabsf(ref) < 1e32f);  // c < 1.5e6
+                float r = __fmul_rn(ref, c);
+                uint64_t acc[4] = {0, 0, 0, 0};  // pairs of +0
+                auto sum_terms = [&](auto is_far) {
+                    const uint64_t nr = pair(-r, -r), cc = pair(c, c), nf = pair(-ref, -ref);
+#pragma unroll
+                    for (int i = 0; i < L::kPieces; ++i) {
+                        uint64_t z[4];
+                        pairs_of<TIn>(w[i], z);
+#pragma unroll
+                        for (int j = 0; j < L::kCols / 2; ++j) {
+                            float a, b;
+                            if constexpr (decltype(is_far)::value)
+                                unpair(mul2(add2(z[j], nf), cc), a, b);
+                            else
+                                unpair(fma2(z[j], cc, nr), a, b);
+                            const int to = (i * (L::kCols / 2) + j) & 3;
+                            acc[to] = add2(acc[to], pair(ex2(a), ex2(b)));
+                        }
+                    }
+                };
+                if (__builtin_expect(far, 0)) {
+                    sum_terms(std::true_type{});
+                    r = 0.f;
+                } else {
+                    sum_terms(std::false_type{});
+                }
+                float s0, s1;
+                unpair(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), s0, s1);
+                float s = __fadd_rn(s0, s1);
+                // relative to m c itself rather than to its rounding
+                if (!far) s = __fmaf_rn(s, __fmul_rn(-kLn2, __fmaf_rn(ref, c, -r)), s);
+                if (listed > 0) {
+                    s = __fadd_rn(s, ex2(__fmul_rn(__fsub_rn(y0, ref), c)));
+                    if (listed > 32)
+                        s = __fadd_rn(s, mt == -INFINITY ? st
+                                                         : __fmul_rn(st, ex2(__fmul_rn(__fsub_rn(mt, ref), c))));
+                }
+                s = warp_sum(s);
+                if (lane == 0) parts[k * slices * kWarps] = make_float2(m, s);
+            } else {
+                const float zt = has_target && owner_lane(tc) == lane ? staged(tc) : 0.f;
+                __syncwarp();  // the stage is read
+                const bool none = OP == kBwd && rows[k].lse == -INFINITY;  // the rules leave nothing
+                const float l = none ? 0.f : rows[k].lse;
+                const float g = OP == kBwd && !none ? __fmul_rn(rows[k].g, q.itau) : 0.f;
+                // x - lse with 1 / temperature to 48 bits (id + i1): the rounding of
+                // 1 / temperature alone would weigh |x| times half a step.  Rounded
+                // down: i1 >= 0, so that -inf times i1 > 0 stays -inf, and i1 = 0 is left
+                // out.
+                const float id = __frcp_rd(q.tau);
+                const float i1 = __fmul_rn(__fmaf_rn(-q.tau, id, 1.f), id);
+                const uint32_t shown = none ? 0u : live;
+                // other columns become -inf, whose result is -inf, or 0
+                if (!__all_sync(0xffffffffu, shown == 0xffffffffu)) keep_columns(w, shown);
+                // a touched column's result
+                auto result = [&](float hot, float z, uint32_t cw, float y) {
+                    if (OP == kApply) return __fmul_rn(y, q.itau);
+                    const float slope = cw ? (z > 0.f ? q.irep : q.rep) : 1.f;
+                    return __fmul_rn(__fmul_rn(g, __fsub_rn(hot, prob(y, id, i1, l))), slope);
+                };
+                auto transform = [&](auto is_split) {
+                    const float f = OP == kApply ? q.itau : id;
+                    const uint64_t f2 = pair(f, f), i2 = pair(i1, i1), nl = pair(-l, -l), ng = pair(-g, -g);
+#pragma unroll
+                    for (int i = 0; i < L::kPieces; ++i) {
+                        constexpr int N = L::kCols;
+                        uint64_t z[4];
+                        float x[8];
+                        pairs_of<TIn>(w[i], z);
+#pragma unroll
+                        for (int j = 0; j < N / 2; ++j) {
+                            uint64_t v;
+                            if constexpr (OP == kApply) {
+                                v = mul2(z[j], f2);
+                            } else {
+                                float a, b;
+                                v = fma2(z[j], f2, nl);
+                                if constexpr (decltype(is_split)::value) v = fma2(z[j], i2, v);
+                                unpair(mul2(v, pair(kLog2e, kLog2e)), a, b);
+                                v = mul2(pair(ex2(a), ex2(b)), ng);
+                            }
+                            unpair(v, x[2 * j], x[2 * j + 1]);
+                        }
+                        unsigned char *o = stage + lane * Lane<TOut>::kPitch + N * i * (int)sizeof(TOut);
+                        if constexpr (sizeof(TOut) == 4) {
+#pragma unroll
+                            for (int h = 0; h < N / 4; ++h)
+                                reinterpret_cast<float4 *>(o)[h] =
+                                    make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
+                        } else if constexpr (N == 8) {
+                            *reinterpret_cast<uint4 *>(o) =
+                                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                           pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+                        } else {
+                            *reinterpret_cast<uint2 *>(o) =
+                                make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+                        }
+                    }
+                };
+                if (OP == kBwd && i1 > 0.f)
+                    transform(std::true_type{});
+                else
+                    transform(std::false_type{});
+                __syncwarp();
+                auto put_column = [&](int j, float v) {
+                    put(reinterpret_cast<TOut *>(stage + owner_lane(j) * Lane<TOut>::kPitch) + (j & 31), v);
+                };
+                if (listed > 0 && !none) {
+                    // the touched columns over what stands there; the stage no longer
+                    // has their logits, so past the list's first 32 they come from the row
+                    if (c0 >= 0) put_column(c0, result(0.f, z0, cw0, y0));
+                    for (int e0 = 32 + lane; e0 - lane < listed; e0 += 128) {
+                        float z[4];
+                        int cu[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            cu[u] = e0 + 32 * u < listed ? list[e0 + 32 * u] : -1;
+                            if (cu[u] >= 0 && !allowed(cu[u])) cu[u] = -1;
+                            z[u] = cu[u] >= 0 ? elem(zrow + cu[u]) : 0.f;
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (cu[u] >= 0) {
+                                const uint32_t cw = sh.count[cu[u]];
+                                put_column(cu[u], result(0.f, z[u], cw, touched_y(cu[u], z[u], cw)));
+                            }
+                    }
+                    __syncwarp();
+                }
+                if (has_target) {
+                    if (owner_lane(tc) == lane && (shown >> (tc & 31) & 1u)) {
+                        const bool t = touched >> (tc & 31) & 1u;
+                        const uint32_t cw = t ? sh.count[tc] : 0u;
+                        put_column(tc, result(1.f, zt, cw, t ? touched_y(tc, zt, cw) : zt));
+                    }
+                    __syncwarp();
+                }
+                write_out<VEC>(stage, oslice + k * io.ld_out, width, warp, lane);
+            }
+            __syncwarp();  // the stage is free again
+            prefetch(k + C::kStages);
+            if (++k >= n) break;
+            const int4 next = *reinterpret_cast<const int4 *>(&rows[k]);  // tgt, mrow, step, step_prompt
+            if (next.x < 0 || next.z == kAnew) break;
+            tgt = next.x;
+            mrow = next.y;
+            if (next.z != kNoToken) {  // one token more
+                ++counted;
+                const uint32_t j = (uint32_t)next.z - (uint32_t)slice0;
+                if (next.z >= 0 && j < (uint32_t)width && owner_warp(j) == warp) {
+                    const uint32_t bit = owner_lane(j) == lane ? 1u << (j & 31) : 0u;
+                    if (bit) sh.count[j] = next.w ? (sh.count[j] | kPromptBit) : sh.count[j] + 1u;
+                    const bool fresh = (bit & ~touched) != 0;
+                    touched |= bit;
+                    if (__any_sync(0xffffffffu, fresh)) listed = make_list(list, touched, own, lane);
+                }
+            }
+        } while (true);
     }
 }
 
@@ -815,7 +896,7 @@ __device__ __forceinline__ void merge_y(float &m, float &s, float mo, float so, 
     m = mn;
 }
 
-// One warp per row: lane l folds segments l, l + 32, ... in order, then a
+// One warp per row: lane l folds partials l, l + 32, ... in order, then a
 // fixed xor tree.
 constexpr int kMergeRows = 8;
 __global__ void __launch_bounds__(32 * kMergeRows)
@@ -837,10 +918,10 @@ __global__ void __launch_bounds__(32 * kMergeRows)
     const bool has_tau = row.tgt >= 0 && rules.num_requests > 0 && rules.temperature;
     const float tau = has_tau ? rules.temperature[row.req] : 1.f;
     const float c = __fmul_rn(kLog2e, __frcp_rn(tau));
-    const int64_t nseg = (io.V + kSegCols - 1) / kSegCols;
+    const int64_t parts = (io.V + kSliceCols - 1) / kSliceCols * kWarps;
     float m = -INFINITY, s = 0.f;
-    for (int64_t k = lane; k < nseg; k += 32) {
-        const float2 p = io.part[t * nseg + k];
+    for (int64_t k = lane; k < parts; k += 32) {
+        const float2 p = io.part[t * parts + k];
         merge_y(m, s, p.x, p.y, c);
     }
 #pragma unroll
@@ -891,7 +972,12 @@ int rows_per_block(int64_t T, int64_t V, const DeviceInfo &di) {
 
 template <RulesOp OP, typename TIn, typename TOut>
 cudaError_t launch(RulesIo io, const rk_logits_rules &r, const DeviceInfo &di, cudaStream_t st) {
-    auto *kernel = rules_kernel<OP, TIn, TOut>;
+    const auto rows_aligned = [](const void *p, int64_t ld, size_t size) {
+        return aligned(p, 16) && ld * (int64_t)size % 16 == 0;
+    };
+    const bool vec = rows_aligned(io.logits, io.ld, sizeof(TIn)) &&
+                     (OP == kLogp || rows_aligned(io.out, io.ld_out, sizeof(TOut)));
+    auto *kernel = vec ? rules_kernel<OP, TIn, TOut, true> : rules_kernel<OP, TIn, TOut, false>;
     const size_t smem = Config<OP, TIn, TOut>::smem(r.bias_ids != nullptr);
     if (smem > 48 * 1024) {
         const cudaError_t e =
@@ -918,15 +1004,11 @@ cudaError_t launch_types(const RulesIo &io, const rk_logits_rules &r, int in, in
                           : launch<OP, float, float>(io, r, di, st);
 }
 
-bool vec16(const void *p, int64_t ld, rk_dtype type) {
-    return aligned(p, 16) && (ld * (type == RK_BF16 ? 2 : 4)) % 16 == 0;
-}
-
 }  // namespace
 
 size_t logp_rules_workspace_bytes(int64_t T, int64_t V) {
-    const size_t nseg = (size_t)((V + kSegCols - 1) / kSegCols);
-    return ((size_t)T * nseg * sizeof(float2) + (size_t)T * sizeof(float) + 255) / 256 * 256;
+    const size_t parts = (size_t)((V + kSliceCols - 1) / kSliceCols * kWarps);
+    return ((size_t)T * parts * sizeof(float2) + (size_t)T * sizeof(float) + 255) / 256 * 256;
 }
 
 cudaError_t launch_rules_apply(const RulesMatrix &logits, const rk_logits_rules &rules, int64_t T,
@@ -935,12 +1017,10 @@ cudaError_t launch_rules_apply(const RulesMatrix &logits, const rk_logits_rules 
     RulesIo io{};
     io.logits = logits.p;
     io.ld = logits.ld;
-    io.vec_in = vec16(logits.p, logits.ld, logits.type);
     io.T = T;
     io.V = V;
     io.out = const_cast<void *>(out.p);
     io.ld_out = out.ld;
-    io.vec_out = vec16(out.p, out.ld, out.type);
     io.err = di.err;
     return launch_types<kApply>(io, rules, logits.type, out.type, di, st);
 }
@@ -952,14 +1032,13 @@ cudaError_t launch_rules_logp(const RulesMatrix &logits, const int64_t *targets,
     RulesIo io{};
     io.logits = logits.p;
     io.ld = logits.ld;
-    io.vec_in = vec16(logits.p, logits.ld, logits.type);
     io.targets = targets;
     io.cu = cu;
     io.num_seqs = num_seqs;
     io.T = T;
     io.V = V;
     io.part = static_cast<float2 *>(workspace);
-    io.ytgt = reinterpret_cast<float *>(io.part + T * ((V + kSegCols - 1) / kSegCols));
+    io.ytgt = reinterpret_cast<float *>(io.part + T * ((V + kSliceCols - 1) / kSliceCols * kWarps));
     io.err = di.err;
     cudaError_t e = logits.type == RK_BF16 ? launch<kLogp, uint16_t, float>(io, rules, di, st)
                                            : launch<kLogp, float, float>(io, rules, di, st);
@@ -977,7 +1056,6 @@ cudaError_t launch_rules_bwd(const RulesMatrix &logits, const int64_t *targets, 
     RulesIo io{};
     io.logits = logits.p;
     io.ld = logits.ld;
-    io.vec_in = vec16(logits.p, logits.ld, logits.type);
     io.targets = targets;
     io.cu = cu;
     io.num_seqs = num_seqs;
@@ -987,7 +1065,6 @@ cudaError_t launch_rules_bwd(const RulesMatrix &logits, const int64_t *targets, 
     io.grad = grad;
     io.out = const_cast<void *>(dlogits.p);
     io.ld_out = dlogits.ld;
-    io.vec_out = vec16(dlogits.p, dlogits.ld, dlogits.type);
     io.err = di.err;
     return launch_types<kBwd>(io, rules, logits.type, dlogits.type, di, st);
 }

@@ -125,8 +125,8 @@ def test_logp_refusals(rk):
     s = rules_struct(rk)
     size = rk.logp_from_logits_rules_workspace_size
     assert size(0, 100) == 0
-    # a (max, sum) pair per 1024 columns and the target's logit, per row
-    assert size(300, 5000) == (300 * 5 * 8 + 300 * 4 + 255) // 256 * 256
+    # eight (max, sum) pairs per 8192 columns and the target's logit, per row
+    assert size(300, 9000) == (300 * 16 * 8 + 300 * 4 + 255) // 256 * 256
 
     def logp(T=4, V=100, z=FAKE, ty=0, ld=100, tg=FAKE, cu=None, ns=0, rules=ctypes.addressof(s),
              out=FAKE, ws=FAKE, wb=1 << 20):
