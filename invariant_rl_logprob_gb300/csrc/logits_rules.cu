@@ -4,9 +4,11 @@
 // (kLogp: selected logprob and log-sum-exp) and differentiated (kBwd).
 //
 // Decomposition.  A block works on a slice of kSliceCols columns and a run of
-// consecutive rows.  Its warps own the slice's blocks of 64 columns in turn,
-// because text is made of few tokens and those sit at the low ids: so the
-// warps of the first slice share them.  Each lane owns 32 neighbouring
+// consecutive rows.  Its warps own 1024 neighbouring columns each; in the
+// first slice they own blocks of 64 columns in turn instead, because text is
+// made of few tokens and those sit at the low ids, so that its warps share
+// them (everywhere, it made the writes of fp32 results 12% slower: 605 us
+// instead of 540 for 4096 x 128256).  Each lane owns 32 neighbouring
 // columns: one word of a grammar mask, and one word that tells which of them
 // the rules touch (seen before, or biased).  The others need the temperature
 // and the mask only.
@@ -56,13 +58,20 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 enum RulesOp { kApply, kLogp, kBwd };
 
-// The first of a lane's columns in the slice.
-__device__ __forceinline__ int lane_col(int warp, int lane) {
-    return ((lane >> 1) * kWarps + warp) * 64 + (lane & 1) * kLaneCols;
-}
-// The warp and lane that own a slice's column.
-__device__ __forceinline__ int owner_warp(int c) { return (c >> 6) & (kWarps - 1); }
-__device__ __forceinline__ int owner_lane(int c) { return (c >> 9 << 1) | (c >> 5 & 1); }
+// Which of a slice's columns a warp's lane owns (see above).
+struct Columns {
+    bool mixed;  // the first slice
+    // the first of a lane's columns
+    __device__ __forceinline__ int first(int warp, int lane) const {
+        return mixed ? ((lane >> 1) * kWarps + warp) * 64 + (lane & 1) * kLaneCols
+                     : (warp * 32 + lane) * kLaneCols;
+    }
+    // the owner of a column
+    __device__ __forceinline__ int warp(int c) const { return mixed ? (c >> 6) & (kWarps - 1) : c >> 10; }
+    __device__ __forceinline__ int lane(int c) const {
+        return mixed ? (c >> 9 << 1) | (c >> 5 & 1) : c >> 5 & 31;
+    }
+};
 
 struct RulesIo {
     const void *logits;
@@ -80,39 +89,56 @@ struct RulesIo {
     unsigned *err;
 };
 
-// What a row says about itself.
-constexpr int32_t kInactive = -1, kBadTarget = -2, kBadRules = -3;
+// What a row says about itself, as far as it concerns a slice.
+constexpr int32_t kOk = 0, kInactive = -1, kBadTarget = -2, kBadRules = -3;
+constexpr int32_t kNoToken = -1, kAnew = -2;
 struct __align__(16) RowInfo {
-    int32_t tgt;  // the target, or one of the codes above
-    int32_t mrow;
-    // how its history differs from the row before: by one token (kPassed: which
-    // is not in the vocabulary), by none, or else (kAnew)
+    int32_t state;   // kOk, or another of these codes
+    int32_t mrow;    // the row of the mask, or negative
+    // how its history differs from the row before in this slice: by one token
+    // (where: see place), by none, or else (kAnew)
     int32_t step;
-    int32_t step_prompt;
-    float lse, g;
-    int32_t req, len;
+    int32_t target;  // where the target is, or -1: not in this slice
 };
-constexpr int32_t kNoToken = -1, kAnew = -2, kPassed = -3;
+// A column of the slice with the warp that owns it, and a flag.
+__device__ __forceinline__ int32_t place(const Columns &own, int c, bool flag) {
+    return c | own.warp(c) << 16 | (flag ? 1 << 24 : 0);
+}
+__device__ __forceinline__ int place_column(int32_t p) { return p & 0xffff; }
+__device__ __forceinline__ int place_warp(int32_t p) { return p >> 16 & 0xff; }
+__device__ __forceinline__ bool place_flag(int32_t p) { return p >> 24 != 0; }
+
+__device__ __forceinline__ int32_t row_request(const rk_logits_rules &r, int64_t t) {
+    return r.row_request ? r.row_request[t] : (r.num_requests > 0 ? (int32_t)t : 0);
+}
+__device__ __forceinline__ int32_t row_length(const rk_logits_rules &r, int64_t t) {
+    return r.row_length ? max(r.row_length[t], 0) : 0x7fffffff;
+}
 
 template <RulesOp OP>
-__device__ __forceinline__ RowInfo row_info(const RulesIo &io, const rk_logits_rules &r, int64_t t) {
-    const int64_t tgt = (OP == kApply) ? 0 : io.targets[t];
+__device__ __forceinline__ int32_t row_state(const RulesIo &io, const rk_logits_rules &r, int64_t t,
+                                             int64_t tgt, int32_t mrow) {
+    const int32_t req = row_request(r, t);
+    if ((OP != kApply && !row_active(t, tgt, io.cu, io.num_seqs)) || (r.row_request && req == -1))
+        return kInactive;
+    if (req < 0 || (r.num_requests > 0 && req >= r.num_requests) || (mrow >= 0 && mrow >= r.mask_rows))
+        return kBadRules;
+    return OP != kApply && tgt >= io.V ? kBadTarget : kOk;
+}
+__device__ __forceinline__ int32_t row_mask(const rk_logits_rules &r, int64_t t) {
+    return r.mask ? (r.row_mask ? r.row_mask[t] : (int32_t)t) : -1;
+}
+
+template <RulesOp OP>
+__device__ __forceinline__ RowInfo row_info(const RulesIo &io, const rk_logits_rules &r, int64_t t,
+                                            const Columns &own, int64_t slice0, int width) {
+    const int64_t tgt = OP == kApply ? -1 : io.targets[t];
     RowInfo i;
-    i.req = r.row_request ? r.row_request[t] : (r.num_requests > 0 ? (int32_t)t : 0);
-    i.len = r.row_length ? max(r.row_length[t], 0) : 0x7fffffff;
-    i.mrow = r.mask ? (r.row_mask ? r.row_mask[t] : (int32_t)t) : -1;
-    i.tgt = (int32_t)tgt;
+    i.mrow = row_mask(r, t);
+    i.state = row_state<OP>(io, r, t, tgt, i.mrow);
     i.step = kAnew;
-    i.step_prompt = 0;
-    i.lse = OP == kBwd ? io.lse[t] : 0.f;
-    i.g = OP == kBwd ? io.grad[t] : 0.f;
-    if ((OP != kApply && !row_active(t, tgt, io.cu, io.num_seqs)) || (r.row_request && i.req == -1))
-        i.tgt = kInactive;
-    else if (i.req < 0 || (r.num_requests > 0 && i.req >= r.num_requests) ||
-             (i.mrow >= 0 && i.mrow >= r.mask_rows))
-        i.tgt = kBadRules;
-    else if (tgt >= io.V)
-        i.tgt = kBadTarget;
+    const int64_t c = tgt - slice0;
+    i.target = tgt >= 0 && c >= 0 && c < width ? place(own, (int)c, false) : -1;
     return i;
 }
 
@@ -166,23 +192,26 @@ __device__ __forceinline__ Request load_request(const rk_logits_rules &r, int32_
     return s;
 }
 
-// row.step and row.step_prompt, given the row before.
-__device__ __forceinline__ void find_step(const RulesIo &io, const rk_logits_rules &r,
-                                          const RowInfo &before, RowInfo &row) {
-    if (row.tgt < 0 || before.tgt < 0 || row.req != before.req) return;
+// row.step of row t, given the row before.
+__device__ __forceinline__ void find_step(const rk_logits_rules &r, int64_t t, const RowInfo &before,
+                                          RowInfo &row, const Columns &own, int64_t slice0, int width) {
+    if (row.state != kOk || before.state != kOk) return;
+    const int32_t q = row_request(r, t);
+    if (q != row_request(r, t - 1)) return;
     row.step = kNoToken;
     if (r.num_requests == 0 || !r.tokens) return;
-    const int64_t a = r.token_offsets[row.req], b = r.token_offsets[row.req + 1];
+    const int64_t a = r.token_offsets[q], b = r.token_offsets[q + 1];
     if (!(a >= 0 && b >= a && b <= r.num_tokens && b - a < 0x7fffffff)) return;  // refused by load_request
-    const int32_t ntok = (int32_t)(b - a), len = min(row.len, ntok), was = min(before.len, ntok);
+    const int32_t ntok = (int32_t)(b - a);
+    const int32_t len = min(row_length(r, t), ntok), was = min(row_length(r, t - 1), ntok);
     if (len == was) return;
     if (len != was + 1) {
         row.step = kAnew;
         return;
     }
-    const int64_t v = r.tokens[a + was];
-    row.step = v >= 0 && v < io.V ? (int32_t)v : kPassed;
-    row.step_prompt = r.prompt_lengths && was < r.prompt_lengths[row.req];
+    const int64_t v = r.tokens[a + was], c = v - slice0;
+    if (v >= 0 && c >= 0 && c < width)
+        row.step = place(own, (int)c, r.prompt_lengths && was < r.prompt_lengths[q]);
 }
 
 // y of a touched column from z, its count word and its bias.
@@ -237,21 +266,15 @@ __device__ __forceinline__ float warp_max(float v) {
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
     return d;
 }
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
-    return v;
-}
-
 // A lane's 32 columns as 16-byte pieces, and the bytes from lane to lane.
 template <typename T>
 struct Lane {
     static constexpr int kCols = 16 / (int)sizeof(T), kPieces = kLaneCols / kCols;
     static constexpr int kPitch = kLaneCols * (int)sizeof(T) + 16;
-    // Spread over the warp piece by piece, lane l has pieces l, l + 32, ...: the
-    // step from one to the next in shared memory and in columns.
+    // Spread over a warp, lane l has pieces l, l + 32, ...: the lanes whose
+    // pieces are had at a time, and the columns from one time to the next.
     static constexpr int kLanes = 32 / kPieces;
-    static constexpr int kPieceRow = kLanes * kPitch, kPieceCols = kLanes / 2 * kWarps * 64;
+    static constexpr int kStep = kLanes * kLaneCols, kMixedStep = kLanes / 2 * kWarps * 64;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -276,35 +299,51 @@ __device__ __forceinline__ bool odd_start(const uint16_t *src) {
 }
 __device__ __forceinline__ bool odd_start(const float *) { return false; }
 
-// Starts the copy of a warp's columns of a row's slice (`src`: its first
-// element, `width`: its columns) into a stage.  After an odd start the columns
-// sit one element further in.  Nothing outside the slice is read.
-template <bool VEC, typename T>
-__device__ __forceinline__ void start_copy(unsigned char *stage, const T *src, int width, int warp,
-                                           int lane) {
+// Copies of a warp's columns of a row's slice into a stage.  Nothing outside
+// the slice (of `width` columns) is read.
+//
+// Rows on 16-byte boundaries: `from` and `dst` are those of the lane's first
+// piece, which is piece `lane` of the warp's; it has pieces lane, lane + 32, ...
+template <typename T>
+__device__ __forceinline__ int first_piece(const Columns &own, int warp, int lane) {
+    using L = Lane<T>;
+    return own.first(warp, lane / L::kPieces) + lane % L::kPieces * L::kCols;
+}
+template <typename T>
+__device__ __forceinline__ int first_piece_at(int lane) {
+    using L = Lane<T>;
+    return lane / L::kPieces * L::kPitch + lane % L::kPieces * 16;
+}
+template <typename T>
+__device__ __forceinline__ void copy_pieces(uint32_t dst, const T *from, int left, bool whole, bool mixed) {
+    using L = Lane<T>;
+    if (!whole) {
+        const int step = mixed ? L::kMixedStep : L::kStep;
+#pragma unroll 1
+        for (int i = 0; i < L::kPieces; ++i) {
+            const int n = min(L::kCols, left - i * step);
+            if (n > 0) cp_async16_part(dst + i * L::kLanes * L::kPitch, from + i * step, n * (int)sizeof(T));
+        }
+    } else if (mixed) {
+#pragma unroll
+        for (int i = 0; i < L::kPieces; ++i) cp_async16(dst + i * L::kLanes * L::kPitch, from + i * L::kMixedStep);
+    } else {
+#pragma unroll
+        for (int i = 0; i < L::kPieces; ++i) cp_async16(dst + i * L::kLanes * L::kPitch, from + i * L::kStep);
+    }
+}
+
+// Other rows (`src`: the slice's first element): 4 bytes at a time.  After an
+// odd start the columns sit one element further in.
+template <typename T>
+__device__ __forceinline__ void copy_words(unsigned char *stage, const T *src, int width, const Columns &own,
+                                           int warp, int lane) {
     using L = Lane<T>;
     const uint32_t dst = smem_u32(stage);
-    if constexpr (VEC) {
-        // piece x = lane + 32 i of the warp's: a fixed step from i to i + 1
-        const int o = lane / L::kPieces, part = lane % L::kPieces;
-        const int c = lane_col(warp, o) + part * L::kCols;
-        const uint32_t d = dst + o * L::kPitch + 16 * part;
-        if (width == kSliceCols) {
-#pragma unroll
-            for (int i = 0; i < L::kPieces; ++i)
-                cp_async16(d + i * L::kPieceRow, src + c + i * L::kPieceCols);
-        } else {
-#pragma unroll 1
-            for (int i = 0; i < L::kPieces; ++i) {
-                const int n = min(L::kCols, width - c - i * L::kPieceCols);
-                if (n > 0)
-                    cp_async16_part(d + i * L::kPieceRow, src + c + i * L::kPieceCols, n * (int)sizeof(T));
-            }
-        }
-    } else if constexpr (sizeof(T) == 4) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll 4
         for (int o = 0; o < 32; ++o) {
-            const int c = lane_col(warp, o) + lane;
+            const int c = own.first(warp, o) + lane;
             if (c < width) cp_async4(dst + o * L::kPitch + 4 * lane, src + c);
         }
     } else {
@@ -314,7 +353,7 @@ __device__ __forceinline__ void start_copy(unsigned char *stage, const T *src, i
 #pragma unroll 2
         for (int x = lane; x < 32 * per; x += 32) {
             const int o = odd ? x / (kLaneCols / 2 + 1) : x / (kLaneCols / 2), w = x - o * per;
-            const int c = lane_col(warp, o) + 2 * w - odd;  // its first column
+            const int c = own.first(warp, o) + 2 * w - odd;  // its first column
             if (c >= 0 && c + 1 < width) {
                 cp_async4(dst + o * L::kPitch + 4 * w, src + c);
             } else {
@@ -485,10 +524,10 @@ __device__ __forceinline__ void pairs_of(const uint4 &w, uint64_t (&z)[4]) {
                               : pair(__uint_as_float(q[(2 * j) & 3]), __uint_as_float(q[(2 * j + 1) & 3]));
 }
 
-// Shared memory of a block: counts, touched words, rows, lists and bias
-// indices, and a ring of stages per warp.  A stage holds the warp's logits and
-// afterwards its results, and its mask words.  Blocks of up to 113 KB run two
-// to an SM, which beats a second stage.
+// Shared memory of a block: what shared_view lays out, and a ring of stages
+// per warp.  A stage holds the warp's logits and afterwards its results, and
+// its mask words.  Two blocks run per SM, which leaves room for two stages of
+// bf16 (logp of 4096 x 128256: 318 us with one, 224 with two, 216 with three).
 template <RulesOp OP, typename TIn, typename TOut>
 struct Config {
     static constexpr bool kWider = OP != kLogp && sizeof(TOut) > sizeof(TIn);
@@ -503,20 +542,22 @@ struct Config {
 
 // Writes a warp's results from its stage to the row's slice.
 template <bool VEC, typename T>
-__device__ __forceinline__ void write_out(const unsigned char *stage, T *dst, int width, int warp, int lane) {
+__device__ __forceinline__ void write_out(const unsigned char *stage, T *dst, int width, const Columns &own,
+                                          int warp, int lane) {
     using L = Lane<T>;
     if (VEC && width == kSliceCols) {
         const int o = lane / L::kPieces, part = lane % L::kPieces;
         const unsigned char *from = stage + o * L::kPitch + 16 * part;
-        T *to = dst + lane_col(warp, o) + part * L::kCols;
+        T *to = dst + own.first(warp, o) + part * L::kCols;
+        const int step = own.mixed ? L::kMixedStep : L::kStep;
 #pragma unroll
         for (int i = 0; i < L::kPieces; ++i)
-            *reinterpret_cast<uint4 *>(to + i * L::kPieceCols) =
-                *reinterpret_cast<const uint4 *>(from + i * L::kPieceRow);
+            *reinterpret_cast<uint4 *>(to + i * step) =
+                *reinterpret_cast<const uint4 *>(from + i * L::kLanes * L::kPitch);
     } else {
 #pragma unroll 4
         for (int o = 0; o < 32; ++o) {
-            const int c = lane_col(warp, o) + lane;
+            const int c = own.first(warp, o) + lane;
             if (c < width) dst[c] = reinterpret_cast<const T *>(stage + o * L::kPitch)[lane];
         }
     }
@@ -544,49 +585,73 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t t0 = (int64_t)(blockIdx.x / slices) * io.run;
     const int n = (int)min((int64_t)io.run, io.T - t0);
     const int64_t words = (io.V + 31) / 32;
-    const int own = lane_col(warp, lane);  // the lane's first column
+    const Columns own{slice == 0};
+    const int mine = own.first(warp, lane);  // the lane's first column
     const uint32_t inside =
-        width >= own + 32 ? 0xffffffffu : width > own ? (1u << (width - own)) - 1u : 0u;
-    uint32_t *my_word = sh.touched + (own >> 5);
+        width >= mine + 32 ? 0xffffffffu : width > mine ? (1u << (width - mine)) - 1u : 0u;
+    uint32_t *my_word = sh.touched + (mine >> 5);
     uint16_t *list = sh.list + warp * kWarpCols;
 
-    for (int k = threadIdx.x; k < n; k += kThreads) rows[k] = row_info<OP>(io, rules, t0 + k);
+    for (int k = threadIdx.x; k < n; k += kThreads)
+        rows[k] = row_info<OP>(io, rules, t0 + k, own, slice0, width);
     __syncthreads();
 
     const TIn *zslice = reinterpret_cast<const TIn *>(io.logits) + t0 * io.ld + slice0;
     TOut *oslice = OP == kLogp ? nullptr : reinterpret_cast<TOut *>(io.out) + t0 * io.ld_out + slice0;
     float2 *parts = OP == kLogp ? io.part + (t0 * slices + slice) * kWarps + warp : nullptr;
-    auto prefetch = [&](int k) {
-        if (k < n) {
-            const int2 r = *reinterpret_cast<const int2 *>(&rows[k]);  // tgt, mrow
-            if (r.x >= 0) {
-                unsigned char *stage = ring + (C::kStages == 1 ? 0 : (k % C::kStages) * C::kStageBytes);
-                start_copy<VEC>(stage, zslice + k * io.ld, width, warp, lane);
+    // Copies run ahead of the rows: the next row to copy, its logits (VEC: the
+    // lane's first piece of them), and its stage.
+    int ahead = 0;
+    const TIn *from = zslice + (VEC ? first_piece<TIn>(own, warp, lane) : 0);
+    unsigned char *into = ring;
+    unsigned char *const both = ring + (C::kStages - 1) * C::kStageBytes;  // stage a + stage b - ring
+    auto other_stage = [&](unsigned char *stage) { return both - (stage - ring); };
+    const bool whole = width == kSliceCols;
+    const int left = width - (VEC ? first_piece<TIn>(own, warp, lane) : 0);
+    auto prefetch = [&] {
+        if (ahead < n) {
+            const int2 r = *reinterpret_cast<const int2 *>(&rows[ahead]);  // state, mrow
+            if (r.x == kOk) {
+                if constexpr (VEC)
+                    copy_pieces(smem_u32(into) + first_piece_at<TIn>(lane), from, left, whole, own.mixed);
+                else
+                    copy_words(into, from, width, own, warp, lane);
                 if (r.y >= 0 && inside)
-                    cp_async4(smem_u32(stage + C::kMaskAt) + 4 * lane,
-                              rules.mask + (int64_t)r.y * words + ((slice0 + own) >> 5));
+                    cp_async4(smem_u32(into + C::kMaskAt) + 4 * lane,
+                              rules.mask + (int64_t)r.y * words + ((slice0 + mine) >> 5));
             }
         }
         cp_commit();
+        ++ahead;
+        from += io.ld;
+        into = other_stage(into);
     };
-    for (int k = 0; k < C::kStages; ++k) prefetch(k);
-    for (int k = threadIdx.x + 1; k < n; k += kThreads) find_step(io, rules, rows[k - 1], rows[k]);
+    for (int k = 0; k < C::kStages; ++k) prefetch();
+    for (int k = threadIdx.x + 1; k < n; k += kThreads)
+        find_step(rules, t0 + k, rows[k - 1], rows[k], own, slice0, width);
     __syncthreads();
 
-    int32_t cur = -1, counted = 0;
+    int32_t cur = -1;
+    int done = -1;  // the last row whose history is counted
     uint32_t touched = 0;
     int listed = 0;  // touched columns of the warp
     Request q{};
+    // kBwd: lse and gradient of rows k & ~31 + lane
+    float lse_of = 0.f, grad_of = 0.f;
+    int held = -1;
+    unsigned char *now = ring;  // row k's stage
     for (int k = 0; k < n;) {
         // The whole block: a request, or a step of more than one token.
-        if (rows[k].tgt >= 0 && (rows[k].req != cur || rows[k].step == kAnew)) {
-            const bool other = rows[k].req != cur;
+        if (rows[k].state == kOk && rows[k].step == kAnew) {
+            const int32_t req = row_request(rules, t0 + k);
+            const bool other = req != cur;
             if (other) {
-                cur = rows[k].req;
+                cur = req;
                 q = load_request(rules, cur);
             }
             if (q.ok) {
-                const int32_t len = min(rows[k].len, q.ntok);
+                const int32_t len = min(row_length(rules, t0 + k), q.ntok);
+                const int32_t counted = other ? 0 : min(row_length(rules, t0 + done), q.ntok);
                 const bool anew = other || len < counted;
                 if (anew) {
                     start_request(sh.bias != nullptr, rules.bias_ids + q.bias0, q.nbias, slice0, width);
@@ -597,175 +662,284 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 count_tokens(q.tokens, q.prompt, anew ? 0 : counted, len, slice0, width);
                 __syncthreads();
-                counted = len;
                 touched = *my_word;
-                listed = make_list(list, touched, own, lane);
+                listed = make_list(list, touched, mine, lane);
             }
         }
         // A row without a result, or without usable rules.
-        if (rows[k].tgt < 0 || !q.ok) {
-            const int32_t tgt = rows[k].tgt;
-            const float fill = tgt == kInactive ? 0.f : __int_as_float(0x7fc00000);
-            if (tgt != kInactive) {
+        if (rows[k].state != kOk || !q.ok) {
+            const int32_t state = rows[k].state;
+            const float v = state == kInactive ? 0.f : __int_as_float(0x7fc00000);
+            if (state != kInactive) {
                 if (slice == 0 && threadIdx.x == 0) {
-                    atomicOr(io.err, tgt == kBadTarget ? kErrTargetRange : kErrRules);
-                    if (OP == kLogp) io.ytgt[t0 + k] = fill;
+                    atomicOr(io.err, state == kBadTarget ? kErrTargetRange : kErrRules);
+                    if (OP == kLogp) io.ytgt[t0 + k] = v;
                 }
-                if (OP == kLogp && lane == 0) parts[k * slices * kWarps] = make_float2(0.f, fill);
+                if (OP == kLogp && lane == 0) *parts = make_float2(0.f, v);
             }
-            if (OP == kBwd || (OP == kApply && tgt != kInactive))
+            if (OP == kBwd || (OP == kApply && state != kInactive))
 #pragma unroll 1
                 for (int o = 0; o < 32; ++o) {
-                    const int c = lane_col(warp, o) + lane;
-                    if (c < width) put(oslice + k * io.ld_out + c, fill);
+                    const int c = own.first(warp, o) + lane;
+                    if (c < width) put(oslice + c, v);
                 }
+            parts += slices * kWarps;
+            oslice += io.ld_out;
             cp_wait<0>();
-            prefetch(k + C::kStages);
+            prefetch();
+            now = other_stage(now);
             ++k;
             continue;
         }
         // Rows of the request, each warp for itself.
         const float c = __fmul_rn(kLog2e, q.itau);
-        int32_t tgt = rows[k].tgt, mrow = rows[k].mrow;
-        do {
-            cp_wait<C::kStages - 1>();  // all copies but those of later rows
-            __syncwarp();
-            unsigned char *stage = ring + (C::kStages == 1 ? 0 : (k % C::kStages) * C::kStageBytes);
-            const TIn *zrow = zslice + k * io.ld;
-            const int odd = VEC ? 0 : odd_start(zrow);
-            const uint32_t *masks = reinterpret_cast<const uint32_t *>(stage + C::kMaskAt);
-            const bool masked = mrow >= 0;
-            const uint32_t live = masked ? inside & masks[lane] : inside;  // columns the mask allows
-            uint4 w[L::kPieces];
+        // Single columns: a column's logit in a stage, a touched one's y from its
+        // logit, and whether the mask allows a column.
+        auto at = [&](unsigned char *stage, int odd, int j) {
+            return reinterpret_cast<TIn *>(stage + own.lane(j) * L::kPitch) + (j & 31) + odd;
+        };
+        auto touched_y = [&](int j, float z) {
+            const int bi = sh.bias ? sh.bias[j] : 0;
+            return rule_y(z, sh.count[j], bi ? rules.bias_values[q.bias0 + bi - 1] : 0.f, q);
+        };
+        auto allowed = [&](const unsigned char *stage, int mrow, int j) {
+            return mrow < 0 || (reinterpret_cast<const uint32_t *>(stage + C::kMaskAt)[own.lane(j)] >> (j & 31) & 1u);
+        };
+        auto load_pieces = [&](uint4 (&w)[L::kPieces], const unsigned char *stage, int odd) {
 #pragma unroll
             for (int i = 0; i < L::kPieces; ++i)
                 w[i] = VEC || !odd ? *reinterpret_cast<const uint4 *>(stage + lane * L::kPitch + 16 * i)
                                    : load_odd_piece(stage + lane * L::kPitch + 16 * i);
-            // a column's logit in the stage; a touched one's y from its logit
-            auto staged = [&](int j) {
-                return elem(reinterpret_cast<const TIn *>(stage + owner_lane(j) * L::kPitch) + (j & 31) + odd);
-            };
-            auto touched_y = [&](int j, float z, uint32_t cw) {
-                const int bi = sh.bias ? sh.bias[j] : 0;
-                return rule_y(z, cw, bi ? rules.bias_values[q.bias0 + bi - 1] : 0.f, q);
-            };
-            auto allowed = [&](int j) { return !masked || (masks[owner_lane(j)] >> (j & 31) & 1u); };
-            // the target, if it is one of this warp's columns
-            const uint32_t tc = (uint32_t)tgt - (uint32_t)slice0;
-            const bool has_target = OP != kApply && tc < (uint32_t)width && owner_warp(tc) == warp;
-            // the list's first 32 columns, one to a lane
-            int c0 = -1;
-            float z0 = 0.f, y0 = -INFINITY;
-            uint32_t cw0 = 0;
-            if (listed > 0 && lane < listed) {
-                c0 = list[lane];
-                if (allowed(c0)) {
-                    z0 = staged(c0);
-                    cw0 = sh.count[c0];
-                    y0 = touched_y(c0, z0, cw0);
-                } else {
-                    c0 = -1;
+        };
+
+        // kLogp of rows k .. k + R - 1, whose histories are the same here.  Two
+        // rows at a time share the list, and each fills the other's latencies.
+        auto score = [&](auto rows_at_once) {
+            constexpr int R = decltype(rows_at_once)::value;
+            unsigned char *stage[R];
+            int odd[R];
+            RowInfo row[R];
+            uint32_t live[R];  // columns the mask allows
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                stage[r] = r == 0 ? now : other_stage(now);
+                odd[r] = VEC ? 0 : odd_start(zslice + (k + r) * io.ld);
+                row[r] = rows[k + r];
+                live[r] = inside;
+                if (row[r].mrow >= 0)
+                    live[r] &= reinterpret_cast<const uint32_t *>(stage[r] + C::kMaskAt)[lane];
+                if (row[r].target >= 0 && place_warp(row[r].target) == warp) {
+                    const int j = place_column(row[r].target);
+                    if (own.lane(j) == lane) {
+                        float y = -INFINITY;
+                        if (live[r] >> (j & 31) & 1u) {
+                            y = elem(at(stage[r], odd[r], j));
+                            if (touched >> (j & 31) & 1u) y = touched_y(j, y);
+                        }
+                        io.ytgt[t0 + k + r] = y;
+                    }
+                    __syncwarp();
                 }
             }
-
-            if constexpr (OP == kLogp) {
-                // the rest of the list: running maximum and sum, four columns at a time
-                float mt = -INFINITY, st = 0.f;
-                for (int e0 = 32 + lane; e0 - lane < listed; e0 += 128) {
-                    float y[4];
+            // the touched columns, 32 at a time: their y are taken here (the first in
+            // y0, the others as a running maximum and sum), and their logits become
+            // -inf for the lanes that own them
+            float mt[R], st[R], y0[R];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int cu = e0 + 32 * u < listed ? list[e0 + 32 * u] : -1;
-                        y[u] = -INFINITY;
-                        if (cu >= 0 && allowed(cu)) y[u] = touched_y(cu, staged(cu), sh.count[cu]);
-                    }
-                    const float mn = fmaxf(fmaxf(mt, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
-                    const float r = mn == -INFINITY ? 0.f : mn;
-                    if (mt != -INFINITY) st = __fmul_rn(st, ex2(__fmul_rn(__fsub_rn(mt, r), c)));
+            for (int r = 0; r < R; ++r) {
+                mt[r] = y0[r] = -INFINITY;
+                st[r] = 0.f;
+            }
+            if (listed > 0) {
+                if (lane < listed) {
+                    const int j = list[lane];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) st = __fadd_rn(st, ex2(__fmul_rn(__fsub_rn(y[u], r), c)));
-                    mt = mn;
-                }
-                if (has_target && owner_lane(tc) == lane) {
-                    float y = -INFINITY;
-                    if (live >> (tc & 31) & 1u) {
-                        y = staged(tc);
-                        if (touched >> (tc & 31) & 1u) y = touched_y(tc, y, sh.count[tc]);
+                    for (int r = 0; r < R; ++r) {
+                        TIn *zj = at(stage[r], odd[r], j);
+                        if (allowed(stage[r], row[r].mrow, j)) y0[r] = touched_y(j, elem(zj));
+                        put(zj, -INFINITY);
                     }
-                    io.ytgt[t0 + k] = y;
                 }
-                // untouched columns: one maximum, then the terms relative to it
-                const uint32_t plain = live & ~touched;
-                float m;
+                for (int e0 = 32 + lane; e0 - lane < listed; e0 += 128)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        float y[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            y[u] = -INFINITY;
+                            if (e0 + 32 * u < listed) {
+                                const int j = list[e0 + 32 * u];
+                                TIn *zj = at(stage[r], odd[r], j);
+                                if (allowed(stage[r], row[r].mrow, j)) y[u] = touched_y(j, elem(zj));
+                                put(zj, -INFINITY);
+                            }
+                        }
+                        const float mn = fmaxf(fmaxf(mt[r], fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
+                        const float ref = mn == -INFINITY ? 0.f : mn;
+                        if (mt[r] != -INFINITY)
+                            st[r] = __fmul_rn(st[r], ex2(__fmul_rn(__fsub_rn(mt[r], ref), c)));
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            st[r] = __fadd_rn(st[r], ex2(__fmul_rn(__fsub_rn(y[u], ref), c)));
+                        mt[r] = mn;
+                    }
+                __syncwarp();
+            }
+            uint4 w[R][L::kPieces];
+#pragma unroll
+            for (int r = 0; r < R; ++r) load_pieces(w[r], stage[r], odd[r]);
+            __syncwarp();  // the stages are free again
+#pragma unroll
+            for (int r = 0; r < R; ++r) prefetch();
+            // the other columns: one maximum, then the terms relative to it
+            float ref[R], rc[R], m[R];
+            bool far = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (!__all_sync(0xffffffffu, live[r] == 0xffffffffu)) keep_columns(w[r], live[r]);
                 if constexpr (sizeof(TIn) == 2) {
-                    if (!__all_sync(0xffffffffu, plain == 0xffffffffu)) keep_columns(w, plain);
                     uint32_t x[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        x[i] = max_bf16x2(max_bf16x2(w[i].x, w[i].y), max_bf16x2(w[i].z, w[i].w));
+                        x[i] = max_bf16x2(max_bf16x2(w[r][i].x, w[r][i].y), max_bf16x2(w[r][i].z, w[r][i].w));
                     x[0] = max_bf16x2(max_bf16x2(x[0], x[1]), max_bf16x2(x[2], x[3]));
-                    m = fmaxf(bf16_lo(x[0]), bf16_hi(x[0]));
+                    m[r] = fmaxf(bf16_lo(x[0]), bf16_hi(x[0]));
                 } else {
-                    if (!__all_sync(0xffffffffu, plain == 0xffffffffu)) keep_columns(w, plain);
                     float x[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        x[i] = fmaxf(fmaxf(__uint_as_float(w[i].x), __uint_as_float(w[i].y)),
-                                     fmaxf(__uint_as_float(w[i].z), __uint_as_float(w[i].w)));
-                    m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                              fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+                        x[i] = fmaxf(fmaxf(__uint_as_float(w[r][i].x), __uint_as_float(w[r][i].y)),
+                                     fmaxf(__uint_as_float(w[r][i].z), __uint_as_float(w[r][i].w)));
+                    m[r] = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                                 fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
                 }
-                // Terms 2^(z c - r), r = the warp's maximum m times c, rounded: one
-                // rounding of the small difference each.  Where m c might leave the
-                // type's range (logits next to its lowest value), 2^((z - m) c).
-                m = warp_max(fmaxf(m, fmaxf(mt, y0)));
-                const float ref = m == -INFINITY ? 0.f : m;
-                const bool far = !(fabsf(ref) < 1e32f);  // c < 1.5e6
-                float r = __fmul_rn(ref, c);
-                uint64_t acc[4] = {0, 0, 0, 0};  // pairs of +0
-                auto sum_terms = [&](auto is_far) {
-                    const uint64_t nr = pair(-r, -r), cc = pair(c, c), nf = pair(-ref, -ref);
+                m[r] = fmaxf(m[r], fmaxf(mt[r], y0[r]));
+            }
 #pragma unroll
-                    for (int i = 0; i < L::kPieces; ++i) {
-                        uint64_t z[4];
-                        pairs_of<TIn>(w[i], z);
+            for (int r = 0; r < R; ++r) {
+                m[r] = warp_max(m[r]);
+                ref[r] = m[r] == -INFINITY ? 0.f : m[r];
+                rc[r] = __fmul_rn(ref[r], c);
+                far = far || !(fabsf(ref[r]) < 1e32f);  // c < 1.5e6
+            }
+            // Terms 2^(z c - m c), m c rounded: one rounding of the small difference
+            // each.  Where m c might leave the type's range (logits next to its
+            // lowest value), 2^((z - m) c).
+            uint64_t acc[R][4] = {};  // pairs of +0
+            auto add_terms = [&](int r, int i, bool fused) {
+                uint64_t z[4];
+                pairs_of<TIn>(w[r][i], z);
 #pragma unroll
-                        for (int j = 0; j < L::kCols / 2; ++j) {
-                            float a, b;
-                            if constexpr (decltype(is_far)::value)
-                                unpair(mul2(add2(z[j], nf), cc), a, b);
-                            else
-                                unpair(fma2(z[j], cc, nr), a, b);
-                            const int to = (i * (L::kCols / 2) + j) & 3;
-                            acc[to] = add2(acc[to], pair(ex2(a), ex2(b)));
-                        }
-                    }
-                };
-                if (__builtin_expect(far, 0)) {
-                    sum_terms(std::true_type{});
-                    r = 0.f;
-                } else {
-                    sum_terms(std::false_type{});
+                for (int j = 0; j < L::kCols / 2; ++j) {
+                    float a, b;
+                    if (fused)
+                        unpair(fma2(z[j], pair(c, c), pair(-rc[r], -rc[r])), a, b);
+                    else
+                        unpair(mul2(add2(z[j], pair(-ref[r], -ref[r])), pair(c, c)), a, b);
+                    const int to = (i * (L::kCols / 2) + j) & 3;
+                    acc[r][to] = add2(acc[r][to], pair(ex2(a), ex2(b)));
                 }
-                float s0, s1;
-                unpair(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), s0, s1);
-                float s = __fadd_rn(s0, s1);
-                // relative to m c itself rather than to its rounding
-                if (!far) s = __fmaf_rn(s, __fmul_rn(-kLn2, __fmaf_rn(ref, c, -r)), s);
-                if (listed > 0) {
-                    s = __fadd_rn(s, ex2(__fmul_rn(__fsub_rn(y0, ref), c)));
-                    if (listed > 32)
-                        s = __fadd_rn(s, mt == -INFINITY ? st
-                                                         : __fmul_rn(st, ex2(__fmul_rn(__fsub_rn(mt, ref), c))));
+            };
+            if (__builtin_expect(far, 0)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const bool fused = fabsf(ref[r]) < 1e32f;
+                    if (!fused) rc[r] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < L::kPieces; ++i) add_terms(r, i, fused);
                 }
-                s = warp_sum(s);
-                if (lane == 0) parts[k * slices * kWarps] = make_float2(m, s);
             } else {
-                const float zt = has_target && owner_lane(tc) == lane ? staged(tc) : 0.f;
+#pragma unroll
+                for (int i = 0; i < L::kPieces; ++i)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) add_terms(r, i, true);
+            }
+            float s[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float s0, s1;
+                unpair(add2(add2(acc[r][0], acc[r][1]), add2(acc[r][2], acc[r][3])), s0, s1);
+                s[r] = __fadd_rn(s0, s1);
+                // relative to m c itself rather than to its rounding
+                if (!far || fabsf(ref[r]) < 1e32f)
+                    s[r] = __fmaf_rn(s[r], __fmul_rn(-kLn2, __fmaf_rn(ref[r], c, -rc[r])), s[r]);
+                if (listed > 0) {
+                    s[r] = __fadd_rn(s[r], ex2(__fmul_rn(__fsub_rn(y0[r], ref[r]), c)));
+                    if (listed > 32)
+                        s[r] = __fadd_rn(s[r], mt[r] == -INFINITY
+                                                   ? st[r]
+                                                   : __fmul_rn(st[r], ex2(__fmul_rn(__fsub_rn(mt[r], ref[r]), c))));
+                }
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    s[r] = __fadd_rn(s[r], __shfl_xor_sync(0xffffffffu, s[r], off));
+            if (lane == 0)
+#pragma unroll
+                for (int r = 0; r < R; ++r) parts[r * slices * kWarps] = make_float2(m[r], s[r]);
+            parts += R * slices * kWarps;
+        };
+
+        do {
+            cp_wait<C::kStages - 1>();  // all copies but those of later rows
+            __syncwarp();
+            if constexpr (OP == kLogp) {
+                bool two = false;
+                if (C::kStages > 1 && k + 1 < n) {
+                    const RowInfo next = rows[k + 1];
+                    two = next.state == kOk && next.step != kAnew &&
+                          !(next.step >= 0 && place_warp(next.step) == warp);
+                }
+                if (two) {
+                    cp_wait<0>();
+                    __syncwarp();
+                    score(std::integral_constant<int, 2>{});
+                    ++k;
+                } else {
+                    score(std::integral_constant<int, 1>{});
+                    now = other_stage(now);
+                }
+            } else {
+                unsigned char *stage = now;
+                const RowInfo row = rows[k];
+                const TIn *zrow = zslice + k * io.ld;
+                const int odd = VEC ? 0 : odd_start(zrow);
+                uint32_t live = inside;  // columns the mask allows
+                if (row.mrow >= 0) live &= reinterpret_cast<const uint32_t *>(stage + C::kMaskAt)[lane];
+                uint4 w[L::kPieces];
+                load_pieces(w, stage, odd);
+                // the list's first 32 columns, one to a lane
+                int c0 = -1;
+                float z0 = 0.f, y0 = 0.f;
+                uint32_t cw0 = 0;
+                if (listed > 0 && lane < listed) {
+                    c0 = list[lane];
+                    if (allowed(stage, row.mrow, c0)) {
+                        z0 = elem(at(stage, odd, c0));
+                        cw0 = sh.count[c0];
+                        y0 = touched_y(c0, z0);
+                    } else {
+                        c0 = -1;
+                    }
+                }
+                // the target, if it is one of this warp's columns
+                const bool has_target = OP == kBwd && row.target >= 0 && place_warp(row.target) == warp;
+                const int tcol = place_column(row.target);
+                const float zt = has_target && own.lane(tcol) == lane ? elem(at(stage, odd, tcol)) : 0.f;
+                if (OP == kBwd && k >> 5 != held) {
+                    held = k >> 5;
+                    const int64_t t = t0 + (held * 32 + lane);
+                    lse_of = t < io.T ? io.lse[t] : 0.f;
+                    grad_of = t < io.T ? io.grad[t] : 0.f;
+                }
                 __syncwarp();  // the stage is read
-                const bool none = OP == kBwd && rows[k].lse == -INFINITY;  // the rules leave nothing
-                const float l = none ? 0.f : rows[k].lse;
-                const float g = OP == kBwd && !none ? __fmul_rn(rows[k].g, q.itau) : 0.f;
+                const float lse = OP == kBwd ? __shfl_sync(0xffffffffu, lse_of, k & 31) : 0.f;
+                const bool none = OP == kBwd && lse == -INFINITY;  // the rules leave nothing
+                const float l = none ? 0.f : lse;
+                const float g =
+                    OP == kBwd && !none ? __fmul_rn(__shfl_sync(0xffffffffu, grad_of, k & 31), q.itau) : 0.f;
                 // x - lse with 1 / temperature to 48 bits (id + i1): the rounding of
                 // 1 / temperature alone would weigh |x| times half a step.  Rounded
                 // down: i1 >= 0, so that -inf times i1 > 0 stays -inf, and i1 = 0 is left
@@ -826,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     transform(std::false_type{});
                 __syncwarp();
                 auto put_column = [&](int j, float v) {
-                    put(reinterpret_cast<TOut *>(stage + owner_lane(j) * Lane<TOut>::kPitch) + (j & 31), v);
+                    put(reinterpret_cast<TOut *>(stage + own.lane(j) * Lane<TOut>::kPitch) + (j & 31), v);
                 };
                 if (listed > 0 && !none) {
                     // the touched columns over what stands there; the stage no longer
@@ -838,45 +1012,43 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
                             cu[u] = e0 + 32 * u < listed ? list[e0 + 32 * u] : -1;
-                            if (cu[u] >= 0 && !allowed(cu[u])) cu[u] = -1;
+                            if (cu[u] >= 0 && !allowed(stage, row.mrow, cu[u])) cu[u] = -1;
                             z[u] = cu[u] >= 0 ? elem(zrow + cu[u]) : 0.f;
                         }
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
                             if (cu[u] >= 0) {
                                 const uint32_t cw = sh.count[cu[u]];
-                                put_column(cu[u], result(0.f, z[u], cw, touched_y(cu[u], z[u], cw)));
+                                put_column(cu[u], result(0.f, z[u], cw, touched_y(cu[u], z[u])));
                             }
                     }
                     __syncwarp();
                 }
                 if (has_target) {
-                    if (owner_lane(tc) == lane && (shown >> (tc & 31) & 1u)) {
-                        const bool t = touched >> (tc & 31) & 1u;
-                        const uint32_t cw = t ? sh.count[tc] : 0u;
-                        put_column(tc, result(1.f, zt, cw, t ? touched_y(tc, zt, cw) : zt));
+                    if (own.lane(tcol) == lane && (shown >> (tcol & 31) & 1u)) {
+                        const bool t = touched >> (tcol & 31) & 1u;
+                        const uint32_t cw = t ? sh.count[tcol] : 0u;
+                        put_column(tcol, result(1.f, zt, cw, t ? touched_y(tcol, zt) : zt));
                     }
                     __syncwarp();
                 }
-                write_out<VEC>(stage, oslice + k * io.ld_out, width, warp, lane);
+                write_out<VEC>(stage, oslice, width, own, warp, lane);
+                oslice += io.ld_out;
+                __syncwarp();  // the stage is free again
+                prefetch();
+                now = other_stage(now);
             }
-            __syncwarp();  // the stage is free again
-            prefetch(k + C::kStages);
+            done = k;
             if (++k >= n) break;
-            const int4 next = *reinterpret_cast<const int4 *>(&rows[k]);  // tgt, mrow, step, step_prompt
-            if (next.x < 0 || next.z == kAnew) break;
-            tgt = next.x;
-            mrow = next.y;
-            if (next.z != kNoToken) {  // one token more
-                ++counted;
-                const uint32_t j = (uint32_t)next.z - (uint32_t)slice0;
-                if (next.z >= 0 && j < (uint32_t)width && owner_warp(j) == warp) {
-                    const uint32_t bit = owner_lane(j) == lane ? 1u << (j & 31) : 0u;
-                    if (bit) sh.count[j] = next.w ? (sh.count[j] | kPromptBit) : sh.count[j] + 1u;
-                    const bool fresh = (bit & ~touched) != 0;
-                    touched |= bit;
-                    if (__any_sync(0xffffffffu, fresh)) listed = make_list(list, touched, own, lane);
-                }
+            const RowInfo next = rows[k];
+            if (next.state != kOk || next.step == kAnew) break;
+            if (next.step >= 0 && place_warp(next.step) == warp) {  // one token more
+                const int j = place_column(next.step);
+                const uint32_t bit = own.lane(j) == lane ? 1u << (j & 31) : 0u;
+                if (bit) sh.count[j] = place_flag(next.step) ? (sh.count[j] | kPromptBit) : sh.count[j] + 1u;
+                const bool fresh = (bit & ~touched) != 0;
+                touched |= bit;
+                if (__any_sync(0xffffffffu, fresh)) listed = make_list(list, touched, mine, lane);
             }
         } while (true);
     }
@@ -907,16 +1079,16 @@ __global__ void __launch_bounds__(32 * kMergeRows)
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kMergeRows + (threadIdx.x >> 5);
     if (t >= io.T) return;
-    const RowInfo row = row_info<kLogp>(io, rules, t);
-    if (row.tgt == kInactive) {
+    const int32_t state = row_state<kLogp>(io, rules, t, io.targets[t], row_mask(rules, t));
+    if (state == kInactive) {
         if (lane == 0) {
             logp[t] = 0.f;
             if (lse) lse[t] = 0.f;
         }
         return;
     }
-    const bool has_tau = row.tgt >= 0 && rules.num_requests > 0 && rules.temperature;
-    const float tau = has_tau ? rules.temperature[row.req] : 1.f;
+    const bool has_tau = state != kBadRules && rules.num_requests > 0 && rules.temperature;
+    const float tau = has_tau ? rules.temperature[row_request(rules, t)] : 1.f;
     const float c = __fmul_rn(kLog2e, __frcp_rn(tau));
     const int64_t parts = (io.V + kSliceCols - 1) / kSliceCols * kWarps;
     float m = -INFINITY, s = 0.f;
@@ -933,7 +1105,7 @@ __global__ void __launch_bounds__(32 * kMergeRows)
     if (lane == 0) {
         const float nan = __int_as_float(0x7fc00000);
         float l, p;
-        if (row.tgt < 0 || s != s) {
+        if (state != kOk || s != s) {
             l = p = nan;
         } else if (s == 0.f) {
             l = p = -INFINITY;
