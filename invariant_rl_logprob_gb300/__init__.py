@@ -670,27 +670,14 @@ class LogitsRules:
                  bias_values: torch.Tensor | None = None, bias_offsets: torch.Tensor | None = None,
                  mask: torch.Tensor | None = None, row_request: torch.Tensor | None = None,
                  row_length: torch.Tensor | None = None, row_mask: torch.Tensor | None = None):
-        kept = {"temperature": temperature, "repetition": repetition, "frequency": frequency,
-                "presence": presence, "tokens": tokens, "token_offsets": token_offsets,
-                "prompt_lengths": prompt_lengths, "bias_ids": bias_ids, "bias_values": bias_values,
-                "bias_offsets": bias_offsets, "mask": mask, "row_request": row_request,
-                "row_length": row_length, "row_mask": row_mask}
-        if (tokens is None) != (token_offsets is None):
-            raise ValueError("tokens and token_offsets go together")
-        if prompt_lengths is not None and tokens is None:
-            raise ValueError("prompt_lengths needs tokens")
-        if not ((bias_ids is None) == (bias_values is None) == (bias_offsets is None)):
-            raise ValueError("bias_ids, bias_values and bias_offsets go together")
-        if row_length is not None and tokens is None:
-            raise ValueError("row_length needs tokens")
-        if row_mask is not None and mask is None:
-            raise ValueError("row_mask needs mask")
-        address = dict.fromkeys(kept)
+        kept = (temperature, repetition, frequency, presence, tokens, token_offsets, prompt_lengths,
+                bias_ids, bias_values, bias_offsets, mask, row_request, row_length, row_mask)
+        address = []
         device = requests = rows = None
-        for name, t in kept.items():
+        for t, (name, dtype, ndim, extra) in zip(kept, _RULES):
             if t is None:
+                address.append(None)
                 continue
-            dtype, ndim, off = _RULES[name]
             if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
                     and t.dim() == ndim and t.is_contiguous()):
                 _need(t, name, dtype, ndim)
@@ -698,51 +685,56 @@ class LogitsRules:
                 device = t.device
             elif t.device != device:
                 raise ValueError(f"{name} is on {t.device}, not on {device}")
-            if off is not None:
-                n = t.shape[0] - off
-                if off < 0:  # per row
-                    n = t.shape[0]
-                    if rows is not None and n != rows:
+            if extra is not None:
+                n = t.size(0) - extra
+                if extra < 0:  # per row
+                    n = t.size(0)
+                    if rows is None:
+                        rows = n
+                    elif n != rows:
                         raise ValueError(f"{name} does not fit {rows} rows")
-                    rows = n
-                else:  # per request
-                    if n < 1 or (requests is not None and n != requests):
-                        raise ValueError(f"{name} does not fit "
-                                         f"{requests if requests else 'one or more'} requests")
+                elif requests is None and n > 0:
                     requests = n
+                elif n != requests:
+                    raise ValueError(f"{name} does not fit {requests or 'one or more'} requests")
             # an empty list still has to be told from a missing one
-            address[name] = t.data_ptr() or _EMPTY
-        if bias_ids is not None and bias_ids.shape[0] != bias_values.shape[0]:
+            address.append(t.data_ptr() or _EMPTY)
+        if (tokens is None) != (token_offsets is None):
+            raise ValueError("tokens and token_offsets go together")
+        if tokens is None and (prompt_lengths is not None or row_length is not None):
+            raise ValueError("prompt_lengths and row_length need tokens")
+        if not ((bias_ids is None) == (bias_values is None) == (bias_offsets is None)):
+            raise ValueError("bias_ids, bias_values and bias_offsets go together")
+        if row_mask is not None and mask is None:
+            raise ValueError("row_mask needs mask")
+        num_bias = 0 if bias_ids is None else bias_ids.size(0)
+        if num_bias and num_bias != bias_values.size(0):
             raise ValueError("bias_ids and bias_values differ in length")
         if requests and row_request is None:
             if rows is not None and rows != requests:
                 raise ValueError(f"{requests} requests for {rows} rows: row_request is missing")
             rows = requests
+        mask_rows, self.mask_words = (0, None) if mask is None else mask.shape
         if mask is not None and row_mask is None:
-            if rows is not None and rows != mask.shape[0]:
-                raise ValueError(f"{mask.shape[0]} masks for {rows} rows: row_mask is missing")
-            rows = mask.shape[0]
-        s = _RulesStruct(requests or 0, address["temperature"], address["repetition"],
-                         address["frequency"], address["presence"], address["tokens"],
-                         0 if tokens is None else tokens.shape[0], address["token_offsets"],
-                         address["prompt_lengths"], address["bias_ids"], address["bias_values"],
-                         0 if bias_ids is None else bias_ids.shape[0], address["bias_offsets"],
-                         address["mask"], 0 if mask is None else mask.shape[0],
-                         address["row_request"], address["row_length"], address["row_mask"])
+            if rows is not None and rows != mask_rows:
+                raise ValueError(f"{mask_rows} masks for {rows} rows: row_mask is missing")
+            rows = mask_rows
+        self.struct = s = _RulesStruct(
+            requests or 0, *address[:5], 0 if tokens is None else tokens.size(0), *address[5:9],
+            num_bias, address[9], address[10], mask_rows, *address[11:])
         self.device, self.rows = device, rows
-        self.mask_words = None if mask is None else mask.shape[1]
-        self.struct, self.address, self._kept = s, ctypes.addressof(s), kept
+        self.address, self._kept = ctypes.addressof(s), kept
 
 
 _EMPTY = 256  # an address that an empty list never reads
-# type, dimensions, and entries beyond one per request (-1: one per row, None: neither)
-_RULES = {"temperature": (torch.float32, 1, 0), "repetition": (torch.float32, 1, 0),
-          "frequency": (torch.float32, 1, 0), "presence": (torch.float32, 1, 0),
-          "tokens": (torch.int64, 1, None), "token_offsets": (torch.int64, 1, 1),
-          "prompt_lengths": (torch.int32, 1, 0), "bias_ids": (torch.int64, 1, None),
-          "bias_values": (torch.float32, 1, None), "bias_offsets": (torch.int64, 1, 1),
-          "mask": (torch.int32, 2, None), "row_request": (torch.int32, 1, -1),
-          "row_length": (torch.int32, 1, -1), "row_mask": (torch.int32, 1, -1)}
+# name, type, dimensions, and entries beyond one per request (-1: one per row, None: neither)
+_RULES = (("temperature", torch.float32, 1, 0), ("repetition", torch.float32, 1, 0),
+          ("frequency", torch.float32, 1, 0), ("presence", torch.float32, 1, 0),
+          ("tokens", torch.int64, 1, None), ("token_offsets", torch.int64, 1, 1),
+          ("prompt_lengths", torch.int32, 1, 0), ("bias_ids", torch.int64, 1, None),
+          ("bias_values", torch.float32, 1, None), ("bias_offsets", torch.int64, 1, 1),
+          ("mask", torch.int32, 2, None), ("row_request", torch.int32, 1, -1),
+          ("row_length", torch.int32, 1, -1), ("row_mask", torch.int32, 1, -1))
 _TYPE_CODES = {torch.bfloat16: 0, torch.float32: 1}
 
 
@@ -852,10 +844,12 @@ def logp_from_logits_rules(logits: torch.Tensor, targets: torch.Tensor, rules: L
     _rules_for(rules, T, V, device)
     if out is None:
         out = torch.empty(T, dtype=torch.float32, device=device)
+    else:
+        _vector(out, "out", T, device)
     if lse is None:
         lse = torch.empty(T, dtype=torch.float32, device=device)
-    _vector(out, "out", T, device)
-    _vector(lse, "lse", T, device)
+    else:
+        _vector(lse, "lse", T, device)
     workspace = _scratch(workspace, lib.rk_logp_from_logits_rules_workspace_size(T, V), device)
     _run("rk_logp_from_logits_rules", lib.rk_logp_from_logits_rules, device, stream,
          logits.data_ptr(), code, ld, targets.data_ptr(), _ptr(cu), ns, rules.address, T, V,

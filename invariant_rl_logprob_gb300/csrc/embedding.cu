@@ -760,26 +760,27 @@ BwdBuffers carve(void *base, int64_t n, int64_t H) {
 }
 
 template <int THREADS>
-cudaError_t launch_small(const Canonical &c, const BwdBuffers &b, int passes, int digit, cudaStream_t st) {
+cudaError_t launch_small(const Canonical &c, const BwdBuffers &b, int passes, int digit, const DeviceInfo &di,
+                         cudaStream_t st) {
     constexpr size_t smem = sizeof(SmallSort<THREADS>);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(emb_sort_small<THREADS>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e =
+        allow_shared(reinterpret_cast<const void *>(emb_sort_small<THREADS>), smem, di, allowed);
+    if (e != cudaSuccess) return e;
     return launch_dependent_smem(emb_sort_small<THREADS>, 1, THREADS, smem, st, c, passes, digit, b.key[0],
                                  b.val[0], b.pieces, b.joins, b.counters);
 }
 
 // Sorts the canonical tokens and finds their pieces; *where: which of the two
 // buffers holds the sorted keys and rows.
-cudaError_t launch_sort(const Canonical &c, const BwdBuffers &b, int *where, cudaStream_t st) {
+cudaError_t launch_sort(const Canonical &c, const BwdBuffers &b, int *where, const DeviceInfo &di,
+                        cudaStream_t st) {
     const int bits = key_bits(c.V);
     const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
     const int digit = (bits + passes - 1) / passes;
     *where = 0;
-    if (c.n <= kSortItems * kTinyThreads) return launch_small<kTinyThreads>(c, b, passes, digit, st);
-    if (c.n <= kSmallSort) return launch_small<kSmallThreads>(c, b, passes, digit, st);
+    if (c.n <= kSortItems * kTinyThreads) return launch_small<kTinyThreads>(c, b, passes, digit, di, st);
+    if (c.n <= kSmallSort) return launch_small<kSmallThreads>(c, b, passes, digit, di, st);
     const int64_t tiles = (c.n + kSortTile - 1) / kSortTile, pitch = tile_pitch(c.n);
     const int bins = 1 << digit;
     cudaError_t e = launch_dependent(emb_keys, tiles, kSortThreads, st, c, b.key[0], b.val[0], bins, b.hist,
@@ -854,7 +855,7 @@ cudaError_t launch_embedding_bwd(const void *dout, rk_dtype dout_type, const int
     const BwdBuffers b = carve(workspace, n, H);
     const Canonical c{ids, cu, num_seqs, T, V, order, n, di.err};
     int where;
-    cudaError_t e = launch_sort(c, b, &where, st);
+    cudaError_t e = launch_sort(c, b, &where, di, st);
     if (e != cudaSuccess) return e;
     // Zeros in the rows without a token.  While one block sorts, the rest of
     // the device writes zeros over all of dE, and the rows with a token are

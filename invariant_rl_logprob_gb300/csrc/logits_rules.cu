@@ -1142,28 +1142,32 @@ int rows_per_block(int64_t T, int64_t V, const DeviceInfo &di) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxRun, want));
 }
 
-template <RulesOp OP, typename TIn, typename TOut>
-cudaError_t launch(RulesIo io, const rk_logits_rules &r, const DeviceInfo &di, cudaStream_t st) {
-    const auto rows_aligned = [](const void *p, int64_t ld, size_t size) {
-        return aligned(p, 16) && ld * (int64_t)size % 16 == 0;
-    };
-    const bool vec = rows_aligned(io.logits, io.ld, sizeof(TIn)) &&
-                     (OP == kLogp || rows_aligned(io.out, io.ld_out, sizeof(TOut)));
-    auto *kernel = vec ? rules_kernel<OP, TIn, TOut, true> : rules_kernel<OP, TIn, TOut, false>;
-    const size_t smem = Config<OP, TIn, TOut>::smem(r.bias_ids != nullptr);
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+template <RulesOp OP, typename TIn, typename TOut, bool VEC>
+cudaError_t launch_rows(RulesIo io, const rk_logits_rules &r, const DeviceInfo &di, cudaStream_t st) {
+    auto *kernel = rules_kernel<OP, TIn, TOut, VEC>;
+    using C = Config<OP, TIn, TOut>;
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), C::smem(true), di, allowed);
+    if (e != cudaSuccess) return e;
     io.run = rows_per_block(io.T, io.V, di);
     const int64_t slices = (io.V + kSliceCols - 1) / kSliceCols;
     const int64_t blocks = slices * ((io.T + io.run - 1) / io.run);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
-    dependent(&cfg, attr, (unsigned)blocks, kThreads, smem, st);
+    dependent(&cfg, attr, (unsigned)blocks, kThreads, C::smem(r.bias_ids != nullptr), st);
     return cudaLaunchKernelEx(&cfg, kernel, io, r);
+}
+
+template <RulesOp OP, typename TIn, typename TOut>
+cudaError_t launch(const RulesIo &io, const rk_logits_rules &r, const DeviceInfo &di, cudaStream_t st) {
+    const auto rows_aligned = [](const void *p, int64_t ld, size_t size) {
+        return aligned(p, 16) && ld * (int64_t)size % 16 == 0;
+    };
+    const bool vec = rows_aligned(io.logits, io.ld, sizeof(TIn)) &&
+                     (OP == kLogp || rows_aligned(io.out, io.ld_out, sizeof(TOut)));
+    return vec ? launch_rows<OP, TIn, TOut, true>(io, r, di, st)
+               : launch_rows<OP, TIn, TOut, false>(io, r, di, st);
 }
 
 template <RulesOp OP>

@@ -1,6 +1,7 @@
 // rk_internal.h -- host-side declarations shared by the librk translation units.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -43,6 +44,19 @@ bool encode_tmap_bf16_2d(CUtensorMap *map, const void *base, uint64_t inner, uin
 // The same with 64-byte swizzle (boxes whose rows are at most 64 bytes).
 bool encode_tmap_bf16_2d_sw64(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer,
                               uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
+
+// Raises a kernel's limit of dynamic shared memory on the current device, once
+// per kernel and device: the runtime call costs more than the rest of a launch.
+// `done`: a static of the caller, one for each kernel, of one bit per device.
+inline cudaError_t allow_shared(const void *kernel, size_t bytes, const DeviceInfo &di,
+                                std::atomic<uint64_t> &done) {
+    const uint64_t bit = uint64_t(1) << di.device;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // ---- logits path (logits_logp.cu) ----
 cudaError_t launch_logits_logp(const uint16_t *logits, const int64_t *targets, const int32_t *cu,

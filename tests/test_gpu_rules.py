@@ -409,7 +409,9 @@ def test_offsets_past_32_bits(rk):
 
 def test_on_another_stream_and_in_a_graph(rk):
     c = rp.make_case(30, 20000, packed=True, requests=3, bias=2, mask="mixed", seed=31)
-    z, tg, rules = rp.cuda_case(rk, c)
+    z, tg, _ = rp.cuda_case(rk, c)
+    kw = {k: v.to(DEV) for k, v in c.kw.items()}
+    rules = rk.LogitsRules(**kw)
     g = torch.randn(30, device=DEV)
     logp, lse = rk.logp_from_logits_rules(z, tg, rules)
     x = rk.logits_rules_apply(z, rules)
@@ -432,11 +434,11 @@ def test_on_another_stream_and_in_a_graph(rk):
     # new logits, tokens, lengths and masks in the captured tensors
     c2 = rp.make_case(30, 20000, packed=True, requests=3, bias=2, mask="mixed", seed=32)
     z2, tg2, rules2 = rp.cuda_case(rk, c2)
-    n = min(rules._kept["tokens"].numel(), rules2._kept["tokens"].numel())
+    n = min(kw["tokens"].numel(), c2.kw["tokens"].numel())
     z.copy_(z2)
-    rules._kept["tokens"][:n] = rules2._kept["tokens"][:n]
-    rules._kept["mask"].copy_(rules2._kept["mask"])
-    rules._kept["row_length"] -= 1
+    kw["tokens"][:n] = c2.kw["tokens"][:n].to(DEV)
+    kw["mask"].copy_(c2.kw["mask"])
+    kw["row_length"] -= 1
     for _ in range(2):
         [o.fill_(NAN) for o in out]
         torch.cuda.synchronize()
@@ -457,6 +459,11 @@ def test_binding_refusals(rk):
                 dict(mask=kw["mask"].t().contiguous().t()), dict(mask=kw["mask"].cpu())):
         with pytest.raises((ValueError, TypeError)):
             rk.LogitsRules(**{**kw, **bad})
+    for half in (("tokens",), ("token_offsets",), ("prompt_lengths",), ("row_length",), ("row_mask",)):
+        with pytest.raises(ValueError):
+            rk.LogitsRules(**{k: kw.get(k, torch.zeros(4, dtype=torch.int32, device=DEV)) for k in half})
+    with pytest.raises(ValueError):
+        rk.LogitsRules(bias_ids=torch.zeros(4, dtype=torch.int64, device=DEV))
     lse, g = torch.zeros(4, device=DEV), torch.zeros(4, device=DEV)
     for call in (lambda: rk.logits_rules_apply(z[:3], rules), lambda: rk.logits_rules_apply(z.half(), rules),
                  lambda: rk.logits_rules_apply(z[:, ::2], rules),

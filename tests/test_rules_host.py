@@ -180,13 +180,3 @@ def test_binding_refuses_cpu_tensors(rk):
         rk.embedding(torch.zeros(3, dtype=torch.int64), torch.zeros(4, 8))
     with pytest.raises(ValueError, match="CUDA"):
         rk.embedding_bwd(torch.zeros(3, 8), torch.zeros(3, dtype=torch.int64), 4)
-
-
-@pytest.mark.parametrize("kw, word", [
-    (dict(tokens=1), "token_offsets"), (dict(token_offsets=1), "tokens"), (dict(prompt_lengths=1), "tokens"),
-    (dict(bias_ids=1), "bias"), (dict(bias_values=1, bias_offsets=1), "bias"), (dict(row_length=1), "tokens"),
-    (dict(row_mask=1), "mask"),
-])
-def test_binding_refuses_half_a_rule(rk, kw, word):
-    with pytest.raises(ValueError, match=word):
-        rk.LogitsRules(**{k: torch.zeros(1) for k in kw})
