@@ -679,24 +679,23 @@ class LogitsRules:
                 address.append(None)
                 continue
             if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
-                    and t.dim() == ndim and t.is_contiguous()):
+                    and t.is_contiguous()) or t.dim() != ndim:
                 _need(t, name, dtype, ndim)
             if device is None:
                 device = t.device
             elif t.device != device:
                 raise ValueError(f"{name} is on {t.device}, not on {device}")
             if extra is not None:
-                n = t.size(0) - extra
+                n = len(t)
                 if extra < 0:  # per row
-                    n = t.size(0)
-                    if rows is None:
+                    if n != rows:
+                        if rows is not None:
+                            raise ValueError(f"{name} does not fit {rows} rows")
                         rows = n
-                    elif n != rows:
-                        raise ValueError(f"{name} does not fit {rows} rows")
-                elif requests is None and n > 0:
-                    requests = n
-                elif n != requests:
-                    raise ValueError(f"{name} does not fit {requests or 'one or more'} requests")
+                elif n - extra != requests:
+                    if requests is not None or n <= extra:
+                        raise ValueError(f"{name} does not fit {requests or 'one or more'} requests")
+                    requests = n - extra
             # an empty list still has to be told from a missing one
             address.append(t.data_ptr() or _EMPTY)
         if (tokens is None) != (token_offsets is None):
@@ -763,6 +762,16 @@ def _matrix(t: torch.Tensor, name: str, shape=None, device=None):
     return code, ld
 
 
+def _result(out, dtype, shape, device):
+    """(matrix, type code, row stride) of a result: ``out`` if it is given, or a new one."""
+    if out is not None:
+        return out, *_matrix(out, "out", shape, device)
+    code = _TYPE_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"out must be bfloat16 or float32, got {dtype}")
+    return torch.empty(shape, dtype=dtype, device=device), code, shape[1]
+
+
 def _rules_for(rules: LogitsRules, T: int, V: int, device) -> None:
     if not isinstance(rules, LogitsRules):
         raise TypeError("rules must be a LogitsRules")
@@ -816,9 +825,7 @@ def logits_rules_apply(logits: torch.Tensor, rules: LogitsRules, *,
     T, V = logits.shape
     device = logits.device
     _rules_for(rules, T, V, device)
-    if out is None:
-        out = torch.empty((T, V), dtype=out_dtype, device=device)
-    out_code, out_ld = _matrix(out, "out", (T, V), device)
+    out, out_code, out_ld = _result(out, out_dtype, (T, V), device)
     _run("rk_logits_rules_apply", lib.rk_logits_rules_apply, device, stream, logits.data_ptr(), code,
          ld, rules.address, T, V, out.data_ptr(), out_code, out_ld)
     return out
@@ -873,9 +880,7 @@ def logp_from_logits_rules_bwd(logits: torch.Tensor, targets: torch.Tensor, rule
     _rules_for(rules, T, V, device)
     _vector(lse, "lse", T, device)
     _vector(grad_logp, "grad_logp", T, device)
-    if out is None:
-        out = torch.empty((T, V), dtype=out_dtype, device=device)
-    out_code, out_ld = _matrix(out, "out", (T, V), device)
+    out, out_code, out_ld = _result(out, out_dtype, (T, V), device)
     _run("rk_logp_from_logits_rules_bwd", lib.rk_logp_from_logits_rules_bwd, device, stream,
          logits.data_ptr(), code, ld, targets.data_ptr(), _ptr(cu), ns, rules.address, T, V,
          lse.data_ptr(), grad_logp.data_ptr(), out.data_ptr(), out_code, out_ld)
@@ -900,12 +905,11 @@ def embedding(ids: torch.Tensor, E: torch.Tensor, cu_seqlens: torch.Tensor | Non
     code = _dense(E, "E", None, None)
     V, H = E.shape
     device = E.device
-    _need(ids, "ids", torch.int64, 1)
-    T = ids.shape[0]
+    T = len(ids)
     cu, ns = _rows(ids, cu_seqlens, T, device)
-    if out is None:
-        out = torch.empty((T, H), dtype=out_dtype or E.dtype, device=device)
-    out_code = _dense(out, "out", (T, H), device)
+    if out is not None and not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    out, out_code, _ = _result(out, out_dtype or E.dtype, (T, H), device)
     _run("rk_embedding", lib.rk_embedding, device, stream, ids.data_ptr(), _ptr(cu), ns, E.data_ptr(),
          code, T, H, V, scale, out.data_ptr(), out_code)
     return out
@@ -941,7 +945,7 @@ def embedding_bwd(grad_out: torch.Tensor, ids: torch.Tensor, V: int,
         if accumulate:
             raise ValueError("accumulate needs a dE to add to")
         dE = torch.empty((V, H), dtype=torch.float32, device=device)
-    if _dense(dE, "dE", (V, H), device) != 1:
+    elif _dense(dE, "dE", (V, H), device) != 1:
         raise TypeError("dE must be float32")
     workspace = _scratch(workspace, lib.rk_embedding_bwd_workspace_size(n, H, V), device)
     _run("rk_embedding_bwd", lib.rk_embedding_bwd, device, stream, grad_out.data_ptr(), code,
