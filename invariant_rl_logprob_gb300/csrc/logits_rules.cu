@@ -50,7 +50,7 @@ constexpr int kLaneCols = 32;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSliceCols = kThreads * kLaneCols;  // 8192 columns per block
-constexpr int kMaxRun = 64;                    // rows per block at most
+constexpr int kMaxRun = 40;                    // rows per block at most
 constexpr int kMaxBiases = 65534;  // per request: indices are kept in 16 bits
 constexpr uint32_t kPromptBit = 0x80000000u;
 constexpr uint32_t kNegInf2 = 0xFF80FF80u;  // two bf16 -inf
@@ -150,7 +150,13 @@ struct Request {
     int32_t ntok, prompt;
     int64_t bias0;
     int32_t nbias;
-    bool ok;
+    int32_t ok;
+};
+
+// A row's, with how many of the tokens it has seen.
+struct RowRequest {
+    Request q;
+    int32_t id, len;
 };
 
 __device__ __forceinline__ bool in_range(float v) { return v >= 1e-6f && v <= 1e6f; }
@@ -192,26 +198,16 @@ __device__ __forceinline__ Request load_request(const rk_logits_rules &r, int32_
     return s;
 }
 
-// row.step of row t, given the row before.
-__device__ __forceinline__ void find_step(const rk_logits_rules &r, int64_t t, const RowInfo &before,
-                                          RowInfo &row, const Columns &own, int64_t slice0, int width) {
-    if (row.state != kOk || before.state != kOk) return;
-    const int32_t q = row_request(r, t);
-    if (q != row_request(r, t - 1)) return;
-    row.step = kNoToken;
-    if (r.num_requests == 0 || !r.tokens) return;
-    const int64_t a = r.token_offsets[q], b = r.token_offsets[q + 1];
-    if (!(a >= 0 && b >= a && b <= r.num_tokens && b - a < 0x7fffffff)) return;  // refused by load_request
-    const int32_t ntok = (int32_t)(b - a);
-    const int32_t len = min(row_length(r, t), ntok), was = min(row_length(r, t - 1), ntok);
-    if (len == was) return;
-    if (len != was + 1) {
-        row.step = kAnew;
-        return;
+// row.step, given the row before.
+__device__ __forceinline__ void find_step(const RowInfo &before, const RowRequest &rb, RowInfo &row,
+                                          const RowRequest &rr, const Columns &own, int64_t slice0, int width) {
+    if (row.state != kOk || before.state != kOk || rr.id != rb.id || !rr.q.ok) return;
+    if (rr.len == rb.len) {
+        row.step = kNoToken;
+    } else if (rr.len == rb.len + 1) {
+        const int64_t v = rr.q.tokens[rb.len], c = v - slice0;
+        row.step = v >= 0 && c >= 0 && c < width ? place(own, (int)c, rb.len < rr.q.prompt) : kNoToken;
     }
-    const int64_t v = r.tokens[a + was], c = v - slice0;
-    if (v >= 0 && c >= 0 && c < width)
-        row.step = place(own, (int)c, r.prompt_lengths && was < r.prompt_lengths[q]);
 }
 
 // y of a touched column from z, its count word and its bias.
@@ -382,20 +378,22 @@ struct Shared {
     uint16_t *list;     // [kWarps][1024]: each warp's touched columns, ascending
     uint16_t *bias;     // [kSliceCols], or null: 1 + the index of the column's bias, 0: none
     RowInfo *rows;      // [kMaxRun]
+    RowRequest *requests;  // [kMaxRun]
     unsigned char *rings;
 };
 constexpr int kWarpCols = 32 * kLaneCols;
 
 extern __shared__ uint4 rules_smem[];
 
-// Its layout: counts, touched words, rows, lists, bias indices if there are
-// biases, and then the warps' rings.
+// Its layout: counts, touched words, rows and their requests, lists, bias indices
+// if there are biases, and then the warps' rings.
 __device__ __forceinline__ Shared shared_view(bool has_bias) {
     Shared sh;
     sh.count = reinterpret_cast<uint32_t *>(rules_smem);
     sh.touched = sh.count + kSliceCols;
     sh.rows = reinterpret_cast<RowInfo *>(sh.touched + kThreads);
-    sh.list = reinterpret_cast<uint16_t *>(sh.rows + kMaxRun);
+    sh.requests = reinterpret_cast<RowRequest *>(sh.rows + kMaxRun);
+    sh.list = reinterpret_cast<uint16_t *>(sh.requests + kMaxRun);
     sh.bias = has_bias ? sh.list + kSliceCols : nullptr;
     sh.rings = reinterpret_cast<unsigned char *>(sh.list + (has_bias ? 2 : 1) * kSliceCols);
     return sh;
@@ -535,7 +533,7 @@ struct Config {
     static constexpr int kMaskAt = 32 * (kWider ? Lane<TOut>::kPitch : Lane<TIn>::kPitch);
     static constexpr int kStageBytes = kMaskAt + 32 * 4;
     static size_t smem(bool bias) {
-        return (size_t)(kSliceCols + kThreads) * 4 + kMaxRun * sizeof(RowInfo) +
+        return (size_t)(kSliceCols + kThreads) * 4 + kMaxRun * (sizeof(RowInfo) + sizeof(RowRequest)) +
                (size_t)kSliceCols * (bias ? 4 : 2) + (size_t)kWarps * kStages * kStageBytes;
     }
 };
@@ -592,8 +590,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t *my_word = sh.touched + (mine >> 5);
     uint16_t *list = sh.list + warp * kWarpCols;
 
-    for (int k = threadIdx.x; k < n; k += kThreads)
+    RowRequest *requests = sh.requests;
+    for (int k = threadIdx.x; k < n; k += kThreads) {
         rows[k] = row_info<OP>(io, rules, t0 + k, own, slice0, width);
+        if (rows[k].state == kOk) {
+            const int32_t id = row_request(rules, t0 + k);
+            const Request r = load_request(rules, id);
+            requests[k] = RowRequest{r, id, min(row_length(rules, t0 + k), r.ntok)};
+        }
+    }
     __syncthreads();
 
     const TIn *zslice = reinterpret_cast<const TIn *>(io.logits) + t0 * io.ld + slice0;
@@ -628,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     for (int k = 0; k < C::kStages; ++k) prefetch();
     for (int k = threadIdx.x + 1; k < n; k += kThreads)
-        find_step(rules, t0 + k, rows[k - 1], rows[k], own, slice0, width);
+        find_step(rows[k - 1], requests[k - 1], rows[k], requests[k], own, slice0, width);
     __syncthreads();
 
     int32_t cur = -1;
@@ -643,15 +648,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int k = 0; k < n;) {
         // The whole block: a request, or a step of more than one token.
         if (rows[k].state == kOk && rows[k].step == kAnew) {
-            const int32_t req = row_request(rules, t0 + k);
-            const bool other = req != cur;
-            if (other) {
-                cur = req;
-                q = load_request(rules, cur);
-            }
+            const bool other = requests[k].id != cur;
+            cur = requests[k].id;
+            q = requests[k].q;
             if (q.ok) {
-                const int32_t len = min(row_length(rules, t0 + k), q.ntok);
-                const int32_t counted = other ? 0 : min(row_length(rules, t0 + done), q.ntok);
+                const int32_t len = requests[k].len;
+                const int32_t counted = other ? 0 : requests[done].len;
                 const bool anew = other || len < counted;
                 if (anew) {
                     start_request(sh.bias != nullptr, rules.bias_ids + q.bias0, q.nbias, slice0, width);
@@ -1134,12 +1136,17 @@ void dependent(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, unsigned grid
     cfg->numAttrs = 1;
 }
 
-// Rows per block: one wave of two blocks per SM where kMaxRun allows it, so
-// that a block counts a history as seldom as possible.
+// Rows per block.  A long run counts a history seldom, a short one spreads the
+// blocks evenly over the SMs: as few waves of two blocks per SM as kMaxRun
+// allows, of equal runs.  kMaxRun at 24, 32, 40, 48, 64 (us): logp of 8192 rows
+// with long histories 549, 536, 525, 519, 526; bwd of 4096 rows 400, 404, 407,
+// 418, 419; 40 costs both little.  One wave with runs up to 64 and an uneven
+// last one: 526 and 424.
 int rows_per_block(int64_t T, int64_t V, const DeviceInfo &di) {
     const int64_t slices = (V + kSliceCols - 1) / kSliceCols, blocks = (int64_t)di.sm_count * 2;
-    const int64_t want = (T * slices + blocks - 1) / blocks;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxRun, want));
+    const int64_t waves = (T * slices + blocks * kMaxRun - 1) / (blocks * kMaxRun);
+    const int64_t want = (T * slices + blocks * waves - 1) / (blocks * waves);
+    return (int)std::max<int64_t>(1, want);
 }
 
 template <RulesOp OP, typename TIn, typename TOut, bool VEC>

@@ -178,6 +178,34 @@ def test_rows_do_not_depend_on_the_batch(rk):
         assert same_bits(lp, logp[t:t + 1]) and same_bits(ls, lse[t:t + 1])
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("ld", [9000, 9003])
+def test_touched_columns_that_lead(rk, dtype, ld):
+    # the largest logits are touched ones that the rules push down by a little or by a lot, at
+    # ordinary and at very low temperatures, one of them or a hundred: their raw terms must
+    # leave no trace in the sum
+    V, T = 9000, 24
+    c = rp.make_case(T, V, dtype=dtype, history=200, bias=1, mask="mixed", ld=ld, seed=77)
+    c.logits = c.logits.clone()
+    for t in range(T):
+        a, b = int(c.kw["token_offsets"][t]), int(c.kw["token_offsets"][t + 1])
+        hot = c.kw["tokens"][a:b].unique()[: 1 if t % 3 else 100]
+        c.logits[t, hot] += [12.0, 30.0, 90.0][t % 3]
+        c.kw["bias_ids"][t] = int(hot[0]) if len(hot) else 5
+        c.kw["bias_values"][t] = [-8.0, -100.0, -float("inf")][t // 3 % 3]
+        c.kw["temperature"][t] = [1.0, 0.7, 0.01, 50.0][t % 4]
+    z, tg, rules = rp.cuda_case(rk, c)
+    logp, lse = rk.logp_from_logits_rules(z, tg, rules)
+    for t in range(T):
+        x, _, size = rp.plain_row(c, t)
+        size = np.where(np.isfinite(size), size, 0.0)
+        ref = rp.plain_lse(x)
+        assert abs(float(lse[t]) - ref) <= rp.lse_bound(size, ref), t
+        k = int(c.targets[t])
+        if np.isfinite(x[k]):
+            assert abs(float(logp[t]) - (x[k] - ref)) <= rp.logp_bound(size, k, x[k] - ref, ref)
+
+
 def test_history_that_jumps_and_shrinks(rk):
     # rows of one request whose lengths grow by one, by many, stay, and go back
     c = rp.make_case(12, 5000, packed=True, requests=1, history=4000, bias=1, seed=5)
