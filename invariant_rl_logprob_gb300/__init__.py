@@ -762,14 +762,23 @@ def _matrix(t: torch.Tensor, name: str, shape=None, device=None):
     return code, ld
 
 
-def _result(out, dtype, shape, device):
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """New memory of the stream that the operator runs on: another stream's may still be
+    in use there, and would be handed out again while this one works on it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(out, dtype, shape, device, stream):
     """(matrix, type code, row stride) of a result: ``out`` if it is given, or a new one."""
     if out is not None:
         return out, *_matrix(out, "out", shape, device)
     code = _TYPE_CODES.get(dtype)
     if code is None:
         raise TypeError(f"out must be bfloat16 or float32, got {dtype}")
-    return torch.empty(shape, dtype=dtype, device=device), code, shape[1]
+    return _empty(shape, dtype, device, stream), code, shape[1]
 
 
 def _rules_for(rules: LogitsRules, T: int, V: int, device) -> None:
@@ -792,8 +801,12 @@ def _vector(t: torch.Tensor, name: str, T: int, device) -> None:
 
 def _run(what: str, fn, device, stream, *args) -> None:
     """Calls the library on ``device``, with the stream's handle behind ``args``."""
-    handle = stream.cuda_stream if stream is not None else \
-        torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    else:
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == device.index:
         st = fn(*args, handle)
     else:
@@ -803,9 +816,9 @@ def _run(what: str, fn, device, stream, *args) -> None:
         _check(st, what)
 
 
-def _scratch(workspace, need: int, device) -> torch.Tensor:
+def _scratch(workspace, need: int, device, stream) -> torch.Tensor:
     if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        return _empty(max(need, 1), torch.uint8, device, stream)
     _need(workspace, "workspace", torch.uint8, 1)
     if workspace.device != device:
         raise ValueError(f"workspace must be on {device}")
@@ -825,7 +838,7 @@ def logits_rules_apply(logits: torch.Tensor, rules: LogitsRules, *,
     T, V = logits.shape
     device = logits.device
     _rules_for(rules, T, V, device)
-    out, out_code, out_ld = _result(out, out_dtype, (T, V), device)
+    out, out_code, out_ld = _result(out, out_dtype, (T, V), device, stream)
     _run("rk_logits_rules_apply", lib.rk_logits_rules_apply, device, stream, logits.data_ptr(), code,
          ld, rules.address, T, V, out.data_ptr(), out_code, out_ld)
     return out
@@ -850,14 +863,15 @@ def logp_from_logits_rules(logits: torch.Tensor, targets: torch.Tensor, rules: L
     cu, ns = _rows(targets, cu_seqlens, T, device)
     _rules_for(rules, T, V, device)
     if out is None:
-        out = torch.empty(T, dtype=torch.float32, device=device)
+        out = _empty(T, torch.float32, device, stream)
     else:
         _vector(out, "out", T, device)
     if lse is None:
-        lse = torch.empty(T, dtype=torch.float32, device=device)
+        lse = _empty(T, torch.float32, device, stream)
     else:
         _vector(lse, "lse", T, device)
-    workspace = _scratch(workspace, lib.rk_logp_from_logits_rules_workspace_size(T, V), device)
+    workspace = _scratch(workspace, lib.rk_logp_from_logits_rules_workspace_size(T, V), device,
+                         stream)
     _run("rk_logp_from_logits_rules", lib.rk_logp_from_logits_rules, device, stream,
          logits.data_ptr(), code, ld, targets.data_ptr(), _ptr(cu), ns, rules.address, T, V,
          out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
@@ -880,7 +894,7 @@ def logp_from_logits_rules_bwd(logits: torch.Tensor, targets: torch.Tensor, rule
     _rules_for(rules, T, V, device)
     _vector(lse, "lse", T, device)
     _vector(grad_logp, "grad_logp", T, device)
-    out, out_code, out_ld = _result(out, out_dtype, (T, V), device)
+    out, out_code, out_ld = _result(out, out_dtype, (T, V), device, stream)
     _run("rk_logp_from_logits_rules_bwd", lib.rk_logp_from_logits_rules_bwd, device, stream,
          logits.data_ptr(), code, ld, targets.data_ptr(), _ptr(cu), ns, rules.address, T, V,
          lse.data_ptr(), grad_logp.data_ptr(), out.data_ptr(), out_code, out_ld)
@@ -909,7 +923,7 @@ def embedding(ids: torch.Tensor, E: torch.Tensor, cu_seqlens: torch.Tensor | Non
     cu, ns = _rows(ids, cu_seqlens, T, device)
     if out is not None and not out.is_contiguous():
         raise ValueError("out must be contiguous")
-    out, out_code, _ = _result(out, out_dtype or E.dtype, (T, H), device)
+    out, out_code, _ = _result(out, out_dtype or E.dtype, (T, H), device, stream)
     _run("rk_embedding", lib.rk_embedding, device, stream, ids.data_ptr(), _ptr(cu), ns, E.data_ptr(),
          code, T, H, V, scale, out.data_ptr(), out_code)
     return out
@@ -944,10 +958,10 @@ def embedding_bwd(grad_out: torch.Tensor, ids: torch.Tensor, V: int,
     if dE is None:
         if accumulate:
             raise ValueError("accumulate needs a dE to add to")
-        dE = torch.empty((V, H), dtype=torch.float32, device=device)
+        dE = _empty((V, H), torch.float32, device, stream)
     elif _dense(dE, "dE", (V, H), device) != 1:
         raise TypeError("dE must be float32")
-    workspace = _scratch(workspace, lib.rk_embedding_bwd_workspace_size(n, H, V), device)
+    workspace = _scratch(workspace, lib.rk_embedding_bwd_workspace_size(n, H, V), device, stream)
     _run("rk_embedding_bwd", lib.rk_embedding_bwd, device, stream, grad_out.data_ptr(), code,
          ids.data_ptr(), _ptr(cu), ns, T, H, V, scale, order, n, dE.data_ptr(), int(accumulate),
          workspace.data_ptr(), workspace.numel())

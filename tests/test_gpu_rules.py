@@ -477,6 +477,33 @@ def test_on_another_stream_and_in_a_graph(rk):
         assert all(same_bits(a, b) for a, b in zip(out, want))
 
 
+def test_memory_made_by_a_call_is_its_streams(rk):
+    """What a call on a side stream allocates does not come out of the current stream's
+    freed memory, which work on that stream may still be using."""
+    c = rp.make_case(6, 3000, seed=3)
+    z, tg, rules = rp.cuda_case(rk, c)
+    lse, g = torch.zeros(6, device=DEV), torch.zeros(6, device=DEV)
+    E = torch.randn(50, 64, device=DEV)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for call in (lambda s: rk.logits_rules_apply(z, rules, stream=s),
+                 lambda s: rk.logp_from_logits_rules(z, tg, rules, stream=s),
+                 lambda s: rk.logp_from_logits_rules_bwd(z, tg, rules, lse, g, stream=s),
+                 lambda s: rk.embedding(tg % 50, E, stream=s),
+                 lambda s: rk.embedding_bwd(E[:6], tg % 50, 50, stream=s)):
+        torch.cuda.empty_cache()
+        freed = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in (24, 512, 1024, 1 << 14, 72000, 1 << 18) * 4]
+        places = {f.data_ptr() for f in freed}
+        del freed
+        res = call(side)
+        res = res if isinstance(res, tuple) else (res,)
+        assert not places & {r.data_ptr() for r in res}
+        side.synchronize()
+        want = call(None)
+        want = want if isinstance(want, tuple) else (want,)
+        assert all(same_bits(a, b) for a, b in zip(res, want))
+
+
 def test_binding_refusals(rk):
     c = rp.make_case(4, 64, mask="half", seed=2)
     z, tg, rules = rp.cuda_case(rk, c)
