@@ -80,7 +80,8 @@ struct RulesIo {
     const int32_t *cu;
     int num_seqs;
     int64_t T, V;
-    int run;         // rows per block
+    int run0, run;   // rows per block, of the first slice and of the others
+    unsigned blocks0;  // the first slice's blocks
     const float *lse, *grad;  // kBwd
     void *out;       // kApply, kBwd
     int64_t ld_out;
@@ -179,7 +180,7 @@ __device__ __forceinline__ Request load_request(const rk_logits_rules &r, int32_
         if (a >= 0 && b >= a && b <= r.num_tokens && b - a < 0x7fffffff) {
             s.tokens = r.tokens + a;
             s.ntok = (int32_t)(b - a);
-            s.prompt = r.prompt_lengths ? r.prompt_lengths[q] : 0;
+            s.prompt = r.prompt_lengths ? max(r.prompt_lengths[q], 0) : 0;
         } else {
             s.ok = false;
         }
@@ -198,16 +199,15 @@ __device__ __forceinline__ Request load_request(const rk_logits_rules &r, int32_
     return s;
 }
 
-// row.step, given the row before.
-__device__ __forceinline__ void find_step(const RowInfo &before, const RowRequest &rb, RowInfo &row,
-                                          const RowRequest &rr, const Columns &own, int64_t slice0, int width) {
-    if (row.state != kOk || before.state != kOk || rr.id != rb.id || !rr.q.ok) return;
-    if (rr.len == rb.len) {
-        row.step = kNoToken;
-    } else if (rr.len == rb.len + 1) {
-        const int64_t v = rr.q.tokens[rb.len], c = v - slice0;
-        row.step = v >= 0 && c >= 0 && c < width ? place(own, (int)c, rb.len < rr.q.prompt) : kNoToken;
-    }
+// How a row's history differs from the row before: by the token *v, by none, or
+// else (RowInfo::step before the token is placed: >= 0, kNoToken, kAnew).
+__device__ __forceinline__ int32_t find_step(const RowInfo &before, const RowRequest &rb, const RowInfo &row,
+                                             const RowRequest &rr, int64_t *v) {
+    if (row.state != kOk || before.state != kOk || rr.id != rb.id || !rr.q.ok) return kAnew;
+    if (rr.len == rb.len) return kNoToken;
+    if (rr.len != rb.len + 1) return kAnew;
+    *v = rr.q.tokens[rb.len];
+    return 0;
 }
 
 // y of a touched column from z, its count word and its bias.
@@ -406,46 +406,70 @@ __device__ __forceinline__ void mark(const Shared &sh, int c) {
 // The functions below run seldom: out of line, and with plain arguments, so
 // that the row loop keeps its values in registers.
 
-// Block-wide: tokens [from, to) of a request into the counts of the columns
-// [slice0, slice0 + width).
-__device__ __noinline__ void count_tokens(const int64_t *tokens, int32_t prompt, int32_t from, int32_t to,
-                                          int64_t slice0, int width) {
-    const Shared sh = shared_view(false);
-    constexpr int kBatch = 8;  // loads in flight per thread
-    for (int32_t i0 = from + (int32_t)threadIdx.x; i0 < to; i0 += kBatch * kThreads) {
-        int64_t v[kBatch];
+// Tokens into the counts of the columns [slice0, slice0 + width): a thread's
+// N loads of v from i0 on, kThreads apart, and adding them.
+template <int N>
+__device__ __forceinline__ void load_tokens(int64_t (&v)[N], const int64_t *tokens, int32_t i0, int32_t to) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) v[k] = i0 + k * kThreads < to ? tokens[i0 + k * kThreads] : -1;
+    for (int k = 0; k < N; ++k) v[k] = k * kThreads < to - i0 ? tokens[i0 + k * kThreads] : -1;
+}
+template <int N>
+__device__ __forceinline__ void add_tokens(const Shared &sh, const int64_t (&v)[N], int32_t i0, int32_t prompt,
+                                           int64_t slice0, int width) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int64_t c = v[k] - slice0;
-            if (v[k] >= 0 && c >= 0 && c < width) {
-                if (i0 + k * kThreads < prompt)
-                    atomicOr(&sh.count[c], kPromptBit);
-                else
-                    atomicAdd(&sh.count[c], 1u);
-                mark(sh, (int)c);
-            }
+    for (int k = 0; k < N; ++k) {
+        const int64_t c = v[k] - slice0;
+        if (v[k] >= 0 && c >= 0 && c < width) {
+            if (k * kThreads < prompt - i0)
+                atomicOr(&sh.count[c], kPromptBit);
+            else
+                atomicAdd(&sh.count[c], 1u);
+            mark(sh, (int)c);
         }
     }
 }
+constexpr int kTokenBatch = 8;  // loads in flight per thread
 
-// Block-wide: nothing counted, the request's biases (`ids` null: none).  Of
-// biases for one column the last counts: the count words find it.
-__device__ __noinline__ void start_request(bool has_bias, const int64_t *ids, int32_t nbias, int64_t slice0,
-                                           int width) {
-    const Shared sh = shared_view(has_bias);
-    __syncthreads();
+// Block-wide: tokens [from, to) of a request into the counts.
+__device__ __noinline__ void count_tokens(const int64_t *tokens, int32_t prompt, int32_t from, int32_t to,
+                                          int64_t slice0, int width) {
+    const Shared sh = shared_view(false);
+    for (int64_t i0 = from + (int64_t)threadIdx.x; i0 < to; i0 += kTokenBatch * kThreads) {
+        int64_t v[kTokenBatch];
+        load_tokens(v, tokens, (int32_t)i0, to);
+        add_tokens(sh, v, (int32_t)i0, prompt, slice0, width);
+    }
+}
+
+__device__ __forceinline__ void clear_counts(const Shared &sh) {
     for (int k = threadIdx.x; k < kSliceCols / 4; k += kThreads)
         reinterpret_cast<uint4 *>(sh.count)[k] = make_uint4(0, 0, 0, 0);
     sh.touched[threadIdx.x] = 0;
-    if (has_bias)
+    if (sh.bias)
         for (int k = threadIdx.x; k < kSliceCols / 8; k += kThreads)
             reinterpret_cast<uint4 *>(sh.bias)[k] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+}
+
+// Block-wide: a request's biases (`ids`) and its first `len` tokens.  Of biases
+// for one column the last counts: the count words find it.  What memory held
+// before goes, unless it is `clear` already; the first loads are on their way
+// meanwhile.
+__device__ __noinline__ void count_request(bool has_bias, bool clear, const int64_t *ids, int32_t nbias,
+                                           const int64_t *tokens, int32_t prompt, int32_t len, int64_t slice0,
+                                           int width) {
+    const Shared sh = shared_view(has_bias);
+    const int32_t i0 = (int32_t)threadIdx.x;
+    const int64_t bias = i0 < nbias ? ids[i0] : -1;
+    int64_t first[kTokenBatch];
+    load_tokens(first, tokens, i0, len);
+    if (!clear) {
+        __syncthreads();
+        clear_counts(sh);
+        __syncthreads();
+    }
     if (nbias > 0) {
-        for (int k = threadIdx.x; k < nbias; k += kThreads) {
-            const int64_t v = ids[k], c = v - slice0;
+        for (int k = i0; k < nbias; k += kThreads) {
+            const int64_t v = k == i0 ? bias : ids[k], c = v - slice0;
             if (v >= 0 && c >= 0 && c < width) {
                 atomicMax(&sh.count[c], (uint32_t)(k + 1));
                 mark(sh, (int)c);
@@ -458,6 +482,11 @@ __device__ __noinline__ void start_request(bool has_bias, const int64_t *ids, in
             sh.count[c] = 0;
         }
         __syncthreads();
+    }
+    add_tokens(sh, first, i0, prompt, slice0, width);
+    for (int64_t i = i0 + (int64_t)kTokenBatch * kThreads; i < len; i += kTokenBatch * kThreads) {
+        load_tokens(first, tokens, (int32_t)i, len);
+        add_tokens(sh, first, (int32_t)i, prompt, slice0, width);
     }
 }
 
@@ -572,16 +601,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     RowInfo *rows = sh.rows;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned char *ring = sh.rings + warp * C::kStages * C::kStageBytes;
+    clear_counts(sh);
     // Launched with programmatic stream serialisation: wait until the previous
     // kernel of the stream has completed before reading or writing anything.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const int64_t slices = (io.V + kSliceCols - 1) / kSliceCols, slice = blockIdx.x % slices;
+    const int64_t slices = (io.V + kSliceCols - 1) / kSliceCols;
+    int64_t slice = 0, t0 = (int64_t)blockIdx.x * io.run0;  // the first slice's blocks come first
+    int run = io.run0;
+    if (blockIdx.x >= io.blocks0) {
+        const unsigned b = blockIdx.x - io.blocks0;
+        slice = 1 + b % (slices - 1);
+        t0 = b / (slices - 1) * io.run;
+        run = io.run;
+    }
     const int64_t slice0 = slice * kSliceCols;
     const int width = (int)min((int64_t)kSliceCols, io.V - slice0);
-    const int64_t t0 = (int64_t)(blockIdx.x / slices) * io.run;
-    const int n = (int)min((int64_t)io.run, io.T - t0);
+    const int n = (int)min((int64_t)run, io.T - t0);
     const int64_t words = (io.V + 31) / 32;
     const Columns own{slice == 0};
     const int mine = own.first(warp, lane);  // the lane's first column
@@ -589,17 +626,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         width >= mine + 32 ? 0xffffffffu : width > mine ? (1u << (width - mine)) - 1u : 0u;
     uint32_t *my_word = sh.touched + (mine >> 5);
     uint16_t *list = sh.list + warp * kWarpCols;
-
-    RowRequest *requests = sh.requests;
-    for (int k = threadIdx.x; k < n; k += kThreads) {
-        rows[k] = row_info<OP>(io, rules, t0 + k, own, slice0, width);
-        if (rows[k].state == kOk) {
-            const int32_t id = row_request(rules, t0 + k);
-            const Request r = load_request(rules, id);
-            requests[k] = RowRequest{r, id, min(row_length(rules, t0 + k), r.ntok)};
-        }
-    }
-    __syncthreads();
 
     const TIn *zslice = reinterpret_cast<const TIn *>(io.logits) + t0 * io.ld + slice0;
     TOut *oslice = OP == kLogp ? nullptr : reinterpret_cast<TOut *>(io.out) + t0 * io.ld_out + slice0;
@@ -613,61 +639,100 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto other_stage = [&](unsigned char *stage) { return both - (stage - ring); };
     const bool whole = width == kSliceCols;
     const int left = width - (VEC ? first_piece<TIn>(own, warp, lane) : 0);
-    auto prefetch = [&] {
+    auto copy_logits = [&] {
+        if constexpr (VEC)
+            copy_pieces(smem_u32(into) + first_piece_at<TIn>(lane), from, left, whole, own.mixed);
+        else
+            copy_words(into, from, width, own, warp, lane);
+    };
+    auto next_copy = [&] {
+        ++ahead;
+        from += io.ld;
+        into = other_stage(into);
+    };
+    auto prefetch = [&](bool logits) {
         if (ahead < n) {
             const int2 r = *reinterpret_cast<const int2 *>(&rows[ahead]);  // state, mrow
             if (r.x == kOk) {
-                if constexpr (VEC)
-                    copy_pieces(smem_u32(into) + first_piece_at<TIn>(lane), from, left, whole, own.mixed);
-                else
-                    copy_words(into, from, width, own, warp, lane);
+                if (logits) copy_logits();
                 if (r.y >= 0 && inside)
                     cp_async4(smem_u32(into + C::kMaskAt) + 4 * lane,
                               rules.mask + (int64_t)r.y * words + ((slice0 + mine) >> 5));
             }
         }
         cp_commit();
-        ++ahead;
-        from += io.ld;
-        into = other_stage(into);
+        next_copy();
     };
-    for (int k = 0; k < C::kStages; ++k) prefetch();
-    for (int k = threadIdx.x + 1; k < n; k += kThreads)
-        find_step(rows[k - 1], requests[k - 1], rows[k], requests[k], own, slice0, width);
+    // The first rows' logits are on their way before anything about the rows is known.
+    for (int k = 0; k < C::kStages; ++k) {
+        if (ahead < n) copy_logits();
+        next_copy();
+    }
+    ahead = 0;
+    from -= C::kStages * io.ld;
+    into = ring;
+
+    RowRequest *requests = sh.requests;
+    for (int k = threadIdx.x; k < n; k += kThreads) {
+        rows[k] = row_info<OP>(io, rules, t0 + k, own, slice0, width);
+        if (rows[k].state == kOk) {
+            const int32_t id = row_request(rules, t0 + k);
+            const Request r = load_request(rules, id);
+            requests[k] = RowRequest{r, id, min(row_length(rules, t0 + k), r.ntok)};
+        }
+    }
     __syncthreads();
+    for (int k = 0; k < C::kStages; ++k) prefetch(false);
 
     int32_t cur = -1;
-    int done = -1;  // the last row whose history is counted
+    int done = -1;      // the last row whose history is counted
+    bool clear = true;  // nothing counted yet
     uint32_t touched = 0;
     int listed = 0;  // touched columns of the warp
     Request q{};
+    // The whole block: row k's request, or a step of more than one token.
+    auto start_row = [&](int k) {
+        const bool other = requests[k].id != cur;
+        cur = requests[k].id;
+        q = requests[k].q;
+        if (!q.ok) return;
+        const int32_t len = requests[k].len;
+        const int32_t counted = other ? 0 : requests[done].len;
+        if (other || len < counted) {
+            count_request(sh.bias != nullptr, clear, rules.bias_ids + q.bias0, q.nbias, q.tokens, q.prompt, len,
+                          slice0, width);
+            clear = false;
+        } else {
+            __syncthreads();
+            *my_word = touched;
+            __syncthreads();
+            count_tokens(q.tokens, q.prompt, counted, len, slice0, width);
+        }
+        __syncthreads();
+        touched = *my_word;
+        listed = make_list(list, touched, mine, lane);
+    };
+    {
+        static_assert(kMaxRun <= kThreads);
+        const int k = (int)threadIdx.x;
+        int64_t v = -1;
+        int32_t step = kAnew;
+        if (k > 0 && k < n) step = find_step(rows[k - 1], requests[k - 1], rows[k], requests[k], &v);
+        if (rows[0].state == kOk) start_row(0);
+        if (step == 0) {
+            const int64_t c = v - slice0;
+            step = v >= 0 && c >= 0 && c < width ? place(own, (int)c, requests[k - 1].len < requests[k].q.prompt)
+                                                 : kNoToken;
+        }
+        if (k < n) rows[k].step = k > 0 ? step : kNoToken;  // row 0 is started
+        __syncthreads();
+    }
     // kBwd: lse and gradient of rows k & ~31 + lane
     float lse_of = 0.f, grad_of = 0.f;
     int held = -1;
     unsigned char *now = ring;  // row k's stage
     for (int k = 0; k < n;) {
-        // The whole block: a request, or a step of more than one token.
-        if (rows[k].state == kOk && rows[k].step == kAnew) {
-            const bool other = requests[k].id != cur;
-            cur = requests[k].id;
-            q = requests[k].q;
-            if (q.ok) {
-                const int32_t len = requests[k].len;
-                const int32_t counted = other ? 0 : requests[done].len;
-                const bool anew = other || len < counted;
-                if (anew) {
-                    start_request(sh.bias != nullptr, rules.bias_ids + q.bias0, q.nbias, slice0, width);
-                } else {
-                    __syncthreads();
-                    *my_word = touched;
-                    __syncthreads();
-                }
-                count_tokens(q.tokens, q.prompt, anew ? 0 : counted, len, slice0, width);
-                __syncthreads();
-                touched = *my_word;
-                listed = make_list(list, touched, mine, lane);
-            }
-        }
+        if (rows[k].state == kOk && rows[k].step == kAnew) start_row(k);
         // A row without a result, or without usable rules.
         if (rows[k].state != kOk || !q.ok) {
             const int32_t state = rows[k].state;
@@ -688,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             parts += slices * kWarps;
             oslice += io.ld_out;
             cp_wait<0>();
-            prefetch();
+            prefetch(true);
             now = other_stage(now);
             ++k;
             continue;
@@ -792,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int r = 0; r < R; ++r) load_pieces(w[r], stage[r], odd[r]);
             __syncwarp();  // the stages are free again
 #pragma unroll
-            for (int r = 0; r < R; ++r) prefetch();
+            for (int r = 0; r < R; ++r) prefetch(true);
             // the other columns: one maximum, then the terms relative to it
             float ref[R], rc[R], m[R];
             bool far = false;
@@ -1037,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 write_out<VEC>(stage, oslice, width, own, warp, lane);
                 oslice += io.ld_out;
                 __syncwarp();  // the stage is free again
-                prefetch();
+                prefetch(true);
                 now = other_stage(now);
             }
             done = k;
@@ -1140,13 +1205,28 @@ void dependent(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, unsigned grid
 // blocks evenly over the SMs: as few waves of two blocks per SM as kMaxRun
 // allows, of equal runs.  kMaxRun at 24, 32, 40, 48, 64 (us): logp of 8192 rows
 // with long histories 549, 536, 525, 519, 526; bwd of 4096 rows 400, 404, 407,
-// 418, 419; 40 costs both little.  One wave with runs up to 64 and an uneven
-// last one: 526 and 424.
-int rows_per_block(int64_t T, int64_t V, const DeviceInfo &di) {
-    const int64_t slices = (V + kSliceCols - 1) / kSliceCols, blocks = (int64_t)di.sm_count * 2;
-    const int64_t waves = (T * slices + blocks * kMaxRun - 1) / (blocks * kMaxRun);
-    const int64_t want = (T * slices + blocks * waves - 1) / (blocks * waves);
-    return (int)std::max<int64_t>(1, want);
+// 418, 419; 40 costs both little.
+//
+// The first slice has most of what a history touches, and a row takes up to
+// twice the time there.  Its blocks come first, so that the others even out the
+// end (logp of 8192 rows 525 us to 501); in a single wave nothing follows that
+// could, and their runs are shorter.  By nothing, 3/4, 2/3, 3/5, 1/2: 55, 50,
+// 47, 47, 49 us for 2048 x 32000, and no difference where runs are short.
+constexpr int kFirstNum = 3, kFirstDen = 5;
+void cut_rows(RulesIo &io, const rk_logits_rules &r, const DeviceInfo &di, int64_t *grid) {
+    const int64_t slices = (io.V + kSliceCols - 1) / kSliceCols, wave = (int64_t)di.sm_count * 2;
+    const int64_t waves = (io.T * slices + wave * kMaxRun - 1) / (wave * kMaxRun);
+    const bool shorter = slices > 1 && waves == 1 && r.tokens;
+    int64_t run = std::max<int64_t>(1, (io.T * slices + wave * waves - 1) / (wave * waves)), run0, blocks0;
+    for (;; ++run) {
+        run0 = shorter ? (run * kFirstNum + kFirstDen - 1) / kFirstDen : run;
+        blocks0 = (io.T + run0 - 1) / run0;
+        *grid = blocks0 + (slices - 1) * ((io.T + run - 1) / run);
+        if (run >= kMaxRun || *grid <= wave * waves) break;
+    }
+    io.run0 = (int)run0;
+    io.run = (int)run;
+    io.blocks0 = (unsigned)std::min<int64_t>(blocks0, 0x7fffffff);
 }
 
 template <RulesOp OP, typename TIn, typename TOut, bool VEC>
@@ -1156,9 +1236,8 @@ cudaError_t launch_rows(RulesIo io, const rk_logits_rules &r, const DeviceInfo &
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), C::smem(true), di, allowed);
     if (e != cudaSuccess) return e;
-    io.run = rows_per_block(io.T, io.V, di);
-    const int64_t slices = (io.V + kSliceCols - 1) / kSliceCols;
-    const int64_t blocks = slices * ((io.T + io.run - 1) / io.run);
+    int64_t blocks;
+    cut_rows(io, r, di, &blocks);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
