@@ -14,14 +14,17 @@
 // and the mask only.
 //
 // Data.  A warp copies its columns of the next row into shared memory of its
-// own (cp.async, 16 bytes a lane, or 4 where rows are not 16-byte aligned; the
-// mask words with them) while it works on the present one, so no barrier
-// stands between the rows.  What the rows say about themselves is read once
+// own (cp.async, 16 bytes a lane, the mask words with them) while it works on
+// the present one, so no barrier stands between the rows.  Rows that do not
+// start on 16-byte boundaries are copied from the boundary before them and
+// shifted on the way into registers (300 x 50257 without rules: logp
+// 23.5 us, fp32 gradient 31.0; 31.7 and 35.3 with 4-byte copies and single
+// columns written; 21.5 and 27.3 at 50264).  What the rows say about themselves is read once
 // per block.  Results of kApply and kBwd leave through the same memory, so
 // that a warp writes whole lines although a lane owns 32 columns.  Each lane's
 // 32 columns are followed by 16 bytes: they spread a quarter warp's 16-byte
-// accesses over all banks, and hold the end of a row that starts on an odd
-// element.
+// accesses over all banks, and hold the end of columns that do not start on a
+// 16-byte boundary.
 //
 // History.  The block counts a request's tokens of its slice in shared
 // memory (one word per column: bit 31 in the prompt, bits 0-30 times
@@ -276,6 +279,7 @@ struct Lane {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// its first `bytes`, zeros behind them
 __device__ __forceinline__ void cp_async16_part(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
@@ -289,11 +293,8 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Whether a row starts on an odd 2-byte element.
-__device__ __forceinline__ bool odd_start(const uint16_t *src) {
-    return (reinterpret_cast<uintptr_t>(src) & 2) != 0;
-}
-__device__ __forceinline__ bool odd_start(const float *) { return false; }
+// Bytes from the 16-byte boundary at or before p to p.
+__device__ __forceinline__ int shift_of(const void *p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15); }
 
 // Copies of a warp's columns of a row's slice into a stage.  Nothing outside
 // the slice (of `width` columns) is read.
@@ -329,44 +330,82 @@ __device__ __forceinline__ void copy_pieces(uint32_t dst, const T *from, int lef
     }
 }
 
-// Other rows (`src`: the slice's first element): 4 bytes at a time.  After an
-// odd start the columns sit one element further in.
+// Other rows (`src`: the slice's first element): every 64 columns (a pair of
+// lanes') as the pieces from the 16-byte boundary before them on, one more than
+// they fill, which goes behind the second lane's.  The columns sit
+// shift_of(src) bytes further in.  Of the first piece the bytes before the
+// columns belong to the columns or the row before; next to the tensor's first
+// element (`top`) they may not, and it is copied by element.
 template <typename T>
-__device__ __forceinline__ void copy_words(unsigned char *stage, const T *src, int width, const Columns &own,
-                                           int warp, int lane) {
+__device__ __forceinline__ void copy_shifted(unsigned char *stage, const T *src, int width, bool top,
+                                             const Columns &own, int warp, int lane) {
     using L = Lane<T>;
-    const uint32_t dst = smem_u32(stage);
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll 4
-        for (int o = 0; o < 32; ++o) {
-            const int c = own.first(warp, o) + lane;
-            if (c < width) cp_async4(dst + o * L::kPitch + 4 * lane, src + c);
+    constexpr int kSize = (int)sizeof(T);
+    const int shift = shift_of(src), end = shift + width * kSize;
+    const char *base = reinterpret_cast<const char *>(src) - shift;
+    const int first = first_piece<T>(own, warp, lane) * kSize, step = (own.mixed ? L::kMixedStep : L::kStep) * kSize;
+    const uint32_t dst = smem_u32(stage) + first_piece_at<T>(lane);
+#pragma unroll
+    for (int i = 0; i < L::kPieces; ++i) {
+        const int b = first + i * step, n = min(16, end - b);
+        if (top && shift > 0 && b == 0) {
+            for (int e = shift; e < n; e += kSize)
+                *reinterpret_cast<T *>(stage + e) = *reinterpret_cast<const T *>(base + e);
+        } else if (n > 0) {
+            cp_async16_part(dst + i * L::kLanes * L::kPitch, base + b, n);
         }
-    } else {
-        // words on 4-byte boundaries; one that reaches out of the slice is
-        // copied by element
-        const int odd = odd_start(src) ? 1 : 0, per = kLaneCols / 2 + odd;  // words of a lane's columns
-#pragma unroll 2
-        for (int x = lane; x < 32 * per; x += 32) {
-            const int o = odd ? x / (kLaneCols / 2 + 1) : x / (kLaneCols / 2), w = x - o * per;
-            const int c = own.first(warp, o) + 2 * w - odd;  // its first column
-            if (c >= 0 && c + 1 < width) {
-                cp_async4(dst + o * L::kPitch + 4 * w, src + c);
-            } else {
-                uint16_t *d = reinterpret_cast<uint16_t *>(stage + o * L::kPitch) + 2 * w;
-                if (c >= 0 && c < width) d[0] = src[c];
-                if (c + 1 < width) d[1] = src[c + 1];
-            }
-        }
+    }
+    if (shift > 0 && lane < 16) {
+        const int o = 2 * lane + 1, b = (own.first(warp, o) + kLaneCols) * kSize, n = min(16, end - b);
+        if (n > 0) cp_async16_part(smem_u32(stage) + o * L::kPitch + kLaneCols * kSize, base + b, n);
     }
 }
 
-// A 16-byte piece that sits one 2-byte element further in.
-__device__ __forceinline__ uint4 load_odd_piece(const unsigned char *p) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t b = *reinterpret_cast<const uint32_t *>(p + 16);
-    return make_uint4(__funnelshift_r(a.x, a.y, 16), __funnelshift_r(a.y, a.z, 16),
-                      __funnelshift_r(a.z, a.w, 16), __funnelshift_r(a.w, b, 16));
+// f(std::integral_constant<int, words>()), words = 0 .. 3 known at run time.
+template <typename F>
+__device__ __forceinline__ void with_words(int words, F f) {
+    switch (words) {
+    case 0: f(std::integral_constant<int, 0>{}); break;
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    default: f(std::integral_constant<int, 3>{}); break;
+    }
+}
+
+// A lane's columns out of what copy_shifted made.
+template <typename T>
+__device__ __forceinline__ void load_shifted(uint4 (&w)[Lane<T>::kPieces], const unsigned char *stage, int shift,
+                                             int lane) {
+    using L = Lane<T>;
+    uint32_t r[4 * L::kPieces + 4];
+    const unsigned char *p = stage + lane * L::kPitch;
+#pragma unroll
+    for (int i = 0; i <= L::kPieces; ++i) {
+        const int next = lane & 1 ? 0 : 16;  // the second lane's first piece
+        const uint4 v = *reinterpret_cast<const uint4 *>(p + 16 * i + (i == L::kPieces ? next : 0));
+        r[4 * i] = v.x;
+        r[4 * i + 1] = v.y;
+        r[4 * i + 2] = v.z;
+        r[4 * i + 3] = v.w;
+    }
+    const int bits = shift & 2 ? 16 : 0;
+    with_words(shift >> 2, [&](auto words) {
+        constexpr int S = decltype(words)::value;
+        auto word = [&](int i) {
+            return sizeof(T) == 2 ? __funnelshift_r(r[i + S], r[i + S + 1], bits) : r[i + S];
+        };
+#pragma unroll
+        for (int i = 0; i < L::kPieces; ++i)
+            w[i] = make_uint4(word(4 * i), word(4 * i + 1), word(4 * i + 2), word(4 * i + 3));
+    });
+}
+
+// Where column j of lane l is in such a stage.
+template <typename T>
+__device__ __forceinline__ T *shifted_at(unsigned char *stage, int shift, int l, int j) {
+    using L = Lane<T>;
+    const int o = (j & 63) * (int)sizeof(T) + shift;
+    return reinterpret_cast<T *>(stage + (l >> 1) * 2 * L::kPitch + o + (o >= kLaneCols * (int)sizeof(T) ? 16 : 0));
 }
 
 // ---- history ----
@@ -567,12 +606,30 @@ struct Config {
     }
 };
 
-// Writes a warp's results from its stage to the row's slice.
-template <bool VEC, typename T>
-__device__ __forceinline__ void write_out(const unsigned char *stage, T *dst, int width, const Columns &own,
-                                          int warp, int lane) {
+// Writes a warp's results from its stage to the row's slice, of `width` columns.
+template <typename T>
+__device__ __forceinline__ void write_part(T *to, const uint4 &v, int n) {  // n of a piece's columns
+    if (n >= Lane<T>::kCols) {
+        *reinterpret_cast<uint4 *>(to) = v;
+    } else if (n > 0) {
+        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < Lane<T>::kCols; ++j)
+            if (j < n) {
+                if constexpr (sizeof(T) == 4)
+                    to[j] = __uint_as_float(q[j]);
+                else
+                    to[j] = (uint16_t)(q[j >> 1] >> (16 * (j & 1)));
+            }
+    }
+}
+
+// dst on a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ void write_pieces(const unsigned char *stage, T *dst, int width, const Columns &own,
+                                             int warp, int lane) {
     using L = Lane<T>;
-    if (VEC && width == kSliceCols) {
+    if (width == kSliceCols) {
         const int o = lane / L::kPieces, part = lane % L::kPieces;
         const unsigned char *from = stage + o * L::kPitch + 16 * part;
         T *to = dst + own.first(warp, o) + part * L::kCols;
@@ -584,8 +641,45 @@ __device__ __forceinline__ void write_out(const unsigned char *stage, T *dst, in
     } else {
 #pragma unroll 4
         for (int o = 0; o < 32; ++o) {
-            const int c = own.first(warp, o) + lane;
-            if (c < width) dst[c] = reinterpret_cast<const T *>(stage + o * L::kPitch)[lane];
+            const int j = own.first(warp, o) + lane;
+            if (j < width) dst[j] = reinterpret_cast<const T *>(stage + o * L::kPitch)[lane];
+        }
+    }
+}
+
+// Elsewhere.  Every 64 columns: the pieces that start on boundaries, and the
+// columns before and behind them one by one.
+template <typename T>
+__device__ __forceinline__ void write_shifted(const unsigned char *stage, T *dst, int width, const Columns &own,
+                                              int warp, int lane) {
+    using L = Lane<T>;
+    constexpr int kSize = (int)sizeof(T), kPair = 2 * L::kPieces;  // pieces of 64 columns
+    const int head = (16 - shift_of(dst)) / kSize % L::kCols;      // columns before the first piece
+    const int bits = head * kSize & 2 ? 16 : 0;
+    with_words(head * kSize >> 2, [&](auto words) {
+        constexpr int S = decltype(words)::value;
+#pragma unroll
+        for (int i = 0; i < L::kPieces; ++i) {
+            const int x = lane + 32 * i, pair = x / kPair, p = x % kPair, q = head + p * L::kCols;
+            if (q + L::kCols > 64) continue;
+            const unsigned char *from = stage + 2 * pair * L::kPitch;
+            const uint4 a = *reinterpret_cast<const uint4 *>(from + 16 * p + (p >= L::kPieces ? 16 : 0));
+            const uint4 b = *reinterpret_cast<const uint4 *>(from + 16 * p + (p + 1 >= L::kPieces ? 32 : 16));
+            const uint32_t r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            auto word = [&](int k) {
+                return kSize == 2 ? __funnelshift_r(r[k + S], r[k + S + 1], bits) : r[k + S];
+            };
+            const int c = own.first(warp, 2 * pair) + q;
+            write_part(dst + c, make_uint4(word(0), word(1), word(2), word(3)), width - c);
+        }
+    });
+    if (head > 0) {
+#pragma unroll
+        for (int i = 0; i < L::kCols / 2; ++i) {
+            const int x = lane + 32 * i, pair = x / L::kCols, e = x % L::kCols;
+            const int q = e < head ? e : 64 - L::kCols + e, o = 2 * pair + (q >> 5);
+            const int c = own.first(warp, o) + (q & 31);
+            if (c < width) dst[c] = reinterpret_cast<const T *>(stage + o * L::kPitch)[q & 31];
         }
     }
 }
@@ -643,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if constexpr (VEC)
             copy_pieces(smem_u32(into) + first_piece_at<TIn>(lane), from, left, whole, own.mixed);
         else
-            copy_words(into, from, width, own, warp, lane);
+            copy_shifted(into, from, width, slice == 0 && (t0 + ahead) * io.ld < 16 / (int)sizeof(TIn), own, warp, lane);
     };
     auto next_copy = [&] {
         ++ahead;
@@ -762,8 +856,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float c = __fmul_rn(kLog2e, q.itau);
         // Single columns: a column's logit in a stage, a touched one's y from its
         // logit, and whether the mask allows a column.
-        auto at = [&](unsigned char *stage, int odd, int j) {
-            return reinterpret_cast<TIn *>(stage + own.lane(j) * L::kPitch) + (j & 31) + odd;
+        auto at = [&](unsigned char *stage, int shift, int j) {
+            if constexpr (VEC)
+                return reinterpret_cast<TIn *>(stage + own.lane(j) * L::kPitch) + (j & 31);
+            else
+                return shifted_at<TIn>(stage, shift, own.lane(j), j);
         };
         auto touched_y = [&](int j, float z) {
             const int bi = sh.bias ? sh.bias[j] : 0;
@@ -772,11 +869,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         auto allowed = [&](const unsigned char *stage, int mrow, int j) {
             return mrow < 0 || (reinterpret_cast<const uint32_t *>(stage + C::kMaskAt)[own.lane(j)] >> (j & 31) & 1u);
         };
-        auto load_pieces = [&](uint4 (&w)[L::kPieces], const unsigned char *stage, int odd) {
+        auto load_pieces = [&](uint4 (&w)[L::kPieces], const unsigned char *stage, int shift) {
+            if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < L::kPieces; ++i)
-                w[i] = VEC || !odd ? *reinterpret_cast<const uint4 *>(stage + lane * L::kPitch + 16 * i)
-                                   : load_odd_piece(stage + lane * L::kPitch + 16 * i);
+                for (int i = 0; i < L::kPieces; ++i)
+                    w[i] = *reinterpret_cast<const uint4 *>(stage + lane * L::kPitch + 16 * i);
+            } else {
+                load_shifted<TIn>(w, stage, shift, lane);
+            }
         };
 
         // kLogp of rows k .. k + R - 1, whose histories are the same here.  Two
@@ -784,13 +884,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         auto score = [&](auto rows_at_once) {
             constexpr int R = decltype(rows_at_once)::value;
             unsigned char *stage[R];
-            int odd[R];
+            int shift[R];
             RowInfo row[R];
             uint32_t live[R];  // columns the mask allows
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 stage[r] = r == 0 ? now : other_stage(now);
-                odd[r] = VEC ? 0 : odd_start(zslice + (k + r) * io.ld);
+                shift[r] = VEC ? 0 : shift_of(zslice + (k + r) * io.ld);
                 row[r] = rows[k + r];
                 live[r] = inside;
                 if (row[r].mrow >= 0)
@@ -800,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (own.lane(j) == lane) {
                         float y = -INFINITY;
                         if (live[r] >> (j & 31) & 1u) {
-                            y = elem(at(stage[r], odd[r], j));
+                            y = elem(at(stage[r], shift[r], j));
                             if (touched >> (j & 31) & 1u) y = touched_y(j, y);
                         }
                         io.ytgt[t0 + k + r] = y;
@@ -822,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const int j = list[lane];
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
-                        TIn *zj = at(stage[r], odd[r], j);
+                        TIn *zj = at(stage[r], shift[r], j);
                         if (allowed(stage[r], row[r].mrow, j)) y0[r] = touched_y(j, elem(zj));
                         put(zj, -INFINITY);
                     }
@@ -836,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                             y[u] = -INFINITY;
                             if (e0 + 32 * u < listed) {
                                 const int j = list[e0 + 32 * u];
-                                TIn *zj = at(stage[r], odd[r], j);
+                                TIn *zj = at(stage[r], shift[r], j);
                                 if (allowed(stage[r], row[r].mrow, j)) y[u] = touched_y(j, elem(zj));
                                 put(zj, -INFINITY);
                             }
@@ -854,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             uint4 w[R][L::kPieces];
 #pragma unroll
-            for (int r = 0; r < R; ++r) load_pieces(w[r], stage[r], odd[r]);
+            for (int r = 0; r < R; ++r) load_pieces(w[r], stage[r], shift[r]);
             __syncwarp();  // the stages are free again
 #pragma unroll
             for (int r = 0; r < R; ++r) prefetch(true);
@@ -972,11 +1072,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 unsigned char *stage = now;
                 const RowInfo row = rows[k];
                 const TIn *zrow = zslice + k * io.ld;
-                const int odd = VEC ? 0 : odd_start(zrow);
+                const int shift = VEC ? 0 : shift_of(zrow);
                 uint32_t live = inside;  // columns the mask allows
                 if (row.mrow >= 0) live &= reinterpret_cast<const uint32_t *>(stage + C::kMaskAt)[lane];
                 uint4 w[L::kPieces];
-                load_pieces(w, stage, odd);
+                load_pieces(w, stage, shift);
                 // the list's first 32 columns, one to a lane
                 int c0 = -1;
                 float z0 = 0.f, y0 = 0.f;
@@ -984,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (listed > 0 && lane < listed) {
                     c0 = list[lane];
                     if (allowed(stage, row.mrow, c0)) {
-                        z0 = elem(at(stage, odd, c0));
+                        z0 = elem(at(stage, shift, c0));
                         cw0 = sh.count[c0];
                         y0 = touched_y(c0, z0);
                     } else {
@@ -994,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // the target, if it is one of this warp's columns
                 const bool has_target = OP == kBwd && row.target >= 0 && place_warp(row.target) == warp;
                 const int tcol = place_column(row.target);
-                const float zt = has_target && own.lane(tcol) == lane ? elem(at(stage, odd, tcol)) : 0.f;
+                const float zt = has_target && own.lane(tcol) == lane ? elem(at(stage, shift, tcol)) : 0.f;
                 if (OP == kBwd && k >> 5 != held) {
                     held = k >> 5;
                     const int64_t t = t0 + (held * 32 + lane);
@@ -1099,7 +1199,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     __syncwarp();
                 }
-                write_out<VEC>(stage, oslice, width, own, warp, lane);
+                if constexpr (VEC)
+                    write_pieces(stage, oslice, width, own, warp, lane);
+                else
+                    write_shifted(stage, oslice, width, own, warp, lane);
                 oslice += io.ld_out;
                 __syncwarp();  // the stage is free again
                 prefetch(true);

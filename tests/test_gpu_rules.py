@@ -145,6 +145,53 @@ def test_address_and_stride_change_no_bit(rk, dtype, ld, shift):
         assert bool((buf[~inside] == 7.0).all())
 
 
+@pytest.mark.parametrize("shift", range(8))
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_every_alignment_of_both_kinds_of_slice(rk, dtype, shift):
+    # columns of a slice that is spread over the warps, of a whole one that is not, and of a partial one
+    V, ld, n = 2 * 8192 + 77, 2 * 8192 + 80, 20
+    c = rp.make_case(n, V, dtype=dtype, ld=ld, packed=True, requests=2, bias=2, mask="mixed", history=60, seed=40 + shift)
+    c.logits[3, :8300] = -INF
+    c.logits[4, 8100:] = torch.finfo(dtype).min
+    aligned, tg, rules = rp.cuda_case(rk, c, 0)
+    z, _, _ = rp.cuda_case(rk, c, shift)
+    assert same_bits(z, aligned)
+    g = torch.randn(n, device=DEV)
+    logp, lse = rk.logp_from_logits_rules(aligned, tg, rules)
+    got = rk.logp_from_logits_rules(z, tg, rules)
+    assert same_bits(got[0], logp) and same_bits(got[1], lse)
+    for d in (FP32, BF16):
+        want = (rk.logits_rules_apply(aligned, rules, out_dtype=d),
+                rk.logp_from_logits_rules_bwd(aligned, tg, rules, lse, g, out_dtype=d))
+        for to in (shift, 0, 5):
+            buf = torch.full((n * (ld + 3) + 8,), 7.0, dtype=d, device=DEV)
+            out = buf.as_strided((n, V), (ld + 3, 1), storage_offset=to)
+            inside = torch.zeros_like(buf, dtype=torch.bool)
+            inside.as_strided((n, V), (ld + 3, 1), storage_offset=to).fill_(True)
+            rk.logits_rules_apply(z, rules, out=out)
+            assert same_bits(out, want[0])
+            rk.logp_from_logits_rules_bwd(z, tg, rules, lse, g, out=out)
+            assert same_bits(out, want[1])
+            assert bool((buf[~inside] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_a_narrow_matrix_at_its_buffers_first_element(rk, dtype):
+    # rows of a few bytes: what lies before the tensor is NaN and is not taken for a logit
+    for V in (1, 2, 3, 5, 7):
+        for shift in range(1, 8):
+            buf = torch.full((9 * V + 24,), NAN, dtype=dtype, device=DEV)
+            z = buf[shift:shift + 9 * V].view(9, V)
+            z.copy_(torch.randn(9, V))
+            base = z.clone()
+            rules = rk.LogitsRules(temperature=torch.full((1,), 0.7, device=DEV),
+                                   row_request=torch.zeros(9, dtype=torch.int32, device=DEV))
+            assert same_bits(rk.logits_rules_apply(z, rules), rk.logits_rules_apply(base, rules))
+            tg = torch.full((9,), V - 1, device=DEV)
+            a, b = rk.logp_from_logits_rules(z, tg, rules), rk.logp_from_logits_rules(base, tg, rules)
+            assert same_bits(a[0], b[0]) and same_bits(a[1], b[1]) and bool(a[0].isfinite().all())
+
+
 def test_rows_do_not_depend_on_the_batch(rk):
     # a packed batch of prefixes: each row again alone, as a request of its own, and permuted
     c = rp.make_case(260, 9001, packed=True, requests=3, bias=2, mask="mixed", history=40, seed=21)
