@@ -673,7 +673,7 @@ class LogitsRules:
         kept = (temperature, repetition, frequency, presence, tokens, token_offsets, prompt_lengths,
                 bias_ids, bias_values, bias_offsets, mask, row_request, row_length, row_mask)
         address = []
-        device = requests = rows = None
+        device = index = requests = rows = None
         for t, (name, dtype, ndim, extra) in zip(kept, _RULES):
             if t is None:
                 address.append(None)
@@ -681,12 +681,12 @@ class LogitsRules:
             if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
                     and t.is_contiguous()) or t.dim() != ndim:
                 _need(t, name, dtype, ndim)
-            if device is None:
-                device = t.device
-            elif t.device != device:
+            if index is None:
+                device, index = t.device, t.get_device()
+            elif t.get_device() != index:
                 raise ValueError(f"{name} is on {t.device}, not on {device}")
             if extra is not None:
-                n = len(t)
+                n = t.numel()  # one dimension
                 if extra < 0:  # per row
                     if n != rows:
                         if rows is not None:
@@ -807,7 +807,7 @@ def _run(what: str, fn, device, stream, *args) -> None:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -919,7 +919,7 @@ def embedding(ids: torch.Tensor, E: torch.Tensor, cu_seqlens: torch.Tensor | Non
     code = _dense(E, "E", None, None)
     V, H = E.shape
     device = E.device
-    T = len(ids)
+    T = ids.shape[0] if isinstance(ids, torch.Tensor) and ids.dim() == 1 else 0
     cu, ns = _rows(ids, cu_seqlens, T, device)
     if out is not None and not out.is_contiguous():
         raise ValueError("out must be contiguous")

@@ -137,6 +137,7 @@ constexpr int kMaxDigitBits = 9;
 constexpr int kMaxBins = 1 << kMaxDigitBits;
 constexpr int kInlineScanTiles = 64;  // up to here each block scans the counts itself
 constexpr int kTinyThreads = 128, kSmallThreads = 1024;         // blocks that sort alone
+constexpr int kTinySort = kTinyThreads * kSortItems;            // 1024
 constexpr int kSmallSort = kSmallThreads * kSortItems;          // 8192
 constexpr int kPiece = 32;       // occurrences of an id summed by one warp
 constexpr int kHalf = kPiece / 2;
@@ -446,15 +447,36 @@ struct SmallSort {
     int joins;
 };
 
+// Block `block` of THREADS * kZeroVectors * 16 bytes of zeros in dE, of n1 floats,
+// the first 4 n4 as vectors.
+constexpr int kZeroVectors = 4;
+template <int THREADS>
+__device__ __forceinline__ void zero_share(float *dE, int64_t n4, int64_t n1, int64_t block) {
+    const int64_t first = block * THREADS * kZeroVectors + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kZeroVectors; ++k) {
+        const int64_t i = first + k * THREADS;
+        if (i < n4)
+            reinterpret_cast<float4 *>(dE)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        else if (4 * n4 + (i - n4) < n1)  // unaligned, or what is left
+            dE[4 * n4 + (i - n4)] = 0.f;
+    }
+}
+
+// The blocks behind the first write zeros over dE (n1 floats).
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
     emb_sort_small(const __grid_constant__ Canonical c, int passes, int digit, int32_t *key, int32_t *val,
-                   Piece *pieces, Piece *joins, int32_t *counters) {
+                   Piece *pieces, Piece *joins, int32_t *counters, float *dE, int64_t n4, int64_t n1) {
     constexpr int kWarps = THREADS / 32;
     constexpr int kPer = kMaxBins > THREADS ? kMaxBins / THREADS : 1;  // digits of a thread
     extern __shared__ uint4 raw[];
     SmallSort<THREADS> &s = *reinterpret_cast<SmallSort<THREADS> *>(raw);
     wait_prior_grid();
+    if (blockIdx.x > 0) {
+        zero_share<THREADS>(dE, n4, n1, (int64_t)blockIdx.x - 1);
+        return;
+    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = (int)c.n, base = warp * 32 * kSortItems, bins = 1 << digit;
     if (threadIdx.x == 0) s.joins = 0;
@@ -546,21 +568,12 @@ __global__ void __launch_bounds__(THREADS)
 // and 332 to 342 us in resident blocks that loop, whose warps drift apart.
 
 constexpr int kZeroThreads = 256;
-constexpr int kZeroVectors = 4;  // per thread
 
 // All of dE, beside the one block that sorts.  That block lets this grid start
 // once the work before it is complete; the last block here waits for the sort,
 // so that whoever waits for this grid has waited for both.
 __global__ void __launch_bounds__(kZeroThreads) emb_zero_all(float *dE, int64_t n4, int64_t n1) {
-    const int64_t first = (int64_t)blockIdx.x * kZeroThreads * kZeroVectors + threadIdx.x;
-#pragma unroll
-    for (int k = 0; k < kZeroVectors; ++k) {
-        const int64_t i = first + k * kZeroThreads;
-        if (i < n4)
-            reinterpret_cast<float4 *>(dE)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        else if (4 * n4 + (i - n4) < n1)  // unaligned, or what is left
-            dE[4 * n4 + (i - n4)] = 0.f;
-    }
+    zero_share<kZeroThreads>(dE, n4, n1, blockIdx.x);
     if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
@@ -595,7 +608,7 @@ __global__ void __launch_bounds__(kAbsentThreads)
 
 constexpr int kSumThreads = 128;
 constexpr int kSumWarps = kSumThreads / 32;
-constexpr int kSumBlocks = 6;  // per SM
+constexpr int kSumBlocks = 5;  // per SM
 constexpr int kLaneCols = 16;
 constexpr int kSumCols = 32 * kLaneCols;  // columns of a warp: 512
 
@@ -603,7 +616,7 @@ constexpr int kSumCols = 32 * kLaneCols;  // columns of a warp: 512
 // column 8 (lane + 32 k)), or 16 single ones (k at lane + 32 k).
 template <bool VEC>
 struct Cols {
-    static constexpr int kN = VEC ? 2 : kLaneCols, kW = VEC ? 8 : 1;
+    static constexpr int kN = VEC ? 2 : kLaneCols;
     static __device__ __forceinline__ int at(int lane, int k) { return VEC ? 8 * (lane + 32 * k) : lane + 32 * k; }
 };
 
@@ -651,14 +664,37 @@ __global__ void __launch_bounds__(kSumThreads, VEC ? kSumBlocks : 3)
     wait_prior_grid();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t ncb = (H + kSumCols - 1) / kSumCols;
-    const int64_t units = (int64_t)counters[0] * ncb, step = (int64_t)gridDim.x * kSumWarps;
-    int64_t u = (int64_t)blockIdx.x * kSumWarps + warp;
-    Piece next = u < units ? pieces[u / ncb] : Piece{};
-    for (; u < units; u += step) {
+    const unsigned count = (unsigned)counters[0], blocks = (unsigned)ncb;
+    const unsigned u = blockIdx.x * kSumWarps + warp, step = gridDim.x * kSumWarps;
+    // Unit u: piece u / ncb, columns from u % ncb * kSumCols on.  A unit's piece is
+    // read two units ahead and its rows one ahead (kPiece == 32).
+    const unsigned at_step = step / blocks, cb_step = step % blocks;
+    unsigned at = u / blocks, cb = u % blocks;
+    auto advance = [&](unsigned &a, unsigned &b) {
+        a += at_step;
+        b += cb_step;
+        if (b >= blocks) {
+            b -= blocks;
+            ++a;
+        }
+    };
+    unsigned at2 = at, cb2 = cb;  // two units ahead, in the end
+    auto piece_ahead = [&] {
+        const Piece p = at2 < count ? pieces[at2] : Piece{};
+        advance(at2, cb2);
+        return p;
+    };
+    auto rows_of = [&](const Piece &p) { return lane < p.len ? val[p.pos + lane] : 0; };
+    Piece next = piece_ahead();
+    int next_row = rows_of(next);
+    Piece after = piece_ahead();
+    for (; at < count; advance(at, cb)) {
         const Piece p = next;
-        const int row = lane < p.len ? val[p.pos + lane] : 0;  // kPiece == 32
-        if (u + step < units) next = pieces[(u + step) / ncb];
-        const int64_t c0 = (u % ncb) * kSumCols, cols = H - c0;
+        const int row = next_row;
+        next = after;
+        next_row = rows_of(next);
+        after = piece_ahead();
+        const int64_t c0 = (int64_t)cb * kSumCols, cols = H - c0;
         const T *src = dout + c0;
         const bool last = p.slot < 0;
         float *dst = (last ? dE + (int64_t)p.id * H : partial + (int64_t)p.slot * H) + c0;
@@ -760,27 +796,32 @@ BwdBuffers carve(void *base, int64_t n, int64_t H) {
 }
 
 template <int THREADS>
-cudaError_t launch_small(const Canonical &c, const BwdBuffers &b, int passes, int digit, const DeviceInfo &di,
-                         cudaStream_t st) {
+cudaError_t launch_small(const Canonical &c, const BwdBuffers &b, int passes, int digit, float *dE,
+                         int64_t zeros, const DeviceInfo &di, cudaStream_t st) {
     constexpr size_t smem = sizeof(SmallSort<THREADS>);
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e =
         allow_shared(reinterpret_cast<const void *>(emb_sort_small<THREADS>), smem, di, allowed);
     if (e != cudaSuccess) return e;
-    return launch_dependent_smem(emb_sort_small<THREADS>, 1, THREADS, smem, st, c, passes, digit, b.key[0],
-                                 b.val[0], b.pieces, b.joins, b.counters);
+    const int64_t n4 = aligned(dE, 16) ? zeros / 4 : 0, per = THREADS * kZeroVectors;
+    const int64_t blocks = (n4 + (zeros - 4 * n4) + per - 1) / per;
+    if (blocks >= 0x7fffffff) return cudaErrorInvalidConfiguration;
+    return launch_dependent_smem(emb_sort_small<THREADS>, 1 + blocks, THREADS, smem, st, c, passes, digit,
+                                 b.key[0], b.val[0], b.pieces, b.joins, b.counters, dE, n4, zeros);
 }
 
 // Sorts the canonical tokens and finds their pieces; *where: which of the two
-// buffers holds the sorted keys and rows.
-cudaError_t launch_sort(const Canonical &c, const BwdBuffers &b, int *where, const DeviceInfo &di,
-                        cudaStream_t st) {
+// buffers holds the sorted keys and rows.  Zeros over dE's first `zeros` floats,
+// if there are any, come along with a sort of up to kTinyThreads * kSortItems
+// tokens.
+cudaError_t launch_sort(const Canonical &c, const BwdBuffers &b, int *where, float *dE, int64_t zeros,
+                        const DeviceInfo &di, cudaStream_t st) {
     const int bits = key_bits(c.V);
     const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
     const int digit = (bits + passes - 1) / passes;
     *where = 0;
-    if (c.n <= kSortItems * kTinyThreads) return launch_small<kTinyThreads>(c, b, passes, digit, di, st);
-    if (c.n <= kSmallSort) return launch_small<kSmallThreads>(c, b, passes, digit, di, st);
+    if (c.n <= kTinySort) return launch_small<kTinyThreads>(c, b, passes, digit, dE, zeros, di, st);
+    if (c.n <= kSmallSort) return launch_small<kSmallThreads>(c, b, passes, digit, dE, 0, di, st);
     const int64_t tiles = (c.n + kSortTile - 1) / kSortTile, pitch = tile_pitch(c.n);
     const int bins = 1 << digit;
     cudaError_t e = launch_dependent(emb_keys, tiles, kSortThreads, st, c, b.key[0], b.val[0], bins, b.hist,
@@ -854,20 +895,23 @@ cudaError_t launch_embedding_bwd(const void *dout, rk_dtype dout_type, const int
         return accumulate ? cudaSuccess : cudaMemsetAsync(dE, 0, (size_t)V * (size_t)H * 4, st);
     const BwdBuffers b = carve(workspace, n, H);
     const Canonical c{ids, cu, num_seqs, T, V, order, n, di.err};
-    int where;
-    cudaError_t e = launch_sort(c, b, &where, di, st);
-    if (e != cudaSuccess) return e;
     // Zeros in the rows without a token.  While one block sorts, the rest of
     // the device writes zeros over all of dE, and the rows with a token are
     // written again, at most 1 / kZeroAllShare of them (8192 tokens, 152064 x
-    // 3584: 34 us of sorting hidden for 8 us more to write).  Otherwise each
-    // row looks itself up in the sorted keys.
-    if (!accumulate && n <= kSmallSort && n * kZeroAllShare <= V) {
-        const int64_t n1 = V * H, n4 = aligned(dE, 16) ? n1 / 4 : 0;
+    // 3584: 34 us of sorting hidden for 8 us more to write).  Few tokens leave
+    // the shared memory for it to be one launch.  Otherwise each row looks
+    // itself up in the sorted keys.
+    const bool zero_all = !accumulate && n <= kSmallSort && n * kZeroAllShare <= V, along = zero_all && n <= kTinySort;
+    const int64_t n1 = V * H;
+    int where;
+    cudaError_t e = launch_sort(c, b, &where, dE, along ? n1 : 0, di, st);
+    if (e != cudaSuccess) return e;
+    if (zero_all && !along) {
+        const int64_t n4 = aligned(dE, 16) ? n1 / 4 : 0;
         const int64_t per = kZeroThreads * kZeroVectors, blocks = (n4 + (n1 - 4 * n4) + per - 1) / per;
         if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
         e = launch_dependent(emb_zero_all, blocks, kZeroThreads, st, dE, n4, n1);
-    } else if (!accumulate) {
+    } else if (!accumulate && !along) {
         const int64_t blocks = (V + kAbsentThreads / 32 - 1) / (kAbsentThreads / 32);
         const bool v4 = H % 4 == 0 && aligned(dE, 16);
         e = launch_dependent(v4 ? emb_zero_absent<true> : emb_zero_absent<false>, blocks, kAbsentThreads, st,
