@@ -420,7 +420,8 @@ rk_status rk_linear_logp_bwd_full_saved(const uint16_t *h, const uint16_t *W,
  *     y[v] = y[v] - frequency[r] * n[v] - presence[r] * (n[v] > 0) + bias[r, v]
  *     x[v] = y[v] / temperature[r],  or -inf where the row's mask has a 0 bit.
  * All in fp32.  What the logits hold in masked places (NaN, infinities) never
- * reaches a result.
+ * reaches a result.  -inf in an allowed place is a token of probability 0; NaN or
+ * +inf there makes the row's logp and lse NaN, and its gradient everywhere.
  *
  * The struct itself is host memory, read during the call; its pointers are
  * device memory.  A NULL pointer leaves the rule out.
@@ -479,7 +480,8 @@ typedef struct {
  *   logits  bf16 or fp32 [T, V], row stride ld_logits >= V elements, aligned to
  *           its element
  *   out     bf16 or fp32 [T, V], row stride ld_out >= V (columns >= V untouched);
- *           one rounding when it is bf16.  Must not overlap logits.
+ *           one rounding when it is bf16.  It may be logits itself (same address,
+ *           type and row stride); otherwise the two must not overlap.
  * Supported: 1 <= V < 2^31, 0 <= T < 2^31.  Needs no workspace.
  */
 rk_status rk_logits_rules_apply(const void *logits, rk_dtype logits_type, int64_t ld_logits,
@@ -512,7 +514,8 @@ rk_status rk_logp_from_logits_rules(const void *logits, rk_dtype logits_type, in
  * on rows of which the rules leave nothing (lse = -inf).
  *   lse      fp32 [T] from rk_logp_from_logits_rules on the same inputs
  *   dlogits  bf16 or fp32 [T, V], row stride ld_dlogits >= V (columns >= V
- *            untouched), one rounding when it is bf16
+ *            untouched), one rounding when it is bf16; it may be logits itself, as
+ *            for rk_logits_rules_apply
  */
 rk_status rk_logp_from_logits_rules_bwd(const void *logits, rk_dtype logits_type,
                                         int64_t ld_logits, const int64_t *targets,

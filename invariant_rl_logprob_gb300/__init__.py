@@ -200,10 +200,10 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(targets, cu_seqlens, T, device):
-    _need(targets, "targets", torch.int64, 1)
+def _rows(targets, cu_seqlens, T, device, name="targets"):
+    _need(targets, name, torch.int64, 1)
     if targets.shape[0] != T or targets.device != device:
-        raise ValueError("targets must be [T] on the same device")
+        raise ValueError(f"{name} must be [T] on the same device")
     if cu_seqlens is None:
         return None, 0
     _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
@@ -657,7 +657,8 @@ class LogitsRules:
     ``row_length``, ``row_mask`` (default ``t``; negative: no mask).  All are
     contiguous CUDA tensors, kept by the object; whatever is left out does not
     apply.  The tensors are read when an operator runs, so their contents may
-    change between calls (a replayed CUDA graph reads the new ones).
+    change between calls (a replayed CUDA graph reads the new ones, and needs the
+    object alive).
     """
 
     __slots__ = ("device", "struct", "address", "rows", "mask_words", "_kept")
@@ -831,8 +832,8 @@ def logits_rules_apply(logits: torch.Tensor, rules: LogitsRules, *,
     """The logits under ``rules``, ``[T, V]`` in ``out_dtype`` (bf16 or fp32).
 
     ``logits`` is bf16 or fp32 ``[T, V]`` with any row stride (the output of
-    :func:`lm_head` as it is).  Rows with ``row_request`` -1 are left as they
-    are in ``out``."""
+    :func:`lm_head` as it is); ``out`` may be ``logits`` itself.  Rows with
+    ``row_request`` -1 are left as they are in ``out`` (undefined in a new one)."""
     lib = _lib or load_library()
     code, ld = _matrix(logits, "logits")
     T, V = logits.shape
@@ -885,7 +886,7 @@ def logp_from_logits_rules_bwd(logits: torch.Tensor, targets: torch.Tensor, rule
                                out_dtype: torch.dtype = torch.float32,
                                stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """The gradient of :func:`logp_from_logits_rules` with respect to the logits,
-    ``[T, V]`` in ``out_dtype`` (bf16 or fp32)."""
+    ``[T, V]`` in ``out_dtype`` (bf16 or fp32); ``out`` may be ``logits`` itself."""
     lib = _lib or load_library()
     code, ld = _matrix(logits, "logits")
     T, V = logits.shape
@@ -920,7 +921,7 @@ def embedding(ids: torch.Tensor, E: torch.Tensor, cu_seqlens: torch.Tensor | Non
     V, H = E.shape
     device = E.device
     T = ids.shape[0] if isinstance(ids, torch.Tensor) and ids.dim() == 1 else 0
-    cu, ns = _rows(ids, cu_seqlens, T, device)
+    cu, ns = _rows(ids, cu_seqlens, T, device, "ids")
     if out is not None and not out.is_contiguous():
         raise ValueError("out must be contiguous")
     out, out_code, _ = _result(out, out_dtype or E.dtype, (T, H), device, stream)
@@ -947,7 +948,7 @@ def embedding_bwd(grad_out: torch.Tensor, ids: torch.Tensor, V: int,
     code = _dense(grad_out, "grad_out", None, None)
     T, H = grad_out.shape
     device = grad_out.device
-    cu, ns = _rows(ids, cu_seqlens, T, device)
+    cu, ns = _rows(ids, cu_seqlens, T, device, "ids")
     n, order = T, None
     if row_order is not None:
         _need(row_order, "row_order", torch.int64, 1)

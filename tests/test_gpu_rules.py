@@ -175,6 +175,23 @@ def test_every_alignment_of_both_kinds_of_slice(rk, dtype, shift):
             assert bool((buf[~inside] == 7.0).all())
 
 
+@pytest.mark.parametrize("V,ld,shift", [(20000, 20000, 0), (9001, 9001, 1), (9001, 9016, 3)])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_results_in_place_of_the_logits(rk, dtype, V, ld, shift):
+    # histories of some hundred tokens: warps with more touched columns than lanes
+    c = rp.make_case(30, V, dtype=dtype, ld=ld, packed=True, requests=3, bias=2, mask="mixed", history=900, seed=70)
+    c.kw["tokens"] %= 700
+    z, tg, rules = rp.cuda_case(rk, c, shift)
+    g = torch.randn(30, device=DEV)
+    _, lse = rk.logp_from_logits_rules(z, tg, rules)
+    x = rk.logits_rules_apply(z, rules, out_dtype=dtype)
+    d = rk.logp_from_logits_rules_bwd(z, tg, rules, lse, g, out_dtype=dtype)
+    z2, _, _ = rp.cuda_case(rk, c, shift)
+    assert rk.logits_rules_apply(z2, rules, out=z2) is z2 and same_bits(z2, x)
+    rk.logp_from_logits_rules_bwd(z, tg, rules, lse, g, out=z)
+    assert same_bits(z, d)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_a_narrow_matrix_at_its_buffers_first_element(rk, dtype):
     # rows of a few bytes: what lies before the tensor is NaN and is not taken for a logit
@@ -522,6 +539,40 @@ def test_on_another_stream_and_in_a_graph(rk):
         logp, lse = rk.logp_from_logits_rules(z, tg, rules)
         want = (logp, lse, rk.logits_rules_apply(z, rules), rk.logp_from_logits_rules_bwd(z, tg, rules, lse, g))
         assert all(same_bits(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_what_is_not_a_number_in_an_allowed_place(rk, dtype, bad):
+    # in a touched column (9), a plain one, and the last; rows 0 and 4 have none, row 5 masks it
+    c = rp.make_case(6, 9001, dtype=dtype, mask="half", seed=77)
+    for t, v in ((1, 9), (2, 5000), (3, 9000), (5, 5001)):
+        c.logits[t, v] = bad
+        c.kw["mask"][t, v // 32] |= torch.tensor(1 << 31, dtype=torch.int64).to(torch.int32) if v % 32 == 31 else 1 << v % 32
+    c.kw["mask"][5, 5001 // 32] &= ~(1 << 5001 % 32)
+    c.kw["tokens"][c.kw["token_offsets"][1]:c.kw["token_offsets"][2]] = 9
+    z, tg, rules = rp.cuda_case(rk, c)
+    logp, lse = rk.logp_from_logits_rules(z, tg, rules)
+    d = rk.logp_from_logits_rules_bwd(z, tg, rules, lse, torch.ones(6, device=DEV))
+    sick = torch.tensor([False, True, True, True, False, False], device=DEV)
+    assert bool((logp.isnan() == sick).all()) and bool((lse.isnan() == sick).all())
+    assert bool(d[sick].isnan().all()) and bool(d[~sick].isfinite().all())
+
+
+def test_calls_on_two_streams_at_once(rk):
+    cases = [rp.make_case(200, 40000, packed=True, requests=3, bias=2, mask="mixed", seed=s) for s in (80, 81)]
+    args = [rp.cuda_case(rk, c) for c in cases]
+    ids = torch.randint(0, 3000, (9000,), device=DEV)
+    d = torch.randn(9000, 256, device=DEV)
+    want = [rk.logp_from_logits_rules(*a[:2], a[2]) + (rk.embedding_bwd(d, ids, 3000 + i),) for i, a in enumerate(args)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [[], []]
+        for i, (a, st) in enumerate(zip(args, streams)):
+            got[i] = rk.logp_from_logits_rules(*a[:2], a[2], stream=st) + (rk.embedding_bwd(d, ids, 3000 + i, stream=st),)
+        torch.cuda.synchronize()
+        assert all(same_bits(x, y) for g, w in zip(got, want) for x, y in zip(g, w))
 
 
 def test_memory_made_by_a_call_is_its_streams(rk):
