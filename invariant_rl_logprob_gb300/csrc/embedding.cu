@@ -142,6 +142,8 @@ constexpr int kSmallSort = kSmallThreads * kSortItems;          // 8192
 constexpr int kPiece = 32;       // occurrences of an id summed by one warp
 constexpr int kHalf = kPiece / 2;
 constexpr int kScanThreads = 1024;
+constexpr int kClasses = 6;      // pieces of 1, 2, 3..4, 5..8, 9..16, 17..32 rows
+constexpr int kCounters = kClasses + 1;  // pieces of each class, joins
 constexpr int kZeroAllShare = 8;
 
 struct Canonical {  // the canonical tokens
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kSortThreads)
     __shared__ int cnt[kMaxBins];
     wait_prior_grid();
     for (int d = threadIdx.x; d < bins; d += kSortThreads) cnt[d] = 0;
-    if (blockIdx.x == 0 && threadIdx.x < 2) counters[threadIdx.x] = 0;
+    if (blockIdx.x == 0 && threadIdx.x < kCounters) counters[threadIdx.x] = 0;
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * kSortTile + threadIdx.x;
     int32_t k[kSortItems];
@@ -406,36 +408,92 @@ __device__ __forceinline__ int64_t run_end(const K *key, int64_t i, int64_t n, i
     return lo;
 }
 
-// The pieces of the run [i, end) of id k.  Their partial sums take slots
-// ceil(i / kHalf), ...: a run of more than kPiece items has at least as many
-// multiples of kHalf as pieces, so no two runs share a slot.
-__device__ __forceinline__ void write_pieces(Piece *p, int np, int32_t k, int64_t i, int64_t end) {
+// Pieces are listed by size, the largest first, so that the warps that take them
+// in turn get the same work (65536 x 4096: 243 us, and 258 to 284 in the order in
+// which blocks found them).  Class c has its own part of the list: n / (its smallest size) + 1
+// pieces at most.
+__host__ __device__ inline int64_t class_pieces(int64_t n, int c) { return n / (c < 2 ? c + 1 : (1 << (c - 1)) + 1) + 1; }
+__host__ __device__ inline int64_t class_first(int64_t n, int c) {  // c = -1: of all
+    int64_t at = 0;
+    for (int d = kClasses - 1; d > c; --d) at += class_pieces(n, d);
+    return at;
+}
+__device__ __forceinline__ int class_of(int len) { return len > 1 ? 32 - __clz(len - 1) : 0; }
+
+// The pieces of the run [i, end) of id k: all but the last are whole.  Where a
+// block's pieces of each class are: `count` (shared) gives the places of this
+// run's, at which write_pieces puts them behind base[class].
+struct Places {
+    int whole, last;
+};
+__device__ __forceinline__ int last_len(int np, int64_t i, int64_t end) {
+    return (int)(end - i) - (np - 1) * kPiece;
+}
+__device__ __forceinline__ Places take_places(int *count, int np, int64_t i, int64_t end) {
+    Places p;
+    p.whole = np > 1 ? atomicAdd(&count[kClasses - 1], np - 1) : 0;
+    p.last = atomicAdd(&count[class_of(last_len(np, i, end))], 1);
+    return p;
+}
+// Their partial sums take slots ceil(i / kHalf), ...: a run of more than kPiece
+// items has at least as many multiples of kHalf as pieces, so no two runs share a
+// slot.
+__device__ __forceinline__ void write_pieces(Piece *pieces, const int64_t *base, const Places &at, int np, int32_t k,
+                                             int64_t i, int64_t end) {
     const int32_t slot = (int32_t)((i + kHalf - 1) / kHalf);
-    for (int j = 0; j < np; ++j) {
-        const int64_t at = i + (int64_t)j * kPiece;
-        p[j] = Piece{k, (int32_t)at, (int32_t)min((int64_t)kPiece, end - at), np > 1 ? slot + j : -1};
-    }
+    Piece *whole = pieces + base[kClasses - 1] + at.whole;
+    for (int j = 0; j < np - 1; ++j) whole[j] = Piece{k, (int32_t)(i + (int64_t)j * kPiece), kPiece, slot + j};
+    const int len = last_len(np, i, end), c = class_of(len);
+    pieces[base[c] + at.last] =
+        Piece{k, (int32_t)(end - len), len, np > 1 ? slot + np - 1 : -1};
 }
 __device__ __forceinline__ Piece join_of(int np, int32_t k, int64_t i) {
     return Piece{k, (int32_t)i, np, (int32_t)((i + kHalf - 1) / kHalf)};
 }
 
-__global__ void __launch_bounds__(256)
+// The runs that start in a block of 256 sorted keys.  Only the last of them can
+// reach beyond it; the block looks for its end together, 256 probes at a time.
+constexpr int kPieceThreads = 256;
+__global__ void __launch_bounds__(kPieceThreads)
     emb_pieces(const int32_t *key, int64_t n, int32_t V, Piece *pieces, Piece *joins, int32_t *counters) {
-    __shared__ int block_base;
+    __shared__ int count[kClasses];
+    __shared__ int64_t place[kClasses];
+    __shared__ unsigned starts[kPieceThreads / 32];  // bit per key: a run starts
     wait_prior_grid();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int32_t k = i < n ? key[i] : V;
-    const bool start = k < V && (i == 0 || key[i - 1] != k);
-    const int64_t end = start ? run_end(key, i, n, k) : 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t base = (int64_t)blockIdx.x * kPieceThreads, i = base + threadIdx.x;
+    const int64_t stop = min(base + kPieceThreads, n);  // the end of the block's keys
+    const int32_t k = i < n ? key[i] : V, last = key[stop - 1];
+    const bool first = i < n && (i == 0 || key[i - 1] != k), start = first && k < V;
+    const unsigned mine = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) starts[warp] = mine;
+    if (threadIdx.x < kClasses) count[threadIdx.x] = 0;
+    int64_t lo = stop, hi = last < V ? n : stop;  // the end of the last run is in [lo, hi]
+    while (lo < hi) {
+        const int64_t step = (hi - lo + kPieceThreads - 1) / kPieceThreads;
+        const int64_t at = lo + ((int64_t)threadIdx.x + 1) * step - 1;  // the last of this thread's share
+        const int same = __syncthreads_count(at < hi && key[at] == last);
+        lo += same * step;
+        hi = min(hi, lo + step - 1);
+    }
+    __syncthreads();
+    int64_t end = lo;
+    if (start) {
+        unsigned rest = lane < 31 ? mine >> (lane + 1) << (lane + 1) : 0;
+        int w = warp;
+        while (rest == 0 && ++w < kPieceThreads / 32) rest = starts[w];
+        if (rest) end = base + 32 * w + __ffs(rest) - 1;
+    }
     const int np = start ? (int)((end - i + kPiece - 1) / kPiece) : 0;
-    int all;
-    const int at = block_scan<8>(np, &all);
-    if (threadIdx.x == 0) block_base = all ? atomicAdd(&counters[0], all) : 0;
+    Places at{};
+    if (start) at = take_places(count, np, i, end);
+    __syncthreads();
+    if (threadIdx.x < kClasses)
+        place[threadIdx.x] = class_first(n, threadIdx.x) + atomicAdd(&counters[threadIdx.x], count[threadIdx.x]);
     __syncthreads();
     if (!start) return;
-    write_pieces(pieces + block_base + at, np, k, i, end);
-    if (np > 1) joins[atomicAdd(&counters[1], 1)] = join_of(np, k, i);
+    write_pieces(pieces, place, at, np, k, i, end);
+    if (np > 1) joins[atomicAdd(&counters[kClasses], 1)] = join_of(np, k, i);
 }
 
 // Keys, sort and pieces of up to kSortItems * THREADS tokens in one block.
@@ -444,7 +502,8 @@ struct SmallSort {
     int32_t key[2][kSortItems * THREADS];
     uint16_t item[2][kSortItems * THREADS];  // canonical index
     int place[THREADS / 32][kMaxBins];
-    int joins;
+    int64_t base[kClasses];
+    int count[kClasses], joins;
 };
 
 // Block `block` of THREADS * kZeroVectors * 16 bytes of zeros in dE, of n1 floats,
@@ -479,6 +538,10 @@ __global__ void __launch_bounds__(THREADS)
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = (int)c.n, base = warp * 32 * kSortItems, bins = 1 << digit;
+    if (threadIdx.x < kClasses) {
+        s.count[threadIdx.x] = 0;
+        s.base[threadIdx.x] = class_first(n, threadIdx.x);
+    }
     if (threadIdx.x == 0) s.joins = 0;
     int32_t k[kSortItems], v[kSortItems];
 #pragma unroll
@@ -531,35 +594,21 @@ __global__ void __launch_bounds__(THREADS)
         }
     }
     const int32_t *sorted = s.key[(passes - 1) & 1];
-    int np[kSortItems], mine = 0;  // pieces that start at this thread's items
-    int end[kSortItems];
 #pragma unroll
     for (int j = 0; j < kSortItems; ++j) {
         const int i = base + 32 * j + lane;
-        np[j] = end[j] = 0;
         if (i >= n) continue;
         key[i] = k[j];
         val[i] = (int32_t)(k[j] < c.V ? (c.order ? c.order[v[j]] : (int64_t)v[j]) : 0);
         if (k[j] >= c.V || (i > 0 && sorted[i - 1] == k[j])) continue;
-        end[j] = (int)run_end(sorted, i, n, k[j]);
-        np[j] = (end[j] - i + kPiece - 1) / kPiece;
-        mine += np[j];
-    }
-    int total;
-    int at = block_scan<kWarps>(mine, &total);
-#pragma unroll
-    for (int j = 0; j < kSortItems; ++j) {
-        if (np[j] == 0) continue;
-        const int i = base + 32 * j + lane;
-        write_pieces(pieces + at, np[j], k[j], i, end[j]);
-        at += np[j];
-        if (np[j] > 1) joins[atomicAdd(&s.joins, 1)] = join_of(np[j], k[j], i);
+        const int64_t end = run_end(sorted, i, n, k[j]);
+        const int np = (int)((end - i + kPiece - 1) / kPiece);
+        write_pieces(pieces, s.base, take_places(s.count, np, i, end), np, k[j], i, end);
+        if (np > 1) joins[atomicAdd(&s.joins, 1)] = join_of(np, k[j], i);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        counters[0] = total;
-        counters[1] = s.joins;
-    }
+    if (threadIdx.x < kClasses) counters[threadIdx.x] = s.count[threadIdx.x];
+    if (threadIdx.x == 0) counters[kClasses] = s.joins;
 }
 
 // ---- gradient: rows of dE without a token ----
@@ -659,12 +708,24 @@ __device__ __forceinline__ void put_cols(float *dst, int64_t cols, int lane, con
 // latency into every unit's chain: 300 us instead of 219 at 65536 x 4096).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSumThreads, VEC ? kSumBlocks : 3)
-    emb_sum(const T *dout, int64_t H, float scale, const int32_t *val, const Piece *pieces,
+    emb_sum(const T *dout, int64_t H, float scale, const int32_t *val, const Piece *pieces, int64_t n,
             const int32_t *counters, int accumulate, float *dE, float *partial) {
+    // the pieces before the end of each class, largest first, and where piece i of it
+    // is in the list: i + shift
+    __shared__ unsigned ends[kClasses];
+    __shared__ int64_t shift[kClasses];
     wait_prior_grid();
+    if (threadIdx.x < kClasses) {
+        const int c = kClasses - 1 - (int)threadIdx.x;
+        unsigned before = 0;
+        for (int d = kClasses - 1; d > c; --d) before += (unsigned)counters[d];
+        ends[threadIdx.x] = before + (unsigned)counters[c];
+        shift[threadIdx.x] = class_first(n, c) - (int64_t)before;
+    }
+    __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t ncb = (H + kSumCols - 1) / kSumCols;
-    const unsigned count = (unsigned)counters[0], blocks = (unsigned)ncb;
+    const unsigned count = ends[kClasses - 1], blocks = (unsigned)ncb;
     const unsigned u = blockIdx.x * kSumWarps + warp, step = gridDim.x * kSumWarps;
     // Unit u: piece u / ncb, columns from u % ncb * kSumCols on.  A unit's piece is
     // read two units ahead and its rows one ahead (kPiece == 32).
@@ -680,7 +741,13 @@ __global__ void __launch_bounds__(kSumThreads, VEC ? kSumBlocks : 3)
     };
     unsigned at2 = at, cb2 = cb;  // two units ahead, in the end
     auto piece_ahead = [&] {
-        const Piece p = at2 < count ? pieces[at2] : Piece{};
+        Piece p{};
+        if (at2 < count) {
+            int c = 0;
+#pragma unroll
+            for (int d = 0; d < kClasses - 1; ++d) c += at2 >= ends[d];
+            p = pieces[shift[c] + at2];
+        }
         advance(at2, cb2);
         return p;
     };
@@ -733,7 +800,7 @@ __global__ void __launch_bounds__(kSumThreads)
              float *dE, const float *partial) {
     wait_prior_grid();
     const int64_t ncb = (H + kSumThreads - 1) / kSumThreads;  // a column per thread
-    const int64_t units = (int64_t)counters[1] * ncb;
+    const int64_t units = (int64_t)counters[kClasses] * ncb;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const Piece p = joins[u / ncb];
         const int64_t c = (u % ncb) * kSumThreads + threadIdx.x;
@@ -787,8 +854,8 @@ BwdBuffers carve(void *base, int64_t n, int64_t H) {
         b.val[i] = static_cast<int32_t *>(take((size_t)n * 4));
     }
     b.hist = static_cast<int32_t *>(take((size_t)tile_pitch(n) * kMaxBins * 4));
-    b.counters = static_cast<int32_t *>(take(2 * 4));  // pieces, joins
-    b.pieces = static_cast<Piece *>(take((size_t)n * sizeof(Piece)));
+    b.counters = static_cast<int32_t *>(take(kCounters * 4));
+    b.pieces = static_cast<Piece *>(take((size_t)class_first(n, -1) * sizeof(Piece)));
     b.joins = static_cast<Piece *>(take((size_t)(n / kPiece + 1) * sizeof(Piece)));
     b.partial = static_cast<float *>(take((size_t)(n / kHalf + 1) * (size_t)H * 4));
     b.bytes = at;
@@ -843,8 +910,8 @@ cudaError_t launch_sort(const Canonical &c, const BwdBuffers &b, int *where, flo
     }
     if (e != cudaSuccess) return e;
     *where = src;
-    return launch_dependent(emb_pieces, (c.n + 255) / 256, 256, st, (const int32_t *)b.key[src], c.n,
-                            (int32_t)c.V, b.pieces, b.joins, b.counters);
+    return launch_dependent(emb_pieces, (c.n + kPieceThreads - 1) / kPieceThreads, kPieceThreads, st,
+                            (const int32_t *)b.key[src], c.n, (int32_t)c.V, b.pieces, b.joins, b.counters);
 }
 
 template <typename T, bool VEC>
@@ -852,8 +919,8 @@ cudaError_t launch_sums(const void *dout, int64_t H, float scale, int64_t n, int
                         bool accumulate, float *dE, const DeviceInfo &di, cudaStream_t st) {
     cudaError_t e = launch_dependent(emb_sum<T, VEC>, (int64_t)di.sm_count * kSumBlocks, kSumThreads, st,
                                      static_cast<const T *>(dout), H, scale, (const int32_t *)b.val[where],
-                                     (const Piece *)b.pieces, (const int32_t *)b.counters, (int)accumulate, dE,
-                                     b.partial);
+                                     (const Piece *)b.pieces, n, (const int32_t *)b.counters, (int)accumulate,
+                                     dE, b.partial);
     if (e != cudaSuccess || n <= kPiece) return e;
     return launch_dependent(emb_join, (int64_t)di.sm_count * 16, kSumThreads, st, H, scale,
                             (const Piece *)b.joins, (const int32_t *)b.counters, (int)accumulate, dE,

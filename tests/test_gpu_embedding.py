@@ -91,6 +91,25 @@ def test_gradient(rk, T, V, H, hot, dtype):
     assert rk.get_device_error() == 0
 
 
+@pytest.mark.parametrize("T", [9001, 140000])
+def test_a_sort_of_four_passes(rk, T):
+    V = (1 << 27) + 3
+    g = torch.Generator().manual_seed(T)
+    some = torch.cat([torch.randint(0, V, (T // 3,), generator=g), torch.tensor([0, V - 1, 1 << 26])])
+    ids = some[torch.randint(0, some.numel(), (T,), generator=g)]
+    d = torch.randn(T, 1, generator=g)
+    dE = rk.embedding_bwd(d.to(DEV), ids.to(DEV), V)
+    u, where = ids.unique(return_inverse=True)
+    want, mag = torch.zeros(len(u), dtype=torch.float64), torch.zeros(len(u), dtype=torch.float64)
+    want.index_add_(0, where, d[:, 0].double())
+    mag.index_add_(0, where, d[:, 0].double().abs())
+    # fewer than 40 rows an id: 32 additions in a piece, one more per piece, the scale
+    assert int(torch.bincount(where).max()) < 40
+    assert bool(((dE[u.to(DEV), 0].cpu().double() - want).abs() <= 36 * rp.U * 1.01 * mag).all())
+    dE[u.to(DEV)] = 0
+    assert not bool(dE.any())
+
+
 def test_one_token_for_every_row(rk):
     T, H = 70001, 16
     d = torch.randn(T, H, generator=torch.Generator().manual_seed(3))
