@@ -798,6 +798,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!q.ok) return;
         const int32_t len = requests[k].len;
         const int32_t counted = other ? 0 : requests[done].len;
+        if (clear && q.ntok == 0 && q.nbias == 0) return;  // nothing touched, as before
         if (other || len < counted) {
             count_request(sh.bias != nullptr, clear, rules.bias_ids + q.bias0, q.nbias, q.tokens, q.prompt, len,
                           slice0, width);

@@ -575,6 +575,31 @@ def test_calls_on_two_streams_at_once(rk):
         assert all(same_bits(x, y) for g, w in zip(got, want) for x, y in zip(g, w))
 
 
+@pytest.mark.parametrize("bias", [0, 1])
+@pytest.mark.parametrize("history", [0, 1, 2])
+def test_requests_without_a_history_between_others(rk, history, bias):
+    # several rows to a block, each of a request of its own, many with no token and no bias
+    c = rp.make_case(200, 30000, history=history, bias=bias, seed=50 + history)
+    if bias:  # every third request has the biases
+        n = [1 if r % 3 == 0 else 0 for r in range(200)]
+        c.kw["bias_offsets"] = torch.tensor(np.concatenate([[0], np.cumsum(n)]))
+    c.kw["tokens"] %= 5
+    z, _, rules = rp.cuda_case(rk, c)
+    x = rk.logits_rules_apply(z, rules).double().cpu().numpy()
+    for t in range(200):
+        want, _, size = rp.plain_row(c, t)
+        assert np.all(np.abs(x[t] - want) <= rp.x_bound(size) + 1e-37), t
+    # the same as rows of packed sequences of three, whose first has seen nothing
+    rq = torch.arange(200, dtype=torch.int32) // 3
+    ln = torch.arange(200, dtype=torch.int32) % 3
+    c.kw.update(row_request=rq, row_length=ln)
+    z, tg, rules = rp.cuda_case(rk, c)
+    x = rk.logits_rules_apply(z, rules).double().cpu().numpy()
+    for t in range(200):
+        want, _, size = rp.plain_row(c, t)
+        assert np.all(np.abs(x[t] - want) <= rp.x_bound(size) + 1e-37), t
+
+
 def test_memory_made_by_a_call_is_its_streams(rk):
     """What a call on a side stream allocates does not come out of the current stream's
     freed memory, which work on that stream may still be using."""
