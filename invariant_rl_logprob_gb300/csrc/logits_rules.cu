@@ -39,8 +39,9 @@
 // Measured, 4096 x 128256 bf16 (us; bytes at the copy rate: logp 157, gradient in
 // bf16 314 and in fp32 471, applied to fp32 471): without rules 206, 364, 526, 492;
 // with histories 247, 391, 567, 531; with masks and biases too 267, 413, 588, 547.
-// The gradient and apply are bound by memory, logp by instruction latency: 16
-// warps per SM are what 128 registers and the counts leave room for.
+// Without rules the gradient and apply are bound by memory; logp, and the touched
+// columns of all three, by instruction latency: 16 warps per SM are what 128
+// registers and the counts leave room for.
 //
 // Batch invariance: a warp's partial (max, sum) of a row is formed by a tree
 // fixed by the columns' indices and by which of them are touched, and the
