@@ -66,6 +66,9 @@ constexpr int kMaxBiases = 65534;  // per request: indices are kept in 16 bits
 constexpr uint32_t kPromptBit = 0x80000000u;
 constexpr uint32_t kNegInf2 = 0xFF80FF80u;  // two bf16 -inf
 constexpr float kLn2 = 0.69314718055994531f;
+// Below this, m c rounds by r <= 2^-12, and 1 - r ln 2 is 2^-r to (r ln 2)^2 / 2 <
+// 2^-26; far above it, it is not even positive.
+constexpr float kNearExponent = 8192.f;
 
 enum RulesOp { kApply, kLogp, kBwd };
 
@@ -1064,11 +1067,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 m[r] = warp_max(m[r]);
                 ref[r] = m[r] == -INFINITY ? 0.f : m[r];
                 rc[r] = __fmul_rn(ref[r], c);
-                far = far || !(fabsf(ref[r]) < 1e32f);  // c < 1.5e6
+                far = far || !(fabsf(rc[r]) < kNearExponent);
             }
             // Terms 2^(z c - m c), m c rounded: one rounding of the small difference
-            // each.  Where m c might leave the type's range (logits next to its
-            // lowest value), 2^((z - m) c).
+            // each, and one factor for the sum.  Where m c is large (a low temperature,
+            // logits far from 0), 2^((z - m) c).
             uint64_t acc[R][4] = {};  // pairs of +0
             auto add_terms = [&](int r, int i, bool fused) {
                 uint64_t z[4];
@@ -1087,8 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (__builtin_expect(far, 0)) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const bool fused = fabsf(ref[r]) < 1e32f;
-                    if (!fused) rc[r] = 0.f;
+                    const bool fused = fabsf(rc[r]) < kNearExponent;
 #pragma unroll
                     for (int i = 0; i < L::kPieces; ++i) add_terms(r, i, fused);
                 }
@@ -1104,8 +1106,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 float s0, s1;
                 unpair(add2(add2(acc[r][0], acc[r][1]), add2(acc[r][2], acc[r][3])), s0, s1);
                 s[r] = __fadd_rn(s0, s1);
-                // relative to m c itself rather than to its rounding
-                if (!far || fabsf(ref[r]) < 1e32f)
+                // relative to m c itself rather than to its rounding, to first order
+                if (!far || fabsf(rc[r]) < kNearExponent)
                     s[r] = __fmaf_rn(s[r], __fmul_rn(-kLn2, __fmaf_rn(ref[r], c, -rc[r])), s[r]);
                 if (listed > 0) {
                     s[r] = __fadd_rn(s[r], ex2(__fmul_rn(__fsub_rn(y0[r], ref[r]), c)));
