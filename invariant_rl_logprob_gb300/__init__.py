@@ -158,9 +158,13 @@ def load_library() -> ctypes.CDLL:
     lib.rk_logp_from_logits_rules.argtypes = [vp, i32, i64, vp, vp, i32, rp, i64, i64, vp, vp, vp, sz,
                                               vp]
     lib.rk_logp_from_logits_rules.restype = ctypes.c_int
+    lib.rk_logp_from_logits_rules_lse64.argtypes = lib.rk_logp_from_logits_rules.argtypes
+    lib.rk_logp_from_logits_rules_lse64.restype = ctypes.c_int
     lib.rk_logp_from_logits_rules_bwd.argtypes = [vp, i32, i64, vp, vp, i32, rp, i64, i64, vp, vp, vp,
                                                   i32, i64, vp]
     lib.rk_logp_from_logits_rules_bwd.restype = ctypes.c_int
+    lib.rk_logp_from_logits_rules_bwd_lse64.argtypes = lib.rk_logp_from_logits_rules_bwd.argtypes
+    lib.rk_logp_from_logits_rules_bwd_lse64.restype = ctypes.c_int
     lib.rk_embedding.argtypes = [vp, vp, i32, vp, i32, i64, i64, i64, f32, vp, i32, vp]
     lib.rk_embedding.restype = ctypes.c_int
     lib.rk_embedding_bwd_workspace_size.argtypes = [i64, i64, i64]
@@ -800,6 +804,17 @@ def _vector(t: torch.Tensor, name: str, T: int, device) -> None:
         raise ValueError(f"{name} must be [T] on {device}")
 
 
+def _is_lse64(lse: torch.Tensor, T: int, device) -> bool:
+    """Whether a log-sum-exp, fp32 or fp64 [T], is the latter."""
+    if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float64:
+        _vector(lse, "lse", T, device)
+        return False
+    _need(lse, "lse", torch.float64, 1)
+    if lse.shape[0] != T or lse.device != device:
+        raise ValueError(f"lse must be [T] on {device}")
+    return True
+
+
 def _run(what: str, fn, device, stream, *args) -> None:
     """Calls the library on ``device``, with the stream's handle behind ``args``."""
     if stream is None:
@@ -852,11 +867,14 @@ def logp_from_logits_rules_workspace_size(T: int, V: int) -> int:
 def logp_from_logits_rules(logits: torch.Tensor, targets: torch.Tensor, rules: LogitsRules,
                            cu_seqlens: torch.Tensor | None = None, *,
                            out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                           lse_dtype: torch.dtype = torch.float32,
                            workspace: torch.Tensor | None = None,
                            stream: torch.cuda.Stream | None = None):
     """Selected-token logprob of the distribution that ``rules`` leave: returns
     ``(logp, lse)``, fp32 ``[T]``.  Both are -inf on a row of which the rules
-    leave nothing, logp where the target is masked."""
+    leave nothing, logp where the target is masked.  With ``lse_dtype``
+    (or an ``lse``) of float64 the log-sum-exp is not rounded to fp32, which
+    :func:`logp_from_logits_rules_bwd` needs at low temperatures."""
     lib = _lib or load_library()
     code, ld = _matrix(logits, "logits")
     T, V = logits.shape
@@ -868,12 +886,16 @@ def logp_from_logits_rules(logits: torch.Tensor, targets: torch.Tensor, rules: L
     else:
         _vector(out, "out", T, device)
     if lse is None:
-        lse = _empty(T, torch.float32, device, stream)
+        if lse_dtype is not torch.float32 and lse_dtype is not torch.float64:
+            raise TypeError(f"lse must be float32 or float64, got {lse_dtype}")
+        lse = _empty(T, lse_dtype, device, stream)
+        wide = lse_dtype is torch.float64
     else:
-        _vector(lse, "lse", T, device)
+        wide = _is_lse64(lse, T, device)
     workspace = _scratch(workspace, lib.rk_logp_from_logits_rules_workspace_size(T, V), device,
                          stream)
-    _run("rk_logp_from_logits_rules", lib.rk_logp_from_logits_rules, device, stream,
+    _run("rk_logp_from_logits_rules",
+         lib.rk_logp_from_logits_rules_lse64 if wide else lib.rk_logp_from_logits_rules, device, stream,
          logits.data_ptr(), code, ld, targets.data_ptr(), _ptr(cu), ns, rules.address, T, V,
          out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out, lse
@@ -886,17 +908,22 @@ def logp_from_logits_rules_bwd(logits: torch.Tensor, targets: torch.Tensor, rule
                                out_dtype: torch.dtype = torch.float32,
                                stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """The gradient of :func:`logp_from_logits_rules` with respect to the logits,
-    ``[T, V]`` in ``out_dtype`` (bf16 or fp32); ``out`` may be ``logits`` itself."""
+    ``[T, V]`` in ``out_dtype`` (bf16 or fp32); ``out`` may be ``logits`` itself.
+
+    An fp32 ``lse`` leaves every probability a relative error of up to 2**-23 * |lse|, and
+    the gradient grows with 1 / temperature: below a temperature of some 0.1 use a float64
+    ``lse`` (``lse_dtype`` of :func:`logp_from_logits_rules`)."""
     lib = _lib or load_library()
     code, ld = _matrix(logits, "logits")
     T, V = logits.shape
     device = logits.device
     cu, ns = _rows(targets, cu_seqlens, T, device)
     _rules_for(rules, T, V, device)
-    _vector(lse, "lse", T, device)
+    wide = _is_lse64(lse, T, device)
     _vector(grad_logp, "grad_logp", T, device)
     out, out_code, out_ld = _result(out, out_dtype, (T, V), device, stream)
-    _run("rk_logp_from_logits_rules_bwd", lib.rk_logp_from_logits_rules_bwd, device, stream,
+    _run("rk_logp_from_logits_rules_bwd",
+         lib.rk_logp_from_logits_rules_bwd_lse64 if wide else lib.rk_logp_from_logits_rules_bwd, device, stream,
          logits.data_ptr(), code, ld, targets.data_ptr(), _ptr(cu), ns, rules.address, T, V,
          lse.data_ptr(), grad_logp.data_ptr(), out.data_ptr(), out_code, out_ld)
     return out

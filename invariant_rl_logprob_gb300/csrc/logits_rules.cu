@@ -97,6 +97,7 @@ struct RulesIo {
     int run0, run;   // rows per block, of the first slice and of the others
     unsigned blocks0;  // the first slice's blocks
     const float *lse, *grad;  // kBwd
+    const double *lse64;      // kBwd: instead of lse, or null
     void *out;       // kApply, kBwd
     int64_t ld_out;
     float2 *part;    // kLogp: [T][kWarps per slice] (max of y, sum relative to it)
@@ -604,11 +605,12 @@ __device__ __forceinline__ int make_list(uint16_t *list, uint32_t touched, int o
     return __shfl_sync(0xffffffffu, incl, 31);
 }
 
-// exp(y / temperature - lse), 1 / temperature = id + i1, i1 >= 0 (-inf stays -inf).
-__device__ __forceinline__ float prob(float y, float id, float i1, float lse) {
+// exp(y / temperature - lse), 1 / temperature = id + i1, i1 >= 0 (-inf stays -inf);
+// `low`: -log2e times what of the log-sum-exp is not in lse.
+__device__ __forceinline__ float prob(float y, float id, float i1, float lse, float low) {
     float x = __fmaf_rn(y, id, -lse);
     if (i1 > 0.f) x = __fmaf_rn(y, i1, x);
-    return ex2(__fmul_rn(x, kLog2e));
+    return ex2(__fmaf_rn(x, kLog2e, low));
 }
 
 // bf16 pieces: where a pair's two bits in `keep` are 0, -inf.  Byte i of `keep`
@@ -901,8 +903,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (k < n) rows[k].step = k > 0 ? step : kNoToken;  // row 0 is started
         __syncthreads();
     }
-    // kBwd: lse and gradient of rows k & ~31 + lane
-    float lse_of = 0.f, grad_of = 0.f;
+    // kBwd: lse (and what a 64-bit one has beyond it, times -log2e) and gradient of
+    // rows k & ~31 + lane
+    float lse_of = 0.f, low_of = 0.f, grad_of = 0.f;
     int held = -1;
     unsigned char *now = ring;  // row k's stage
     for (int k = 0; k < n;) {
@@ -1177,13 +1180,22 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (OP == kBwd && k >> 5 != held) {
                     held = k >> 5;
                     const int64_t t = t0 + (held * 32 + lane);
-                    lse_of = t < io.T ? io.lse[t] : 0.f;
+                    if (io.lse64) {
+                        const double d = t < io.T ? io.lse64[t] : 0.0;
+                        lse_of = __double2float_rn(d);
+                        low_of = fabsf(lse_of) < INFINITY
+                                     ? __fmul_rn(-kLog2e, __double2float_rn(d - (double)lse_of))
+                                     : 0.f;
+                    } else {
+                        lse_of = t < io.T ? io.lse[t] : 0.f;
+                    }
                     grad_of = t < io.T ? io.grad[t] : 0.f;
                 }
                 __syncwarp();  // the stage is read
                 const float lse = OP == kBwd ? __shfl_sync(0xffffffffu, lse_of, k & 31) : 0.f;
                 const bool none = OP == kBwd && lse == -INFINITY;  // the rules leave nothing
                 const float l = none ? 0.f : lse;
+                const float low = OP == kBwd ? __shfl_sync(0xffffffffu, low_of, k & 31) : 0.f;
                 const float g =
                     OP == kBwd && !none ? __fmul_rn(__shfl_sync(0xffffffffu, grad_of, k & 31), q.itau) : 0.f;
                 // x - lse with 1 / temperature to 48 bits (id + i1): the rounding of
@@ -1199,11 +1211,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 auto result = [&](float hot, float z, uint32_t cw, float y) {
                     if (OP == kApply) return __fmul_rn(y, q.itau);
                     const float slope = cw ? (z > 0.f ? q.irep : q.rep) : 1.f;
-                    return __fmul_rn(__fmul_rn(g, __fsub_rn(hot, prob(y, id, i1, l))), slope);
+                    return __fmul_rn(__fmul_rn(g, __fsub_rn(hot, prob(y, id, i1, l, low))), slope);
                 };
                 auto transform = [&](auto is_split) {
                     const float f = OP == kApply ? q.itau : id;
-                    const uint64_t f2 = pair(f, f), i2 = pair(i1, i1), nl = pair(-l, -l), ng = pair(-g, -g);
+                    const uint64_t f2 = pair(f, f), i2 = pair(i1, i1), nl = pair(-l, -l), ng = pair(-g, -g),
+                                   lo = pair(low, low);
 #pragma unroll
                     for (int i = 0; i < L::kPieces; ++i) {
                         constexpr int N = L::kCols;
@@ -1219,7 +1232,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                 float a, b;
                                 v = fma2(z[j], f2, nl);
                                 if constexpr (decltype(is_split)::value) v = fma2(z[j], i2, v);
-                                unpair(mul2(v, pair(kLog2e, kLog2e)), a, b);
+                                unpair(fma2(v, pair(kLog2e, kLog2e), lo), a, b);
                                 v = mul2(pair(ex2(a), ex2(b)), ng);
                             }
                             unpair(v, x[2 * j], x[2 * j + 1]);
@@ -1322,7 +1335,7 @@ __device__ __forceinline__ void merge_y(float &m, float &s, float mo, float so, 
 constexpr int kMergeRows = 8;
 __global__ void __launch_bounds__(32 * kMergeRows)
     rules_merge(const __grid_constant__ RulesIo io, const __grid_constant__ rk_logits_rules rules,
-                float *logp, float *lse) {
+                float *logp, float *lse, double *lse64) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31;
@@ -1333,6 +1346,7 @@ __global__ void __launch_bounds__(32 * kMergeRows)
         if (lane == 0) {
             logp[t] = 0.f;
             if (lse) lse[t] = 0.f;
+            if (lse64) lse64[t] = 0.0;
         }
         return;
     }
@@ -1353,13 +1367,13 @@ __global__ void __launch_bounds__(32 * kMergeRows)
     }
     if (lane == 0) {
         const float nan = __int_as_float(0x7fc00000);
-        float l, p;
+        float l, p, ls = 0.f;
         if (state != kOk || s != s) {
             l = p = nan;
         } else if (s == 0.f) {
             l = p = -INFINITY;
         } else {
-            const float ls = logf(s);
+            ls = logf(s);
             l = __fadd_rn(__fdiv_rn(m, tau), ls);  // -inf where m / tau is past the type
             p = __fsub_rn(__fdiv_rn(__fsub_rn(io.ytgt[t], m), tau), ls);
             if (p > 0.f) p = 0.f;  // rounding alone can take it there
@@ -1367,6 +1381,8 @@ __global__ void __launch_bounds__(32 * kMergeRows)
         }
         logp[t] = p;
         if (lse) lse[t] = l;
+        // past fp32 what l says (an infinity)
+        if (lse64) lse64[t] = fabsf(l) < INFINITY ? (double)m / (double)tau + (double)ls : (double)l;
     }
 }
 
@@ -1471,8 +1487,8 @@ cudaError_t launch_rules_apply(const RulesMatrix &logits, const rk_logits_rules 
 
 cudaError_t launch_rules_logp(const RulesMatrix &logits, const int64_t *targets, const int32_t *cu,
                               int num_seqs, const rk_logits_rules &rules, int64_t T, int64_t V,
-                              float *logp, float *lse, void *workspace, const DeviceInfo &di,
-                              cudaStream_t st) {
+                              float *logp, float *lse, double *lse64, void *workspace,
+                              const DeviceInfo &di, cudaStream_t st) {
     RulesIo io{};
     io.logits = logits.p;
     io.ld = logits.ld;
@@ -1490,13 +1506,13 @@ cudaError_t launch_rules_logp(const RulesMatrix &logits, const int64_t *targets,
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     dependent(&cfg, attr, (unsigned)((T + kMergeRows - 1) / kMergeRows), 32 * kMergeRows, 0, st);
-    return cudaLaunchKernelEx(&cfg, rules_merge, io, rules, logp, lse);
+    return cudaLaunchKernelEx(&cfg, rules_merge, io, rules, logp, lse, lse64);
 }
 
 cudaError_t launch_rules_bwd(const RulesMatrix &logits, const int64_t *targets, const int32_t *cu,
                              int num_seqs, const rk_logits_rules &rules, int64_t T, int64_t V,
-                             const float *lse, const float *grad, const RulesMatrix &dlogits,
-                             const DeviceInfo &di, cudaStream_t st) {
+                             const float *lse, const double *lse64, const float *grad,
+                             const RulesMatrix &dlogits, const DeviceInfo &di, cudaStream_t st) {
     RulesIo io{};
     io.logits = logits.p;
     io.ld = logits.ld;
@@ -1506,6 +1522,7 @@ cudaError_t launch_rules_bwd(const RulesMatrix &logits, const int64_t *targets, 
     io.T = T;
     io.V = V;
     io.lse = lse;
+    io.lse64 = lse64;
     io.grad = grad;
     io.out = const_cast<void *>(dlogits.p);
     io.ld_out = dlogits.ld;

@@ -590,11 +590,12 @@ size_t rk_logp_from_logits_rules_workspace_size(int64_t T, int64_t V) {
     return rk::logp_rules_workspace_bytes(T, V);
 }
 
-rk_status rk_logp_from_logits_rules(const void *logits, rk_dtype logits_type, int64_t ld_logits,
-                                    const int64_t *targets, const int32_t *cu_seqlens,
-                                    int32_t num_seqs, const rk_logits_rules *rules, int64_t T,
-                                    int64_t V, float *logp, float *lse, void *workspace,
-                                    size_t workspace_bytes, void *stream) {
+// rk_logp_from_logits_rules with the log-sum-exp in fp32 or (lse64) in fp64; either may be NULL.
+static rk_status logp_rules(const void *logits, rk_dtype logits_type, int64_t ld_logits,
+                            const int64_t *targets, const int32_t *cu_seqlens, int32_t num_seqs,
+                            const rk_logits_rules *rules, int64_t T, int64_t V, float *logp,
+                            float *lse, double *lse64, void *workspace, size_t workspace_bytes,
+                            void *stream) {
     if (T < 0 || V <= 0 || !good_type(logits_type)) return RK_ERR_INVALID_ARG;
     if (T == 0) return RK_OK;
     if (!logits || !logp || ld_logits < V) return RK_ERR_INVALID_ARG;
@@ -605,12 +606,61 @@ rk_status rk_logp_from_logits_rules(const void *logits, rk_dtype logits_type, in
     if (st != RK_OK) return st;
     if (!elem_aligned(logits, logits_type)) return RK_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < rk::logp_rules_workspace_bytes(T, V)) return RK_ERR_WORKSPACE;
-    if (!aligned(workspace, 16)) return RK_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16) || !aligned(lse64, 8)) return RK_ERR_INVALID_ARG;
     DeviceInfo di;
     cudaError_t e = rk::current_device_info(&di);
     if (e != cudaSuccess) return rk::cuda_fail(e);
     e = rk::launch_rules_logp({logits, logits_type, ld_logits}, targets, cu_seqlens, num_seqs, *rules,
-                              T, V, logp, lse, workspace, di, static_cast<cudaStream_t>(stream));
+                              T, V, logp, lse, lse64, workspace, di,
+                              static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    return RK_OK;
+}
+
+rk_status rk_logp_from_logits_rules(const void *logits, rk_dtype logits_type, int64_t ld_logits,
+                                    const int64_t *targets, const int32_t *cu_seqlens,
+                                    int32_t num_seqs, const rk_logits_rules *rules, int64_t T,
+                                    int64_t V, float *logp, float *lse, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
+    return logp_rules(logits, logits_type, ld_logits, targets, cu_seqlens, num_seqs, rules, T, V, logp,
+                      lse, nullptr, workspace, workspace_bytes, stream);
+}
+
+rk_status rk_logp_from_logits_rules_lse64(const void *logits, rk_dtype logits_type,
+                                          int64_t ld_logits, const int64_t *targets,
+                                          const int32_t *cu_seqlens, int32_t num_seqs,
+                                          const rk_logits_rules *rules, int64_t T, int64_t V,
+                                          float *logp, double *lse, void *workspace,
+                                          size_t workspace_bytes, void *stream) {
+    return logp_rules(logits, logits_type, ld_logits, targets, cu_seqlens, num_seqs, rules, T, V, logp,
+                      nullptr, lse, workspace, workspace_bytes, stream);
+}
+
+// rk_logp_from_logits_rules_bwd from a log-sum-exp in fp32 or (lse64) in fp64; one of them is NULL.
+static rk_status logp_rules_bwd(const void *logits, rk_dtype logits_type, int64_t ld_logits,
+                                const int64_t *targets, const int32_t *cu_seqlens, int32_t num_seqs,
+                                const rk_logits_rules *rules, int64_t T, int64_t V, const float *lse,
+                                const double *lse64, const float *grad_logp, void *dlogits,
+                                rk_dtype dlogits_type, int64_t ld_dlogits, void *stream) {
+    if (T < 0 || V <= 0 || !good_type(logits_type) || !good_type(dlogits_type))
+        return RK_ERR_INVALID_ARG;
+    if (T == 0) return RK_OK;
+    if (!logits || (!lse && !lse64) || !grad_logp || !dlogits || ld_logits < V || ld_dlogits < V)
+        return RK_ERR_INVALID_ARG;
+    rk_status st = check_rows(targets, cu_seqlens, num_seqs);
+    if (st != RK_OK) return st;
+    if (V >= (int64_t(1) << 31) || T >= (int64_t(1) << 31)) return RK_ERR_UNSUPPORTED;
+    st = check_rules(rules, T);
+    if (st != RK_OK) return st;
+    if (!elem_aligned(logits, logits_type) || !elem_aligned(dlogits, dlogits_type) ||
+        !aligned(lse64, 8))
+        return RK_ERR_INVALID_ARG;
+    DeviceInfo di;
+    cudaError_t e = rk::current_device_info(&di);
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    e = rk::launch_rules_bwd({logits, logits_type, ld_logits}, targets, cu_seqlens, num_seqs, *rules,
+                             T, V, lse, lse64, grad_logp, {dlogits, dlogits_type, ld_dlogits}, di,
+                             static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return rk::cuda_fail(e);
     return RK_OK;
 }
@@ -621,26 +671,19 @@ rk_status rk_logp_from_logits_rules_bwd(const void *logits, rk_dtype logits_type
                                         const rk_logits_rules *rules, int64_t T, int64_t V,
                                         const float *lse, const float *grad_logp, void *dlogits,
                                         rk_dtype dlogits_type, int64_t ld_dlogits, void *stream) {
-    if (T < 0 || V <= 0 || !good_type(logits_type) || !good_type(dlogits_type))
-        return RK_ERR_INVALID_ARG;
-    if (T == 0) return RK_OK;
-    if (!logits || !lse || !grad_logp || !dlogits || ld_logits < V || ld_dlogits < V)
-        return RK_ERR_INVALID_ARG;
-    rk_status st = check_rows(targets, cu_seqlens, num_seqs);
-    if (st != RK_OK) return st;
-    if (V >= (int64_t(1) << 31) || T >= (int64_t(1) << 31)) return RK_ERR_UNSUPPORTED;
-    st = check_rules(rules, T);
-    if (st != RK_OK) return st;
-    if (!elem_aligned(logits, logits_type) || !elem_aligned(dlogits, dlogits_type))
-        return RK_ERR_INVALID_ARG;
-    DeviceInfo di;
-    cudaError_t e = rk::current_device_info(&di);
-    if (e != cudaSuccess) return rk::cuda_fail(e);
-    e = rk::launch_rules_bwd({logits, logits_type, ld_logits}, targets, cu_seqlens, num_seqs, *rules,
-                             T, V, lse, grad_logp, {dlogits, dlogits_type, ld_dlogits}, di,
-                             static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return rk::cuda_fail(e);
-    return RK_OK;
+    return logp_rules_bwd(logits, logits_type, ld_logits, targets, cu_seqlens, num_seqs, rules, T, V, lse,
+                          nullptr, grad_logp, dlogits, dlogits_type, ld_dlogits, stream);
+}
+
+rk_status rk_logp_from_logits_rules_bwd_lse64(const void *logits, rk_dtype logits_type,
+                                              int64_t ld_logits, const int64_t *targets,
+                                              const int32_t *cu_seqlens, int32_t num_seqs,
+                                              const rk_logits_rules *rules, int64_t T, int64_t V,
+                                              const double *lse, const float *grad_logp,
+                                              void *dlogits, rk_dtype dlogits_type,
+                                              int64_t ld_dlogits, void *stream) {
+    return logp_rules_bwd(logits, logits_type, ld_logits, targets, cu_seqlens, num_seqs, rules, T, V,
+                          nullptr, lse, grad_logp, dlogits, dlogits_type, ld_dlogits, stream);
 }
 
 rk_status rk_embedding(const int64_t *ids, const int32_t *cu_seqlens, int32_t num_seqs,

@@ -100,12 +100,12 @@ cudaError_t launch_rules_apply(const RulesMatrix &logits, const rk_logits_rules 
                                cudaStream_t st);
 cudaError_t launch_rules_logp(const RulesMatrix &logits, const int64_t *targets, const int32_t *cu,
                               int num_seqs, const rk_logits_rules &rules, int64_t T, int64_t V,
-                              float *logp, float *lse, void *workspace, const DeviceInfo &di,
-                              cudaStream_t st);
+                              float *logp, float *lse, double *lse64, void *workspace,
+                              const DeviceInfo &di, cudaStream_t st);
 cudaError_t launch_rules_bwd(const RulesMatrix &logits, const int64_t *targets, const int32_t *cu,
                              int num_seqs, const rk_logits_rules &rules, int64_t T, int64_t V,
-                             const float *lse, const float *grad, const RulesMatrix &dlogits,
-                             const DeviceInfo &di, cudaStream_t st);
+                             const float *lse, const double *lse64, const float *grad,
+                             const RulesMatrix &dlogits, const DeviceInfo &di, cudaStream_t st);
 
 // ---- embedding and its gradient (embedding.cu) ----
 cudaError_t launch_embedding(const int64_t *ids, const int32_t *cu, int num_seqs, const void *E,
