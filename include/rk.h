@@ -481,7 +481,8 @@ typedef struct {
  *           its element
  *   out     bf16 or fp32 [T, V], row stride ld_out >= V (columns >= V untouched);
  *           one rounding when it is bf16.  It may be logits itself (same address,
- *           type and row stride); otherwise the two must not overlap.
+ *           type and row stride); any other overlap of their rows is refused
+ *           (RK_ERR_INVALID_ARG).
  * Supported: 1 <= V < 2^31, 0 <= T < 2^31.  Needs no workspace.
  */
 rk_status rk_logits_rules_apply(const void *logits, rk_dtype logits_type, int64_t ld_logits,
@@ -527,8 +528,8 @@ rk_status rk_logp_from_logits_rules_lse64(const void *logits, rk_dtype logits_ty
  *            grows with 1 / temperature.  rk_logp_from_logits_rules_bwd_lse64 takes the fp64
  *            lse of rk_logp_from_logits_rules_lse64 and has no such term.
  *   dlogits  bf16 or fp32 [T, V], row stride ld_dlogits >= V (columns >= V
- *            untouched), one rounding when it is bf16; it may be logits itself, as
- *            for rk_logits_rules_apply
+ *            untouched), one rounding when it is bf16; it may be logits itself, or
+ *            apart from it, as for rk_logits_rules_apply
  */
 rk_status rk_logp_from_logits_rules_bwd(const void *logits, rk_dtype logits_type,
                                         int64_t ld_logits, const int64_t *targets,

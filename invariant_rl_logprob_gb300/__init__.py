@@ -847,8 +847,9 @@ def logits_rules_apply(logits: torch.Tensor, rules: LogitsRules, *,
     """The logits under ``rules``, ``[T, V]`` in ``out_dtype`` (bf16 or fp32).
 
     ``logits`` is bf16 or fp32 ``[T, V]`` with any row stride (the output of
-    :func:`lm_head` as it is); ``out`` may be ``logits`` itself.  Rows with
-    ``row_request`` -1 are left as they are in ``out`` (undefined in a new one)."""
+    :func:`lm_head` as it is); ``out`` may be ``logits`` itself, or a matrix whose rows
+    have no byte in common with those of ``logits``.  Rows with ``row_request`` -1 are
+    left as they are in ``out`` (undefined in a new one)."""
     lib = _lib or load_library()
     code, ld = _matrix(logits, "logits")
     T, V = logits.shape
@@ -908,7 +909,7 @@ def logp_from_logits_rules_bwd(logits: torch.Tensor, targets: torch.Tensor, rule
                                out_dtype: torch.dtype = torch.float32,
                                stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """The gradient of :func:`logp_from_logits_rules` with respect to the logits,
-    ``[T, V]`` in ``out_dtype`` (bf16 or fp32); ``out`` may be ``logits`` itself.
+    ``[T, V]`` in ``out_dtype`` (bf16 or fp32); ``out`` as for :func:`logits_rules_apply`.
 
     An fp32 ``lse`` leaves every probability a relative error of up to 2**-23 * |lse|, and
     the gradient grows with 1 / temperature: below a temperature of some 0.1 use a float64

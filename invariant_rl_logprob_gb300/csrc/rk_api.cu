@@ -549,6 +549,37 @@ rk_status rk_linear_logp_bwd_full_saved(const uint16_t *h, const uint16_t *W,
 static bool good_type(rk_dtype t) { return t == RK_BF16 || t == RK_FP32; }
 static bool elem_aligned(const void *p, rk_dtype t) { return aligned(p, t == RK_BF16 ? 2 : 4); }
 
+// Whether a [T, V] matrix can be made from another one that other blocks still read: in
+// its place, or with no byte of it among the other's.  (Rows side by side in one buffer have
+// none, and take the first branch; the loop is for strides of different lengths in ranges that
+// meet.)
+static bool can_hold(const rk::RulesMatrix &in, const rk::RulesMatrix &out, int64_t T, int64_t V) {
+    using i128 = __int128;  // no address or stride takes it past its range
+    const i128 size_a = in.type == RK_BF16 ? 2 : 4, size_b = out.type == RK_BF16 ? 2 : 4;
+    const i128 a = (i128)reinterpret_cast<uintptr_t>(in.p), b = (i128)reinterpret_cast<uintptr_t>(out.p);
+    const i128 step_a = in.ld * size_a, step_b = out.ld * size_b;  // bytes from row to row
+    const i128 row_a = V * size_a, row_b = V * size_b;             // bytes of a row
+    if (a == b && in.type == out.type && (in.ld == out.ld || T == 1)) return true;
+    if (a + (T - 1) * step_a + row_a <= b || b + (T - 1) * step_b + row_b <= a) return true;
+    // row i of a meets row j of b if and only if b_j + row_b > a_i and b_j < a_i + row_a: the first j
+    // with the former decides
+    const auto first_above = [](i128 x, i128 step) {  // the least k with k step > x
+        return x >= 0 ? x / step + 1 : -((-x - 1) / step);
+    };
+    if (step_a == step_b) {  // k = j - i
+        i128 k = first_above(a - b - row_b, step_a);
+        if (k < 1 - T) k = 1 - T;
+        return k > T - 1 || b + k * step_a >= a + row_a;
+    }
+    for (int64_t i = 0; i < T; ++i) {
+        const i128 at = a + i * step_a;
+        i128 j = first_above(at - b - row_b, step_b);
+        if (j < 0) j = 0;
+        if (j < T && b + j * step_b < at + row_a) return false;
+    }
+    return true;
+}
+
 // Argument checks of a rules struct against T rows.
 static rk_status check_rules(const rk_logits_rules *r, int64_t T) {
     if (!r) return RK_ERR_INVALID_ARG;
@@ -576,11 +607,12 @@ rk_status rk_logits_rules_apply(const void *logits, rk_dtype logits_type, int64_
     rk_status st = check_rules(rules, T);
     if (st != RK_OK) return st;
     if (!elem_aligned(logits, logits_type) || !elem_aligned(out, out_type)) return RK_ERR_INVALID_ARG;
+    const rk::RulesMatrix from{logits, logits_type, ld_logits}, to{out, out_type, ld_out};
+    if (!can_hold(from, to, T, V)) return RK_ERR_INVALID_ARG;
     DeviceInfo di;
     cudaError_t e = rk::current_device_info(&di);
     if (e != cudaSuccess) return rk::cuda_fail(e);
-    e = rk::launch_rules_apply({logits, logits_type, ld_logits}, *rules, T, V,
-                               {out, out_type, ld_out}, di, static_cast<cudaStream_t>(stream));
+    e = rk::launch_rules_apply(from, *rules, T, V, to, di, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return rk::cuda_fail(e);
     return RK_OK;
 }
@@ -655,12 +687,13 @@ static rk_status logp_rules_bwd(const void *logits, rk_dtype logits_type, int64_
     if (!elem_aligned(logits, logits_type) || !elem_aligned(dlogits, dlogits_type) ||
         !aligned(lse64, 8))
         return RK_ERR_INVALID_ARG;
+    const rk::RulesMatrix from{logits, logits_type, ld_logits}, to{dlogits, dlogits_type, ld_dlogits};
+    if (!can_hold(from, to, T, V)) return RK_ERR_INVALID_ARG;
     DeviceInfo di;
     cudaError_t e = rk::current_device_info(&di);
     if (e != cudaSuccess) return rk::cuda_fail(e);
-    e = rk::launch_rules_bwd({logits, logits_type, ld_logits}, targets, cu_seqlens, num_seqs, *rules,
-                             T, V, lse, lse64, grad_logp, {dlogits, dlogits_type, ld_dlogits}, di,
-                             static_cast<cudaStream_t>(stream));
+    e = rk::launch_rules_bwd(from, targets, cu_seqlens, num_seqs, *rules, T, V, lse, lse64, grad_logp, to,
+                             di, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return rk::cuda_fail(e);
     return RK_OK;
 }
