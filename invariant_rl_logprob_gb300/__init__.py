@@ -698,8 +698,8 @@ class LogitsRules:
                             raise ValueError(f"{name} does not fit {rows} rows")
                         rows = n
                 elif n - extra != requests:
-                    if requests is not None or n <= extra:
-                        raise ValueError(f"{name} does not fit {requests or 'one or more'} requests")
+                    if requests is not None or n < extra:
+                        raise ValueError(f"{name} does not fit {'any' if requests is None else requests} requests")
                     requests = n - extra
             # an empty list still has to be told from a missing one
             address.append(t.data_ptr() or _EMPTY)
@@ -714,7 +714,9 @@ class LogitsRules:
         num_bias = 0 if bias_ids is None else bias_ids.size(0)
         if num_bias and num_bias != bias_values.size(0):
             raise ValueError("bias_ids and bias_values differ in length")
-        if requests and row_request is None:
+        if requests == 0 and rows:
+            raise ValueError(f"no requests for {rows} rows")
+        if requests is not None and row_request is None:
             if rows is not None and rows != requests:
                 raise ValueError(f"{requests} requests for {rows} rows: row_request is missing")
             rows = requests
