@@ -53,3 +53,40 @@ def test_wide_rows(rk, dtype, T, hot, H):
     buf = torch.empty(T * H + 1, dtype=dtype, device=DEV)[1:].view(T, H)
     buf.copy_(d)
     assert same_bits(rk.embedding_bwd(buf, ids.to(DEV), V, scale=0.75), got)
+
+
+# zeros in the grid of the smallest sort; beside the other one-block sort; in rows that no key names
+@pytest.mark.parametrize("n,V,H", [(700, 8000, 64), (4000, 40000, 64), (8192, 65536, 9), (4000, 9000, 64), (20000, 200000, 16)])
+def test_zeros_in_a_graph_and_between_readers(rk, n, V, H):
+    """dE and the workspace used over and over on one stream, with readers of dE in between."""
+    steps = 6
+    ids = [some_ids(n, V, 20 + i, 0.3).to(DEV) for i in range(steps)]
+    d = [torch.randn(n, H, device=DEV) for _ in range(steps)]
+    want = [rk.embedding_bwd(d[i], ids[i], V) for i in range(steps)]
+    for i in range(steps):  # the references: summed by index, zero elsewhere
+        live = ids[i] >= 0
+        ref = torch.zeros(V, H, dtype=torch.float64, device=DEV).index_add_(0, ids[i][live], d[i][live].double())
+        mag = torch.zeros(V, H, dtype=torch.float64, device=DEV).index_add_(0, ids[i][live], d[i][live].double().abs())
+        most = int(torch.bincount(ids[i][live]).max())
+        assert bool(((want[i].double() - ref).abs() <= (32 + most // 32 + 3) * rp.U * 1.01 * mag).all())
+    ws = torch.empty(rk.embedding_bwd_workspace_size(n, H, V), dtype=torch.uint8, device=DEV)
+    dE = torch.full((V, H), float("nan"), device=DEV)
+    seen = [torch.empty(V, H, device=DEV) for _ in range(2 * steps)]
+    torch.cuda.synchronize()
+    for k in range(2 * steps):
+        rk.embedding_bwd(d[k % steps], ids[k % steps], V, dE=dE, workspace=ws)
+        seen[k].copy_(dE)
+    assert all(same_bits(seen[k], want[k % steps]) for k in range(2 * steps))
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        for k in range(steps):
+            rk.embedding_bwd(d[k], ids[k], V, dE=dE, workspace=ws, stream=side)
+            seen[k].copy_(dE)
+    for _ in range(3):
+        for s in seen:
+            s.fill_(float("nan"))
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(same_bits(seen[k], want[k]) for k in range(steps))
