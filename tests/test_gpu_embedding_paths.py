@@ -55,6 +55,51 @@ def test_wide_rows(rk, dtype, T, hot, H):
     assert same_bits(rk.embedding_bwd(buf, ids.to(DEV), V, scale=0.75), got)
 
 
+# the one-block sorts reach to 1024 and 8192 tokens, tiles that scan the counts themselves to 131072
+@pytest.mark.parametrize("n", [1024, 1025, 8192, 8193, 30000, 131072, 131073, 200000])
+def test_the_sorts_agree(rk, n):
+    """The same tokens in the same canonical order, and padding among them that takes n past the limits."""
+    T, V, H = 1000, 700, 24
+    ids = some_ids(T, V, 5)
+    d = torch.randn(T, H, generator=torch.Generator().manual_seed(6)).to(BF16)
+    base = rk.embedding_bwd(d.to(DEV), ids.to(DEV), V)
+    want, mag, count = rp.plain_embedding_bwd(d, ids.numpy(), V, 1.0)
+    bound = (np.minimum(count, 32) + (count + 31) // 32 + 2)[:, None] * rp.U * 1.01 * mag
+    assert np.all(np.abs(base.double().cpu().numpy() - want) <= bound)
+    g = torch.Generator().manual_seed(n)
+    place = torch.randperm(n, generator=g)[:T].sort().values
+    ids2 = torch.full((n,), -1)
+    d2 = torch.full((n, H), float("nan"), dtype=BF16)
+    ids2[place], d2[place] = ids, d
+    assert same_bits(rk.embedding_bwd(d2.to(DEV), ids2.to(DEV), V), base)
+    # as a canonical order of n entries into rows that lie elsewhere, most of them out of range
+    where = torch.randperm(T, generator=g)
+    order = torch.randint(-1000, 0, (n,), generator=g)
+    order[::3] = torch.randint(T, 1 << 40, (len(order[::3]),), generator=g)
+    order[place] = where
+    d3, ids3 = torch.empty_like(d), torch.empty_like(ids)
+    d3[where], ids3[where] = d, ids
+    assert same_bits(rk.embedding_bwd(d3.to(DEV), ids3.to(DEV), V, row_order=order.to(DEV)), base)
+    # between the rows that cu_seqlens leaves out
+    lead = 13
+    ids4 = torch.cat([torch.zeros(lead, dtype=torch.int64), ids2, torch.ones(5, dtype=torch.int64)])
+    d4 = torch.full((n + lead + 5, H), float("nan"), dtype=BF16)
+    d4[lead:lead + n] = d2
+    cu = torch.tensor([lead, lead + 7, lead + n], dtype=torch.int32, device=DEV)
+    assert same_bits(rk.embedding_bwd(d4.to(DEV), ids4.to(DEV), V, cu), base)
+    assert rk.get_device_error() == 0
+
+
+def test_a_row_named_twice_among_many(rk):
+    T, V, H = 9000, 50, 8
+    ids = some_ids(T, V, 8, 0.2)
+    d = torch.randn(T, H, generator=torch.Generator().manual_seed(9))
+    order = torch.randint(0, T, (20000,), generator=torch.Generator().manual_seed(10))
+    want, mag, count = rp.plain_embedding_bwd(d, ids.numpy(), V, 1.0, order=order.tolist())
+    got = rk.embedding_bwd(d.to(DEV), ids.to(DEV), V, row_order=order.to(DEV)).double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= (np.minimum(count, 32) + (count + 31) // 32 + 2)[:, None] * rp.U * 1.01 * mag)
+
+
 # zeros in the grid of the smallest sort; beside the other one-block sort; in rows that no key names
 @pytest.mark.parametrize("n,V,H", [(700, 8000, 64), (4000, 40000, 64), (8192, 65536, 9), (4000, 9000, 64), (20000, 200000, 16)])
 def test_zeros_in_a_graph_and_between_readers(rk, n, V, H):
