@@ -59,3 +59,24 @@ def test_requests_without_tokens_biases_or_rows(rk):
     for k in ("row_request", "row_length", "row_mask"):
         kw[k] = kw[k][:0]
     assert rk.logits_rules_apply(z[:0], rk.LogitsRules(**kw)).shape == (0, 100)
+
+
+@pytest.mark.parametrize("V", [1, 33, 9001, 40000])
+def test_without_rules_as_the_call_that_knows_none(rk, V):
+    # two kernels, and each within its own rounding: the values agree, the last bits need not
+    import rules_plain as rp
+    T = 20
+    z = (torch.randn(T, V, generator=torch.Generator().manual_seed(V)) * 5).bfloat16()
+    tg = torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(1))
+    tg[3] = -1
+    a = rk.logp_from_logits_rules(z.to(DEV), tg.to(DEV), rk.LogitsRules())
+    b = rk.logp_from_logits(z.to(DEV), tg.to(DEV))
+    for t in range(T):
+        if t == 3:
+            assert all(float(v[t]) == 0 for v in a + tuple(b))
+            continue
+        size = z[t].double().abs().numpy()
+        ref = float(torch.logsumexp(z[t].double(), 0))
+        k = int(tg[t])
+        assert abs(float(a[1][t]) - float(b[1][t])) <= 2 * rp.lse_bound(size, ref)
+        assert abs(float(a[0][t]) - float(b[0][t])) <= 2 * rp.logp_bound(size, k, float(z[t, k]) - ref, ref)
