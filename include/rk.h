@@ -552,7 +552,8 @@ rk_status rk_logp_from_logits_rules_bwd_lse64(const void *logits, rk_dtype logit
  * for every active row (ids[t] >= 0 and inside the cu_seqlens range), 0 on the
  * others; NaN and RK_DEVERR_TARGET_RANGE where ids[t] >= V.
  *   ids  int64 [T];  E  bf16 or fp32 [V, H];  out  bf16 or fp32 [T, H] (the product in
- *   fp32, rounded once when out is bf16); both contiguous, aligned to their element
+ *   fp32, rounded once when out is bf16); both contiguous, aligned to their element,
+ *   out not over E (RK_ERR_INVALID_ARG)
  * Supported: 1 <= H < 2^31, 1 <= V < 2^31, 0 <= T < 2^31.
  */
 rk_status rk_embedding(const int64_t *ids, const int32_t *cu_seqlens, int32_t num_seqs,
@@ -570,7 +571,8 @@ rk_status rk_embedding(const int64_t *ids, const int32_t *cu_seqlens, int32_t nu
  * 32 occurrences whose sums are then added in order: dE[v] is bitwise the same for the
  * same tokens of id v in the same canonical order, whatever their physical layout and
  * whatever the other tokens are.  A row listed twice counts twice.
- *   dout  bf16 or fp32 [T, H]; dE fp32 [V, H]; both contiguous, aligned to their element
+ *   dout  bf16 or fp32 [T, H]; dE fp32 [V, H]; both contiguous, aligned to their element,
+ *         dE not over dout (RK_ERR_INVALID_ARG)
  *   accumulate  0: dE is overwritten (0 in rows without a token); 1: the sum is added to
  *               what dE holds, as for a weight tied to the lm_head's (rows without a
  *               token are not touched)

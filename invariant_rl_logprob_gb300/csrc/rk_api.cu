@@ -547,7 +547,14 @@ rk_status rk_linear_logp_bwd_full_saved(const uint16_t *h, const uint16_t *W,
 }
 
 static bool good_type(rk_dtype t) { return t == RK_BF16 || t == RK_FP32; }
-static bool elem_aligned(const void *p, rk_dtype t) { return aligned(p, t == RK_BF16 ? 2 : 4); }
+static int elem_size(rk_dtype t) { return t == RK_BF16 ? 2 : 4; }
+static bool elem_aligned(const void *p, rk_dtype t) { return aligned(p, elem_size(t)); }
+
+// Whether two ranges of memory have a byte in common.
+static bool ranges_meet(const void *a, __int128 bytes_a, const void *b, __int128 bytes_b) {
+    const __int128 x = (__int128)reinterpret_cast<uintptr_t>(a), y = (__int128)reinterpret_cast<uintptr_t>(b);
+    return x < y + bytes_b && y < x + bytes_a;
+}
 
 // Whether a [T, V] matrix can be made from another one that other blocks still read: in
 // its place, or with no byte of it among the other's.  (Rows side by side in one buffer have
@@ -555,12 +562,12 @@ static bool elem_aligned(const void *p, rk_dtype t) { return aligned(p, t == RK_
 // meet.)
 static bool can_hold(const rk::RulesMatrix &in, const rk::RulesMatrix &out, int64_t T, int64_t V) {
     using i128 = __int128;  // no address or stride takes it past its range
-    const i128 size_a = in.type == RK_BF16 ? 2 : 4, size_b = out.type == RK_BF16 ? 2 : 4;
+    const i128 size_a = elem_size(in.type), size_b = elem_size(out.type);
     const i128 a = (i128)reinterpret_cast<uintptr_t>(in.p), b = (i128)reinterpret_cast<uintptr_t>(out.p);
     const i128 step_a = in.ld * size_a, step_b = out.ld * size_b;  // bytes from row to row
     const i128 row_a = V * size_a, row_b = V * size_b;             // bytes of a row
     if (a == b && in.type == out.type && (in.ld == out.ld || T == 1)) return true;
-    if (a + (T - 1) * step_a + row_a <= b || b + (T - 1) * step_b + row_b <= a) return true;
+    if (!ranges_meet(in.p, (T - 1) * step_a + row_a, out.p, (T - 1) * step_b + row_b)) return true;
     // row i of a meets row j of b if and only if b_j + row_b > a_i and b_j < a_i + row_a: the first j
     // with the former decides
     const auto first_above = [](i128 x, i128 step) {  // the least k with k step > x
@@ -731,6 +738,8 @@ rk_status rk_embedding(const int64_t *ids, const int32_t *cu_seqlens, int32_t nu
     const int64_t lim = int64_t(1) << 31;
     if (V >= lim || T >= lim || H >= lim) return RK_ERR_UNSUPPORTED;
     if (!elem_aligned(E, e_type) || !elem_aligned(out, out_type)) return RK_ERR_INVALID_ARG;
+    if (ranges_meet(E, (__int128)V * H * elem_size(e_type), out, (__int128)T * H * elem_size(out_type)))
+        return RK_ERR_INVALID_ARG;
     DeviceInfo di;
     cudaError_t e = rk::current_device_info(&di);
     if (e != cudaSuccess) return rk::cuda_fail(e);
@@ -765,6 +774,9 @@ rk_status rk_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *
     if (n > 0 && (!workspace || workspace_bytes < rk::embedding_bwd_workspace_bytes(n, H)))
         return RK_ERR_WORKSPACE;
     if (n > 0 && !aligned(workspace, 16)) return RK_ERR_INVALID_ARG;
+    if (T > 0 && n > 0 &&
+        ranges_meet(dout, (__int128)T * H * elem_size(dout_type), dE, (__int128)V * H * 4))
+        return RK_ERR_INVALID_ARG;
     DeviceInfo di;
     cudaError_t e = rk::current_device_info(&di);
     if (e != cudaSuccess) return rk::cuda_fail(e);
