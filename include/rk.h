@@ -419,7 +419,10 @@ rk_status rk_linear_logp_bwd_full_saved(const uint16_t *h, const uint16_t *W,
  *                                      z[v] * repetition[r]  otherwise
  *     y[v] = y[v] - frequency[r] * n[v] - presence[r] * (n[v] > 0) + bias[r, v]
  *     x[v] = y[v] / temperature[r],  or -inf where the row's mask has a 0 bit.
- * All in fp32.  What the logits hold in masked places (NaN, infinities) never
+ * All in fp32; quotients by repetition and temperature are products with the rounded
+ * reciprocal.  The bias comes after the penalties: the sign that repetition looks at is
+ * that of the logit itself, so a program that adds biases first leaves another
+ * distribution where a request has both.  What the logits hold in masked places (NaN, infinities) never
  * reaches a result.  -inf in an allowed place is a token of probability 0; NaN or
  * +inf there makes the row's logp and lse NaN, and its gradient everywhere.
  *
@@ -493,7 +496,8 @@ rk_status rk_logits_rules_apply(const void *logits, rk_dtype logits_type, int64_
  * rk_logp_from_logits under the rules, x never written to memory:
  *     lse[t] = log sum_v exp(x[v]),   logp[t] = x[targets[t]] - lse[t].
  * A row of which the mask (or biases of -inf) leaves nothing has lse = logp =
- * -inf, and a target that is masked has logp = -inf.
+ * -inf, and a target that is masked has logp = -inf.  Without any rule it is the
+ * value of rk_logp_from_logits, not its bits: the two sum in different orders.
  *   logits as for rk_logits_rules_apply; targets, cu_seqlens, num_seqs, logp and
  *   lse (may be NULL) as for rk_logp_from_logits
  *   workspace  >= rk_logp_from_logits_rules_workspace_size(T, V) bytes, 16-byte

@@ -6,25 +6,26 @@
 // Decomposition.  A block works on a slice of kSliceCols columns and a run of
 // consecutive rows.  Its warps own 1024 neighbouring columns each; in the
 // first slice they own blocks of 64 columns in turn instead, because text is
-// made of few tokens and those sit at the low ids, so that its warps share
-// them (everywhere, it made the writes of fp32 results 12% slower: 605 us
-// instead of 540 for 4096 x 128256).  Each lane owns 32 neighbouring
-// columns: one word of a grammar mask, and one word that tells which of them
-// the rules touch (seen before, or biased).  The others need the temperature
-// and the mask only.
+// made of few tokens and those sit at the low ids where a vocabulary is
+// ordered by frequency, so that its warps share them.  In the first slice,
+// nowhere, everywhere (us): logp of 2048 x 32000 49, 67, -; logp of 8192 x
+// 128256 506, 512, -; gradient of 4096 x 128256 in bf16 399, 392, -, and in
+// fp32 without rules 524, 506, 579 (a warp's writes are then in short pieces).
+// Each lane owns 32 neighbouring columns: one word of a grammar mask, and one
+// word that tells which of them the rules touch (seen before, or biased).  The
+// others need the temperature and the mask only.
 //
 // Data.  A warp copies its columns of the next row into shared memory of its
 // own (cp.async, 16 bytes a lane, the mask words with them) while it works on
 // the present one, so no barrier stands between the rows.  Rows that do not
 // start on 16-byte boundaries are copied from the boundary before them and
 // shifted on the way into registers (300 x 50257 without rules: logp
-// 23.5 us, fp32 gradient 31.0; 31.7 and 35.3 with 4-byte copies and single
-// columns written; 21.5 and 27.3 at 50264).  What the rows say about themselves is read once
-// per block.  Results of kApply and kBwd leave through the same memory, so
-// that a warp writes whole lines although a lane owns 32 columns.  Each lane's
-// 32 columns are followed by 16 bytes: they spread a quarter warp's 16-byte
-// accesses over all banks, and hold the end of columns that do not start on a
-// 16-byte boundary.
+// 23.2 us, fp32 gradient 31.2; 21.6 and 26.5 at 50264, where they do).  What the
+// rows say about themselves is read once per block.  Results of kApply and kBwd
+// leave through the same memory, so that a warp writes whole lines although a
+// lane owns 32 columns.  Each lane's 32 columns are followed by 16 bytes: they
+// spread a quarter warp's 16-byte accesses over all banks, and hold the end of
+// columns that do not start on a 16-byte boundary.
 //
 // History.  The block (its warps, each for itself, if they are few) counts a
 // request's tokens of its slice in shared memory (one word per column: bit 31 in
@@ -37,11 +38,13 @@
 // would wait for the one with the most.
 //
 // Measured, 4096 x 128256 bf16 (us; bytes at the copy rate: logp 157, gradient in
-// bf16 314 and in fp32 471, applied to fp32 471): without rules 206, 364, 526, 492;
-// with histories 247, 391, 567, 531; with masks and biases too 267, 413, 588, 547.
-// Without rules the gradient and apply are bound by memory; logp, and the touched
-// columns of all three, by instruction latency: 16 warps per SM are what 128
-// registers and the counts leave room for.
+// bf16 314 and in fp32 471, applied to bf16 314 and to fp32 471): without rules
+// 202, 361, 524, 341, 491; with histories 250, 391, 569, 363, 532; with masks and
+// biases too 272, 416, 590, 377, 549.  fp32 logits (314, 471, 628, 471, 628): 325,
+// 517, 638, 491, 630; 344, 561, 668, 517, 643; 364, 583, 686, 532, 653.  Without
+// rules the gradient and apply are bound by memory; logp of bf16, and the touched
+// columns of all, by instruction latency: 16 warps per SM are what 128 registers
+// and counts of 32 bits leave room for.
 //
 // Batch invariance: a warp's partial (max, sum) of a row is formed by a tree
 // fixed by the columns' indices and by which of them are touched, and the
@@ -654,7 +657,8 @@ __device__ __forceinline__ void pairs_of(const uint4 &w, uint64_t (&z)[4]) {
 // Shared memory of a block: what shared_view lays out, and a ring of stages
 // per warp.  A stage holds the warp's logits and afterwards its results, and
 // its mask words.  Two blocks run per SM, which leaves room for two stages of
-// bf16 (logp of 4096 x 128256: 318 us with one, 224 with two, 216 with three).
+// bf16 (logp of 4096 x 128256 without rules 219 us with one, 202 with two; its
+// gradient in bf16 425 and 361).
 template <RulesOp OP, typename TIn, typename TOut>
 struct Config {
     static constexpr bool kWider = OP != kLogp && sizeof(TOut) > sizeof(TIn);
@@ -848,9 +852,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     // Row k's request, or a step of more than one token.  Short histories each
     // warp counts for itself, so that no barrier holds the rows back; long ones
     // the whole block (apply of 256 requests with up to 4096 tokens, warps alone up
-    // to 0, 128, 256, 512, 1024, 2048 tokens: 77.8, 73.1, 72.8, 71.3, 75.6, 84.0 us;
+    // to 0, 128, 256, 512, 1024, 2048 tokens: 80.0, 75.7, 74.7, 74.1, 76.7, 85.8 us;
     // logp of 64 on the device 15.5, 15.2, 15.4, 15.5, 21, 26; logp of 8192 packed
-    // rows 503, 504, 503, 506, 510, 530).
+    // rows 506, 506, 506, 507, 514, 528).
     auto start_row = [&](int k) {
         const bool other = requests[k].id != cur;
         cur = requests[k].id;
@@ -1402,14 +1406,15 @@ void dependent(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, unsigned grid
 // Rows per block.  A long run counts a history seldom, a short one spreads the
 // blocks evenly over the SMs: as few waves of two blocks per SM as kMaxRun
 // allows, of equal runs.  kMaxRun at 24, 32, 40, 48, 64 (us): logp of 8192 rows
-// with long histories 549, 536, 525, 519, 526; bwd of 4096 rows 400, 404, 407,
-// 418, 419; 40 costs both little.
+// with long histories 538, 525, 506, 500, 496; bwd of 4096 rows 395, 396, 398,
+// 404, 414; 40 costs both little.
 //
 // The first slice has most of what a history touches, and a row takes up to
 // twice the time there.  Its blocks come first, so that the others even out the
-// end (logp of 8192 rows 525 us to 501); in a single wave nothing follows that
-// could, and their runs are shorter.  By nothing, 3/4, 2/3, 3/5, 1/2: 55, 50,
-// 47, 47, 49 us for 2048 x 32000, and no difference where runs are short.
+// end; in a single wave nothing follows that could, and their runs are shorter.
+// By nothing, 3/4, 2/3, 3/5, 1/2: 57, 52, 49, 48.5, 50 us for logp of 2048 x
+// 32000, 32, 30, 30, 30, 29.5 for the gradient of 300 x 50257, and no difference
+// where runs are short.
 constexpr int kFirstNum = 3, kFirstDen = 5;
 void cut_rows(RulesIo &io, const rk_logits_rules &r, const DeviceInfo &di, int64_t *grid) {
     const int64_t slices = (io.V + kSliceCols - 1) / kSliceCols, wave = (int64_t)di.sm_count * 2;
