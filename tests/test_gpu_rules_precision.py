@@ -190,3 +190,31 @@ def test_refusals_of_a_64_bit_lse(rk):
                                                    vp + 4, g.data_ptr(), out.data_ptr(), 1, 64, None) == 1
     assert lib.rk_logp_from_logits_rules_bwd_lse64(z.data_ptr(), 0, 64, tg.data_ptr(), None, 0, rules.address, 4, 64,
                                                    None, g.data_ptr(), out.data_ptr(), 1, 64, None) == 1
+
+
+@pytest.mark.parametrize("tau", [1.0, 1e-2, 1e-4, 1e-6])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_probabilities_of_the_gradient_add_up_under_all_rules(rk, dtype, tau):
+    """Forward and backward take the same y of a touched column, whatever it was rounded to: with the 64-bit lse
+    the gradient's probabilities add up to 1 at any temperature."""
+    T, V = 60, 20001
+    c = rp.make_case(T, V, dtype=dtype, packed=True, requests=4, bias=5, mask="mixed", history=90, seed=33)
+    c.kw["repetition"] = torch.ones(4)  # dx/dz is 1 / tau then
+    c.kw["temperature"] = torch.full((4,), tau)
+    c.logits = c.logits * 8
+    hot = c.kw["tokens"][0]
+    c.logits[::2, hot] = c.logits.double().abs().max().to(dtype)  # a touched column that leads in every other row
+    z, tg, rules = rp.cuda_case(rk, c)
+    t32 = float(c.kw["temperature"][0])
+    logp, lse = rk.logp_from_logits_rules(z, tg, rules, lse_dtype=torch.float64)
+    dz = rk.logp_from_logits_rules_bwd(z, tg, rules, lse, torch.ones(T, device=DEV)).double()
+    mask, row_mask = c.kw["mask"], c.kw["row_mask"]
+    for t in range(T):
+        k = int(c.targets[t])
+        allowed = int(row_mask[t]) < 0 or int(mask[t, k // 32]) >> (k % 32) & 1
+        left = float(dz[t].sum()) * t32 - (1.0 if allowed else 0.0)  # minus the sum of p; a masked target's 1 is not there
+        x = max(abs(float(lse[t])), 1.0) * 4
+        # every p to sum_bound + 2^-45 x + 5u (D + 1), sum p D <= ln V + 1; the result's own roundings
+        bound = sum_bound(V, np.log(V)) + x * 2.0 ** -45 + 5 * U * (np.log(V) + 3) + 6 * U
+        assert abs(left + 1.0) <= 1.01 * bound, (t, left)
+    assert rk.get_device_error() == 0
