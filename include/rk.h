@@ -87,7 +87,9 @@ typedef enum {
 /* Element type of a matrix that is passed as void*. */
 typedef enum {
     RK_BF16 = 0, /* IEEE bfloat16 bit patterns, 2 bytes */
-    RK_FP32 = 1  /* 4 bytes */
+    RK_FP32 = 1, /* 4 bytes */
+    RK_E4M3 = 2  /* 8-bit floating point, 4 exponent and 3 mantissa bits, largest value 448:
+                    outputs of rk_rms_norm and states of rk_adamw_step only */
 } rk_dtype;
 
 /*
@@ -592,6 +594,65 @@ rk_status rk_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *
                            int64_t V, float scale, const int64_t *row_order, int64_t n_order,
                            float *dE, int32_t accumulate, void *workspace,
                            size_t workspace_bytes, void *stream);
+
+/*
+ * Root-mean-square norm, the operator in front of the lm_head and of every other
+ * projection ("rms_norm", issue #101 P0 list; chain index 2 of PR #264), with the
+ * residual's addition before it and an output in 8 bits after it.  For every active row
+ *     r[t, :] = x[t, :],  or round(x[t, :] + residual[t, :]) to residual's type
+ *     y[t, :] = r[t, :] * rstd * weight,   rstd = 1 / sqrt(mean(r[t, :]^2) + eps)
+ * in fp32.  The norm sees r as it is kept, so the call has the bits of an addition
+ * followed by a call without a residual, and the backward needs nothing but r.  A row
+ * whose sum of squares leaves fp32 is scaled by a power of two for it.  Row t is active
+ * iff targets[t] >= 0 (when targets is given) and it lies in the cu_seqlens range (when
+ * that is); the others are not read and get 0 in every output.
+ *   x, residual  bf16 or fp32 [T, H], row strides ld >= H elements, aligned to their element;
+ *                residual NULL: none (and residual_out NULL)
+ *   weight       bf16 or fp32 [H];  eps > 0
+ *   residual_out [T, H] of residual's type: r
+ *   out          [T, H], bf16 or fp32 (y, rounded once), or e4m3: y / s, with one scale s for
+ *                a row (group 0) or for each 128 columns of it (group 128)
+ *   scales       fp32 [T] or [T, ceil(H / 128)], contiguous (NULL unless out is e4m3):
+ *                s = max |y| / 448 of its columns, at least 2^-120; 0 where y is 0
+ * out and residual_out may be x or residual itself (same address, type and row stride); any
+ * other overlap of a result with an input or another result is refused (RK_ERR_INVALID_ARG).
+ * Supported: 1 <= H <= 16384, 0 <= T < 2^31.  Needs no workspace.
+ */
+rk_status rk_rms_norm(const void *x, rk_dtype x_type, int64_t ld_x, const void *residual,
+                      rk_dtype residual_type, int64_t ld_residual, const void *weight,
+                      rk_dtype weight_type, float eps, const int64_t *targets,
+                      const int32_t *cu_seqlens, int32_t num_seqs, int64_t T, int64_t H,
+                      void *residual_out, int64_t ld_residual_out, void *out, rk_dtype out_type,
+                      int64_t ld_out, float *scales, int64_t group, void *stream);
+
+/*
+ * The gradient of rk_rms_norm.  With n = r rstd and g = dout * weight, for every canonical
+ * row (as for rk_linear_logp_dw: the active rows among row_order[0..n_order), or among rows
+ * 0..T-1 in ascending order when row_order is NULL)
+ *     dx[t, :] = rstd * (g - n * mean(g * n)) + dr[t, :]
+ * which is the gradient of x and of residual alike, 0 on all other rows; and
+ *     dweight (+)= sum over the canonical rows of dout * n
+ * in an order that depends on the number of canonical rows alone: the same rows in the same
+ * canonical order give the same bits whatever their layout.  A row that row_order lists twice
+ * counts twice in dweight.
+ *   dout, r, dr  bf16 or fp32 [T, H] with row strides, as above; r: x, or residual_out; dr:
+ *                gradient that arrives at r from elsewhere (the residual stream), or NULL
+ *   dx           bf16 or fp32 [T, H] with a row stride, one rounding when it is bf16.  It may be
+ *                dout, r or dr itself (same address, type and stride) unless row_order is given;
+ *                other overlaps are refused
+ *   dweight      fp32 [H], or NULL; accumulate 1: added to what it holds
+ *   workspace    >= rk_rms_norm_bwd_workspace_size(T, n, H) bytes, 16-byte aligned, n = n_order
+ *                (or T): the blocks' partial sums and the list of canonical rows
+ * Supported: as rk_rms_norm, n < 2^31.
+ */
+size_t rk_rms_norm_bwd_workspace_size(int64_t T, int64_t n, int64_t H);
+rk_status rk_rms_norm_bwd(const void *dout, rk_dtype dout_type, int64_t ld_dout, const void *r,
+                          rk_dtype r_type, int64_t ld_r, const void *weight, rk_dtype weight_type,
+                          float eps, const void *dr, rk_dtype dr_type, int64_t ld_dr,
+                          const int64_t *targets, const int32_t *cu_seqlens, int32_t num_seqs, int64_t T,
+                          int64_t H, const int64_t *row_order, int64_t n_order, void *dx,
+                          rk_dtype dx_type, int64_t ld_dx, float *dweight, int32_t accumulate,
+                          void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * rk_linear_logp without a workspace argument, for callers that cannot

@@ -17,6 +17,8 @@ Operators (RL-Kernel issue #101, maintainer comment, P0 operator list):
   selected logprob under them and its gradient
 * :func:`embedding`, :func:`embedding_bwd` -- the scaled token embedding and
   its gradient, summed per token in canonical order
+* :func:`rms_norm`, :func:`rms_norm_e4m3`, :func:`rms_norm_bwd` -- root-mean-square
+  norm with the residual's addition, with an output in 8 bits, and its gradient
 
 Each is bitwise invariant for a given logical row under changes of batch
 size, row position, neighbour content, padding and varlen packing.
@@ -41,6 +43,7 @@ __all__ = [
     "LogitsRules", "logits_rules_apply", "logp_from_logits_rules",
     "logp_from_logits_rules_workspace_size", "logp_from_logits_rules_bwd",
     "embedding", "embedding_bwd", "embedding_bwd_workspace_size",
+    "rms_norm", "rms_norm_e4m3", "rms_norm_bwd", "rms_norm_bwd_workspace_size",
     "get_device_error", "selftest_wait_timeout", "set_row_blocks", "last_row_blocks", "DEVERR_TARGET_RANGE", "DEVERR_TIMEOUT", "DEVERR_LSE",
     "DEVERR_RULES",
 ]
@@ -172,6 +175,14 @@ def load_library() -> ctypes.CDLL:
     lib.rk_embedding_bwd.argtypes = [vp, i32, vp, vp, i32, i64, i64, i64, f32, vp, i64, vp, i32, vp,
                                      sz, vp]
     lib.rk_embedding_bwd.restype = ctypes.c_int
+    lib.rk_rms_norm.argtypes = [vp, i32, i64, vp, i32, i64, vp, i32, f32, vp, vp, i32, i64, i64, vp, i64,
+                                vp, i32, i64, vp, i64, vp]
+    lib.rk_rms_norm.restype = ctypes.c_int
+    lib.rk_rms_norm_bwd_workspace_size.argtypes = [i64, i64, i64]
+    lib.rk_rms_norm_bwd_workspace_size.restype = sz
+    lib.rk_rms_norm_bwd.argtypes = [vp, i32, i64, vp, i32, i64, vp, i32, f32, vp, i32, i64, vp, vp, i32,
+                                    i64, i64, vp, i64, vp, i32, i64, vp, i32, vp, sz, vp]
+    lib.rk_rms_norm_bwd.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -997,6 +1008,163 @@ def embedding_bwd(grad_out: torch.Tensor, ids: torch.Tensor, V: int,
          ids.data_ptr(), _ptr(cu), ns, T, H, V, scale, order, n, dE.data_ptr(), int(accumulate),
          workspace.data_ptr(), workspace.numel())
     return dE
+
+
+def _weight(weight, H: int, device) -> int:
+    """Type code of a norm's weight."""
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor")
+    code = _TYPE_CODES.get(weight.dtype)
+    if code is None:
+        raise TypeError(f"weight must be bfloat16 or float32, got {weight.dtype}")
+    if weight.dim() != 1 or weight.shape[0] != H or weight.device != device or not weight.is_contiguous():
+        raise ValueError(f"weight must be contiguous [{H}] on {device}, got shape "
+                         f"{tuple(weight.shape)} on {weight.device}")
+    return code
+
+
+def _mask(targets, cu_seqlens, T: int, device):
+    """Addresses of targets and cu_seqlens (both may be missing) and the sequences' number."""
+    if targets is not None:
+        cu, ns = _rows(targets, cu_seqlens, T, device)
+        return targets.data_ptr() or _EMPTY, None if cu is None else cu.data_ptr(), ns
+    if cu_seqlens is None:
+        return None, None, 0
+    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    if cu_seqlens.device != device or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be a non-empty int32 tensor on the same device")
+    return None, cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
+
+
+def _norm(x, weight, targets, cu_seqlens, residual, eps, out, out_code, out_ld, residual_out, scales, group,
+          device, stream):
+    lib = _lib or load_library()
+    code, ld = _matrix(x, "x")
+    T, H = x.shape
+    w_code = _weight(weight, H, device)
+    tg, cu, ns = _mask(targets, cu_seqlens, T, device)
+    r, res, res_code, res_ld, ro, ro_ld = x, None, 0, 0, None, 0
+    if residual is not None:
+        res_code, res_ld = _matrix(residual, "residual", (T, H), device)
+        if residual_out is None:
+            residual_out = _empty((T, H), residual.dtype, device, stream)
+            ro_ld = H
+        else:
+            ro_code, ro_ld = _matrix(residual_out, "residual_out", (T, H), device)
+            if ro_code != res_code:
+                raise TypeError(f"residual_out must be {residual.dtype}, got {residual_out.dtype}")
+        r, res, ro = residual_out, residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    _run("rk_rms_norm", lib.rk_rms_norm, device, stream, x.data_ptr(), code, ld, res, res_code, res_ld,
+         weight.data_ptr(), w_code, eps, tg, cu, ns, T, H, ro, ro_ld, out.data_ptr(), out_code, out_ld,
+         None if scales is None else scales.data_ptr(), group)
+    return r
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor | None = None,
+             cu_seqlens: torch.Tensor | None = None, *, residual: torch.Tensor | None = None,
+             eps: float = 1e-6, out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+             residual_out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """``y = r / sqrt(mean(r^2) + eps) * weight`` over rows, with ``r = x`` or, given a
+    ``residual``, their sum rounded to residual's type: returns ``(y, r)``, where r is
+    what :func:`rms_norm_bwd` takes.
+
+    ``x`` and ``residual`` are bf16 or fp32 ``[T, H]`` with any row stride, ``weight`` bf16
+    or fp32 ``[H]``, y is in ``out_dtype`` (bf16 or fp32, default: x's).  Rows with a
+    negative target or outside ``cu_seqlens`` are not read and get 0; without either every
+    row is active.  ``out`` and ``residual_out`` may be ``x`` or ``residual`` itself."""
+    _matrix(x, "x")
+    device = x.device
+    out, out_code, out_ld = _result(out, out_dtype or x.dtype, x.shape, device, stream)
+    return out, _norm(x, weight, targets, cu_seqlens, residual, eps, out, out_code, out_ld, residual_out, None,
+                      0, device, stream)
+
+
+def rms_norm_e4m3(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor | None = None,
+                  cu_seqlens: torch.Tensor | None = None, *, residual: torch.Tensor | None = None,
+                  eps: float = 1e-6, group: int = 0, out: torch.Tensor | None = None,
+                  scales: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                  stream: torch.cuda.Stream | None = None):
+    """:func:`rms_norm` with y in 8 bits: returns ``(q, scales, r)`` with ``q``
+    float8_e4m3fn ``[T, H]`` and ``y ~ q * scales``.  One scale for a row (``group`` 0,
+    ``scales`` fp32 ``[T, 1]``) or for each 128 columns (``group`` 128, ``[T, ceil(H /
+    128)]``): the largest magnitude / 448, 0 where there is none."""
+    _matrix(x, "x")
+    T, H = x.shape
+    device = x.device
+    if group != 0 and group != 128:
+        raise ValueError(f"group must be 0 (a row) or 128, got {group}")
+    if out is None:
+        out, out_ld = _empty((T, H), torch.float8_e4m3fn, device, stream), H
+    else:
+        if not isinstance(out, torch.Tensor) or out.dtype is not torch.float8_e4m3fn:
+            raise TypeError("out must be a float8_e4m3fn tensor")
+        if out.shape != (T, H) or out.device != device or (H > 1 and out.stride(1) != 1):
+            raise ValueError(f"out must be {[T, H]} on {device} with unit column stride")
+        out_ld = out.stride(0) if T > 1 else H
+    shape = (T, (H + 127) // 128 if group else 1)
+    if scales is None:
+        scales = _empty(shape, torch.float32, device, stream)
+    else:
+        _need(scales, "scales", torch.float32, 2)
+        if scales.shape != shape or scales.device != device:
+            raise ValueError(f"scales must be {list(shape)} on {device}")
+    return out, scales, _norm(x, weight, targets, cu_seqlens, residual, eps, out, 2, out_ld, residual_out,
+                              scales, group, device, stream)
+
+
+def rms_norm_bwd_workspace_size(T: int, n: int, H: int) -> int:
+    return int(load_library().rk_rms_norm_bwd_workspace_size(T, n, H))
+
+
+def rms_norm_bwd(grad_out: torch.Tensor, r: torch.Tensor, weight: torch.Tensor,
+                 targets: torch.Tensor | None = None, cu_seqlens: torch.Tensor | None = None, *,
+                 grad_residual: torch.Tensor | None = None, eps: float = 1e-6,
+                 row_order: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 out_dtype: torch.dtype | None = None, dweight: torch.Tensor | None = None,
+                 accumulate: bool = False, workspace: torch.Tensor | None = None,
+                 stream: torch.cuda.Stream | None = None):
+    """The gradient of :func:`rms_norm`: returns ``(dx, dweight)``.  ``r`` is what the
+    forward returned, ``grad_residual`` a gradient that arrives at r from elsewhere; dx
+    (``[T, H]`` in ``out_dtype``, default: r's) is the gradient of x and of residual
+    alike.  dweight, fp32 ``[H]``, is summed over the active rows in canonical order
+    (``row_order``; ascending rows by default), with ``accumulate`` onto what it holds.
+    Rows that are not among them get dx = 0.  ``out`` may be ``grad_out``, ``r`` or
+    ``grad_residual`` itself unless ``row_order`` is given."""
+    lib = _lib or load_library()
+    code, ld = _matrix(grad_out, "grad_out")
+    T, H = grad_out.shape
+    device = grad_out.device
+    r_code, r_ld = _matrix(r, "r", (T, H), device)
+    w_code = _weight(weight, H, device)
+    g, g_code, g_ld = None, 0, 0
+    if grad_residual is not None:
+        g_code, g_ld = _matrix(grad_residual, "grad_residual", (T, H), device)
+        g = grad_residual.data_ptr()
+    tg, cu, ns = _mask(targets, cu_seqlens, T, device)
+    n, order = T, None
+    if row_order is not None:
+        _need(row_order, "row_order", torch.int64, 1)
+        if row_order.device != device:
+            raise ValueError(f"row_order must be on {device}")
+        n = row_order.shape[0]
+        order = row_order.data_ptr() or _EMPTY
+    out, out_code, out_ld = _result(out, out_dtype or r.dtype, (T, H), device, stream)
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dweight to add to")
+        dweight = _empty(H, torch.float32, device, stream)
+    else:
+        _need(dweight, "dweight", torch.float32, 1)
+        if dweight.shape[0] != H or dweight.device != device:
+            raise ValueError(f"dweight must be [{H}] on {device}")
+    workspace = _scratch(workspace, lib.rk_rms_norm_bwd_workspace_size(T, n, H), device, stream)
+    _run("rk_rms_norm_bwd", lib.rk_rms_norm_bwd, device, stream, grad_out.data_ptr(), code, ld, r.data_ptr(),
+         r_code, r_ld, weight.data_ptr(), w_code, eps, g, g_code, g_ld, tg, cu, ns, T, H, order, n,
+         out.data_ptr(), out_code, out_ld, dweight.data_ptr(), int(accumulate), workspace.data_ptr(),
+         workspace.numel())
+    return out, dweight
 
 
 def selftest_wait_timeout(limit_ns: int, stream: torch.cuda.Stream | None = None) -> None:

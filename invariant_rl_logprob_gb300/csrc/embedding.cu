@@ -30,73 +30,12 @@
 #include <algorithm>
 #include <utility>
 
+#include "elements.cuh"
 #include "rk_device.cuh"
 #include "rk_internal.h"
 
 namespace rk {
 namespace {
-
-__device__ __forceinline__ void wait_prior_grid() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-// Launch with programmatic stream serialisation: the kernel's blocks may
-// become resident while the previous kernel of the stream ends; each waits
-// (wait_prior_grid) before it reads or writes anything.
-template <typename... P, typename... A>
-cudaError_t launch_dependent_smem(void (*kernel)(P...), int64_t grid, int block, size_t smem,
-                                  cudaStream_t st, A... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kernel)(P...), int64_t grid, int block, cudaStream_t st,
-                             A... args) {
-    return launch_dependent_smem(kernel, grid, block, 0, st, args...);
-}
-
-// ---- elements, eight at a time or one by one ----
-
-__device__ __forceinline__ float get1(const uint16_t *p) { return bf16_bits_to_f32(*p); }
-__device__ __forceinline__ float get1(const float *p) { return *p; }
-__device__ __forceinline__ void get8(const uint16_t *p, float (&v)[8]) {
-    const uint4 w = reinterpret_cast<const uint4 *>(p)[0];
-    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[2 * j] = bf16_lo(q[j]);
-        v[2 * j + 1] = bf16_hi(q[j]);
-    }
-}
-__device__ __forceinline__ void get8(const float *p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0];
-    const float4 b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void put1(uint16_t *p, float v) {
-    *p = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
-}
-__device__ __forceinline__ void put1(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put8(uint16_t *p, const float (&v)[8]) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void put8(float *p, const float (&v)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
 
 // ---- lookup ----
 

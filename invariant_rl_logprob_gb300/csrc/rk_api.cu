@@ -3,6 +3,7 @@
 // encoding, and dispatch to the kernels' launchers.
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -547,7 +548,7 @@ rk_status rk_linear_logp_bwd_full_saved(const uint16_t *h, const uint16_t *W,
 }
 
 static bool good_type(rk_dtype t) { return t == RK_BF16 || t == RK_FP32; }
-static int elem_size(rk_dtype t) { return t == RK_BF16 ? 2 : 4; }
+static int elem_size(rk_dtype t) { return t == RK_E4M3 ? 1 : t == RK_BF16 ? 2 : 4; }
 static bool elem_aligned(const void *p, rk_dtype t) { return aligned(p, elem_size(t)); }
 
 // Whether two ranges of memory have a byte in common.
@@ -556,17 +557,14 @@ static bool ranges_meet(const void *a, __int128 bytes_a, const void *b, __int128
     return x < y + bytes_b && y < x + bytes_a;
 }
 
-// Whether a [T, V] matrix can be made from another one that other blocks still read: in
-// its place, or with no byte of it among the other's.  (Rows side by side in one buffer have
-// none, and take the first branch; the loop is for strides of different lengths in ranges that
-// meet.)
-static bool can_hold(const rk::RulesMatrix &in, const rk::RulesMatrix &out, int64_t T, int64_t V) {
+// Whether two [T, V] matrices have no byte in common.  (Rows side by side in one buffer take
+// the first branch; the loop is for strides of different lengths in ranges that meet.)
+static bool rows_apart(const rk::RulesMatrix &in, const rk::RulesMatrix &out, int64_t T, int64_t V) {
     using i128 = __int128;  // no address or stride takes it past its range
     const i128 size_a = elem_size(in.type), size_b = elem_size(out.type);
     const i128 a = (i128)reinterpret_cast<uintptr_t>(in.p), b = (i128)reinterpret_cast<uintptr_t>(out.p);
     const i128 step_a = in.ld * size_a, step_b = out.ld * size_b;  // bytes from row to row
     const i128 row_a = V * size_a, row_b = V * size_b;             // bytes of a row
-    if (a == b && in.type == out.type && (in.ld == out.ld || T == 1)) return true;
     if (!ranges_meet(in.p, (T - 1) * step_a + row_a, out.p, (T - 1) * step_b + row_b)) return true;
     // row i of a meets row j of b if and only if b_j + row_b > a_i and b_j < a_i + row_a: the first j
     // with the former decides
@@ -585,6 +583,13 @@ static bool can_hold(const rk::RulesMatrix &in, const rk::RulesMatrix &out, int6
         if (j < T && b + j * step_b < at + row_a) return false;
     }
     return true;
+}
+
+// Whether a [T, V] matrix can be made from another one that other blocks still read: in
+// its place, or with no byte of it among the other's.
+static bool can_hold(const rk::RulesMatrix &in, const rk::RulesMatrix &out, int64_t T, int64_t V) {
+    return (in.p == out.p && in.type == out.type && (in.ld == out.ld || T == 1)) ||
+           rows_apart(in, out, T, V);
 }
 
 // Argument checks of a rules struct against T rows.
@@ -783,6 +788,118 @@ rk_status rk_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *
     e = rk::launch_embedding_bwd(dout, dout_type, ids, cu_seqlens, num_seqs, T, H, V, scale,
                                  row_order, T > 0 ? n : 0, dE, accumulate != 0, workspace, di,
                                  static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    return RK_OK;
+}
+
+// Bytes from a [T, H] matrix's first element to its last.
+static __int128 span(const rk::RulesMatrix &m, int64_t T, int64_t H) {
+    return ((__int128)(T - 1) * m.ld + H) * elem_size(m.type);
+}
+
+static bool good_matrix(const rk::RulesMatrix &m, int64_t H) {
+    return m.p && m.ld >= H && elem_aligned(m.p, m.type);
+}
+
+rk_status rk_rms_norm(const void *x, rk_dtype x_type, int64_t ld_x, const void *residual,
+                      rk_dtype residual_type, int64_t ld_residual, const void *weight,
+                      rk_dtype weight_type, float eps, const int64_t *targets,
+                      const int32_t *cu_seqlens, int32_t num_seqs, int64_t T, int64_t H,
+                      void *residual_out, int64_t ld_residual_out, void *out, rk_dtype out_type,
+                      int64_t ld_out, float *scales, int64_t group, void *stream) {
+    const bool e4m3 = out_type == RK_E4M3;
+    if (T < 0 || H <= 0 || !good_type(x_type) || !good_type(weight_type) ||
+        (!good_type(out_type) && !e4m3) || (residual && !good_type(residual_type)))
+        return RK_ERR_INVALID_ARG;
+    if (!(eps > 0.f && eps < INFINITY) || (cu_seqlens && num_seqs < 0)) return RK_ERR_INVALID_ARG;
+    if (e4m3 ? group != 0 && group != 128 : group != 0 || scales) return RK_ERR_INVALID_ARG;
+    if (T == 0) return RK_OK;
+    const rk::RulesMatrix mx{x, x_type, ld_x}, mr{residual, residual_type, ld_residual},
+        mro{residual_out, residual_type, ld_residual_out}, mo{out, out_type, ld_out};
+    if (!good_matrix(mx, H) || !good_matrix(mo, H) || !weight || !elem_aligned(weight, weight_type))
+        return RK_ERR_INVALID_ARG;
+    if (residual ? !good_matrix(mr, H) || !good_matrix(mro, H) : residual_out != nullptr)
+        return RK_ERR_INVALID_ARG;
+    if (e4m3 && (!scales || !aligned(scales, 4))) return RK_ERR_INVALID_ARG;
+    if (T >= (int64_t(1) << 31) || H > rk::kNormMaxColumns) return RK_ERR_UNSUPPORTED;
+    // results in place of x or residual, or apart from everything
+    const int64_t weight_bytes = H * elem_size(weight_type);
+    if (!can_hold(mx, mo, T, H) || ranges_meet(weight, weight_bytes, out, span(mo, T, H)))
+        return RK_ERR_INVALID_ARG;
+    if (residual && (!can_hold(mr, mo, T, H) || !can_hold(mx, mro, T, H) || !can_hold(mr, mro, T, H) ||
+                     !rows_apart(mo, mro, T, H) ||
+                     ranges_meet(weight, weight_bytes, residual_out, span(mro, T, H))))
+        return RK_ERR_INVALID_ARG;
+    if (e4m3) {
+        const __int128 bytes = (__int128)T * (group ? (H + group - 1) / group : 1) * 4;
+        if (ranges_meet(scales, bytes, x, span(mx, T, H)) || ranges_meet(scales, bytes, out, span(mo, T, H)) ||
+            ranges_meet(scales, bytes, weight, weight_bytes))
+            return RK_ERR_INVALID_ARG;
+        if (residual && (ranges_meet(scales, bytes, residual, span(mr, T, H)) ||
+                         ranges_meet(scales, bytes, residual_out, span(mro, T, H))))
+            return RK_ERR_INVALID_ARG;
+    }
+    DeviceInfo di;
+    cudaError_t e = rk::current_device_info(&di);
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    e = rk::launch_rms_norm(mx, residual ? &mr : nullptr, weight, weight_type, eps, targets, cu_seqlens,
+                            num_seqs, T, H, residual ? &mro : nullptr, mo, scales, (int)group, di,
+                            static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    return RK_OK;
+}
+
+size_t rk_rms_norm_bwd_workspace_size(int64_t T, int64_t n, int64_t H) {
+    if (T <= 0 || n < 0 || H <= 0 || H > rk::kNormMaxColumns) return 0;
+    return rk::rms_norm_bwd_workspace_bytes(T, n, H);
+}
+
+rk_status rk_rms_norm_bwd(const void *dout, rk_dtype dout_type, int64_t ld_dout, const void *r,
+                          rk_dtype r_type, int64_t ld_r, const void *weight, rk_dtype weight_type,
+                          float eps, const void *dr, rk_dtype dr_type, int64_t ld_dr,
+                          const int64_t *targets, const int32_t *cu_seqlens, int32_t num_seqs, int64_t T,
+                          int64_t H, const int64_t *row_order, int64_t n_order, void *dx,
+                          rk_dtype dx_type, int64_t ld_dx, float *dweight, int32_t accumulate,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+    if (T < 0 || H <= 0 || !good_type(dout_type) || !good_type(r_type) || !good_type(weight_type) ||
+        !good_type(dx_type) || (dr && !good_type(dr_type)))
+        return RK_ERR_INVALID_ARG;
+    if (!(eps > 0.f && eps < INFINITY) || (cu_seqlens && num_seqs < 0)) return RK_ERR_INVALID_ARG;
+    if ((accumulate != 0 && accumulate != 1) || !aligned(dweight, 4)) return RK_ERR_INVALID_ARG;
+    const int64_t n = row_order ? n_order : T;
+    if (n < 0) return RK_ERR_INVALID_ARG;
+    if (T >= (int64_t(1) << 31) || n >= (int64_t(1) << 31) || H > rk::kNormMaxColumns)
+        return RK_ERR_UNSUPPORTED;
+    const rk::RulesMatrix md{dout, dout_type, ld_dout}, mr{r, r_type, ld_r}, mg{dr, dr_type, ld_dr},
+        mx{dx, dx_type, ld_dx};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T > 0) {
+        if (!good_matrix(md, H) || !good_matrix(mr, H) || !good_matrix(mx, H) || (dr && !good_matrix(mg, H)) ||
+            !weight || !elem_aligned(weight, weight_type))
+            return RK_ERR_INVALID_ARG;
+        // A row that row_order names twice is read twice: dx is apart from what it is made of.
+        const auto fits = row_order ? rows_apart : can_hold;
+        if (!fits(md, mx, T, H) || !fits(mr, mx, T, H) || (dr && !fits(mg, mx, T, H)))
+            return RK_ERR_INVALID_ARG;
+        const int64_t weight_bytes = H * elem_size(weight_type);
+        if (ranges_meet(weight, weight_bytes, dx, span(mx, T, H))) return RK_ERR_INVALID_ARG;
+        if (dweight && (ranges_meet(dweight, H * 4, weight, weight_bytes) ||
+                        ranges_meet(dweight, H * 4, dx, span(mx, T, H)) ||
+                        ranges_meet(dweight, H * 4, dout, span(md, T, H)) ||
+                        ranges_meet(dweight, H * 4, r, span(mr, T, H)) ||
+                        (dr && ranges_meet(dweight, H * 4, dr, span(mg, T, H)))))
+            return RK_ERR_INVALID_ARG;
+        if (!workspace || workspace_bytes < rk::rms_norm_bwd_workspace_bytes(T, n, H)) return RK_ERR_WORKSPACE;
+        if (!aligned(workspace, 16)) return RK_ERR_INVALID_ARG;
+    }
+    DeviceInfo di;
+    cudaError_t e = rk::current_device_info(&di);
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    if (T == 0)
+        e = dweight && !accumulate ? cudaMemsetAsync(dweight, 0, (size_t)H * 4, st) : cudaSuccess;
+    else
+        e = rk::launch_rms_norm_bwd(md, mr, weight, weight_type, eps, dr ? &mg : nullptr, targets, cu_seqlens,
+                                    num_seqs, T, H, row_order, n, mx, dweight, accumulate != 0, workspace, di, st);
     if (e != cudaSuccess) return rk::cuda_fail(e);
     return RK_OK;
 }

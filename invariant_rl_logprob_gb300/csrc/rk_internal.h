@@ -89,7 +89,7 @@ cudaError_t launch_logits_bwd(const uint16_t *logits, const int64_t *targets, co
                               cudaStream_t st);
 
 // ---- logits under sampling rules (logits_rules.cu) ----
-struct RulesMatrix {  // logits, or what is made of them
+struct RulesMatrix {  // rows of elements: logits, hidden states, or what is made of them
     const void *p;  // written through where it is an output
     rk_dtype type;
     int64_t ld;
@@ -117,6 +117,21 @@ cudaError_t launch_embedding_bwd(const void *dout, rk_dtype dout_type, const int
                                  float scale, const int64_t *order, int64_t n, float *dE,
                                  bool accumulate, void *workspace, const DeviceInfo &di,
                                  cudaStream_t st);
+
+// ---- root-mean-square norm and its gradient (rms_norm.cu) ----
+constexpr int64_t kNormMaxColumns = 16384;
+cudaError_t launch_rms_norm(const RulesMatrix &x, const RulesMatrix *residual, const void *weight,
+                            rk_dtype weight_type, float eps, const int64_t *targets, const int32_t *cu,
+                            int num_seqs, int64_t T, int64_t H, const RulesMatrix *residual_out,
+                            const RulesMatrix &out, float *scales, int group, const DeviceInfo &di,
+                            cudaStream_t st);
+size_t rms_norm_bwd_workspace_bytes(int64_t T, int64_t n, int64_t H);
+cudaError_t launch_rms_norm_bwd(const RulesMatrix &dout, const RulesMatrix &r, const void *weight,
+                                rk_dtype weight_type, float eps, const RulesMatrix *dr,
+                                const int64_t *targets, const int32_t *cu, int num_seqs, int64_t T,
+                                int64_t H, const int64_t *order, int64_t n, const RulesMatrix &dx,
+                                float *dweight, bool accumulate, void *workspace, const DeviceInfo &di,
+                                cudaStream_t st);
 
 // ---- per-token GRPO loss (token_loss.cu) ----
 cudaError_t launch_grpo_token(const float *logp, const float *logp_old, const float *logp_ref,
