@@ -82,14 +82,15 @@ typedef enum {
                                        mask index out of range, offsets that do not
                                        ascend or leave their list, too many biases, a
                                        temperature or repetition penalty outside its
-                                       range */
+                                       range; a preference pair or its sequences'
+                                       offsets out of range; an optimizer step below 1 */
 
 /* Element type of a matrix that is passed as void*. */
 typedef enum {
     RK_BF16 = 0, /* IEEE bfloat16 bit patterns, 2 bytes */
     RK_FP32 = 1, /* 4 bytes */
     RK_E4M3 = 2  /* 8-bit floating point, 4 exponent and 3 mantissa bits, largest value 448:
-                    outputs of rk_rms_norm and states of rk_adamw_step only */
+                    an output of rk_rms_norm and the 8-bit states of rk_adamw_step */
 } rk_dtype;
 
 /*
@@ -653,6 +654,101 @@ rk_status rk_rms_norm_bwd(const void *dout, rk_dtype dout_type, int64_t ld_dout,
                           int64_t H, const int64_t *row_order, int64_t n_order, void *dx,
                           rk_dtype dx_type, int64_t ld_dx, float *dweight, int32_t accumulate,
                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Preference loss: sequences compared in pairs by their selected logprobs, a loss beside
+ * rk_grpo_token_loss at the end of the chain (chain index 9 of PR #264; a caller-given
+ * `scale` stands for the caller's fixed denominator).  For sequence q, the rows
+ * cu_seqlens[q] .. cu_seqlens[q + 1] - 1, and pair p
+ *     s[q] = sum over the sequence's active rows of (logp[t] - logp_ref[t])
+ *            (logp[t] alone if logp_ref is NULL; with `average` divided by their number)
+ *     d[p] = s[chosen[p]] - s[rejected[p]] - margin[p]           (margin NULL: 0)
+ *     loss[p] = scale * f(d[p])
+ *       RK_PREFERENCE_SIGMOID  f = (1 - e) log(1 + exp(-beta d)) + e log(1 + exp(beta d)),
+ *                              e = label_smoothing
+ *       RK_PREFERENCE_HINGE    f = max(0, 1 - beta d); f' = -beta where beta d < 1, else 0
+ *       RK_PREFERENCE_IPO      f = (d - 1 / (2 beta))^2
+ *     grad_logp[t] = d (sum of all losses) / d logp[t], the g for rk_linear_logp_bwd
+ * A sequence may be in any number of pairs (their terms are added in ascending order) or in
+ * none.  Inactive rows and rows outside all sequences get grad_logp = 0; what logp and
+ * logp_ref hold there (NaN, infinities) reaches nothing.  A sequence without active rows
+ * has s = 0.
+ * The sums over tokens are exact sums of logprobs rounded to multiples of 2^-42, in integers:
+ * s has the same bits for the same active tokens in whatever order, padding and layout.  A
+ * logprob of magnitude 2^20 and more counts as infinite; s is then infinite or NaN, and so are
+ * the losses that it is in.
+ *   logp, logp_ref, grad_logp  fp32 [T];  targets int64 [T], negative: inactive
+ *   cu_seqlens  int32 [num_seqs + 1], required: ascending, in 0 .. T.  Others set
+ *               RK_DEVERR_RULES and leave results that are not specified
+ *   chosen, rejected  int32 [P]: sequences.  Negative in either: the pair is padding (loss 0);
+ *               num_seqs and more: loss NaN, no gradient, RK_DEVERR_RULES
+ *   loss fp32 [P];  logratio fp32 [num_seqs] or NULL: s
+ *   workspace   >= rk_preference_loss_workspace_size(num_seqs, P) bytes, 16-byte aligned
+ * Requires beta > 0, 0 <= label_smoothing <= 1 (0 unless SIGMOID), num_seqs >= 0, P < 2^31.
+ */
+typedef enum {
+    RK_PREFERENCE_SIGMOID = 0,
+    RK_PREFERENCE_HINGE = 1,
+    RK_PREFERENCE_IPO = 2
+} rk_preference;
+size_t rk_preference_loss_workspace_size(int64_t num_seqs, int64_t P);
+rk_status rk_preference_loss(const float *logp, const float *logp_ref, const int64_t *targets,
+                             const int32_t *cu_seqlens, int32_t num_seqs, int64_t T,
+                             const int32_t *chosen, const int32_t *rejected, int64_t P,
+                             const float *margin, rk_preference kind, float beta,
+                             float label_smoothing, int32_t average, float scale, float *loss,
+                             float *grad_logp, float *logratio, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * AdamW step over many tensors at once: what the parameter gradients (rk_linear_logp_dw,
+ * rk_embedding_bwd, rk_rms_norm_bwd) are for.  For every element of every tensor
+ *     g = grad * grad_scale
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *     w = w - lr' weight_decay w - lr' (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ * with lr' = lr * lr_scale and w the parameter or, where there is one, its fp32 master, of
+ * which the parameter is then the rounded copy.  An element's results depend on that element
+ * alone (8-bit states: on its block of 256 elements), so the step has no order to fix.
+ *   param      bf16 or fp32 [n];  master fp32 [n] or NULL (NULL with an fp32 param)
+ *   grad       bf16 or fp32 [n]
+ *   m, v       fp32 [n], with m_scale and v_scale NULL; or e4m3 [n] with m_scale and v_scale
+ *              fp32 [ceil(n / 256)]: m = code * m_scale and v = (code * v_scale)^2 of the
+ *              element's block of 256.  The new scales are the blocks' largest |m| and sqrt(v)
+ *              / 448 (at least 2^-120, 0 where all are 0); a positive v keeps a code of 2^-9 at
+ *              least.  The update itself uses m and v as they are before they are rounded
+ *   n          0 <= n < 2^40
+ * All pointers are device memory, aligned to their element; the arrays of structs themselves
+ * are host memory, read during the call (a captured graph has its own copy).  Tensors must not
+ * overlap.
+ *   lr, beta1, beta2 in [0, 1), eps > 0, step >= 1 (the first step is 1)
+ *   lr_device    fp32 [1] or NULL: read instead of lr;  step_device int64 [1] or NULL: read
+ *                instead of step.  A graph that is replayed follows them.  A step below 1 there
+ *                sets RK_DEVERR_RULES and changes nothing
+ *   grad_scale   fp32 [1] or NULL (1): a factor of all gradients, of clipping or loss scaling
+ */
+typedef struct {
+    void *param;
+    float *master;
+    const void *grad;
+    void *m;
+    void *v;
+    float *m_scale;
+    float *v_scale;
+    int64_t n;
+    rk_dtype param_type;
+    rk_dtype grad_type;
+    float lr_scale;
+    float weight_decay;
+} rk_adamw_tensor;
+typedef struct {
+    double lr, beta1, beta2, eps;
+    int64_t step;
+    const float *lr_device;
+    const int64_t *step_device;
+    const float *grad_scale;
+} rk_adamw_options;
+rk_status rk_adamw_step(const rk_adamw_tensor *tensors, int64_t count,
+                        const rk_adamw_options *options, void *stream);
 
 /*
  * rk_linear_logp without a workspace argument, for callers that cannot

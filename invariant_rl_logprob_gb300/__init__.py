@@ -19,6 +19,10 @@ Operators (RL-Kernel issue #101, maintainer comment, P0 operator list):
   its gradient, summed per token in canonical order
 * :func:`rms_norm`, :func:`rms_norm_e4m3`, :func:`rms_norm_bwd` -- root-mean-square
   norm with the residual's addition, with an output in 8 bits, and its gradient
+* :func:`preference_loss` -- sequences compared in pairs by their selected logprobs,
+  and the gradient of every token's logprob
+* :func:`adamw_step` -- an AdamW step over the many tensors of an :class:`AdamW`,
+  with 32-bit or 8-bit states
 
 Each is bitwise invariant for a given logical row under changes of batch
 size, row position, neighbour content, padding and varlen packing.
@@ -44,6 +48,7 @@ __all__ = [
     "logp_from_logits_rules_workspace_size", "logp_from_logits_rules_bwd",
     "embedding", "embedding_bwd", "embedding_bwd_workspace_size",
     "rms_norm", "rms_norm_e4m3", "rms_norm_bwd", "rms_norm_bwd_workspace_size",
+    "preference_loss", "preference_loss_workspace_size", "AdamW", "adamw_step",
     "get_device_error", "selftest_wait_timeout", "set_row_blocks", "last_row_blocks", "DEVERR_TARGET_RANGE", "DEVERR_TIMEOUT", "DEVERR_LSE",
     "DEVERR_RULES",
 ]
@@ -183,6 +188,13 @@ def load_library() -> ctypes.CDLL:
     lib.rk_rms_norm_bwd.argtypes = [vp, i32, i64, vp, i32, i64, vp, i32, f32, vp, i32, i64, vp, vp, i32,
                                     i64, i64, vp, i64, vp, i32, i64, vp, i32, vp, sz, vp]
     lib.rk_rms_norm_bwd.restype = ctypes.c_int
+    lib.rk_preference_loss_workspace_size.argtypes = [i64, i64]
+    lib.rk_preference_loss_workspace_size.restype = sz
+    lib.rk_preference_loss.argtypes = [vp, vp, vp, vp, i32, i64, vp, vp, i64, vp, i32, f32, f32, i32, f32,
+                                       vp, vp, vp, vp, sz, vp]
+    lib.rk_preference_loss.restype = ctypes.c_int
+    lib.rk_adamw_step.argtypes = [vp, i64, vp, vp]
+    lib.rk_adamw_step.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -1165,6 +1177,212 @@ def rms_norm_bwd(grad_out: torch.Tensor, r: torch.Tensor, weight: torch.Tensor,
          out.data_ptr(), out_code, out_ld, dweight.data_ptr(), int(accumulate), workspace.data_ptr(),
          workspace.numel())
     return out, dweight
+
+
+_PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
+
+
+def preference_loss_workspace_size(num_seqs: int, P: int) -> int:
+    return int(load_library().rk_preference_loss_workspace_size(num_seqs, P))
+
+
+def preference_loss(logp: torch.Tensor, targets: torch.Tensor, cu_seqlens: torch.Tensor,
+                    chosen: torch.Tensor, rejected: torch.Tensor, *,
+                    logp_ref: torch.Tensor | None = None, margin: torch.Tensor | None = None,
+                    kind: str = "sigmoid", beta: float = 0.1, label_smoothing: float = 0.0,
+                    average: bool = False, scale: float = 1.0, workspace: torch.Tensor | None = None,
+                    stream: torch.cuda.Stream | None = None) -> dict:
+    """Preference loss of pairs of sequences: dict with fp32 ``loss`` ``[P]``, ``grad`` ``[T]``
+    (of the sum of the losses with respect to ``logp``) and ``logratio`` ``[num_seqs]``.
+
+    Sequence q is rows ``cu_seqlens[q] .. cu_seqlens[q + 1] - 1`` of ``logp`` and ``logp_ref``
+    (fp32 ``[T]``), its logratio the sum of ``logp - logp_ref`` over the rows whose target is
+    not negative, or their mean with ``average``.  Pair p compares ``d = logratio[chosen[p]] -
+    logratio[rejected[p]] - margin[p]`` (int32 ``[P]``; a negative index: no pair)::
+
+        sigmoid:  (1 - e) log(1 + exp(-beta d)) + e log(1 + exp(beta d)),  e = label_smoothing
+        hinge:    max(0, 1 - beta d)
+        ipo:      (d - 1 / (2 beta))^2
+
+    times ``scale``.  A sequence may be in any number of pairs."""
+    lib = _lib or load_library()
+    T = logp.shape[0] if isinstance(logp, torch.Tensor) and logp.dim() == 1 else 0
+    _need(logp, "logp", torch.float32, 1)
+    device = logp.device
+    if cu_seqlens is None:
+        raise TypeError("cu_seqlens must be a torch.Tensor")
+    cu, ns = _rows(targets, cu_seqlens, T, device)
+    _need(chosen, "chosen", torch.int32, 1)
+    P = chosen.shape[0]
+    _need(rejected, "rejected", torch.int32, 1)
+    if rejected.shape[0] != P or rejected.device != device or chosen.device != device:
+        raise ValueError(f"chosen and rejected must be [P] on {device}")
+    if logp_ref is not None:
+        _vector(logp_ref, "logp_ref", T, device)
+    if margin is not None:
+        _need(margin, "margin", torch.float32, 1)
+        if margin.shape[0] != P or margin.device != device:
+            raise ValueError(f"margin must be [P] on {device}")
+    code = _PREFERENCE_KINDS.get(kind)
+    if code is None:
+        raise ValueError(f"kind must be one of {sorted(_PREFERENCE_KINDS)}, got {kind!r}")
+    loss = _empty(P, torch.float32, device, stream)
+    grad = _empty(T, torch.float32, device, stream)
+    ratio = _empty(ns, torch.float32, device, stream)
+    workspace = _scratch(workspace, lib.rk_preference_loss_workspace_size(ns, P), device, stream)
+    _run("rk_preference_loss", lib.rk_preference_loss, device, stream, logp.data_ptr(),
+         None if logp_ref is None else logp_ref.data_ptr(), targets.data_ptr(), cu.data_ptr(), ns, T,
+         chosen.data_ptr(), rejected.data_ptr(), P, None if margin is None else margin.data_ptr(), code,
+         beta, label_smoothing, int(average), scale, loss.data_ptr(), grad.data_ptr(), ratio.data_ptr(),
+         workspace.data_ptr(), workspace.numel())
+    return {"loss": loss, "grad": grad, "logratio": ratio}
+
+
+class _AdamWTensor(ctypes.Structure):
+    """rk_adamw_tensor of include/rk.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + \
+        [("n", ctypes.c_int64), ("param_type", ctypes.c_int), ("grad_type", ctypes.c_int),
+         ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class _AdamWOptions(ctypes.Structure):
+    """rk_adamw_options of include/rk.h."""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + [("step", ctypes.c_int64)] + \
+        [(n, ctypes.c_void_p) for n in ("lr_device", "step_device", "grad_scale")]
+
+
+class AdamW:
+    """The tensors of an AdamW step: parameters, gradients and states.
+
+    ``params`` are contiguous bf16 or fp32 CUDA tensors, ``grads`` (bf16 or fp32) have
+    their shapes.  ``master`` holds fp32 copies that the step updates and rounds to the
+    parameters: None (none), True (made here for the bf16 parameters) or a list whose
+    entries may be None.  The states are made here, as zeros of ``bits`` 32 or 8, or given:
+    ``m`` and ``v`` in fp32, or in float8_e4m3fn with ``m_scale`` and ``v_scale`` (fp32, one
+    for each 256 elements): ``m = code * scale``, ``v = (code * scale)^2``.
+    ``weight_decay`` and ``lr_scale`` are numbers, or lists with one for each tensor.
+
+    All are kept by the object and changed in place by :func:`adamw_step`; a replayed CUDA
+    graph of the step needs the object alive."""
+
+    def __init__(self, params, grads, m=None, v=None, *, m_scale=None, v_scale=None, master=None,
+                 bits: int = 32, weight_decay=0.0, lr_scale=1.0):
+        params = list(params)
+        count = len(params)
+        self.device = params[0].device if count and isinstance(params[0], torch.Tensor) else None
+        each = lambda x, name: self._each(x, name, count)  # noqa: E731
+        if (m is None) != (v is None):
+            raise ValueError("m and v go together")
+        if (m_scale is None) != (v_scale is None) or (m is None and m_scale is not None):
+            raise ValueError("m_scale and v_scale go together, with m and v")
+        for p in params:
+            self._check(p, "a parameter", (torch.bfloat16, torch.float32), None)
+        if m is None:
+            if bits not in (8, 32):
+                raise ValueError(f"bits must be 8 or 32, got {bits}")
+            kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
+            blank = lambda p: torch.zeros(p.shape, dtype=torch.uint8 if bits == 8 else kind, device=p.device).view(kind)  # noqa: E731
+            m, v = [blank(p) for p in params], [blank(p) for p in params]
+            if bits == 8:
+                scales = lambda: [torch.zeros((p.numel() + 255) // 256, device=p.device) for p in params]  # noqa: E731
+                m_scale, v_scale = scales(), scales()
+        if master is True:
+            master = [p.float() if p.dtype is torch.bfloat16 else None for p in params]
+        self.params, self.m, self.v = params, each(m, "m"), each(v, "v")
+        self.m_scale, self.v_scale = (None, None) if m_scale is None else (each(m_scale, "m_scale"), each(v_scale, "v_scale"))
+        self.master = None if master is None else each(master, "master")
+        decay = each(weight_decay if hasattr(weight_decay, "__len__") else [weight_decay] * count, "weight_decay")
+        rates = each(lr_scale if hasattr(lr_scale, "__len__") else [lr_scale] * count, "lr_scale")
+        state = (torch.float32,) if m_scale is None else (torch.float8_e4m3fn,)
+        self._array = (_AdamWTensor * max(count, 1))()
+        for i, p in enumerate(params):
+            n = p.numel()
+            s = self._array[i]
+            s.param, s.n, s.param_type = p.data_ptr(), n, _TYPE_CODES[p.dtype]
+            s.lr_scale, s.weight_decay = rates[i], decay[i]
+            for name, t in (("m", self.m[i]), ("v", self.v[i])):
+                self._check(t, name, state, n)
+                setattr(s, name, t.data_ptr())
+            if m_scale is not None:
+                for name, t in (("m_scale", self.m_scale[i]), ("v_scale", self.v_scale[i])):
+                    self._check(t, name, (torch.float32,), (n + 255) // 256)
+                    setattr(s, name, t.data_ptr() or _EMPTY)
+            if self.master is not None and self.master[i] is not None:
+                self._check(self.master[i], "master", (torch.float32,), n)
+                if p.dtype is torch.float32:
+                    raise ValueError("an fp32 parameter has no master")
+                s.master = self.master[i].data_ptr()
+        self.address, self.count = ctypes.addressof(self._array), count
+        self.use_grads(grads)
+
+    def use_grads(self, grads) -> None:
+        """Takes other tensors as the gradients of the next steps."""
+        grads = self._each(grads, "grads", self.count)
+        for p, g in zip(self.params, grads):
+            self._check(g, "a gradient", (torch.bfloat16, torch.float32), p.numel())
+        for s, g in zip(self._array, grads):
+            s.grad, s.grad_type = g.data_ptr(), _TYPE_CODES[g.dtype]
+        self.grads = grads
+
+    @staticmethod
+    def _each(x, name, count):
+        x = list(x)
+        if len(x) != count:
+            raise ValueError(f"{name} must have one entry for each of the {count} parameters, got {len(x)}")
+        return x
+
+    def _check(self, t, name, dtypes, numel) -> None:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (no CPU path), got {t.device}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        if not t.is_contiguous() or (numel is not None and t.numel() != numel):
+            raise ValueError(f"{name} must be contiguous" + ("" if numel is None else f" with {numel} elements"))
+
+
+def _scalar(t, name, dtype, device):
+    """Address of a one-element tensor that the device reads, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or t.numel() != 1 or t.device != device:
+        raise ValueError(f"{name} must be one {dtype} on {device}")
+    return t.data_ptr()
+
+
+def adamw_step(tensors: AdamW, *, lr: float | torch.Tensor, step: int | torch.Tensor, beta1: float = 0.9,
+               beta2: float = 0.999, eps: float = 1e-8, grad_scale: torch.Tensor | None = None,
+               stream: torch.cuda.Stream | None = None) -> None:
+    """One AdamW step of all ``tensors``, in place::
+
+        g = grad * grad_scale
+        m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+        w = w - lr' weight_decay w - lr' (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+
+    with ``lr' = lr * lr_scale``.  ``step`` counts from 1.  ``lr`` (fp32) and ``step`` (int64)
+    may be one-element CUDA tensors, read when the step runs: a replayed CUDA graph follows
+    them.  ``grad_scale`` is such a tensor too (fp32), a factor of all gradients."""
+    if not isinstance(tensors, AdamW):
+        raise TypeError("tensors must be an AdamW")
+    lib = _lib or load_library()
+    device = tensors.device
+    if tensors.count == 0:
+        return
+    o = _AdamWOptions(0.0, beta1, beta2, eps, 1, None, None, _scalar(grad_scale, "grad_scale", torch.float32, device))
+    if isinstance(lr, torch.Tensor):
+        o.lr_device = _scalar(lr, "lr", torch.float32, device)
+    else:
+        o.lr = lr
+    if isinstance(step, torch.Tensor):
+        o.step_device = _scalar(step, "step", torch.int64, device)
+    else:
+        o.step = step
+    _run("rk_adamw_step", lib.rk_adamw_step, device, stream, tensors.address, tensors.count, ctypes.addressof(o))
 
 
 def selftest_wait_timeout(limit_ns: int, stream: torch.cuda.Stream | None = None) -> None:

@@ -1,0 +1,278 @@
+// adamw.cu -- one AdamW step over many tensors, with 32-bit states or states
+// in 8 bits, and fp32 master weights beside bf16 parameters (what consumes
+// the parameter gradients of issue #244, Workstream 3 #153: linear_logp_dw,
+// embedding_bwd, rms_norm_bwd).
+//
+//   g = grad * grad_scale
+//   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+//   w = w - lr wd w - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+//
+// Bound by memory: 22 to 30 bytes an element with 32-bit states, 12 to 18 with
+// 8-bit ones.  Every result depends on its own element (in 8 bits: on its block of 256
+// elements) alone.  One launch takes up to kTensors tensors, described in the
+// kernel's parameters (nothing to copy, nothing to keep alive for a graph);
+// a block takes kChunk elements of one of them, a warp 256 at a time, a thread 8
+// consecutive ones, so that a block of 8-bit states is a warp's.
+//
+// 8-bit states: m = e4m3 * scale, and for v its root, u = e4m3 * scale (e4m3
+// spans 2^18, so v spans 2^36 within a block); scale = largest magnitude of
+// the new block / 448.  A positive u takes the code 2^-9 at least: an element whose m
+// is kept while its v is rounded away would be divided by eps alone.
+#include <algorithm>
+#include <cmath>
+
+#include "elements.cuh"
+#include "rk_device.cuh"
+#include "rk_internal.h"
+
+namespace rk {
+namespace {
+
+constexpr int kTensors = 256;    // of a launch
+constexpr int kThreads = 256;
+constexpr int kBlock = 256;      // elements that share a scale: a warp's, 8 a lane
+constexpr int kChunk = 8 * kThreads * 2;  // elements of a block
+
+struct Tensor {
+    void *param;
+    float *master;
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    int64_t n;
+    float lr_scale, weight_decay;
+    uint8_t param_wide, grad_wide, vec;
+};
+
+struct Table {
+    int32_t first[kTensors + 1];  // chunks before each tensor
+    int32_t count;
+    float lr, rise, root;  // learning rate, 1 / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
+    float beta1, rest1, log1, beta2, rest2, log2, eps;  // rest = 1 - beta, log = log(beta)
+    const float *lr_device;
+    const int64_t *step_device;
+    const float *grad_scale;
+    unsigned *err;
+    Tensor tensor[kTensors];
+};
+static_assert(sizeof(Table) <= 32764, "kernel parameters");
+
+// ---- e4m3 ----
+
+__device__ __forceinline__ void unpack_e4m3x8(uint2 w, float (&v)[8]) {
+    const uint32_t q[2] = {w.x, w.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint16_t pair = (uint16_t)(q[i / 2] >> 16 * (i % 2));
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(pair));
+        asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+            : "=f"(v[2 * i]), "=f"(v[2 * i + 1])
+            : "r"(h));
+    }
+}
+
+// The codes of a warp's block of values and, for its first lane to write, their scale.
+__device__ __forceinline__ uint2 encode(float (&x)[8], bool floor, float *scale) {
+    unsigned top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fmaxf(fabsf(x[i]), 0.f)));
+    top = __reduce_max_sync(0xffffffffu, top);
+    // 2^-120 at least, for a finite reciprocal
+    const float s = top ? fmaxf(__fdiv_rn(__uint_as_float(top), 448.f), 0x1p-120f) : 0.f;
+    const float inverse = top ? __frcp_rn(s) : 0.f;
+    *scale = s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float q = __fmul_rn(x[i], inverse);
+        if (floor && x[i] > 0.f) q = fmaxf(q, 0x1p-9f);
+        x[i] = q;
+    }
+    return pack_e4m3x8(x);
+}
+
+// ---- 8 elements of a tensor ----
+
+template <typename T>
+__device__ __forceinline__ void get(const T *p, int64_t at, int left, bool vec, float (&v)[8]) {
+    if (vec && left >= 8) {
+        get8(p + at, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? get1(p + at + i) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void put(T *p, int64_t at, int left, bool vec, const float (&v)[8]) {
+    if (vec && left >= 8) {
+        put8(p + at, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) put1(p + at + i, v[i]);
+    }
+}
+__device__ __forceinline__ uint2 get_codes(const void *p, int64_t at, int left, bool vec) {
+    const uint8_t *q = static_cast<const uint8_t *>(p) + at;
+    if (vec && left >= 8) return *reinterpret_cast<const uint2 *>(q);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) w[i / 4] |= (uint32_t)q[i] << 8 * (i % 4);
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void put_codes(void *p, int64_t at, int left, bool vec, uint2 c) {
+    uint8_t *q = static_cast<uint8_t *>(p) + at;
+    if (vec && left >= 8) {
+        *reinterpret_cast<uint2 *>(q) = c;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) q[i] = (uint8_t)((i < 4 ? c.x : c.y) >> 8 * (i % 4));
+}
+
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table a) {
+    wait_prior_grid();
+    // the block's tensor
+    int lo = 0, hi = a.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.first[mid] <= (int)blockIdx.x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const Tensor &t = a.tensor[lo];
+    float rise = a.rise, root = a.root;
+    if (a.step_device) {
+        const int64_t step = *a.step_device;
+        if (step < 1) {
+            if (threadIdx.x == 0) atomicOr(a.err, kErrRules);
+            return;
+        }
+        // 1 - beta^step = -expm1(step log(beta)): no difference of numbers close to 1
+        rise = __fdiv_rn(1.f, -expm1f((float)step * a.log1));
+        root = __fdiv_rn(1.f, __fsqrt_rn(-expm1f((float)step * a.log2)));
+    }
+    const float lr = __fmul_rn(a.lr_device ? *a.lr_device : a.lr, t.lr_scale);
+    const float rate = __fmul_rn(lr, rise), decay = __fmul_rn(lr, t.weight_decay);
+    const float scale = a.grad_scale ? *a.grad_scale : 1.f;
+    const bool vec = t.vec, eight = t.m_scale != nullptr;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t chunk = (int64_t)((int)blockIdx.x - a.first[lo]) * kChunk;
+    for (int64_t block = chunk + warp * kBlock; block < min(t.n, chunk + kChunk); block += kThreads / 32 * kBlock) {
+        const int64_t at = block + 8 * lane;
+        const int left = (int)min((int64_t)8, max((int64_t)0, t.n - at));
+        float g[8], m[8], v[8], w[8];
+        if (t.grad_wide)
+            get(static_cast<const float *>(t.grad), at, left, vec, g);
+        else
+            get(static_cast<const uint16_t *>(t.grad), at, left, vec, g);
+        if (t.master)
+            get(t.master, at, left, vec, w);
+        else if (t.param_wide)
+            get(static_cast<const float *>(t.param), at, left, vec, w);
+        else
+            get(static_cast<const uint16_t *>(t.param), at, left, vec, w);
+        if (eight) {
+            unpack_e4m3x8(get_codes(t.m, at, left, vec), m);
+            unpack_e4m3x8(get_codes(t.v, at, left, vec), v);
+            const float ms = t.m_scale[block / kBlock], vs = t.v_scale[block / kBlock];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                m[i] = __fmul_rn(m[i], ms);
+                v[i] = __fmul_rn(v[i], vs);
+                v[i] = __fmul_rn(v[i], v[i]);
+            }
+        } else {
+            get(static_cast<const float *>(t.m), at, left, vec, m);
+            get(static_cast<const float *>(t.v), at, left, vec, v);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = __fmul_rn(g[i], scale);
+            m[i] = __fmaf_rn(m[i], a.beta1, __fmul_rn(x, a.rest1));
+            v[i] = __fmaf_rn(v[i], a.beta2, __fmul_rn(__fmul_rn(x, x), a.rest2));
+            const float u = __fsqrt_rn(v[i]);
+            const float move = __fdiv_rn(__fmul_rn(m[i], rate), __fmaf_rn(u, root, a.eps));
+            w[i] = __fsub_rn(__fmaf_rn(-decay, w[i], w[i]), move);
+            if (eight) v[i] = u;
+        }
+        if (t.master) put(t.master, at, left, vec, w);
+        if (t.param_wide)
+            put(static_cast<float *>(t.param), at, left, vec, w);
+        else
+            put(static_cast<uint16_t *>(t.param), at, left, vec, w);
+        if (eight) {
+            float ms, vs;
+            const uint2 mc = encode(m, false, &ms), vc = encode(v, true, &vs);
+            put_codes(t.m, at, left, vec, mc);
+            put_codes(t.v, at, left, vec, vc);
+            if (lane == 0) {
+                t.m_scale[block / kBlock] = ms;
+                t.v_scale[block / kBlock] = vs;
+            }
+        } else {
+            put(static_cast<float *>(t.m), at, left, vec, m);
+            put(static_cast<float *>(t.v), at, left, vec, v);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const rk_adamw_tensor *tensors, int64_t count, const rk_adamw_options &o,
+                         const DeviceInfo &di, cudaStream_t st) {
+    Table a;
+    const double step = o.step_device ? 1.0 : (double)o.step;
+    a.lr = (float)o.lr;
+    a.rise = (float)(1.0 / -std::expm1(step * std::log(o.beta1)));
+    a.root = (float)(1.0 / std::sqrt(-std::expm1(step * std::log(o.beta2))));
+    a.beta1 = (float)o.beta1;
+    a.rest1 = (float)(1.0 - o.beta1);
+    a.log1 = (float)std::log(o.beta1);
+    a.beta2 = (float)o.beta2;
+    a.rest2 = (float)(1.0 - o.beta2);
+    a.log2 = (float)std::log(o.beta2);
+    a.eps = (float)o.eps;
+    a.lr_device = o.lr_device;
+    a.step_device = o.step_device;
+    a.grad_scale = o.grad_scale;
+    a.err = di.err;
+    for (int64_t i = 0; i < count;) {
+        a.count = 0;
+        int64_t chunks = 0;
+        for (; i < count && a.count < kTensors; ++i) {
+            const rk_adamw_tensor &s = tensors[i];
+            if (s.n == 0) continue;
+            const int64_t more = (s.n + kChunk - 1) / kChunk;
+            if (chunks + more > 0x7fffffff) break;
+            Tensor &t = a.tensor[a.count];
+            t.param = s.param;
+            t.master = s.master;
+            t.grad = s.grad;
+            t.m = s.m;
+            t.v = s.v;
+            t.m_scale = s.m_scale;
+            t.v_scale = s.v_scale;
+            t.n = s.n;
+            t.lr_scale = s.lr_scale;
+            t.weight_decay = s.weight_decay;
+            t.param_wide = s.param_type == RK_FP32;
+            t.grad_wide = s.grad_type == RK_FP32;
+            const uintptr_t state = s.m_scale ? 8 : 16;
+            t.vec = aligned(s.param, 16) && aligned(s.grad, 16) && aligned(s.master, 16) && aligned(s.m, state) &&
+                    aligned(s.v, state);
+            a.first[a.count++] = (int32_t)chunks;
+            chunks += more;
+        }
+        if (a.count == 0) break;
+        a.first[a.count] = (int32_t)chunks;
+        const cudaError_t e = launch_dependent(adamw_kernel, chunks, kThreads, st, a);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace rk

@@ -904,6 +904,90 @@ rk_status rk_rms_norm_bwd(const void *dout, rk_dtype dout_type, int64_t ld_dout,
     return RK_OK;
 }
 
+size_t rk_preference_loss_workspace_size(int64_t num_seqs, int64_t P) {
+    if (num_seqs < 0 || P < 0) return 0;
+    return rk::preference_workspace_bytes(num_seqs, P);
+}
+
+rk_status rk_preference_loss(const float *logp, const float *logp_ref, const int64_t *targets,
+                             const int32_t *cu_seqlens, int32_t num_seqs, int64_t T,
+                             const int32_t *chosen, const int32_t *rejected, int64_t P,
+                             const float *margin, rk_preference kind, float beta,
+                             float label_smoothing, int32_t average, float scale, float *loss,
+                             float *grad_logp, float *logratio, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    if (T < 0 || P < 0 || num_seqs < 0 || !cu_seqlens) return RK_ERR_INVALID_ARG;
+    if (kind != RK_PREFERENCE_SIGMOID && kind != RK_PREFERENCE_HINGE && kind != RK_PREFERENCE_IPO)
+        return RK_ERR_INVALID_ARG;
+    if (!(beta > 0.f && beta < INFINITY) || !(label_smoothing >= 0.f && label_smoothing <= 1.f) ||
+        (label_smoothing != 0.f && kind != RK_PREFERENCE_SIGMOID) || (average != 0 && average != 1))
+        return RK_ERR_INVALID_ARG;
+    if (T == 0 && P == 0 && num_seqs == 0) return RK_OK;
+    if (T > 0 && (!logp || !targets || !grad_logp)) return RK_ERR_INVALID_ARG;
+    if (P > 0 && (!chosen || !rejected || !loss)) return RK_ERR_INVALID_ARG;
+    const int64_t lim = int64_t(1) << 31;
+    if (T >= lim || P >= lim) return RK_ERR_UNSUPPORTED;
+    if (!aligned(logp, 4) || !aligned(logp_ref, 4) || !aligned(targets, 8) || !aligned(cu_seqlens, 4) ||
+        !aligned(chosen, 4) || !aligned(rejected, 4) || !aligned(margin, 4) || !aligned(loss, 4) ||
+        !aligned(grad_logp, 4) || !aligned(logratio, 4))
+        return RK_ERR_INVALID_ARG;
+    // results apart from what is read, and from one another
+    const struct { const void *p; int64_t bytes; } in[] = {
+        {logp, T * 4}, {logp_ref, T * 4}, {targets, T * 8}, {cu_seqlens, ((int64_t)num_seqs + 1) * 4},
+        {chosen, P * 4}, {rejected, P * 4}, {margin, P * 4},
+    }, out[] = {{loss, P * 4}, {grad_logp, T * 4}, {logratio, (int64_t)num_seqs * 4}};
+    for (int i = 0; i < 3; ++i) {
+        if (!out[i].p || !out[i].bytes) continue;
+        for (const auto &b : in)
+            if (b.p && b.bytes && ranges_meet(out[i].p, out[i].bytes, b.p, b.bytes)) return RK_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (out[j].p && out[j].bytes && ranges_meet(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                return RK_ERR_INVALID_ARG;
+    }
+    if (!workspace || workspace_bytes < rk::preference_workspace_bytes(num_seqs, P)) return RK_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return RK_ERR_INVALID_ARG;
+    DeviceInfo di;
+    cudaError_t e = rk::current_device_info(&di);
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    e = rk::launch_preference(logp, logp_ref, targets, cu_seqlens, num_seqs, T, chosen, rejected, P, margin,
+                              (int)kind, beta, label_smoothing, average != 0, scale, loss, grad_logp, logratio,
+                              workspace, di, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    return RK_OK;
+}
+
+rk_status rk_adamw_step(const rk_adamw_tensor *tensors, int64_t count, const rk_adamw_options *options,
+                        void *stream) {
+    if (count < 0 || !options || (count > 0 && !tensors)) return RK_ERR_INVALID_ARG;
+    const rk_adamw_options &o = *options;
+    if (!std::isfinite(o.lr) || !(o.beta1 >= 0.0 && o.beta1 < 1.0) || !(o.beta2 >= 0.0 && o.beta2 < 1.0) ||
+        !((float)o.eps > 0.f && std::isfinite((float)o.eps)) || (!o.step_device && o.step < 1) ||
+        !aligned(o.lr_device, 4) || !aligned(o.step_device, 8) || !aligned(o.grad_scale, 4))
+        return RK_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < count; ++i) {
+        const rk_adamw_tensor &t = tensors[i];
+        if (t.n < 0 || !good_type(t.param_type) || !good_type(t.grad_type) || !std::isfinite(t.lr_scale) ||
+            !std::isfinite(t.weight_decay))
+            return RK_ERR_INVALID_ARG;
+        if ((t.m_scale == nullptr) != (t.v_scale == nullptr) || (t.master && t.param_type == RK_FP32))
+            return RK_ERR_INVALID_ARG;
+        if (t.n >= (int64_t(1) << 40)) return RK_ERR_UNSUPPORTED;
+        if (t.n == 0) continue;
+        if (!t.param || !t.grad || !t.m || !t.v) return RK_ERR_INVALID_ARG;
+        const int state = t.m_scale ? 1 : 4;
+        if (!elem_aligned(t.param, t.param_type) || !elem_aligned(t.grad, t.grad_type) || !aligned(t.master, 4) ||
+            !aligned(t.m, state) || !aligned(t.v, state) || !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
+            return RK_ERR_INVALID_ARG;
+    }
+    if (count == 0) return RK_OK;
+    DeviceInfo di;
+    cudaError_t e = rk::current_device_info(&di);
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    e = rk::launch_adamw(tensors, count, o, di, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return rk::cuda_fail(e);
+    return RK_OK;
+}
+
 rk_status rk_selftest_wait_timeout(int64_t limit_ns, void *stream) {
     if (limit_ns <= 0 || limit_ns > 10000000000ll) return RK_ERR_INVALID_ARG;
     DeviceInfo di;

@@ -140,6 +140,18 @@ cudaError_t launch_grpo_token(const float *logp, const float *logp_old, const fl
                               float scale, float *loss, float *grad, float *ratio, float *kl,
                               const DeviceInfo &di, cudaStream_t st);
 
+// ---- preference loss (preference.cu) ----
+size_t preference_workspace_bytes(int64_t num_seqs, int64_t P);
+cudaError_t launch_preference(const float *logp, const float *ref, const int64_t *targets, const int32_t *cu,
+                              int num_seqs, int64_t T, const int32_t *chosen, const int32_t *rejected, int64_t P,
+                              const float *margin, int kind, float beta, float smoothing, bool average, float scale,
+                              float *loss, float *grad, float *logratio, void *workspace, const DeviceInfo &di,
+                              cudaStream_t st);
+
+// ---- AdamW step (adamw.cu) ----
+cudaError_t launch_adamw(const rk_adamw_tensor *tensors, int64_t count, const rk_adamw_options &o,
+                         const DeviceInfo &di, cudaStream_t st);
+
 // ---- backward: columns handled exactly in fp32 ----
 // In every backward row, the target column and every column with
 // p = exp(z - lse) >= kEntTau leave the bf16 g*softmax matrix (they are
