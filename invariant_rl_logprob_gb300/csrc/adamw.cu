@@ -79,12 +79,15 @@ __device__ __forceinline__ uint2 encode(float (&x)[8], bool floor, float *scale)
     for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fmaxf(fabsf(x[i]), 0.f)));
     top = __reduce_max_sync(0xffffffffu, top);
     // 2^-120 at least, for a finite reciprocal
-    const float s = top ? fmaxf(__fdiv_rn(__uint_as_float(top), 448.f), 0x1p-120f) : 0.f;
+    const float s = top ? fmaxf(__fmul_rn(__uint_as_float(top), 1.f / 448.f), 0x1p-120f) : 0.f;
     const float inverse = top ? __frcp_rn(s) : 0.f;
     *scale = s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float q = __fmul_rn(x[i], inverse);
+        // x / s, correctly rounded (Markstein, 1990: a faithful quotient and its remainder times
+        // the rounded reciprocal): a code next to a border is that of the quotient
+        const float near = __fmul_rn(x[i], inverse);
+        float q = __fmaf_rn(__fmaf_rn(-near, s, x[i]), inverse, near);
         if (floor && x[i] > 0.f) q = fmaxf(q, 0x1p-9f);
         x[i] = q;
     }
@@ -192,10 +195,12 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float x = __fmul_rn(g[i], scale);
-            m[i] = __fmaf_rn(m[i], a.beta1, __fmul_rn(x, a.rest1));
-            v[i] = __fmaf_rn(v[i], a.beta2, __fmul_rn(__fmul_rn(x, x), a.rest2));
+            // every product and sum of the states is rounded by itself: they are what elementary
+            // fp32 operations give, and so are their codes
+            m[i] = __fadd_rn(__fmul_rn(m[i], a.beta1), __fmul_rn(x, a.rest1));
+            v[i] = __fadd_rn(__fmul_rn(v[i], a.beta2), __fmul_rn(__fmul_rn(x, x), a.rest2));
             const float u = __fsqrt_rn(v[i]);
-            const float move = __fdiv_rn(__fmul_rn(m[i], rate), __fmaf_rn(u, root, a.eps));
+            const float move = __fdividef(__fmul_rn(m[i], rate), __fmaf_rn(u, root, a.eps));
             w[i] = __fsub_rn(__fmaf_rn(-decay, w[i], w[i]), move);
             if (eight) v[i] = u;
         }

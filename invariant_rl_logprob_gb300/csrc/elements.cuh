@@ -68,6 +68,33 @@ __device__ __forceinline__ void put8(float *p, const float (&v)[8]) {
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// Two products, sums or fused sums of fp32 at once, each rounded as the single operation.
+__device__ __forceinline__ void mul2(float &x0, float &x1, float y0, float y1) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(x0), "+f"(x1)
+        : "f"(y0), "f"(y1));
+}
+__device__ __forceinline__ void add2(float &x0, float &x1, float y0, float y1) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(x0), "+f"(x1)
+        : "f"(y0), "f"(y1));
+}
+// z = x y + z
+__device__ __forceinline__ void fma2(float &z0, float &z1, float x0, float x1, float y0, float y1) {
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%0, %1};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "+f"(z0), "+f"(z1)
+        : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
+}
+// Two bf16 sums, each rounded once.
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Two floats -> packed e4m3x2 (round to nearest even, saturating at 448; NaN
 // stays NaN); `lo` in bits 0-7.
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {

@@ -12,12 +12,10 @@
 //   dx = rstd * (g - n * mean(g * n)) + dr,   dweight (+)= sum over rows of dout * n
 //
 // Both are bound by memory: 8 and 15 flop an element, against 7 to 12 bytes.
-// A team of threads (a warp up to 512 columns, a block beyond) owns a run of
-// consecutive rows and a ring of stages in shared memory; one of its warps
-// copies whole rows into the ring with cp.async.bulk, several rows ahead, so
-// that what is in flight does not depend on registers or on the rows' sums.
-// Copies start and end on 16-byte boundaries around the row (the bytes beside
-// it are not looked at), so a row may start on any element.
+// A team of threads (a warp up to 1024 columns, up to 16 warps beyond) has a
+// row in registers, as it was read: bf16 words where all is bf16 on 16-byte
+// boundaries, floats otherwise.  A thread owns up to 32 columns: fewer threads
+// a row mean fewer that sum, scale and wait for one another.
 //
 // The backward needs nothing but r: the sums of r^2 and of g * r come out of
 // one reduction.  dweight: a team adds its rows in registers, in order; blocks
@@ -25,9 +23,9 @@
 //
 // Which thread owns which column, and with it the order of every sum, depends
 // on H alone: eight consecutive columns where H is a multiple of 8, columns
-// TEAM apart otherwise (stores stay coalesced).  The team's run of rows
-// depends on the number of canonical rows alone.  A sum of squares that
-// leaves fp32 is formed again from r * 2^-80.
+// TEAM apart otherwise (loads and stores stay coalesced).  Which rows a team
+// of the backward takes depends on the number of canonical rows alone.  A sum
+// of squares that leaves fp32 is formed again from r * 2^-80.
 #include <algorithm>
 
 #include "elements.cuh"
@@ -37,316 +35,144 @@
 namespace rk {
 namespace {
 
-constexpr int kMaxStages = 8;
-constexpr int kMaxUnit = 16;           // rows of a stage
-constexpr int kSharedPerSm = 227 * 1024;
-constexpr float kShrink = 0x1p-80f;    // for rows whose sum of squares leaves fp32
+constexpr float kShrink = 0x1p-80f;  // for rows whose sum of squares leaves fp32
 
-// ---- rows on their way into shared memory ----
-
-struct Input {
-    const char *p;
+struct Matrix {
+    char *p;
     int64_t step;  // bytes from row to row
-    int32_t bytes; // of a row
-    int32_t wide;  // fp32 (else bf16)
-    int32_t slot;  // bytes that a row may take in a stage
-    int32_t offset;  // where the input's slots begin in a stage
+    int32_t type;  // rk_dtype
+    __device__ __forceinline__ char *row(int64_t t) const { return p + t * step; }
 };
 
-struct Ring {
-    Input in[3];
-    int32_t inputs, stages, stage_bytes, unit;
-    int32_t compact;  // rows follow one another without a gap, in every input
-};
-
-struct TeamHead {
-    uint64_t full[kMaxStages];
-    int32_t row[kMaxStages][kMaxUnit];  // of each row in a stage; -1: inactive, not copied
-    int32_t merged[kMaxStages];         // the stage's rows came as one copy
-    int32_t abort;
-    int32_t pad[7];
-};
-static_assert(sizeof(TeamHead) % 16 == 0, "rings start on 16 bytes");
-
-// Untiled bulk copy global -> shared; both addresses and the size are multiples of 16.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
+__device__ __forceinline__ bool on(const void *p, unsigned a) {
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
-
-// The rows [begin, end) of a list, unit by unit; `row_of(i)` is the physical row
-// of entry i, or -1.  Every unit completes one phase of its stage's barrier,
-// whether or not it has anything to copy.
-template <typename RowOf>
-struct Feed {
-    const Ring &g;
-    TeamHead *head;
-    unsigned char *ring;
-    RowOf row_of;
-    int64_t begin, end;
-    int units;
-    int next, next_stage;  // the unit to be issued, and its stage
-    int pending;           // its rows, one a lane
-    int stage;             // of the unit to be read
-    unsigned phases;
-
-    __device__ __forceinline__ Feed(const Ring &ring_, TeamHead *head_, unsigned char *at, RowOf f, int64_t b,
-                                    int64_t e)
-        : g(ring_), head(head_), ring(at), row_of(f), begin(b), end(e),
-          units(e > b ? (int)((e - b + ring_.unit - 1) / ring_.unit) : 0), next(0), next_stage(0), stage(0),
-          phases(0) {}
-
-    __device__ __forceinline__ int rows_in(int unit) const {
-        const int64_t left = end - begin - (int64_t)unit * g.unit;
-        return left < g.unit ? (int)left : g.unit;
-    }
-    __device__ __forceinline__ int lookup(int unit, int lane) const {
-        return unit < units && lane < rows_in(unit) ? row_of(begin + (int64_t)unit * g.unit + lane) : -1;
-    }
-
-    // By one warp: barriers, and the first stages on their way.
-    __device__ __forceinline__ void start(int lane) {
-        if (lane == 0) {
-            head->abort = 0;
-            for (int s = 0; s < g.stages; ++s) mbar_init(smem_u32(&head->full[s]), 1);
-            fence_mbar_init();
-        }
-        __syncwarp();
-        pending = lookup(0, lane);
-        for (int s = 0; s < g.stages; ++s) issue(lane);
-    }
-
-    // By one warp: the next unit on its way; nobody reads its stage any more.
-    __device__ __forceinline__ void issue(int lane) {
-        if (next >= units) return;
-        const int row = pending, s = next_stage;
-        pending = lookup(next + 1, lane);
-        const int count = rows_in(next);
-        ++next;
-        if (++next_stage == g.stages) next_stage = 0;
-        const int first = __shfl_sync(0xffffffffu, row, 0);
-        const bool merged = g.compact && count > 1 && first >= 0 &&
-                            __all_sync(0xffffffffu, lane >= count || row == first + lane);
-        if (lane < g.unit) head->row[s][lane] = row;
-        if (lane == 0) head->merged[s] = merged;
-        const uint32_t bar = smem_u32(&head->full[s]);
-        uint32_t mine = 0;
-        if (merged) {
-            if (lane < g.inputs) mine = hull(g.in[lane], first, count * g.in[lane].bytes);
-        } else if (row >= 0) {
-            for (int k = 0; k < g.inputs; ++k) mine += hull(g.in[k], row, g.in[k].bytes);
-        }
-        const uint32_t all = __reduce_add_sync(0xffffffffu, mine);
-        if (lane == 0) mbar_arrive_expect_tx(bar, all);
-        __syncwarp();
-        const uint32_t dst = smem_u32(ring + (size_t)s * g.stage_bytes);
-        if (merged) {
-            if (lane < g.inputs) copy(g.in[lane], first, count * g.in[lane].bytes, dst, bar);
-        } else if (row >= 0) {
-            for (int k = 0; k < g.inputs; ++k)
-                copy(g.in[k], row, g.in[k].bytes, dst + lane * g.in[k].slot, bar);
-        }
-    }
-
-    static __device__ __forceinline__ uint32_t hull(const Input &in, int row, int bytes) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(in.p + row * in.step);
-        return (uint32_t)(((a + bytes + 15) & ~uintptr_t(15)) - (a & ~uintptr_t(15)));
-    }
-    static __device__ __forceinline__ void copy(const Input &in, int row, int bytes, uint32_t dst, uint32_t bar) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(in.p + row * in.step);
-        bulk_load(dst + in.offset, reinterpret_cast<const void *>(a & ~uintptr_t(15)), hull(in, row, bytes), bar);
-    }
-
-    // The unit to be read has arrived (false: it has not, within the time limit).
-    __device__ __forceinline__ bool wait(unsigned *err) {
-        const bool mine = mbar_wait(smem_u32(&head->full[stage]), phases >> stage & 1u, &head->abort, err);
-        const bool ok = __all_sync(0xffffffffu, mine);
-        if (ok) phases ^= 1u << stage;
-        return ok;
-    }
-    __device__ __forceinline__ int row(int j) const { return head->row[stage][j]; }
-    // Row j of input k in shared memory.
-    __device__ __forceinline__ const unsigned char *at(int k, int j) const {
-        const Input &in = g.in[k];
-        const unsigned char *base = ring + (size_t)stage * g.stage_bytes + in.offset;
-        const bool merged = g.unit > 1 && head->merged[stage];
-        const int from = head->row[stage][merged ? 0 : j];
-        return base + (reinterpret_cast<uintptr_t>(in.p + from * in.step) & 15) + j * (merged ? in.bytes : in.slot);
-    }
-    __device__ __forceinline__ void advance() {
-        if (++stage == g.stages) stage = 0;
-    }
-    // After a wait that gave up: copies still in flight must land before the block ends.
-    __device__ __forceinline__ void drain() {
-        for (int s = 0; s < g.stages; ++s)
-            mbar_wait_drain(smem_u32(&head->full[s]), phases >> s & 1u, kWaitLimitNs / kMaxStages);
-    }
-};
 
 // ---- a thread's columns of a row ----
 
-// Thread `lane` of the team owns columns 8 (lane + TEAM k) .. + 7 (VEC: H is a multiple
-// of 8) or lane + TEAM e; values past H are 0.
+// Thread `lane` of the team owns columns 8 (lane + TEAM k) .. + 7 (VEC: H is a multiple of 8)
+// or lane + TEAM e; values past H are 0.
 template <int TEAM, int NV, bool VEC>
 struct Columns {
-    static constexpr int kCount = 8 * NV;
-    static __device__ __forceinline__ int at(int lane, int e) {
-        return VEC ? 8 * (lane + TEAM * (e / 8)) + e % 8 : lane + TEAM * e;
+    static __device__ __forceinline__ int at(int lane, int k, int e) {
+        return VEC ? 8 * (lane + TEAM * k) + e : lane + TEAM * (8 * k + e);
     }
 
-    // From shared memory, where the row may start on any element.
-    static __device__ __forceinline__ void read(const unsigned char *row, bool wide, int H, int lane,
-                                                float (&v)[kCount]) {
-        __builtin_assume(__isShared(row));
+    // The 16 bytes of vector k of a bf16 row on a 16-byte boundary.
+    static __device__ __forceinline__ uint4 words(const void *row, int k, int H, int lane) {
+        const int c = at(lane, k, 0);
+        return c < H ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + c)
+                     : make_uint4(0, 0, 0, 0);
+    }
+
+    // The 8 columns of vector k, wherever the row starts.
+    template <typename T>
+    static __device__ __forceinline__ void load(const T *row, int k, int H, int lane, float (&x)[8]) {
         if constexpr (VEC) {
-            const unsigned shift = smem_u32(row) & 15u;
+            const int c = at(lane, k, 0);
+            if (c >= H) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = at(lane, 8 * k);
-                float x[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = 0.f;
-                if (c < H) {
-                    if (shift == 0) {
-                        if (wide)
-                            get8(reinterpret_cast<const float *>(row) + c, x);
-                        else
-                            get8(reinterpret_cast<const uint16_t *>(row) + c, x);
-                    } else if (wide) {
-                        uint32_t w[12];
-                        words<3>(row + 4 * c - shift, w);
-                        shifted<8>(w, shift);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(w[j]);
-                    } else {
-                        uint32_t w[8];
-                        words<2>(row + 2 * c - shift, w);
-                        shifted<4>(w, shift);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            x[2 * j] = bf16_lo(w[j]);
-                            x[2 * j + 1] = bf16_hi(w[j]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[8 * k + j] = x[j];
+                for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            } else if (on(row, 16)) {
+                get8(row + c, x);
+            } else {
+                shifted(row + c, x);
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < kCount; ++e) {
-                const int c = at(lane, e);
-                v[e] = c >= H ? 0.f : wide ? get1(reinterpret_cast<const float *>(row) + c)
-                                           : get1(reinterpret_cast<const uint16_t *>(row) + c);
+            for (int e = 0; e < 8; ++e) {
+                const int c = at(lane, k, e);
+                x[e] = c < H ? get1(row + c) : 0.f;
             }
         }
     }
-    template <int N>
-    static __device__ __forceinline__ void words(const unsigned char *p, uint32_t (&w)[4 * N]) {
+    static __device__ __forceinline__ void load(const void *row, int type, int k, int H, int lane, float (&x)[8]) {
+        if (type == RK_FP32)
+            load(static_cast<const float *>(row), k, H, lane, x);
+        else
+            load(static_cast<const uint16_t *>(row), k, H, lane, x);
+    }
+
+    // Eight elements off 16-byte boundaries, from the aligned 16 bytes that each of them lies in.
+    template <typename T>
+    static __device__ __forceinline__ void shifted(const T *p, float (&x)[8]) {
+        constexpr int kWords = 8 * sizeof(T) / 4;
+        const unsigned shift = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15);
+        const uint4 *from = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - shift);
+        uint32_t w[kWords + 4];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint4 q = reinterpret_cast<const uint4 *>(p)[i];
+        for (int i = 0; i < kWords / 4 + 1; ++i) {
+            const uint4 q = from[i];
             w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
         }
-    }
-    // The N words that begin `shift` (2 .. 14) bytes into w.
-    template <int N>
-    static __device__ __forceinline__ void shifted(uint32_t (&w)[N + 4], unsigned shift) {
         if (shift & 8u) {
 #pragma unroll
-            for (int i = 0; i < N + 2; ++i) w[i] = w[i + 2];
+            for (int i = 0; i < kWords + 2; ++i) w[i] = w[i + 2];
         }
         if (shift & 4u) {
 #pragma unroll
-            for (int i = 0; i < N + 1; ++i) w[i] = w[i + 1];
+            for (int i = 0; i < kWords + 1; ++i) w[i] = w[i + 1];
         }
-        if (shift & 2u) {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-        }
-    }
-
-    // From global memory (the weight).
-    static __device__ __forceinline__ void load(const void *p, bool wide, int H, int lane, float (&v)[kCount]) {
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+        } else {
+            if (shift & 2u) {
 #pragma unroll
-        for (int e = 0; e < kCount; ++e) v[e] = 0.f;
-        const bool vec = VEC && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+                for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+            }
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            if (vec) {
-                const int c = at(lane, 8 * k);
-                if (c >= H) continue;
-                float x[8];
-                if (wide)
-                    get8(static_cast<const float *>(p) + c, x);
-                else
-                    get8(static_cast<const uint16_t *>(p) + c, x);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[8 * k + j] = x[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = at(lane, 8 * k + j);
-                    if (c < H)
-                        v[8 * k + j] = wide ? get1(static_cast<const float *>(p) + c)
-                                            : get1(static_cast<const uint16_t *>(p) + c);
-                }
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = bf16_lo(w[i]);
+                x[2 * i + 1] = bf16_hi(w[i]);
             }
         }
     }
 
-    // To global memory in fp32 or bf16.
-    static __device__ __forceinline__ void store(void *p, bool wide, int H, int lane, const float (&v)[kCount]) {
-        const bool vec = VEC && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            if (vec) {
-                const int c = at(lane, 8 * k);
-                if (c >= H) continue;
-                float x[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = v[8 * k + j];
-                if (wide)
-                    put8(static_cast<float *>(p) + c, x);
-                else
-                    put8(static_cast<uint16_t *>(p) + c, x);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = at(lane, 8 * k + j);
-                    if (c >= H) continue;
-                    if (wide)
-                        put1(static_cast<float *>(p) + c, v[8 * k + j]);
-                    else
-                        put1(static_cast<uint16_t *>(p) + c, v[8 * k + j]);
-                }
-            }
-        }
-    }
-    // Eight of them (columns of at(lane, 8k ..)) as e4m3.
-    static __device__ __forceinline__ void store_e4m3(uint8_t *p, int k, int H, int lane, const float (&x)[8]) {
-        if (VEC && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
-            const int c = at(lane, 8 * k);
-            if (c < H) *reinterpret_cast<uint2 *>(p + c) = pack_e4m3x8(x);
+    static __device__ __forceinline__ void store(void *row, int type, int k, int H, int lane, const float (&x)[8]) {
+        if (VEC && on(row, 16)) {
+            const int c = at(lane, k, 0);
+            if (c >= H) return;
+            if (type == RK_FP32)
+                put8(static_cast<float *>(row) + c, x);
+            else
+                put8(static_cast<uint16_t *>(row) + c, x);
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = at(lane, 8 * k + j);
-                if (c < H) p[c] = (uint8_t)(pack_e4m3x2(x[j], 0.f) & 0xffu);
+            for (int e = 0; e < 8; ++e) {
+                const int c = at(lane, k, e);
+                if (c >= H) continue;
+                if (type == RK_FP32)
+                    put1(static_cast<float *>(row) + c, x[e]);
+                else
+                    put1(static_cast<uint16_t *>(row) + c, x[e]);
+            }
+        }
+    }
+    static __device__ __forceinline__ void store_e4m3(uint8_t *row, int k, int H, int lane, const float (&x)[8]) {
+        if (VEC && on(row, 8)) {
+            const int c = at(lane, k, 0);
+            if (c < H) *reinterpret_cast<uint2 *>(row + c) = pack_e4m3x8(x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = at(lane, k, e);
+                if (c < H) row[c] = (uint8_t)(pack_e4m3x2(x[e], 0.f) & 0xffu);
             }
         }
     }
 };
 
-// ---- sums and maxima over a team ----
+__device__ __forceinline__ void unpack(uint4 p, float (&x)[8]) {
+    const uint32_t q[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(q[i]);
+        x[2 * i + 1] = bf16_hi(q[i]);
+    }
+}
 
-struct TeamScratch {
-    float2 sum[2][32];
-    unsigned max[2][32];
-    unsigned group[128];  // of 128 columns each, H <= 16384
-};
+// ---- sums and maxima over a team ----
 
 template <int TEAM>
 __device__ __forceinline__ void team_sync() {
@@ -356,77 +182,72 @@ __device__ __forceinline__ void team_sync() {
         __syncthreads();
 }
 
-// Sums of a and b over the team, in an order that depends on TEAM alone.  Contains one
-// team_sync; a buffer serves every other row.
+// Sums over the team, in an order that depends on TEAM alone.  A buffer may serve again when
+// another one has served in between.
 template <int TEAM>
-__device__ __forceinline__ float2 team_sum(float a, float b, float2 (&buffer)[32]) {
+__device__ __forceinline__ float2 team_sums(float a, float b, float2 (&buffer)[32]) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, off));
-        b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, off));
-    }
-    if constexpr (TEAM == 32) {
-        __syncwarp();
-    } else {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        if (lane == 0) buffer[warp] = make_float2(a, b);
+    for (int off = 16; off > 0; off >>= 1)
+        add2(a, b, __shfl_xor_sync(0xffffffffu, a, off), __shfl_xor_sync(0xffffffffu, b, off));
+    if constexpr (TEAM > 32) {
+        if ((threadIdx.x & 31) == 0) buffer[threadIdx.x >> 5] = make_float2(a, b);
         __syncthreads();
-        constexpr int kWarps = TEAM / 32;
-        const float2 v = buffer[lane % kWarps];
-        a = v.x;
-        b = v.y;
+        const float2 s = buffer[0];
+        a = s.x;
+        b = s.y;
 #pragma unroll
-        for (int off = kWarps / 2; off > 0; off >>= 1) {
-            a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, off));
-            b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, off));
+        for (int w = 1; w < TEAM / 32; ++w) {
+            const float2 t = buffer[w];
+            add2(a, b, t.x, t.y);
         }
     }
     return make_float2(a, b);
 }
-
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float a, float2 (&buffer)[32]) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, off));
+    if constexpr (TEAM > 32) {
+        if ((threadIdx.x & 31) == 0) buffer[threadIdx.x >> 5].x = a;
+        __syncthreads();
+        a = buffer[0].x;
+#pragma unroll
+        for (int w = 1; w < TEAM / 32; ++w) a = __fadd_rn(a, buffer[w].x);
+    }
+    return a;
+}
 template <int TEAM>
 __device__ __forceinline__ unsigned team_max(unsigned m, unsigned (&buffer)[32]) {
     m = __reduce_max_sync(0xffffffffu, m);
     if constexpr (TEAM > 32) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        if (lane == 0) buffer[warp] = m;
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) buffer[threadIdx.x >> 5] = m;
         __syncthreads();
         m = __reduce_max_sync(0xffffffffu, buffer[lane % (TEAM / 32)]);
     }
     return m;
 }
 
+// 1 / sqrt(sum / H + eps) of a sum of squares of k r, for k r (rstd of r is k times that).
+__device__ __forceinline__ float root(float sum, float per_column, float eps, float k) {
+    return __frsqrt_rn(__fadd_rn(__fmul_rn(sum, per_column), __fmul_rn(__fmul_rn(eps, k), k)));
+}
+
 // ---- forward ----
 
-struct Output {
-    char *p;
-    int64_t step;   // bytes from row to row
-    int32_t type;   // rk_dtype
-};
-
 struct NormArgs {
-    Ring ring;  // x, residual
+    Matrix x, residual;  // residual.p may be NULL
     const void *weight;
-    int32_t weight_wide;
-    float eps;
+    int32_t weight_type;
+    float eps, per_column;  // 1 / H
     const int64_t *targets;
     const int32_t *cu;
     int32_t num_seqs;
     int64_t T;
     int32_t H;
-    Output out, residual_out;
+    Matrix out, residual_out;
     float *scales;
     int32_t group;  // columns that share a scale: 128, or 0 for all
-    unsigned *err;
-};
-
-// The active rows among 0 .. T-1; others are -1.
-struct ActiveRows {
-    const int64_t *targets;
-    int64_t lo, hi;
-    __device__ __forceinline__ int operator()(int64_t i) const {
-        return i >= lo && i < hi && (!targets || targets[i] >= 0) ? (int)i : -1;
-    }
 };
 
 __device__ __forceinline__ void row_range(const int32_t *cu, int num_seqs, int64_t T, int64_t *lo, int64_t *hi) {
@@ -438,203 +259,254 @@ __device__ __forceinline__ void row_range(const int32_t *cu, int num_seqs, int64
     }
 }
 
-// A team's share of n list entries: whole units, the same for the same n and number of teams.
-__device__ __forceinline__ int64_t team_share(int64_t n, int64_t teams, int unit) {
-    const int64_t units = (n + unit - 1) / unit;
-    return (units + teams - 1) / teams * unit;
-}
-
 // The scale of the largest magnitude `top` (as bits) and what to multiply with.  A scale is
 // 2^-120 at least, so that its reciprocal is finite; 0 if there is nothing to scale.
 __device__ __forceinline__ float scale_of(unsigned top, float *inverse) {
-    const float m = __uint_as_float(top);
-    if (m == 0.f) {
-        *inverse = 0.f;
-        return 0.f;
-    }
-    const float s = fmaxf(__fdiv_rn(m, 448.f), 0x1p-120f);
-    *inverse = __frcp_rn(s);
-    return s;
+    const float s = fmaxf(__fmul_rn(__uint_as_float(top), 1.f / 448.f), 0x1p-120f);
+    *inverse = top ? __fdividef(1.f, s) : 0.f;
+    return top ? s : 0.f;
 }
 
-template <int TEAM, int NV, bool VEC, int BLOCK, int PER_SM>
+// How a row is read: kWords where x, residual, residual_out and weight are bf16 on 16-byte
+// boundaries, kFloats anything else.
+enum Read { kWords, kFloats };
+
+// A thread's part of a row.
+template <int NV, int READ>
+struct Part {
+    float v[NV][8];
+    __device__ __forceinline__ void get(int k, float (&x)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = v[k][e];
+    }
+};
+template <int NV>
+struct Part<NV, kWords> {
+    uint4 p[NV];
+    __device__ __forceinline__ void get(int k, float (&x)[8]) const { unpack(p[k], x); }
+};
+
+template <int TEAM, int NV, bool VEC, int READ, int ROWS, int BLOCK, int PER_SM>
 __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_constant__ NormArgs a) {
     using C = Columns<TEAM, NV, VEC>;
-    constexpr int kTeams = BLOCK / TEAM;
-    extern __shared__ __align__(128) unsigned char shared[];
-    TeamScratch *scratch = reinterpret_cast<TeamScratch *>(shared) + threadIdx.x / TEAM;
-    TeamHead *head =
-        reinterpret_cast<TeamHead *>(shared + kTeams * sizeof(TeamScratch)) + threadIdx.x / TEAM;
-    unsigned char *ring = shared + kTeams * (sizeof(TeamScratch) + sizeof(TeamHead)) +
-                          (size_t)(threadIdx.x / TEAM) * a.ring.stages * a.ring.stage_bytes;
-    const int lane = threadIdx.x % TEAM, wlane = threadIdx.x & 31;
-    const bool feeder = lane < 32;
-    const int H = a.H;
+    __shared__ float2 sums[2][32];
+    __shared__ unsigned maxima[32], grouped[VEC ? 1 : BLOCK / TEAM][VEC ? 1 : 128];  // 128 columns each, H <= 16384
+    const int lane = threadIdx.x % TEAM, wlane = threadIdx.x & 31, H = a.H;
     wait_prior_grid();
+    const int64_t t0 = ((int64_t)blockIdx.x * (BLOCK / TEAM) + threadIdx.x / TEAM) * ROWS;
+    int64_t lo, hi;
+    row_range(a.cu, a.num_seqs, a.T, &lo, &hi);
 
-    ActiveRows rows{a.targets, 0, 0};
-    row_range(a.cu, a.num_seqs, a.T, &rows.lo, &rows.hi);
-    const int64_t team = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM;
-    const int64_t share = team_share(a.T, (int64_t)gridDim.x * kTeams, a.ring.unit);
-    Feed<ActiveRows> feed(a.ring, head, ring, rows, min(a.T, team * share), min(a.T, (team + 1) * share));
-    if (feeder) feed.start(wlane);
-    float w[C::kCount];
-    C::load(a.weight, a.weight_wide, H, lane, w);
-    if constexpr (TEAM > 32) __syncthreads();
-
-    const float count = (float)H;
-    bool dead = false;
-    int parity = 0;
-    for (int u = 0; u < feed.units; ++u) {
-        if (!feed.wait(a.err)) dead = true;
-        const int n = feed.rows_in(u);
-        for (int j = 0; j < n; ++j, parity ^= 1) {
-            const int row = feed.row(j);
-            const int64_t t = feed.begin + (int64_t)u * a.ring.unit + j;
-            float v[C::kCount];
-            char *out = a.out.p + t * a.out.step, *stream = a.residual_out.p + t * a.residual_out.step;
-            const bool with_residual = a.ring.inputs > 1;
-            float k = 1.f, q = 0.f;  // rstd = k q
-            if (row >= 0) {
-                C::read(feed.at(0, j), a.ring.in[0].wide, H, lane, v);
-                if (with_residual) {
-                    float z[C::kCount];
-                    C::read(feed.at(1, j), a.ring.in[1].wide, H, lane, z);
+    // r, as it is kept
+    Part<NV, READ> part[ROWS];
+    bool live[ROWS];
 #pragma unroll
-                    for (int e = 0; e < C::kCount; ++e) v[e] = __fadd_rn(v[e], z[e]);
-                    if (a.residual_out.type == RK_BF16) {
-                        // the sum as it is kept is what the norm, and a backward that reads it, sees
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t t = t0 + i;
+        live[i] = t >= lo && t < hi && (!a.targets || a.targets[t] >= 0);
+        const char *x = a.x.row(t), *z = a.residual.row(t);
+        if constexpr (READ == kWords) {
 #pragma unroll
-                        for (int e = 0; e < C::kCount; e += 2) {
-                            const uint32_t b = pack_bf16x2(v[e], v[e + 1]);
-                            v[e] = bf16_lo(b);
-                            v[e + 1] = bf16_hi(b);
-                        }
+            for (int k = 0; k < NV; ++k)
+                part[i].p[k] = live[i] ? C::words(x, k, H, lane) : make_uint4(0, 0, 0, 0);
+            if (a.residual.p) {
+                uint4 q[NV];
+#pragma unroll
+                for (int k = 0; k < NV; ++k) q[k] = live[i] ? C::words(z, k, H, lane) : make_uint4(0, 0, 0, 0);
+                // A sum of two bf16 rounded once is what rounding it to fp32 before would leave: 24
+                // bits are more than twice 8 and two.
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    uint4 &p = part[i].p[k];
+                    p = make_uint4(add_bf16x2(p.x, q[k].x), add_bf16x2(p.y, q[k].y), add_bf16x2(p.z, q[k].z),
+                                   add_bf16x2(p.w, q[k].w));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) part[i].v[k][e] = 0.f;
+                if (live[i]) C::load(x, a.x.type, k, H, lane, part[i].v[k]);
+            }
+            if (a.residual.p && live[i]) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    float q[8];
+                    C::load(z, a.residual.type, k, H, lane, q);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float &v = part[i].v[k][e];
+                        v = __fadd_rn(v, q[e]);
+                        // what is kept is what the norm, and a backward that reads it, sees
+                        if (a.residual_out.type == RK_BF16) v = bf16_lo(pack_bf16x2(v, 0.f));
                     }
                 }
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < C::kCount; ++e) ss = __fmaf_rn(v[e], v[e], ss);
-                ss = team_sum<TEAM>(ss, 0.f, scratch->sum[parity]).x;
-                if (!(ss < INFINITY)) {
-                    k = kShrink;
-                    ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < C::kCount; ++e) ss = __fmaf_rn(v[e] * k, v[e] * k, ss);
-                    team_sync<TEAM>();
-                    ss = team_sum<TEAM>(ss, 0.f, scratch->sum[parity]).x;
-                }
-                q = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, count), __fmul_rn(__fmul_rn(a.eps, k), k)));
-            } else {
-                team_sync<TEAM>();
-#pragma unroll
-                for (int e = 0; e < C::kCount; ++e) v[e] = 0.f;
             }
-            // every thread has read the row: its stage is free
-            if (TEAM > 32 && feeder && !dead) feed.issue(wlane);
-            const int to = dead ? 0 : H;  // columns to write
-            if (with_residual) C::store(stream, a.residual_out.type == RK_FP32, to, lane, v);
-            const float rstd = q * k;
-#pragma unroll
-            for (int e = 0; e < C::kCount; ++e) v[e] = row >= 0 ? __fmul_rn(__fmul_rn(v[e], rstd), w[e]) : 0.f;
-            if (a.out.type != RK_E4M3) {
-                C::store(out, a.out.type == RK_FP32, to, lane, v);
-                continue;
-            }
-            float inverse = 0.f;
-            if (a.group == 0) {
-                unsigned top = 0;
-#pragma unroll
-                for (int e = 0; e < C::kCount; ++e) top = max(top, __float_as_uint(fmaxf(fabsf(v[e]), 0.f)));
-                top = team_max<TEAM>(top, scratch->max[parity]);
-                const float s = scale_of(top, &inverse);
-                if (lane == 0 && !dead) a.scales[t] = s;
-            } else if (!VEC) {
-                // a warp's columns of one e lie in one group of 128
-                team_sync<TEAM>();
-                for (int g = lane; g < 128; g += TEAM) scratch->group[g] = 0;
-                team_sync<TEAM>();
-#pragma unroll
-                for (int e = 0; e < C::kCount; ++e) {
-                    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(v[e]), 0.f)));
-                    const int c = C::at(lane - wlane, e);
-                    if (wlane == 0 && c < H) atomicMax(&scratch->group[c / 128], top);
-                }
-                team_sync<TEAM>();
-            }
-            const int groups = (H + 127) / 128;
-#pragma unroll
-            for (int m = 0; m < NV; ++m) {
-                float x[8];
-                if (a.group != 0 && VEC) {
-                    unsigned top = 0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fmaxf(fabsf(v[8 * m + i]), 0.f)));
-                    top = __reduce_max_sync(0xffffu << (wlane & 16), top);
-                    const float s = scale_of(top, &inverse);
-                    const int c = C::at(lane, 8 * m);
-                    if ((wlane & 15) == 0 && c < to) a.scales[t * groups + c / 128] = s;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (a.group != 0 && !VEC) {
-                        const int c = C::at(lane, 8 * m + i);
-                        const float s = scale_of(scratch->group[min(c, H - 1) / 128], &inverse);
-                        if (c % 128 == 0 && c < to) a.scales[t * groups + c / 128] = s;
-                    }
-                    x[i] = __fmul_rn(v[8 * m + i], inverse);
-                }
-                C::store_e4m3(reinterpret_cast<uint8_t *>(out), m, to, lane, x);
-            }
-        }
-        feed.advance();
-        if (TEAM == 32 && !dead) {
-            __syncwarp();
-            feed.issue(wlane);
         }
     }
-    if (dead && lane == 0) feed.drain();
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t t = t0 + i;
+        if (t >= a.T) return;  // a warp's own row, or the block's
+        if (a.residual.p) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if constexpr (READ == kWords) {
+                    const int c = C::at(lane, k, 0);
+                    if (c < H) *reinterpret_cast<uint4 *>(a.residual_out.row(t) + 2 * c) = part[i].p[k];
+                } else {
+                    C::store(a.residual_out.row(t), a.residual_out.type, k, H, lane, part[i].v[k]);
+                }
+            }
+        }
+        float rstd = 0.f;
+        if (live[i]) {
+            float even = 0.f, odd = 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float x[8];
+                part[i].get(k, x);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) fma2(even, odd, x[e], x[e + 1], x[e], x[e + 1]);
+            }
+            float sum = team_sum<TEAM>(__fadd_rn(even, odd), sums[0]);
+            rstd = root(sum, a.per_column, a.eps, 1.f);
+            if (!(sum < INFINITY)) {
+                sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    float x[8];
+                    part[i].get(k, x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum = __fmaf_rn(x[e] * kShrink, x[e] * kShrink, sum);
+                }
+                rstd = kShrink * root(team_sum<TEAM>(sum, sums[1]), a.per_column, a.eps, kShrink);
+            }
+        }
+
+        // y, a row that is not active being 0 as it is
+        const auto result = [&](int k, float (&y)[8]) {
+            float w[8];
+            if constexpr (READ == kWords)
+                unpack(C::words(a.weight, k, H, lane), w);
+            else
+                C::load(a.weight, a.weight_type, k, H, lane, w);
+            part[i].get(k, y);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                mul2(y[e], y[e + 1], rstd, rstd);
+                mul2(y[e], y[e + 1], w[e], w[e + 1]);
+            }
+        };
+        if (a.out.type != RK_E4M3) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float y[8];
+                result(k, y);
+                C::store(a.out.row(t), a.out.type, k, H, lane, y);
+            }
+            continue;
+        }
+        uint8_t *out = reinterpret_cast<uint8_t *>(a.out.row(t));
+        float *scales = a.scales + t * (a.group ? (H + 127) / 128 : 1);
+        float inverse = 0.f;
+        unsigned *mine = grouped[VEC ? 0 : threadIdx.x / TEAM];
+        if (a.group == 0 || !VEC) {
+            float top = 0.f;  // fmaxf passes over NaN
+            if (!VEC && a.group != 0) {
+                for (int g = lane; g < 128; g += TEAM) mine[g] = 0;
+                team_sync<TEAM>();
+            }
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float y[8];
+                result(k, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (!VEC && a.group != 0) {
+                        // a warp's columns of one e lie in one group
+                        const unsigned m = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(y[e]), 0.f)));
+                        const int c = C::at(lane - wlane, k, e);
+                        if (wlane == 0 && c < H) atomicMax(&mine[c / 128], m);
+                    } else {
+                        top = fmaxf(top, fabsf(y[e]));
+                    }
+                }
+            }
+            if (a.group == 0) {
+                const float s = scale_of(team_max<TEAM>(__float_as_uint(top), maxima), &inverse);
+                if (lane == 0) scales[0] = s;
+            } else {
+                team_sync<TEAM>();
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float y[8];
+            result(k, y);
+            if (VEC) {
+                if (a.group != 0) {
+                    float top = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
+                    const float s = scale_of(__reduce_max_sync(0xffffu << (wlane & 16), __float_as_uint(top)), &inverse);
+                    const int c = C::at(lane, k, 0);
+                    if ((wlane & 15) == 0 && c < H) scales[c / 128] = s;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) mul2(y[e], y[e + 1], inverse, inverse);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int c = C::at(lane, k, e);
+                    if (a.group != 0) {
+                        const float s = scale_of(mine[min(c, H - 1) / 128], &inverse);
+                        if (c % 128 == 0 && c < H) scales[c / 128] = s;
+                    }
+                    y[e] = __fmul_rn(y[e], inverse);
+                }
+            }
+            C::store_e4m3(out, k, H, lane, y);
+        }
+    }
 }
 
 // ---- backward ----
 
+__device__ __forceinline__ float one(const void *p, int type, int c) {
+    return type == RK_FP32 ? get1(static_cast<const float *>(p) + c) : get1(static_cast<const uint16_t *>(p) + c);
+}
+
 struct NormBwdArgs {
-    Ring ring;  // r, dout, dr
+    Matrix r, dout, dr;  // dr.p may be NULL
     const void *weight;
-    int32_t weight_wide;
-    float eps;
+    int32_t weight_type;
+    float eps, per_column;  // 1 / H
     const int32_t *cu;
     int32_t num_seqs;
     int64_t T;
     int32_t H;
-    const int32_t *rows;      // the canonical rows, or NULL: those of the cu_seqlens range
-    const int64_t *n_rows;    // how many
-    const uint8_t *listed;    // which rows are among them
-    Output dx;
+    const int32_t *rows;    // the canonical rows, or NULL: those of the cu_seqlens range
+    const int64_t *n_rows;  // how many
+    const uint8_t *listed;  // which rows are among them
+    Matrix dx;
     float *partial;  // [blocks, H], or NULL: no dweight
-    unsigned *err;
 };
 
-struct ListedRows {
-    const int32_t *rows;
-    int64_t first;
-    __device__ __forceinline__ int operator()(int64_t i) const { return rows ? rows[i] : (int)(first + i); }
-};
+// What a row is read as, and kept as between its sums and its results.
+//   kWords    r, dout, dr and weight bf16 on 16-byte boundaries: words
+//   kMixed    the same with dout in fp32
+//   kFloats   anything else: nothing is kept, it is read again (from the first caches)
+constexpr int kMixed = 2;
 
-template <int TEAM, int NV, bool VEC, int BLOCK, int PER_SM>
+template <int TEAM, int NV, bool VEC, int READ, int BLOCK, int PER_SM>
 __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_constant__ NormBwdArgs a) {
     using C = Columns<TEAM, NV, VEC>;
     constexpr int kTeams = BLOCK / TEAM;
-    constexpr bool kKeep = TEAM < 1024;  // the weight and the row stay in registers
-    extern __shared__ __align__(128) unsigned char shared[];
-    TeamScratch *scratch = reinterpret_cast<TeamScratch *>(shared) + threadIdx.x / TEAM;
-    TeamHead *head =
-        reinterpret_cast<TeamHead *>(shared + kTeams * sizeof(TeamScratch)) + threadIdx.x / TEAM;
-    unsigned char *rings = shared + kTeams * (sizeof(TeamScratch) + sizeof(TeamHead));
-    unsigned char *ring = rings + (size_t)(threadIdx.x / TEAM) * a.ring.stages * a.ring.stage_bytes;
-    const int lane = threadIdx.x % TEAM, wlane = threadIdx.x & 31;
-    const bool feeder = lane < 32;
-    const int H = a.H;
+    __shared__ float2 sums[2][32];
+    extern __shared__ float joined[];  // [H], where a block has several teams
+    const int lane = threadIdx.x % TEAM, H = a.H;
     wait_prior_grid();
 
     int64_t lo, hi;
@@ -642,106 +514,150 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
     const int64_t n = a.rows ? *a.n_rows : max((int64_t)0, hi - lo);
     const int64_t teams = (int64_t)gridDim.x * kTeams;
     const int64_t team = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM;
-    const int64_t share = team_share(n, teams, a.ring.unit);
-    Feed<ListedRows> feed(a.ring, head, ring, ListedRows{a.rows, lo}, min(n, team * share),
-                          min(n, (team + 1) * share));
-    if (feeder) feed.start(wlane);
-    float w[C::kCount], acc[C::kCount];
-    if (kKeep) C::load(a.weight, a.weight_wide, H, lane, w);
+    float acc[NV][8];
 #pragma unroll
-    for (int e = 0; e < C::kCount; ++e) acc[e] = 0.f;
-    if constexpr (TEAM > 32) __syncthreads();
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
 
-    const float count = (float)H;
-    const bool late = a.ring.stages > 1;  // a stage is refilled one row later
-    bool dead = false;
     int parity = 0;
-    for (int u = 0; u < feed.units; ++u) {
-        if (!feed.wait(a.err)) dead = true;
-        const int rows = feed.rows_in(u);
-        for (int j = 0; j < rows; ++j, parity ^= 1) {
-            const int64_t t = feed.row(j);
-            float r[C::kCount], d[C::kCount];
-            C::read(feed.at(0, j), a.ring.in[0].wide, H, lane, r);
-            C::read(feed.at(1, j), a.ring.in[1].wide, H, lane, d);
-            if (!kKeep) C::load(a.weight, a.weight_wide, H, lane, w);
-            float s1 = 0.f, s2 = 0.f, k = 1.f;
+    // fewer than 2^31 rows
+    const int last = (int)n, step = (int)teams, first = (int)lo;
+    const auto row_at = [&](int64_t i) { return i >= last ? 0 : a.rows ? a.rows[i] : first + (int)i; };
+    int next = row_at(team);
+    for (int64_t i = team; i < last; i += step) {
+        const int t = next;
+        next = row_at(i + step);
+        const auto r = [&] { return a.r.row(t); };
+        const auto d = [&] { return a.dout.row(t); };
+        const auto z = [&] { return a.dr.row(t); };
+        uint4 rw[NV], dw[NV * (READ == kMixed ? 2 : 1)], zw[NV];
+        if constexpr (READ != kFloats) {
 #pragma unroll
-            for (int e = 0; e < C::kCount; ++e) {
-                s1 = __fmaf_rn(r[e], r[e], s1);
-                s2 = __fmaf_rn(__fmul_rn(d[e], w[e]), r[e], s2);
-            }
-            float2 s = team_sum<TEAM>(s1, s2, scratch->sum[parity]);
-            // every thread is done with the row before: its stage is free
-            if (TEAM > 32 && feeder && late && u > 0 && !dead) feed.issue(wlane);
-            if (!(s.x < INFINITY)) {
-                k = kShrink;
-                s1 = s2 = 0.f;
-#pragma unroll
-                for (int e = 0; e < C::kCount; ++e) {
-                    s1 = __fmaf_rn(r[e] * k, r[e] * k, s1);
-                    s2 = __fmaf_rn(__fmul_rn(d[e], w[e]), r[e] * k, s2);
+            for (int k = 0; k < NV; ++k) {
+                const int c = C::at(lane, k, 0);
+                rw[k] = C::words(r(), k, H, lane);
+                if constexpr (READ == kWords) {
+                    dw[k] = C::words(d(), k, H, lane);
+                } else {
+                    const uint4 *from = reinterpret_cast<const uint4 *>(d() + 4 * c);
+                    dw[2 * k] = c < H ? from[0] : make_uint4(0, 0, 0, 0);
+                    dw[2 * k + 1] = c < H ? from[1] : make_uint4(0, 0, 0, 0);
                 }
-                team_sync<TEAM>();
-                s = team_sum<TEAM>(s1, s2, scratch->sum[parity]);
+                zw[k] = a.dr.p ? C::words(z(), k, H, lane) : make_uint4(0, 0, 0, 0);
             }
-            // with z = k r:  rstd = k q,  n = r rstd,  mean(g n) = q mean(g z)
-            const float q = __frsqrt_rn(__fadd_rn(__fdiv_rn(s.x, count), __fmul_rn(__fmul_rn(a.eps, k), k)));
-            const float rstd = q * k, c = __fmul_rn(q, __fdiv_rn(s.y, count));
-            float z[C::kCount];
-            if (a.ring.inputs > 2) {
-                C::read(feed.at(2, j), a.ring.in[2].wide, H, lane, z);
-            } else {
-#pragma unroll
-                for (int e = 0; e < C::kCount; ++e) z[e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < C::kCount; ++e) {
-                const float x = __fmul_rn(r[e], rstd);
-                acc[e] = __fmaf_rn(d[e], x, acc[e]);
-                z[e] = __fmaf_rn(rstd, __fmaf_rn(-x, c, __fmul_rn(d[e], w[e])), z[e]);
-            }
-            if (!dead) C::store(a.dx.p + t * a.dx.step, a.dx.type == RK_FP32, H, lane, z);
         }
-        feed.advance();
-        if (TEAM == 32) {
-            __syncwarp();
-            if (!dead) feed.issue(wlane);
-        } else if (!late) {
-            __syncthreads();
-            if (feeder && !dead) feed.issue(wlane);
+        const auto values = [&](int k, float (&x)[8], float (&g)[8], float (&w)[8]) {
+            if constexpr (READ == kFloats) {
+                C::load(a.weight, a.weight_type, k, H, lane, w);
+                C::load(r(), a.r.type, k, H, lane, x);
+                C::load(d(), a.dout.type, k, H, lane, g);
+            } else {
+                unpack(C::words(a.weight, k, H, lane), w);
+                unpack(rw[k], x);
+                if constexpr (READ == kWords) {
+                    unpack(dw[k], g);
+                } else {
+                    const uint4 p = dw[2 * k], q = dw[2 * k + 1];
+                    const uint32_t v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] = __uint_as_float(v[e]);
+                }
+            }
+        };
+
+        // sums of z^2 and g z, z = k r
+        float k1 = 1.f;
+        float2 s;
+        {
+            float even1 = 0.f, odd1 = 0.f, even2 = 0.f, odd2 = 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float x[8], g[8], w[8];
+                values(k, x, g, w);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    mul2(g[e], g[e + 1], w[e], w[e + 1]);
+                    fma2(even1, odd1, x[e], x[e + 1], x[e], x[e + 1]);
+                    fma2(even2, odd2, g[e], g[e + 1], x[e], x[e + 1]);
+                }
+            }
+            add2(even1, even2, odd1, odd2);
+            s = team_sums<TEAM>(even1, even2, sums[parity]);
+            parity ^= 1;
+        }
+        if (!(s.x < INFINITY)) {
+            float squares = 0.f, products = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < NV; ++k) {
+#pragma unroll 1
+                for (int e = 0; e < 8; ++e) {
+                    const int c = C::at(lane, k, e);
+                    if (c >= H) continue;
+                    const float x = kShrink * one(r(), a.r.type, c);
+                    squares = __fmaf_rn(x, x, squares);
+                    products = __fmaf_rn(__fmul_rn(one(d(), a.dout.type, c), one(a.weight, a.weight_type, c)), x, products);
+                }
+            }
+            s = team_sums<TEAM>(squares, products, sums[parity]);
+            parity ^= 1;
+            k1 = kShrink;
+        }
+        // rstd = k q,  n = r rstd,  mean(g n) = q mean(g z)
+        const float q = root(s.x, a.per_column, a.eps, k1), rstd = q * k1;
+        const float c = -__fmul_rn(q, __fmul_rn(s.y, a.per_column));
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float x[8], g[8], w[8], y[8];
+            values(k, x, g, w);
+            if constexpr (READ == kFloats) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = 0.f;
+                if (a.dr.p) C::load(z(), a.dr.type, k, H, lane, y);
+            } else {
+                unpack(zw[k], y);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                mul2(x[e], x[e + 1], rstd, rstd);
+                fma2(acc[k][e], acc[k][e + 1], g[e], g[e + 1], x[e], x[e + 1]);
+                mul2(g[e], g[e + 1], w[e], w[e + 1]);
+                fma2(g[e], g[e + 1], x[e], x[e + 1], c, c);
+                fma2(y[e], y[e + 1], rstd, rstd, g[e], g[e + 1]);
+            }
+            C::store(a.dx.row(t), a.dx.type, k, H, lane, y);
         }
     }
-    if (dead && lane == 0) feed.drain();
 
     // 0 in the rows that are not among the canonical ones
     if (a.cu || a.listed) {
-        float zero[C::kCount];
+        const float zero[8] = {};
+        for (int64_t u = team; u < a.T; u += teams) {
+            if (a.listed ? a.listed[u] : u >= lo && u < hi) continue;
 #pragma unroll
-        for (int e = 0; e < C::kCount; ++e) zero[e] = 0.f;
-        for (int64_t t = team; t < a.T; t += teams)
-            if (a.listed ? !a.listed[t] : t < lo || t >= hi)
-                C::store(a.dx.p + t * a.dx.step, a.dx.type == RK_FP32, H, lane, zero);
+            for (int k = 0; k < NV; ++k) C::store(a.dx.row(u), a.dx.type, k, H, lane, zero);
+        }
     }
     if (!a.partial) return;
     float *partial = a.partial + (int64_t)blockIdx.x * H;
     if constexpr (kTeams == 1) {
-        C::store(partial, true, H, lane, acc);
-    } else {
-        // the block's teams one after the other, over the rings (every copy has landed)
-        float *sum = reinterpret_cast<float *>(rings);
-        __syncthreads();
-        for (int i = 0; i < kTeams; ++i) {
-            if ((int)(threadIdx.x / TEAM) == i) {
 #pragma unroll
-                for (int e = 0; e < C::kCount; ++e) {
-                    const int col = C::at(lane, e);
-                    if (col < H) sum[col] = i == 0 ? acc[e] : __fadd_rn(sum[col], acc[e]);
-                }
+        for (int k = 0; k < NV; ++k) C::store(partial, RK_FP32, k, H, lane, acc[k]);
+    } else {
+        // the block's teams one after the other
+        for (int j = 0; j < kTeams; ++j) {
+            if ((int)(threadIdx.x / TEAM) == j) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int col = C::at(lane, k, e);
+                        if (col < H) joined[col] = j == 0 ? acc[k][e] : __fadd_rn(joined[col], acc[k][e]);
+                    }
             }
             __syncthreads();
         }
-        for (int col = threadIdx.x; col < H; col += BLOCK) partial[col] = sum[col];
+        for (int col = threadIdx.x; col < H; col += BLOCK) partial[col] = joined[col];
     }
 }
 
@@ -852,91 +768,45 @@ __global__ void __launch_bounds__(kListThreads)
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-int element_bytes(rk_dtype t) { return t == RK_E4M3 ? 1 : t == RK_BF16 ? 2 : 4; }
+int element_bytes(int type) { return type == RK_E4M3 ? 1 : type == RK_BF16 ? 2 : 4; }
 
-// Rows of a unit: about 1024 columns for a warp, one row for a block.
-int unit_rows(int H, int team) {
-    if (team > 32) return 1;
-    int u = 1;
-    while (u < kMaxUnit && 2 * u * H <= 1024) u *= 2;
-    return u;
+Matrix matrix(const RulesMatrix *m) {
+    if (!m) return Matrix{};
+    return Matrix{static_cast<char *>(const_cast<void *>(m->p)), m->ld * element_bytes(m->type), (int32_t)m->type};
 }
 
-// Fills the ring's layout for blocks of `teams` teams, `per_sm` of them per SM; returns
-// their shared memory, 0 if not even one stage fits into an SM.
-size_t lay_out(Ring *g, int teams, int per_sm) {
-    const size_t fixed = teams * (sizeof(TeamScratch) + sizeof(TeamHead));
-    g->stage_bytes = 0;
-    for (int k = 0; k < g->inputs; ++k) {
-        g->in[k].slot = (g->in[k].bytes + 15) / 16 * 16 + 16;
-        g->in[k].offset = g->stage_bytes;
-        g->stage_bytes += g->in[k].slot * g->unit;
-    }
-    const size_t stage = (size_t)g->stage_bytes * teams;
-    size_t room = kSharedPerSm / per_sm - 1024;
-    if (fixed + stage > room) room = kSharedPerSm - 1024;
-    if (fixed + stage > room) return 0;
-    g->stages = (int)std::min<size_t>(kMaxStages, (room - fixed) / stage);
-    return fixed + g->stages * stage;
-}
+// Of a type, with every row on a 16-byte boundary (or missing).
+bool plain(const Matrix &m, int type) { return !m.p || (m.type == type && aligned(m.p, 16) && m.step % 16 == 0); }
 
-Input input(const RulesMatrix &m, int64_t H) {
-    Input in{};
-    in.p = static_cast<const char *>(m.p);
-    in.step = m.ld * element_bytes(m.type);
-    in.bytes = (int32_t)(H * element_bytes(m.type));
-    in.wide = m.type == RK_FP32;
-    return in;
-}
-
-Output output(const RulesMatrix &m) {
-    return Output{static_cast<char *>(const_cast<void *>(m.p)), m.ld * element_bytes(m.type), (int32_t)m.type};
-}
-
-// Team, vectors of 8 a thread, block, blocks per SM (forward, backward).
-#define RK_NORM_SHAPES(SHAPE)         \
-    SHAPE(256, 32, 1, 256, 4, 4)      \
-    SHAPE(512, 32, 2, 256, 4, 3)      \
-    SHAPE(1024, 128, 1, 128, 8, 6)    \
-    SHAPE(2048, 128, 2, 128, 8, 4)    \
-    SHAPE(4096, 256, 2, 256, 4, 2)    \
-    SHAPE(8192, 512, 2, 512, 2, 1)    \
-    SHAPE(16384, 1024, 2, 1024, 1, 1)
+// Widest row, team, vectors of 8 a thread, the forward's rows a team and block and its blocks per
+// SM, the backward's block and blocks per SM.
+#define RK_NORM_SHAPES(SHAPE)                \
+    SHAPE(256, 32, 1, 4, 128, 8, 256, 3)     \
+    SHAPE(512, 32, 2, 2, 128, 8, 256, 2)     \
+    SHAPE(1024, 32, 4, 1, 128, 6, 128, 4)    \
+    SHAPE(2048, 64, 4, 1, 64, 12, 64, 8)     \
+    SHAPE(4096, 128, 4, 1, 128, 7, 128, 4)   \
+    SHAPE(8192, 256, 4, 1, 256, 3, 256, 2)   \
+    SHAPE(16384, 512, 4, 1, 512, 2, 512, 1)
 
 constexpr int kSmCount = 152;  // what the backward's partial sums are laid out for, on any device
 
-template <int TEAM, int NV, bool VEC, int BLOCK, int PER_SM>
-cudaError_t forward_launch(NormArgs &a, const DeviceInfo &di, cudaStream_t st) {
-    auto *kernel = rms_norm_forward<TEAM, NV, VEC, BLOCK, PER_SM>;
-    static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kSharedPerSm, di, allowed);
-    if (e != cudaSuccess) return e;
-    constexpr int kTeams = BLOCK / TEAM;
-    a.ring.unit = unit_rows(a.H, TEAM);
-    const size_t shared = lay_out(&a.ring, kTeams, PER_SM);
-    if (!shared) return cudaErrorInvalidConfiguration;
-    const int64_t per_block = (int64_t)kTeams * a.ring.unit;
-    const int64_t grid = std::min((a.T + per_block - 1) / per_block, (int64_t)di.sm_count * PER_SM);
-    return launch_dependent_smem(kernel, grid, BLOCK, shared, st, a);
+template <int TEAM, int NV, bool VEC, int READ, int ROWS, int BLOCK, int PER_SM>
+cudaError_t forward_launch(const NormArgs &a, cudaStream_t st) {
+    constexpr int64_t kRows = (int64_t)BLOCK / TEAM * ROWS;
+    return launch_dependent(rms_norm_forward<TEAM, NV, VEC, READ, ROWS, BLOCK, PER_SM>, (a.T + kRows - 1) / kRows, BLOCK,
+                            st, a);
 }
 
-template <int TEAM, int NV, bool VEC, int BLOCK, int PER_SM>
-cudaError_t backward_launch(NormBwdArgs &a, const DeviceInfo &di, cudaStream_t st) {
-    auto *kernel = rms_norm_backward<TEAM, NV, VEC, BLOCK, PER_SM>;
-    static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kSharedPerSm, di, allowed);
-    if (e != cudaSuccess) return e;
-    constexpr int kTeams = BLOCK / TEAM;
-    a.ring.unit = unit_rows(a.H, TEAM);
-    size_t shared = lay_out(&a.ring, kTeams, PER_SM);
-    if (!shared) return cudaErrorInvalidConfiguration;
-    if (kTeams > 1) shared = std::max(shared, kTeams * (sizeof(TeamScratch) + sizeof(TeamHead)) + (size_t)a.H * 4);
-    return launch_dependent_smem(kernel, (int64_t)kSmCount * PER_SM, BLOCK, shared, st, a);
+template <int TEAM, int NV, bool VEC, int READ, int BLOCK, int PER_SM>
+cudaError_t backward_launch(const NormBwdArgs &a, cudaStream_t st) {
+    return launch_dependent_smem(rms_norm_backward<TEAM, NV, VEC, READ, BLOCK, PER_SM>, (int64_t)kSmCount * PER_SM, BLOCK,
+                                 BLOCK > TEAM ? (size_t)a.H * 4 : 0, st, a);
 }
 
 int backward_blocks(int64_t H) {
-#define SHAPE(MAX, TEAM, NV, BLOCK, FWD, BWD) \
-    if (H <= MAX) return kSmCount * BWD;
+#define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER) \
+    if (H <= MAX) return kSmCount * BPER;
     RK_NORM_SHAPES(SHAPE)
 #undef SHAPE
     return 0;
@@ -973,31 +843,16 @@ cudaError_t launch_rms_norm(const RulesMatrix &x, const RulesMatrix *residual, c
                             int num_seqs, int64_t T, int64_t H, const RulesMatrix *residual_out,
                             const RulesMatrix &out, float *scales, int group, const DeviceInfo &di,
                             cudaStream_t st) {
-    NormArgs a{};
-    a.ring.in[0] = input(x, H);
-    a.ring.inputs = 1;
-    if (residual) {
-        a.ring.in[a.ring.inputs++] = input(*residual, H);
-        a.residual_out = output(*residual_out);
-    }
-    a.ring.compact = 1;
-    for (int k = 0; k < a.ring.inputs; ++k) a.ring.compact &= a.ring.in[k].step == a.ring.in[k].bytes;
-    a.weight = weight;
-    a.weight_wide = weight_type == RK_FP32;
-    a.eps = eps;
-    a.targets = targets;
-    a.cu = cu;
-    a.num_seqs = num_seqs;
-    a.T = T;
-    a.H = (int32_t)H;
-    a.out = output(out);
-    a.scales = scales;
-    a.group = group;
-    a.err = di.err;
-#define SHAPE(MAX, TEAM, NV, BLOCK, FWD, BWD)                                        \
-    if (H <= MAX)                                                                    \
-        return H % 8 == 0 ? forward_launch<TEAM, NV, true, BLOCK, FWD>(a, di, st)    \
-                          : forward_launch<TEAM, NV, false, BLOCK, FWD>(a, di, st);
+    (void)di;
+    const NormArgs a{matrix(&x), matrix(residual), weight, (int32_t)weight_type, eps, 1.f / (float)H, targets, cu,
+                     num_seqs, T, (int32_t)H, matrix(&out), matrix(residual_out), scales, group};
+    const bool words = plain(a.x, RK_BF16) && plain(a.residual, RK_BF16) && plain(a.residual_out, RK_BF16) &&
+                       weight_type == RK_BF16 && aligned(weight, 16);
+#define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER)                                          \
+    if (H <= MAX)                                                                                       \
+        return H % 8 != 0 ? forward_launch<TEAM, NV, false, kFloats, ROWS, FBLOCK, FPER>(a, st)         \
+               : words    ? forward_launch<TEAM, NV, true, kWords, ROWS, FBLOCK, FPER>(a, st)           \
+                          : forward_launch<TEAM, NV, true, kFloats, ROWS, FBLOCK, FPER>(a, st);
     RK_NORM_SHAPES(SHAPE)
 #undef SHAPE
     return cudaErrorInvalidValue;
@@ -1011,24 +866,10 @@ cudaError_t launch_rms_norm_bwd(const RulesMatrix &dout, const RulesMatrix &r, c
                                 int64_t H, const int64_t *order, int64_t n, const RulesMatrix &dx,
                                 float *dweight, bool accumulate, void *workspace, const DeviceInfo &di,
                                 cudaStream_t st) {
+    (void)di;
     const BwdBuffers b = carve(workspace, T, n, H);
-    NormBwdArgs a{};
-    a.ring.in[0] = input(r, H);
-    a.ring.in[1] = input(dout, H);
-    a.ring.inputs = 2;
-    if (dr) a.ring.in[a.ring.inputs++] = input(*dr, H);
-    a.ring.compact = 1;
-    for (int k = 0; k < a.ring.inputs; ++k) a.ring.compact &= a.ring.in[k].step == a.ring.in[k].bytes;
-    a.weight = weight;
-    a.weight_wide = weight_type == RK_FP32;
-    a.eps = eps;
-    a.cu = cu;
-    a.num_seqs = num_seqs;
-    a.T = T;
-    a.H = (int32_t)H;
-    a.dx = output(dx);
-    a.partial = dweight ? b.partial : nullptr;
-    a.err = di.err;
+    NormBwdArgs a{matrix(&r), matrix(&dout), matrix(dr), weight, (int32_t)weight_type, eps, 1.f / (float)H, cu, num_seqs,
+                  T, (int32_t)H, nullptr, nullptr, nullptr, matrix(&dx), dweight ? b.partial : nullptr};
     if (targets || order) {
         const Candidates c{order, n, T, targets, cu, num_seqs};
         const int64_t tiles = std::max<int64_t>(1, (n + kListTile - 1) / kListTile);
@@ -1041,14 +882,20 @@ cudaError_t launch_rms_norm_bwd(const RulesMatrix &dout, const RulesMatrix &r, c
         a.n_rows = b.n_rows;
         a.listed = b.listed;
     }
-    cudaError_t e = cudaErrorInvalidValue;
-#define SHAPE(MAX, TEAM, NV, BLOCK, FWD, BWD)                                         \
-    if (H <= MAX && e == cudaErrorInvalidValue)                                       \
-        e = H % 8 == 0 ? backward_launch<TEAM, NV, true, BLOCK, BWD>(a, di, st)       \
-                       : backward_launch<TEAM, NV, false, BLOCK, BWD>(a, di, st);     \
-    else
-    RK_NORM_SHAPES(SHAPE) {}
+    const bool words = plain(a.r, RK_BF16) && plain(a.dr, RK_BF16) && weight_type == RK_BF16 && aligned(weight, 16);
+    const int read = words && plain(a.dout, RK_BF16) ? kWords : words && plain(a.dout, RK_FP32) ? kMixed : kFloats;
+    const auto run = [&] {
+#define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER)                                          \
+    if (H <= MAX)                                                                                       \
+        return H % 8 != 0       ? backward_launch<TEAM, NV, false, kFloats, BBLOCK, BPER>(a, st)        \
+               : read == kWords ? backward_launch<TEAM, NV, true, kWords, BBLOCK, BPER>(a, st)          \
+               : read == kMixed ? backward_launch<TEAM, NV, true, kMixed, BBLOCK, BPER>(a, st)          \
+                                : backward_launch<TEAM, NV, true, kFloats, BBLOCK, BPER>(a, st);
+        RK_NORM_SHAPES(SHAPE)
 #undef SHAPE
+        return cudaErrorInvalidValue;
+    };
+    const cudaError_t e = run();
     if (e != cudaSuccess || !dweight) return e;
     return launch_dependent(rms_norm_join, (H + 31) / 32, 32 * kJoinLanes, st, (const float *)a.partial,
                             backward_blocks(H), (int)H, dweight, (int)accumulate);

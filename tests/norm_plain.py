@@ -46,9 +46,9 @@ def forward(r, weight, live, eps=EPS):
     return torch.where(live[:, None], y, 0.0)
 
 
-# rstd: at most 16 products and sums in a thread, 10 sums over the team, the quotient by H,
-# eps and its addition: 29 roundings of which the root takes half, then its own; two
-# products: 15.5 + 2 half steps of fp32
+# rstd: at most 16 products and sums in a thread, 10 sums over the team, 1 / H and its product,
+# eps and its addition: 30 roundings of which the root takes half, then its own; two
+# products: 15 + 1 + 2 half steps of fp32
 FORWARD = 18 * U
 
 
@@ -63,10 +63,10 @@ def backward(dout, r, weight, dr, live, eps=EPS):
     rstd = (z.square().mean(1, keepdim=True) + eps).rsqrt()
     n, g = z * rstd, d * w
     dx = rstd * (g - n * (g * n).mean(1, keepdim=True))
-    # relative to rstd |g|: g 1, the fused difference 1, rstd 15.5 and its product 1.  Relative
-    # to rstd |n| mean|g n|: n 16.5, the mean's sums 28, its quotient and root 1 + 15.5 + 1, their
-    # product and the difference 2, rstd 15.5 + 1
-    bound = 20 * U * rstd * g.abs() + 82 * U * rstd * n.abs() * (g * n).abs().mean(1, keepdim=True)
+    # relative to rstd |g|: g 1, the fused difference 1, rstd 16 and its product 1.  Relative
+    # to rstd |n| mean|g n|: n 17, the mean's sums 28, 1 / H, its product and the root 2 + 16 + 1, their
+    # product and the difference 2, rstd 16 + 1
+    bound = 20 * U * rstd * g.abs() + 84 * U * rstd * n.abs() * (g * n).abs().mean(1, keepdim=True)
     if dr is not None:
         dx = dx + dr.double()
     bound = 1.01 * (bound + U * dx.abs())

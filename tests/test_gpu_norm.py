@@ -76,7 +76,8 @@ def test_forward_in_8_bits(rk, T, H, group):
     n = -(-H // width)
     assert s.shape == (T, n)
     top = torch.nn.functional.pad(y, (0, n * width - H)).view(T, n, width).abs().amax(2) / 448
-    assert close(s, top, top * (npl.FORWARD + npl.U) * 1.01)[0]
+    # y, its product with 1 / 448, and that number's own rounding
+    assert close(s, top, top * (npl.FORWARD + 2 * npl.U) * 1.01)[0]
     s = s.double().cpu()
     z = y / torch.where(s > 0, s, 1.0).repeat_interleave(width, 1)[:, :H]
     assert close(q.float(), z, npl.e4m3_bound(z))[0]
@@ -99,7 +100,7 @@ def check_bwd(got, dw, r, dout, dr, w, live, old=None, times=None):
     if times is not None:
         terms = terms * times[:, None]
     want, mag = terms.sum(0), terms.abs().sum(0)
-    # a term: n 16.5; sums: a run of rows, 8 teams of a block, 40 blocks of a lane, 32 lanes
+    # a term: n 17; sums: a run of rows, 8 teams of a block, 40 blocks of a lane, 32 lanes
     adds = 17 + min(int(live.sum()) if times is None else int(times.sum()), 2000) + 80
     if old is not None:
         want, mag, adds = want + old.double(), mag + old.double().abs(), adds + 1
