@@ -32,6 +32,11 @@ constexpr int kTensors = 256;    // of a launch
 constexpr int kThreads = 256;
 constexpr int kBlock = 256;      // elements that share a scale: a warp's, 8 a lane
 constexpr int kChunk = 8 * kThreads * 2;  // elements of a block
+// A block with 8-bit states asks for the chunk that comes this much later, into the second cache:
+// 12 bytes an element and some 60 instructions do not keep enough loads in flight by themselves
+// (64M elements 205 us without, 162 at 152 chunks, 164 at 304, 172 at 608, 232 at 1216; with 32-bit
+// states 298 without, 353 with).
+constexpr int kPrefetch = 152;
 
 struct Tensor {
     void *param;
@@ -73,23 +78,30 @@ __device__ __forceinline__ void unpack_e4m3x8(uint2 w, float (&v)[8]) {
 }
 
 // The codes of a warp's block of values and, for its first lane to write, their scale.
-__device__ __forceinline__ uint2 encode(float (&x)[8], bool floor, float *scale) {
-    unsigned top = 0;
+template <bool FLOOR>
+__device__ __forceinline__ uint2 encode(float (&x)[8], float *scale) {
+    float most = 0.f;  // fmaxf passes over NaN
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fmaxf(fabsf(x[i]), 0.f)));
-    top = __reduce_max_sync(0xffffffffu, top);
+    for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[i]));
+    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
     // 2^-120 at least, for a finite reciprocal
     const float s = top ? fmaxf(__fmul_rn(__uint_as_float(top), 1.f / 448.f), 0x1p-120f) : 0.f;
     const float inverse = top ? __frcp_rn(s) : 0.f;
     *scale = s;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; i += 2) {
         // x / s, correctly rounded (Markstein, 1990: a faithful quotient and its remainder times
         // the rounded reciprocal): a code next to a border is that of the quotient
-        const float near = __fmul_rn(x[i], inverse);
-        float q = __fmaf_rn(__fmaf_rn(-near, s, x[i]), inverse, near);
-        if (floor && x[i] > 0.f) q = fmaxf(q, 0x1p-9f);
-        x[i] = q;
+        float n0 = x[i], n1 = x[i + 1], r0 = x[i], r1 = x[i + 1];
+        mul2(n0, n1, inverse, inverse);
+        fma2(r0, r1, -n0, -n1, s, s);
+        fma2(n0, n1, r0, r1, inverse, inverse);
+        if (FLOOR) {
+            if (x[i] > 0.f) n0 = fmaxf(n0, 0x1p-9f);
+            if (x[i + 1] > 0.f) n1 = fmaxf(n1, 0x1p-9f);
+        }
+        x[i] = n0;
+        x[i + 1] = n1;
     }
     return pack_e4m3x8(x);
 }
@@ -135,17 +147,152 @@ __device__ __forceinline__ void put_codes(void *p, int64_t at, int left, bool ve
         if (i < left) q[i] = (uint8_t)((i < 4 ? c.x : c.y) >> 8 * (i % 4));
 }
 
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table a) {
-    wait_prior_grid();
-    // the block's tensor
+// ---- the step ----
+
+struct Rates {
+    float rate, root, decay, scale;  // lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step), lr wd, grad_scale
+};
+
+// What a warp reads of 256 elements, 8 a lane, before it computes on them.
+template <bool EIGHT>
+struct States {
+    float m[8], v[8];
+    __device__ __forceinline__ void load(const Tensor &t, int64_t, int64_t at, int left) {
+        get(static_cast<const float *>(t.m), at, left, t.vec, m);
+        get(static_cast<const float *>(t.v), at, left, t.vec, v);
+    }
+};
+template <>
+struct States<true> {
+    uint2 m, v;
+    float ms, vs;
+    __device__ __forceinline__ void load(const Tensor &t, int64_t block, int64_t at, int left) {
+        m = get_codes(t.m, at, left, t.vec);
+        v = get_codes(t.v, at, left, t.vec);
+        ms = t.m_scale[block / kBlock];
+        vs = t.v_scale[block / kBlock];
+    }
+};
+
+template <bool EIGHT, typename G>
+struct Elements {
+    float g[8], w[8];
+    States<EIGHT> s;
+    int64_t at;
+    int left;
+    __device__ __forceinline__ void load(const Tensor &t, int64_t block) {
+        at = block + 8 * (threadIdx.x & 31);
+        left = (int)min((int64_t)8, max((int64_t)0, t.n - at));
+        get(static_cast<const G *>(t.grad), at, left, t.vec, g);
+        if (t.master)
+            get(t.master, at, left, t.vec, w);
+        else if (t.param_wide)
+            get(static_cast<const float *>(t.param), at, left, t.vec, w);
+        else
+            get(static_cast<const uint16_t *>(t.param), at, left, t.vec, w);
+        s.load(t, block, at, left);
+    }
+    __device__ __forceinline__ void update(const Table &a, const Tensor &t, const Rates &r, int64_t block) {
+        float m[8], v[8];
+        if constexpr (EIGHT) {
+            unpack_e4m3x8(s.m, m);
+            unpack_e4m3x8(s.v, v);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                mul2(m[i], m[i + 1], s.ms, s.ms);
+                mul2(v[i], v[i + 1], s.vs, s.vs);
+                mul2(v[i], v[i + 1], v[i], v[i + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = s.m[i], v[i] = s.v[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            // every product and sum of the states is rounded by itself: they are what elementary
+            // fp32 operations give, and so are their codes
+            float x0 = g[i], x1 = g[i + 1];
+            mul2(x0, x1, r.scale, r.scale);
+            float y0 = x0, y1 = x1;
+            mul2(y0, y1, x0, x1);
+            mul2(y0, y1, a.rest2, a.rest2);
+            mul2(x0, x1, a.rest1, a.rest1);
+            mul2(m[i], m[i + 1], a.beta1, a.beta1);
+            add2(m[i], m[i + 1], x0, x1);
+            mul2(v[i], v[i + 1], a.beta2, a.beta2);
+            add2(v[i], v[i + 1], y0, y1);
+            const float u0 = __fsqrt_rn(v[i]), u1 = __fsqrt_rn(v[i + 1]);
+            float d0 = a.eps, d1 = a.eps, p0 = m[i], p1 = m[i + 1];
+            fma2(d0, d1, u0, u1, r.root, r.root);
+            mul2(p0, p1, r.rate, r.rate);
+            fma2(w[i], w[i + 1], w[i], w[i + 1], -r.decay, -r.decay);
+            w[i] = __fsub_rn(w[i], __fdividef(p0, d0));
+            w[i + 1] = __fsub_rn(w[i + 1], __fdividef(p1, d1));
+            if (EIGHT) v[i] = u0, v[i + 1] = u1;
+        }
+        if (t.master) put(t.master, at, left, t.vec, w);
+        if (t.param_wide)
+            put(static_cast<float *>(t.param), at, left, t.vec, w);
+        else
+            put(static_cast<uint16_t *>(t.param), at, left, t.vec, w);
+        if constexpr (EIGHT) {
+            float ms, vs;
+            const uint2 mc = encode<false>(m, &ms), vc = encode<true>(v, &vs);
+            put_codes(t.m, at, left, t.vec, mc);
+            put_codes(t.v, at, left, t.vec, vc);
+            if ((threadIdx.x & 31) == 0) {
+                t.m_scale[block / kBlock] = ms;
+                t.v_scale[block / kBlock] = vs;
+            }
+        } else {
+            put(static_cast<float *>(t.m), at, left, t.vec, m);
+            put(static_cast<float *>(t.v), at, left, t.vec, v);
+        }
+    }
+};
+
+template <bool EIGHT, typename G>
+__device__ __forceinline__ void chunk_step(const Table &a, const Tensor &t, const Rates &r, int64_t chunk) {
+#pragma unroll 1
+    for (int64_t block = chunk + (threadIdx.x >> 5) * kBlock; block < min(t.n, chunk + kChunk);
+         block += kThreads / 32 * kBlock) {
+        Elements<EIGHT, G> e;
+        e.load(t, block);
+        e.update(a, t, r, block);
+    }
+}
+
+// The tensor that a chunk belongs to.
+__device__ __forceinline__ int tensor_of(const Table &a, int chunk) {
     int lo = 0, hi = a.count;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.first[mid] <= (int)blockIdx.x)
+        if (a.first[mid] <= chunk)
             lo = mid;
         else
             hi = mid;
     }
+    return lo;
+}
+
+// By four threads: a chunk's gradient, weights and states, into the second cache.
+__device__ __forceinline__ void prefetch(const Table &a, int chunk) {
+    const int k = tensor_of(a, chunk);
+    const Tensor &t = a.tensor[k];
+    const int64_t from = (int64_t)(chunk - a.first[k]) * kChunk, n = min((int64_t)kChunk, t.n - from);
+    const int weight = t.master || t.param_wide ? 4 : 2, grad = t.grad_wide ? 4 : 2;
+    const void *p = threadIdx.x == 0 ? t.grad : threadIdx.x == 1 ? t.m : threadIdx.x == 2 ? t.v : t.master ? t.master : t.param;
+    const int size = threadIdx.x == 0 ? grad : threadIdx.x < 3 ? 1 : weight;
+    const char *q = static_cast<const char *>(p) + from * size;
+    const uint32_t bytes = (uint32_t)(n * size) & ~15u;
+    if (bytes && (reinterpret_cast<uintptr_t>(q) & 15) == 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(bytes) : "memory");
+}
+
+template <bool EIGHT>
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Table a) {
+    wait_prior_grid();
+    const int lo = tensor_of(a, (int)blockIdx.x);
     const Tensor &t = a.tensor[lo];
     float rise = a.rise, root = a.root;
     if (a.step_device) {
@@ -159,70 +306,13 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         root = __fdiv_rn(1.f, __fsqrt_rn(-expm1f((float)step * a.log2)));
     }
     const float lr = __fmul_rn(a.lr_device ? *a.lr_device : a.lr, t.lr_scale);
-    const float rate = __fmul_rn(lr, rise), decay = __fmul_rn(lr, t.weight_decay);
-    const float scale = a.grad_scale ? *a.grad_scale : 1.f;
-    const bool vec = t.vec, eight = t.m_scale != nullptr;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Rates r{__fmul_rn(lr, rise), root, __fmul_rn(lr, t.weight_decay), a.grad_scale ? *a.grad_scale : 1.f};
     const int64_t chunk = (int64_t)((int)blockIdx.x - a.first[lo]) * kChunk;
-    for (int64_t block = chunk + warp * kBlock; block < min(t.n, chunk + kChunk); block += kThreads / 32 * kBlock) {
-        const int64_t at = block + 8 * lane;
-        const int left = (int)min((int64_t)8, max((int64_t)0, t.n - at));
-        float g[8], m[8], v[8], w[8];
-        if (t.grad_wide)
-            get(static_cast<const float *>(t.grad), at, left, vec, g);
-        else
-            get(static_cast<const uint16_t *>(t.grad), at, left, vec, g);
-        if (t.master)
-            get(t.master, at, left, vec, w);
-        else if (t.param_wide)
-            get(static_cast<const float *>(t.param), at, left, vec, w);
-        else
-            get(static_cast<const uint16_t *>(t.param), at, left, vec, w);
-        if (eight) {
-            unpack_e4m3x8(get_codes(t.m, at, left, vec), m);
-            unpack_e4m3x8(get_codes(t.v, at, left, vec), v);
-            const float ms = t.m_scale[block / kBlock], vs = t.v_scale[block / kBlock];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                m[i] = __fmul_rn(m[i], ms);
-                v[i] = __fmul_rn(v[i], vs);
-                v[i] = __fmul_rn(v[i], v[i]);
-            }
-        } else {
-            get(static_cast<const float *>(t.m), at, left, vec, m);
-            get(static_cast<const float *>(t.v), at, left, vec, v);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = __fmul_rn(g[i], scale);
-            // every product and sum of the states is rounded by itself: they are what elementary
-            // fp32 operations give, and so are their codes
-            m[i] = __fadd_rn(__fmul_rn(m[i], a.beta1), __fmul_rn(x, a.rest1));
-            v[i] = __fadd_rn(__fmul_rn(v[i], a.beta2), __fmul_rn(__fmul_rn(x, x), a.rest2));
-            const float u = __fsqrt_rn(v[i]);
-            const float move = __fdividef(__fmul_rn(m[i], rate), __fmaf_rn(u, root, a.eps));
-            w[i] = __fsub_rn(__fmaf_rn(-decay, w[i], w[i]), move);
-            if (eight) v[i] = u;
-        }
-        if (t.master) put(t.master, at, left, vec, w);
-        if (t.param_wide)
-            put(static_cast<float *>(t.param), at, left, vec, w);
-        else
-            put(static_cast<uint16_t *>(t.param), at, left, vec, w);
-        if (eight) {
-            float ms, vs;
-            const uint2 mc = encode(m, false, &ms), vc = encode(v, true, &vs);
-            put_codes(t.m, at, left, vec, mc);
-            put_codes(t.v, at, left, vec, vc);
-            if (lane == 0) {
-                t.m_scale[block / kBlock] = ms;
-                t.v_scale[block / kBlock] = vs;
-            }
-        } else {
-            put(static_cast<float *>(t.m), at, left, vec, m);
-            put(static_cast<float *>(t.v), at, left, vec, v);
-        }
-    }
+    if (EIGHT && threadIdx.x < 4 && (int)blockIdx.x < a.first[a.count] - kPrefetch) prefetch(a, (int)blockIdx.x + kPrefetch);
+    if (t.grad_wide)
+        chunk_step<EIGHT, float>(a, t, r, chunk);
+    else
+        chunk_step<EIGHT, uint16_t>(a, t, r, chunk);
 }
 
 }  // namespace
@@ -246,11 +336,14 @@ cudaError_t launch_adamw(const rk_adamw_tensor *tensors, int64_t count, const rk
     a.grad_scale = o.grad_scale;
     a.err = di.err;
     for (int64_t i = 0; i < count;) {
+        // as many tensors with the same kind of states as fit
+        const bool eight = tensors[i].m_scale != nullptr;
         a.count = 0;
         int64_t chunks = 0;
         for (; i < count && a.count < kTensors; ++i) {
             const rk_adamw_tensor &s = tensors[i];
             if (s.n == 0) continue;
+            if ((s.m_scale != nullptr) != eight) break;
             const int64_t more = (s.n + kChunk - 1) / kChunk;
             if (chunks + more > 0x7fffffff) break;
             Tensor &t = a.tensor[a.count];
@@ -272,9 +365,9 @@ cudaError_t launch_adamw(const rk_adamw_tensor *tensors, int64_t count, const rk
             a.first[a.count++] = (int32_t)chunks;
             chunks += more;
         }
-        if (a.count == 0) break;
+        if (a.count == 0) continue;  // empty ones, or one of the other kind next
         a.first[a.count] = (int32_t)chunks;
-        const cudaError_t e = launch_dependent(adamw_kernel, chunks, kThreads, st, a);
+        const cudaError_t e = launch_dependent(eight ? adamw_kernel<true> : adamw_kernel<false>, chunks, kThreads, st, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

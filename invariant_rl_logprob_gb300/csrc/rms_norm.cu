@@ -638,7 +638,8 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
             for (int k = 0; k < NV; ++k) C::store(a.dx.row(u), a.dx.type, k, H, lane, zero);
         }
     }
-    if (!a.partial) return;
+    // a block without rows has nothing to leave, and rms_norm_join does not look for it
+    if (!a.partial || (int64_t)blockIdx.x * kTeams >= n) return;
     float *partial = a.partial + (int64_t)blockIdx.x * H;
     if constexpr (kTeams == 1) {
 #pragma unroll
@@ -661,18 +662,23 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
     }
 }
 
-// dweight[c] (+)= the blocks' partial sums: lane y takes blocks y, y + 32, ... in order,
-// then the lanes' sums are added in order.
+// dweight[c] (+)= the partial sums of the blocks that had rows: lane y takes blocks y, y + 32, ...
+// in order, then the lanes' sums are added in order.
 constexpr int kJoinLanes = 32;
 __global__ void __launch_bounds__(32 * kJoinLanes)
-    rms_norm_join(const float *partial, int blocks, int H, float *dweight, int accumulate) {
+    rms_norm_join(const float *partial, int blocks, int rows_of_block, const int64_t *n_rows, const int32_t *cu,
+                  int num_seqs, int64_t T, int H, float *dweight, int accumulate) {
     __shared__ float sums[kJoinLanes][33];
     wait_prior_grid();
+    int64_t lo, hi;
+    row_range(cu, num_seqs, T, &lo, &hi);
+    const int64_t n = n_rows ? *n_rows : max((int64_t)0, hi - lo);
+    const int busy = (int)min((int64_t)blocks, (n + rows_of_block - 1) / rows_of_block);
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
     float s = 0.f;
     if (c < H) {
 #pragma unroll 4
-        for (int b = y; b < blocks; b += kJoinLanes) s = __fadd_rn(s, partial[(int64_t)b * H + c]);
+        for (int b = y; b < busy; b += kJoinLanes) s = __fadd_rn(s, partial[(int64_t)b * H + c]);
     }
     sums[y][x] = s;
     __syncthreads();
@@ -721,26 +727,28 @@ __device__ __forceinline__ int block_sum(int v, int *scratch) {
     return v;
 }
 
-__global__ void __launch_bounds__(kListThreads) norm_rows_count(Candidates c, int32_t *counts, uint8_t *listed) {
+__global__ void __launch_bounds__(kListThreads) norm_rows_count(Candidates c, int32_t *counts) {
     __shared__ int scratch[32];
     wait_prior_grid();
     int64_t lo, hi;
     row_range(c.cu, c.num_seqs, c.T, &lo, &hi);
-    for (int64_t t = (int64_t)blockIdx.x * kListThreads + threadIdx.x; t < c.T; t += (int64_t)gridDim.x * kListThreads)
-        listed[t] = 0;
     int row[kListItems];
     const int total = block_sum(candidate_rows(c, lo, hi, row), scratch);
     if (threadIdx.x == 0) counts[blockIdx.x] = total;
 }
 
 __global__ void __launch_bounds__(kListThreads)
-    norm_rows_write(Candidates c, const int32_t *counts, int32_t *rows, uint8_t *listed, int64_t *n_rows) {
+    norm_rows_write(Candidates c, const int32_t *counts, int32_t *rows, uint8_t *listed, int64_t *n_rows) {  // counts NULL: one block
     __shared__ int scratch[32], warps[32];
     wait_prior_grid();
     int64_t lo, hi;
     row_range(c.cu, c.num_seqs, c.T, &lo, &hi);
+    if (!counts) {  // nobody has cleared `listed` either
+        for (int64_t t = threadIdx.x; t < c.T; t += kListThreads) listed[t] = 0;
+        __syncthreads();
+    }
     int before = 0;  // rows of the blocks before this one (fewer than 2^31)
-    for (int b = threadIdx.x; b < (int)blockIdx.x; b += kListThreads) before += counts[b];
+    for (int b = threadIdx.x; counts && b < (int)blockIdx.x; b += kListThreads) before += counts[b];
     before = block_sum(before, scratch);
     int row[kListItems];
     const int mine = candidate_rows(c, lo, hi, row);
@@ -811,6 +819,13 @@ int backward_blocks(int64_t H) {
 #undef SHAPE
     return 0;
 }
+int rows_of_block(int64_t H) {
+#define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER) \
+    if (H <= MAX) return BBLOCK / TEAM;
+    RK_NORM_SHAPES(SHAPE)
+#undef SHAPE
+    return 1;
+}
 
 struct BwdBuffers {
     float *partial;
@@ -873,10 +888,12 @@ cudaError_t launch_rms_norm_bwd(const RulesMatrix &dout, const RulesMatrix &r, c
     if (targets || order) {
         const Candidates c{order, n, T, targets, cu, num_seqs};
         const int64_t tiles = std::max<int64_t>(1, (n + kListTile - 1) / kListTile);
-        cudaError_t e = launch_dependent(norm_rows_count, tiles, kListThreads, st, c, b.counts, b.listed);
+        const bool one = tiles == 1 && T <= kListTile;  // block does it all
+        cudaError_t e = one ? cudaSuccess : cudaMemsetAsync(b.listed, 0, (size_t)T, st);
+        if (e == cudaSuccess && !one) e = launch_dependent(norm_rows_count, tiles, kListThreads, st, c, b.counts);
         if (e == cudaSuccess)
-            e = launch_dependent(norm_rows_write, tiles, kListThreads, st, c, (const int32_t *)b.counts, b.rows,
-                                 b.listed, b.n_rows);
+            e = launch_dependent(norm_rows_write, tiles, kListThreads, st, c, one ? (const int32_t *)nullptr : b.counts,
+                                 b.rows, b.listed, b.n_rows);
         if (e != cudaSuccess) return e;
         a.rows = b.rows;
         a.n_rows = b.n_rows;
@@ -898,7 +915,8 @@ cudaError_t launch_rms_norm_bwd(const RulesMatrix &dout, const RulesMatrix &r, c
     const cudaError_t e = run();
     if (e != cudaSuccess || !dweight) return e;
     return launch_dependent(rms_norm_join, (H + 31) / 32, 32 * kJoinLanes, st, (const float *)a.partial,
-                            backward_blocks(H), (int)H, dweight, (int)accumulate);
+                            backward_blocks(H), rows_of_block(H), a.n_rows, cu, num_seqs, T, (int)H, dweight,
+                            (int)accumulate);
 }
 
 }  // namespace rk

@@ -56,8 +56,8 @@ def plain(c: Case, kind="sigmoid", beta=0.125, smoothing=0.0, average=False, sca
         n[q] = max(1, len(part)) if average else 1
         total = math.fsum(part)
         s[q] = total / n[q]
-        # two roundings to 2^-42 a token; the sum and the quotient in 64 bits
-        ds[q] = (len(part) * 2.0 ** -42) / n[q] + 4 * 2.0 ** -53 * abs(s[q])
+        # two roundings to 2^-42 a token and one of the quotient; 64 bits where fixed point ends
+        ds[q] = (len(part) * 2.0 ** -42) / n[q] + 2.0 ** -43 + 4 * 2.0 ** -53 * abs(s[q])
     loss, dloss = np.zeros(P), np.zeros(P)
     coef, dcoef, terms = [0.0] * Q, [0.0] * Q, [0] * Q
     for p in range(P):
@@ -65,7 +65,8 @@ def plain(c: Case, kind="sigmoid", beta=0.125, smoothing=0.0, average=False, sca
         if i < 0 or j < 0:
             continue
         d = s[i] - s[j] - (0.0 if c.margin is None else float(c.margin[p]))
-        dd = ds[i] + ds[j] + 4 * 2.0 ** -53 * (abs(s[i]) + abs(s[j]) + abs(d))
+        # ... and of the margin and 1 / (2 beta)
+        dd = ds[i] + ds[j] + 2.0 ** -42 + 4 * 2.0 ** -53 * (abs(s[i]) + abs(s[j]) + abs(d))
         x = beta * d
         if kind == "sigmoid":
             soft = lambda t: max(t, 0.0) + math.log1p(math.exp(-abs(t)))  # noqa: E731
