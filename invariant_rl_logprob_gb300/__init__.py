@@ -215,6 +215,9 @@ def _stream_handle(stream, device) -> ctypes.c_void_p:
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> None:
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == ndim
+            and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -1029,7 +1032,7 @@ def _weight(weight, H: int, device) -> int:
     code = _TYPE_CODES.get(weight.dtype)
     if code is None:
         raise TypeError(f"weight must be bfloat16 or float32, got {weight.dtype}")
-    if weight.dim() != 1 or weight.shape[0] != H or weight.device != device or not weight.is_contiguous():
+    if weight.shape != (H,) or weight.device != device or not weight.is_contiguous():
         raise ValueError(f"weight must be contiguous [{H}] on {device}, got shape "
                          f"{tuple(weight.shape)} on {weight.device}")
     return code
@@ -1048,21 +1051,19 @@ def _mask(targets, cu_seqlens, T: int, device):
     return None, cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
 
 
-def _norm(x, weight, targets, cu_seqlens, residual, eps, out, out_code, out_ld, residual_out, scales, group,
-          device, stream):
+def _norm(x, code, ld, weight, targets, cu_seqlens, residual, eps, out, out_code, out_ld, residual_out, scales,
+          group, device, stream):
     lib = _lib or load_library()
-    code, ld = _matrix(x, "x")
-    T, H = x.shape
+    T, H = shape = x.shape
     w_code = _weight(weight, H, device)
     tg, cu, ns = _mask(targets, cu_seqlens, T, device)
     r, res, res_code, res_ld, ro, ro_ld = x, None, 0, 0, None, 0
     if residual is not None:
-        res_code, res_ld = _matrix(residual, "residual", (T, H), device)
+        res_code, res_ld = _matrix(residual, "residual", shape, device)
         if residual_out is None:
-            residual_out = _empty((T, H), residual.dtype, device, stream)
-            ro_ld = H
+            residual_out, ro_ld = _empty(shape, residual.dtype, device, stream), H
         else:
-            ro_code, ro_ld = _matrix(residual_out, "residual_out", (T, H), device)
+            ro_code, ro_ld = _matrix(residual_out, "residual_out", shape, device)
             if ro_code != res_code:
                 raise TypeError(f"residual_out must be {residual.dtype}, got {residual_out.dtype}")
         r, res, ro = residual_out, residual.data_ptr(), residual_out.data_ptr()
@@ -1086,11 +1087,11 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor | None
     or fp32 ``[H]``, y is in ``out_dtype`` (bf16 or fp32, default: x's).  Rows with a
     negative target or outside ``cu_seqlens`` are not read and get 0; without either every
     row is active.  ``out`` and ``residual_out`` may be ``x`` or ``residual`` itself."""
-    _matrix(x, "x")
+    code, ld = _matrix(x, "x")
     device = x.device
     out, out_code, out_ld = _result(out, out_dtype or x.dtype, x.shape, device, stream)
-    return out, _norm(x, weight, targets, cu_seqlens, residual, eps, out, out_code, out_ld, residual_out, None,
-                      0, device, stream)
+    return out, _norm(x, code, ld, weight, targets, cu_seqlens, residual, eps, out, out_code, out_ld, residual_out,
+                      None, 0, device, stream)
 
 
 def rms_norm_e4m3(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor | None = None,
@@ -1102,7 +1103,7 @@ def rms_norm_e4m3(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor |
     float8_e4m3fn ``[T, H]`` and ``y ~ q * scales``.  One scale for a row (``group`` 0,
     ``scales`` fp32 ``[T, 1]``) or for each 128 columns (``group`` 128, ``[T, ceil(H /
     128)]``): the largest magnitude / 448, 0 where there is none."""
-    _matrix(x, "x")
+    code, ld = _matrix(x, "x")
     T, H = x.shape
     device = x.device
     if group != 0 and group != 128:
@@ -1122,7 +1123,7 @@ def rms_norm_e4m3(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor |
         _need(scales, "scales", torch.float32, 2)
         if scales.shape != shape or scales.device != device:
             raise ValueError(f"scales must be {list(shape)} on {device}")
-    return out, scales, _norm(x, weight, targets, cu_seqlens, residual, eps, out, 2, out_ld, residual_out,
+    return out, scales, _norm(x, code, ld, weight, targets, cu_seqlens, residual, eps, out, 2, out_ld, residual_out,
                               scales, group, device, stream)
 
 

@@ -9,7 +9,7 @@
 //   loss_p = scale * f(d_p),   grad_logp[t] = sum over p of the sequence: +-scale f'(d_p) [/ number]
 //
 // Bound by latency: 12 to 16 bytes a token, and results that wait for one another
-// (sums, pairs, coefficients, gradients).  Where a thread has at most one run of
+// (sums, pairs, gradients).  Where a thread has at most one run of
 // tokens and one pair, one cluster of up to 16 blocks does all of it with the
 // hardware's cluster barrier between the steps, and every thread keeps its run and
 // its pair in registers; beyond, every step is a launch of its own over the whole
@@ -40,7 +40,6 @@ enum Flag : unsigned { kPlusInf = 1, kMinusInf = 2, kNaN = 4 };
 
 struct Sequence {
     unsigned long long hi, lo;  // sum of the tokens' fixed-point words
-    float coef;                 // d (sum of losses) / d logp of each of its tokens
     int count;                  // active tokens
     unsigned flags;
     int pairs, first, last;     // how many times pairs name it, and the range they are in
@@ -309,30 +308,78 @@ __device__ __forceinline__ void compare(const Args &a, const Pair &pair, int64_t
     a.slope[p] = slope;
 }
 
-// By a warp: the slopes of a sequence's pairs in ascending order.
-__device__ __forceinline__ void gather(const Args &a, int64_t q) {
+// d (sum of the losses) / d logp of sequence q's tokens: the slopes of its pairs in ascending order.
+__device__ __forceinline__ float share_of(const Args &a, const Sequence &s, float sum) {
+    const int count = __ldcg(&s.count);
+    return a.average && count > 1 ? __fdiv_rn(sum, (float)count) : sum;
+}
+__device__ __forceinline__ float slope_at(const Args &a, int q, int64_t p, bool *named) {
+    Pair pair;
+    pair.load(a, p);
+    const float slope = __ldcg(&a.slope[p]);
+    *named = pair.c == q || pair.r == q;
+    return (pair.c == q ? slope : 0.f) - (pair.r == q ? slope : 0.f);
+}
+// By a warp.
+__device__ __forceinline__ float gather(const Args &a, int q) {
     const int lane = threadIdx.x & 31;
-    Sequence &s = a.seq[q];
-    const int pairs = __ldcg(&s.pairs), first = __ldcg(&s.first), last = __ldcg(&s.last), count = __ldcg(&s.count);
+    const Sequence &s = a.seq[q];
+    const int pairs = __ldcg(&s.pairs), first = __ldcg(&s.first), last = __ldcg(&s.last);
     float sum = 0.f;
     for (int64_t p0 = first; pairs > 0 && p0 <= last; p0 += 32) {
-        const int64_t p = p0 + lane;
-        Pair pair{-1, -1, 0.f, false};
-        float slope = 0.f;
-        if (p <= last) {
-            pair.load(a, p);
-            slope = __ldcg(&a.slope[p]);
-        }
-        const float mine = (pair.c == q ? slope : 0.f) - (pair.r == q ? slope : 0.f);
-        unsigned named = __ballot_sync(0xffffffffu, pair.c == q || pair.r == q);
-        for (; named; named &= named - 1) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, mine, __ffs((int)named) - 1));
+        bool named = false;
+        const float mine = p0 + lane <= last ? slope_at(a, q, p0 + lane, &named) : 0.f;
+        for (unsigned m = __ballot_sync(0xffffffffu, named); m; m &= m - 1)
+            sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, mine, __ffs((int)m) - 1));
     }
-    if (a.average && count > 1) sum = __fdiv_rn(sum, (float)count);
-    if (lane == 0) s.coef = sum;
+    return share_of(a, s, sum);
+}
+// By a thread, where a tile has more sequences than there is room for.
+__device__ __noinline__ float gather_alone(const Args &a, int q) {
+    const Sequence &s = a.seq[q];
+    const int pairs = __ldcg(&s.pairs), first = __ldcg(&s.first), last = __ldcg(&s.last);
+    float sum = 0.f;
+    for (int64_t p = first; pairs > 0 && p <= last; ++p) {
+        bool named;
+        const float mine = slope_at(a, q, p, &named);
+        if (named) sum = __fadd_rn(sum, mine);
+    }
+    return share_of(a, s, sum);
 }
 
-__device__ __forceinline__ void write_run(const Args &a, const int32_t *cu, Run run) {
-    const auto coef_of = [&](int q) { return q >= 0 && q < a.Q ? __ldcg(&a.seq[q].coef) : 0.f; };
+constexpr int kTileSequences = 1024;
+
+struct Tile {
+    int first, last;  // sequences that the block's tokens belong to
+    float coef[kTileSequences];
+};
+
+// The gradients of a block's runs; `mine`: this thread has one.
+template <int THREADS>
+__device__ __forceinline__ void write_runs(const Args &a, const int32_t *cu, Run run, bool mine, Tile &tile) {
+    const bool end = mine && (run.t + kRun >= a.T || threadIdx.x == THREADS - 1);
+    if (threadIdx.x == 0) tile.first = mine ? max(run.q, 0) : 0;
+    if (threadIdx.x == 0 && !mine) tile.last = -1;
+    if (end) {
+        Run last = run;
+        last.advance(cu, a.Q, a.T, min(a.T, run.t + kRun) - 1);
+        tile.last = min(last.q, a.Q - 1);
+    }
+    __syncthreads();
+    const int first = tile.first, count = tile.last - first + 1;
+    const bool near = count <= kTileSequences;
+    if (near)
+        for (int k = threadIdx.x >> 5; k < count; k += THREADS / 32) {
+            const float c = gather(a, first + k);
+            if ((threadIdx.x & 31) == 0) tile.coef[k] = c;
+        }
+    __syncthreads();
+    if (!mine) return;
+    // offsets that do not ascend may lead out of the tile
+    const auto coef_of = [&](int q) {
+        if (q < 0 || q >= a.Q) return 0.f;
+        return near && q >= first && q < first + count ? tile.coef[q - first] : gather_alone(a, q);
+    };
     float coef = coef_of(run.q), g[kRun];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
@@ -374,8 +421,9 @@ __device__ __forceinline__ void load_logprobs(const Args &a, int64_t t, float (&
 // All steps by one cluster whose threads have at most one run, one sequence and one pair each.
 __global__ void __launch_bounds__(kThreads) preference_cluster(const __grid_constant__ Args a) {
     __shared__ int32_t offsets[kSharedOffsets + 1];
+    __shared__ Tile tile;
     wait_prior_grid();
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, n = (int64_t)gridDim.x * kThreads;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int64_t runs = (a.T + kRun - 1) / kRun;
     const bool mine = i - (threadIdx.x & 31) < runs;  // whole warps
     Run run{};
@@ -396,13 +444,11 @@ __global__ void __launch_bounds__(kThreads) preference_cluster(const __grid_cons
     if (i < a.P) compare(a, pair, i);
     if (i < a.Q && a.logratio) a.logratio[i] = ratio_of(a, (int)i).rounded();
     cluster_sync();
-    for (int64_t q = i >> 5; q < a.Q; q += n >> 5) gather(a, q);
-    cluster_sync();
-    if (mine) write_run(a, cu, run);
+    write_runs<kThreads>(a, cu, run, i < runs, tile);
 }
 
 // The same steps as launches of their own.
-enum Step { kClear, kSums, kPairs, kCoefs, kGrads };
+enum Step { kClear, kSums, kPairs, kGrads };
 
 template <int STEP>
 __global__ void __launch_bounds__(kStepThreads) preference_step(const __grid_constant__ Args a) {
@@ -435,16 +481,18 @@ __global__ void __launch_bounds__(kStepThreads) preference_step(const __grid_con
         }
         if (a.logratio)
             for (int64_t q = i; q < a.Q; q += n) a.logratio[q] = ratio_of(a, (int)q).rounded();
-    } else if constexpr (STEP == kCoefs) {
-        for (int64_t q = i >> 5; q < a.Q; q += n >> 5) gather(a, q);
     } else {
         __shared__ int32_t offsets[kSharedOffsets + 1];
         const int32_t *cu = offsets_near<kStepThreads>(a, offsets);
-        for (int64_t r = i; r < runs; r += n) {
-            Run run;
-            run.load_targets(a, r);
-            run.find(cu, a.Q);
-            write_run(a, cu, run);
+        __shared__ Tile tile;
+        for (int64_t r = i, b = (int64_t)blockIdx.x * kStepThreads; b < runs; r += n, b += n) {
+            Run run{};
+            if (r < runs) {
+                run.load_targets(a, r);
+                run.find(cu, a.Q);
+            }
+            write_runs<kStepThreads>(a, cu, run, r < runs, tile);
+            __syncthreads();
         }
     }
 }
@@ -511,7 +559,6 @@ cudaError_t launch_preference(const float *logp, const float *ref, const int64_t
     cudaError_t e = launch_step<kClear>(a, num_seqs, di, st);
     if (e == cudaSuccess) e = launch_step<kSums>(a, std::max(runs, P), di, st);
     if (e == cudaSuccess) e = launch_step<kPairs>(a, std::max<int64_t>(P, num_seqs), di, st);
-    if (e == cudaSuccess) e = launch_step<kCoefs>(a, (int64_t)num_seqs * 32, di, st);
     if (e == cudaSuccess) e = launch_step<kGrads>(a, runs, di, st);
     return e;
 }

@@ -531,6 +531,14 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
         const auto r = [&] { return a.r.row(t); };
         const auto d = [&] { return a.dout.row(t); };
         const auto z = [&] { return a.dr.row(t); };
+        if (READ != kFloats && lane < 3 && i + step < last) {
+            // the team's next row, on its way into the second cache
+            const Matrix &m = lane == 0 ? a.r : lane == 1 ? a.dout : a.dr;
+            if (m.p)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(m.row(next)),
+                             "r"(H * (m.type == RK_FP32 ? 4 : 2))
+                             : "memory");
+        }
         uint4 rw[NV], dw[NV * (READ == kMixed ? 2 : 1)], zw[NV];
         if constexpr (READ != kFloats) {
 #pragma unroll
