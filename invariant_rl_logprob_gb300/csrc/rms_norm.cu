@@ -12,8 +12,8 @@
 //   dx = rstd * (g - n * mean(g * n)) + dr,   dweight (+)= sum over rows of dout * n
 //
 // Both are bound by memory: 8 and 15 flop an element, against 7 to 12 bytes.
-// A team of threads (a warp up to 1024 columns, up to 16 warps beyond) has a
-// row in registers, as it was read: bf16 words where all is bf16 on 16-byte
+// A team of threads (part of a warp up to 128 columns, a warp up to 1024, up to
+// 16 warps beyond) has a row in registers, as it was read: bf16 words where all is bf16 on 16-byte
 // boundaries, floats otherwise.  A thread owns up to 32 columns: fewer threads
 // a row mean fewer that sum, scale and wait for one another.
 //
@@ -21,11 +21,15 @@
 // one reduction.  dweight: a team adds its rows in registers, in order; blocks
 // leave partial sums that a last kernel adds in order.
 //
+// A thread owns eight consecutive columns at a time.  Rows off 16-byte boundaries
+// (any row of an odd H, say) are read in the aligned 16 bytes around each eight and
+// shifted on the way; results for such rows go through shared memory and leave in
+// aligned 16 bytes as well.
+//
 // Which thread owns which column, and with it the order of every sum, depends
-// on H alone: eight consecutive columns where H is a multiple of 8, columns
-// TEAM apart otherwise (loads and stores stay coalesced).  Which rows a team
-// of the backward takes depends on the number of canonical rows alone.  A sum
-// of squares that leaves fp32 is formed again from r * 2^-80.
+// on H alone.  Which rows a team of the backward takes depends on the number of
+// canonical rows alone.  A sum of squares that leaves fp32 is formed again from
+// r * 2^-80.
 #include <algorithm>
 
 #include "elements.cuh"
@@ -44,124 +48,163 @@ struct Matrix {
     __device__ __forceinline__ char *row(int64_t t) const { return p + t * step; }
 };
 
-__device__ __forceinline__ bool on(const void *p, unsigned a) {
-    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+// ---- teams ----
+
+// The lanes of a warp that belong to the thread's team.
+template <int TEAM>
+__device__ __forceinline__ unsigned team_lanes() {
+    if constexpr (TEAM >= 32)
+        return 0xffffffffu;
+    else
+        return ((1u << TEAM) - 1u) << (threadIdx.x & 31 & ~(TEAM - 1));
+}
+template <int TEAM>
+__device__ __forceinline__ void team_sync() {
+    if constexpr (TEAM > 32)
+        __syncthreads();
+    else
+        __syncwarp(team_lanes<TEAM>());
 }
 
 // ---- a thread's columns of a row ----
 
-// Thread `lane` of the team owns columns 8 (lane + TEAM k) .. + 7 (VEC: H is a multiple of 8)
-// or lane + TEAM e; values past H are 0.
-template <int TEAM, int NV, bool VEC>
-struct Columns {
-    static __device__ __forceinline__ int at(int lane, int k, int e) {
-        return VEC ? 8 * (lane + TEAM * k) + e : lane + TEAM * (8 * k + e);
+// N words that begin `shift` bytes into w.
+template <int N>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[N + 4], unsigned shift) {
+    if (shift & 8u) {
+#pragma unroll
+        for (int i = 0; i < N + 2; ++i) w[i] = w[i + 2];
     }
+    if (shift & 4u) {
+#pragma unroll
+        for (int i = 0; i < N + 1; ++i) w[i] = w[i + 1];
+    }
+    if (shift & 3u) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (shift & 3u));
+    }
+}
+template <int N>
+__device__ __forceinline__ void read_words(const void *p, uint32_t (&w)[4 * N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint4 q = static_cast<const uint4 *>(p)[i];
+        w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+    }
+}
 
-    // The 16 bytes of vector k of a bf16 row on a 16-byte boundary.
+// Thread `lane` of the team owns columns 8 (lane + TEAM k) .. + 7; values past H are 0.
+template <int TEAM>
+struct Columns {
+    static __device__ __forceinline__ int at(int lane, int k) { return 8 * (lane + TEAM * k); }
+
+    // The 16 bytes of vector k of a bf16 row on a 16-byte boundary, H a multiple of 8.
     static __device__ __forceinline__ uint4 words(const void *row, int k, int H, int lane) {
-        const int c = at(lane, k, 0);
+        const int c = at(lane, k);
         return c < H ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + c)
                      : make_uint4(0, 0, 0, 0);
     }
 
-    // The 8 columns of vector k, wherever the row starts.
-    template <typename T>
-    static __device__ __forceinline__ void load(const T *row, int k, int H, int lane, float (&x)[8]) {
-        if constexpr (VEC) {
-            const int c = at(lane, k, 0);
-            if (c >= H) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 0.f;
-            } else if (on(row, 16)) {
-                get8(row + c, x);
-            } else {
-                shifted(row + c, x);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = at(lane, k, e);
-                x[e] = c < H ? get1(row + c) : 0.f;
-            }
-        }
-    }
-    static __device__ __forceinline__ void load(const void *row, int type, int k, int H, int lane, float (&x)[8]) {
-        if (type == RK_FP32)
-            load(static_cast<const float *>(row), k, H, lane, x);
-        else
-            load(static_cast<const uint16_t *>(row), k, H, lane, x);
-    }
-
-    // Eight elements off 16-byte boundaries, from the aligned 16 bytes that each of them lies in.
-    template <typename T>
-    static __device__ __forceinline__ void shifted(const T *p, float (&x)[8]) {
+    // Vectors k0 .. k0 + N - 1, wherever the row starts; all loads are on their way before the first
+    // is waited for.
+    template <int N, typename T>
+    static __device__ __forceinline__ void load_as(const T *row, int k0, int H, int lane, float (&x)[N][8]) {
         constexpr int kWords = 8 * sizeof(T) / 4;
-        const unsigned shift = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15);
-        const uint4 *from = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - shift);
-        uint32_t w[kWords + 4];
+        const unsigned shift = (unsigned)(reinterpret_cast<uintptr_t>(row) & 15);
+        if (shift == 0 && H % 8 == 0) {
 #pragma unroll
-        for (int i = 0; i < kWords / 4 + 1; ++i) {
-            const uint4 q = from[i];
-            w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
-        }
-        if (shift & 8u) {
+            for (int i = 0; i < N; ++i) {
+                const int c = at(lane, k0 + i);
 #pragma unroll
-            for (int i = 0; i < kWords + 2; ++i) w[i] = w[i + 2];
-        }
-        if (shift & 4u) {
-#pragma unroll
-            for (int i = 0; i < kWords + 1; ++i) w[i] = w[i + 1];
-        }
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
-        } else {
-            if (shift & 2u) {
-#pragma unroll
-                for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+                for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+                if (c < H) get8(row + c, x[i]);
             }
+            return;
+        }
+        // the aligned 16 bytes that a column of the row lies in, and no others
+        const char *from = reinterpret_cast<const char *>(row) - shift, *end = reinterpret_cast<const char *>(row + H);
+        uint32_t w[N][kWords + 4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = bf16_lo(w[i]);
-                x[2 * i + 1] = bf16_hi(w[i]);
+        for (int i = 0; i < N; ++i) {
+            const char *p = from + sizeof(T) * at(lane, k0 + i);
+#pragma unroll
+            for (int j = 0; j < kWords / 4 + 1; ++j) {
+                const uint4 q = p + 16 * j < end ? *reinterpret_cast<const uint4 *>(p + 16 * j) : make_uint4(0, 0, 0, 0);
+                w[i][4 * j] = q.x; w[i][4 * j + 1] = q.y; w[i][4 * j + 2] = q.z; w[i][4 * j + 3] = q.w;
             }
         }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            shift_words<kWords>(w[i], shift);
+            const int left = H - at(lane, k0 + i);
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[i][e] = __uint_as_float(w[i][e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[i][2 * e] = bf16_lo(w[i][e]);
+                    x[i][2 * e + 1] = bf16_hi(w[i][e]);
+                }
+            }
+            if (left < 8) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e >= left) x[i][e] = 0.f;
+            }
+        }
+    }
+    template <int N>
+    static __device__ __forceinline__ void load(const void *row, int type, int k0, int H, int lane, float (&x)[N][8]) {
+        if (type == RK_FP32)
+            load_as<N>(static_cast<const float *>(row), k0, H, lane, x);
+        else
+            load_as<N>(static_cast<const uint16_t *>(row), k0, H, lane, x);
     }
 
-    static __device__ __forceinline__ void store(void *row, int type, int k, int H, int lane, const float (&x)[8]) {
-        if (VEC && on(row, 16)) {
-            const int c = at(lane, k, 0);
-            if (c >= H) return;
-            if (type == RK_FP32)
-                put8(static_cast<float *>(row) + c, x);
-            else
-                put8(static_cast<uint16_t *>(row) + c, x);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = at(lane, k, e);
-                if (c >= H) continue;
-                if (type == RK_FP32)
-                    put1(static_cast<float *>(row) + c, x[e]);
-                else
-                    put1(static_cast<uint16_t *>(row) + c, x[e]);
-            }
-        }
+    // Vector k of a row that starts and ends on 16 bytes (e4m3: 8), in global memory or in the stage.
+    static __device__ __forceinline__ void store(char *row, int type, int k, int H, int lane, const float (&x)[8]) {
+        const int c = at(lane, k);
+        if (c >= H) return;
+        if (type == RK_FP32)
+            put8(reinterpret_cast<float *>(row) + c, x);
+        else if (type == RK_BF16)
+            put8(reinterpret_cast<uint16_t *>(row) + c, x);
+        else
+            *reinterpret_cast<uint2 *>(row + c) = pack_e4m3x8(x);
     }
-    static __device__ __forceinline__ void store_e4m3(uint8_t *row, int k, int H, int lane, const float (&x)[8]) {
-        if (VEC && on(row, 8)) {
-            const int c = at(lane, k, 0);
-            if (c < H) *reinterpret_cast<uint2 *>(row + c) = pack_e4m3x8(x);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = at(lane, k, e);
-                if (c < H) row[c] = (uint8_t)(pack_e4m3x2(x[e], 0.f) & 0xffu);
+
+    // A row's `bytes` bytes from the stage (16-byte aligned, 16 bytes and more behind them) to
+    // wherever the row starts; element size 1, 2 or 4.
+    static __device__ __forceinline__ void flush(const char *stage, char *row, int bytes, int size, int lane) {
+        if (size == 4) {
+#pragma unroll 4
+            for (int b = 4 * lane; b < bytes; b += 4 * TEAM)
+                *reinterpret_cast<uint32_t *>(row + b) = *reinterpret_cast<const uint32_t *>(stage + b);
+            return;
+        }
+        const int before = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+        for (int p = 16 * lane - before; p < bytes; p += 16 * TEAM) {
+            if (p >= 0 && p + 16 <= bytes) {
+                uint32_t w[8];
+                read_words<2>(stage + (p & ~15), w);
+                shift_words<4>(w, (unsigned)p & 15u);
+                *reinterpret_cast<uint4 *>(row + p) = make_uint4(w[0], w[1], w[2], w[3]);
+                continue;
+            }
+            for (int b = max(p, 0); b < min(p + 16, bytes); b += size) {
+                if (size == 2)
+                    *reinterpret_cast<uint16_t *>(row + b) = *reinterpret_cast<const uint16_t *>(stage + b);
+                else
+                    row[b] = stage[b];
             }
         }
     }
 };
+
+__host__ __device__ constexpr int size_of(int type) { return type == RK_E4M3 ? 1 : type == RK_BF16 ? 2 : 4; }
+// Bytes of a team's stage.
+__host__ __device__ constexpr int stage_bytes(int H) { return (H + 7) / 8 * 32 + 32; }
 
 __device__ __forceinline__ void unpack(uint4 p, float (&x)[8]) {
     const uint32_t q[4] = {p.x, p.y, p.z, p.w};
@@ -174,21 +217,13 @@ __device__ __forceinline__ void unpack(uint4 p, float (&x)[8]) {
 
 // ---- sums and maxima over a team ----
 
-template <int TEAM>
-__device__ __forceinline__ void team_sync() {
-    if constexpr (TEAM == 32)
-        __syncwarp();
-    else
-        __syncthreads();
-}
-
 // Sums over the team, in an order that depends on TEAM alone.  A buffer may serve again when
 // another one has served in between.
 template <int TEAM>
 __device__ __forceinline__ float2 team_sums(float a, float b, float2 (&buffer)[32]) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        add2(a, b, __shfl_xor_sync(0xffffffffu, a, off), __shfl_xor_sync(0xffffffffu, b, off));
+    for (int off = (TEAM < 32 ? TEAM : 32) / 2; off > 0; off >>= 1)
+        add2(a, b, __shfl_xor_sync(team_lanes<TEAM>(), a, off), __shfl_xor_sync(team_lanes<TEAM>(), b, off));
     if constexpr (TEAM > 32) {
         if ((threadIdx.x & 31) == 0) buffer[threadIdx.x >> 5] = make_float2(a, b);
         __syncthreads();
@@ -206,7 +241,8 @@ __device__ __forceinline__ float2 team_sums(float a, float b, float2 (&buffer)[3
 template <int TEAM>
 __device__ __forceinline__ float team_sum(float a, float2 (&buffer)[32]) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, off));
+    for (int off = (TEAM < 32 ? TEAM : 32) / 2; off > 0; off >>= 1)
+        a = __fadd_rn(a, __shfl_xor_sync(team_lanes<TEAM>(), a, off));
     if constexpr (TEAM > 32) {
         if ((threadIdx.x & 31) == 0) buffer[threadIdx.x >> 5].x = a;
         __syncthreads();
@@ -218,7 +254,7 @@ __device__ __forceinline__ float team_sum(float a, float2 (&buffer)[32]) {
 }
 template <int TEAM>
 __device__ __forceinline__ unsigned team_max(unsigned m, unsigned (&buffer)[32]) {
-    m = __reduce_max_sync(0xffffffffu, m);
+    m = __reduce_max_sync(team_lanes<TEAM>(), m);
     if constexpr (TEAM > 32) {
         const int lane = threadIdx.x & 31;
         if (lane == 0) buffer[threadIdx.x >> 5] = m;
@@ -248,6 +284,7 @@ struct NormArgs {
     Matrix out, residual_out;
     float *scales;
     int32_t group;  // columns that share a scale: 128, or 0 for all
+    int32_t stage_out, stage_residual;  // rows leave through shared memory
 };
 
 __device__ __forceinline__ void row_range(const int32_t *cu, int num_seqs, int64_t T, int64_t *lo, int64_t *hi) {
@@ -286,12 +323,15 @@ struct Part<NV, kWords> {
     __device__ __forceinline__ void get(int k, float (&x)[8]) const { unpack(p[k], x); }
 };
 
-template <int TEAM, int NV, bool VEC, int READ, int ROWS, int BLOCK, int PER_SM>
+template <int TEAM, int NV, int READ, int ROWS, int BLOCK, int PER_SM>
 __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_constant__ NormArgs a) {
-    using C = Columns<TEAM, NV, VEC>;
+    using C = Columns<TEAM>;
     __shared__ float2 sums[2][32];
-    __shared__ unsigned maxima[32], grouped[VEC ? 1 : BLOCK / TEAM][VEC ? 1 : 128];  // 128 columns each, H <= 16384
-    const int lane = threadIdx.x % TEAM, wlane = threadIdx.x & 31, H = a.H;
+    __shared__ unsigned maxima[32];
+    extern __shared__ __align__(16) char stages[];  // where rows leave through them
+    constexpr int kPair = NV > 1 ? 2 : 1;  // vectors read at once where nothing is kept as words
+    const int lane = threadIdx.x % TEAM, H = a.H;
+    char *stage = stages + (size_t)(threadIdx.x / TEAM) * stage_bytes(H);
     wait_prior_grid();
     const int64_t t0 = ((int64_t)blockIdx.x * (BLOCK / TEAM) + threadIdx.x / TEAM) * ROWS;
     int64_t lo, hi;
@@ -324,20 +364,27 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
+            for (int k = 0; k < NV; ++k)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) part[i].v[k][e] = 0.f;
-                if (live[i]) C::load(x, a.x.type, k, H, lane, part[i].v[k]);
+            if (live[i]) {
+#pragma unroll
+                for (int k = 0; k < NV; k += kPair) {
+                    float q[kPair][8];
+                    C::load(x, a.x.type, k, H, lane, q);
+#pragma unroll
+                    for (int j = 0; j < 8 * kPair; ++j) part[i].v[k + j / 8][j % 8] = q[j / 8][j % 8];
+                }
             }
             if (a.residual.p && live[i]) {
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    float q[8];
+                for (int k = 0; k < NV; k += kPair) {
+                    float q[kPair][8];
                     C::load(z, a.residual.type, k, H, lane, q);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float &v = part[i].v[k][e];
-                        v = __fadd_rn(v, q[e]);
+                    for (int j = 0; j < 8 * kPair; ++j) {
+                        float &v = part[i].v[k + j / 8][j % 8];
+                        v = __fadd_rn(v, q[j / 8][j % 8]);
                         // what is kept is what the norm, and a backward that reads it, sees
                         if (a.residual_out.type == RK_BF16) v = bf16_lo(pack_bf16x2(v, 0.f));
                     }
@@ -348,16 +395,23 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int64_t t = t0 + i;
-        if (t >= a.T) return;  // a warp's own row, or the block's
+        if (t >= a.T) return;  // the whole team
         if (a.residual.p) {
+            char *to = READ == kFloats && a.stage_residual ? stage : a.residual_out.row(t);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 if constexpr (READ == kWords) {
-                    const int c = C::at(lane, k, 0);
-                    if (c < H) *reinterpret_cast<uint4 *>(a.residual_out.row(t) + 2 * c) = part[i].p[k];
+                    const int c = C::at(lane, k);
+                    if (c < H) *reinterpret_cast<uint4 *>(to + 2 * c) = part[i].p[k];
                 } else {
-                    C::store(a.residual_out.row(t), a.residual_out.type, k, H, lane, part[i].v[k]);
+                    C::store(to, a.residual_out.type, k, H, lane, part[i].v[k]);
                 }
+            }
+            if (READ == kFloats && a.stage_residual) {
+                const int size = size_of(a.residual_out.type);
+                team_sync<TEAM>();
+                C::flush(stage, a.residual_out.row(t), H * size, size, lane);
+                team_sync<TEAM>();
             }
         }
         float rstd = 0.f;
@@ -387,87 +441,58 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
 
         // y, a row that is not active being 0 as it is
         const auto result = [&](int k, float (&y)[8]) {
-            float w[8];
+            float w[1][8];
             if constexpr (READ == kWords)
-                unpack(C::words(a.weight, k, H, lane), w);
+                unpack(C::words(a.weight, k, H, lane), w[0]);
             else
                 C::load(a.weight, a.weight_type, k, H, lane, w);
             part[i].get(k, y);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 mul2(y[e], y[e + 1], rstd, rstd);
-                mul2(y[e], y[e + 1], w[e], w[e + 1]);
+                mul2(y[e], y[e + 1], w[0][e], w[0][e + 1]);
             }
         };
-        if (a.out.type != RK_E4M3) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                float y[8];
-                result(k, y);
-                C::store(a.out.row(t), a.out.type, k, H, lane, y);
-            }
-            continue;
-        }
-        uint8_t *out = reinterpret_cast<uint8_t *>(a.out.row(t));
+        const bool e4m3 = a.out.type == RK_E4M3;
         float *scales = a.scales + t * (a.group ? (H + 127) / 128 : 1);
-        float inverse = 0.f;
-        unsigned *mine = grouped[VEC ? 0 : threadIdx.x / TEAM];
-        if (a.group == 0 || !VEC) {
+        float inverse = 1.f;
+        if (e4m3 && a.group == 0) {
             float top = 0.f;  // fmaxf passes over NaN
-            if (!VEC && a.group != 0) {
-                for (int g = lane; g < 128; g += TEAM) mine[g] = 0;
-                team_sync<TEAM>();
-            }
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 float y[8];
                 result(k, y);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (!VEC && a.group != 0) {
-                        // a warp's columns of one e lie in one group
-                        const unsigned m = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(y[e]), 0.f)));
-                        const int c = C::at(lane - wlane, k, e);
-                        if (wlane == 0 && c < H) atomicMax(&mine[c / 128], m);
-                    } else {
-                        top = fmaxf(top, fabsf(y[e]));
-                    }
-                }
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
             }
-            if (a.group == 0) {
-                const float s = scale_of(team_max<TEAM>(__float_as_uint(top), maxima), &inverse);
-                if (lane == 0) scales[0] = s;
-            } else {
-                team_sync<TEAM>();
-            }
+            const float s = scale_of(team_max<TEAM>(__float_as_uint(top), maxima), &inverse);
+            if (lane == 0) scales[0] = s;
         }
+        char *to = a.stage_out ? stage : a.out.row(t);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             float y[8];
             result(k, y);
-            if (VEC) {
-                if (a.group != 0) {
+            if (e4m3) {
+                if (a.group != 0) {  // 128 columns: 16 lanes (H > 128, so that a team has them)
                     float top = 0.f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
-                    const float s = scale_of(__reduce_max_sync(0xffffu << (wlane & 16), __float_as_uint(top)), &inverse);
-                    const int c = C::at(lane, k, 0);
-                    if ((wlane & 15) == 0 && c < H) scales[c / 128] = s;
+                    const unsigned lanes = TEAM < 32 ? team_lanes<TEAM>() : 0xffffu << (threadIdx.x & 16);
+                    const float s = scale_of(__reduce_max_sync(lanes, __float_as_uint(top)), &inverse);
+                    const int c = C::at(lane, k);
+                    if ((lane & 15) == 0 && c < H) scales[c / 128] = s;
                 }
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) mul2(y[e], y[e + 1], inverse, inverse);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int c = C::at(lane, k, e);
-                    if (a.group != 0) {
-                        const float s = scale_of(mine[min(c, H - 1) / 128], &inverse);
-                        if (c % 128 == 0 && c < H) scales[c / 128] = s;
-                    }
-                    y[e] = __fmul_rn(y[e], inverse);
-                }
             }
-            C::store_e4m3(out, k, H, lane, y);
+            C::store(to, a.out.type, k, H, lane, y);
+        }
+        if (a.stage_out) {
+            const int size = size_of(a.out.type);
+            team_sync<TEAM>();
+            C::flush(stage, a.out.row(t), H * size, size, lane);
+            if (ROWS > 1) team_sync<TEAM>();
         }
     }
 }
@@ -491,8 +516,11 @@ struct NormBwdArgs {
     const int64_t *n_rows;  // how many
     const uint8_t *listed;  // which rows are among them
     Matrix dx;
-    float *partial;  // [blocks, H], or NULL: no dweight
+    int32_t stage_dx;  // its rows leave through shared memory
+    float *partial;    // [blocks, pitch_of(H)], or NULL: no dweight
 };
+
+__host__ __device__ constexpr int64_t pitch_of(int64_t H) { return (H + 7) / 8 * 8; }
 
 // What a row is read as, and kept as between its sums and its results.
 //   kWords    r, dout, dr and weight bf16 on 16-byte boundaries: words
@@ -500,13 +528,15 @@ struct NormBwdArgs {
 //   kFloats   anything else: nothing is kept, it is read again (from the first caches)
 constexpr int kMixed = 2;
 
-template <int TEAM, int NV, bool VEC, int READ, int BLOCK, int PER_SM>
+template <int TEAM, int NV, int READ, int BLOCK, int PER_SM>
 __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_constant__ NormBwdArgs a) {
-    using C = Columns<TEAM, NV, VEC>;
+    using C = Columns<TEAM>;
     constexpr int kTeams = BLOCK / TEAM;
     __shared__ float2 sums[2][32];
-    extern __shared__ float joined[];  // [H], where a block has several teams
+    // the teams' stages, and in the end their sums of dweight
+    extern __shared__ __align__(16) char stages[];
     const int lane = threadIdx.x % TEAM, H = a.H;
+    char *stage = stages + (size_t)(threadIdx.x / TEAM) * stage_bytes(H);
     wait_prior_grid();
 
     int64_t lo, hi;
@@ -531,19 +561,22 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
         const auto r = [&] { return a.r.row(t); };
         const auto d = [&] { return a.dout.row(t); };
         const auto z = [&] { return a.dr.row(t); };
-        if (READ != kFloats && lane < 3 && i + step < last) {
+        if (lane < 3 && i + step < last) {
             // the team's next row, on its way into the second cache
             const Matrix &m = lane == 0 ? a.r : lane == 1 ? a.dout : a.dr;
-            if (m.p)
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(m.row(next)),
-                             "r"(H * (m.type == RK_FP32 ? 4 : 2))
+            if (m.p) {
+                const uintptr_t from = reinterpret_cast<uintptr_t>(m.row(next)), to = from + H * size_of(m.type);
+                const uintptr_t first16 = from & ~uintptr_t(15);
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(first16),
+                             "r"((uint32_t)((to + 15 & ~uintptr_t(15)) - first16))
                              : "memory");
+            }
         }
         uint4 rw[NV], dw[NV * (READ == kMixed ? 2 : 1)], zw[NV];
         if constexpr (READ != kFloats) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int c = C::at(lane, k, 0);
+                const int c = C::at(lane, k);
                 rw[k] = C::words(r(), k, H, lane);
                 if constexpr (READ == kWords) {
                     dw[k] = C::words(d(), k, H, lane);
@@ -555,21 +588,26 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
                 zw[k] = a.dr.p ? C::words(z(), k, H, lane) : make_uint4(0, 0, 0, 0);
             }
         }
-        const auto values = [&](int k, float (&x)[8], float (&g)[8], float (&w)[8]) {
+        constexpr int kPair = NV > 1 ? 2 : 1;
+        // vectors k .. k + kPair - 1 of r, dout and the weight
+        const auto values = [&](int k, float (&x)[kPair][8], float (&g)[kPair][8], float (&w)[kPair][8]) {
             if constexpr (READ == kFloats) {
-                C::load(a.weight, a.weight_type, k, H, lane, w);
                 C::load(r(), a.r.type, k, H, lane, x);
                 C::load(d(), a.dout.type, k, H, lane, g);
+                C::load(a.weight, a.weight_type, k, H, lane, w);
             } else {
-                unpack(C::words(a.weight, k, H, lane), w);
-                unpack(rw[k], x);
-                if constexpr (READ == kWords) {
-                    unpack(dw[k], g);
-                } else {
-                    const uint4 p = dw[2 * k], q = dw[2 * k + 1];
-                    const uint32_t v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) g[e] = __uint_as_float(v[e]);
+                for (int i = 0; i < kPair; ++i) {
+                    unpack(C::words(a.weight, k + i, H, lane), w[i]);
+                    unpack(rw[k + i], x[i]);
+                    if constexpr (READ == kWords) {
+                        unpack(dw[k + i], g[i]);
+                    } else {
+                        const uint4 p = dw[2 * (k + i)], q = dw[2 * (k + i) + 1];
+                        const uint32_t v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) g[i][e] = __uint_as_float(v[e]);
+                    }
                 }
             }
         };
@@ -580,15 +618,17 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
         {
             float even1 = 0.f, odd1 = 0.f, even2 = 0.f, odd2 = 0.f;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                float x[8], g[8], w[8];
+            for (int k = 0; k < NV; k += kPair) {
+                float x[kPair][8], g[kPair][8], w[kPair][8];
                 values(k, x, g, w);
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    mul2(g[e], g[e + 1], w[e], w[e + 1]);
-                    fma2(even1, odd1, x[e], x[e + 1], x[e], x[e + 1]);
-                    fma2(even2, odd2, g[e], g[e + 1], x[e], x[e + 1]);
-                }
+                for (int i = 0; i < kPair; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        mul2(g[i][e], g[i][e + 1], w[i][e], w[i][e + 1]);
+                        fma2(even1, odd1, x[i][e], x[i][e + 1], x[i][e], x[i][e + 1]);
+                        fma2(even2, odd2, g[i][e], g[i][e + 1], x[i][e], x[i][e + 1]);
+                    }
             }
             add2(even1, even2, odd1, odd2);
             s = team_sums<TEAM>(even1, even2, sums[parity]);
@@ -600,7 +640,7 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
             for (int k = 0; k < NV; ++k) {
 #pragma unroll 1
                 for (int e = 0; e < 8; ++e) {
-                    const int c = C::at(lane, k, e);
+                    const int c = C::at(lane, k) + e;
                     if (c >= H) continue;
                     const float x = kShrink * one(r(), a.r.type, c);
                     squares = __fmaf_rn(x, x, squares);
@@ -615,25 +655,38 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
         const float q = root(s.x, a.per_column, a.eps, k1), rstd = q * k1;
         const float c = -__fmul_rn(q, __fmul_rn(s.y, a.per_column));
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            float x[8], g[8], w[8], y[8];
+        for (int k = 0; k < NV; k += kPair) {
+            float x[kPair][8], g[kPair][8], w[kPair][8], y[kPair][8];
             values(k, x, g, w);
             if constexpr (READ == kFloats) {
+                if (a.dr.p) {
+                    C::load(z(), a.dr.type, k, H, lane, y);
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = 0.f;
-                if (a.dr.p) C::load(z(), a.dr.type, k, H, lane, y);
+                    for (int j = 0; j < 8 * kPair; ++j) y[j / 8][j % 8] = 0.f;
+                }
             } else {
-                unpack(zw[k], y);
+#pragma unroll
+                for (int i = 0; i < kPair; ++i) unpack(zw[k + i], y[i]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                mul2(x[e], x[e + 1], rstd, rstd);
-                fma2(acc[k][e], acc[k][e + 1], g[e], g[e + 1], x[e], x[e + 1]);
-                mul2(g[e], g[e + 1], w[e], w[e + 1]);
-                fma2(g[e], g[e + 1], x[e], x[e + 1], c, c);
-                fma2(y[e], y[e + 1], rstd, rstd, g[e], g[e + 1]);
+            for (int i = 0; i < kPair; ++i) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    mul2(x[i][e], x[i][e + 1], rstd, rstd);
+                    fma2(acc[k + i][e], acc[k + i][e + 1], g[i][e], g[i][e + 1], x[i][e], x[i][e + 1]);
+                    mul2(g[i][e], g[i][e + 1], w[i][e], w[i][e + 1]);
+                    fma2(g[i][e], g[i][e + 1], x[i][e], x[i][e + 1], c, c);
+                    fma2(y[i][e], y[i][e + 1], rstd, rstd, g[i][e], g[i][e + 1]);
+                }
+                C::store(a.stage_dx ? stage : a.dx.row(t), a.dx.type, k + i, H, lane, y[i]);
             }
-            C::store(a.dx.row(t), a.dx.type, k, H, lane, y);
+        }
+        if (a.stage_dx) {
+            const int size = size_of(a.dx.type);
+            team_sync<TEAM>();
+            C::flush(stage, a.dx.row(t), H * size, size, lane);
+            team_sync<TEAM>();
         }
     }
 
@@ -642,31 +695,43 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
         const float zero[8] = {};
         for (int64_t u = team; u < a.T; u += teams) {
             if (a.listed ? a.listed[u] : u >= lo && u < hi) continue;
+            char *row = a.dx.row(u);
+            if (!a.stage_dx) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) C::store(a.dx.row(u), a.dx.type, k, H, lane, zero);
+                for (int k = 0; k < NV; ++k) C::store(row, a.dx.type, k, H, lane, zero);
+            } else {
+                for (int c = lane; c < H; c += TEAM) {
+                    if (a.dx.type == RK_FP32)
+                        reinterpret_cast<float *>(row)[c] = 0.f;
+                    else
+                        reinterpret_cast<uint16_t *>(row)[c] = 0;
+                }
+            }
         }
     }
     // a block without rows has nothing to leave, and rms_norm_join does not look for it
     if (!a.partial || (int64_t)blockIdx.x * kTeams >= n) return;
-    float *partial = a.partial + (int64_t)blockIdx.x * H;
+    float *partial = a.partial + (int64_t)blockIdx.x * pitch_of(H);
     if constexpr (kTeams == 1) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) C::store(partial, RK_FP32, k, H, lane, acc[k]);
+        for (int k = 0; k < NV; ++k) C::store(reinterpret_cast<char *>(partial), RK_FP32, k, H, lane, acc[k]);
     } else {
         // the block's teams one after the other
+        float *joined = reinterpret_cast<float *>(stages);
+        __syncthreads();
         for (int j = 0; j < kTeams; ++j) {
             if ((int)(threadIdx.x / TEAM) == j) {
 #pragma unroll
-                for (int k = 0; k < NV; ++k)
+                for (int k = 0; k < NV; ++k) {
+                    const int c = C::at(lane, k);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int col = C::at(lane, k, e);
-                        if (col < H) joined[col] = j == 0 ? acc[k][e] : __fadd_rn(joined[col], acc[k][e]);
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        if (c < H) joined[c + e] = j == 0 ? acc[k][e] : __fadd_rn(joined[c + e], acc[k][e]);
+                }
             }
             __syncthreads();
         }
-        for (int col = threadIdx.x; col < H; col += BLOCK) partial[col] = joined[col];
+        for (int c = threadIdx.x; c < H; c += BLOCK) partial[c] = joined[c];
     }
 }
 
@@ -686,7 +751,7 @@ __global__ void __launch_bounds__(32 * kJoinLanes)
     float s = 0.f;
     if (c < H) {
 #pragma unroll 4
-        for (int b = y; b < busy; b += kJoinLanes) s = __fadd_rn(s, partial[(int64_t)b * H + c]);
+        for (int b = y; b < busy; b += kJoinLanes) s = __fadd_rn(s, partial[b * pitch_of(H) + c]);
     }
     sums[y][x] = s;
     __syncthreads();
@@ -784,19 +849,23 @@ __global__ void __launch_bounds__(kListThreads)
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-int element_bytes(int type) { return type == RK_E4M3 ? 1 : type == RK_BF16 ? 2 : 4; }
-
 Matrix matrix(const RulesMatrix *m) {
     if (!m) return Matrix{};
-    return Matrix{static_cast<char *>(const_cast<void *>(m->p)), m->ld * element_bytes(m->type), (int32_t)m->type};
+    return Matrix{static_cast<char *>(const_cast<void *>(m->p)), m->ld * size_of(m->type), (int32_t)m->type};
 }
 
-// Of a type, with every row on a 16-byte boundary (or missing).
-bool plain(const Matrix &m, int type) { return !m.p || (m.type == type && aligned(m.p, 16) && m.step % 16 == 0); }
+// With every row on a boundary of its vectors of 8 and made of whole ones (or missing).
+bool plain(const Matrix &m, int64_t H) {
+    const int vector = m.type == RK_E4M3 ? 8 : 16;
+    return !m.p || (aligned(m.p, vector) && m.step % vector == 0 && H % 8 == 0);
+}
+bool plain(const Matrix &m, int type, int64_t H) { return !m.p || (m.type == type && plain(m, H)); }
 
 // Widest row, team, vectors of 8 a thread, the forward's rows a team and block and its blocks per
 // SM, the backward's block and blocks per SM.
 #define RK_NORM_SHAPES(SHAPE)                \
+    SHAPE(64, 8, 1, 4, 128, 8, 256, 3)       \
+    SHAPE(128, 16, 1, 4, 128, 8, 256, 3)     \
     SHAPE(256, 32, 1, 4, 128, 8, 256, 3)     \
     SHAPE(512, 32, 2, 2, 128, 8, 256, 2)     \
     SHAPE(1024, 32, 4, 1, 128, 6, 128, 4)    \
@@ -806,18 +875,32 @@ bool plain(const Matrix &m, int type) { return !m.p || (m.type == type && aligne
     SHAPE(16384, 512, 4, 1, 512, 2, 512, 1)
 
 constexpr int kSmCount = 152;  // what the backward's partial sums are laid out for, on any device
+constexpr size_t kMostShared = 200 * 1024;  // beside the static part; a stage of the widest row is a third of it
 
-template <int TEAM, int NV, bool VEC, int READ, int ROWS, int BLOCK, int PER_SM>
-cudaError_t forward_launch(const NormArgs &a, cudaStream_t st) {
+template <int TEAM, int NV, int READ, int ROWS, int BLOCK, int PER_SM>
+cudaError_t forward_launch(const NormArgs &a, const DeviceInfo &di, cudaStream_t st) {
+    auto *kernel = rms_norm_forward<TEAM, NV, READ, ROWS, BLOCK, PER_SM>;
     constexpr int64_t kRows = (int64_t)BLOCK / TEAM * ROWS;
-    return launch_dependent(rms_norm_forward<TEAM, NV, VEC, READ, ROWS, BLOCK, PER_SM>, (a.T + kRows - 1) / kRows, BLOCK,
-                            st, a);
+    const size_t shared = a.stage_out || a.stage_residual ? (size_t)(BLOCK / TEAM) * stage_bytes(a.H) : 0;
+    if (shared > 48 * 1024 - 1024) {
+        static std::atomic<uint64_t> allowed{0};
+        const cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kMostShared, di, allowed);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent_smem(kernel, (a.T + kRows - 1) / kRows, BLOCK, shared, st, a);
 }
 
-template <int TEAM, int NV, bool VEC, int READ, int BLOCK, int PER_SM>
-cudaError_t backward_launch(const NormBwdArgs &a, cudaStream_t st) {
-    return launch_dependent_smem(rms_norm_backward<TEAM, NV, VEC, READ, BLOCK, PER_SM>, (int64_t)kSmCount * PER_SM, BLOCK,
-                                 BLOCK > TEAM ? (size_t)a.H * 4 : 0, st, a);
+template <int TEAM, int NV, int READ, int BLOCK, int PER_SM>
+cudaError_t backward_launch(const NormBwdArgs &a, const DeviceInfo &di, cudaStream_t st) {
+    auto *kernel = rms_norm_backward<TEAM, NV, READ, BLOCK, PER_SM>;
+    size_t shared = a.stage_dx ? (size_t)(BLOCK / TEAM) * stage_bytes(a.H) : 0;
+    if (BLOCK > TEAM) shared = std::max(shared, (size_t)pitch_of(a.H) * 4);
+    if (shared > 48 * 1024 - 1024) {
+        static std::atomic<uint64_t> allowed{0};
+        const cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kMostShared, di, allowed);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent_smem(kernel, (int64_t)kSmCount * PER_SM, BLOCK, shared, st, a);
 }
 
 int backward_blocks(int64_t H) {
@@ -851,7 +934,7 @@ BwdBuffers carve(void *base, int64_t T, int64_t n, int64_t H) {
         b.bytes += round256(bytes);
         return static_cast<void *>(q);
     };
-    b.partial = static_cast<float *>(take((size_t)backward_blocks(H) * (size_t)H * 4));
+    b.partial = static_cast<float *>(take((size_t)backward_blocks(H) * (size_t)pitch_of(H) * 4));
     b.rows = static_cast<int32_t *>(take((size_t)n * 4));
     b.counts = static_cast<int32_t *>(take((size_t)(n / kListTile + 1) * 4));
     b.n_rows = static_cast<int64_t *>(take(8));
@@ -866,16 +949,16 @@ cudaError_t launch_rms_norm(const RulesMatrix &x, const RulesMatrix *residual, c
                             int num_seqs, int64_t T, int64_t H, const RulesMatrix *residual_out,
                             const RulesMatrix &out, float *scales, int group, const DeviceInfo &di,
                             cudaStream_t st) {
-    (void)di;
-    const NormArgs a{matrix(&x), matrix(residual), weight, (int32_t)weight_type, eps, 1.f / (float)H, targets, cu,
-                     num_seqs, T, (int32_t)H, matrix(&out), matrix(residual_out), scales, group};
-    const bool words = plain(a.x, RK_BF16) && plain(a.residual, RK_BF16) && plain(a.residual_out, RK_BF16) &&
+    NormArgs a{matrix(&x), matrix(residual), weight, (int32_t)weight_type, eps, 1.f / (float)H, targets, cu, num_seqs,
+               T, (int32_t)H, matrix(&out), matrix(residual_out), scales, H <= 128 ? 0 : group, 0, 0};
+    a.stage_out = !plain(a.out, H);
+    a.stage_residual = !plain(a.residual_out, H);
+    const bool words = plain(a.x, RK_BF16, H) && plain(a.residual, RK_BF16, H) && plain(a.residual_out, RK_BF16, H) &&
                        weight_type == RK_BF16 && aligned(weight, 16);
-#define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER)                                          \
-    if (H <= MAX)                                                                                       \
-        return H % 8 != 0 ? forward_launch<TEAM, NV, false, kFloats, ROWS, FBLOCK, FPER>(a, st)         \
-               : words    ? forward_launch<TEAM, NV, true, kWords, ROWS, FBLOCK, FPER>(a, st)           \
-                          : forward_launch<TEAM, NV, true, kFloats, ROWS, FBLOCK, FPER>(a, st);
+#define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER)                                       \
+    if (H <= MAX)                                                                                    \
+        return words ? forward_launch<TEAM, NV, kWords, ROWS, FBLOCK, FPER>(a, di, st)               \
+                     : forward_launch<TEAM, NV, kFloats, ROWS, FBLOCK, FPER>(a, di, st);
     RK_NORM_SHAPES(SHAPE)
 #undef SHAPE
     return cudaErrorInvalidValue;
@@ -889,10 +972,10 @@ cudaError_t launch_rms_norm_bwd(const RulesMatrix &dout, const RulesMatrix &r, c
                                 int64_t H, const int64_t *order, int64_t n, const RulesMatrix &dx,
                                 float *dweight, bool accumulate, void *workspace, const DeviceInfo &di,
                                 cudaStream_t st) {
-    (void)di;
     const BwdBuffers b = carve(workspace, T, n, H);
     NormBwdArgs a{matrix(&r), matrix(&dout), matrix(dr), weight, (int32_t)weight_type, eps, 1.f / (float)H, cu, num_seqs,
-                  T, (int32_t)H, nullptr, nullptr, nullptr, matrix(&dx), dweight ? b.partial : nullptr};
+                  T, (int32_t)H, nullptr, nullptr, nullptr, matrix(&dx), 0, dweight ? b.partial : nullptr};
+    a.stage_dx = !plain(a.dx, H);
     if (targets || order) {
         const Candidates c{order, n, T, targets, cu, num_seqs};
         const int64_t tiles = std::max<int64_t>(1, (n + kListTile - 1) / kListTile);
@@ -907,15 +990,14 @@ cudaError_t launch_rms_norm_bwd(const RulesMatrix &dout, const RulesMatrix &r, c
         a.n_rows = b.n_rows;
         a.listed = b.listed;
     }
-    const bool words = plain(a.r, RK_BF16) && plain(a.dr, RK_BF16) && weight_type == RK_BF16 && aligned(weight, 16);
-    const int read = words && plain(a.dout, RK_BF16) ? kWords : words && plain(a.dout, RK_FP32) ? kMixed : kFloats;
+    const bool words = plain(a.r, RK_BF16, H) && plain(a.dr, RK_BF16, H) && weight_type == RK_BF16 && aligned(weight, 16);
+    const int read = words && plain(a.dout, RK_BF16, H) ? kWords : words && plain(a.dout, RK_FP32, H) ? kMixed : kFloats;
     const auto run = [&] {
-#define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER)                                          \
-    if (H <= MAX)                                                                                       \
-        return H % 8 != 0       ? backward_launch<TEAM, NV, false, kFloats, BBLOCK, BPER>(a, st)        \
-               : read == kWords ? backward_launch<TEAM, NV, true, kWords, BBLOCK, BPER>(a, st)          \
-               : read == kMixed ? backward_launch<TEAM, NV, true, kMixed, BBLOCK, BPER>(a, st)          \
-                                : backward_launch<TEAM, NV, true, kFloats, BBLOCK, BPER>(a, st);
+#define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER)                                       \
+    if (H <= MAX)                                                                                    \
+        return read == kWords   ? backward_launch<TEAM, NV, kWords, BBLOCK, BPER>(a, di, st)         \
+               : read == kMixed ? backward_launch<TEAM, NV, kMixed, BBLOCK, BPER>(a, di, st)         \
+                                : backward_launch<TEAM, NV, kFloats, BBLOCK, BPER>(a, di, st);
         RK_NORM_SHAPES(SHAPE)
 #undef SHAPE
         return cudaErrorInvalidValue;

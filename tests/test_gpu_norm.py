@@ -14,7 +14,7 @@ BF16, FP32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 # last unit that is not full
 SHAPES = [(1, 1), (3, 7), (37, 8), (2, 100), (640, 64), (17, 256), (9, 264), (33, 513), (40, 512), (300, 1000),
           (7, 1023), (65, 1024), (11, 2047), (12, 2048), (1300, 2056), (13, 4096), (5, 4097), (700, 5000),
-          (6, 8192), (3, 8193), (3, 16384), (2, 16383)]
+          (6, 8192), (3, 8193), (3, 16384), (2, 16383), (1000, 65), (999, 128), (301, 129)]
 
 
 @pytest.fixture(scope="module")
