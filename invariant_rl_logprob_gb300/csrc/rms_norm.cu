@@ -206,6 +206,22 @@ __host__ __device__ constexpr int size_of(int type) { return type == RK_E4M3 ? 1
 // Bytes of a team's stage.
 __host__ __device__ constexpr int stage_bytes(int H) { return (H + 7) / 8 * 32 + 32; }
 
+// Vector k of a bf16 or fp32 row on a 16-byte boundary, H a multiple of 8, as it was read: loads of
+// several rows are on their way before one is looked at, whatever their types.
+struct Raw {
+    uint4 a, b;  // b: the second half of eight fp32
+};
+template <int TEAM>
+__device__ __forceinline__ Raw raw_vector(const char *row, bool wide, bool wanted, int k, int H, int lane) {
+    const int c = Columns<TEAM>::at(lane, k);
+    const uint4 *p = reinterpret_cast<const uint4 *>(row + (wide ? 4 : 2) * c);
+    wanted = wanted && c < H;
+    Raw r;
+    r.a = wanted ? p[0] : make_uint4(0, 0, 0, 0);
+    r.b = wanted && wide ? p[1] : make_uint4(0, 0, 0, 0);
+    return r;
+}
+
 __device__ __forceinline__ void unpack(uint4 p, float (&x)[8]) {
     const uint32_t q[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
@@ -213,6 +229,14 @@ __device__ __forceinline__ void unpack(uint4 p, float (&x)[8]) {
         x[2 * i] = bf16_lo(q[i]);
         x[2 * i + 1] = bf16_hi(q[i]);
     }
+}
+
+__device__ __forceinline__ void unpack(const Raw &r, bool wide, float (&x)[8]) {
+    float narrow[8];
+    unpack(r.a, narrow);
+    const uint32_t v[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = wide ? __uint_as_float(v[e]) : narrow[e];
 }
 
 // ---- sums and maxima over a team ----
@@ -304,9 +328,33 @@ __device__ __forceinline__ float scale_of(unsigned top, float *inverse) {
     return top ? s : 0.f;
 }
 
-// How a row is read: kWords where x, residual, residual_out and weight are bf16 on 16-byte
-// boundaries, kFloats anything else.
-enum Read { kWords, kFloats };
+// How rows are read.
+//   kWords    activations in bf16 on 16-byte boundaries: kept as their words
+//   kAligned  bf16 or fp32 on 16-byte boundaries: kept as floats
+//   kFloats   anything else, shifted on the way
+// The weight is on a 16-byte boundary in the first two.
+enum Read { kWords, kAligned, kFloats };
+
+// Vector k of the weight.
+template <int TEAM, int READ>
+__device__ __forceinline__ void weight_vector(const void *w, int type, int k, int H, int lane, float (&x)[8]) {
+    if constexpr (READ == kFloats) {
+        float y[1][8];
+        Columns<TEAM>::load(w, type, k, H, lane, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = y[0][e];
+    } else {
+        const int c = Columns<TEAM>::at(lane, k);
+        if (c >= H) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        } else if (type == RK_FP32) {
+            get8(static_cast<const float *>(w) + c, x);
+        } else {
+            get8(static_cast<const uint16_t *>(w) + c, x);
+        }
+    }
+}
 
 // A thread's part of a row.
 template <int NV, int READ>
@@ -329,7 +377,7 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
     __shared__ float2 sums[2][32];
     __shared__ unsigned maxima[32];
     extern __shared__ __align__(16) char stages[];  // where rows leave through them
-    constexpr int kPair = NV > 1 ? 2 : 1;  // vectors read at once where nothing is kept as words
+    constexpr int kPair = NV > 1 ? 2 : 1;  // vectors read at once where they are shifted
     const int lane = threadIdx.x % TEAM, H = a.H;
     char *stage = stages + (size_t)(threadIdx.x / TEAM) * stage_bytes(H);
     wait_prior_grid();
@@ -360,6 +408,26 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
                     uint4 &p = part[i].p[k];
                     p = make_uint4(add_bf16x2(p.x, q[k].x), add_bf16x2(p.y, q[k].y), add_bf16x2(p.z, q[k].z),
                                    add_bf16x2(p.w, q[k].w));
+                }
+            }
+        } else if constexpr (READ == kAligned) {
+            const bool x_wide = a.x.type == RK_FP32, z_wide = a.residual.type == RK_FP32;
+            Raw p[NV], q[NV];
+#pragma unroll
+            for (int k = 0; k < NV; ++k) p[k] = raw_vector<TEAM>(x, x_wide, live[i], k, H, lane);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) q[k] = raw_vector<TEAM>(z, z_wide, live[i] && a.residual.p, k, H, lane);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                unpack(p[k], x_wide, part[i].v[k]);
+                if (!a.residual.p) continue;
+                float y[8];
+                unpack(q[k], z_wide, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float &v = part[i].v[k][e];
+                    v = __fadd_rn(v, y[e]);
+                    if (a.residual_out.type == RK_BF16) v = bf16_lo(pack_bf16x2(v, 0.f));
                 }
             }
         } else {
@@ -397,7 +465,7 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
         const int64_t t = t0 + i;
         if (t >= a.T) return;  // the whole team
         if (a.residual.p) {
-            char *to = READ == kFloats && a.stage_residual ? stage : a.residual_out.row(t);
+            char *to = READ != kWords && a.stage_residual ? stage : a.residual_out.row(t);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 if constexpr (READ == kWords) {
@@ -407,7 +475,7 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
                     C::store(to, a.residual_out.type, k, H, lane, part[i].v[k]);
                 }
             }
-            if (READ == kFloats && a.stage_residual) {
+            if (READ != kWords && a.stage_residual) {
                 const int size = size_of(a.residual_out.type);
                 team_sync<TEAM>();
                 C::flush(stage, a.residual_out.row(t), H * size, size, lane);
@@ -441,16 +509,13 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
 
         // y, a row that is not active being 0 as it is
         const auto result = [&](int k, float (&y)[8]) {
-            float w[1][8];
-            if constexpr (READ == kWords)
-                unpack(C::words(a.weight, k, H, lane), w[0]);
-            else
-                C::load(a.weight, a.weight_type, k, H, lane, w);
+            float w[8];
+            weight_vector<TEAM, READ>(a.weight, a.weight_type, k, H, lane, w);
             part[i].get(k, y);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 mul2(y[e], y[e + 1], rstd, rstd);
-                mul2(y[e], y[e + 1], w[0][e], w[0][e + 1]);
+                mul2(y[e], y[e + 1], w[e], w[e + 1]);
             }
         };
         const bool e4m3 = a.out.type == RK_E4M3;
@@ -522,11 +587,10 @@ struct NormBwdArgs {
 
 __host__ __device__ constexpr int64_t pitch_of(int64_t H) { return (H + 7) / 8 * 8; }
 
-// What a row is read as, and kept as between its sums and its results.
-//   kWords    r, dout, dr and weight bf16 on 16-byte boundaries: words
-//   kMixed    the same with dout in fp32
-//   kFloats   anything else: nothing is kept, it is read again (from the first caches)
-constexpr int kMixed = 2;
+// What the backward keeps of a row between its sums and its results: with kWords (r, dout and dr in
+// bf16) and kMixed (the same with dout in fp32) its words; otherwise nothing, it is read again,
+// from the caches.
+constexpr int kMixed = 3;
 
 template <int TEAM, int NV, int READ, int BLOCK, int PER_SM>
 __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_constant__ NormBwdArgs a) {
@@ -573,7 +637,7 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
             }
         }
         uint4 rw[NV], dw[NV * (READ == kMixed ? 2 : 1)], zw[NV];
-        if constexpr (READ != kFloats) {
+        if constexpr (READ == kWords || READ == kMixed) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int c = C::at(lane, k);
@@ -595,10 +659,24 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
                 C::load(r(), a.r.type, k, H, lane, x);
                 C::load(d(), a.dout.type, k, H, lane, g);
                 C::load(a.weight, a.weight_type, k, H, lane, w);
+            } else if constexpr (READ == kAligned) {
+                const bool r_wide = a.r.type == RK_FP32, d_wide = a.dout.type == RK_FP32;
+                Raw p[kPair], q[kPair];
+#pragma unroll
+                for (int i = 0; i < kPair; ++i) {
+                    p[i] = raw_vector<TEAM>(r(), r_wide, true, k + i, H, lane);
+                    q[i] = raw_vector<TEAM>(d(), d_wide, true, k + i, H, lane);
+                }
+#pragma unroll
+                for (int i = 0; i < kPair; ++i) {
+                    weight_vector<TEAM, READ>(a.weight, a.weight_type, k + i, H, lane, w[i]);
+                    unpack(p[i], r_wide, x[i]);
+                    unpack(q[i], d_wide, g[i]);
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < kPair; ++i) {
-                    unpack(C::words(a.weight, k + i, H, lane), w[i]);
+                    weight_vector<TEAM, READ>(a.weight, a.weight_type, k + i, H, lane, w[i]);
                     unpack(rw[k + i], x[i]);
                     if constexpr (READ == kWords) {
                         unpack(dw[k + i], g[i]);
@@ -657,8 +735,17 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
 #pragma unroll
         for (int k = 0; k < NV; k += kPair) {
             float x[kPair][8], g[kPair][8], w[kPair][8], y[kPair][8];
+            const bool z_wide = a.dr.type == RK_FP32;
+            Raw zr[kPair];
+            if constexpr (READ == kAligned) {
+#pragma unroll
+                for (int i = 0; i < kPair; ++i) zr[i] = raw_vector<TEAM>(z(), z_wide, a.dr.p, k + i, H, lane);
+            }
             values(k, x, g, w);
-            if constexpr (READ == kFloats) {
+            if constexpr (READ == kAligned) {
+#pragma unroll
+                for (int i = 0; i < kPair; ++i) unpack(zr[i], z_wide, y[i]);
+            } else if constexpr (READ == kFloats) {
                 if (a.dr.p) {
                     C::load(z(), a.dr.type, k, H, lane, y);
                 } else {
@@ -953,12 +1040,13 @@ cudaError_t launch_rms_norm(const RulesMatrix &x, const RulesMatrix *residual, c
                T, (int32_t)H, matrix(&out), matrix(residual_out), scales, H <= 128 ? 0 : group, 0, 0};
     a.stage_out = !plain(a.out, H);
     a.stage_residual = !plain(a.residual_out, H);
-    const bool words = plain(a.x, RK_BF16, H) && plain(a.residual, RK_BF16, H) && plain(a.residual_out, RK_BF16, H) &&
-                       weight_type == RK_BF16 && aligned(weight, 16);
+    const bool on16 = plain(a.x, H) && plain(a.residual, H) && aligned(weight, 16);
+    const bool words = on16 && plain(a.x, RK_BF16, H) && plain(a.residual, RK_BF16, H) && plain(a.residual_out, RK_BF16, H);
 #define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER)                                       \
     if (H <= MAX)                                                                                    \
-        return words ? forward_launch<TEAM, NV, kWords, ROWS, FBLOCK, FPER>(a, di, st)               \
-                     : forward_launch<TEAM, NV, kFloats, ROWS, FBLOCK, FPER>(a, di, st);
+        return words  ? forward_launch<TEAM, NV, kWords, ROWS, FBLOCK, FPER>(a, di, st)              \
+               : on16 ? forward_launch<TEAM, NV, kAligned, ROWS, FBLOCK, (FPER * 2 + 2) / 3>(a, di, st) \
+                      : forward_launch<TEAM, NV, kFloats, ROWS, FBLOCK, FPER>(a, di, st);
     RK_NORM_SHAPES(SHAPE)
 #undef SHAPE
     return cudaErrorInvalidValue;
@@ -990,14 +1078,16 @@ cudaError_t launch_rms_norm_bwd(const RulesMatrix &dout, const RulesMatrix &r, c
         a.n_rows = b.n_rows;
         a.listed = b.listed;
     }
-    const bool words = plain(a.r, RK_BF16, H) && plain(a.dr, RK_BF16, H) && weight_type == RK_BF16 && aligned(weight, 16);
-    const int read = words && plain(a.dout, RK_BF16, H) ? kWords : words && plain(a.dout, RK_FP32, H) ? kMixed : kFloats;
+    const bool on16 = plain(a.r, H) && plain(a.dout, H) && plain(a.dr, H) && aligned(weight, 16);
+    const bool words = a.r.type == RK_BF16 && (!dr || a.dr.type == RK_BF16);
+    const int read = !on16 ? kFloats : !words ? kAligned : a.dout.type == RK_BF16 ? kWords : kMixed;
     const auto run = [&] {
 #define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER)                                       \
     if (H <= MAX)                                                                                    \
-        return read == kWords   ? backward_launch<TEAM, NV, kWords, BBLOCK, BPER>(a, di, st)         \
-               : read == kMixed ? backward_launch<TEAM, NV, kMixed, BBLOCK, BPER>(a, di, st)         \
-                                : backward_launch<TEAM, NV, kFloats, BBLOCK, BPER>(a, di, st);
+        return read == kWords     ? backward_launch<TEAM, NV, kWords, BBLOCK, BPER>(a, di, st)       \
+               : read == kMixed   ? backward_launch<TEAM, NV, kMixed, BBLOCK, BPER>(a, di, st)       \
+               : read == kAligned ? backward_launch<TEAM, NV, kAligned, BBLOCK, BPER>(a, di, st)     \
+                                  : backward_launch<TEAM, NV, kFloats, BBLOCK, BPER>(a, di, st);
         RK_NORM_SHAPES(SHAPE)
 #undef SHAPE
         return cudaErrorInvalidValue;
