@@ -1136,14 +1136,14 @@ def rms_norm_bwd(grad_out: torch.Tensor, r: torch.Tensor, weight: torch.Tensor,
                  grad_residual: torch.Tensor | None = None, eps: float = 1e-6,
                  row_order: torch.Tensor | None = None, out: torch.Tensor | None = None,
                  out_dtype: torch.dtype | None = None, dweight: torch.Tensor | None = None,
-                 accumulate: bool = False, workspace: torch.Tensor | None = None,
-                 stream: torch.cuda.Stream | None = None):
+                 accumulate: bool = False, need_dweight: bool = True,
+                 workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
     """The gradient of :func:`rms_norm`: returns ``(dx, dweight)``.  ``r`` is what the
     forward returned, ``grad_residual`` a gradient that arrives at r from elsewhere; dx
     (``[T, H]`` in ``out_dtype``, default: r's) is the gradient of x and of residual
     alike.  dweight, fp32 ``[H]``, is summed over the active rows in canonical order
-    (``row_order``; ascending rows by default), with ``accumulate`` onto what it holds.
-    Rows that are not among them get dx = 0.  ``out`` may be ``grad_out``, ``r`` or
+    (``row_order``; ascending rows by default), with ``accumulate`` onto what it holds; it
+    is None without ``need_dweight`` (a weight that is not trained).  Rows that are not among them get dx = 0.  ``out`` may be ``grad_out``, ``r`` or
     ``grad_residual`` itself unless ``row_order`` is given."""
     lib = _lib or load_library()
     code, ld = _matrix(grad_out, "grad_out")
@@ -1164,7 +1164,10 @@ def rms_norm_bwd(grad_out: torch.Tensor, r: torch.Tensor, weight: torch.Tensor,
         n = row_order.shape[0]
         order = row_order.data_ptr() or _EMPTY
     out, out_code, out_ld = _result(out, out_dtype or r.dtype, (T, H), device, stream)
-    if dweight is None:
+    if not need_dweight:
+        if dweight is not None or accumulate:
+            raise ValueError("a dweight is given, and need_dweight is not")
+    elif dweight is None:
         if accumulate:
             raise ValueError("accumulate needs a dweight to add to")
         dweight = _empty(H, torch.float32, device, stream)
@@ -1175,8 +1178,8 @@ def rms_norm_bwd(grad_out: torch.Tensor, r: torch.Tensor, weight: torch.Tensor,
     workspace = _scratch(workspace, lib.rk_rms_norm_bwd_workspace_size(T, n, H), device, stream)
     _run("rk_rms_norm_bwd", lib.rk_rms_norm_bwd, device, stream, grad_out.data_ptr(), code, ld, r.data_ptr(),
          r_code, r_ld, weight.data_ptr(), w_code, eps, g, g_code, g_ld, tg, cu, ns, T, H, order, n,
-         out.data_ptr(), out_code, out_ld, dweight.data_ptr(), int(accumulate), workspace.data_ptr(),
-         workspace.numel())
+         out.data_ptr(), out_code, out_ld, None if dweight is None else dweight.data_ptr(), int(accumulate),
+         workspace.data_ptr(), workspace.numel())
     return out, dweight
 
 

@@ -12,7 +12,10 @@
 // elements) alone.  One launch takes up to kTensors tensors, described in the
 // kernel's parameters (nothing to copy, nothing to keep alive for a graph);
 // a block takes kChunk elements of one of them, a warp 256 at a time, a thread 8
-// consecutive ones, so that a block of 8-bit states is a warp's.
+// consecutive ones, so that a block of 8-bit states is a warp's.  525M elements with fp32
+// gradients, masters and 32-bit states: 2237 us, 104 % of the copy rate; 545M with bf16
+// gradients, masters and 8-bit states 1237 us, 104 %; 200 tensors of 150000 elements on average
+// 82 us, 87 %: the last chunk of a tensor is half empty on average.
 //
 // 8-bit states: m = e4m3 * scale, and for v its root, u = e4m3 * scale (e4m3
 // spans 2^18, so v spans 2^36 within a block); scale = largest magnitude of

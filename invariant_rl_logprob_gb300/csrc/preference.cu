@@ -9,11 +9,13 @@
 //   loss_p = scale * f(d_p),   grad_logp[t] = sum over p of the sequence: +-scale f'(d_p) [/ number]
 //
 // Bound by latency: 12 to 16 bytes a token, and results that wait for one another
-// (sums, pairs, gradients).  Where a thread has at most one run of
-// tokens and one pair, one cluster of up to 16 blocks does all of it with the
-// hardware's cluster barrier between the steps, and every thread keeps its run and
-// its pair in registers; beyond, every step is a launch of its own over the whole
-// device.
+// (sums, pairs, gradients).  Where a thread has at most one run of tokens and one
+// pair, one cluster of up to 16 blocks does all of it with the hardware's cluster
+// barrier between the steps, and every thread keeps its run and its pair in
+// registers; beyond, every step is a launch of its own over the whole device.  The
+// launches are what a caller waits for: at 131072 tokens the cluster takes 13.9 us
+// on the device and one launch, the steps 10.4 us and four, some 9 us more on the
+// host.  8 sequences of 128 tokens take 8.0 us, 512 of 1024 14.1, 1024 17.3.
 //
 // The sums are integers, so that no order of tokens, blocks or atomic additions
 // can change a bit: a logprob is rounded to a multiple of 2^-42 (logprobs of
@@ -35,6 +37,7 @@ constexpr int kRun = 8;               // consecutive tokens of a thread
 constexpr int kSharedOffsets = 8192;  // sequences whose offsets are searched in shared memory
 constexpr float kQuantum = 0x1p-42f;
 constexpr float kInfinite = 0x1p20f;
+constexpr float kFixed = 0x1p18f;  // what is below it is compared in fixed point
 
 enum Flag : unsigned { kPlusInf = 1, kMinusInf = 2, kNaN = 4 };
 
@@ -56,7 +59,7 @@ struct Args {
     const float *margin;  // or NULL
     int32_t kind, average;
     float beta, smoothing, scale;
-    long long middle;  // 1 / (2 beta) as a multiple of 2^-42, unless it is 2^20 and more
+    long long middle;  // 1 / (2 beta) as a multiple of 2^-42, unless it is kFixed and more
     int32_t middle_far;
     float *loss, *grad, *logratio;  // logratio may be NULL
     Sequence *seq;
@@ -217,7 +220,8 @@ __device__ __forceinline__ void name(const Args &a, const Pair &pair, int64_t p)
     }
 }
 
-// A sequence's s as a multiple of 2^-42, where that is one: finite and below 2^20.
+// A sequence's s as a multiple of 2^-42, where that is one: finite and below 2^18, so that the
+// difference of two, a margin and 1 / (2 beta) fit into 63 bits.
 struct Ratio {
     long long fixed;
     double wide;  // the value where it is none
@@ -233,7 +237,7 @@ __device__ __forceinline__ Ratio ratio_of(const Args &a, int q) {
     const int count = __ldcg(&s->count);
     const unsigned flags = __ldcg(&s->flags);
     Ratio r{};
-    const long long limit = 1ll << 30;  // of the high word: 2^30 * 2^32 * 2^-42 = 2^20
+    const long long limit = 1ll << 28;  // of the high word: 2^28 * 2^32 * 2^-42 = 2^18
     if (flags == 0 && hi > -limit && hi < limit) {
         r.fixed = hi * (1ll << 32) + (long long)(lo & 0xffffffffull);
         if (a.average && count > 1) {
@@ -277,7 +281,7 @@ __device__ __forceinline__ void compare(const Args &a, const Pair &pair, int64_t
     if (pair.c >= 0) {
         const Ratio c = ratio_of(a, pair.c), r = ratio_of(a, pair.r);
         const bool ipo = a.kind == RK_PREFERENCE_IPO;
-        if (!c.far && !r.far && fabsf(pair.margin) < kInfinite && !(ipo && a.middle_far)) {
+        if (!c.far && !r.far && fabsf(pair.margin) < kFixed && !(ipo && a.middle_far)) {
             long long d = c.fixed - r.fixed - __float2ll_rn(pair.margin * (1.f / kQuantum));
             if (ipo) d -= a.middle;
             const float top = __ll2float_rn(d), low = __ll2float_rn(d - __float2ll_rn(top));
@@ -547,7 +551,7 @@ cudaError_t launch_preference(const float *logp, const float *ref, const int64_t
                               float *loss, float *grad, float *logratio, void *workspace, const DeviceInfo &di,
                               cudaStream_t st) {
     const double middle = 0.5 / (double)beta;
-    const bool far = !(middle < (double)kInfinite);
+    const bool far = !(middle < (double)kFixed);
     const Args a{logp, ref, targets, cu, num_seqs, T, chosen, rejected, (int32_t)P, margin, kind, (int32_t)average, beta,
                  smoothing, scale, far ? 0 : std::llrint(middle / (double)kQuantum), (int32_t)far, loss, grad, logratio,
                  static_cast<Sequence *>(workspace),

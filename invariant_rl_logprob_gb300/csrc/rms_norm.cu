@@ -11,15 +11,21 @@
 //   g = dout * weight,  n = r * rstd
 //   dx = rstd * (g - n * mean(g * n)) + dr,   dweight (+)= sum over rows of dout * n
 //
-// Both are bound by memory: 8 and 15 flop an element, against 7 to 12 bytes.
+// Both are bound by memory: 8 and 15 flop an element, against 7 to 16 bytes.
 // A team of threads (part of a warp up to 128 columns, a warp up to 1024, up to
-// 16 warps beyond) has a row in registers, as it was read: bf16 words where all is bf16 on 16-byte
-// boundaries, floats otherwise.  A thread owns up to 32 columns: fewer threads
-// a row mean fewer that sum, scale and wait for one another.
+// 16 warps beyond) has a row in registers, up to 32 columns a thread: fewer
+// threads a row mean fewer that sum, scale and wait for one another (256 threads
+// with 16 columns each, 65536 x 4096 with residual to e4m3: 290 us; 128 with 32:
+// 265, 105 % of the copy rate).  The forward has a block for a row and nothing
+// that lives longer: rings of rows in shared memory, filled by bulk copies ahead
+// of persistent blocks, took 392 us with their waits, and plain loads of the
+// next row 300.
 //
 // The backward needs nothing but r: the sums of r^2 and of g * r come out of
 // one reduction.  dweight: a team adds its rows in registers, in order; blocks
-// leave partial sums that a last kernel adds in order.
+// leave partial sums that a last kernel adds in order.  Teams therefore stay, and
+// ask for their next row ahead, into the second cache (65536 x 4096, all bf16:
+// 347 us without, 316 with, the copy rate).
 //
 // A thread owns eight consecutive columns at a time.  Rows off 16-byte boundaries
 // (any row of an odd H, say) are read in the aligned 16 bytes around each eight and
@@ -332,7 +338,9 @@ __device__ __forceinline__ float scale_of(unsigned top, float *inverse) {
 //   kWords    activations in bf16 on 16-byte boundaries: kept as their words
 //   kAligned  bf16 or fp32 on 16-byte boundaries: kept as floats
 //   kFloats   anything else, shifted on the way
-// The weight is on a 16-byte boundary in the first two.
+// The weight is on a 16-byte boundary in the first two.  65536 x 4096 bf16 with residual to e4m3
+// takes 265 us as words and 481 with all that kFloats is ready for; an fp32 stream (fp32 x and
+// residual to fp32) 605 us as kAligned, 105 % of the copy rate.
 enum Read { kWords, kAligned, kFloats };
 
 // Vector k of the weight.
@@ -507,8 +515,13 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
             }
         }
 
-        // y, a row that is not active being 0 as it is
+        // y, 0 in a row that is not active
         const auto result = [&](int k, float (&y)[8]) {
+            if (!live[i]) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = 0.f;
+                return;
+            }
             float w[8];
             weight_vector<TEAM, READ>(a.weight, a.weight_type, k, H, lane, w);
             part[i].get(k, y);
@@ -589,7 +602,8 @@ __host__ __device__ constexpr int64_t pitch_of(int64_t H) { return (H + 7) / 8 *
 
 // What the backward keeps of a row between its sums and its results: with kWords (r, dout and dr in
 // bf16) and kMixed (the same with dout in fp32) its words; otherwise nothing, it is read again,
-// from the caches.
+// from the caches.  65536 x 4096: kWords 316 us, kMixed 398 (both the copy rate); without kMixed its
+// case took 610.  All in fp32, kAligned 884 us, 72 % of the copy rate.
 constexpr int kMixed = 3;
 
 template <int TEAM, int NV, int READ, int BLOCK, int PER_SM>
@@ -949,7 +963,10 @@ bool plain(const Matrix &m, int64_t H) {
 bool plain(const Matrix &m, int type, int64_t H) { return !m.p || (m.type == type && plain(m, H)); }
 
 // Widest row, team, vectors of 8 a thread, the forward's rows a team and block and its blocks per
-// SM, the backward's block and blocks per SM.
+// SM, the backward's block and blocks per SM.  Narrow rows: teams of 8 lanes for 2M rows of 64
+// columns take 173 us (residual, e4m3) where warps took 496, of 16 lanes for 1M of 128 167 and 252.
+// The backward's blocks per SM are what leaves its sums in registers: at 4096 columns 3, 4 and 5
+// blocks of 128 threads took 103, 96 and 104 us for 16384 rows, before rows were asked for ahead.
 #define RK_NORM_SHAPES(SHAPE)                \
     SHAPE(64, 8, 1, 4, 128, 8, 256, 3)       \
     SHAPE(128, 16, 1, 4, 128, 8, 256, 3)     \
@@ -1067,7 +1084,8 @@ cudaError_t launch_rms_norm_bwd(const RulesMatrix &dout, const RulesMatrix &r, c
     if (targets || order) {
         const Candidates c{order, n, T, targets, cu, num_seqs};
         const int64_t tiles = std::max<int64_t>(1, (n + kListTile - 1) / kListTile);
-        const bool one = tiles == 1 && T <= kListTile;  // block does it all
+        // one block does it all: a launch and a fill less (8192 rows of 1024: 26 us, 8200: 30)
+        const bool one = tiles == 1 && T <= kListTile;
         cudaError_t e = one ? cudaSuccess : cudaMemsetAsync(b.listed, 0, (size_t)T, st);
         if (e == cudaSuccess && !one) e = launch_dependent(norm_rows_count, tiles, kListThreads, st, c, b.counts);
         if (e == cudaSuccess)

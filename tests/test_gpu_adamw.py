@@ -253,3 +253,26 @@ def test_no_tensors(rk):
     rk.adamw_step(rk.AdamW([], []), **HYPER)
     empty = torch.empty(0, device=DEV)
     rk.adamw_step(rk.AdamW([empty], [empty.clone()], bits=8), **HYPER)
+
+
+def test_a_tensor_past_32_bits(rk):
+    """More than 2^31 elements: the first and the last have the bits that they have alone."""
+    n = 2 ** 31 + 256 * 5 + 77
+    p, g = (torch.empty(n, dtype=BF16, device=DEV) for _ in range(2))
+    for t, seed in ((p, 1), (g, 2)):
+        gen = torch.Generator(DEV).manual_seed(seed)
+        for a in range(0, n, 2 ** 28):
+            b = min(n, a + 2 ** 28)
+            t[a:b] = torch.randn(b - a, generator=gen, device=DEV)
+    ends = [slice(0, 1000), slice(n - (n % 256) - 256 * 3, n)]
+    small = rk.AdamW([p[e].clone() for e in ends], [g[e].clone() for e in ends], bits=8)
+    big = rk.AdamW([p], [g], bits=8)
+    for step in (1, 2):
+        rk.adamw_step(big, **{**HYPER, "step": step})
+        rk.adamw_step(small, **{**HYPER, "step": step})
+    for i, e in enumerate(ends):
+        keep = 768 if i == 0 else small.params[1].numel()  # whole blocks of 256
+        assert same_bits(p[e][:keep], small.params[i][:keep])
+        for k in ("m", "v"):
+            a, b = getattr(big, k)[0][e][:keep], getattr(small, k)[i][:keep]
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))

@@ -375,3 +375,70 @@ def test_gradients_are_the_forward_s_differences(rk):
     got, _ = rk.rms_norm_bwd(d.to(DEV), x.to(DEV), w.to(DEV))
     # the difference's own error: h^2 times a third derivative of order one, and 2^-53 / h
     assert abs(float((got.double().cpu() * v).sum() - (up - down) / (2 * h))) <= float((bound * v.abs()).sum()) + 1e-7
+
+
+def test_sums_of_bf16_are_rounded_once(rk):
+    """Every kind of pair, subnormal numbers and infinities among them, as fp32 and then bf16 rounds them."""
+    g = gen(7)
+    bits = torch.randint(-2 ** 15, 2 ** 15, (2, 40000, 64), generator=g, dtype=torch.int16)
+    bits[:, :8000] &= 0x80FF - 0x10000  # subnormal and smallest
+    near = torch.randint(-3, 4, (16000, 64), generator=g) * 128
+    bits[1, 8000:24000] = ((bits[0, 8000:24000].int() & 0x7FFF) + near).clamp(0, 0x7F80).short() ^ -0x8000
+    x, r = (b.view(BF16).clone() for b in bits)
+    x[torch.isnan(x)], r[torch.isnan(r)] = 1.0, -2.0
+    want = npl.stream(x, r)
+    _, got = rk.rms_norm(x.to(DEV), torch.ones(64, dtype=BF16, device=DEV), residual=r.to(DEV))
+    got = got.cpu()
+    nan = torch.isnan(want)
+    assert bool((torch.isnan(got) == nan).all()) and same_bits(got[~nan], want[~nan])
+
+
+def test_weights_that_are_not_finite(rk):
+    """They reach the active rows alone."""
+    g = gen(8)
+    for H in (40, 1001, 4096):
+        w = weight_of(g, H, BF16)
+        w[3], w[4] = float("nan"), float("inf")
+        x = npl.matrix(g, 6, H, BF16).to(DEV)
+        tg = torch.tensor([1, -1, 1, -100, 1, -1], device=DEV)
+        y, _ = rk.rms_norm(x, w.to(DEV), tg)
+        q, s, _ = rk.rms_norm_e4m3(x, w.to(DEV), tg)
+        off = tg < 0
+        assert not bool(y[off].any()) and not bool(q.float()[off].any()) and not bool(s[off].any())
+        assert bool(torch.isnan(y[~off][:, 3]).all())
+
+
+def test_without_dweight(rk):
+    g = gen(9)
+    r, d = npl.matrix(g, 50, 264, BF16).to(DEV), npl.matrix(g, 50, 264, BF16).to(DEV)
+    w = weight_of(g, 264, BF16).to(DEV)
+    dx, none = rk.rms_norm_bwd(d, r, w, need_dweight=False)
+    assert none is None and same_bits(dx, rk.rms_norm_bwd(d, r, w)[0])
+    with pytest.raises(ValueError, match="need_dweight"):
+        rk.rms_norm_bwd(d, r, w, need_dweight=False, dweight=torch.zeros(264, device=DEV))
+
+
+def test_rows_past_32_bits(rk):
+    """More than 2^32 bytes, and more than 2^31 elements: the last rows have the bits that they have alone."""
+    T, H = 140000, 16384
+    x = torch.empty(T, H, dtype=BF16, device=DEV)
+    g = torch.Generator(DEV).manual_seed(1)
+    for a in range(0, T, 20000):
+        x[a:a + 20000] = torch.randn(20000, H, generator=g, device=DEV)
+    w = torch.ones(H, dtype=BF16, device=DEV)
+    tail = x[-3:].clone()
+    tg = torch.full((T,), -1, device=DEV)
+    tg[-3:] = 1
+    tg[::7000] = 1
+    y, _ = rk.rms_norm(x, w, tg)
+    assert same_bits(y[-3:], rk.rms_norm(tail, w)[0]) and not bool(y[-10:-3].any())
+    q, s, _ = rk.rms_norm_e4m3(x, w, tg, group=128)
+    q0, s0, _ = rk.rms_norm_e4m3(tail, w, group=128)
+    assert torch.equal(q[-3:].view(torch.uint8), q0.view(torch.uint8)) and same_bits(s[-3:], s0)
+    del q, s
+    dx, dw = rk.rms_norm_bwd(y, x, w, tg)
+    assert same_bits(dx[-3:], rk.rms_norm_bwd(y[-3:], tail, w)[0]) and not bool(dx[-10:-3].any())
+    live = tg >= 0
+    _, dw0 = rk.rms_norm_bwd(y[live], x[live], w)
+    assert same_bits(dw, dw0)
+    assert rk.get_device_error() == 0

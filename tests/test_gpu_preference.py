@@ -252,3 +252,17 @@ def test_streams_and_graphs(rk):
     again = rk.preference_loss(*args, **named)
     assert all(same_bits(got[k], again[k]) for k in want)
     assert rk.get_device_error() == 0
+
+
+def test_sums_and_margins_past_fixed_point(rk):
+    """Ratios, margins and 1 / (2 beta) on both sides of where 64-bit floating point takes over."""
+    n = 600
+    logp = torch.cat([torch.full((n,), -400.0), torch.full((n,), -440.0), torch.full((n,), -0.25), torch.full((n,), -900.0)])
+    cu = torch.arange(5, dtype=torch.int32) * n
+    chosen, rejected = torch.tensor([0, 1, 2, 3, 0, 2, 1], dtype=torch.int32), torch.tensor([1, 0, 3, 1, 2, 0, 2], dtype=torch.int32)
+    for margin in (None, torch.tensor([2.0 ** 18, -(2.0 ** 18), 1.0, 3e5, 1e9, -1e5, 24000.0])):
+        c = pp.Case(logp, None, torch.zeros(4 * n, dtype=torch.int64), cu, chosen, rejected, margin)
+        for kind, beta in (("sigmoid", 2.0 ** -14), ("hinge", 2.0 ** -10), ("ipo", 0.5), ("ipo", 2.0 ** -20), ("ipo", 2.0 ** -18)):
+            want, bound = pp.plain(c, kind=kind, beta=beta)
+            check(run(rk, c, kind=kind, beta=beta), want, bound)
+    assert rk.get_device_error() == 0
