@@ -352,15 +352,7 @@ __device__ __forceinline__ void weight_vector(const void *w, int type, int k, in
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = y[0][e];
     } else {
-        const int c = Columns<TEAM>::at(lane, k);
-        if (c >= H) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        } else if (type == RK_FP32) {
-            get8(static_cast<const float *>(w) + c, x);
-        } else {
-            get8(static_cast<const uint16_t *>(w) + c, x);
-        }
+        unpack(raw_vector<TEAM>(static_cast<const char *>(w), type == RK_FP32, true, k, H, lane), type == RK_FP32, x);
     }
 }
 
@@ -517,11 +509,6 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
 
         // y, 0 in a row that is not active
         const auto result = [&](int k, float (&y)[8]) {
-            if (!live[i]) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = 0.f;
-                return;
-            }
             float w[8];
             weight_vector<TEAM, READ>(a.weight, a.weight_type, k, H, lane, w);
             part[i].get(k, y);
@@ -530,6 +517,9 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
                 mul2(y[e], y[e + 1], rstd, rstd);
                 mul2(y[e], y[e + 1], w[e], w[e + 1]);
             }
+            // (not a branch: the weight's loads would wait for one another)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = live[i] ? y[e] : 0.f;
         };
         const bool e4m3 = a.out.type == RK_E4M3;
         float *scales = a.scales + t * (a.group ? (H + 127) / 128 : 1);
