@@ -669,12 +669,14 @@ rk_status rk_rms_norm_bwd(const void *dout, rk_dtype dout_type, int64_t ld_dout,
  *       RK_PREFERENCE_HINGE    f = max(0, 1 - beta d); f' = -beta where beta d < 1, else 0
  *       RK_PREFERENCE_IPO      f = (d - 1 / (2 beta))^2
  *     grad_logp[t] = d (sum of all losses) / d logp[t], the g for rk_linear_logp_bwd
- * A sequence may be in any number of pairs (their terms are added in ascending order) or in
- * none.  Inactive rows and rows outside all sequences get grad_logp = 0; what logp and
+ * A sequence may be in any number of pairs (their terms are added in ascending order; the pairs
+ * between the first and the last that name it are looked through, so they are best kept together)
+ * or in none.  Inactive rows and rows outside all sequences get grad_logp = 0; what logp and
  * logp_ref hold there (NaN, infinities) reaches nothing.  A sequence without active rows
  * has s = 0.
- * The sums over tokens are exact sums of logprobs rounded to multiples of 2^-42, in integers:
- * s has the same bits for the same active tokens in whatever order, padding and layout.  A
+ * The sums over tokens are exact sums of logprobs rounded to multiples of 2^-42, in integers (a
+ * mean is rounded to such a multiple too): s has the same bits for the same active tokens in
+ * whatever order, padding and layout.  A
  * logprob of magnitude 2^20 and more counts as infinite; s is then infinite or NaN, and so are
  * the losses that it is in.
  *   logp, logp_ref, grad_logp  fp32 [T];  targets int64 [T], negative: inactive

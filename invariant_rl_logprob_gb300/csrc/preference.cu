@@ -103,12 +103,13 @@ struct Run {
 #pragma unroll
         for (int j = 0; j < kRun; ++j) live |= (tg[j] >= 0 ? 1u : 0u) << j;
     }
-    // cu[0 .. Q] ascends; whatever it holds, q stays in range.
-    __device__ __forceinline__ void find(const int32_t *cu, int Q) {
-        int lo = 0, hi = Q;  // cu[lo - 1] <= t < cu[hi]
+    // The last sequence that begins at or before token u; cu[0 .. Q] ascends, and whatever it holds
+    // q stays in range.
+    __device__ __forceinline__ void find(const int32_t *cu, int Q, int64_t u) {
+        int lo = 0, hi = Q;  // cu[lo - 1] <= u < cu[hi]
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if (cu[mid] <= t)
+            if (cu[mid] <= u)
                 lo = mid + 1;
             else
                 hi = mid;
@@ -116,11 +117,13 @@ struct Run {
         q = lo - 1;
         end = cu[q + 1];
     }
-    // On to the sequence of token u, one at which a sequence begins.
+    // On to the sequence of token u, at or behind `end`.
     __device__ __forceinline__ void advance(const int32_t *cu, int Q, int64_t T, int64_t u) {
-        while (q < Q && u >= end) {
-            ++q;
-            end = q < Q ? cu[q + 1] : T;
+        if (++q < Q) end = cu[q + 1];
+        if (q < Q && u >= end) find(cu, Q, u);  // over empty ones, however many
+        if (q >= Q || u >= end) {
+            q = Q;
+            end = T;
         }
     }
 };
@@ -366,8 +369,8 @@ __device__ __forceinline__ void write_runs(const Args &a, const int32_t *cu, Run
     if (threadIdx.x == 0 && !mine) tile.last = -1;
     if (end) {
         Run last = run;
-        last.advance(cu, a.Q, a.T, min(a.T, run.t + kRun) - 1);
-        tile.last = min(last.q, a.Q - 1);
+        last.find(cu, a.Q, min(a.T, run.t + kRun) - 1);
+        tile.last = last.q;
     }
     __syncthreads();
     const int first = tile.first, count = tile.last - first + 1;
@@ -440,7 +443,7 @@ __global__ void __launch_bounds__(kThreads) preference_cluster(const __grid_cons
     if (i < a.P) pair.load(a, i);
     if (i < a.Q) clear(a, i);
     const int32_t *cu = offsets_near<kThreads>(a, offsets);
-    if (mine) run.find(cu, a.Q);
+    if (mine) run.find(cu, a.Q, run.t);
     cluster_sync();
     if (mine) add_run(a, cu, run, lp, rf);
     if (i < a.P) name(a, pair, i);
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(kStepThreads) preference_step(const __grid_con
             float lp[kRun], rf[kRun];
             run.load_targets(a, r);
             load_logprobs(a, run.t, lp, rf);
-            run.find(cu, a.Q);
+            run.find(cu, a.Q, run.t);
             add_run(a, cu, run, lp, rf);
         }
         for (int64_t p = i; p < a.P; p += n) {
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kStepThreads) preference_step(const __grid_con
             Run run{};
             if (r < runs) {
                 run.load_targets(a, r);
-                run.find(cu, a.Q);
+                run.find(cu, a.Q, run.t);
             }
             write_runs<kStepThreads>(a, cu, run, r < runs, tile);
             __syncthreads();

@@ -33,6 +33,7 @@ def check(got, want, bound):
 
 LENGTHS = {
     "one": [1], "pair": [3, 5], "short": [0, 1, 2, 0, 0, 7, 8, 9, 0], "runs": [8, 16, 24, 8], "long": [5000, 1, 3001],
+    "empty": [3] + [0] * 700 + [2] + [0] * 600 + [9, 0, 30],
     "many": [(7 * i) % 13 for i in range(900)], "mixed": [1000, 40, 0, 2047, 256, 255, 257, 31, 33, 1024],
 }
 
@@ -52,8 +53,8 @@ def test_against_64_bits(rk, name, ref, margin, average, kind, smoothing):
 
 def test_many_pairs_and_sequences(rk):
     """More sequences than are searched in shared memory, and one that nearly every pair names."""
-    for Q, P in ((9000, 4000), (300, 5000)):
-        c = pp.make_case([(5 * i) % 7 for i in range(Q)], P, seed=Q)
+    for Q, P in ((9000, 4000), (300, 5000), (20000, 300)):
+        c = pp.make_case([(5 * i) % 7 if Q < 20000 else (i % 997 == 5) * 11 for i in range(Q)], P, seed=Q)
         c.chosen[::2] = 17
         c.rejected[5] = 17
         c.chosen[5] = 17
