@@ -29,6 +29,7 @@ size, row position, neighbour content, padding and varlen packing.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 
@@ -1143,8 +1144,9 @@ def rms_norm_bwd(grad_out: torch.Tensor, r: torch.Tensor, weight: torch.Tensor,
     (``[T, H]`` in ``out_dtype``, default: r's) is the gradient of x and of residual
     alike.  dweight, fp32 ``[H]``, is summed over the active rows in canonical order
     (``row_order``; ascending rows by default), with ``accumulate`` onto what it holds; it
-    is None without ``need_dweight`` (a weight that is not trained).  Rows that are not among them get dx = 0.  ``out`` may be ``grad_out``, ``r`` or
-    ``grad_residual`` itself unless ``row_order`` is given."""
+    is None without ``need_dweight`` (a weight that is not trained).  Rows that are not among
+    them get dx = 0.  ``out`` may be ``grad_out``, ``r`` or ``grad_residual`` itself unless
+    ``row_order`` is given."""
     lib = _lib or load_library()
     code, ld = _matrix(grad_out, "grad_out")
     T, H = grad_out.shape
@@ -1264,7 +1266,8 @@ class AdamW:
     entries may be None.  The states are made here, as zeros of ``bits`` 32 or 8, or given:
     ``m`` and ``v`` in fp32, or in float8_e4m3fn with ``m_scale`` and ``v_scale`` (fp32, one
     for each 256 elements): ``m = code * scale``, ``v = (code * scale)^2``.
-    ``weight_decay`` and ``lr_scale`` are numbers, or lists with one for each tensor.
+    ``weight_decay`` and ``lr_scale`` are numbers, or lists with one for each tensor.  Nothing
+    that a step writes may overlap anything else of it: a shared parameter is listed once.
 
     All are kept by the object and changed in place by :func:`adamw_step`; a replayed CUDA
     graph of the step needs the object alive."""
@@ -1317,6 +1320,12 @@ class AdamW:
                     raise ValueError("an fp32 parameter has no master")
                 s.master = self.master[i].data_ptr()
         self.address, self.count = ctypes.addressof(self._array), count
+        # [begin, end) of all memory that a step writes, ascending
+        written = [t for each_of in (params, self.m, self.v, self.m_scale, self.v_scale, self.master)
+                   for t in each_of or () if t is not None and t.numel()]
+        self._written = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in written)
+        if any(a[1] > b[0] for a, b in zip(self._written, self._written[1:])):
+            raise ValueError("parameters, masters and states must not overlap (a shared parameter is listed once)")
         self.use_grads(grads)
 
     def use_grads(self, grads) -> None:
@@ -1324,6 +1333,9 @@ class AdamW:
         grads = self._each(grads, "grads", self.count)
         for p, g in zip(self.params, grads):
             self._check(g, "a gradient", (torch.bfloat16, torch.float32), p.numel())
+            at = bisect.bisect_left(self._written, (g.data_ptr() + g.numel() * g.element_size(),))
+            if g.numel() and at and self._written[at - 1][1] > g.data_ptr():
+                raise ValueError("a gradient must not overlap a parameter, a master or a state")
         for s, g in zip(self._array, grads):
             s.grad, s.grad_type = g.data_ptr(), _TYPE_CODES[g.dtype]
         self.grads = grads

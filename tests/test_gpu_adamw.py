@@ -103,6 +103,38 @@ def test_against_64_bits(rk, param, grad, master, bits):
     assert rk.get_device_error() == 0
 
 
+@pytest.mark.parametrize("grad", [FP32, BF16])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_have_the_bits_of_elementary_operations(rk, bits, grad):
+    """Products, sums, roots and quotients in fp32, each rounded by itself; only zeros may differ in sign."""
+    opt = make(rk, [70001], BF16, grad, bits)
+    before = snapshot(opt)
+    scale = torch.tensor([0.37], device=DEV)
+    rk.adamw_step(opt, grad_scale=scale, **HYPER)
+    after = snapshot(opt)
+    g = before["grads"][0].float() * scale.cpu()
+    m, v = before["m"][0], before["v"][0]
+    if bits == 8:
+        m = m.float() * before["m_scale"][0].repeat_interleave(256)[:70001]
+        v = (v.float() * before["v_scale"][0].repeat_interleave(256)[:70001]).square()
+    b1, b2 = HYPER["beta1"], HYPER["beta2"]
+    f = lambda x: torch.tensor(x, dtype=torch.float32)  # noqa: E731
+    m = m * f(b1) + g * f(1 - b1)
+    v = v * f(b2) + g * g * f(1 - b2)
+    if bits == 32:
+        assert torch.equal(after["m"][0], m) and torch.equal(after["v"][0], v)
+        return
+    for name, x in (("m", m), ("v", v.sqrt())):
+        x = torch.nn.functional.pad(x, (0, -70001 % 256)).view(-1, 256)
+        s = x.abs().amax(1, keepdim=True) * (f(1.0) / f(448.0))
+        q = torch.where(s > 0, x / s, 0.0)
+        if name == "v":
+            q = torch.where(x > 0, q.clamp(min=2.0 ** -9), q)
+        code = q.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(-1)[:70001]
+        assert torch.equal(after[name + "_scale"][0], s[:, 0])
+        assert torch.equal(after[name][0].float(), code.float())
+
+
 @pytest.mark.parametrize("offset", [1, 2, 3])
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("param", [BF16, FP32])
@@ -276,3 +308,18 @@ def test_a_tensor_past_32_bits(rk):
         for k in ("m", "v"):
             a, b = getattr(big, k)[0][e][:keep], getattr(small, k)[i][:keep]
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_overlaps_are_refused(rk):
+    p, g = torch.zeros(600, device=DEV), torch.zeros(600, device=DEV)
+    rk.AdamW([p[:300], p[300:]], [g[:300], g[:300]])  # side by side; gradients may be shared
+    for params, grads in (([p, p], [g, g]), ([p[:300], p[299:]], [g[:300], g[299:]]), ([p], [p]),
+                          ([p[:300]], [p[299:599]]), ([p[300:]], [p[1:301]])):
+        with pytest.raises(ValueError, match="overlap"):
+            rk.AdamW(params, grads)
+    with pytest.raises(ValueError, match="overlap"):
+        rk.AdamW([p], [g], [g.clone()], [p])
+    opt = rk.AdamW([p], [g])
+    with pytest.raises(ValueError, match="overlap"):
+        opt.use_grads([opt.m[0]])
+    assert opt.grads[0] is g
