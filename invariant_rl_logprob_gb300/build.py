@@ -18,9 +18,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librk.so")
 SOURCES = ["rk_api.cu", "logits_logp.cu", "linear_logp_tc.cu", "rk_noalloc.cu", "token_loss.cu",
-           "dw_prep.cu", "saved_bwd.cu", "logits_rules.cu", "embedding.cu", "rms_norm.cu",
+           "dw_prep.cu", "saved_bwd.cu", "logits_rules.cu", "embedding.cu", "rms_norm.cu", "rms_norm_bwd.cu",
            "preference.cu", "adamw.cu"]
-HEADERS = ["rk_device.cuh", "elements.cuh", "rk_internal.h", "token_loss.cuh"]
+HEADERS = ["rk_device.cuh", "elements.cuh", "rms_norm.cuh", "rk_internal.h", "token_loss.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,6 +1,6 @@
 // elements.cuh -- elements of bf16 and fp32 matrices as floats, eight at a time
 // or one by one, and launches that overlap the end of the kernel before them;
-// shared by the memory-bound kernels (embedding.cu, rms_norm.cu, adamw.cu,
+// shared by the memory-bound kernels (embedding.cu, rms_norm.cuh, adamw.cu,
 // preference.cu).
 #pragma once
 
@@ -75,6 +75,7 @@ __device__ __forceinline__ void mul2(float &x0, float &x1, float y0, float y1) {
         : "+f"(x0), "+f"(x1)
         : "f"(y0), "f"(y1));
 }
+// A product of mul2 that goes into add2 is compiled into one fma2, with one rounding.
 __device__ __forceinline__ void add2(float &x0, float &x1, float y0, float y1) {
     asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
         "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"

@@ -254,6 +254,36 @@ def test_long_candidate_lists(rk):
     check_bwd(dx, dw, r, d, None, w, live)
 
 
+@pytest.mark.parametrize("H", [40, 264, 1000, 2047, 2048, 4096, 5000])
+@pytest.mark.parametrize("n", [0, 1, 300, 1023, 1024, 1025])
+def test_short_and_long_candidate_lists(rk, n, H):
+    """Inactive candidates in between change neither bits nor which rows are 0, however the list is
+    made of them; more rows than candidates and fewer."""
+    g = gen(n + H)
+    T = 1024
+    r, d = npl.matrix(g, T, H, BF16).to(DEV), npl.matrix(g, T, H, FP32).to(DEV)
+    w = weight_of(g, H, BF16).to(DEV)
+    targets = torch.ones(T, dtype=torch.int64)
+    targets[::5] = -1
+    alive, dead = torch.arange(T)[targets >= 0], torch.arange(T)[targets < 0]
+    order = torch.cat([alive, dead, alive, dead])[torch.randperm(2 * T, generator=g)[:n]]
+    gaps = torch.randint(0, 4, (n,), generator=g) + (2048 if n == 1 else 0)
+    mixed = torch.cat([torch.cat([o[None], dead[torch.randint(0, len(dead), (int(k),), generator=g)]])
+                       for o, k in zip(order, gaps)] + [dead, dead[:7]]) if n else dead.repeat(10)
+    call = lambda o, t: rk.rms_norm_bwd(d[:t], r[:t], w, targets[:t].to(DEV), eps=npl.EPS, row_order=o.to(DEV))  # noqa: E731
+    dx, dw = call(order, T)
+    mx, mw = call(mixed, T)
+    assert same_bits(dx, mx) and same_bits(dw, mw)
+    named = torch.zeros(T, dtype=torch.bool)
+    named[order] = True
+    assert not dx[~(named & (targets >= 0)).to(DEV)].any()
+    # the same rows of a matrix that is too long for the short list
+    long = lambda x: torch.cat([x, torch.full_like(x, float("nan"))])  # noqa: E731
+    lx, lw = rk.rms_norm_bwd(long(d), long(r), w, torch.cat([targets, -targets.abs()]).to(DEV), eps=npl.EPS,
+                             row_order=order.to(DEV))
+    assert same_bits(lx[:T], dx) and same_bits(lw, dw) and not lx[T:].any()
+
+
 def test_fused_addition_has_the_bits_of_two_calls(rk):
     g = gen(2)
     for H in (100, 1000, 4096):
