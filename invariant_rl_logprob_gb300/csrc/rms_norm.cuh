@@ -12,7 +12,7 @@
 // leave in aligned 16 bytes as well.
 //
 // Which thread owns which column, and with it the order of every sum, depends on H
-// alone.  A sum of squares that leaves fp32 is formed again from r * 2^-80.
+// and, in the gradient, on the types.  A sum of squares that leaves fp32 is formed again from r * 2^-80.
 #pragma once
 
 #include "elements.cuh"
@@ -321,22 +321,6 @@ inline bool plain(const Matrix &m, int64_t H) {
     return !m.p || (aligned(m.p, vector) && m.step % vector == 0 && H % 8 == 0);
 }
 inline bool plain(const Matrix &m, int type, int64_t H) { return !m.p || (m.type == type && plain(m, H)); }
-
-// Widest row, team, vectors of 8 a thread, the forward's rows a team and block and its blocks per
-// SM, the backward's block and blocks per SM.  Narrow rows: teams of 8 lanes for 2M rows of 64
-// columns take 173 us (residual, e4m3) where warps took 496, of 16 lanes for 1M of 128 167 and 252.
-// The backward's blocks per SM are what leaves its sums in registers: at 4096 columns 3, 4 and 5
-// blocks of 128 threads took 103, 96 and 104 us for 16384 rows, before rows were asked for ahead.
-#define RK_NORM_SHAPES(SHAPE)                \
-    SHAPE(64, 8, 1, 4, 128, 8, 256, 3)       \
-    SHAPE(128, 16, 1, 4, 128, 8, 256, 3)     \
-    SHAPE(256, 32, 1, 4, 128, 8, 256, 3)     \
-    SHAPE(512, 32, 2, 2, 128, 8, 256, 2)     \
-    SHAPE(1024, 32, 4, 1, 128, 6, 128, 4)    \
-    SHAPE(2048, 64, 4, 1, 64, 12, 64, 8)     \
-    SHAPE(4096, 128, 4, 1, 128, 7, 128, 4)   \
-    SHAPE(8192, 256, 4, 1, 256, 3, 256, 2)   \
-    SHAPE(16384, 512, 4, 1, 512, 2, 512, 1)
 
 constexpr size_t kMostShared = 200 * 1024;  // beside the static part; a stage of the widest row is a third of it
 

@@ -114,9 +114,10 @@ struct NormBwdArgs {
 __host__ __device__ constexpr int64_t pitch_of(int64_t H) { return (H + 7) / 8 * 8; }
 
 // What the backward keeps of a row between its sums and its results: with kWords (r, dout and dr in
-// bf16) and kMixed (the same with dout in fp32) its words; otherwise nothing, it is read again,
-// from the caches.  65536 x 4096: kWords 316 us, kMixed 398 (both the copy rate); without kMixed its
-// case took 610.  All in fp32, kAligned 884 us, 72 % of the copy rate.
+// bf16) and kMixed (the same with dout in fp32) its words, with kAligned up to 16 columns a thread;
+// otherwise nothing, it is read again, from the caches.  65536 x 4096: kWords 316 us, kMixed 398 (both
+// the copy rate); without kMixed its case took 610.  32768 x 4096 all in fp32: 323, 98 % of the copy
+// rate, where 32 columns a thread, read again, took 420.
 constexpr int kMixed = 3;
 
 // LIST: every block lists the canonical rows for itself.  (A variant of its own: as a branch it cost
@@ -194,6 +195,16 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
                 zw[k] = a.dr.p ? C::words(z(), k, H, lane) : make_uint4(0, 0, 0, 0);
             }
         }
+        constexpr bool kKeep = READ == kAligned && NV <= 2;
+        Raw kr[kKeep ? NV : 1], kd[kKeep ? NV : 1], kz[kKeep ? NV : 1];
+        if constexpr (kKeep) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                kr[k] = raw_vector<TEAM>(r(), a.r.type == RK_FP32, true, k, H, lane);
+                kd[k] = raw_vector<TEAM>(d(), a.dout.type == RK_FP32, true, k, H, lane);
+                kz[k] = raw_vector<TEAM>(z(), a.dr.type == RK_FP32, a.dr.p, k, H, lane);
+            }
+        }
         constexpr int kPair = NV > 1 ? 2 : 1;
         // vectors k .. k + kPair - 1 of r, dout and the weight
         const auto values = [&](int k, float (&x)[kPair][8], float (&g)[kPair][8], float (&w)[kPair][8]) {
@@ -206,8 +217,8 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
                 Raw p[kPair], q[kPair];
 #pragma unroll
                 for (int i = 0; i < kPair; ++i) {
-                    p[i] = raw_vector<TEAM>(r(), r_wide, true, k + i, H, lane);
-                    q[i] = raw_vector<TEAM>(d(), d_wide, true, k + i, H, lane);
+                    p[i] = kKeep ? kr[kKeep ? k + i : 0] : raw_vector<TEAM>(r(), r_wide, true, k + i, H, lane);
+                    q[i] = kKeep ? kd[kKeep ? k + i : 0] : raw_vector<TEAM>(d(), d_wide, true, k + i, H, lane);
                 }
 #pragma unroll
                 for (int i = 0; i < kPair; ++i) {
@@ -281,7 +292,8 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
             Raw zr[kPair];
             if constexpr (READ == kAligned) {
 #pragma unroll
-                for (int i = 0; i < kPair; ++i) zr[i] = raw_vector<TEAM>(z(), z_wide, a.dr.p, k + i, H, lane);
+                for (int i = 0; i < kPair; ++i)
+                    zr[i] = kKeep ? kz[kKeep ? k + i : 0] : raw_vector<TEAM>(z(), z_wide, a.dr.p, k + i, H, lane);
             }
             values(k, x, g, w);
             if constexpr (READ == kAligned) {
@@ -475,28 +487,53 @@ cudaError_t backward_launch(NormBwdArgs &a, const DeviceInfo &di, cudaStream_t s
     return launch_dependent_smem(kernel, (int64_t)kSmCount * PER_SM, BLOCK, shared, st, a);
 }
 template <int TEAM, int NV, int BLOCK, int PER_SM, bool LIST>
-cudaError_t backward_launch(int read, NormBwdArgs &a, const DeviceInfo &di, cudaStream_t st) {
+cudaError_t whole_launch(int read, NormBwdArgs &a, const DeviceInfo &di, cudaStream_t st) {
     switch (read) {
         case kWords: return backward_launch<TEAM, NV, kWords, BLOCK, PER_SM, LIST>(a, di, st);
         case kMixed: return backward_launch<TEAM, NV, kMixed, BLOCK, PER_SM, LIST>(a, di, st);
-        case kAligned: return backward_launch<TEAM, NV, kAligned, BLOCK, PER_SM, LIST>(a, di, st);
+        case kAligned:
+            // (the one width whose rows are halved whenever they are read so)
+            if constexpr (TEAM != 32 || NV != 4) return backward_launch<TEAM, NV, kAligned, BLOCK, PER_SM, LIST>(a, di, st);
+            return cudaErrorInvalidValue;
         default: return backward_launch<TEAM, NV, kFloats, BLOCK, PER_SM, LIST>(a, di, st);
     }
 }
-
-int backward_blocks(int64_t H) {
-#define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER) \
-    if (H <= MAX) return kSmCount * BPER;
-    RK_NORM_SHAPES(SHAPE)
-#undef SHAPE
-    return 0;
+template <int TEAM, int NV, int BLOCK, int PER_SM, bool LIST>
+cudaError_t halved_launch(int read, NormBwdArgs &a, const DeviceInfo &di, cudaStream_t st) {
+    return read == kAligned ? backward_launch<TEAM, NV, kAligned, BLOCK, PER_SM, LIST>(a, di, st)
+                            : backward_launch<TEAM, NV, kFloats, BLOCK, PER_SM, LIST>(a, di, st);
 }
-int rows_of_block(int64_t H) {
-#define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER) \
-    if (H <= MAX) return BBLOCK / TEAM;
-    RK_NORM_SHAPES(SHAPE)
+
+// Whether a row is kept by twice the threads, half the columns each, where r or dr is fp32.  All in
+// fp32, 2^27 elements, halved against not: 1024 columns 315 against 422 us, 2048 316 and 415, 4096 323
+// and 420, 8192 338 and 408; 5120 (where 192 of 512 threads would have none) 404 and 347.  Without dr, a
+// third less to wait for: 1024 columns 215 and 272, but 2040 256 and 227, 4096 271 and 221.
+bool halved(int64_t H, bool wide, bool dr) { return wide && (H <= 1024 || (dr && (H <= 4096 || H > 6144))); }
+
+// Widest row, and for rows as they are and halved ones team, vectors of 8 a thread, block and blocks per
+// SM.  The blocks per SM are what leaves a team's sums in registers: at 4096 columns of bf16 3, 4 and 5
+// blocks of 128 threads took 103, 96 and 104 us for 16384 rows, before rows were asked for ahead.
+#define RK_NORM_BWD_SHAPES(SHAPE)                  \
+    SHAPE(64, 8, 1, 256, 3, 8, 1, 256, 3)          \
+    SHAPE(128, 16, 1, 256, 3, 16, 1, 256, 3)       \
+    SHAPE(256, 32, 1, 256, 3, 32, 1, 256, 3)       \
+    SHAPE(512, 32, 2, 256, 2, 32, 2, 256, 2)       \
+    SHAPE(1024, 32, 4, 128, 4, 64, 2, 64, 8)       \
+    SHAPE(2048, 64, 4, 64, 8, 128, 2, 128, 4)      \
+    SHAPE(4096, 128, 4, 128, 4, 256, 2, 256, 2)    \
+    SHAPE(8192, 256, 4, 256, 2, 512, 2, 512, 1)    \
+    SHAPE(16384, 512, 4, 512, 1, 512, 4, 512, 1)
+
+// Blocks of the backward, and rows that a block takes at once.
+struct Split {
+    int blocks, rows;
+};
+Split split_of(int64_t H, bool half) {
+#define SHAPE(MAX, TEAM, NV, BLOCK, PER, HTEAM, HNV, HBLOCK, HPER) \
+    if (H <= MAX) return half ? Split{kSmCount * HPER, HBLOCK / HTEAM} : Split{kSmCount * PER, BLOCK / TEAM};
+    RK_NORM_BWD_SHAPES(SHAPE)
 #undef SHAPE
-    return 1;
+    return Split{0, 1};
 }
 
 struct BwdBuffers {
@@ -515,7 +552,8 @@ BwdBuffers carve(void *base, int64_t T, int64_t n, int64_t H) {
         b.bytes += round256(bytes);
         return static_cast<void *>(q);
     };
-    b.partial = static_cast<float *>(take((size_t)backward_blocks(H) * (size_t)pitch_of(H) * 4));
+    const int blocks = std::max(split_of(H, false).blocks, split_of(H, true).blocks);  // whatever the types
+    b.partial = static_cast<float *>(take((size_t)blocks * (size_t)pitch_of(H) * 4));
     b.rows = static_cast<int32_t *>(take((size_t)n * 4));
     b.counts = static_cast<int32_t *>(take((size_t)(n / kListTile + 1) * 4));
     b.n_rows = static_cast<int64_t *>(take(8));
@@ -557,21 +595,25 @@ cudaError_t launch_rms_norm_bwd(const RulesMatrix &dout, const RulesMatrix &r, c
         a.listed = b.listed;
     }
     const bool on16 = plain(a.r, H) && plain(a.dout, H) && plain(a.dr, H) && aligned(weight, 16);
-    const bool words = a.r.type == RK_BF16 && (!dr || a.dr.type == RK_BF16);
-    const int read = !on16 ? kFloats : !words ? kAligned : a.dout.type == RK_BF16 ? kWords : kMixed;
+    const bool wide = a.r.type == RK_FP32 || (dr && a.dr.type == RK_FP32);
+    const bool half = halved(H, wide, dr != nullptr);
+    const int read = !on16 ? kFloats : wide ? kAligned : a.dout.type == RK_BF16 ? kWords : kMixed;
     const auto run = [&] {
-#define SHAPE(MAX, TEAM, NV, ROWS, FBLOCK, FPER, BBLOCK, BPER)                                \
-    if (H <= MAX)                                                                             \
-        return list ? backward_launch<TEAM, NV, BBLOCK, BPER, true>(read, a, di, st)          \
-                    : backward_launch<TEAM, NV, BBLOCK, BPER, false>(read, a, di, st);
-        RK_NORM_SHAPES(SHAPE)
+#define SHAPE(MAX, TEAM, NV, BLOCK, PER, HTEAM, HNV, HBLOCK, HPER)                          \
+    if (H <= MAX)                                                                           \
+        return half   ? list ? halved_launch<HTEAM, HNV, HBLOCK, HPER, true>(read, a, di, st)  \
+                             : halved_launch<HTEAM, HNV, HBLOCK, HPER, false>(read, a, di, st) \
+               : list ? whole_launch<TEAM, NV, BLOCK, PER, true>(read, a, di, st)           \
+                      : whole_launch<TEAM, NV, BLOCK, PER, false>(read, a, di, st);
+        RK_NORM_BWD_SHAPES(SHAPE)
 #undef SHAPE
         return cudaErrorInvalidValue;
     };
     const cudaError_t e = run();
     if (e != cudaSuccess || !dweight) return e;
+    const Split split = split_of(H, half);
     return launch_dependent(rms_norm_join, (H + 31) / 32, 32 * kJoinLanes, st, (const float *)a.partial,
-                            backward_blocks(H), rows_of_block(H), (const int64_t *)a.n_rows, cu, num_seqs, T, (int)H, dweight,
+                            split.blocks, split.rows, (const int64_t *)a.n_rows, cu, num_seqs, T, (int)H, dweight,
                             (int)accumulate);
 }
 
