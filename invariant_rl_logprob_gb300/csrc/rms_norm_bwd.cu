@@ -161,49 +161,83 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
     // fewer than 2^31 rows
     const int last = (int)n, step = (int)teams, first = (int)lo;
     const auto row_at = [&](int64_t i) { return i >= last ? 0 : rows ? rows[i] : first + (int)i; };
+    // what is kept of a row between its sums and its results
+    constexpr bool kKeep = READ == kAligned && NV <= 2;
+    struct Held {
+        uint4 r[NV], d[NV * (READ == kMixed ? 2 : 1)], z[NV];
+        Raw raw_r[kKeep ? NV : 1], raw_d[kKeep ? NV : 1], raw_z[kKeep ? NV : 1];
+    };
+    const auto hold = [&](int t, Held &h) {
+        const char *r = a.r.row(t), *d = a.dout.row(t), *z = a.dr.row(t);
+        if constexpr (READ == kWords || READ == kMixed) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = C::at(lane, k);
+                h.r[k] = C::words(r, k, H, lane);
+                if constexpr (READ == kWords) {
+                    h.d[k] = C::words(d, k, H, lane);
+                } else {
+                    const uint4 *from = reinterpret_cast<const uint4 *>(d + 4 * c);
+                    h.d[2 * k] = c < H ? from[0] : make_uint4(0, 0, 0, 0);
+                    h.d[2 * k + 1] = c < H ? from[1] : make_uint4(0, 0, 0, 0);
+                }
+                h.z[k] = a.dr.p ? C::words(z, k, H, lane) : make_uint4(0, 0, 0, 0);
+            }
+        } else if constexpr (kKeep) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                h.raw_r[k] = raw_vector<TEAM>(r, a.r.type == RK_FP32, true, k, H, lane);
+                h.raw_d[k] = raw_vector<TEAM>(d, a.dout.type == RK_FP32, true, k, H, lane);
+                h.raw_z[k] = raw_vector<TEAM>(z, a.dr.type == RK_FP32, a.dr.p, k, H, lane);
+            }
+        }
+    };
+    // A narrow row is asked for a row ahead in registers, not in the second cache: 2^27 elements of bf16 with
+    // dr, 64 columns 227 us against 277, with the weight kept as well 184 (128 columns: 184 for 210, 256: 182 for
+    // 190).
+    constexpr bool kAhead = NV == 1 && (READ == kWords || READ == kMixed);
+    Held h, ahead;
+    // the weight, kept as well where there is room (512 columns 162 us for 187)
+    constexpr bool kWeight = NV <= 2 && READ != kFloats;
+    float kept[kWeight ? NV : 1][8];
+    if constexpr (kWeight) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) weight_vector<TEAM, READ>(a.weight, a.weight_type, k, H, lane, kept[k]);
+    }
+    const auto weight = [&](int k, float (&w)[8]) {
+        if constexpr (kWeight) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = kept[k][e];
+        } else {
+            weight_vector<TEAM, READ>(a.weight, a.weight_type, k, H, lane, w);
+        }
+    };
     int next = row_at(team);
+    if constexpr (kAhead) {
+        if (team < last) hold(next, ahead);
+    }
     for (int64_t i = team; i < last; i += step) {
         const int t = next;
         next = row_at(i + step);
         const auto r = [&] { return a.r.row(t); };
         const auto d = [&] { return a.dout.row(t); };
         const auto z = [&] { return a.dr.row(t); };
-        if (lane < 3 && i + step < last) {
-            // the team's next row, on its way into the second cache
-            const Matrix &m = lane == 0 ? a.r : lane == 1 ? a.dout : a.dr;
-            if (m.p) {
-                const uintptr_t from = reinterpret_cast<uintptr_t>(m.row(next)), to = from + H * size_of(m.type);
-                const uintptr_t first16 = from & ~uintptr_t(15);
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(first16),
-                             "r"((uint32_t)((to + 15 & ~uintptr_t(15)) - first16))
-                             : "memory");
-            }
-        }
-        uint4 rw[NV], dw[NV * (READ == kMixed ? 2 : 1)], zw[NV];
-        if constexpr (READ == kWords || READ == kMixed) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = C::at(lane, k);
-                rw[k] = C::words(r(), k, H, lane);
-                if constexpr (READ == kWords) {
-                    dw[k] = C::words(d(), k, H, lane);
-                } else {
-                    const uint4 *from = reinterpret_cast<const uint4 *>(d() + 4 * c);
-                    dw[2 * k] = c < H ? from[0] : make_uint4(0, 0, 0, 0);
-                    dw[2 * k + 1] = c < H ? from[1] : make_uint4(0, 0, 0, 0);
+        if constexpr (kAhead) {
+            h = ahead;
+            if (i + step < last) hold(next, ahead);
+        } else {
+            if (lane < 3 && i + step < last) {
+                // the team's next row, on its way into the second cache
+                const Matrix &m = lane == 0 ? a.r : lane == 1 ? a.dout : a.dr;
+                if (m.p) {
+                    const uintptr_t from = reinterpret_cast<uintptr_t>(m.row(next)), to = from + H * size_of(m.type);
+                    const uintptr_t first16 = from & ~uintptr_t(15);
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(first16),
+                                 "r"((uint32_t)((to + 15 & ~uintptr_t(15)) - first16))
+                                 : "memory");
                 }
-                zw[k] = a.dr.p ? C::words(z(), k, H, lane) : make_uint4(0, 0, 0, 0);
             }
-        }
-        constexpr bool kKeep = READ == kAligned && NV <= 2;
-        Raw kr[kKeep ? NV : 1], kd[kKeep ? NV : 1], kz[kKeep ? NV : 1];
-        if constexpr (kKeep) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                kr[k] = raw_vector<TEAM>(r(), a.r.type == RK_FP32, true, k, H, lane);
-                kd[k] = raw_vector<TEAM>(d(), a.dout.type == RK_FP32, true, k, H, lane);
-                kz[k] = raw_vector<TEAM>(z(), a.dr.type == RK_FP32, a.dr.p, k, H, lane);
-            }
+            hold(t, h);
         }
         constexpr int kPair = NV > 1 ? 2 : 1;
         // vectors k .. k + kPair - 1 of r, dout and the weight
@@ -217,24 +251,24 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
                 Raw p[kPair], q[kPair];
 #pragma unroll
                 for (int i = 0; i < kPair; ++i) {
-                    p[i] = kKeep ? kr[kKeep ? k + i : 0] : raw_vector<TEAM>(r(), r_wide, true, k + i, H, lane);
-                    q[i] = kKeep ? kd[kKeep ? k + i : 0] : raw_vector<TEAM>(d(), d_wide, true, k + i, H, lane);
+                    p[i] = kKeep ? h.raw_r[kKeep ? k + i : 0] : raw_vector<TEAM>(r(), r_wide, true, k + i, H, lane);
+                    q[i] = kKeep ? h.raw_d[kKeep ? k + i : 0] : raw_vector<TEAM>(d(), d_wide, true, k + i, H, lane);
                 }
 #pragma unroll
                 for (int i = 0; i < kPair; ++i) {
-                    weight_vector<TEAM, READ>(a.weight, a.weight_type, k + i, H, lane, w[i]);
+                    weight(k + i, w[i]);
                     unpack(p[i], r_wide, x[i]);
                     unpack(q[i], d_wide, g[i]);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < kPair; ++i) {
-                    weight_vector<TEAM, READ>(a.weight, a.weight_type, k + i, H, lane, w[i]);
-                    unpack(rw[k + i], x[i]);
+                    weight(k + i, w[i]);
+                    unpack(h.r[k + i], x[i]);
                     if constexpr (READ == kWords) {
-                        unpack(dw[k + i], g[i]);
+                        unpack(h.d[k + i], g[i]);
                     } else {
-                        const uint4 p = dw[2 * (k + i)], q = dw[2 * (k + i) + 1];
+                        const uint4 p = h.d[2 * (k + i)], q = h.d[2 * (k + i) + 1];
                         const uint32_t v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
                         for (int e = 0; e < 8; ++e) g[i][e] = __uint_as_float(v[e]);
@@ -293,7 +327,7 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
             if constexpr (READ == kAligned) {
 #pragma unroll
                 for (int i = 0; i < kPair; ++i)
-                    zr[i] = kKeep ? kz[kKeep ? k + i : 0] : raw_vector<TEAM>(z(), z_wide, a.dr.p, k + i, H, lane);
+                    zr[i] = kKeep ? h.raw_z[kKeep ? k + i : 0] : raw_vector<TEAM>(z(), z_wide, a.dr.p, k + i, H, lane);
             }
             values(k, x, g, w);
             if constexpr (READ == kAligned) {
@@ -308,7 +342,7 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < kPair; ++i) unpack(zw[k + i], y[i]);
+                for (int i = 0; i < kPair; ++i) unpack(h.z[k + i], y[i]);
             }
 #pragma unroll
             for (int i = 0; i < kPair; ++i) {
@@ -466,8 +500,8 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 constexpr int kSmCount = 152;  // what the backward's partial sums are laid out for, on any device
 // Up to so many candidates every block lists the rows for itself, beyond a launch does.  With targets,
-// 64 / 2048 / 4096 columns: 300 rows 7.7 / 8.9 / 10.1 us against 9.5 / 10.2 / 11.2, 1000 rows 8.1 / 14.4 /
-// 14.5 against 10.1 / 14.7 / 15.6; 2048 rows 9.4 / 20.5 / 18.4 against 11.5 / 17.8 / 19.7.
+// 64 / 2048 / 4096 columns: 300 rows 7.7 / 7.9 / 9.5 us against 9.4 / 9.2 / 11.2, 1000 rows 8.1 / 10.4 /
+// 13.9 against 10.1 / 12.0 / 15.6; 2048 rows in an order, with 2048 columns, 25.2 against 19.5.
 constexpr int kListed = 1024;
 
 template <int TEAM, int NV, int READ, int BLOCK, int PER_SM, bool LIST>
@@ -491,10 +525,7 @@ cudaError_t whole_launch(int read, NormBwdArgs &a, const DeviceInfo &di, cudaStr
     switch (read) {
         case kWords: return backward_launch<TEAM, NV, kWords, BLOCK, PER_SM, LIST>(a, di, st);
         case kMixed: return backward_launch<TEAM, NV, kMixed, BLOCK, PER_SM, LIST>(a, di, st);
-        case kAligned:
-            // (the one width whose rows are halved whenever they are read so)
-            if constexpr (TEAM != 32 || NV != 4) return backward_launch<TEAM, NV, kAligned, BLOCK, PER_SM, LIST>(a, di, st);
-            return cudaErrorInvalidValue;
+        case kAligned: return backward_launch<TEAM, NV, kAligned, BLOCK, PER_SM, LIST>(a, di, st);
         default: return backward_launch<TEAM, NV, kFloats, BLOCK, PER_SM, LIST>(a, di, st);
     }
 }
@@ -504,22 +535,24 @@ cudaError_t halved_launch(int read, NormBwdArgs &a, const DeviceInfo &di, cudaSt
                             : backward_launch<TEAM, NV, kFloats, BLOCK, PER_SM, LIST>(a, di, st);
 }
 
-// Whether a row is kept by twice the threads, half the columns each, where r or dr is fp32.  All in
-// fp32, 2^27 elements, halved against not: 1024 columns 315 against 422 us, 2048 316 and 415, 4096 323
-// and 420, 8192 338 and 408; 5120 (where 192 of 512 threads would have none) 404 and 347.  Without dr, a
-// third less to wait for: 1024 columns 215 and 272, but 2040 256 and 227, 4096 271 and 221.
-bool halved(int64_t H, bool wide, bool dr) { return wide && (H <= 1024 || (dr && (H <= 4096 || H > 6144))); }
+// Whether a row of more than 2048 columns is kept by twice the threads, half the columns each: where r or
+// dr is fp32 and there is a dr.  All in fp32, 2^27 elements, halved against not: 4096 columns 323 and 420
+// us, 8192 338 and 408; 5120 (where 192 of 512 threads would have none) 404 and 347.  Without dr, a third
+// less to wait for: 4096 columns 271 and 221.
+bool halved(int64_t H, bool wide, bool dr) { return wide && dr && (H <= 4096 || H > 6144); }
 
 // Widest row, and for rows as they are and halved ones team, vectors of 8 a thread, block and blocks per
 // SM.  The blocks per SM are what leaves a team's sums in registers: at 4096 columns of bf16 3, 4 and 5
-// blocks of 128 threads took 103, 96 and 104 us for 16384 rows, before rows were asked for ahead.
+// blocks of 128 threads took 103, 96 and 104 us for 16384 rows, before rows were asked for ahead.  Up to
+// 2048 columns a thread has 16: 2^27 elements of bf16 with dr, 1024 columns 164 us where 32 took 188, 2048
+// 162 and 171 (1536, of which 128 threads' last 64 have half, 196 and 184).
 #define RK_NORM_BWD_SHAPES(SHAPE)                  \
     SHAPE(64, 8, 1, 256, 3, 8, 1, 256, 3)          \
     SHAPE(128, 16, 1, 256, 3, 16, 1, 256, 3)       \
     SHAPE(256, 32, 1, 256, 3, 32, 1, 256, 3)       \
     SHAPE(512, 32, 2, 256, 2, 32, 2, 256, 2)       \
-    SHAPE(1024, 32, 4, 128, 4, 64, 2, 64, 8)       \
-    SHAPE(2048, 64, 4, 64, 8, 128, 2, 128, 4)      \
+    SHAPE(1024, 64, 2, 64, 8, 64, 2, 64, 8)        \
+    SHAPE(2048, 128, 2, 128, 4, 128, 2, 128, 4)    \
     SHAPE(4096, 128, 4, 128, 4, 256, 2, 256, 2)    \
     SHAPE(8192, 256, 4, 256, 2, 512, 2, 512, 1)    \
     SHAPE(16384, 512, 4, 512, 1, 512, 4, 512, 1)
