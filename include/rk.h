@@ -611,8 +611,9 @@ rk_status rk_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *
  *                residual NULL: none (and residual_out NULL)
  *   weight       bf16 or fp32 [H];  eps > 0
  *   residual_out [T, H] of residual's type: r
- *   out          [T, H], bf16 or fp32 (y, rounded once), or e4m3: y / s, with one scale s for
- *                a row (group 0) or for each 128 columns of it (group 128)
+ *   out          [T, H], bf16 or fp32 (y, rounded once), or e4m3: the correctly rounded fp32
+ *                quotient y / s rounded to 8 bits, with one scale s for a row (group 0) or for
+ *                each 128 columns of it (group 128)
  *   scales       fp32 [T] or [T, ceil(H / 128)], contiguous (NULL unless out is e4m3):
  *                s = max |y| / 448 of its columns, at least 2^-120; 0 where y is 0
  * out and residual_out may be x or residual itself (same address, type and row stride); any

@@ -103,6 +103,42 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
     return d;
 }
+// x / s, each correctly rounded (Markstein, 1990: a faithful quotient and its remainder times the
+// rounded reciprocal), so that a code next to a border is that of the quotient.  s is 2^-120 at least and
+// |x| at most 448 s; an infinite s leaves 0 of a finite x and NaN of an infinite one, and so does a 0
+// (where x is 0 or NaN).
+struct Divisor {
+    float s, inverse;
+    __device__ __forceinline__ explicit Divisor(float scale) {
+        s = scale;
+        inverse = __frcp_rn(scale);
+    }
+    __device__ __forceinline__ void divide(float (&x)[8]) const {
+        if (s >= 0x1p-60f && s < INFINITY) {
+            quotients(x, -s, inverse);
+            return;
+        }
+        // below 2^-60 both are moved up, by a power of two: the remainder would leave the normal numbers
+        const bool some = s > 0.f && s < INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= some ? 0x1p64f : 0.f;
+        if (some) quotients(x, s * -0x1p64f, __frcp_rn(s * 0x1p64f));
+    }
+
+private:
+    static __device__ __forceinline__ void quotients(float (&x)[8], float minus, float inverse) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            float n0 = x[i], n1 = x[i + 1];
+            mul2(n0, n1, inverse, inverse);
+            fma2(x[i], x[i + 1], n0, n1, minus, minus);
+            fma2(n0, n1, x[i], x[i + 1], inverse, inverse);
+            x[i] = n0;
+            x[i + 1] = n1;
+        }
+    }
+};
+
 __device__ __forceinline__ uint2 pack_e4m3x8(const float (&v)[8]) {
     return make_uint2(pack_e4m3x2(v[0], v[1]) | pack_e4m3x2(v[2], v[3]) << 16,
                       pack_e4m3x2(v[4], v[5]) | pack_e4m3x2(v[6], v[7]) << 16);

@@ -31,12 +31,10 @@ struct NormArgs {
     int32_t stage_out, stage_residual;  // rows leave through shared memory
 };
 
-// The scale of the largest magnitude `top` (as bits) and what to multiply with.  A scale is
-// 2^-120 at least, so that its reciprocal is finite; 0 if there is nothing to scale.
-__device__ __forceinline__ float scale_of(unsigned top, float *inverse) {
-    const float s = fmaxf(__fmul_rn(__uint_as_float(top), 1.f / 448.f), 0x1p-120f);
-    *inverse = top ? __fdividef(1.f, s) : 0.f;
-    return top ? s : 0.f;
+// The scale of the largest magnitude `top` (as bits): 2^-120 at least, so that its reciprocal is
+// finite; 0 if there is nothing to scale.
+__device__ __forceinline__ float scale_of(unsigned top) {
+    return top ? fmaxf(__fmul_rn(__uint_as_float(top), 1.f / 448.f), 0x1p-120f) : 0.f;
 }
 
 // A thread's part of a row.
@@ -206,7 +204,7 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
         };
         const bool e4m3 = a.out.type == RK_E4M3;
         float *scales = a.scales + t * (a.group ? (H + 127) / 128 : 1);
-        float inverse = 1.f;
+        Divisor divisor(0.f);
         if (e4m3 && a.group == 0) {
             float top = 0.f;  // fmaxf passes over NaN
 #pragma unroll
@@ -216,8 +214,9 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
 #pragma unroll
                 for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
             }
-            const float s = scale_of(team_max<TEAM>(__float_as_uint(top), maxima), &inverse);
-            if (lane == 0) scales[0] = s;
+            const float scale = scale_of(team_max<TEAM>(__float_as_uint(top), maxima));
+            if (lane == 0) scales[0] = scale;
+            divisor = Divisor(scale);
         }
         char *to = a.stage_out ? stage : a.out.row(t);
 #pragma unroll
@@ -230,12 +229,12 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
 #pragma unroll
                     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
                     const unsigned lanes = TEAM < 32 ? team_lanes<TEAM>() : 0xffffu << (threadIdx.x & 16);
-                    const float s = scale_of(__reduce_max_sync(lanes, __float_as_uint(top)), &inverse);
+                    const float scale = scale_of(__reduce_max_sync(lanes, __float_as_uint(top)));
                     const int c = C::at(lane, k);
-                    if ((lane & 15) == 0 && c < H) scales[c / 128] = s;
+                    if ((lane & 15) == 0 && c < H) scales[c / 128] = scale;
+                    divisor = Divisor(scale);
                 }
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) mul2(y[e], y[e + 1], inverse, inverse);
+                divisor.divide(y);
             }
             C::store(to, a.out.type, k, H, lane, y);
         }
