@@ -719,6 +719,8 @@ rk_status rk_preference_loss(const float *logp, const float *logp_ref, const int
  *              element's block of 256.  The new scales are the blocks' largest |m| and sqrt(v)
  *              / 448 (at least 2^-120, 0 where all are 0); a positive v keeps a code of 2^-9 at
  *              least.  The update itself uses m and v as they are before they are rounded
+ *              An infinite gradient makes its block's scales infinite, so that all 256 states are
+ *              NaN from the next step on; a NaN stays in its element, and so does either in 32 bits
  *   n          0 <= n < 2^40
  * All pointers are device memory, aligned to their element; the arrays of structs themselves
  * are host memory, read during the call (a captured graph has its own copy).  Tensors must not

@@ -1265,7 +1265,8 @@ class AdamW:
     parameters: None (none), True (made here for the bf16 parameters) or a list whose
     entries may be None.  The states are made here, as zeros of ``bits`` 32 or 8, or given:
     ``m`` and ``v`` in fp32, or in float8_e4m3fn with ``m_scale`` and ``v_scale`` (fp32, one
-    for each 256 elements): ``m = code * scale``, ``v = (code * scale)^2``.
+    for each 256 elements): ``m = code * scale``, ``v = (code * scale)^2``; an infinite
+    gradient takes the 8-bit states of its 256 elements with it.
     ``weight_decay`` and ``lr_scale`` are numbers, or lists with one for each tensor.  Nothing
     that a step writes may overlap anything else of it: a shared parameter is listed once.
 

@@ -20,7 +20,9 @@
 // 8-bit states: m = e4m3 * scale, and for v its root, u = e4m3 * scale (e4m3
 // spans 2^18, so v spans 2^36 within a block); scale = largest magnitude of
 // the new block / 448.  A positive u takes the code 2^-9 at least: an element whose m
-// is kept while its v is rounded away would be divided by eps alone.
+// is kept while its v is rounded away would be divided by eps alone.  Codes are those of
+// the quotients where a block has an infinite value too: its scales are infinite, the other
+// elements' codes 0 or 2^-9, and all of them NaN when they are read again.
 #include <algorithm>
 #include <cmath>
 
@@ -83,31 +85,24 @@ __device__ __forceinline__ void unpack_e4m3x8(uint2 w, float (&v)[8]) {
 
 // The codes of a warp's block of values and, for its first lane to write, their scale.
 template <bool FLOOR>
-__device__ __forceinline__ uint2 encode(float (&x)[8], float *scale) {
+__device__ __forceinline__ uint2 encode(const float (&x)[8], float *scale) {
     float most = 0.f;  // fmaxf passes over NaN
 #pragma unroll
     for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[i]));
     const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
     // 2^-120 at least, for a finite reciprocal
     const float s = top ? fmaxf(__fmul_rn(__uint_as_float(top), 1.f / 448.f), 0x1p-120f) : 0.f;
-    const float inverse = top ? __frcp_rn(s) : 0.f;
     *scale = s;
+    float n[8];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        // x / s, correctly rounded (Markstein, 1990: a faithful quotient and its remainder times
-        // the rounded reciprocal): a code next to a border is that of the quotient
-        float n0 = x[i], n1 = x[i + 1], r0 = x[i], r1 = x[i + 1];
-        mul2(n0, n1, inverse, inverse);
-        fma2(r0, r1, -n0, -n1, s, s);
-        fma2(n0, n1, r0, r1, inverse, inverse);
-        if (FLOOR) {
-            if (x[i] > 0.f) n0 = fmaxf(n0, 0x1p-9f);
-            if (x[i + 1] > 0.f) n1 = fmaxf(n1, 0x1p-9f);
-        }
-        x[i] = n0;
-        x[i + 1] = n1;
+    for (int i = 0; i < 8; ++i) n[i] = x[i];
+    Divisor(s).divide(n);
+    if (FLOOR) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (x[i] > 0.f) asm("max.NaN.f32 %0, %0, %1;" : "+f"(n[i]) : "f"(0x1p-9f));  // NaN stays NaN
     }
-    return pack_e4m3x8(x);
+    return pack_e4m3x8(n);
 }
 
 // ---- 8 elements of a tensor ----

@@ -1,0 +1,76 @@
+"""The AdamW step where its definition leaves little room: 8-bit states of very small values and of blocks with
+values that are not finite."""
+import pytest
+import torch
+
+from helpers import same_bits
+from test_gpu_adamw import BF16, DEV, E4M3, FP32, HYPER, make, snapshot
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def rk():
+    from invariant_rl_logprob_gb300 import build
+    build.build()
+    import invariant_rl_logprob_gb300 as rk
+    rk.load_library()
+    return rk
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+def test_8_bit_states_of_blocks_that_are_not_finite(rk, offset):
+    """An infinite gradient makes the scales of its block infinite: the codes are those of the quotients, 0 (the root's
+    smallest) for the others and NaN for itself, and the block's states are NaN from then on.  A NaN stays in its element.
+    Neighbouring blocks, and every weight but that one in this step, know nothing of it."""
+    n = 256 * 4 + 40
+    opt, other = (make(rk, [n], BF16, FP32, 8, offset=offset) for _ in range(2))
+    g = opt.grads[0]
+    g[256 + 7] = float("inf")
+    g[512 + 9] = float("nan")
+    g[256 * 4 + 39] = -float("inf")
+    hit = torch.zeros(n, dtype=torch.bool)
+    hit[[256 + 7, 512 + 9, 256 * 4 + 39]] = True
+    blocks = torch.arange(n) // 256
+    wide = (blocks == 1) | (blocks == 4)
+    rk.adamw_step(opt, **HYPER)
+    rk.adamw_step(other, **HYPER)
+    a, b = snapshot(opt), snapshot(other)
+    assert same_bits(a["master"][0][~hit], b["master"][0][~hit]) and same_bits(a["params"][0][~hit], b["params"][0][~hit])
+    assert bool(torch.isnan(a["master"][0][hit]).all())
+    for k, rest in (("m", 0.0), ("v", 2.0 ** -9)):
+        code, clean, scale = a[k][0].float(), b[k][0].float(), a[k + "_scale"][0]
+        assert torch.equal(torch.isinf(scale), torch.tensor([False, True, False, False, True]))
+        assert bool((scale[[0, 2, 3]] > 0).all())
+        assert bool(torch.isnan(code[hit]).all()) and not bool(torch.isnan(code[~hit]).any())
+        nonzero = clean[wide & ~hit] != 0
+        assert torch.equal(code[wide & ~hit].abs(), torch.where(nonzero, rest, 0.0))
+        far = ~wide & (blocks != 2)
+        assert torch.equal(code[far], clean[far])
+    # the next step: the two blocks are lost, the third but for its element is not
+    g.fill_(1e-3)
+    rk.adamw_step(opt, **{**HYPER, "step": 8})
+    w = opt.master[0].cpu()
+    assert torch.equal(torch.isnan(w), wide | hit)
+
+
+def test_codes_of_very_small_states(rk):
+    """Scales down to 2^-120: codes are those of the quotients in fp32, as everywhere."""
+    g = torch.Generator().manual_seed(1)
+    for power in (-130, -118, -100, -90, -70, -62, -58, -30):
+        n = 256 * 40
+        p, grad = torch.zeros(n, device=DEV), (torch.randn(n, generator=g) * 2.0 ** power).to(DEV)
+        opt = rk.AdamW([p], [grad], bits=8)
+        rk.adamw_step(opt, lr=1e-3, step=1, beta1=0.5, beta2=0.75)
+        m = grad.cpu() * 0.5
+        v = grad.cpu().square() * 0.25
+        for name, x in (("m", m), ("v", v.sqrt())):
+            x = x.view(-1, 256)
+            top = x.abs().amax(1, keepdim=True)
+            s = torch.where(top > 0, (top * (torch.tensor(1.0) / 448.0)).clamp(min=2.0 ** -120), 0.0)
+            q = torch.where(s > 0, x / s, 0.0)
+            if name == "v":
+                q = torch.where(x > 0, q.clamp(min=2.0 ** -9), q)
+            assert torch.equal(getattr(opt, name + "_scale")[0].cpu(), s[:, 0]), (name, power)
+            assert torch.equal(getattr(opt, name)[0].cpu().float(), q.clamp(-448, 448).to(E4M3).float().view(-1)), (name, power)
+    assert rk.get_device_error() == 0
