@@ -632,7 +632,9 @@ rk_status rk_rms_norm(const void *x, rk_dtype x_type, int64_t ld_x, const void *
  * row (as for rk_linear_logp_dw: the active rows among row_order[0..n_order), or among rows
  * 0..T-1 in ascending order when row_order is NULL)
  *     dx[t, :] = rstd * (g - n * mean(g * n)) + dr[t, :]
- * which is the gradient of x and of residual alike, 0 on all other rows; and
+ * which is the gradient of x and of residual alike, 0 on all other rows (a row whose sums of
+ * squares or of products leave fp32 is scaled for them, as above; g and n mean(g n) themselves have to
+ * fit); and
  *     dweight (+)= sum over the canonical rows of dout * n
  * in an order that depends on the number of canonical rows alone: the same rows in the same
  * canonical order give the same bits whatever their layout.  A row that row_order lists twice

@@ -318,7 +318,27 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
         }
         // rstd = k q,  n = r rstd,  mean(g n) = q mean(g z)
         const float q = root(s.x, a.per_column, a.eps, k1), rstd = q * k1;
-        const float c = -__fmul_rn(q, __fmul_rn(s.y, a.per_column));
+        float c = -__fmul_rn(q, __fmul_rn(s.y, a.per_column));
+        if (!(fabsf(c) < INFINITY)) {
+            // The products leave fp32: those of g n, or of g 2^-32 and n where g is so large that no more
+            // than its mean fits.
+            float whole = 0.f, part = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < NV; ++k) {
+#pragma unroll 1
+                for (int e = 0; e < 8; ++e) {
+                    const int col = C::at(lane, k) + e;
+                    if (col >= H) continue;
+                    const float up = one(d(), a.dout.type, col), w = one(a.weight, a.weight_type, col);
+                    const float n = __fmul_rn(one(r(), a.r.type, col), rstd);
+                    whole = __fmaf_rn(__fmul_rn(up, w), n, whole);
+                    part = __fmaf_rn(__fmul_rn(__fmul_rn(up, 0x1p-32f), w), n, part);
+                }
+            }
+            s = team_sums<TEAM>(whole, part, sums[parity]);
+            parity ^= 1;
+            c = fabsf(s.x) < INFINITY ? -__fmul_rn(s.x, a.per_column) : -__fmul_rn(s.y, a.per_column) * 0x1p32f;
+        }
 #pragma unroll
         for (int k = 0; k < NV; k += kPair) {
             float x[kPair][8], g[kPair][8], w[kPair][8], y[kPair][8];

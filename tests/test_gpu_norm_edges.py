@@ -1,0 +1,52 @@
+"""The norm and its gradient at the edges: sums that leave fp32."""
+import pytest
+import torch
+
+import norm_plain as npl
+from helpers import same_bits
+from test_gpu_norm import BF16, DEV, FP32, gen
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def rk():
+    from invariant_rl_logprob_gb300 import build
+    build.build()
+    import invariant_rl_logprob_gb300 as rk
+    rk.load_library()
+    return rk
+
+
+@pytest.mark.parametrize("H", [1, 40, 264, 512, 1000, 1001, 2048, 3000, 4096, 5000, 8192, 16384])
+def test_products_past_fp32(rk, H):
+    """Gradients so large that the sum of g r, or of g n, leaves fp32 where the result does not; with and
+    without a sum of squares that leaves it too."""
+    g = gen(H)
+    # (size of r, size of dout): sizes of g r, g n and of the result, rstd g
+    sizes = [(1e17, 1e22), (1e17, 1e34), (1e30, 1e20), (1e37, 1e36), (1e3, 2e37), (1e-3, 1e-20), (1.0, 1.0)]
+    kinds = ((FP32, FP32, None), (BF16, BF16, BF16), (BF16, FP32, FP32), (FP32, BF16, BF16))
+    for r_type, d_type, dr_type, one_sign in [(*k, s) for k in kinds for s in (True, False)]:
+        r = npl.matrix(g, len(sizes), H, FP32)
+        d = npl.matrix(g, len(sizes), H, FP32)
+        for i, (size, up) in enumerate(sizes):
+            r[i] *= size
+            d[i] = (d[i] * up).clamp(-5e37, 5e37)
+        if one_sign:
+            d = d.abs() * torch.where(r < 0, -1.0, 1.0)
+        r, d = r.to(r_type), d.to(d_type)
+        w = (1 + 0.2 * torch.rand(H, generator=g)).to(BF16)
+        dr = None if dr_type is None else npl.matrix(g, len(sizes), H, dr_type)
+        live = torch.ones(len(sizes), dtype=torch.bool)
+        got, dw = rk.rms_norm_bwd(d.to(DEV), r.to(DEV), w.to(DEV), grad_residual=None if dr is None else dr.to(DEV),
+                                  eps=npl.EPS, out_dtype=FP32)
+        want, terms, bound = npl.backward(d, r, w, dr, live)
+        ok = (got.double().cpu() - want).abs() <= bound + 2.0 ** -126
+        assert bool(ok.all()), [(sizes[i], int((~ok[i]).sum())) for i in range(len(sizes))]
+        ok = (dw.double().cpu() - terms.sum(0)).abs() <= (17 + 80) * 1.01 * npl.U * terms.abs().sum(0)
+        assert bool(ok.all())
+        # a row of its own has the same bits, beside whatever
+        alone = [rk.rms_norm_bwd(d[i:i + 1].to(DEV), r[i:i + 1].to(DEV), w.to(DEV), eps=npl.EPS, out_dtype=FP32,
+                                 grad_residual=None if dr is None else dr[i:i + 1].to(DEV))[0] for i in range(len(sizes))]
+        assert same_bits(torch.cat(alone), got)
+    assert rk.get_device_error() == 0
