@@ -1087,12 +1087,15 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor | None
     ``x`` and ``residual`` are bf16 or fp32 ``[T, H]`` with any row stride, ``weight`` bf16
     or fp32 ``[H]``, y is in ``out_dtype`` (bf16 or fp32, default: x's).  Rows with a
     negative target or outside ``cu_seqlens`` are not read and get 0; without either every
-    row is active.  ``out`` and ``residual_out`` may be ``x`` or ``residual`` itself."""
+    row is active.  ``out`` and ``residual_out`` may be ``x`` or ``residual`` itself; without a
+    residual nothing is left of r where ``out`` is ``x``, and None is returned for it."""
     code, ld = _matrix(x, "x")
     device = x.device
     out, out_code, out_ld = _result(out, out_dtype or x.dtype, x.shape, device, stream)
-    return out, _norm(x, code, ld, weight, targets, cu_seqlens, residual, eps, out, out_code, out_ld, residual_out,
-                      None, 0, device, stream)
+    r = _norm(x, code, ld, weight, targets, cu_seqlens, residual, eps, out, out_code, out_ld, residual_out,
+              None, 0, device, stream)
+    # (a result of another address has no byte in common with x)
+    return out, None if residual is None and x.numel() and out.data_ptr() == x.data_ptr() else r
 
 
 def rms_norm_e4m3(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor | None = None,
@@ -1140,7 +1143,7 @@ def rms_norm_bwd(grad_out: torch.Tensor, r: torch.Tensor, weight: torch.Tensor,
                  accumulate: bool = False, need_dweight: bool = True,
                  workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
     """The gradient of :func:`rms_norm`: returns ``(dx, dweight)``.  ``r`` is what the
-    forward returned, ``grad_residual`` a gradient that arrives at r from elsewhere; dx
+    forward returned (in place of x it leaves none), ``grad_residual`` a gradient that arrives at r from elsewhere; dx
     (``[T, H]`` in ``out_dtype``, default: r's) is the gradient of x and of residual
     alike.  dweight, fp32 ``[H]``, is summed over the active rows in canonical order
     (``row_order``; ascending rows by default), with ``accumulate`` onto what it holds; it

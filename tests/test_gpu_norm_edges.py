@@ -1,10 +1,10 @@
-"""The norm and its gradient at the edges: sums that leave fp32."""
+"""The norm and its gradient at the edges: sums that leave fp32, a norm over its own input."""
 import pytest
 import torch
 
 import norm_plain as npl
 from helpers import same_bits
-from test_gpu_norm import BF16, DEV, FP32, gen
+from test_gpu_norm import BF16, DEV, FP32, gen, weight_of
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,27 @@ def test_products_past_fp32(rk, H):
                                  grad_residual=None if dr is None else dr[i:i + 1].to(DEV))[0] for i in range(len(sizes))]
         assert same_bits(torch.cat(alone), got)
     assert rk.get_device_error() == 0
+
+
+def test_in_place_without_a_residual(rk):
+    """The norm over its own input keeps no r: none is returned, and the gradient refuses to work without."""
+    g = gen(4)
+    for H in (24, 777, 4096):
+        x = npl.matrix(g, 9, H, BF16).to(DEV)
+        w = weight_of(g, H, BF16).to(DEV)
+        y0, r0 = rk.rms_norm(x, w)
+        assert r0 is x
+        over = x.clone()
+        y, r = rk.rms_norm(over, w, out=over)
+        assert y is over and r is None and same_bits(y, y0)
+        over.copy_(x)
+        y, r = rk.rms_norm(over, w, out=over.view(9, H))
+        assert r is None and same_bits(y, y0)
+        with pytest.raises(TypeError, match="r must be a torch.Tensor"):
+            rk.rms_norm_bwd(y0, r, w)
+        # with one, r is residual_out
+        over.copy_(x)
+        y, r = rk.rms_norm(over, w, residual=x, out=over)
+        assert y is over and same_bits(r, (x.float() + x.float()).bfloat16())
+    none = torch.empty(0, 8, device=DEV)
+    assert rk.rms_norm(none, torch.ones(8, device=DEV), out=none)[1] is none
