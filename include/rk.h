@@ -617,7 +617,8 @@ rk_status rk_embedding_bwd(const void *dout, rk_dtype dout_type, const int64_t *
  *   scales       fp32 [T] or [T, ceil(H / 128)], contiguous (NULL unless out is e4m3):
  *                s = max |y| / 448 of its columns, at least 2^-120; 0 where y is 0
  * out and residual_out may be x or residual itself (same address, type and row stride); any
- * other overlap of a result with an input or another result is refused (RK_ERR_INVALID_ARG).
+ * other overlap of a result with an input (targets and cu_seqlens among them) or another result is
+ * refused (RK_ERR_INVALID_ARG).
  * Supported: 1 <= H <= 16384, 0 <= T < 2^31.  Needs no workspace.
  */
 rk_status rk_rms_norm(const void *x, rk_dtype x_type, int64_t ld_x, const void *residual,
@@ -643,7 +644,7 @@ rk_status rk_rms_norm(const void *x, rk_dtype x_type, int64_t ld_x, const void *
  *                gradient that arrives at r from elsewhere (the residual stream), or NULL
  *   dx           bf16 or fp32 [T, H] with a row stride, one rounding when it is bf16.  It may be
  *                dout, r or dr itself (same address, type and stride) unless row_order is given;
- *                other overlaps are refused
+ *                other overlaps, with targets, cu_seqlens and row_order too, are refused
  *   dweight      fp32 [H], or NULL; accumulate 1: added to what it holds
  *   workspace    >= rk_rms_norm_bwd_workspace_size(T, n, H) bytes, 16-byte aligned, n = n_order
  *                (or T): the blocks' partial sums and the list of canonical rows

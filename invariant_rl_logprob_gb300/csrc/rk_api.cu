@@ -801,6 +801,23 @@ static bool good_matrix(const rk::RulesMatrix &m, int64_t H) {
     return m.p && m.ld >= H && elem_aligned(m.p, m.type);
 }
 
+// The lists that say which rows are active, and in which order: aligned, and apart from a result, which
+// some blocks write while others still read them.
+struct RowLists {
+    const int64_t *targets;
+    int64_t T;
+    const int32_t *cu;
+    int64_t num_seqs;
+    const int64_t *order;
+    int64_t n;
+    bool good() const { return aligned(targets, 8) && aligned(cu, 4) && aligned(order, 8); }
+    bool apart(const void *p, __int128 bytes) const {
+        return !(targets && ranges_meet(p, bytes, targets, T * 8)) &&
+               !(cu && ranges_meet(p, bytes, cu, (num_seqs + 1) * 4)) &&
+               !(order && n > 0 && ranges_meet(p, bytes, order, n * 8));
+    }
+};
+
 rk_status rk_rms_norm(const void *x, rk_dtype x_type, int64_t ld_x, const void *residual,
                       rk_dtype residual_type, int64_t ld_residual, const void *weight,
                       rk_dtype weight_type, float eps, const int64_t *targets,
@@ -822,6 +839,9 @@ rk_status rk_rms_norm(const void *x, rk_dtype x_type, int64_t ld_x, const void *
         return RK_ERR_INVALID_ARG;
     if (e4m3 && (!scales || !aligned(scales, 4))) return RK_ERR_INVALID_ARG;
     if (T >= (int64_t(1) << 31) || H > rk::kNormMaxColumns) return RK_ERR_UNSUPPORTED;
+    const RowLists lists{targets, T, cu_seqlens, num_seqs, nullptr, 0};
+    if (!lists.good() || !lists.apart(out, span(mo, T, H)) || (residual && !lists.apart(residual_out, span(mro, T, H))))
+        return RK_ERR_INVALID_ARG;
     // results in place of x or residual, or apart from everything
     const int64_t weight_bytes = H * elem_size(weight_type);
     if (!can_hold(mx, mo, T, H) || ranges_meet(weight, weight_bytes, out, span(mo, T, H)))
@@ -832,8 +852,8 @@ rk_status rk_rms_norm(const void *x, rk_dtype x_type, int64_t ld_x, const void *
         return RK_ERR_INVALID_ARG;
     if (e4m3) {
         const __int128 bytes = (__int128)T * (group ? (H + group - 1) / group : 1) * 4;
-        if (ranges_meet(scales, bytes, x, span(mx, T, H)) || ranges_meet(scales, bytes, out, span(mo, T, H)) ||
-            ranges_meet(scales, bytes, weight, weight_bytes))
+        if (!lists.apart(scales, bytes) || ranges_meet(scales, bytes, x, span(mx, T, H)) ||
+            ranges_meet(scales, bytes, out, span(mo, T, H)) || ranges_meet(scales, bytes, weight, weight_bytes))
             return RK_ERR_INVALID_ARG;
         if (residual && (ranges_meet(scales, bytes, residual, span(mr, T, H)) ||
                          ranges_meet(scales, bytes, residual_out, span(mro, T, H))))
@@ -876,6 +896,9 @@ rk_status rk_rms_norm_bwd(const void *dout, rk_dtype dout_type, int64_t ld_dout,
     if (T > 0) {
         if (!good_matrix(md, H) || !good_matrix(mr, H) || !good_matrix(mx, H) || (dr && !good_matrix(mg, H)) ||
             !weight || !elem_aligned(weight, weight_type))
+            return RK_ERR_INVALID_ARG;
+        const RowLists lists{targets, T, cu_seqlens, num_seqs, row_order, n};
+        if (!lists.good() || !lists.apart(dx, span(mx, T, H)) || (dweight && !lists.apart(dweight, H * 4)))
             return RK_ERR_INVALID_ARG;
         // A row that row_order names twice is read twice: dx is apart from what it is made of.
         const auto fits = row_order ? rows_apart : can_hold;
