@@ -861,6 +861,14 @@ def _run(what: str, fn, device, stream, *args) -> None:
         _check(st, what)
 
 
+def _is_capturing(stream) -> bool:
+    """Whether the stream that an operator runs on is being captured into a graph."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _scratch(workspace, need: int, device, stream) -> torch.Tensor:
     if workspace is None:
         return _empty(max(need, 1), torch.uint8, device, stream)
@@ -1274,7 +1282,8 @@ class AdamW:
     that a step writes may overlap anything else of it: a shared parameter is listed once.
 
     All are kept by the object and changed in place by :func:`adamw_step`; a replayed CUDA
-    graph of the step needs the object alive."""
+    graph of the step needs the object alive, which keeps the gradients that it was captured
+    with too."""
 
     def __init__(self, params, grads, m=None, v=None, *, m_scale=None, v_scale=None, master=None,
                  bits: int = 32, weight_decay=0.0, lr_scale=1.0):
@@ -1330,10 +1339,12 @@ class AdamW:
         self._written = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in written)
         if any(a[1] > b[0] for a, b in zip(self._written, self._written[1:])):
             raise ValueError("parameters, masters and states must not overlap (a shared parameter is listed once)")
+        self._captured = []  # lists of gradients that a captured step reads
         self.use_grads(grads)
 
     def use_grads(self, grads) -> None:
-        """Takes other tensors as the gradients of the next steps."""
+        """Takes other tensors as the gradients of the next steps.  A graph that is captured
+        already goes on reading those it was captured with."""
         grads = self._each(grads, "grads", self.count)
         for p, g in zip(self.params, grads):
             self._check(g, "a gradient", (torch.bfloat16, torch.float32), p.numel())
@@ -1386,7 +1397,8 @@ def adamw_step(tensors: AdamW, *, lr: float | torch.Tensor, step: int | torch.Te
 
     with ``lr' = lr * lr_scale``.  ``step`` counts from 1.  ``lr`` (fp32) and ``step`` (int64)
     may be one-element CUDA tensors, read when the step runs: a replayed CUDA graph follows
-    them.  ``grad_scale`` is such a tensor too (fp32), a factor of all gradients."""
+    them, and needs them alive.  ``grad_scale`` is such a tensor too (fp32), a factor of all
+    gradients."""
     if not isinstance(tensors, AdamW):
         raise TypeError("tensors must be an AdamW")
     lib = _lib or load_library()
@@ -1403,6 +1415,8 @@ def adamw_step(tensors: AdamW, *, lr: float | torch.Tensor, step: int | torch.Te
     else:
         o.step = step
     _run("rk_adamw_step", lib.rk_adamw_step, device, stream, tensors.address, tensors.count, ctypes.addressof(o))
+    if _is_capturing(stream) and not (tensors._captured and tensors._captured[-1] is tensors.grads):
+        tensors._captured.append(tensors.grads)
 
 
 def selftest_wait_timeout(limit_ns: int, stream: torch.cuda.Stream | None = None) -> None:

@@ -1,5 +1,8 @@
 """The AdamW step where its definition leaves little room: 8-bit states of very small values and of blocks with
-values that are not finite."""
+values that are not finite, gradients that a graph holds."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -74,3 +77,42 @@ def test_codes_of_very_small_states(rk):
             assert torch.equal(getattr(opt, name + "_scale")[0].cpu(), s[:, 0]), (name, power)
             assert torch.equal(getattr(opt, name)[0].cpu().float(), q.clamp(-448, 448).to(E4M3).float().view(-1)), (name, power)
     assert rk.get_device_error() == 0
+
+
+def test_a_graph_keeps_the_gradients_that_it_was_captured_with(rk):
+    """use_grads is for steps to come: what a captured step reads stays alive with the object."""
+    opt, other = (make(rk, [5000, 300], BF16, FP32, 32) for _ in range(2))
+    old = [g.clone() for g in opt.grads]
+    opt.use_grads(old)
+    alive = [weakref.ref(g) for g in old]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rk.adamw_step(opt, **HYPER)
+    new = [torch.full_like(g, 3.0) for g in old]
+    opt.use_grads(new)
+    del old
+    gc.collect()
+    assert all(ref() is not None for ref in alive)
+    graph.replay()
+    rk.adamw_step(other, **HYPER)
+    assert all(same_bits(a, b) for a, b in zip(opt.master, other.master))
+    # eager steps hold on to nothing
+    last = weakref.ref(new[0])
+    rk.adamw_step(opt, **HYPER)
+    opt.use_grads([torch.zeros_like(g) for g in new])
+    torch.cuda.synchronize()
+    del new
+    gc.collect()
+    assert last() is None
+    # captured on a stream that is passed
+    held = [torch.zeros_like(g) for g in opt.grads]
+    opt.use_grads(held)
+    ref, side, beside = weakref.ref(held[0]), torch.cuda.Stream(), torch.cuda.Stream()
+    graph2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph2, stream=side):
+        with torch.cuda.stream(beside):
+            rk.adamw_step(opt, stream=side, **HYPER)
+    del held
+    opt.use_grads(other.grads)
+    gc.collect()
+    assert ref() is not None
