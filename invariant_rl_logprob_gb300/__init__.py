@@ -1277,7 +1277,8 @@ class AdamW:
     entries may be None.  The states are made here, as zeros of ``bits`` 32 or 8, or given:
     ``m`` and ``v`` in fp32, or in float8_e4m3fn with ``m_scale`` and ``v_scale`` (fp32, one
     for each 256 elements): ``m = code * scale``, ``v = (code * scale)^2``; an infinite
-    gradient takes the 8-bit states of its 256 elements with it.
+    gradient takes the 8-bit states of its 256 elements with it.  What is made here is there
+    for every stream when the object is: making it waits for the current one.
     ``weight_decay`` and ``lr_scale`` are numbers, or lists with one for each tensor.  Nothing
     that a step writes may overlap anything else of it: a shared parameter is listed once.
 
@@ -1297,6 +1298,7 @@ class AdamW:
             raise ValueError("m_scale and v_scale go together, with m and v")
         for p in params:
             self._check(p, "a parameter", (torch.bfloat16, torch.float32), None)
+        made = m is None or master is True
         if m is None:
             if bits not in (8, 32):
                 raise ValueError(f"bits must be 8 or 32, got {bits}")
@@ -1308,6 +1310,8 @@ class AdamW:
                 m_scale, v_scale = scales(), scales()
         if master is True:
             master = [p.float() if p.dtype is torch.bfloat16 else None for p in params]
+        if made and count and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).synchronize()  # the first step may be on another stream
         self.params, self.m, self.v = params, each(m, "m"), each(v, "v")
         self.m_scale, self.v_scale = (None, None) if m_scale is None else (each(m_scale, "m_scale"), each(v_scale, "v_scale"))
         self.master = None if master is None else each(master, "master")

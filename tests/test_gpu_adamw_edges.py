@@ -1,5 +1,5 @@
 """The AdamW step where its definition leaves little room: 8-bit states of very small values and of blocks with
-values that are not finite, gradients that a graph holds."""
+values that are not finite, gradients that a graph holds, the first step on another stream."""
 import gc
 import weakref
 
@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from helpers import same_bits
-from test_gpu_adamw import BF16, DEV, E4M3, FP32, HYPER, make, snapshot
+from test_gpu_adamw import BF16, DEV, E4M3, FP32, HYPER, make, snapshot, tensors
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +116,25 @@ def test_a_graph_keeps_the_gradients_that_it_was_captured_with(rk):
     opt.use_grads(other.grads)
     gc.collect()
     assert ref() is not None
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_first_step_may_be_on_another_stream(rk, bits):
+    """States and masters that are made with the object are there when it is, while the stream that
+    made them is still busy with something else."""
+    side = torch.cuda.Stream()
+    busy = torch.zeros(1 << 28, device=DEV)
+    for turn in range(4):
+        p, g = tensors([70001, 300], BF16, 0.1, turn), tensors([70001, 300], FP32, 0.1, turn + 1)
+        want = rk.AdamW([t.clone() for t in p], g, bits=bits, master=True)
+        rk.adamw_step(want, **HYPER)
+        # memory of the states' sizes that is not zero, for the allocator to hand out again
+        junk = [torch.full((t.numel(),), 7.0, device=DEV) for t in p for _ in range(4)]
+        torch.cuda.synchronize()
+        del junk
+        for _ in range(20):
+            busy.add_(1.0)
+        opt = rk.AdamW(p, g, bits=bits, master=True)
+        rk.adamw_step(opt, **HYPER, stream=side)
+        torch.cuda.synchronize()
+        assert all(same_bits(a, b) for a, b in zip(opt.master, want.master))
