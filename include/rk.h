@@ -730,8 +730,9 @@ rk_status rk_preference_loss(const float *logp, const float *logp_ref, const int
  * overlap.
  *   lr, beta1, beta2 in [0, 1), eps > 0, step >= 1 (the first step is 1)
  *   lr_device    fp32 [1] or NULL: read instead of lr;  step_device int64 [1] or NULL: read
- *                instead of step.  A graph that is replayed follows them.  A step below 1 there
- *                sets RK_DEVERR_RULES and changes nothing
+ *                instead of step.  A graph that is replayed follows them, and a step has the same
+ *                bits either way (lr is rounded to fp32).  A step below 1 there sets
+ *                RK_DEVERR_RULES and changes nothing
  *   grad_scale   fp32 [1] or NULL (1): a factor of all gradients, of clipping or loss scaling
  */
 typedef struct {

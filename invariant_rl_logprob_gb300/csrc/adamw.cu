@@ -57,7 +57,7 @@ struct Tensor {
 struct Table {
     int32_t first[kTensors + 1];  // chunks before each tensor
     int32_t count;
-    float lr, rise, root;  // learning rate, 1 / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
+    float lr, rise, root;  // learning rate and the corrections of the host's step
     float beta1, rest1, log1, beta2, rest2, log2, eps;  // rest = 1 - beta, log = log(beta)
     float one;  // 1
     const float *lr_device;
@@ -147,6 +147,31 @@ __device__ __forceinline__ void put_codes(void *p, int64_t at, int left, bool ve
 }
 
 // ---- the step ----
+
+// 1 - exp(x) for x <= 0, within two units in the last place and without a difference of numbers close to
+// 1: x = k log 2 + r (Cody and Waite, 1980), e^r - 1 by its Taylor series up to r^7.  Every operation is
+// one of IEEE 754, so that the host and the device get the same bits.
+__host__ __device__ inline float one_minus_exp(float x) {
+    x = fmaxf(x, -80.f);  // 1 from there on
+    const float k = rintf(x * 1.44269504f);
+    const float r = fmaf(k, -3.19461845e-5f, fmaf(k, -0.693115234375f, x));
+    float p = fmaf(r, 1.f / 5040.f, 1.f / 720.f);
+    p = fmaf(r, p, 1.f / 120.f);
+    p = fmaf(r, p, 1.f / 24.f);
+    p = fmaf(r, p, 1.f / 6.f);
+    p = fmaf(r, p, 0.5f);
+    const float power = ldexpf(1.f, (int)k);
+    return fmaf(-power, fmaf(r * r, p, r), 1.f - power);
+}
+
+// What the moments' bias leaves of a step: 1 / (1 - beta1^step) and 1 / sqrt(1 - beta2^step), of log(beta).
+struct Corrections {
+    float rise, root;
+    __host__ __device__ Corrections(int64_t step, float log1, float log2) {
+        rise = 1.f / one_minus_exp((float)step * log1);
+        root = 1.f / sqrtf(one_minus_exp((float)step * log2));
+    }
+};
 
 struct Rates {
     float rate, root, decay, scale;  // lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step), lr wd, grad_scale
@@ -304,9 +329,9 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
             if (threadIdx.x == 0) atomicOr(a.err, kErrRules);
             return;
         }
-        // 1 - beta^step = -expm1(step log(beta)): no difference of numbers close to 1
-        rise = __fdiv_rn(1.f, -expm1f((float)step * a.log1));
-        root = __fdiv_rn(1.f, __fsqrt_rn(-expm1f((float)step * a.log2)));
+        const Corrections c(step, a.log1, a.log2);
+        rise = c.rise;
+        root = c.root;
     }
     const float lr = __fmul_rn(a.lr_device ? *a.lr_device : a.lr, t.lr_scale);
     const Rates r{__fmul_rn(lr, rise), root, __fmul_rn(lr, t.weight_decay), a.grad_scale ? *a.grad_scale : 1.f};
@@ -323,16 +348,16 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
 cudaError_t launch_adamw(const rk_adamw_tensor *tensors, int64_t count, const rk_adamw_options &o,
                          const DeviceInfo &di, cudaStream_t st) {
     Table a;
-    const double step = o.step_device ? 1.0 : (double)o.step;
     a.lr = (float)o.lr;
-    a.rise = (float)(1.0 / -std::expm1(step * std::log(o.beta1)));
-    a.root = (float)(1.0 / std::sqrt(-std::expm1(step * std::log(o.beta2))));
     a.beta1 = (float)o.beta1;
     a.rest1 = (float)(1.0 - o.beta1);
     a.log1 = (float)std::log(o.beta1);
     a.beta2 = (float)o.beta2;
     a.rest2 = (float)(1.0 - o.beta2);
     a.log2 = (float)std::log(o.beta2);
+    const Corrections c(o.step_device ? 1 : o.step, a.log1, a.log2);
+    a.rise = c.rise;
+    a.root = c.root;
     a.eps = (float)o.eps;
     a.one = 1.f;
     a.lr_device = o.lr_device;

@@ -1,5 +1,6 @@
 """The AdamW step where its definition leaves little room: 8-bit states of very small values and of blocks with
-values that are not finite, gradients that a graph holds, the first step on another stream."""
+values that are not finite, gradients that a graph holds, the first step on another stream, rates from the host
+and from the device."""
 import gc
 import weakref
 
@@ -7,7 +8,7 @@ import pytest
 import torch
 
 from helpers import same_bits
-from test_gpu_adamw import BF16, DEV, E4M3, FP32, HYPER, make, snapshot, tensors
+from test_gpu_adamw import BF16, DEV, E4M3, FP32, HYPER, SIZES, make, snapshot, tensors
 
 pytestmark = pytest.mark.gpu
 
@@ -138,3 +139,19 @@ def test_the_first_step_may_be_on_another_stream(rk, bits):
         rk.adamw_step(opt, **HYPER, stream=side)
         torch.cuda.synchronize()
         assert all(same_bits(a, b) for a, b in zip(opt.master, want.master))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("betas", [(0.9, 0.999), (0.9, 0.95), (0.0, 0.5), (0.99, 0.9999)])
+def test_a_step_has_the_same_bits_from_the_host_and_from_the_device(rk, bits, betas):
+    """... so an eager step and a captured one that follows a counter agree."""
+    for step in (1, 2, 3, 7, 10, 33, 100, 1000, 12345, 10 ** 6, 10 ** 9, 2 ** 40):
+        hyper = dict(step=step, beta1=betas[0], beta2=betas[1], eps=1e-8)
+        a, b = (make(rk, SIZES, BF16, FP32, bits, seed=step % 1000) for _ in range(2))
+        rk.adamw_step(a, lr=1e-3, **hyper)
+        rk.adamw_step(b, lr=torch.tensor([1e-3], device=DEV), **{**hyper, "step": torch.tensor([step], device=DEV)})
+        x, y = snapshot(a), snapshot(b)
+        for k in x:
+            for s, t in zip(x[k] or [], y[k] or []):
+                assert torch.equal(s.view(torch.uint8), t.view(torch.uint8)), (k, step)
+    assert rk.get_device_error() == 0
