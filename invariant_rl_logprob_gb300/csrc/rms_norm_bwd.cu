@@ -545,34 +545,54 @@ cudaError_t whole_launch(int read, NormBwdArgs &a, const DeviceInfo &di, cudaStr
     switch (read) {
         case kWords: return backward_launch<TEAM, NV, kWords, BLOCK, PER_SM, LIST>(a, di, st);
         case kMixed: return backward_launch<TEAM, NV, kMixed, BLOCK, PER_SM, LIST>(a, di, st);
-        case kAligned: return backward_launch<TEAM, NV, kAligned, BLOCK, PER_SM, LIST>(a, di, st);
+        case kAligned:
+            // (the one width whose rows are halved whenever they are read so)
+            if constexpr (TEAM != 64 || NV != 4) return backward_launch<TEAM, NV, kAligned, BLOCK, PER_SM, LIST>(a, di, st);
+            return cudaErrorInvalidValue;
         default: return backward_launch<TEAM, NV, kFloats, BLOCK, PER_SM, LIST>(a, di, st);
     }
 }
 template <int TEAM, int NV, int BLOCK, int PER_SM, bool LIST>
 cudaError_t halved_launch(int read, NormBwdArgs &a, const DeviceInfo &di, cudaStream_t st) {
+    if constexpr (TEAM == 128) {  // the one width that halves rows in bf16
+        if (read == kWords) return backward_launch<TEAM, NV, kWords, BLOCK, PER_SM, LIST>(a, di, st);
+        if (read == kMixed) return backward_launch<TEAM, NV, kMixed, BLOCK, PER_SM, LIST>(a, di, st);
+    }
     return read == kAligned ? backward_launch<TEAM, NV, kAligned, BLOCK, PER_SM, LIST>(a, di, st)
                             : backward_launch<TEAM, NV, kFloats, BLOCK, PER_SM, LIST>(a, di, st);
 }
 
-// Whether a row of more than 2048 columns is kept by twice the threads, half the columns each: where r or
-// dr is fp32 and there is a dr.  All in fp32, 2^27 elements, halved against not: 4096 columns 323 and 420
-// us, 8192 338 and 408; 5120 (where 192 of 512 threads would have none) 404 and 347.  Without dr, a third
-// less to wait for: 4096 columns 271 and 221.
-bool halved(int64_t H, bool wide, bool dr) { return wide && dr && (H <= 4096 || H > 6144); }
+// Whether a row of more than 1024 columns is kept by twice the threads, half the columns each.  2^27
+// elements, halved against not:
+//   up to 2048 columns, rows that are made of whole vectors: where r or dr is fp32 (all fp32 without dr, 1536
+//   columns 248 us and 259, 1792 256 and 297), or where so many of the threads have work that it pays: in bf16
+//   beyond 1792 columns (1536 with dr 194 and 184, 1792 173 and 170, 2048 161 and 182), with dout in fp32
+//   beyond 1408 (1408 220 and 212, 1536 213 and 240).  Other rows are read twice in any case: with a wide dr
+//   only (2047 columns, bf16 472 and 456, without dr 413 and 387, all fp32 without dr 499 and 472).
+//   beyond: where r or dr is fp32 and there is a dr (all fp32, 4096 columns 323 and 420, 8192 338 and 408; 5120,
+//   where 192 of 512 threads would have none, 404 and 347; without dr, a third less to wait for, 4096 columns 271
+//   and 221).
+struct Kind {
+    bool wide, dr, dout_wide;  // r or dr in fp32, dr given, dout in fp32
+};
+bool halved(int64_t H, const Kind &k) {
+    if (H <= 1024) return false;
+    if (H > 2048) return k.wide && k.dr && (H <= 4096 || H > 6144);
+    if (H % 8 != 0) return k.wide && k.dr;
+    return k.wide || H > (k.dout_wide ? 1408 : 1792);
+}
 
 // Widest row, and for rows as they are and halved ones team, vectors of 8 a thread, block and blocks per
 // SM.  The blocks per SM are what leaves a team's sums in registers: at 4096 columns of bf16 3, 4 and 5
 // blocks of 128 threads took 103, 96 and 104 us for 16384 rows, before rows were asked for ahead.  Up to
-// 2048 columns a thread has 16: 2^27 elements of bf16 with dr, 1024 columns 164 us where 32 took 188, 2048
-// 162 and 171 (1536, of which 128 threads' last 64 have half, 196 and 184).
+// 1024 columns a thread has 16 (2^27 elements of bf16 with dr, 1024 columns 164 us where 32 took 188).
 #define RK_NORM_BWD_SHAPES(SHAPE)                  \
     SHAPE(64, 8, 1, 256, 3, 8, 1, 256, 3)          \
     SHAPE(128, 16, 1, 256, 3, 16, 1, 256, 3)       \
     SHAPE(256, 32, 1, 256, 3, 32, 1, 256, 3)       \
     SHAPE(512, 32, 2, 256, 2, 32, 2, 256, 2)       \
     SHAPE(1024, 64, 2, 64, 8, 64, 2, 64, 8)        \
-    SHAPE(2048, 128, 2, 128, 4, 128, 2, 128, 4)    \
+    SHAPE(2048, 64, 4, 64, 8, 128, 2, 128, 4)      \
     SHAPE(4096, 128, 4, 128, 4, 256, 2, 256, 2)    \
     SHAPE(8192, 256, 4, 256, 2, 512, 2, 512, 1)    \
     SHAPE(16384, 512, 4, 512, 1, 512, 4, 512, 1)
@@ -649,7 +669,7 @@ cudaError_t launch_rms_norm_bwd(const RulesMatrix &dout, const RulesMatrix &r, c
     }
     const bool on16 = plain(a.r, H) && plain(a.dout, H) && plain(a.dr, H) && aligned(weight, 16);
     const bool wide = a.r.type == RK_FP32 || (dr && a.dr.type == RK_FP32);
-    const bool half = halved(H, wide, dr != nullptr);
+    const bool half = halved(H, Kind{wide, dr != nullptr, a.dout.type == RK_FP32});
     const int read = !on16 ? kFloats : wide ? kAligned : a.dout.type == RK_BF16 ? kWords : kMixed;
     const auto run = [&] {
 #define SHAPE(MAX, TEAM, NV, BLOCK, PER, HTEAM, HNV, HBLOCK, HPER)                          \
