@@ -637,8 +637,10 @@ rk_status rk_rms_norm(const void *x, rk_dtype x_type, int64_t ld_x, const void *
  * squares or of products leave fp32 is scaled for them, as above; g and n mean(g n) themselves have to
  * fit); and
  *     dweight (+)= sum over the canonical rows of dout * n
- * in an order that depends on the number of canonical rows alone: the same rows in the same
- * canonical order give the same bits whatever their layout.  A row that row_order lists twice
+ * in an order that depends on the number of canonical rows, on H, on the types of dout, r and dr and
+ * on whether there is a dr, and on nothing else: the same rows in the same canonical order give the
+ * same bits whatever their layout, and so does each row's dx.  (dr has no term in dweight, but with an
+ * fp32 dr some widths divide rows among threads in another way.)  A row that row_order lists twice
  * counts twice in dweight.
  *   dout, r, dr  bf16 or fp32 [T, H] with row strides, as above; r: x, or residual_out; dr:
  *                gradient that arrives at r from elsewhere (the residual stream), or NULL

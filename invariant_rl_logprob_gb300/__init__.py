@@ -1154,7 +1154,8 @@ def rms_norm_bwd(grad_out: torch.Tensor, r: torch.Tensor, weight: torch.Tensor,
     forward returned (in place of x it leaves none), ``grad_residual`` a gradient that
     arrives at r from elsewhere; dx (``[T, H]`` in ``out_dtype``, default: r's) is the
     gradient of x and of residual alike.  dweight, fp32 ``[H]``, is summed over the active rows in canonical order
-    (``row_order``; ascending rows by default), with ``accumulate`` onto what it holds; it
+    (``row_order``; ascending rows by default), with ``accumulate`` onto what it holds
+    (its bits depend on those rows, the types and whether there is a ``grad_residual``); it
     is None without ``need_dweight`` (a weight that is not trained).  Rows that are not among
     them get dx = 0.  ``out`` may be ``grad_out``, ``r`` or ``grad_residual`` itself unless
     ``row_order`` is given."""

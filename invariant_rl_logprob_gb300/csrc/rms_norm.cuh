@@ -2,8 +2,8 @@
 // team of threads holds, reads, sums and writes them (rms_norm.cu,
 // rms_norm_bwd.cu).
 //
-// A team (part of a warp up to 128 columns, a warp up to 1024, up to 16 warps
-// beyond) has a row in registers, up to 32 columns a thread: fewer threads a row
+// A team (part of a warp up to 128 columns, a warp up to 1024 or, in the gradient, 512, up to
+// 16 warps beyond) has a row in registers, up to 32 columns a thread: fewer threads a row
 // mean fewer that sum, scale and wait for one another (256 threads with 16 columns
 // each, 65536 x 4096 with residual to e4m3: 290 us; 128 with 32: 265, 105 % of the
 // copy rate).  A thread owns eight consecutive columns at a time.  Rows off 16-byte
@@ -12,7 +12,7 @@
 // leave in aligned 16 bytes as well.
 //
 // Which thread owns which column, and with it the order of every sum, depends on H
-// and, in the gradient, on the types.  A sum of squares that leaves fp32 is formed again from r * 2^-80, and
+// and, in the gradient, on the types and on whether there is a residual's gradient.  A sum of squares that leaves fp32 is formed again from r * 2^-80, and
 // the gradient's sum of g r from n, of the size of 1, in place of r.
 #pragma once
 

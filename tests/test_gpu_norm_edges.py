@@ -1,4 +1,5 @@
-"""The norm and its gradient at the edges: sums that leave fp32, a norm over its own input."""
+"""The norm and its gradient at the edges: sums that leave fp32, a norm over its own input, what
+the weight's gradient knows of the residual's."""
 import pytest
 import torch
 
@@ -74,3 +75,27 @@ def test_in_place_without_a_residual(rk):
         assert y is over and same_bits(r, (x.float() + x.float()).bfloat16())
     none = torch.empty(0, 8, device=DEV)
     assert rk.rms_norm(none, torch.ones(8, device=DEV), out=none)[1] is none
+
+
+# both sides of every limit between a team and its vectors, whole and halved
+WIDTHS = [24, 264, 513, 1000, 1024, 1025, 1408, 1416, 1536, 1537, 1792, 1800, 2048, 2049, 2056, 3000, 3001, 4096, 4104,
+          6144, 6145, 6152, 8190, 8192, 8200]
+
+
+@pytest.mark.parametrize("r_type", [BF16, FP32])
+@pytest.mark.parametrize("H", WIDTHS)
+def test_a_residual_s_gradient_of_the_same_type_leaves_dweight_s_bits(rk, H, r_type):
+    """dweight has no term of dr, and the order of its sum knows of dr by its type alone where r is bf16; where r is
+    fp32 it knows whether there is one in some widths, and then of no type."""
+    g = gen(H + 1)
+    T = 3000 if H <= 2056 else 1300
+    r, dout = npl.matrix(g, T, H, r_type).to(DEV), npl.matrix(g, T, H, BF16).to(DEV)
+    w = weight_of(g, H, BF16).to(DEV)
+    _, without = rk.rms_norm_bwd(dout, r, w)
+    a, b = (rk.rms_norm_bwd(dout, r, w, grad_residual=npl.matrix(g, T, H, t).to(DEV))[1] for t in (BF16, FP32))
+    if r_type is BF16:
+        assert same_bits(a, without)
+    else:
+        assert same_bits(a, b)
+    if H <= 1024 or 4096 < H <= 6144 or H > 8192:
+        assert same_bits(a, without) and same_bits(b, without)
