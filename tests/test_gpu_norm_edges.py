@@ -1,11 +1,12 @@
 """The norm and its gradient at the edges: sums that leave fp32, a norm over its own input, what
-the weight's gradient knows of the residual's."""
+the weight's gradient knows of the residual's, and the gradient in every combination of types at every width
+where its shape changes, with masks and off alignment."""
 import pytest
 import torch
 
 import norm_plain as npl
 from helpers import same_bits
-from test_gpu_norm import BF16, DEV, FP32, gen, weight_of
+from test_gpu_norm import BF16, DEV, FP32, bwd_case, check_bwd, gen, padded_like, weight_of
 
 pytestmark = pytest.mark.gpu
 
@@ -77,9 +78,58 @@ def test_in_place_without_a_residual(rk):
     assert rk.rms_norm(none, torch.ones(8, device=DEV), out=none)[1] is none
 
 
-# both sides of every limit between a team and its vectors, whole and halved
+# every pair of a team and its vectors, whole and halved, on both sides of every limit
 WIDTHS = [24, 264, 513, 1000, 1024, 1025, 1408, 1416, 1536, 1537, 1792, 1800, 2048, 2049, 2056, 3000, 3001, 4096, 4104,
           6144, 6145, 6152, 8190, 8192, 8200]
+TYPES = [(r, d, z) for r in (BF16, FP32) for d in (BF16, FP32) for z in (None, BF16, FP32)]
+
+
+def moved(t, ld, offset):
+    m = npl.matrix(gen(0), *t.shape, t.dtype, ld, offset)
+    m.copy_(t)
+    return npl.to(m, DEV)
+
+
+@pytest.mark.parametrize("r_type,d_type,dr_type", TYPES)
+@pytest.mark.parametrize("H", WIDTHS)
+def test_backward_of_every_combination_of_types(rk, H, r_type, d_type, dr_type):
+    """Against 64 bits with a mask, all at once and by short lists; NaN in rows that are not active; rows
+    off 16 bytes have the same bits."""
+    g = gen(H)
+    T = 37
+    r, dout, dr, w = bwd_case(g, T, H, r_type, d_type, dr_type)
+    targets = padded_like(g, T)
+    live = targets >= 0
+    rp, dp, zp = r.clone(), dout.clone(), None if dr is None else dr.clone()
+    for m in (rp, dp, zp):
+        if m is not None:
+            m[~live] = float("nan")
+    to = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    w_dev, tg = w.to(DEV), targets.to(DEV)
+    full = torch.full((T, H), float("nan"), device=DEV)
+    dx, dw = rk.rms_norm_bwd(to(dp), to(rp), w_dev, tg, grad_residual=to(zp), eps=npl.EPS, out=full)
+    check_bwd(dx, dw, r, dout, dr, w, live)
+    assert not bool(dx[~live.to(DEV)].any())
+    # packed, without a mask
+    px, pw = rk.rms_norm_bwd(to(dout[live]), to(r[live]), w_dev, grad_residual=to(None if dr is None else dr[live]),
+                             eps=npl.EPS, out_dtype=FP32)
+    assert same_bits(px, dx[live.to(DEV)]) and same_bits(pw, dw)
+    # behind more rows than blocks list for themselves
+    far = lambda t: None if t is None else torch.cat([torch.full((1100, H), float("nan"), dtype=t.dtype), t]).to(DEV)  # noqa: E731
+    fx, fw = rk.rms_norm_bwd(far(dp), far(rp), w_dev, torch.cat([torch.full((1100,), -1), targets]).to(DEV),
+                             grad_residual=far(zp), eps=npl.EPS, out_dtype=FP32)
+    assert same_bits(fx[1100:], dx) and same_bits(fw, dw) and not bool(fx[:1100].any())
+    # off 16 bytes
+    for ld, offset in ((3, 1), (8, 4)):
+        off = lambda t: None if t is None else moved(t, ld, offset)  # noqa: E731
+        ox, ow = rk.rms_norm_bwd(off(dp), off(rp), w_dev, tg, grad_residual=off(zp), eps=npl.EPS, out=off(full.cpu()))
+        assert same_bits(ox.contiguous(), dx) and same_bits(ow, dw)
+    # some rows twice, with the mask
+    order = torch.randint(0, T, (50,), generator=g)
+    times = torch.bincount(order, minlength=T) * live
+    dx, dw = rk.rms_norm_bwd(to(dp), to(rp), w_dev, tg, grad_residual=to(zp), eps=npl.EPS, out_dtype=FP32, row_order=to(order))
+    check_bwd(dx, dw, r, dout, dr, w, times > 0, times=times)
+    assert rk.get_device_error() == 0
 
 
 @pytest.mark.parametrize("r_type", [BF16, FP32])
