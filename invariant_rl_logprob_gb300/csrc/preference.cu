@@ -256,7 +256,8 @@ __device__ __forceinline__ Ratio ratio_of(const Args &a, int q) {
     return r;
 }
 
-// loss and f' of x = beta d, given as a rounded number and what is left of it.
+// loss and f' of x = beta d, given as a rounded number and what is left of it.  (Here and in `compare`
+// every product says whether it is fused with the sum that it goes into: both kernels have the same bits.)
 __device__ __forceinline__ void lose(const Args &a, float x, float rest, float *loss, float *slope) {
     if (a.kind == RK_PREFERENCE_HINGE) {
         const float gap = (1.f - x) - rest;
@@ -266,15 +267,15 @@ __device__ __forceinline__ void lose(const Args &a, float x, float rest, float *
     }
     // e = exp(-|x|): softplus(+-x) = max(+-x, 0) + log1p(e), sigmoid(|x|) = 1 / (1 + e)
     const float sign = x < 0.f ? -1.f : 1.f;
-    const float m = expf(-fabsf(x)), e = m - m * (sign * rest);
+    const float m = expf(-fabsf(x)), e = __fmaf_rn(-m, sign * rest, m);
     const float tail = log1pf(e), minor = e / (1.f + e), major = 1.f / (1.f + e);
     const float up = x < 0.f ? minor : major, down = x < 0.f ? major : minor;
     const float keep = 1.f - a.smoothing;
     *loss = tail;
-    if (x < 0.f && keep > 0.f) *loss += keep * -(x + rest);
-    if (x > 0.f && a.smoothing > 0.f) *loss += a.smoothing * (x + rest);
+    if (x < 0.f && keep > 0.f) *loss = __fmaf_rn(keep, -(x + rest), *loss);
+    if (x > 0.f && a.smoothing > 0.f) *loss = __fmaf_rn(a.smoothing, x + rest, *loss);
     if (x != x) *loss = x;
-    *slope = a.beta * (a.smoothing * up - keep * down);
+    *slope = a.beta * __fmaf_rn(-keep, down, __fmul_rn(a.smoothing, up));
 }
 
 // Differences are exact in multiples of 2^-42; 64-bit floating point, of which this GPU does two a
@@ -291,7 +292,7 @@ __device__ __forceinline__ void compare(const Args &a, const Pair &pair, int64_t
             const float unit = (ipo ? 1.f : a.beta) * kQuantum;
             const float x = __fmul_rn(top, unit), rest = __fmaf_rn(low, unit, __fmaf_rn(top, unit, -x));
             if (ipo) {
-                loss = __fmaf_rn(x, x, 2.f * x * rest);
+                loss = __fmaf_rn(x, x, __fmul_rn(2.f * x, rest));
                 slope = 2.f * (x + rest);
             } else {
                 lose(a, x, rest, &loss, &slope);
@@ -303,7 +304,7 @@ __device__ __forceinline__ void compare(const Args &a, const Pair &pair, int64_t
                 loss = (float)(gap * gap);
                 slope = (float)(2.0 * gap);
             } else {
-                const double wide = (double)a.beta * d;
+                const double wide = __dmul_rn((double)a.beta, d);
                 const float x = (float)wide;
                 lose(a, x, fabsf(x) < INFINITY ? (float)(wide - (double)x) : 0.f, &loss, &slope);
             }
