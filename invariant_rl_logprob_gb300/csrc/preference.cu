@@ -290,7 +290,8 @@ __device__ __forceinline__ void compare(const Args &a, const Pair &pair, int64_t
             if (ipo) d -= a.middle;
             const float top = __ll2float_rn(d), low = __ll2float_rn(d - __float2ll_rn(top));
             const float unit = (ipo ? 1.f : a.beta) * kQuantum;
-            const float x = __fmul_rn(top, unit), rest = __fmaf_rn(low, unit, __fmaf_rn(top, unit, -x));
+            const float x = __fmul_rn(top, unit);
+            const float rest = fabsf(x) < INFINITY ? __fmaf_rn(low, unit, __fmaf_rn(top, unit, -x)) : 0.f;
             if (ipo) {
                 loss = __fmaf_rn(x, x, __fmul_rn(2.f * x, rest));
                 slope = 2.f * (x + rest);
