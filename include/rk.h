@@ -730,7 +730,7 @@ rk_status rk_preference_loss(const float *logp, const float *logp_ref, const int
  * All pointers are device memory, aligned to their element; the arrays of structs themselves
  * are host memory, read during the call (a captured graph has its own copy).  Tensors must not
  * overlap.
- *   lr, beta1, beta2 in [0, 1), eps > 0, step >= 1 (the first step is 1)
+ *   lr, beta1, beta2 in [0, 1), 0 < eps < 2^100, step >= 1 (the first step is 1)
  *   lr_device    fp32 [1] or NULL: read instead of lr;  step_device int64 [1] or NULL: read
  *                instead of step.  A graph that is replayed follows them, and a step has the same
  *                bits either way (lr is rounded to fp32).  A step below 1 there sets

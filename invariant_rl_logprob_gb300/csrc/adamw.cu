@@ -254,6 +254,8 @@ struct Elements {
             fma2(d0, d1, u0, u1, r.root, r.root);
             mul2(p0, p1, r.rate, r.rate);
             fma2(w[i], w[i + 1], w[i], w[i + 1], -r.decay, -r.decay);
+            // (the move's quotient within two units in its last place, of what is a correction to w; d0 stays
+            // far below 2^126, where this one ends)
             w[i] = __fsub_rn(w[i], __fdividef(p0, d0));
             w[i + 1] = __fsub_rn(w[i + 1], __fdividef(p1, d1));
             if (EIGHT) v[i] = u0, v[i + 1] = u1;

@@ -984,7 +984,7 @@ rk_status rk_adamw_step(const rk_adamw_tensor *tensors, int64_t count, const rk_
     if (count < 0 || !options || (count > 0 && !tensors)) return RK_ERR_INVALID_ARG;
     const rk_adamw_options &o = *options;
     if (!std::isfinite(o.lr) || !(o.beta1 >= 0.0 && o.beta1 < 1.0) || !(o.beta2 >= 0.0 && o.beta2 < 1.0) ||
-        !((float)o.eps > 0.f && std::isfinite((float)o.eps)) || (!o.step_device && o.step < 1) ||
+        !((float)o.eps > 0.f && (float)o.eps < 0x1p100f) || (!o.step_device && o.step < 1) ||
         !aligned(o.lr_device, 4) || !aligned(o.step_device, 8) || !aligned(o.grad_scale, 4))
         return RK_ERR_INVALID_ARG;
     for (int64_t i = 0; i < count; ++i) {
