@@ -219,11 +219,18 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
             divisor = Divisor(scale);
         }
         char *to = a.stage_out ? stage : a.out.row(t);
+        if (!e4m3) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            float y[8];
-            result(k, y);
-            if (e4m3) {
+            for (int k = 0; k < NV; ++k) {
+                float y[8];
+                result(k, y);
+                C::store(to, a.out.type, k, H, lane, y);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float y[8];
+                result(k, y);
                 if (a.group != 0) {  // 128 columns: 16 lanes (H > 128, so that a team has them)
                     float top = 0.f;
 #pragma unroll
@@ -235,8 +242,8 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
                     divisor = Divisor(scale);
                 }
                 divisor.divide(y);
+                C::store(to, RK_E4M3, k, H, lane, y);
             }
-            C::store(to, a.out.type, k, H, lane, y);
         }
         if (a.stage_out) {
             const int size = size_of(a.out.type);
