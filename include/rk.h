@@ -676,7 +676,8 @@ rk_status rk_rms_norm_bwd(const void *dout, rk_dtype dout_type, int64_t ld_dout,
  *       RK_PREFERENCE_IPO      f = (d - 1 / (2 beta))^2
  *     grad_logp[t] = d (sum of all losses) / d logp[t], the g for rk_linear_logp_bwd
  * A sequence may be in any number of pairs (their terms are added in ascending order; the pairs
- * between the first and the last that name it are looked through, so they are best kept together)
+ * between the first and the last that name it are looked through, so they are best kept together:
+ * thousands of pairs that are shuffled take many times as long)
  * or in none.  Inactive rows and rows outside all sequences get grad_logp = 0; what logp and
  * logp_ref hold there (NaN, infinities) reaches nothing.  A sequence without active rows
  * has s = 0.

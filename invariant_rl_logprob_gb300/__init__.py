@@ -1222,7 +1222,8 @@ def preference_loss(logp: torch.Tensor, targets: torch.Tensor, cu_seqlens: torch
         hinge:    max(0, 1 - beta d)
         ipo:      (d - 1 / (2 beta))^2
 
-    times ``scale``.  A sequence may be in any number of pairs."""
+    times ``scale``.  A sequence may be in any number of pairs, which are best kept together:
+    thousands that are shuffled take many times as long."""
     lib = _lib or load_library()
     T = logp.shape[0] if isinstance(logp, torch.Tensor) and logp.dim() == 1 else 0
     _need(logp, "logp", torch.float32, 1)

@@ -6,7 +6,7 @@
 //   r = x,  or x + residual rounded to residual's type (written to residual_out)
 //   y = r * rstd * weight,  rstd = 1 / sqrt(mean(r^2) + eps)
 //
-// Bound by memory: 8 flop an element, against 4 to 16 bytes.  A block has a row, or a
+// Bound by memory: 8 flop an element (in 8 bits 14), against 4 to 16 bytes.  A block has a row, or a
 // few narrow ones, in registers (rms_norm.cuh) and nothing lives longer: rings of
 // rows in shared memory, filled by bulk copies ahead of persistent blocks, took
 // 392 us with their waits where this takes 265, and plain loads of the next row 300.
@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_forward(const __grid_c
 // ---- launches ----
 
 // Widest row, team, vectors of 8 a thread, rows a team, block and blocks per SM.  Narrow rows: teams of 8
-// lanes for 2M rows of 64 columns take 173 us (residual, e4m3) where warps took 496, of 16 lanes for 1M
-// of 128 167 and 252.
+// lanes for 2M rows of 64 columns took 173 us (residual, e4m3) where warps took 496, of 16 lanes for 1M
+// of 128 167 and 252 (now, with rounded quotients, 202 and 199; to bf16 153 both).
 #define RK_NORM_SHAPES(SHAPE)        \
     SHAPE(64, 8, 1, 4, 128, 8)       \
     SHAPE(128, 16, 1, 4, 128, 8)     \

@@ -5,7 +5,7 @@
 // A team (part of a warp up to 128 columns, a warp up to 1024 or, in the gradient, 512, up to
 // 16 warps beyond) has a row in registers, up to 32 columns a thread: fewer threads a row
 // mean fewer that sum, scale and wait for one another (256 threads with 16 columns
-// each, 65536 x 4096 with residual to e4m3: 290 us; 128 with 32: 265, 105 % of the
+// each, 65536 x 4096 with residual to e4m3: 290 us; 128 with 32: 264, 105 % of the
 // copy rate).  A thread owns eight consecutive columns at a time.  Rows off 16-byte
 // boundaries (any row of an odd H, say) are read in the aligned 16 bytes around each
 // eight and shifted on the way; results for such rows go through shared memory and
@@ -292,7 +292,7 @@ __device__ __forceinline__ void row_range(const int32_t *cu, int num_seqs, int64
 //   kAligned  bf16 or fp32 on 16-byte boundaries: kept as floats
 //   kFloats   anything else, shifted on the way
 // The weight is on a 16-byte boundary in the first two.  65536 x 4096 bf16 with residual to e4m3
-// takes 265 us as words and 481 with all that kFloats is ready for; an fp32 stream (fp32 x and
+// takes 264 us as words and 481 with all that kFloats is ready for; an fp32 stream (fp32 x and
 // residual to fp32) 605 us as kAligned, 105 % of the copy rate.
 enum Read { kWords, kAligned, kFloats };
 

@@ -9,7 +9,7 @@
 // r: the sums of r^2 and of g * r come out of one reduction.  dweight: a team
 // (rms_norm.cuh) adds its rows in registers, in order; blocks leave partial sums
 // that a last kernel adds in order.  Teams therefore stay, and ask for their next row
-// ahead, into the second cache (65536 x 4096, all bf16: 347 us without, 316 with, the
+// ahead, into the second cache (65536 x 4096, all bf16: 347 us without, 318 with, the
 // copy rate).
 //
 // Which rows a team takes depends on the number of canonical rows and on the number of teams, which
@@ -116,9 +116,9 @@ __host__ __device__ constexpr int64_t pitch_of(int64_t H) { return (H + 7) / 8 *
 
 // What the backward keeps of a row between its sums and its results: with kWords (r, dout and dr in
 // bf16) and kMixed (the same with dout in fp32) its words, with kAligned up to 16 columns a thread;
-// otherwise nothing, it is read again, from the caches.  65536 x 4096: kWords 316 us, kMixed 398 (both
-// the copy rate); without kMixed its case took 610.  32768 x 4096 all in fp32: 323, 98 % of the copy
-// rate, where 32 columns a thread, read again, took 420.
+// otherwise nothing, it is read again, from the caches.  65536 x 4096: kWords 318 us, kMixed 398 (both
+// the copy rate); without kMixed its case took 610.  32768 x 4096 all in fp32: 316, the copy rate, where
+// 32 columns a thread, read again, take 417.
 constexpr int kMixed = 3;
 
 // LIST: every block lists the canonical rows for itself.  (A variant of its own: as a branch it cost
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) rms_norm_backward(const __grid_
         }
     };
     // A narrow row is asked for a row ahead in registers, not in the second cache: 2^27 elements of bf16 with
-    // dr, 64 columns 227 us against 277, with the weight kept as well 184 (128 columns: 184 for 210, 256: 182 for
+    // dr, 64 columns 227 us against 277, with the weight kept as well 186 (128 columns: 185 for 210, 256: 182 for
     // 190).
     constexpr bool kAhead = NV == 1 && (READ == kWords || READ == kMixed);
     Held h, ahead;
@@ -570,9 +570,10 @@ cudaError_t halved_launch(int read, NormBwdArgs &a, const DeviceInfo &di, cudaSt
 //   beyond 1792 columns (1536 with dr 194 and 184, 1792 173 and 170, 2048 161 and 182), with dout in fp32
 //   beyond 1408 (1408 220 and 212, 1536 213 and 240).  Other rows are read twice in any case: with a wide dr
 //   only (2047 columns, bf16 472 and 456, without dr 413 and 387, all fp32 without dr 499 and 472).
-//   beyond: where r or dr is fp32 and there is a dr (all fp32, 4096 columns 323 and 420, 8192 338 and 408; 5120,
-//   where 192 of 512 threads would have none, 404 and 347; without dr, a third less to wait for, 4096 columns 271
-//   and 221).
+//   beyond: where r or dr is fp32 and there is a dr (all fp32, 4096 columns 315 and 417, 7168 335 and 385, 8192
+//   325 and 409), but for 4097 to 6144 columns, where up to half of 512 threads would have none (5120 386 and 349;
+//   6144 350 and 371, but 311 and 268 with r and dx in bf16).  Without dr there is a third less to wait for: r and
+//   dx in fp32, 4096 columns 249 and 223, 8192 263 and 242 (all fp32 268 and 298, 286 and 278).
 struct Kind {
     bool wide, dr, dout_wide;  // r or dr in fp32, dr given, dout in fp32
 };
@@ -584,8 +585,9 @@ bool halved(int64_t H, const Kind &k) {
 }
 
 // Widest row, and for rows as they are and halved ones team, vectors of 8 a thread, block and blocks per
-// SM.  The blocks per SM are what leaves a team's sums in registers: at 4096 columns of bf16 3, 4 and 5
-// blocks of 128 threads took 103, 96 and 104 us for 16384 rows, before rows were asked for ahead.  Up to
+// SM.  The blocks per SM are what leaves a team's sums in registers (but for 16 to 32 bytes a thread of bf16
+// and mixed rows of four vectors): at 4096 columns of bf16 3, 4 and 5 blocks of 128 threads took 103, 96
+// and 104 us for 16384 rows, before rows were asked for ahead.  Up to
 // 1024 columns a thread has 16 (2^27 elements of bf16 with dr, 1024 columns 164 us where 32 took 188).
 #define RK_NORM_BWD_SHAPES(SHAPE)                  \
     SHAPE(64, 8, 1, 256, 3, 8, 1, 256, 3)          \
