@@ -12,8 +12,9 @@
 // leave in aligned 16 bytes as well.
 //
 // Which thread owns which column, and with it the order of every sum, depends on H
-// and, in the gradient, on the types and on whether there is a residual's gradient.  A sum of squares that leaves fp32 is formed again from r * 2^-80, and
-// the gradient's sum of g r from n, of the size of 1, in place of r.
+// and, in the gradient, on the types and on whether there is a residual's gradient.
+// A sum of squares that leaves fp32 is formed again from r * 2^-80, and the gradient's
+// sum of g r from n, of the size of 1, in place of r.
 #pragma once
 
 #include "elements.cuh"

@@ -587,8 +587,8 @@ bool halved(int64_t H, const Kind &k) {
 // Widest row, and for rows as they are and halved ones team, vectors of 8 a thread, block and blocks per
 // SM.  The blocks per SM are what leaves a team's sums in registers (but for 16 to 32 bytes a thread of bf16
 // and mixed rows of four vectors): at 4096 columns of bf16 3, 4 and 5 blocks of 128 threads took 103, 96
-// and 104 us for 16384 rows, before rows were asked for ahead.  Up to
-// 1024 columns a thread has 16 (2^27 elements of bf16 with dr, 1024 columns 164 us where 32 took 188).
+// and 104 us for 16384 rows, before rows were asked for ahead.  Up to 1024 columns a thread has 16 (2^27
+// elements of bf16 with dr, 1024 columns 163 us where 32 took 188).
 #define RK_NORM_BWD_SHAPES(SHAPE)                  \
     SHAPE(64, 8, 1, 256, 3, 8, 1, 256, 3)          \
     SHAPE(128, 16, 1, 256, 3, 16, 1, 256, 3)       \

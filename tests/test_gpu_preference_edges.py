@@ -43,7 +43,7 @@ def test_steep_losses(rk, tokens):
             # token 1: its sequence is rejected by 10 and chosen by -10, of which the second has a slope
             grad = float(got["grad"][1])
             assert abs(grad + beta) <= 16 * pp.U * beta, (beta, kind, grad)
-    # in 64-bit floats, with a margin past fixed point, it was so before
+    # a margin past fixed point: in 64-bit floats
     c.margin = torch.tensor([-3e5, 3e5, 0.0, 0.0, 0.0])
     got = run(rk, c, beta=3e38)
     assert got["loss"][0] == 0 and got["loss"][1] == math.inf and not bool(torch.isnan(got["grad"]).any())
